@@ -17,6 +17,7 @@ import torch
 E4M3, E5M2 = 0, 1
 F32, BF16 = 0, 1
 AMAX_MAX, AMAX_MOST_RECENT = 0, 1
+SILU, GELU_TANH = 0, 1
 MAX_HISTORY = 8192
 FMT_MAX = {E4M3: 448.0, E5M2: 57344.0}
 
@@ -29,8 +30,8 @@ EXPORTS = ("fp8_quantize", "fp8_quantize_ex", "fp8_quantize_current", "fp8_quant
            "fp8_linear_bwd", "fp8_linear_bwd_rowmajor", "fp8_linear_bwd_rowmajor_ex", "delayed_scaling_update",
            "delayed_scaling_update_ex", "mp_master_step", "mp_master_step_adam", "mp_master_step_prescanned", "mp_master_step_adam_prescanned",
            "mp_master_step_prescanned_ex", "mp_master_step_adam_prescanned_ex",
-           "mp_master_step_prescanned_scaling_ex", "mp_master_step_adam_prescanned_scaling_ex", "fp8mp_check",
-           "fp8mp_last_error",
+           "mp_master_step_prescanned_scaling_ex", "mp_master_step_adam_prescanned_scaling_ex", "mp_adamw_workspace_bytes", "mp_grad_norm", "mp_adamw_step",
+           "fp8mp_check", "fp8mp_last_error",
            "fp8mp_version", "fp8mp_selftest_timeout", "fp8mp_selftest_barrier_timeout")
 
 _lib = None
@@ -48,6 +49,16 @@ class fp8mp_meta(ctypes.Structure):
     _fields_ = [("amax_history", ctypes.c_void_p), ("scale", ctypes.c_void_p),
                 ("scale_inv", ctypes.c_void_p), ("cur_amax", ctypes.c_void_p),
                 ("history_len", ctypes.c_int32), ("fmt", ctypes.c_int32)]
+
+
+class fp8mp_adamw_tensor(ctypes.Structure):
+    """Mirror of the C struct fp8mp_adamw_tensor."""
+
+    _fields_ = [("grad", ctypes.c_void_p), ("master", ctypes.c_void_p), ("exp_avg", ctypes.c_void_p),
+                ("exp_avg_sq", ctypes.c_void_p), ("exp_avg_scale", ctypes.c_void_p),
+                ("exp_avg_sq_scale", ctypes.c_void_p), ("copy", ctypes.c_void_p), ("copy_scale", ctypes.c_void_p),
+                ("copy_amax", ctypes.c_void_p), ("n", ctypes.c_int64), ("weight_decay", ctypes.c_float),
+                ("grad_dtype", ctypes.c_int32), ("state_bits", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 def build(force: bool = False) -> str:
@@ -97,6 +108,13 @@ def load(path: str | None = None):
                                                        M, I32, I32, I32, U32, P]
     L.mp_master_step_adam_prescanned_scaling_ex.argtypes = [P, I64, P, P, P, P, P, P, P, P, P, P, P, P, F, F, F,
                                                             F, F, F, I32, M, I32, I32, I32, U32, P]
+    A = ctypes.POINTER(fp8mp_adamw_tensor)
+    L.mp_adamw_workspace_bytes.argtypes = []
+    L.mp_adamw_workspace_bytes.restype = I64
+    L.mp_grad_norm.argtypes = [A, I32, P, P, P, I64, P]
+    L.mp_grad_norm.restype = ctypes.c_int
+    L.mp_adamw_step.argtypes = [A, I32, P, P, P, P, P, P, F, F, F, F, F, F, F, I32, P, I64, P]
+    L.mp_adamw_step.restype = ctypes.c_int
     L.fp8mp_check.argtypes = [P]
     L.fp8mp_selftest_timeout.argtypes = [P]
     L.fp8mp_selftest_barrier_timeout.argtypes = [P]
@@ -429,6 +447,111 @@ def mp_master_step_adam(grad_bf16: torch.Tensor, master: torch.Tensor, exp_avg: 
                                       _ptr(found_inf), _ptr(beta_pows), float(lr), float(beta1), float(beta2),
                                       float(eps), float(backoff), float(growth_factor), int(growth_interval),
                                       _stream(stream)))
+
+
+class AdamWTensors:
+    """The tensors of mp_grad_norm and mp_adamw_step: add each one once, keep
+    the object over the steps. It holds references to every tensor it was
+    given; set_grads replaces the gradients when a step has new ones."""
+
+    def __init__(self):
+        self._rows, self._keep, self._array = [], [], None
+
+    def __len__(self) -> int:
+        return len(self._rows)
+
+    def add(self, grad: torch.Tensor, master: torch.Tensor | None = None, exp_avg: torch.Tensor | None = None,
+            exp_avg_sq: torch.Tensor | None = None, exp_avg_scale: torch.Tensor | None = None,
+            exp_avg_sq_scale: torch.Tensor | None = None, copy: torch.Tensor | None = None,
+            copy_scale: torch.Tensor | None = None, copy_amax: torch.Tensor | None = None,
+            weight_decay: float = 0.0) -> None:
+        """One tensor. grad: bf16 or fp32; master: fp32. Moments: fp32, or int8
+        and uint8 codes with exp_avg_scale and exp_avg_sq_scale (fp32, one for
+        each 256 elements). copy: uint8 (E4M3 codes under copy_scale, |w| into
+        copy_amax), bf16, or None. For mp_grad_norm alone grad is enough."""
+        n = grad.numel()
+        bits = 32
+        if master is not None:
+            if exp_avg is None or exp_avg_sq is None:
+                raise Fp8mpError(ERR_INVALID, "a master weight needs exp_avg and exp_avg_sq")
+            bits = 8 if exp_avg.dtype == torch.int8 else 32
+            state = (torch.int8, torch.uint8) if bits == 8 else (torch.float32, torch.float32)
+            blocks = (n + 255) // 256
+            _expect(master, "master", torch.float32, n)
+            _expect(exp_avg, "exp_avg", state[0], n)
+            _expect(exp_avg_sq, "exp_avg_sq", state[1], n)
+            if bits == 8:
+                if exp_avg_scale is None or exp_avg_sq_scale is None:
+                    raise Fp8mpError(ERR_INVALID, "8-bit moments need exp_avg_scale and exp_avg_sq_scale")
+                _expect(exp_avg_scale, "exp_avg_scale", torch.float32, blocks)
+                _expect(exp_avg_sq_scale, "exp_avg_sq_scale", torch.float32, blocks)
+            if copy is not None:
+                _expect(copy, "copy", torch.bfloat16 if copy_scale is None else torch.uint8, n)
+        self._rows.append(fp8mp_adamw_tensor(
+            None, _ptr(master), _ptr(exp_avg), _ptr(exp_avg_sq), _ptr(exp_avg_scale), _ptr(exp_avg_sq_scale),
+            _ptr(copy), _ptr(copy_scale), _ptr(copy_amax), n, float(weight_decay), F32, bits, 0))
+        self._keep.append([None, master, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, copy, copy_scale,
+                           copy_amax])
+        self._array = None
+        self._set_grad(len(self._rows) - 1, self._rows[-1], grad)
+
+    def _set_grad(self, i: int, row, grad: torch.Tensor) -> None:
+        if grad.numel() != row.n or not grad.is_contiguous():
+            raise Fp8mpError(ERR_INVALID, f"gradient {i} must be dense with {row.n} elements")
+        row.grad, row.grad_dtype = grad.data_ptr(), _dtype_code(grad)
+        self._keep[i][0] = grad
+
+    def set_grads(self, grads) -> None:
+        """This step's gradients, one for each tensor, in the order of add."""
+        grads = list(grads)
+        if len(grads) != len(self._rows):
+            raise Fp8mpError(ERR_INVALID, f"{len(grads)} gradients for {len(self._rows)} tensors")
+        rows = self.c_array()
+        for i, g in enumerate(grads):
+            self._set_grad(i, rows[i], g)
+
+    def c_array(self):
+        if self._array is None:
+            self._array = (fp8mp_adamw_tensor * max(1, len(self._rows)))(*self._rows)
+            self._rows = [self._array[i] for i in range(len(self._rows))]
+        return self._array
+
+
+def _expect(t: torch.Tensor, name: str, dtype: torch.dtype, n: int) -> None:
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        raise Fp8mpError(ERR_INVALID, f"{name} must be dense {dtype} with {n} elements, got {t.dtype} with {t.numel()}")
+
+
+def mp_adamw_workspace_bytes() -> int:
+    return int(load().mp_adamw_workspace_bytes())
+
+
+def _workspace(workspace: torch.Tensor):
+    return _ptr(workspace), workspace.numel() * workspace.element_size()
+
+
+def mp_grad_norm(tensors: AdamWTensors, norm: torch.Tensor, found_inf: torch.Tensor, workspace: torch.Tensor,
+                 stream=None) -> None:
+    """norm = the 2-norm of all the tensors' gradients (under the loss scale),
+    found_inf = 1 if their sum of squares is not finite, else 0. workspace: at
+    least mp_adamw_workspace_bytes() bytes, zero-filled before its first use."""
+    _check(load().mp_grad_norm(tensors.c_array(), len(tensors), _ptr(norm), _ptr(found_inf), *_workspace(workspace),
+                               _stream(stream)))
+
+
+def mp_adamw_step(tensors: AdamWTensors, loss_scale: torch.Tensor, growth_tracker: torch.Tensor,
+                  found_inf: torch.Tensor, beta_pows: torch.Tensor, workspace: torch.Tensor, lr: float,
+                  beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8, seed: torch.Tensor | None = None,
+                  grad_norm: torch.Tensor | None = None, max_norm: float = 0.0, backoff: float = 0.5,
+                  growth_factor: float = 2.0, growth_interval: int = 2000, stream=None) -> None:
+    """One AdamW step over all the tensors, in place: unscale, skip when
+    found_inf is set, clip to max_norm by grad_norm (mp_grad_norm's), moments,
+    weights, weight copies, then the loss scale. seed (int32[1], advanced by
+    every step taken) is what 8-bit moments are rounded with."""
+    _check(load().mp_adamw_step(tensors.c_array(), len(tensors), _ptr(loss_scale), _ptr(growth_tracker),
+                                _ptr(found_inf), _ptr(beta_pows), _ptr(seed), _ptr(grad_norm), float(max_norm),
+                                float(lr), float(beta1), float(beta2), float(eps), float(backoff),
+                                float(growth_factor), int(growth_interval), *_workspace(workspace), _stream(stream)))
 
 
 def fp8mp_check(stream=None) -> int:

@@ -1,0 +1,597 @@
+// adamw.cu -- the global gradient norm and one AdamW step over many tensors
+// at once, with the moments in fp32 or in 8-bit codes under block scales.
+//
+// Both kernels walk the tensors' elements in units of 256 (one warp, eight
+// consecutive elements per lane), eight units to a chunk, one chunk per block
+// at a time. The tensors' descriptors travel as kernel parameters with the
+// prefix sums of their chunk counts, so a call needs no table in device
+// memory and can be captured in a graph; a call with more tensors than one
+// launch's parameters hold is split into several launches.
+//
+// Both are bound by HBM: the norm reads the gradients once (2 or 4 B per
+// parameter); the step reads gradient, master and moments and writes master,
+// moments and the weight copy (bf16 gradient, E4M3 copy: 27 B per parameter
+// with fp32 moments, 15.06 B with 8-bit ones).
+#include <cstring>
+
+#include "fp8mp_internal.cuh"
+
+namespace fp8mp {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kUnit = 256;                            // elements of a unit: one warp, one scale of the 8-bit moments
+constexpr int kChunk = kUnit * (kThreads / 32);       // elements of a chunk
+constexpr int kNormChunk = 8192;                      // elements of a chunk of the norm
+constexpr int kNormBlocksPerSm = 8;
+constexpr int kMaxNormBlocks = 4096;
+constexpr int kStepBlocksPerSm = 16;
+
+// The workspace: the arrival counter, then the running sum over launches,
+// both zero between calls, then the blocks' partial sums.
+struct Workspace {
+    unsigned int arrivals;
+    unsigned int pad;
+    double sum;
+    float partial[kMaxNormBlocks];
+};
+
+// ------------------------------------------------------------------- norm
+
+struct NormTensor {
+    const void *grad;
+    int64_t n;
+    int32_t bf16;
+};
+template <int CAP>
+struct NormBatch {
+    NormTensor t[CAP];
+    int32_t first[CAP + 1];  // chunks before tensor i
+    int32_t count;
+};
+
+__device__ __forceinline__ float sum_squares(const float (&f)[8]) {
+    const float a = __fmaf_rn(f[0], f[0], __fmul_rn(f[1], f[1])), b = __fmaf_rn(f[2], f[2], __fmul_rn(f[3], f[3]));
+    const float c = __fmaf_rn(f[4], f[4], __fmul_rn(f[5], f[5])), d = __fmaf_rn(f[6], f[6], __fmul_rn(f[7], f[7]));
+    return __fadd_rn(__fadd_rn(a, b), __fadd_rn(c, d));
+}
+
+__device__ __forceinline__ void unpack_bf16(const uint4 &d, float (&f)[8]) {
+    const uint32_t w[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        f[2 * j] = __uint_as_float(w[j] << 16);
+        f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    }
+}
+
+__device__ __forceinline__ float block_sum(float v, float *red) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, o));
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float s = 0.0f;
+    if (threadIdx.x == 0)
+        for (int w = 0; w < kThreads / 32; ++w) s = __fadd_rn(s, red[w]);
+    return s;
+}
+
+// The sum of squares over the batch's tensors: each thread adds its vectors'
+// squares in fp32 (eight at a time, pairwise), a block its threads', the last
+// block to arrive the blocks' sums in double and in block order, so the result
+// does not depend on which block that is. Inf and NaN need no test of their
+// own: either makes the sum Inf or NaN. So do squares that overflow fp32
+// (|g| > 1.8e19), which count as an overflow of the step too.
+template <int CAP>
+__global__ void __launch_bounds__(kThreads)
+grad_norm_kernel(const __grid_constant__ NormBatch<CAP> batch, Workspace *ws, float *norm, int32_t *found_inf,
+                 int finish) {
+    pdl_wait();
+    pdl_launch_dependents();
+    __shared__ float red[kThreads / 32];
+    __shared__ int last;
+    float acc = 0.0f;
+    int t = 0;
+    const int chunks = batch.first[batch.count];
+    for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
+        while (c >= batch.first[t + 1]) ++t;
+        const NormTensor &T = batch.t[t];
+        const int64_t base = static_cast<int64_t>(c - batch.first[t]) * kNormChunk;
+        const int64_t left = T.n - base;
+        if (T.bf16) {
+            const uint16_t *g = static_cast<const uint16_t *>(T.grad) + base;
+            if (left >= kNormChunk) {
+                uint4 d[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) d[u] = __ldcs(reinterpret_cast<const uint4 *>(g) + u * kThreads + threadIdx.x);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    float f[8];
+                    unpack_bf16(d[u], f);
+                    acc = __fadd_rn(acc, sum_squares(f));
+                }
+            } else {
+                for (int64_t i = threadIdx.x; i < left; i += kThreads) {
+                    const float f = bf16_bits_to_f32(g[i]);
+                    acc = __fmaf_rn(f, f, acc);
+                }
+            }
+        } else {
+            const float *g = static_cast<const float *>(T.grad) + base;
+            if (left >= kNormChunk) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float4 d[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        d[u] = __ldcs(reinterpret_cast<const float4 *>(g) + (4 * h + u) * kThreads + threadIdx.x);
+#pragma unroll
+                    for (int u = 0; u < 4; u += 2) {
+                        const float f[8] = {d[u].x,     d[u].y,     d[u].z,     d[u].w,
+                                            d[u + 1].x, d[u + 1].y, d[u + 1].z, d[u + 1].w};
+                        acc = __fadd_rn(acc, sum_squares(f));
+                    }
+                }
+            } else {
+                for (int64_t i = threadIdx.x; i < left; i += kThreads) acc = __fmaf_rn(g[i], g[i], acc);
+            }
+        }
+    }
+    const float s = block_sum(acc, red);
+    if (threadIdx.x == 0) {
+        ws->partial[blockIdx.x] = s;
+        __threadfence();
+        last = atomicAdd(&ws->arrivals, 1u) == gridDim.x - 1;
+    }
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    // thread i adds the partial sums i, i + 256, ...; then a fixed tree
+    __shared__ double dred[kThreads];
+    double d = 0.0;
+    for (unsigned i = threadIdx.x; i < gridDim.x; i += kThreads) d += static_cast<double>(__ldcg(&ws->partial[i]));
+    dred[threadIdx.x] = d;
+    __syncthreads();
+    for (int o = kThreads / 2; o > 0; o >>= 1) {
+        if (threadIdx.x < static_cast<unsigned>(o)) dred[threadIdx.x] += dred[threadIdx.x + o];
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) {
+        const double total = ws->sum + dred[0];
+        ws->arrivals = 0u;
+        ws->sum = finish ? 0.0 : total;
+        if (finish) {
+            *norm = static_cast<float>(sqrt(total));
+            *found_inf = isfinite(total) ? 0 : 1;
+        }
+    }
+}
+
+// ------------------------------------------------------------------- step
+
+struct StepTensor {
+    const void *grad;
+    float *w;
+    void *m, *v;
+    float *sm, *sv;
+    void *copy;
+    const float *copy_scale;
+    float *copy_amax;
+    int64_t n;
+    float decay;
+    uint32_t ordinal;
+    int32_t grad_bf16;
+    int32_t copy_kind;  // 0 none, 1 bf16, 2 E4M3
+};
+template <int CAP>
+struct StepBatch {
+    StepTensor t[CAP];
+    int32_t first[CAP + 1];
+    int32_t count;
+};
+struct StepArgs {
+    float *loss_scale;
+    int32_t *growth;
+    const int32_t *found_inf;
+    float *beta_pows;
+    uint32_t *seed;
+    const float *grad_norm;
+    float max_norm, lr, b1, b2, eps, backoff, growth_factor;
+    int32_t interval;
+    int32_t finish;
+    Workspace *ws;
+};
+
+struct Scalars {
+    float coef, b1, c1, b2, c2, step, root, eps, lr;
+};
+
+// What every element of the step shares. The clip takes the gradients' norm
+// as measured, under the loss scale.
+__device__ __forceinline__ Scalars make_scalars(const StepArgs &a) {
+    Scalars s;
+    const float inv_s = __fdiv_rn(1.0f, *a.loss_scale);
+    s.coef = inv_s;
+    if (a.grad_norm != nullptr) {
+        const float clip = __fdiv_rn(a.max_norm, __fadd_rn(__fmul_rn(*a.grad_norm, inv_s), 1e-6f));
+        if (clip < 1.0f) s.coef = __fmul_rn(inv_s, clip);
+    }
+    s.b1 = a.b1;
+    s.b2 = a.b2;
+    s.c1 = __fsub_rn(1.0f, a.b1);
+    s.c2 = __fsub_rn(1.0f, a.b2);
+    s.step = __fdiv_rn(a.lr, __fsub_rn(1.0f, __fmul_rn(a.beta_pows[0], a.b1)));
+    s.root = __fdiv_rn(1.0f, __fsqrt_rn(__fsub_rn(1.0f, __fmul_rn(a.beta_pows[1], a.b2))));
+    s.eps = a.eps;
+    s.lr = a.lr;
+    return s;
+}
+
+__device__ __forceinline__ float sqrt_fast(float x) {
+    float r;
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// The moments' recurrences, every operation rounded once (no contraction:
+// the 8-bit codes are a function of these bits).
+__device__ __forceinline__ void moments(const Scalars &s, float g, float &m, float &v) {
+    const float u = __fmul_rn(g, s.coef);
+    m = __fadd_rn(__fmul_rn(m, s.b1), __fmul_rn(u, s.c1));
+    v = __fadd_rn(__fmul_rn(v, s.b2), __fmul_rn(__fmul_rn(u, u), s.c2));
+}
+// The weight: w (1 - lr decay) - (lr / (1 - b1^t)) m / (sqrt(v / (1 - b2^t)) + eps).
+// The square root and the quotient are the hardware's approximations (2 ulp):
+// their error is 2^-22 of a step, far below half an ulp of w.
+__device__ __forceinline__ float updated(const Scalars &s, float shrink, float w, float m, float v) {
+    const float den = __fmaf_rn(sqrt_fast(v), s.root, s.eps);
+    return __fmaf_rn(-s.step, __fdividef(m, den), __fmul_rn(w, shrink));
+}
+
+// The counter hash of the stochastic rounding: xor-shifts and odd multiplies.
+__device__ __forceinline__ uint32_t mix32(uint32_t x) {
+    x = (x ^ (x >> 16)) * 0x7FEB352Du;
+    x = (x ^ (x >> 15)) * 0x846CA68Bu;
+    return x ^ (x >> 16);
+}
+
+__device__ __forceinline__ float square(float c) { return __fmul_rn(c, c); }
+__device__ __forceinline__ float fourth(float c) { return square(square(c)); }
+
+// y on the grid of 0, 1, 2^p, ..., TOP^p: the largest code c with c^p <= y (the
+// approximate root is corrected, so the code does not depend on its error),
+// one more with probability (y - c^p) / ((c + 1)^p - c^p), r being uniform.
+template <bool FOURTH>
+__device__ __forceinline__ float quantize(float y, float r) {
+    constexpr float TOP = FOURTH ? 255.0f : 127.0f;
+    float root = sqrt_fast(y);
+    if constexpr (FOURTH) root = sqrt_fast(root);
+    float c = fminf(floorf(root), TOP);
+    auto power = [](float x) { return FOURTH ? fourth(x) : square(x); };
+    if (power(__fadd_rn(c, 1.0f)) <= y) c = __fadd_rn(c, 1.0f);
+    if (power(c) > y) c = __fsub_rn(c, 1.0f);
+    c = fminf(c, TOP);
+    const float lo = power(c);
+    const bool up = __fmul_rn(r, __fsub_rn(power(__fadd_rn(c, 1.0f)), lo)) < __fsub_rn(y, lo);
+    return up ? fminf(__fadd_rn(c, 1.0f), TOP) : c;
+}
+
+constexpr float kLevelsM = 16129.0f;       // 127^2
+constexpr float kLevelsV = 4228250624.0f;  // 255^4, rounded to fp32
+
+// One unit of 8 elements per lane: cnt of them exist (8 but at a tensor's end).
+__device__ __forceinline__ void load8(const float *p, int cnt, float (&x)[8]) {
+    if (cnt == 8) {
+        const float4 a = __ldcs(reinterpret_cast<const float4 *>(p)), b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = j < cnt ? p[j] : 0.0f;
+    }
+}
+__device__ __forceinline__ void store8(float *p, int cnt, const float (&x)[8]) {
+    if (cnt == 8) {
+        __stcs(reinterpret_cast<float4 *>(p), make_float4(x[0], x[1], x[2], x[3]));
+        __stcs(reinterpret_cast<float4 *>(p) + 1, make_float4(x[4], x[5], x[6], x[7]));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < cnt) p[j] = x[j];
+    }
+}
+__device__ __forceinline__ uint2 load_bytes(const uint8_t *p, int cnt) {
+    if (cnt == 8) return __ldcs(reinterpret_cast<const uint2 *>(p));
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (j < cnt) w[j >> 2] |= static_cast<uint32_t>(p[j]) << (8 * (j & 3));
+    return make_uint2(w[0], w[1]);
+}
+__device__ __forceinline__ void store_bytes(uint8_t *p, int cnt, uint2 d) {
+    if (cnt == 8) {
+        *reinterpret_cast<uint2 *>(p) = d;
+    } else {
+        const uint32_t w[2] = {d.x, d.y};
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < cnt) p[j] = static_cast<uint8_t>(w[j >> 2] >> (8 * (j & 3)));
+    }
+}
+__device__ __forceinline__ void load_grad(const StepTensor &T, int64_t at, int cnt, float (&g)[8]) {
+    if (!T.grad_bf16) {
+        load8(static_cast<const float *>(T.grad) + at, cnt, g);
+        return;
+    }
+    const uint16_t *p = static_cast<const uint16_t *>(T.grad) + at;
+    if (cnt == 8) {
+        unpack_bf16(__ldcs(reinterpret_cast<const uint4 *>(p)), g);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[j] = j < cnt ? bf16_bits_to_f32(p[j]) : 0.0f;
+    }
+}
+__device__ __forceinline__ void store_copy(const StepTensor &T, int64_t at, int cnt, const float (&w)[8]) {
+    if (T.copy_kind == 2) {
+        const float sw = __ldg(T.copy_scale);
+        const uint2 q = make_uint2(cvt_quad<FP8MP_E4M3>(__fmul_rn(w[0], sw), __fmul_rn(w[1], sw), __fmul_rn(w[2], sw),
+                                                        __fmul_rn(w[3], sw)),
+                                   cvt_quad<FP8MP_E4M3>(__fmul_rn(w[4], sw), __fmul_rn(w[5], sw), __fmul_rn(w[6], sw),
+                                                        __fmul_rn(w[7], sw)));
+        store_bytes(static_cast<uint8_t *>(T.copy) + at, cnt, q);
+    } else if (T.copy_kind == 1) {
+        __nv_bfloat16 *p = static_cast<__nv_bfloat16 *>(T.copy) + at;
+        if (cnt == 8) {
+            uint32_t q[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(w[2 * j], w[2 * j + 1]);
+                q[j] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+            *reinterpret_cast<uint4 *>(p) = make_uint4(q[0], q[1], q[2], q[3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < cnt) p[j] = __float2bfloat16_rn(w[j]);
+        }
+    }
+}
+
+// Both kinds of moments share the walk; BITS is the moments' width.
+// The warp's 256 elements of a unit are one block of the 8-bit moments, so a
+// block's largest moment is a warp reduction and nothing leaves the warp.
+template <int BITS, int CAP>
+__global__ void __launch_bounds__(kThreads)
+adamw_kernel(const __grid_constant__ StepBatch<CAP> batch, const StepArgs a) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int found = a.found_inf != nullptr && *reinterpret_cast<const volatile int32_t *>(a.found_inf) != 0;
+    if (!found) {
+        const Scalars s = make_scalars(a);
+        const uint32_t seed = BITS == 8 ? *a.seed : 0u;
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        const int chunks = batch.first[batch.count];
+        int t = -1;
+        float am = 0.0f, shrink = 0.0f;
+        uint32_t key = 0;
+        for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
+            if (t < 0 || c >= batch.first[t + 1]) {
+                if (t >= 0 && batch.t[t].copy_amax != nullptr) {
+                    am = warp_max(am);
+                    if (lane == 0) atomicMax(reinterpret_cast<int *>(batch.t[t].copy_amax), __float_as_int(am));
+                }
+                am = 0.0f;
+                t = t < 0 ? 0 : t;
+                while (c >= batch.first[t + 1]) ++t;
+                shrink = __fsub_rn(1.0f, __fmul_rn(s.lr, batch.t[t].decay));
+                key = mix32(seed + (batch.t[t].ordinal + 1u) * 0x9E3779B9u);
+            }
+            const StepTensor &T = batch.t[t];
+            const int64_t unit = static_cast<int64_t>(c - batch.first[t]) * (kThreads / 32) + warp;
+            const int64_t at = unit * kUnit + 8 * lane;
+            if (unit * kUnit >= T.n) continue;  // the whole warp: past the tensor's end
+            const int64_t left = T.n - at;
+            const int cnt = left >= 8 ? 8 : (left > 0 ? static_cast<int>(left) : 0);
+            float g[8], w[8], m[8], v[8];
+            load_grad(T, at, cnt, g);
+            load8(T.w + at, cnt, w);
+            if constexpr (BITS == 8) {
+                const uint2 cm = load_bytes(static_cast<const uint8_t *>(T.m) + at, cnt);
+                const uint2 cv = load_bytes(static_cast<const uint8_t *>(T.v) + at, cnt);
+                const float sm = __ldg(T.sm + unit), sv = __ldg(T.sv + unit);
+                const uint32_t bm[2] = {cm.x, cm.y}, bv[2] = {cv.x, cv.y};
+                float mmax = 0.0f, vmax = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float fm = static_cast<float>(static_cast<int8_t>(bm[j >> 2] >> (8 * (j & 3))));
+                    const float fv = static_cast<float>((bv[j >> 2] >> (8 * (j & 3))) & 0xFFu);
+                    m[j] = __fmul_rn(__fmul_rn(fm, fabsf(fm)), sm);
+                    v[j] = __fmul_rn(fourth(fv), sv);
+                    moments(s, g[j], m[j], v[j]);
+                    w[j] = updated(s, shrink, w[j], m[j], v[j]);
+                    mmax = fmaxf(mmax, fabsf(m[j]));
+                    vmax = fmaxf(vmax, v[j]);
+                    am = fmaxf(am, j < cnt ? fabsf(w[j]) : 0.0f);
+                }
+                store8(T.w + at, cnt, w);
+                store_copy(T, at, cnt, w);
+                mmax = warp_max(mmax);
+                vmax = warp_max(vmax);
+                // a block that small is zero: its scale's reciprocal would not be finite
+                mmax = mmax >= 0x1p-100f ? mmax : 0.0f;
+                vmax = vmax >= 0x1p-90f ? vmax : 0.0f;
+                const float im = mmax > 0.0f ? __fdiv_rn(kLevelsM, mmax) : 0.0f;
+                const float iv = vmax > 0.0f ? __fdiv_rn(kLevelsV, vmax) : 0.0f;
+                uint32_t om[2] = {0u, 0u}, ov[2] = {0u, 0u};
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint64_t i = static_cast<uint64_t>(at + j);
+                    const uint32_t h =
+                        mix32(key + static_cast<uint32_t>(i) + static_cast<uint32_t>(i >> 32) * 0x85EBCA77u);
+                    const float rm = __fmul_rn(static_cast<float>(h & 0xFFFFu), 0x1p-16f);
+                    const float rv = __fmul_rn(static_cast<float>(h >> 16), 0x1p-16f);
+                    const float qm = quantize<false>(__fmul_rn(fabsf(m[j]), im), rm);
+                    float qv = quantize<true>(__fmul_rn(v[j], iv), rv);
+                    if (v[j] > 0.0f && vmax > 0.0f) qv = fmaxf(qv, 1.0f);  // v stays above 0 where it was: m / sqrt(v) stays bounded
+                    const int km = static_cast<int>(m[j] < 0.0f ? -qm : qm);
+                    om[j >> 2] |= (static_cast<uint32_t>(km) & 0xFFu) << (8 * (j & 3));
+                    ov[j >> 2] |= static_cast<uint32_t>(qv) << (8 * (j & 3));
+                }
+                store_bytes(static_cast<uint8_t *>(T.m) + at, cnt, make_uint2(om[0], om[1]));
+                store_bytes(static_cast<uint8_t *>(T.v) + at, cnt, make_uint2(ov[0], ov[1]));
+                if (lane == 0) {
+                    T.sm[unit] = __fdiv_rn(mmax, kLevelsM);
+                    T.sv[unit] = __fdiv_rn(vmax, kLevelsV);
+                }
+            } else {
+                load8(static_cast<const float *>(T.m) + at, cnt, m);
+                load8(static_cast<const float *>(T.v) + at, cnt, v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    moments(s, g[j], m[j], v[j]);
+                    w[j] = updated(s, shrink, w[j], m[j], v[j]);
+                    am = fmaxf(am, j < cnt ? fabsf(w[j]) : 0.0f);
+                }
+                store8(static_cast<float *>(T.m) + at, cnt, m);
+                store8(static_cast<float *>(T.v) + at, cnt, v);
+                store8(T.w + at, cnt, w);
+                store_copy(T, at, cnt, w);
+            }
+        }
+        if (t >= 0 && batch.t[t].copy_amax != nullptr) {
+            am = warp_max(am);
+            if (lane == 0) atomicMax(reinterpret_cast<int *>(batch.t[t].copy_amax), __float_as_int(am));
+        }
+    }
+    if (!a.finish) return;
+    // the last block of the call's last launch: every element has read the
+    // scalars, so they may change
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __threadfence();
+        if (atomicAdd(&a.ws->arrivals, 1u) == gridDim.x - 1) {
+            __threadfence();
+            a.ws->arrivals = 0u;
+            if (found) {
+                *a.loss_scale = __fmul_rn(*a.loss_scale, a.backoff);
+                *a.growth = 0;
+            } else {
+                int32_t gr = *a.growth + 1;
+                if (gr >= a.interval) {
+                    *a.loss_scale = __fmul_rn(*a.loss_scale, a.growth_factor);
+                    gr = 0;
+                }
+                *a.growth = gr;
+                a.beta_pows[0] = __fmul_rn(a.beta_pows[0], a.b1);
+                a.beta_pows[1] = __fmul_rn(a.beta_pows[1], a.b2);
+                if (a.seed != nullptr) *a.seed += 1u;
+            }
+        }
+    }
+}
+
+// Tensors of one launch: as many as its parameters (at most 32,764 bytes)
+// hold, or few where few are left, for a launch with more parameters costs more.
+constexpr int kNormCapLarge = 1000, kNormCapSmall = 64;
+constexpr int kStepCapLarge = 280, kStepCapSmall = 32;
+static_assert(sizeof(NormBatch<kNormCapLarge>) + 64 <= 32764, "kernel parameters");
+static_assert(sizeof(StepBatch<kStepCapLarge>) + sizeof(StepArgs) <= 32764, "kernel parameters");
+
+template <int CAP>
+cudaError_t launch_norm_batch(const fp8mp_adamw_tensor *t, int32_t n, Workspace *ws, float *norm, int32_t *found,
+                              int finish, cudaStream_t s, const DeviceInfo &dev) {
+    NormBatch<CAP> b;
+    b.count = 0;
+    int64_t chunks = 0;
+    b.first[0] = 0;
+    for (int32_t i = 0; i < n; ++i) {
+        if (t[i].n == 0) continue;
+        b.t[b.count] = NormTensor{t[i].grad, t[i].n, t[i].grad_dtype == FP8MP_BF16};
+        chunks += (t[i].n + kNormChunk - 1) / kNormChunk;
+        b.first[++b.count] = static_cast<int32_t>(chunks);
+    }
+    int64_t blocks = static_cast<int64_t>(dev.num_sms) * kNormBlocksPerSm;
+    if (blocks > kMaxNormBlocks) blocks = kMaxNormBlocks;
+    if (blocks > chunks) blocks = chunks < 1 ? 1 : chunks;
+    return launch_kernel(grad_norm_kernel<CAP>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, s, b, ws, norm,
+                         found, finish);
+}
+
+template <int BITS, int CAP>
+cudaError_t launch_step_batch(const fp8mp_adamw_tensor *t, const int32_t *which, int32_t n, const StepArgs &a,
+                              cudaStream_t s, const DeviceInfo &dev) {
+    StepBatch<CAP> b;
+    b.count = n;
+    int64_t chunks = 0;
+    b.first[0] = 0;
+    for (int32_t i = 0; i < n; ++i) {
+        const fp8mp_adamw_tensor &T = t[which[i]];
+        b.t[i] = StepTensor{T.grad, T.master, T.exp_avg, T.exp_avg_sq, T.exp_avg_scale, T.exp_avg_sq_scale, T.copy,
+                            T.copy_scale, T.copy_amax, T.n, T.weight_decay, static_cast<uint32_t>(which[i]),
+                            T.grad_dtype == FP8MP_BF16, T.copy == nullptr ? 0 : (T.copy_scale == nullptr ? 1 : 2)};
+        chunks += (T.n + kChunk - 1) / kChunk;
+        b.first[i + 1] = static_cast<int32_t>(chunks);
+    }
+    int64_t blocks = static_cast<int64_t>(dev.num_sms) * kStepBlocksPerSm;
+    if (blocks > chunks) blocks = chunks < 1 ? 1 : chunks;
+    return launch_kernel(adamw_kernel<BITS, CAP>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, s, b, a);
+}
+
+}  // namespace
+
+int64_t adamw_workspace_bytes() { return (static_cast<int64_t>(sizeof(Workspace)) + 15) & ~static_cast<int64_t>(15); }
+
+int64_t adamw_max_elements() { return static_cast<int64_t>(kChunk) << 30; }
+
+int launch_grad_norm(const fp8mp_adamw_tensor *t, int32_t n, float *norm, int32_t *found_inf, void *workspace,
+                     cudaStream_t s, const DeviceInfo &dev) {
+    Workspace *ws = static_cast<Workspace *>(workspace);
+    int32_t at = 0;
+    do {
+        const int32_t cnt = n - at < kNormCapLarge ? n - at : kNormCapLarge;
+        const int finish = at + cnt == n;
+        const cudaError_t e =
+            cnt <= kNormCapSmall
+                ? launch_norm_batch<kNormCapSmall>(t + at, cnt, ws, norm, found_inf, finish, s, dev)
+                : launch_norm_batch<kNormCapLarge>(t + at, cnt, ws, norm, found_inf, finish, s, dev);
+        if (e != cudaSuccess)
+            return fail(FP8MP_ERR_LAUNCH, "mp_grad_norm: launch failed: %s", cudaGetErrorString(e));
+        at += cnt;
+    } while (at < n);
+    return FP8MP_OK;
+}
+
+int launch_adamw_step(const fp8mp_adamw_tensor *t, int32_t n, const AdamwArgs &args, cudaStream_t s,
+                      const DeviceInfo &dev) {
+    StepArgs a = {args.loss_scale, args.growth, args.found_inf, args.beta_pows, args.seed, args.grad_norm,
+                  args.max_norm, args.lr, args.b1, args.b2, args.eps, args.backoff, args.growth_factor, args.interval,
+                  0, static_cast<Workspace *>(args.workspace)};
+    // the tensors with fp32 moments first, then those with 8-bit ones, each in launches of one kind
+    int32_t left = 0;
+    for (int32_t i = 0; i < n; ++i) left += t[i].n > 0;
+    bool launched = false;
+    for (int bits = 32; bits >= 8; bits -= 24) {
+        int32_t which[kStepCapLarge], cnt = 0;
+        for (int32_t i = 0; i <= n; ++i) {
+            if (i < n && t[i].n > 0 && t[i].state_bits == bits) which[cnt++] = i;
+            if (cnt < kStepCapLarge && i < n) continue;
+            if (cnt == 0 && !(i == n && bits == 8 && !launched)) continue;
+            left -= cnt;
+            a.finish = left == 0;
+            cudaError_t e;
+            if (bits == 32)
+                e = cnt <= kStepCapSmall ? launch_step_batch<32, kStepCapSmall>(t, which, cnt, a, s, dev)
+                                         : launch_step_batch<32, kStepCapLarge>(t, which, cnt, a, s, dev);
+            else
+                e = cnt <= kStepCapSmall ? launch_step_batch<8, kStepCapSmall>(t, which, cnt, a, s, dev)
+                                         : launch_step_batch<8, kStepCapLarge>(t, which, cnt, a, s, dev);
+            if (e != cudaSuccess)
+                return fail(FP8MP_ERR_LAUNCH, "mp_adamw_step: launch failed: %s", cudaGetErrorString(e));
+            launched = true;
+            cnt = 0;
+        }
+    }
+    return FP8MP_OK;
+}
+
+}  // namespace fp8mp

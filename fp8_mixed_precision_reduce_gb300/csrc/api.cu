@@ -735,6 +735,93 @@ int mp_master_step_adam_prescanned_scaling_ex(const uint16_t *grad_bf16, int64_t
                            growth_factor, growth_interval, stream, w8_in, flags, &fb);
 }
 
+int64_t mp_adamw_workspace_bytes(void) { return adamw_workspace_bytes(); }
+
+// What mp_grad_norm and mp_adamw_step read of a call's tensors, but for the
+// step's own arrays.
+static int check_adamw_tensors(const char *fn, const fp8mp_adamw_tensor *tensors, int32_t n_tensors,
+                               const void *workspace, int64_t workspace_bytes) {
+    REQUIRE(n_tensors >= 0, "%s: negative count", fn);
+    REQUIRE(n_tensors == 0 || tensors != nullptr, "%s: tensors is NULL", fn);
+    CHECK_PTR(workspace, true);
+    REQUIRE(workspace_bytes >= adamw_workspace_bytes(), "%s: workspace of %lld bytes, %lld needed", fn,
+            (long long)workspace_bytes, (long long)adamw_workspace_bytes());
+    int64_t total = 0;
+    for (int32_t i = 0; i < n_tensors; ++i) {
+        const fp8mp_adamw_tensor &t = tensors[i];
+        REQUIRE(t.n >= 0 && t.n <= adamw_max_elements(), "%s: tensor %d has n = %lld", fn, i, (long long)t.n);
+        if (t.n == 0) continue;
+        total += t.n + 8192;
+        REQUIRE(total <= adamw_max_elements(), "%s: too many elements", fn);
+        REQUIRE(valid_dtype(t.grad_dtype), "%s: tensor %d has grad_dtype %d", fn, i, t.grad_dtype);
+        REQUIRE(t.grad != nullptr && aligned16(t.grad), "%s: tensor %d: grad is NULL or not 16-byte aligned", fn, i);
+    }
+    return FP8MP_OK;
+}
+
+int mp_grad_norm(const fp8mp_adamw_tensor *tensors, int32_t n_tensors, float *norm, int32_t *found_inf,
+                 void *workspace, int64_t workspace_bytes, void *stream) {
+    const char *fn = "mp_grad_norm";
+    clear_error();
+    int rc = check_adamw_tensors(fn, tensors, n_tensors, workspace, workspace_bytes);
+    if (rc) return rc;
+    CHECK_SCALAR(norm, true);
+    CHECK_SCALAR(found_inf, true);
+    DeviceInfo dev;
+    rc = current_device(&dev);
+    if (rc) return rc;
+    return launch_grad_norm(tensors, n_tensors, norm, found_inf, workspace, static_cast<cudaStream_t>(stream), dev);
+}
+
+int mp_adamw_step(const fp8mp_adamw_tensor *tensors, int32_t n_tensors, float *loss_scale, int32_t *growth_tracker,
+                  const int32_t *found_inf, float *beta_pows, uint32_t *seed, const float *grad_norm, float max_norm,
+                  float lr, float beta1, float beta2, float eps, float backoff, float growth_factor,
+                  int32_t growth_interval, void *workspace, int64_t workspace_bytes, void *stream) {
+    const char *fn = "mp_adamw_step";
+    clear_error();
+    int rc = check_adamw_tensors(fn, tensors, n_tensors, workspace, workspace_bytes);
+    if (rc) return rc;
+    bool codes = false;
+    for (int32_t i = 0; i < n_tensors; ++i) {
+        const fp8mp_adamw_tensor &t = tensors[i];
+        if (t.n == 0) continue;
+        REQUIRE(t.state_bits == 32 || t.state_bits == 8, "%s: tensor %d has state_bits %d (32 or 8)", fn, i,
+                t.state_bits);
+        REQUIRE(t.reserved == 0, "%s: tensor %d: reserved is not 0", fn, i);
+        REQUIRE(t.master && t.exp_avg && t.exp_avg_sq, "%s: tensor %d has a NULL pointer", fn, i);
+        REQUIRE(aligned16(t.master) && aligned16(t.exp_avg) && aligned16(t.exp_avg_sq) && aligned16(t.copy),
+                "%s: tensor %d has an array that is not 16-byte aligned", fn, i);
+        if (t.state_bits == 8) {
+            codes = true;
+            REQUIRE(t.exp_avg_scale && t.exp_avg_sq_scale, "%s: tensor %d: 8-bit moments need their scales", fn, i);
+            CHECK_SCALAR(t.exp_avg_scale, true);
+            CHECK_SCALAR(t.exp_avg_sq_scale, true);
+        }
+        REQUIRE(t.copy != nullptr || (t.copy_scale == nullptr && t.copy_amax == nullptr),
+                "%s: tensor %d has a copy's scale or amax but no copy", fn, i);
+        REQUIRE(t.copy_scale != nullptr || t.copy_amax == nullptr, "%s: tensor %d has an amax but no scale", fn, i);
+        CHECK_SCALAR(t.copy_scale, false);
+        CHECK_SCALAR(t.copy_amax, false);
+    }
+    CHECK_SCALAR(loss_scale, true);
+    CHECK_SCALAR(growth_tracker, true);
+    CHECK_SCALAR(found_inf, true);
+    CHECK_SCALAR(beta_pows, true);
+    CHECK_SCALAR(seed, codes);
+    CHECK_SCALAR(grad_norm, false);
+    REQUIRE(grad_norm == nullptr || max_norm > 0.0f, "%s: clipping needs max_norm > 0", fn);
+    REQUIRE(beta1 >= 0.0f && beta1 < 1.0f && beta2 >= 0.0f && beta2 < 1.0f, "%s: betas must lie in [0, 1)", fn);
+    REQUIRE(eps > 0.0f, "%s: eps must be > 0", fn);
+    REQUIRE(growth_interval >= 1, "%s: growth_interval must be >= 1", fn);
+    DeviceInfo dev;
+    rc = current_device(&dev);
+    if (rc) return rc;
+    const AdamwArgs a = {loss_scale, growth_tracker, found_inf, beta_pows, seed,          grad_norm,
+                         max_norm,   lr,             beta1,     beta2,     eps,           backoff,
+                         growth_factor, growth_interval, workspace};
+    return launch_adamw_step(tensors, n_tensors, a, static_cast<cudaStream_t>(stream), dev);
+}
+
 int fp8mp_selftest_timeout(void *stream) {
     clear_error();
     DeviceInfo dev;

@@ -183,6 +183,25 @@ int launch_adam_step(const uint16_t *g, int64_t n, float *w, float *m, float *v,
                      int32_t growth_interval, cudaStream_t s, const DeviceInfo &dev,
                      int32_t *grad_nonfinite = nullptr, const uint8_t *w8_in = nullptr, bool early = false,
                      bool wait_done = false, const FoldBatch *fold = nullptr);
+// The many-tensor AdamW step (adamw.cu): its workspace, the most elements a
+// call may hold, the gradients' norm and the step (arguments validated).
+struct AdamwArgs {
+    float *loss_scale;
+    int32_t *growth;
+    const int32_t *found_inf;
+    float *beta_pows;
+    uint32_t *seed;
+    const float *grad_norm;
+    float max_norm, lr, b1, b2, eps, backoff, growth_factor;
+    int32_t interval;
+    void *workspace;
+};
+int64_t adamw_workspace_bytes();
+int64_t adamw_max_elements();
+int launch_grad_norm(const fp8mp_adamw_tensor *t, int32_t n, float *norm, int32_t *found_inf, void *workspace,
+                     cudaStream_t s, const DeviceInfo &dev);
+int launch_adamw_step(const fp8mp_adamw_tensor *t, int32_t n, const AdamwArgs &args, cudaStream_t s,
+                      const DeviceInfo &dev);
 // Enqueues the one-thread kernel whose bounded wait is meant to run out.
 int launch_timeout_selftest(cudaStream_t s);
 // Reads and clears the GEMM wait-timeout flag (after a stream sync).

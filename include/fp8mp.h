@@ -613,6 +613,109 @@ int mp_master_step_adam_prescanned_scaling_ex(const uint16_t *grad_bf16, int64_t
                                               int32_t margin, uint32_t flags, void *stream);
 
 /*
+ * One tensor of mp_grad_norm and mp_adamw_step. All pointers are device
+ * pointers; the arrays of n elements are 16-byte aligned, the scales and
+ * copy_amax 4-byte aligned. All are dense and none overlaps another.
+ *   grad         [n] of grad_dtype (FP8MP_F32 or FP8MP_BF16), the gradient of
+ *                the loss times the loss scale; read only.
+ *   master       [n] fp32 weights, in place.
+ *   exp_avg, exp_avg_sq  the moments, in place. state_bits 32: fp32 [n].
+ *                state_bits 8: codes [n] (int8_t and uint8_t) and, for each
+ *                block of 256 consecutive elements (the last may be short),
+ *                one fp32 step in exp_avg_scale / exp_avg_sq_scale
+ *                [ceil(n / 256)]:
+ *                  m = c |c| exp_avg_scale[b]       c in -127 .. 127
+ *                  v = c^4   exp_avg_sq_scale[b]    c in 0 .. 255
+ *                All zero is the state before the first step, in either width.
+ *   copy         [n] the weights the next forward pass reads, or NULL: E4M3
+ *                codes under *copy_scale when copy_scale is given (and
+ *                *copy_amax, if given, is raised to the largest new |master|
+ *                with an atomic max, as fp8_quantize raises amax), else bf16.
+ *   weight_decay the decoupled decay of this tensor.
+ * mp_grad_norm reads grad, n and grad_dtype only.
+ */
+typedef struct fp8mp_adamw_tensor {
+    const void *grad;
+    float *master;
+    void *exp_avg;
+    void *exp_avg_sq;
+    float *exp_avg_scale;
+    float *exp_avg_sq_scale;
+    void *copy;
+    const float *copy_scale;
+    float *copy_amax;
+    int64_t n;
+    float weight_decay;
+    int32_t grad_dtype;
+    int32_t state_bits; /* 32 or 8 */
+    int32_t reserved;   /* 0 */
+} fp8mp_adamw_tensor;
+
+/* Bytes of the workspace of mp_grad_norm and mp_adamw_step. It must be
+ * zero-filled before its first use; every call leaves what it needs zero
+ * again. Calls that share one must not overlap on the GPU. */
+int64_t mp_adamw_workspace_bytes(void);
+
+/*
+ * mp_grad_norm -- the norm of all the tensors' gradients and the step's
+ * overflow flag, in one pass over them:
+ *   *norm      = sqrt(sum over tensors and elements of fl32(grad)^2)
+ *   *found_inf = 1 if that sum is not finite, else 0
+ * The sum is not finite when a gradient is Inf or NaN, or when squares leave
+ * fp32 (|grad| above 1.8e19): the dynamic loss scaler then skips the step and
+ * lowers S ([MP], the dynamic loss-scale procedure). The norm is that of the
+ * gradients as they are, under the loss scale. Sums in fp32 within a block of
+ * threads, in double across blocks, in an order fixed by the sizes and the
+ * device (deterministic).
+ * tensors  HOST array of n_tensors >= 0 structs, read during the call only.
+ */
+int mp_grad_norm(const fp8mp_adamw_tensor *tensors, int32_t n_tensors, float *norm, int32_t *found_inf,
+                 void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * mp_adamw_step -- one AdamW step (Adam with decoupled weight decay) over many
+ * tensors at once, under dynamic loss scaling ([MP], [PT-FP8] as
+ * mp_master_step_adam), with the gradients' norm clipped and the weights'
+ * next copy written. When *found_inf != 0: S = S * backoff, growth = 0 and
+ * nothing else changes. Else, each operation rounded once to fp32:
+ *   k  = fl32(1 / S);  with grad_norm: c = max_norm / (*grad_norm * k + 1e-6),
+ *        k = k * c if c < 1
+ *   u  = fl32(grad) * k
+ *   m  = m * beta1 + u * (1 - beta1)
+ *   v  = v * beta2 + (u * u) * (1 - beta2)
+ *   w  = w * (1 - lr * weight_decay)
+ *        - lr / (1 - beta_pows[0] * beta1) * m
+ *          / (sqrt(v) / sqrt(1 - beta_pows[1] * beta2) + eps)
+ *        (to 2^-20 of the second term)
+ * then beta_pows advance by beta1 and beta2, *seed by 1 (when given),
+ * growth += 1, and S grows as in mp_master_step.
+ * The update uses m and v before they are stored. 8-bit moments are stored
+ * with stochastic rounding: with M the block's largest |m|, y = |m| * (127^2 / M)
+ * and c the largest code with c^2 <= y, the code is c + 1 with probability
+ * (y - c^2) / ((c + 1)^2 - c^2), so its mean is y; v likewise with 255^4 and
+ * fourth powers, but a v above 0 never gets the code 0. The random numbers
+ * r_m, r_v are the low and the high 16 bits of
+ *   h = mix(mix(*seed + (t + 1) * 0x9E3779B9) + lo32(i) + hi32(i) * 0x85EBCA77)
+ * over 2^16, for element i of tensor t of the call, with
+ *   mix(x): x ^= x >> 16; x *= 0x7FEB352D; x ^= x >> 15; x *= 0x846CA68B; x ^= x >> 16
+ * in 32-bit arithmetic. A block whose M is below 2^-100 (V below 2^-90) is
+ * stored as 0.
+ * tensors     HOST array, read during the call only; tensors with n == 0 count
+ *             in t but are skipped.
+ * found_inf   device int32 (mp_grad_norm's, or a backward launch's
+ *             dw_nonfinite), read only.
+ * beta_pows   device float[2], (beta1^(t-1), beta2^(t-1)); 1 at first.
+ * seed        device uint32, required when a tensor has 8-bit moments.
+ * grad_norm   device float (mp_grad_norm's) or NULL for no clipping;
+ *             max_norm > 0 with it.
+ * beta1, beta2 in [0, 1), eps > 0, growth_interval >= 1.
+ */
+int mp_adamw_step(const fp8mp_adamw_tensor *tensors, int32_t n_tensors, float *loss_scale, int32_t *growth_tracker,
+                  const int32_t *found_inf, float *beta_pows, uint32_t *seed, const float *grad_norm, float max_norm,
+                  float lr, float beta1, float beta2, float eps, float backoff, float growth_factor,
+                  int32_t growth_interval, void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
  * fp8mp_check -- synchronises `stream`, then reports and clears the device
  * flags a kernel sets when one of its bounded waits runs out (a GEMM's
  * mbarrier wait, the master step's grid barrier): FP8MP_ERR_TIMEOUT if one
