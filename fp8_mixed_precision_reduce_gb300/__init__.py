@@ -30,7 +30,8 @@ EXPORTS = ("fp8_quantize", "fp8_quantize_ex", "fp8_quantize_current", "fp8_quant
            "fp8_linear_bwd", "fp8_linear_bwd_rowmajor", "fp8_linear_bwd_rowmajor_ex", "delayed_scaling_update",
            "delayed_scaling_update_ex", "mp_master_step", "mp_master_step_adam", "mp_master_step_prescanned", "mp_master_step_adam_prescanned",
            "mp_master_step_prescanned_ex", "mp_master_step_adam_prescanned_ex",
-           "mp_master_step_prescanned_scaling_ex", "mp_master_step_adam_prescanned_scaling_ex", "mp_adamw_workspace_bytes", "mp_grad_norm", "mp_adamw_step",
+           "mp_master_step_prescanned_scaling_ex", "mp_master_step_adam_prescanned_scaling_ex", "fp8_gated_fwd", "fp8_gated_dgrad", "fp8_gated_bwd",
+           "mp_adamw_workspace_bytes", "mp_grad_norm", "mp_adamw_step",
            "fp8mp_check", "fp8mp_last_error",
            "fp8mp_version", "fp8mp_selftest_timeout", "fp8mp_selftest_barrier_timeout")
 
@@ -108,6 +109,11 @@ def load(path: str | None = None):
                                                        M, I32, I32, I32, U32, P]
     L.mp_master_step_adam_prescanned_scaling_ex.argtypes = [P, I64, P, P, P, P, P, P, P, P, P, P, P, P, F, F, F,
                                                             F, F, F, I32, M, I32, I32, I32, U32, P]
+    L.fp8_gated_fwd.argtypes = [P, P, I64, I64, I64, I32, P, P, P, P, P, P, P]
+    L.fp8_gated_dgrad.argtypes = [P, P, P, I64, I64, I64, I32, I32, P, P, P, P, P, P]
+    L.fp8_gated_bwd.argtypes = [P, I32, P, P, P, I64, I64, I64, I32, P, P, P, P, P, P, P, I32, P, I32, P, P]
+    for name in ("fp8_gated_fwd", "fp8_gated_dgrad", "fp8_gated_bwd"):
+        getattr(L, name).restype = ctypes.c_int
     A = ctypes.POINTER(fp8mp_adamw_tensor)
     L.mp_adamw_workspace_bytes.argtypes = []
     L.mp_adamw_workspace_bytes.restype = I64
@@ -447,6 +453,75 @@ def mp_master_step_adam(grad_bf16: torch.Tensor, master: torch.Tensor, exp_avg: 
                                       _ptr(found_inf), _ptr(beta_pows), float(lr), float(beta1), float(beta2),
                                       float(eps), float(backoff), float(growth_factor), int(growth_interval),
                                       _stream(stream)))
+
+
+def _shape(t: torch.Tensor, name: str, shape, *dtypes: torch.dtype) -> None:
+    if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes or not t.is_contiguous():
+        raise Fp8mpError(ERR_INVALID, f"{name} must be a dense {tuple(shape)} of {' or '.join(map(str, dtypes))}, got "
+                         f"{t.dtype} {tuple(t.shape)}")
+
+
+def fp8_gated_fwd(x8: torch.Tensor, w8: torch.Tensor, sinv_x: torch.Tensor, sinv_w: torch.Tensor, h: torch.Tensor,
+                  act: int = SILU, h_scale: torch.Tensor | None = None, h_amax: torch.Tensor | None = None,
+                  gu: torch.Tensor | None = None, stream=None) -> None:
+    """h[M, F] = act(x8 . wg^T) * (x8 . wu^T) with wg = w8[:F], wu = w8[F:] (w8
+    is [2F, K]), both products times sinv_x * sinv_w: E4M3 codes (uint8) under
+    h_scale, or bf16 without it. h_amax = max(h_amax, max|h|); gu [M, 2F] bf16
+    receives the pre-activations for the backward pass. Any M."""
+    M, K = x8.shape
+    F = w8.shape[0] // 2
+    _shape(x8, "x8", (M, K), torch.uint8)
+    _shape(w8, "w8", (2 * F, K), torch.uint8)
+    _shape(h, "h", (M, F), torch.uint8 if h_scale is not None else torch.bfloat16)
+    if gu is not None:
+        _shape(gu, "gu", (M, 2 * F), torch.bfloat16)
+    _check(load().fp8_gated_fwd(_ptr(x8), _ptr(w8), M, F, K, act, _ptr(sinv_x), _ptr(sinv_w), _ptr(h_scale), _ptr(h),
+                                _ptr(h_amax), _ptr(gu), _stream(stream)))
+
+
+def fp8_gated_dgrad(dy8: torch.Tensor, wd8: torch.Tensor, gu: torch.Tensor, sinv_dy: torch.Tensor,
+                    sinv_wd: torch.Tensor, dgu_scale: torch.Tensor, dgu8: torch.Tensor, act: int = SILU,
+                    dgu_amax: torch.Tensor | None = None, dy_fmt: int = E5M2, stream=None) -> None:
+    """dgu8[M, 2F] = E5M2 codes of [dh u act'(g) | dh act(g)] under dgu_scale,
+    with dh = (dy8 . wd8) * sinv_dy * sinv_wd from the output gradient's codes
+    and the down projection's weight wd8 [N, F]."""
+    M, N = dy8.shape
+    F = wd8.shape[1]
+    _shape(dy8, "dy8", (M, N), torch.uint8)
+    _shape(wd8, "wd8", (N, F), torch.uint8)
+    _shape(gu, "gu", (M, 2 * F), torch.bfloat16)
+    _shape(dgu8, "dgu8", (M, 2 * F), torch.uint8)
+    _check(load().fp8_gated_dgrad(_ptr(dy8), _ptr(wd8), _ptr(gu), M, F, N, act, dy_fmt, _ptr(sinv_dy), _ptr(sinv_wd),
+                                  _ptr(dgu_scale), _ptr(dgu8), _ptr(dgu_amax), _stream(stream)))
+
+
+def fp8_gated_bwd(dh: torch.Tensor | None, gu: torch.Tensor | None, x8: torch.Tensor, w8: torch.Tensor,
+                  sinv_x: torch.Tensor, sinv_w: torch.Tensor, dgu_scale: torch.Tensor | None, dgu_sinv: torch.Tensor,
+                  dgu8: torch.Tensor, dx: torch.Tensor | None, dw: torch.Tensor | None, act: int = SILU,
+                  dgu_amax: torch.Tensor | None = None, dw_nonfinite: torch.Tensor | None = None, stream=None) -> None:
+    """Backward pass of fp8_gated_fwd: dgu8 [M, 2F] from dh [M, F] (bf16 or
+    fp32) and gu, unless dh is None (dgu8 holds fp8_gated_dgrad's codes); then
+    dx[M, K] = (dgu8 . w8) * dgu_sinv * sinv_w and
+    dw[2F, K] = (dgu8^T . x8) * dgu_sinv * sinv_x, either of which may be None."""
+    M, K = x8.shape
+    F = w8.shape[0] // 2
+    _shape(x8, "x8", (M, K), torch.uint8)
+    _shape(w8, "w8", (2 * F, K), torch.uint8)
+    _shape(dgu8, "dgu8", (M, 2 * F), torch.uint8)
+    high = (torch.bfloat16, torch.float32)
+    if dh is not None:
+        _shape(dh, "dh", (M, F), *high)
+        if gu is None or dgu_scale is None:
+            raise Fp8mpError(ERR_INVALID, "dh needs gu and dgu_scale")
+        _shape(gu, "gu", (M, 2 * F), torch.bfloat16)
+    for t, name, shape in ((dx, "dx", (M, K)), (dw, "dw", (2 * F, K))):
+        if t is not None:
+            _shape(t, name, shape, *high)
+    _check(load().fp8_gated_bwd(_ptr(dh), _dtype_code(dh) if dh is not None else F32, _ptr(gu), _ptr(x8), _ptr(w8),
+                                M, F, K, act, _ptr(sinv_x), _ptr(sinv_w), _ptr(dgu_scale), _ptr(dgu_sinv),
+                                _ptr(dgu8), _ptr(dgu_amax), _ptr(dx), _dtype_code(dx) if dx is not None else F32,
+                                _ptr(dw), _dtype_code(dw) if dw is not None else F32, _ptr(dw_nonfinite),
+                                _stream(stream)))
 
 
 class AdamWTensors:

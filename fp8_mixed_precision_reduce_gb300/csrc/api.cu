@@ -735,6 +735,131 @@ int mp_master_step_adam_prescanned_scaling_ex(const uint16_t *grad_bf16, int64_t
                            growth_factor, growth_interval, stream, w8_in, flags, &fb);
 }
 
+// Sizes of the gated feed-forward calls: any number of rows (they are the
+// outer dimension of every operand), the others in steps of 16.
+static int check_gated_dims(const char *fn, int64_t M, int64_t F, int64_t K, const char *k_name) {
+    REQUIRE(M >= 0 && F >= 0 && K >= 0, "%s: negative dimension", fn);
+    REQUIRE(F % 16 == 0 && K % 16 == 0, "%s: F and %s must be multiples of 16 (got %lld, %lld)", fn, k_name,
+            (long long)F, (long long)K);
+    REQUIRE(M <= (1ll << 30) && F <= (1ll << 29) && K <= (1ll << 30), "%s: dimension too large", fn);
+    return FP8MP_OK;
+}
+
+static bool valid_act(int32_t a) { return a == FP8MP_SILU || a == FP8MP_GELU_TANH; }
+
+int fp8_gated_fwd(const uint8_t *x8, const uint8_t *w8, int64_t M, int64_t F, int64_t K, int32_t act,
+                  const float *sinv_x, const float *sinv_w, const float *h_scale, void *h, float *h_amax,
+                  uint16_t *gu_bf16, void *stream) {
+    const char *fn = "fp8_gated_fwd";
+    clear_error();
+    int rc = check_gated_dims(fn, M, F, K, "K");
+    if (rc) return rc;
+    REQUIRE(valid_act(act), "%s: act %d invalid", fn, act);
+    if (M == 0 || F == 0) return FP8MP_OK;
+    CHECK_PTR(h, true);
+    CHECK_PTR(gu_bf16, false);
+    CHECK_SCALAR(h_scale, false);
+    CHECK_SCALAR(h_amax, false);
+    CHECK_SCALAR(sinv_x, true);
+    CHECK_SCALAR(sinv_w, true);
+    if (K > 0) {
+        CHECK_PTR(x8, true);
+        CHECK_PTR(w8, true);
+    }
+    DeviceInfo dev;
+    rc = current_device(&dev);
+    if (rc) return rc;
+    return launch_gated_fwd(x8, w8, M, F, K, act, sinv_x, sinv_w, h_scale, h, h_amax, gu_bf16,
+                            static_cast<cudaStream_t>(stream), dev);
+}
+
+int fp8_gated_dgrad(const uint8_t *dy8, const uint8_t *wd8, const uint16_t *gu, int64_t M, int64_t F, int64_t N,
+                    int32_t act, int32_t dy_fmt, const float *sinv_dy, const float *sinv_wd, const float *dgu_scale,
+                    uint8_t *dgu8, float *dgu_amax, void *stream) {
+    const char *fn = "fp8_gated_dgrad";
+    clear_error();
+    int rc = check_gated_dims(fn, M, F, N, "N");
+    if (rc) return rc;
+    REQUIRE(valid_act(act), "%s: act %d invalid", fn, act);
+    REQUIRE(valid_fmt(dy_fmt), "%s: dy_fmt %d invalid", fn, dy_fmt);
+    if (M == 0 || F == 0) return FP8MP_OK;
+    CHECK_PTR(gu, true);
+    CHECK_PTR(dgu8, true);
+    CHECK_SCALAR(dgu_scale, true);
+    CHECK_SCALAR(dgu_amax, false);
+    CHECK_SCALAR(sinv_dy, true);
+    CHECK_SCALAR(sinv_wd, true);
+    if (N > 0) {
+        CHECK_PTR(dy8, true);
+        CHECK_PTR(wd8, true);
+    }
+    DeviceInfo dev;
+    rc = current_device(&dev);
+    if (rc) return rc;
+    return launch_gated_dgrad(dy8, wd8, gu, M, F, N, act, dy_fmt, sinv_dy, sinv_wd, dgu_scale, dgu8, dgu_amax,
+                              static_cast<cudaStream_t>(stream), dev);
+}
+
+int fp8_gated_bwd(const void *dh, int32_t dh_dtype, const uint16_t *gu, const uint8_t *x8, const uint8_t *w8,
+                  int64_t M, int64_t F, int64_t K, int32_t act, const float *sinv_x, const float *sinv_w,
+                  const float *dgu_scale, const float *dgu_sinv, uint8_t *dgu8, float *dgu_amax, void *dx,
+                  int32_t dx_dtype, void *dw, int32_t dw_dtype, int32_t *dw_nonfinite, void *stream) {
+    const char *fn = "fp8_gated_bwd";
+    clear_error();
+    int rc = check_gated_dims(fn, M, F, K, "K");
+    if (rc) return rc;
+    REQUIRE(valid_act(act), "%s: act %d invalid", fn, act);
+    REQUIRE(dh == nullptr || valid_dtype(dh_dtype), "%s: dh_dtype %d invalid", fn, dh_dtype);
+    REQUIRE(dx == nullptr || valid_dtype(dx_dtype), "%s: dx_dtype %d invalid", fn, dx_dtype);
+    REQUIRE(dw == nullptr || valid_dtype(dw_dtype), "%s: dw_dtype %d invalid", fn, dw_dtype);
+    const bool gate = dh != nullptr && M > 0 && F > 0;
+    const bool want_dx = dx != nullptr && M > 0 && K > 0, want_dw = dw != nullptr && F > 0 && K > 0;
+    if (!gate && !want_dx && !want_dw) return FP8MP_OK;
+    if (M > 0 && F > 0) CHECK_PTR(dgu8, true);
+    if (gate) {
+        CHECK_PTR(dh, true);
+        CHECK_PTR(gu, true);
+        CHECK_SCALAR(dgu_scale, true);
+        CHECK_SCALAR(dgu_amax, false);
+    }
+    CHECK_PTR(dx, false);
+    CHECK_PTR(dw, false);
+    CHECK_SCALAR(dw_nonfinite, false);
+    if (want_dx || want_dw) CHECK_SCALAR(dgu_sinv, true);
+    if (want_dx) {
+        CHECK_SCALAR(sinv_w, true);
+        if (F > 0) CHECK_PTR(w8, true);
+    }
+    if (want_dw) {
+        CHECK_SCALAR(sinv_x, true);
+        if (M > 0) CHECK_PTR(x8, true);
+    }
+    if (want_dx && want_dw) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(dx), b = reinterpret_cast<uintptr_t>(dw);
+        const uintptr_t na = static_cast<uintptr_t>(M * K) * (dx_dtype == FP8MP_BF16 ? 2 : 4);
+        const uintptr_t nb = static_cast<uintptr_t>(2 * F * K) * (dw_dtype == FP8MP_BF16 ? 2 : 4);
+        REQUIRE(a + na <= b || b + nb <= a, "%s: dx and dw overlap", fn);
+    }
+    DeviceInfo dev;
+    rc = current_device(&dev);
+    if (rc) return rc;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (gate) {
+        rc = launch_gate_bwd(dh, dh_dtype, gu, M, F, act, dgu_scale, dgu8, dgu_amax, s, dev);
+        if (rc) return rc;
+    }
+    // the two projections are one linear of 2F outputs, as in bwd_rowmajor_entry
+    GemmDesc d[2];
+    int n = 0;
+    if (want_dx)
+        d[n++] = {dgu8, FP8MP_E5M2, w8, FP8MP_E4M3, M, K, 2 * F, dgu_sinv, sinv_w, nullptr, FP8MP_F32, dx, dx_dtype,
+                  nullptr, nullptr, FP8MP_E4M3, 0, 1};
+    if (want_dw)
+        d[n++] = {dgu8, FP8MP_E5M2, x8, FP8MP_E4M3, 2 * F, K, M, dgu_sinv, sinv_x, nullptr, FP8MP_F32, dw, dw_dtype,
+                  nullptr, nullptr, FP8MP_E4M3, 1, 1, dw_nonfinite};
+    return n > 0 ? launch_gemms(d, n, s, dev) : FP8MP_OK;
+}
+
 int64_t mp_adamw_workspace_bytes(void) { return adamw_workspace_bytes(); }
 
 // What mp_grad_norm and mp_adamw_step read of a call's tensors, but for the
@@ -849,6 +974,11 @@ int fp8mp_check(void *stream) {
     if (rc) return rc;
     rc = read_and_clear_cast_timeout_flag(&cflag);
     if (rc) return rc;
+    unsigned int gflag = 0;
+    rc = read_and_clear_gated_timeout_flag(&gflag);
+    if (rc) return rc;
+    if (gflag)
+        return fail(FP8MP_ERR_TIMEOUT, "a gated feed-forward kernel's bounded wait expired; its output is undefined");
     if (flag) return fail(FP8MP_ERR_TIMEOUT, "a GEMM kernel's bounded wait expired; its output is undefined");
     if (cflag)
         return fail(FP8MP_ERR_TIMEOUT, "the bias-gradient cast's bounded wait expired; its outputs are undefined");

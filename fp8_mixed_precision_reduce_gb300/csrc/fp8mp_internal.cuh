@@ -183,6 +183,16 @@ int launch_adam_step(const uint16_t *g, int64_t n, float *w, float *m, float *v,
                      int32_t growth_interval, cudaStream_t s, const DeviceInfo &dev,
                      int32_t *grad_nonfinite = nullptr, const uint8_t *w8_in = nullptr, bool early = false,
                      bool wait_done = false, const FoldBatch *fold = nullptr);
+// The gated feed-forward block (gated.cu; arguments validated, M, F > 0).
+int launch_gated_fwd(const uint8_t *x8, const uint8_t *w8, int64_t M, int64_t F, int64_t K, int act,
+                     const float *sinv_x, const float *sinv_w, const float *h_scale, void *h, float *h_amax,
+                     uint16_t *gu, cudaStream_t s, const DeviceInfo &dev);
+int launch_gated_dgrad(const uint8_t *dy8, const uint8_t *wd8, const uint16_t *gu, int64_t M, int64_t F, int64_t N,
+                       int act, int dy_fmt, const float *sinv_dy, const float *sinv_wd, const float *dgu_scale,
+                       uint8_t *dgu8, float *dgu_amax, cudaStream_t s, const DeviceInfo &dev);
+int launch_gate_bwd(const void *dh, int dh_dtype, const uint16_t *gu, int64_t M, int64_t F, int act,
+                    const float *dgu_scale, uint8_t *dgu8, float *dgu_amax, cudaStream_t s, const DeviceInfo &dev);
+int read_and_clear_gated_timeout_flag(unsigned int *value);
 // The many-tensor AdamW step (adamw.cu): its workspace, the most elements a
 // call may hold, the gradients' norm and the step (arguments validated).
 struct AdamwArgs {

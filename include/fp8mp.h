@@ -67,6 +67,10 @@ typedef enum { FP8MP_F32 = 0, FP8MP_BF16 = 1 } fp8mp_dtype;
  * 사용방안(recipe)"): the largest amax of the history, or the newest one. */
 typedef enum { FP8MP_AMAX_MAX = 0, FP8MP_AMAX_MOST_RECENT = 1 } fp8mp_algo;
 
+/* Activations of the gated feed-forward block: g / (1 + exp(-g)), and
+ * g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2. */
+typedef enum { FP8MP_SILU = 0, FP8MP_GELU_TANH = 1 } fp8mp_act;
+
 enum {
     FP8MP_OK = 0,
     FP8MP_ERR_INVALID = -1,
@@ -611,6 +615,60 @@ int mp_master_step_adam_prescanned_scaling_ex(const uint16_t *grad_bf16, int64_t
                                               float backoff, float growth_factor, int32_t growth_interval,
                                               const fp8mp_meta *metas, int32_t n_metas, int32_t amax_algo,
                                               int32_t margin, uint32_t flags, void *stream);
+
+/*
+ * fp8_gated_fwd -- the gated feed-forward block's first half in one launch:
+ * both projections, the activation and the product, from E4M3 operands with
+ * fp32 accumulation (as fp8_linear_fwd):
+ *   g[m, f] = (sum_k x8[m, k] * w8[f, k])     * sinv_x[0] * sinv_w[0]
+ *   u[m, f] = (sum_k x8[m, k] * w8[F + f, k]) * sinv_x[0] * sinv_w[0]
+ *   y       = act(g) * u                                       (fp32)
+ *   h       = sat_rne_E4M3(fl32(y * h_scale[0]))  when h_scale != NULL, the
+ *             next linear's input under its delayed scale; else bf16(y)
+ *   *h_amax = max(*h_amax, max |y|)    (fp32 y, NaN left out; when != NULL)
+ *   gu      = bf16([g | u])            (when != NULL: the backward pass's)
+ *
+ * x8 [M x K], w8 [2F x K] (the gate projection's F rows, then the up
+ * projection's: one tensor under one scale), h [M x F] bytes or bf16,
+ * gu [M x 2F] bf16. act: fp8mp_act. F and K multiples of 16; any M >= 0 (one
+ * token when serving). M == 0 or F == 0: no-op. K == 0: zeros.
+ */
+int fp8_gated_fwd(const uint8_t *x8, const uint8_t *w8, int64_t M, int64_t F, int64_t K, int32_t act,
+                  const float *sinv_x, const float *sinv_w, const float *h_scale, void *h, float *h_amax,
+                  uint16_t *gu, void *stream);
+
+/*
+ * fp8_gated_dgrad -- back through the down projection and the gate in one
+ * launch, without storing dh:
+ *   dh[m, f]  = (sum_n dy8[m, n] * wd8[n, f]) * sinv_dy[0] * sinv_wd[0]  (fp32)
+ *   dg        = dh * u * act'(g),   du = dh * act(g)      (g, u from gu)
+ *   dgu8      = sat_rne_E5M2(fl32([dg | du] * dgu_scale[0]))
+ *   *dgu_amax = max(*dgu_amax, max |[dg | du]|)      (NaN left out; when != NULL)
+ * dy8 [M x N] codes of dy_fmt (the block's output gradient), wd8 [N x F] E4M3
+ * codes (the down projection's weight as its forward pass reads it), gu and
+ * dgu8 [M x 2F]. F and N multiples of 16, any M >= 0. N == 0: dgu8 = 0.
+ */
+int fp8_gated_dgrad(const uint8_t *dy8, const uint8_t *wd8, const uint16_t *gu, int64_t M, int64_t F, int64_t N,
+                    int32_t act, int32_t dy_fmt, const float *sinv_dy, const float *sinv_wd, const float *dgu_scale,
+                    uint8_t *dgu8, float *dgu_amax, void *stream);
+
+/*
+ * fp8_gated_bwd -- backward pass of fp8_gated_fwd. From dh, the gradient of y,
+ * dgu8 and *dgu_amax as fp8_gated_dgrad writes them; then, as
+ * fp8_linear_bwd_rowmajor on the two projections as one linear of 2F outputs,
+ *   dx[m, k] = (sum_j dgu8[m, j] * w8[j, k]) * dgu_sinv[0] * sinv_w[0]
+ *   dw[j, k] = (sum_m dgu8[m, j] * x8[m, k]) * dgu_sinv[0] * sinv_x[0]
+ * in one launch, dw_nonfinite as there.
+ * dh [M x F] of dh_dtype, or NULL: dgu8 already holds the codes
+ * (fp8_gated_dgrad's); gu, dgu_scale and dgu_amax are then not used.
+ * dgu_sinv is the scale_inv of the scale dgu8 was cast with. dx [M x K] or NULL,
+ * dw [2F x K] or NULL; they must not overlap. F and K multiples of 16, any
+ * M >= 0 (M == 0 gives dw = 0).
+ */
+int fp8_gated_bwd(const void *dh, int32_t dh_dtype, const uint16_t *gu, const uint8_t *x8, const uint8_t *w8,
+                  int64_t M, int64_t F, int64_t K, int32_t act, const float *sinv_x, const float *sinv_w,
+                  const float *dgu_scale, const float *dgu_sinv, uint8_t *dgu8, float *dgu_amax, void *dx,
+                  int32_t dx_dtype, void *dw, int32_t dw_dtype, int32_t *dw_nonfinite, void *stream);
 
 /*
  * One tensor of mp_grad_norm and mp_adamw_step. All pointers are device
