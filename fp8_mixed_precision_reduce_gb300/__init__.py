@@ -30,7 +30,7 @@ EXPORTS = ("fp8_quantize", "fp8_quantize_ex", "fp8_quantize_current", "fp8_quant
            "fp8_linear_bwd", "fp8_linear_bwd_rowmajor", "fp8_linear_bwd_rowmajor_ex", "delayed_scaling_update",
            "delayed_scaling_update_ex", "mp_master_step", "mp_master_step_adam", "mp_master_step_prescanned", "mp_master_step_adam_prescanned",
            "mp_master_step_prescanned_ex", "mp_master_step_adam_prescanned_ex",
-           "mp_master_step_prescanned_scaling_ex", "mp_master_step_adam_prescanned_scaling_ex", "fp8_gated_fwd", "fp8_gated_dgrad", "fp8_gated_bwd",
+           "mp_master_step_prescanned_scaling_ex", "mp_master_step_adam_prescanned_scaling_ex", "fp8_gated_fwd", "fp8_linear_few", "fp8_gated_dgrad", "fp8_gated_bwd",
            "mp_adamw_workspace_bytes", "mp_grad_norm", "mp_adamw_step",
            "fp8mp_check", "fp8mp_last_error",
            "fp8mp_version", "fp8mp_selftest_timeout", "fp8mp_selftest_barrier_timeout")
@@ -112,7 +112,8 @@ def load(path: str | None = None):
     L.fp8_gated_fwd.argtypes = [P, P, I64, I64, I64, I32, P, P, P, P, P, P, P]
     L.fp8_gated_dgrad.argtypes = [P, P, P, I64, I64, I64, I32, I32, P, P, P, P, P, P]
     L.fp8_gated_bwd.argtypes = [P, I32, P, P, P, I64, I64, I64, I32, P, P, P, P, P, P, P, I32, P, I32, P, P]
-    for name in ("fp8_gated_fwd", "fp8_gated_dgrad", "fp8_gated_bwd"):
+    L.fp8_linear_few.argtypes = [P, P, I64, I64, I64, P, P, P, I32, P, I32, P, P]
+    for name in ("fp8_gated_fwd", "fp8_linear_few", "fp8_gated_dgrad", "fp8_gated_bwd"):
         getattr(L, name).restype = ctypes.c_int
     A = ctypes.POINTER(fp8mp_adamw_tensor)
     L.mp_adamw_workspace_bytes.argtypes = []
@@ -477,6 +478,25 @@ def fp8_gated_fwd(x8: torch.Tensor, w8: torch.Tensor, sinv_x: torch.Tensor, sinv
         _shape(gu, "gu", (M, 2 * F), torch.bfloat16)
     _check(load().fp8_gated_fwd(_ptr(x8), _ptr(w8), M, F, K, act, _ptr(sinv_x), _ptr(sinv_w), _ptr(h_scale), _ptr(h),
                                 _ptr(h_amax), _ptr(gu), _stream(stream)))
+
+
+FEW_TOKENS = 64  # FP8MP_FEW_TOKENS: most tokens of fp8_linear_few
+
+
+def fp8_linear_few(x8: torch.Tensor, w8: torch.Tensor, sinv_x: torch.Tensor, sinv_w: torch.Tensor, y: torch.Tensor,
+                   bias: torch.Tensor | None = None, y_amax: torch.Tensor | None = None, stream=None) -> None:
+    """fp8_linear_fwd for 0 to FEW_TOKENS tokens, any number of them:
+    y[M, N] = (x8[M, K] . w8[N, K]^T) * sinv_x * sinv_w + bias."""
+    M, K = x8.shape
+    N = w8.shape[0]
+    _shape(x8, "x8", (M, K), torch.uint8)
+    _shape(w8, "w8", (N, K), torch.uint8)
+    _shape(y, "y", (M, N), torch.bfloat16, torch.float32)
+    if bias is not None:
+        _shape(bias, "bias", (N,), torch.bfloat16, torch.float32)
+    _check(load().fp8_linear_few(_ptr(x8), _ptr(w8), M, N, K, _ptr(sinv_x), _ptr(sinv_w), _ptr(bias),
+                                 _dtype_code(bias) if bias is not None else F32, _ptr(y), _dtype_code(y),
+                                 _ptr(y_amax), _stream(stream)))
 
 
 def fp8_gated_dgrad(dy8: torch.Tensor, wd8: torch.Tensor, gu: torch.Tensor, sinv_dy: torch.Tensor,

@@ -100,6 +100,8 @@ using namespace fp8mp;
 
 namespace {
 
+static_assert(FP8MP_FEW_TOKENS == kFewTokens, "the header's limit");
+
 bool valid_fmt(int32_t f) { return f == FP8MP_E4M3 || f == FP8MP_E5M2; }
 bool valid_dtype(int32_t d) { return d == FP8MP_F32 || d == FP8MP_BF16; }
 
@@ -773,6 +775,37 @@ int fp8_gated_fwd(const uint8_t *x8, const uint8_t *w8, int64_t M, int64_t F, in
                             static_cast<cudaStream_t>(stream), dev);
 }
 
+int fp8_linear_few(const uint8_t *x8, const uint8_t *w8, int64_t M, int64_t N, int64_t K, const float *sinv_x,
+                   const float *sinv_w, const void *bias, int32_t bias_dtype, void *y, int32_t y_dtype,
+                   float *y_amax, void *stream) {
+    const char *fn = "fp8_linear_few";
+    clear_error();
+    REQUIRE(M >= 0 && M <= FP8MP_FEW_TOKENS, "%s: M = %lld outside 0..%d", fn, (long long)M, FP8MP_FEW_TOKENS);
+    REQUIRE(N >= 0 && K >= 0 && N <= (1ll << 30) && K <= (1ll << 30), "%s: dimension outside 0..2^30", fn);
+    REQUIRE(N % 16 == 0 && K % 16 == 0, "%s: N and K must be multiples of 16 (got %lld, %lld)", fn, (long long)N,
+            (long long)K);
+    REQUIRE(valid_dtype(y_dtype), "%s: y_dtype %d invalid", fn, y_dtype);
+    REQUIRE(bias == nullptr || valid_dtype(bias_dtype), "%s: bias_dtype %d invalid", fn, bias_dtype);
+    if (M == 0 || N == 0) return FP8MP_OK;
+    CHECK_PTR(y, true);
+    CHECK_PTR(bias, false);
+    CHECK_SCALAR(y_amax, false);
+    CHECK_SCALAR(sinv_x, true);
+    CHECK_SCALAR(sinv_w, true);
+    if (K > 0) {
+        CHECK_PTR(x8, true);
+        CHECK_PTR(w8, true);
+    }
+    DeviceInfo dev;
+    const int rc = current_device(&dev);
+    if (rc) return rc;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (K == 0)  // y = bias or 0
+        return launch_gemm(x8, FP8MP_E4M3, w8, FP8MP_E4M3, M, N, K, sinv_x, sinv_w, bias, bias_dtype, y, y_dtype,
+                           y_amax, s, dev);
+    return launch_few_linear(x8, w8, M, N, K, sinv_x, sinv_w, bias, bias_dtype, y, y_dtype, y_amax, s, dev);
+}
+
 int fp8_gated_dgrad(const uint8_t *dy8, const uint8_t *wd8, const uint16_t *gu, int64_t M, int64_t F, int64_t N,
                     int32_t act, int32_t dy_fmt, const float *sinv_dy, const float *sinv_wd, const float *dgu_scale,
                     uint8_t *dgu8, float *dgu_amax, void *stream) {
@@ -974,9 +1007,12 @@ int fp8mp_check(void *stream) {
     if (rc) return rc;
     rc = read_and_clear_cast_timeout_flag(&cflag);
     if (rc) return rc;
-    unsigned int gflag = 0;
+    unsigned int gflag = 0, wflag = 0;
     rc = read_and_clear_gated_timeout_flag(&gflag);
     if (rc) return rc;
+    rc = read_and_clear_few_timeout_flag(&wflag);
+    if (rc) return rc;
+    if (wflag) return fail(FP8MP_ERR_TIMEOUT, "a few-token kernel's bounded wait expired; its output is undefined");
     if (gflag)
         return fail(FP8MP_ERR_TIMEOUT, "a gated feed-forward kernel's bounded wait expired; its output is undefined");
     if (flag) return fail(FP8MP_ERR_TIMEOUT, "a GEMM kernel's bounded wait expired; its output is undefined");

@@ -1,0 +1,376 @@
+// few.cu -- products of FP8 weights with a few tokens (1 to 64): the gated
+// feed-forward block's first half, h = act(x Wg^T) (x Wu^T), and a plain linear,
+// y = x W^T (+ b), as a model that serves runs them token by token.
+//
+// Every weight byte is read once and used for at most 64 products, so the
+// kernel is bound by HBM. It is shaped to keep many weight loads in flight on
+// all SMs rather than to keep the tensor cores busy:
+//   - the weights are the MMA's M operand (128 rows per tile; gated: 64 gate
+//     rows and the 64 up rows of the same outputs), the tokens its N operand
+//     (16, 32 or 64 columns, rows past the last token zero-filled), so a stage
+//     is 16 KB of weights and 2-8 KB of tokens, in a ring of about 108 KB: two
+//     CTAs share an SM and one streams while the other starts or ends;
+//   - a tile's contraction is split over the S CTAs of a cluster (split_for
+//     below); each leaves its fp32 partial sums in its shared memory, and each
+//     adds S-th of the outputs over all of them, in rank order, through
+//     distributed shared memory: no workspace, no atomics on the sums.
+#include <atomic>
+#include <cstring>
+#include <mutex>
+
+#include "fp8mp_gate.cuh"
+#include "fp8mp_mma.cuh"
+
+namespace fp8mp {
+
+__device__ unsigned int g_few_timeout_flag = 0;
+
+namespace {
+
+constexpr int NUM_THREADS = 192;  // producer warp, MMA warp, four epilogue warps
+constexpr int W_ROWS = 128;       // weight rows of a tile
+
+template <int NT>
+struct Cfg {
+    static constexpr int STAGE_BYTES = W_ROWS * BK + NT * BK;
+    static constexpr int STAGES = (108 * 1024) / STAGE_BYTES;
+    static constexpr int PITCH = NT + 4;  // floats per row of the partial sums: conflict-free 16-byte stores
+    static constexpr int BAR_OFFSET = STAGES * STAGE_BYTES;
+    static constexpr int SLOT_OFFSET = BAR_OFFSET + (2 * STAGES + 2) * 8;
+    static constexpr int FLAG_OFFSET = SLOT_OFFSET + 8;
+    static constexpr int SMEM_ALLOC = FLAG_OFFSET + 8 + 1024;
+    static constexpr uint32_t TMEM_COLS = NT < 32 ? 32 : NT;
+    static_assert(W_ROWS * PITCH * 4 <= STAGES * STAGE_BYTES, "the partial sums reuse the ring");
+    static_assert(2 * (SMEM_ALLOC + 1024) <= 233472, "two CTAs per SM");
+};
+
+struct FewParams {
+    CUtensorMap tw0, tw1, tx;  // the weights (gated: gate rows, up rows) and the tokens
+    int rows, outs, num_kb;    // tokens, outputs (gated: F), 128-byte k-blocks
+    uint32_t idesc;
+    const float *sinv_a, *sinv_b;
+    // gated: h as E4M3 under *out_scale or as bf16, gu when saved; linear: y as bf16 or fp32, with a bias
+    const float *out_scale;
+    void *out;
+    uint16_t *gu;
+    const void *bias;
+    int bias_bf16, out_bf16;
+    float *out_amax;
+};
+
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
+    return fp8mp::wait_bounded(bar, parity, abort_flag, &g_few_timeout_flag);
+}
+
+// 16 consecutive fp32 columns of this warp's 32 TMEM lanes.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+// Adds the cluster's partial sums of weight row `row` and token `m`, in rank order.
+template <int NT>
+__device__ __forceinline__ float joined(uint32_t base, int row, int m, uint32_t splits) {
+    const uint32_t at = base + static_cast<uint32_t>((row * Cfg<NT>::PITCH + m) * 4);
+    float s = ld_shared_cluster_f32(mapa_shared(at, 0));
+    for (uint32_t r = 1; r < splits; ++r) s = __fadd_rn(s, ld_shared_cluster_f32(mapa_shared(at, r)));
+    return s;
+}
+
+// GATED: ACT is the activation; otherwise unused.
+template <bool GATED, int ACT, int NT>
+__global__ void __launch_bounds__(NUM_THREADS, 2) few_kernel(const __grid_constant__ FewParams P, uint32_t splits) {
+    using C = Cfg<NT>;
+    extern __shared__ uint8_t smem_raw[];
+    uint32_t base = smem_u32(smem_raw);
+    const uint32_t pad = (1024u - (base & 1023u)) & 1023u;
+    uint8_t *smem = smem_raw + pad;
+    base += pad;
+    const uint32_t bar0 = base + C::BAR_OFFSET;
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (C::STAGES + s); };
+    const uint32_t done_bar = bar0 + 8u * (2 * C::STAGES), drain_bar = done_bar + 8u;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::SLOT_OFFSET);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::FLAG_OFFSET);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = splits > 1 ? cluster_ctarank() : 0u;
+    const int tile = static_cast<int>(blockIdx.x / splits);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        mbar_init(done_bar, 1);
+        mbar_init(drain_bar, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tmap(&P.tw0);
+        if (GATED) prefetch_tmap(&P.tw1);
+        prefetch_tmap(&P.tx);
+    }
+    if (warp == 1) {
+        tmem_alloc<false>(smem_u32(tmem_slot), C::TMEM_COLS);
+        tmem_relinquish<false>();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();
+
+    // this CTA's share of the contraction (never empty: splits <= num_kb)
+    const int kb0 = static_cast<int>(static_cast<int64_t>(P.num_kb) * rank / splits);
+    const int kb1 = static_cast<int>(static_cast<int64_t>(P.num_kb) * (rank + 1) / splits);
+    if (warp == 0) {
+        if (lane == 0) {
+            pdl_launch_dependents();
+            uint32_t it = 0;
+            bool ok = true;
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                const int s = static_cast<int>(it % C::STAGES);
+                if (!wait_bounded(empty_bar(s), ((it / C::STAGES) & 1u) ^ 1u, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t sw = base + s * C::STAGE_BYTES;
+                mbar_arrive_expect_tx(full_bar(s), C::STAGE_BYTES);
+                if constexpr (GATED) {
+                    tma_load_2d<false>(sw, &P.tw0, full_bar(s), kb * BK, tile * 64);
+                    tma_load_2d<false>(sw + 64 * BK, &P.tw1, full_bar(s), kb * BK, tile * 64);
+                } else {
+                    tma_load_2d<false>(sw, &P.tw0, full_bar(s), kb * BK, tile * W_ROWS);
+                }
+                tma_load_2d<false>(sw + W_ROWS * BK, &P.tx, full_bar(s), kb * BK, 0);
+            }
+            if (!ok) {  // let the loads already issued land before the CTA goes away
+                for (uint32_t j = 1; j <= static_cast<uint32_t>(C::STAGES) && j <= it; ++j) {
+                    const uint32_t at = it - j;
+                    volatile int never = 0;
+                    wait_bounded(full_bar(static_cast<int>(at % C::STAGES)), (at / C::STAGES) & 1u, &never);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            bool ok = true;
+            uint32_t it = 0;
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                const int s = static_cast<int>(it % C::STAGES);
+                if (!wait_bounded(full_bar(s), (it / C::STAGES) & 1u, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t sw = base + s * C::STAGE_BYTES;
+#pragma unroll
+                for (int k = 0; k < BK / UMMA_K; ++k)
+                    umma_f8f6f4<false>(tmem, sw128_kmajor_desc(sw + k * UMMA_K),
+                                       sw128_kmajor_desc(sw + W_ROWS * BK + k * UMMA_K), P.idesc,
+                                       (it > 0 || k > 0) ? 1u : 0u);
+                umma_commit_all<false>(empty_bar(s));
+            }
+            umma_commit_all<false>(ok ? done_bar : drain_bar);
+            if (!ok) {  // wait for the MMAs in flight before TMEM is released
+                volatile int never = 0;
+                wait_bounded(drain_bar, 0u, &never);
+            }
+        }
+    } else {
+        int ok = 1;
+        if (lane == 0) ok = wait_bounded(done_bar, 0u, abort_flag) ? 1 : 0;
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (ok) {
+            // every MMA is complete, so every stage has been read: the ring
+            // holds the partial sums from here on
+            tc_fence_after();
+            const int q = warp & 3, row = 32 * q + lane;
+            float *dst = reinterpret_cast<float *>(smem) + row * C::PITCH;
+#pragma unroll
+            for (int c = 0; c < NT; c += 16) {
+                uint32_t r[16];
+                tmem_ld16(tmem + static_cast<uint32_t>(c) + (static_cast<uint32_t>(32 * q) << 16), r);
+#pragma unroll
+                for (int j = 0; j < 16; j += 4)
+                    *reinterpret_cast<uint4 *>(dst + c + j) = make_uint4(r[j], r[j + 1], r[j + 2], r[j + 3]);
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    if (splits > 1)
+        cluster_sync_all();
+    else
+        __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc<false>(tmem, C::TMEM_COLS);
+
+    // this CTA's share of the tile's outputs, all tokens; neighbouring threads take neighbouring outputs
+    const float scale = __fmul_rn(__ldg(P.sinv_a), __ldg(P.sinv_b));
+    constexpr int TILE_OUTS = GATED ? 64 : W_ROWS;
+    const int mine = TILE_OUTS / static_cast<int>(splits);
+    float am = 0.0f;
+    for (int i = threadIdx.x; i < mine * P.rows; i += NUM_THREADS) {
+        const int m = i / mine, o = static_cast<int>(rank) * mine + (i - m * mine);
+        const int64_t col = static_cast<int64_t>(tile) * TILE_OUTS + o;
+        if (col >= P.outs) continue;
+        const float a = joined<NT>(base, o, m, splits);
+        if constexpr (GATED) {
+            const float g = __fmul_rn(a, scale), u = __fmul_rn(joined<NT>(base, 64 + o, m, splits), scale);
+            const float h = gate_act<ACT>(g) * u;
+            am = fmaxf(am, fabsf(h));
+            const int64_t at = static_cast<int64_t>(m) * P.outs + col;
+            if (P.out_scale != nullptr)
+                static_cast<uint8_t *>(P.out)[at] =
+                    static_cast<uint8_t>(cvt_pair<FP8MP_E4M3>(__fmul_rn(h, __ldg(P.out_scale)), 0.0f) & 0xFFu);
+            else
+                static_cast<__nv_bfloat16 *>(P.out)[at] = __float2bfloat16_rn(h);
+            if (P.gu != nullptr) {
+                __nv_bfloat16 *row = reinterpret_cast<__nv_bfloat16 *>(P.gu) + static_cast<int64_t>(m) * 2 * P.outs;
+                row[col] = __float2bfloat16_rn(g);
+                row[P.outs + col] = __float2bfloat16_rn(u);
+            }
+        } else {
+            float y = __fmul_rn(a, scale);
+            if (P.bias != nullptr)
+                y = __fmaf_rn(a, scale,
+                              P.bias_bf16 ? bf16_bits_to_f32(static_cast<const uint16_t *>(P.bias)[col])
+                                          : static_cast<const float *>(P.bias)[col]);
+            const int64_t at = static_cast<int64_t>(m) * P.outs + col;
+            if (P.out_bf16) {
+                const __nv_bfloat16 b = __float2bfloat16_rn(y);
+                static_cast<__nv_bfloat16 *>(P.out)[at] = b;
+                y = __bfloat162float(b);
+            } else {
+                static_cast<float *>(P.out)[at] = y;
+            }
+            am = fmaxf(am, fabsf(y));
+        }
+    }
+    if (P.out_amax != nullptr) block_amax_atomic(am, P.out_amax);
+    if (splits > 1) cluster_sync_all();  // no CTA leaves while a peer may read its sums
+}
+
+// How many CTAs share a tile's contraction. The grid runs two CTAs to an SM;
+// each costs its share of k-blocks and, for starting, filling its ring and
+// joining, about as long as `kFixed` k-blocks of streaming take it. The split
+// with the least (waves of CTAs) x (cost of one) is taken: more CTAs even out
+// the last wave of a few tiles, fewer save fixed costs when there are many.
+constexpr int kFixed = 8;
+
+int split_for(int64_t tiles, int num_kb, int num_sms) {
+    int best = 1;
+    double least = 0.0;
+    for (int s = 1; s <= 8 && s <= num_kb; s *= 2) {
+        const int64_t slots = 2 * static_cast<int64_t>(num_sms);
+        const int64_t waves = (tiles * s + slots - 1) / slots;
+        const double cost = static_cast<double>(waves) * ((num_kb + s - 1) / s + kFixed);
+        if (s == 1 || cost < least) {
+            least = cost;
+            best = s;
+        }
+    }
+    return best;
+}
+
+std::mutex g_prepare_mutex;
+
+template <bool GATED, int ACT, int NT>
+int launch(const FewParams &P, int64_t tiles, int splits, cudaStream_t s, const DeviceInfo &dev) {
+    static std::atomic<bool> ready[64];
+    std::atomic<bool> &mine = ready[dev.device & 63];
+    if (!mine.load(std::memory_order_acquire)) {
+        std::lock_guard<std::mutex> lock(g_prepare_mutex);
+        const cudaError_t e = cudaFuncSetAttribute(few_kernel<GATED, ACT, NT>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<NT>::SMEM_ALLOC);
+        if (e != cudaSuccess) return fail(FP8MP_ERR_LAUNCH, "few: smem attribute failed: %s", cudaGetErrorString(e));
+        mine.store(true, std::memory_order_release);
+    }
+    const cudaError_t e = launch_kernel_cluster(few_kernel<GATED, ACT, NT>, dim3(static_cast<unsigned>(tiles * splits)),
+                                                dim3(NUM_THREADS), Cfg<NT>::SMEM_ALLOC, s,
+                                                static_cast<unsigned>(splits), P, static_cast<uint32_t>(splits));
+    if (e != cudaSuccess) return fail(FP8MP_ERR_LAUNCH, "few: launch failed: %s", cudaGetErrorString(e));
+    return FP8MP_OK;
+}
+
+template <bool GATED, int ACT>
+int launch_tokens(const FewParams &P, int nt, int64_t tiles, int splits, cudaStream_t s, const DeviceInfo &dev) {
+    if (nt == 16) return launch<GATED, ACT, 16>(P, tiles, splits, s, dev);
+    if (nt == 32) return launch<GATED, ACT, 32>(P, tiles, splits, s, dev);
+    return launch<GATED, ACT, 64>(P, tiles, splits, s, dev);
+}
+
+// The operands of rows <= kFewTokens tokens against `outs` outputs (gated: of
+// w8's 2 * outs rows) over K.
+int set_operands(FewParams &P, const uint8_t *x8, const uint8_t *w8, int64_t M, int64_t outs, int64_t K, bool gated,
+                 int nt) {
+    std::memset(&P, 0, sizeof P);
+    P.rows = static_cast<int>(M);
+    P.outs = static_cast<int>(outs);
+    P.num_kb = static_cast<int>((K + BK - 1) / BK);
+    P.idesc = make_idesc(FP8MP_E4M3, FP8MP_E4M3, W_ROWS, nt, 0, 0);
+    const uint64_t m = static_cast<uint64_t>(M), n = static_cast<uint64_t>(outs), k = static_cast<uint64_t>(K);
+    const uint32_t box = gated ? 64 : W_ROWS;
+    int rc = make_box_tmap(&P.tx, x8, 1, k, m, k, BK, static_cast<uint32_t>(nt), true);
+    if (!rc) rc = make_box_tmap(&P.tw0, w8, 1, k, n, k, BK, box, true);
+    if (!rc && gated) rc = make_box_tmap(&P.tw1, w8 + outs * K, 1, k, n, k, BK, box, true);
+    return rc;
+}
+
+int token_columns(int64_t M) { return M <= 16 ? 16 : (M <= 32 ? 32 : 64); }
+
+}  // namespace
+
+int launch_few_gated(const uint8_t *x8, const uint8_t *w8, int64_t M, int64_t F, int64_t K, int act,
+                     const float *sinv_x, const float *sinv_w, const float *h_scale, void *h, float *h_amax,
+                     uint16_t *gu, cudaStream_t s, const DeviceInfo &dev) {
+    FewParams P;
+    const int nt = token_columns(M);
+    const int rc = set_operands(P, x8, w8, M, F, K, true, nt);
+    if (rc) return rc;
+    P.sinv_a = sinv_x;
+    P.sinv_b = sinv_w;
+    P.out_scale = h_scale;
+    P.out = h;
+    P.gu = gu;
+    P.out_amax = h_amax;
+    const int64_t tiles = (F + 63) / 64;
+    const int splits = split_for(tiles, P.num_kb, dev.num_sms);
+    return act == FP8MP_SILU ? launch_tokens<true, FP8MP_SILU>(P, nt, tiles, splits, s, dev)
+                             : launch_tokens<true, FP8MP_GELU_TANH>(P, nt, tiles, splits, s, dev);
+}
+
+int launch_few_linear(const uint8_t *x8, const uint8_t *w8, int64_t M, int64_t N, int64_t K, const float *sinv_x,
+                      const float *sinv_w, const void *bias, int bias_dtype, void *y, int y_dtype, float *y_amax,
+                      cudaStream_t s, const DeviceInfo &dev) {
+    FewParams P;
+    const int nt = token_columns(M);
+    const int rc = set_operands(P, x8, w8, M, N, K, false, nt);
+    if (rc) return rc;
+    P.sinv_a = sinv_x;
+    P.sinv_b = sinv_w;
+    P.out = y;
+    P.out_bf16 = y_dtype == FP8MP_BF16;
+    P.bias = bias;
+    P.bias_bf16 = bias_dtype == FP8MP_BF16;
+    P.out_amax = y_amax;
+    const int64_t tiles = (N + W_ROWS - 1) / W_ROWS;
+    return launch_tokens<false, FP8MP_SILU>(P, nt, tiles, split_for(tiles, P.num_kb, dev.num_sms), s, dev);
+}
+
+int read_and_clear_few_timeout_flag(unsigned int *value) {
+    unsigned int v = 0, zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_few_timeout_flag, sizeof v);
+    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_few_timeout_flag, &zero, sizeof zero);
+    if (e != cudaSuccess) return fail(FP8MP_ERR_LAUNCH, "reading the timeout flag failed: %s", cudaGetErrorString(e));
+    *value = v;
+    return FP8MP_OK;
+}
+
+}  // namespace fp8mp

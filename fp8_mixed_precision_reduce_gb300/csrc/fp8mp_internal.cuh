@@ -193,6 +193,15 @@ int launch_gated_dgrad(const uint8_t *dy8, const uint8_t *wd8, const uint16_t *g
 int launch_gate_bwd(const void *dh, int dh_dtype, const uint16_t *gu, int64_t M, int64_t F, int act,
                     const float *dgu_scale, uint8_t *dgu8, float *dgu_amax, cudaStream_t s, const DeviceInfo &dev);
 int read_and_clear_gated_timeout_flag(unsigned int *value);
+// Products with at most kFewTokens tokens (few.cu; sizes > 0, arguments validated).
+constexpr int64_t kFewTokens = 64;
+int launch_few_gated(const uint8_t *x8, const uint8_t *w8, int64_t M, int64_t F, int64_t K, int act,
+                     const float *sinv_x, const float *sinv_w, const float *h_scale, void *h, float *h_amax,
+                     uint16_t *gu, cudaStream_t s, const DeviceInfo &dev);
+int launch_few_linear(const uint8_t *x8, const uint8_t *w8, int64_t M, int64_t N, int64_t K, const float *sinv_x,
+                      const float *sinv_w, const void *bias, int bias_dtype, void *y, int y_dtype, float *y_amax,
+                      cudaStream_t s, const DeviceInfo &dev);
+int read_and_clear_few_timeout_flag(unsigned int *value);
 // The many-tensor AdamW step (adamw.cu): its workspace, the most elements a
 // call may hold, the gradients' norm and the step (arguments validated).
 struct AdamwArgs {

@@ -637,6 +637,21 @@ int fp8_gated_fwd(const uint8_t *x8, const uint8_t *w8, int64_t M, int64_t F, in
                   const float *sinv_x, const float *sinv_w, const float *h_scale, void *h, float *h_amax,
                   uint16_t *gu, void *stream);
 
+/* Most tokens of fp8_linear_few. */
+#define FP8MP_FEW_TOKENS 64
+
+/*
+ * fp8_linear_few -- fp8_linear_fwd for a few tokens, any number of them up to
+ * FP8MP_FEW_TOKENS (fp8_linear_fwd takes multiples of 16): the same y, with
+ * the contraction split over several SMs so that the weight is read at the
+ * memory's rate (its partial sums are added in fp32 in a fixed order). The
+ * down projection of a gated block when serving.
+ * N and K multiples of 16. M == 0 or N == 0: no-op. K == 0: y = bias (or 0).
+ */
+int fp8_linear_few(const uint8_t *x8, const uint8_t *w8, int64_t M, int64_t N, int64_t K, const float *sinv_x,
+                   const float *sinv_w, const void *bias, int32_t bias_dtype, void *y, int32_t y_dtype,
+                   float *y_amax, void *stream);
+
 /*
  * fp8_gated_dgrad -- back through the down projection and the gate in one
  * launch, without storing dh:

@@ -181,6 +181,57 @@ def test_saturating_preactivations(cuda_lib):
         assert torch.equal(h.double().cpu(), want.bfloat16().double().expand(4, 32))
 
 
+# -------------------------------------------------------- a few tokens' linear
+
+
+@pytest.mark.parametrize("y_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("bias", [None, torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,N,K", [(1, 16, 16), (1, 4096, 14336), (2, 48, 80), (5, 144, 4112), (16, 128, 128),
+                                   (17, 2064, 768), (33, 6000, 1552), (64, 400, 2064), (64, 16, 16), (63, 30000, 144)])
+def test_linear_few(cuda_lib, M, N, K, bias, y_dtype):
+    g = gen(M + N + K)
+    x8, sx = codes((M, K), 1.0, 64.0, E4M3, g)
+    w8, sw = codes((N, K), 1.0 / K ** 0.5, 32.0 * K ** 0.5, E4M3, g)
+    b = torch.randn(N, generator=g, device="cuda").to(bias) if bias is not None else None
+    y = torch.full((M, N), 5.0, dtype=y_dtype, device="cuda")
+    amax = torch.zeros(1, device="cuda")
+    cuda_lib.fp8_linear_few(x8, w8, sx, sw, y, bias=b, y_amax=amax)
+    assert cuda_lib.fp8mp_check() == 0
+    s = (sx * sw).double().item()
+    ref, size = (wide(x8, E4M3) @ wide(w8, E4M3).T) * s, (wide(x8, E4M3).abs() @ wide(w8, E4M3).abs().T) * s
+    if b is not None:
+        ref, size = ref + b.double(), size + b.double().abs()
+    D = 1e-5 * size + 2.0 ** -22 * ref.abs()
+    between(y.double(), (ref - D).to(y_dtype).double(), (ref + D).to(y_dtype).double(), "y")
+    assert amax.item() == y.abs().max().item()
+    again = torch.empty_like(y)
+    for _ in range(5):
+        cuda_lib.fp8_linear_few(x8, w8, sx, sw, again, bias=b)
+        assert torch.equal(y, again)
+
+
+def test_linear_few_equals_the_linear_where_both_run(cuda_lib):
+    """Whole numbers whose sums are exact in fp32: the split changes nothing."""
+    g = gen(8)
+    x8 = torch.randint(0, 2, (32, 4096), generator=g, device="cuda", dtype=torch.uint8) * 0x38  # 0 or 1
+    w8 = torch.randint(0, 2, (272, 4096), generator=g, device="cuda", dtype=torch.uint8) * 0x38 + 0
+    one = torch.ones(1, device="cuda")
+    a, b = torch.empty((32, 272), device="cuda"), torch.empty((32, 272), device="cuda")
+    cuda_lib.fp8_linear_fwd(x8, w8, one, one, a)
+    cuda_lib.fp8_linear_few(x8, w8, one, one, b)
+    assert torch.equal(a, b) and a.max() > 100
+
+
+def test_linear_few_of_nothing(cuda_lib):
+    z = lambda *s: torch.zeros(s, dtype=torch.uint8, device="cuda")  # noqa: E731
+    one, b = torch.ones(1, device="cuda"), torch.arange(32, device="cuda", dtype=torch.float32)
+    cuda_lib.fp8_linear_few(z(0, 64), z(32, 64), one, one, torch.empty((0, 32), device="cuda"))
+    y = torch.full((3, 32), 7.0, device="cuda")
+    cuda_lib.fp8_linear_few(z(3, 0), z(32, 0), one, one, y, bias=b)
+    assert torch.equal(y, b.expand(3, 32))
+    assert cuda_lib.fp8mp_check() == 0
+
+
 # ---------------------------------------------------------------- backward
 
 

@@ -60,6 +60,17 @@ def test_backward(lib, kw, word):
     assert word in fp8mp.last_error(), fp8mp.last_error()
 
 
+@pytest.mark.parametrize("kw,word", [
+    (dict(M=65), "outside 0..64"), (dict(M=-1), "outside"), (dict(N=24), "multiples of 16"), (dict(K=8), "multiples of 16"),
+    (dict(N=1 << 31), "2^30"), (dict(y=None), "y is NULL"), (dict(y_dtype=4), "y_dtype"), (dict(bias=P, bias_dtype=4), "bias_dtype"),
+    (dict(x8=P + 1), "aligned"), (dict(w8=None), "w8"), (dict(sx=None), "sinv_x"), (dict(amax=P + 1), "misaligned")])
+def test_linear_few(lib, kw, word):
+    a = dict(x8=P, w8=P, M=5, N=32, K=48, sx=P, sw=P, bias=None, bias_dtype=0, y=P, y_dtype=1, amax=None)
+    a.update(kw)
+    assert lib.fp8_linear_few(*a.values(), None) == fp8mp.ERR_INVALID
+    assert word in fp8mp.last_error(), fp8mp.last_error()
+
+
 def test_nothing_to_do_needs_no_device(lib):
     assert fwd(lib, M=0, x8=None, h=None) == fp8mp.OK
     assert fwd(lib, F=0, w8=None, h=None) == fp8mp.OK
