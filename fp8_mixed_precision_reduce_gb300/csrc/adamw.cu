@@ -14,6 +14,7 @@
 // with fp32 moments, 15.06 B with 8-bit ones).
 #include <cstring>
 
+#include "fp8mp_f32x2.cuh"
 #include "fp8mp_internal.cuh"
 
 namespace fp8mp {
@@ -280,6 +281,21 @@ __device__ __forceinline__ float quantize(float y, float r) {
 constexpr float kLevelsM = 16129.0f;       // 127^2
 constexpr float kLevelsV = 4228250624.0f;  // 255^4, rounded to fp32
 
+// The codes of one element's moments, in the last bytes: im and iv are the
+// levels over the block's largest moments (0 for a block of zeros), `counter`
+// the element's place in the random stream.
+__device__ __forceinline__ void quantize_both(float m, float v, float im, float iv, uint32_t counter, uint32_t &cm,
+                                              uint32_t &cv) {
+    const uint32_t h = mix32(counter);
+    const float rm = __fmul_rn(static_cast<float>(h & 0xFFFFu), 0x1p-16f);
+    const float rv = __fmul_rn(static_cast<float>(h >> 16), 0x1p-16f);
+    const float qm = quantize<false>(__fmul_rn(fabsf(m), im), rm);
+    float qv = quantize<true>(__fmul_rn(v, iv), rv);
+    if (v > 0.0f && iv > 0.0f) qv = fmaxf(qv, 1.0f);  // v stays above 0 where it was: m / sqrt(v) stays bounded
+    cm = static_cast<uint32_t>(static_cast<int>(m < 0.0f ? -qm : qm)) & 0xFFu;
+    cv = static_cast<uint32_t>(qv);
+}
+
 // One unit of 8 elements per lane: cnt of them exist (8 but at a tensor's end).
 __device__ __forceinline__ void load8(const float *p, int cnt, float (&x)[8]) {
     if (cnt == 8) {
@@ -357,6 +373,164 @@ __device__ __forceinline__ void store_copy(const StepTensor &T, int64_t at, int 
     }
 }
 
+// A whole unit with 8-bit moments. Per parameter it moves 15 bytes, which
+// leaves about 80 instructions at the memory's rate, so the arithmetic is done
+// two lanes at a time where it can be, and the codes are made without
+// conversions:
+//   - a byte joins the exponent of 2^23 (a byte permute) and loses it again (an
+//     add): the code as fp32; a 16-bit random number joins that of 128, whose
+//     last place is 2^-16;
+//   - fma.rz(root, 1 - 2^-21, 2^23) is 2^23 + c with c the code sought or one
+//     below: the roots are good to 2^-22. Its last byte is the code. One below,
+//     the remainder e = y - c^p reaches the cell's width d and the code always
+//     steps up to the one sought; should it step once more, r (the next cell's
+//     width) < e - d, then r d < e - d too (e, d and e - d are exact): a lane
+//     that meets that does its eight again with quantize(). So the codes are
+//     those of the definition, and where they have to be exact does not depend on
+//     the root's error. (Testing e >= d alone sent nearly every warp that way
+//     when the gradients are small: all moments then decay alike and y stays next
+//     to c^p.)
+__device__ __forceinline__ float sqrt_ftz(float x) {
+    float r;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp_ftz(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint64_t f2_same(float x) { return f2_pack(x, x); }
+// Byte `sel` of x, as 2^23 + byte.
+__device__ __forceinline__ uint32_t byte_on_2_23(uint32_t x, uint32_t sel) {
+    return __byte_perm(x, 0x4B000000u, 0x7650u | sel);
+}
+__device__ __forceinline__ void unit_8_bits(const StepTensor &T, int64_t at, int64_t unit, const Scalars &s,
+                                            float shrink, uint32_t key, float &am) {
+    const int lane = threadIdx.x & 31;
+    float g[8], w[8];
+    load_grad(T, at, 8, g);
+    load8(T.w + at, 8, w);
+    const uint2 cm = load_bytes(static_cast<const uint8_t *>(T.m) + at, 8);
+    const uint2 cv = load_bytes(static_cast<const uint8_t *>(T.v) + at, 8);
+    const uint64_t sm = f2_same(__ldg(T.sm + unit)), sv = f2_same(__ldg(T.sv + unit));
+    uint64_t m2[4], v2[4];
+    float mmax = 0.0f, vmax = 0.0f;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        const uint32_t bm = (p < 2 ? cm.x : cm.y) ^ 0x80808080u, bv = p < 2 ? cv.x : cv.y;
+        const uint32_t b0 = (2 * p) & 3, b1 = b0 + 1;
+        // codes as fp32: a signed one is a byte 128 higher
+        const uint64_t fm = f2_add(f2_from_bits(byte_on_2_23(bm, b0), byte_on_2_23(bm, b1)), f2_same(-8388736.0f));
+        const uint64_t fv = f2_add(f2_from_bits(byte_on_2_23(bv, b0), byte_on_2_23(bv, b1)), f2_same(-8388608.0f));
+        float f0, f1;
+        f2_split(fm, f0, f1);
+        const uint64_t sq = f2_mul(fv, fv);
+        uint64_t m = f2_mul(f2_pack(__fmul_rn(f0, fabsf(f0)), __fmul_rn(f1, fabsf(f1))), sm);
+        uint64_t v = f2_mul(f2_mul(sq, sq), sv);
+        const uint64_t u = f2_mul(f2_pack(g[2 * p], g[2 * p + 1]), f2_same(s.coef));
+        m = f2_add(f2_mul(m, f2_same(s.b1)), f2_mul(u, f2_same(s.c1)));
+        v = f2_add(f2_mul(v, f2_same(s.b2)), f2_mul(f2_mul(u, u), f2_same(s.c2)));
+        m2[p] = m;
+        v2[p] = v;
+        float m0, m1, v0, v1, d0, d1;
+        f2_split(m, m0, m1);
+        f2_split(v, v0, v1);
+        f2_split(f2_fma(f2_pack(sqrt_ftz(v0), sqrt_ftz(v1)), f2_same(s.root), f2_same(s.eps)), d0, d1);
+        const uint64_t q = f2_mul(m, f2_pack(rcp_ftz(d0), rcp_ftz(d1)));
+        f2_split(f2_fma(f2_same(-s.step), q, f2_mul(f2_pack(w[2 * p], w[2 * p + 1]), f2_same(shrink))), w[2 * p],
+                 w[2 * p + 1]);
+        mmax = fmaxf(mmax, fmaxf(fabsf(m0), fabsf(m1)));
+        vmax = fmaxf(vmax, fmaxf(v0, v1));
+        am = fmaxf(am, fmaxf(fabsf(w[2 * p]), fabsf(w[2 * p + 1])));
+    }
+    store8(T.w + at, 8, w);
+    store_copy(T, at, 8, w);
+    mmax = warp_max(mmax);
+    vmax = warp_max(vmax);
+    mmax = mmax >= 0x1p-100f ? mmax : 0.0f;
+    vmax = vmax >= 0x1p-90f ? vmax : 0.0f;
+    const float im = mmax > 0.0f ? __fdiv_rn(kLevelsM, mmax) : 0.0f;
+    const float iv = vmax > 0.0f ? __fdiv_rn(kLevelsV, vmax) : 0.0f;
+    const uint32_t base = key + static_cast<uint32_t>(at) +
+                          static_cast<uint32_t>(static_cast<uint64_t>(at) >> 32) * 0x85EBCA77u;
+    const uint64_t below = f2_same(1.0f - 0x1p-21f), one = f2_same(1.0f), minus = f2_same(-1.0f);
+    const uint64_t on = f2_same(8388608.0f), off = f2_same(-8388608.0f);
+    uint32_t om[4], ov[4];  // the codes of elements 2p and 2p + 1, in the last two bytes
+    bool again = false;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        const uint32_t h0 = mix32(base + 2 * p), h1 = mix32(base + 2 * p + 1);
+        const uint64_t rm = f2_add(f2_from_bits(__byte_perm(h0, 0x43000000u, 0x7610u),
+                                                __byte_perm(h1, 0x43000000u, 0x7610u)), f2_same(-128.0f));
+        const uint64_t rv = f2_add(f2_from_bits(__byte_perm(h0, 0x43000000u, 0x7632u),
+                                                __byte_perm(h1, 0x43000000u, 0x7632u)), f2_same(-128.0f));
+        float m0, m1, v0, v1, y0, y1, s0, s1, x0, x1, e0, e1, t0, t1;
+        f2_split(m2[p], m0, m1);
+        f2_split(v2[p], v0, v1);
+        {  // |m|: (c + 1)^2 - c^2 = 2 c + 1
+            const uint64_t y = f2_mul(f2_pack(fabsf(m0), fabsf(m1)), f2_same(im));
+            f2_split(y, y0, y1);
+            const uint64_t t = f2_fma_rz(f2_pack(sqrt_ftz(y0), sqrt_ftz(y1)), below, on);
+            const uint64_t c = f2_add(t, off), d = f2_fma(c, f2_same(2.0f), one);
+            const uint64_t e = f2_fma(f2_mul(c, c), minus, y);
+            f2_split(e, e0, e1);
+            f2_split(f2_mul(rm, d), s0, s1);
+            f2_split(f2_fma(d, minus, e), x0, x1);
+            f2_split(t, t0, t1);
+            again |= (s0 < x0) | (s1 < x1);
+            const uint32_t n0 = static_cast<uint32_t>(__float_as_int(m0) >> 31);
+            const uint32_t n1 = static_cast<uint32_t>(__float_as_int(m1) >> 31);
+            const uint32_t c0 = __float_as_uint(t0) + (s0 < e0 ? 1u : 0u);
+            const uint32_t c1 = __float_as_uint(t1) + (s1 < e1 ? 1u : 0u);
+            om[p] = __byte_perm((c0 ^ n0) - n0, (c1 ^ n1) - n1, 0x0040u);
+        }
+        {
+            const uint64_t y = f2_mul(v2[p], f2_same(iv));
+            f2_split(y, y0, y1);
+            const uint64_t t = f2_fma_rz(f2_pack(sqrt_ftz(sqrt_ftz(y0)), sqrt_ftz(sqrt_ftz(y1))), below, on);
+            const uint64_t c = f2_add(t, off), up = f2_add(c, one);
+            const uint64_t q = f2_mul(c, c), lo = f2_mul(q, q), q1 = f2_mul(up, up);
+            const uint64_t d = f2_fma(lo, minus, f2_mul(q1, q1));
+            const uint64_t e = f2_fma(lo, minus, y);
+            f2_split(e, e0, e1);
+            f2_split(f2_mul(rv, d), s0, s1);
+            f2_split(f2_fma(d, minus, e), x0, x1);
+            f2_split(t, t0, t1);
+            again |= (s0 < x0) | (s1 < x1);
+            // a v above 0 keeps a code above 0
+            const uint32_t c0 = max(__float_as_uint(t0) + (s0 < e0 ? 1u : 0u),
+                                    0x4B000000u + min(__float_as_uint(v0), 1u));
+            const uint32_t c1 = max(__float_as_uint(t1) + (s1 < e1 ? 1u : 0u),
+                                    0x4B000000u + min(__float_as_uint(v1), 1u));
+            ov[p] = __byte_perm(c0, c1, 0x0040u);
+        }
+    }
+    if (again) {
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            uint32_t cm2[2], cv2[2];
+            float m[2], v[2];
+            f2_split(m2[p], m[0], m[1]);
+            f2_split(v2[p], v[0], v[1]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) quantize_both(m[j], v[j], im, iv, base + 2 * p + j, cm2[j], cv2[j]);
+            om[p] = __byte_perm(cm2[0], cm2[1], 0x0040u);
+            ov[p] = __byte_perm(cv2[0], cv2[1], 0x0040u);
+        }
+    }
+    const bool none = vmax == 0.0f;
+    store_bytes(static_cast<uint8_t *>(T.m) + at, 8,
+                make_uint2(__byte_perm(om[0], om[1], 0x5410u), __byte_perm(om[2], om[3], 0x5410u)));
+    store_bytes(static_cast<uint8_t *>(T.v) + at, 8,
+                make_uint2(none ? 0u : __byte_perm(ov[0], ov[1], 0x5410u),
+                           none ? 0u : __byte_perm(ov[2], ov[3], 0x5410u)));
+    if (lane == 0) {
+        T.sm[unit] = __fdiv_rn(mmax, kLevelsM);
+        T.sv[unit] = __fdiv_rn(vmax, kLevelsV);
+    }
+}
+
 // Both kinds of moments share the walk; BITS is the moments' width.
 // The warp's 256 elements of a unit are one block of the 8-bit moments, so a
 // block's largest moment is a warp reduction and nothing leaves the warp.
@@ -390,6 +564,12 @@ adamw_kernel(const __grid_constant__ StepBatch<CAP> batch, const StepArgs a) {
             const int64_t unit = static_cast<int64_t>(c - batch.first[t]) * (kThreads / 32) + warp;
             const int64_t at = unit * kUnit + 8 * lane;
             if (unit * kUnit >= T.n) continue;  // the whole warp: past the tensor's end
+            if constexpr (BITS == 8) {
+                if (unit * kUnit + kUnit <= T.n) {
+                    unit_8_bits(T, at, unit, s, shrink, key, am);
+                    continue;
+                }
+            }
             const int64_t left = T.n - at;
             const int cnt = left >= 8 ? 8 : (left > 0 ? static_cast<int>(left) : 0);
             float g[8], w[8], m[8], v[8];
@@ -423,19 +603,14 @@ adamw_kernel(const __grid_constant__ StepBatch<CAP> batch, const StepArgs a) {
                 const float im = mmax > 0.0f ? __fdiv_rn(kLevelsM, mmax) : 0.0f;
                 const float iv = vmax > 0.0f ? __fdiv_rn(kLevelsV, vmax) : 0.0f;
                 uint32_t om[2] = {0u, 0u}, ov[2] = {0u, 0u};
+                const uint32_t base = key + static_cast<uint32_t>(at) +
+                                      static_cast<uint32_t>(static_cast<uint64_t>(at) >> 32) * 0x85EBCA77u;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const uint64_t i = static_cast<uint64_t>(at + j);
-                    const uint32_t h =
-                        mix32(key + static_cast<uint32_t>(i) + static_cast<uint32_t>(i >> 32) * 0x85EBCA77u);
-                    const float rm = __fmul_rn(static_cast<float>(h & 0xFFFFu), 0x1p-16f);
-                    const float rv = __fmul_rn(static_cast<float>(h >> 16), 0x1p-16f);
-                    const float qm = quantize<false>(__fmul_rn(fabsf(m[j]), im), rm);
-                    float qv = quantize<true>(__fmul_rn(v[j], iv), rv);
-                    if (v[j] > 0.0f && vmax > 0.0f) qv = fmaxf(qv, 1.0f);  // v stays above 0 where it was: m / sqrt(v) stays bounded
-                    const int km = static_cast<int>(m[j] < 0.0f ? -qm : qm);
-                    om[j >> 2] |= (static_cast<uint32_t>(km) & 0xFFu) << (8 * (j & 3));
-                    ov[j >> 2] |= static_cast<uint32_t>(qv) << (8 * (j & 3));
+                    uint32_t qm, qv;
+                    quantize_both(m[j], v[j], im, iv, base + j, qm, qv);
+                    om[j >> 2] |= qm << (8 * (j & 3));
+                    ov[j >> 2] |= qv << (8 * (j & 3));
                 }
                 store_bytes(static_cast<uint8_t *>(T.m) + at, cnt, make_uint2(om[0], om[1]));
                 store_bytes(static_cast<uint8_t *>(T.v) + at, cnt, make_uint2(ov[0], ov[1]));

@@ -15,6 +15,7 @@
 #include <mutex>
 
 #include "fp8mp_async.cuh"
+#include "fp8mp_f32x2.cuh"
 
 namespace fp8mp {
 
@@ -390,28 +391,6 @@ struct TileCfg {
 };
 
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-
-// Pairs of fp32 values in one 64-bit register (low lane first) and the
-// two-lane fp32 arithmetic of sm_100-class GPUs: each lane is one IEEE
-// round-to-nearest-even operation, bit-identical to the scalar one.
-__device__ __forceinline__ uint64_t f2_from_bits(uint32_t lo, uint32_t hi) {
-    uint64_t d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
-    return d;
-}
-__device__ __forceinline__ void f2_split(uint64_t v, float &lo, float &hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
 
 // Two (lo, hi) pairs -> four codes under scale2 = (scale, scale); the pairs
 // join the column sums and their |x| the running amax. NaN inputs give NaN
