@@ -347,13 +347,27 @@ __device__ __forceinline__ void load_grad(const StepTensor &T, int64_t at, int c
         for (int j = 0; j < 8; ++j) g[j] = j < cnt ? bf16_bits_to_f32(p[j]) : 0.0f;
     }
 }
+// cvt_quad, with NaN looked for in the packed codes: a byte's low 7 bits plus 1
+// reach 0x80 for the NaN code alone, which is then rewritten to 0x7F.
+__device__ __forceinline__ uint32_t cvt_quad_e4m3(float a, float b, float c, float d) {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    uint32_t q = lo | (static_cast<uint32_t>(hi) << 16);
+    const uint32_t nan = ((q & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+    if (nan != 0u) {
+        const uint32_t bytes = (nan >> 7) * 0xFFu;
+        q = (q & ~bytes) | (0x7F7F7F7Fu & bytes);
+    }
+    return q;
+}
 __device__ __forceinline__ void store_copy(const StepTensor &T, int64_t at, int cnt, const float (&w)[8]) {
     if (T.copy_kind == 2) {
         const float sw = __ldg(T.copy_scale);
-        const uint2 q = make_uint2(cvt_quad<FP8MP_E4M3>(__fmul_rn(w[0], sw), __fmul_rn(w[1], sw), __fmul_rn(w[2], sw),
-                                                        __fmul_rn(w[3], sw)),
-                                   cvt_quad<FP8MP_E4M3>(__fmul_rn(w[4], sw), __fmul_rn(w[5], sw), __fmul_rn(w[6], sw),
-                                                        __fmul_rn(w[7], sw)));
+        const uint2 q = make_uint2(cvt_quad_e4m3(__fmul_rn(w[0], sw), __fmul_rn(w[1], sw), __fmul_rn(w[2], sw),
+                                                 __fmul_rn(w[3], sw)),
+                                   cvt_quad_e4m3(__fmul_rn(w[4], sw), __fmul_rn(w[5], sw), __fmul_rn(w[6], sw),
+                                                 __fmul_rn(w[7], sw)));
         store_bytes(static_cast<uint8_t *>(T.copy) + at, cnt, q);
     } else if (T.copy_kind == 1) {
         __nv_bfloat16 *p = static_cast<__nv_bfloat16 *>(T.copy) + at;
@@ -401,6 +415,29 @@ __device__ __forceinline__ float rcp_ftz(float x) {
     return r;
 }
 __device__ __forceinline__ uint64_t f2_same(float x) { return f2_pack(x, x); }
+// Largest of the warp's values >= 0 (whose bits order as they do).
+__device__ __forceinline__ float warp_max_bits(float x) {
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));
+}
+// 0xFF or 0 in the last two bytes for the signs of a and b.
+__device__ __forceinline__ uint32_t sign_bytes(float a, float b) {
+    uint32_t r;
+    asm("prmt.b32 %0, %1, %2, 0xBBFB;" : "=r"(r) : "r"(__float_as_uint(a)), "r"(__float_as_uint(b)));
+    return r;
+}
+// The last bytes of t's lanes, one more where s < e, in the last two bytes of the
+// result; `again` collects in its first bit whether s < e - d anywhere. Signs of
+// differences stand for the comparisons.
+__device__ __forceinline__ uint32_t stepped(uint64_t t, uint64_t s, uint64_t d, uint64_t e, uint32_t &again) {
+    const uint64_t minus = f2_pack(-1.0f, -1.0f);
+    float t0, t1, z0, z1, x0, x1;
+    f2_split(t, t0, t1);
+    f2_split(f2_fma(e, minus, s), z0, z1);
+    f2_split(f2_fma(f2_fma(d, minus, e), minus, s), x0, x1);
+    again |= __float_as_uint(x0) | __float_as_uint(x1);
+    return __byte_perm(__float_as_uint(t0) + (__float_as_uint(z0) >> 31),
+                       __float_as_uint(t1) + (__float_as_uint(z1) >> 31), 0x0040u);
+}
 // Byte `sel` of x, as 2^23 + byte.
 __device__ __forceinline__ uint32_t byte_on_2_23(uint32_t x, uint32_t sel) {
     return __byte_perm(x, 0x4B000000u, 0x7650u | sel);
@@ -446,18 +483,23 @@ __device__ __forceinline__ void unit_8_bits(const StepTensor &T, int64_t at, int
     }
     store8(T.w + at, 8, w);
     store_copy(T, at, 8, w);
-    mmax = warp_max(mmax);
-    vmax = warp_max(vmax);
+    mmax = warp_max_bits(mmax);
+    vmax = warp_max_bits(vmax);
     mmax = mmax >= 0x1p-100f ? mmax : 0.0f;
     vmax = vmax >= 0x1p-90f ? vmax : 0.0f;
-    const float im = mmax > 0.0f ? __fdiv_rn(kLevelsM, mmax) : 0.0f;
-    const float iv = vmax > 0.0f ? __fdiv_rn(kLevelsV, vmax) : 0.0f;
+    // the block's four quotients in one division: lanes 0 and 1 the levels over
+    // the maxima, lanes 2 and 3 the steps
+    const float top = lane & 1 ? vmax : mmax, levels = lane & 1 ? kLevelsV : kLevelsM;
+    float ratio = __fdiv_rn(lane & 2 ? top : levels, lane & 2 ? levels : top);
+    if (lane < 2 && top == 0.0f) ratio = 0.0f;
+    const float im = __shfl_sync(0xffffffffu, ratio, 0), iv = __shfl_sync(0xffffffffu, ratio, 1);
+    if ((lane & ~1) == 2) (lane == 2 ? T.sm : T.sv)[unit] = ratio;
     const uint32_t base = key + static_cast<uint32_t>(at) +
                           static_cast<uint32_t>(static_cast<uint64_t>(at) >> 32) * 0x85EBCA77u;
     const uint64_t below = f2_same(1.0f - 0x1p-21f), one = f2_same(1.0f), minus = f2_same(-1.0f);
     const uint64_t on = f2_same(8388608.0f), off = f2_same(-8388608.0f);
     uint32_t om[4], ov[4];  // the codes of elements 2p and 2p + 1, in the last two bytes
-    bool again = false;
+    uint32_t again = 0u;    // its first bit: a step up that has to be looked at
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
         const uint32_t h0 = mix32(base + 2 * p), h1 = mix32(base + 2 * p + 1);
@@ -465,25 +507,15 @@ __device__ __forceinline__ void unit_8_bits(const StepTensor &T, int64_t at, int
                                                 __byte_perm(h1, 0x43000000u, 0x7610u)), f2_same(-128.0f));
         const uint64_t rv = f2_add(f2_from_bits(__byte_perm(h0, 0x43000000u, 0x7632u),
                                                 __byte_perm(h1, 0x43000000u, 0x7632u)), f2_same(-128.0f));
-        float m0, m1, v0, v1, y0, y1, s0, s1, x0, x1, e0, e1, t0, t1;
+        float m0, m1, y0, y1;
         f2_split(m2[p], m0, m1);
-        f2_split(v2[p], v0, v1);
         {  // |m|: (c + 1)^2 - c^2 = 2 c + 1
             const uint64_t y = f2_mul(f2_pack(fabsf(m0), fabsf(m1)), f2_same(im));
             f2_split(y, y0, y1);
             const uint64_t t = f2_fma_rz(f2_pack(sqrt_ftz(y0), sqrt_ftz(y1)), below, on);
             const uint64_t c = f2_add(t, off), d = f2_fma(c, f2_same(2.0f), one);
             const uint64_t e = f2_fma(f2_mul(c, c), minus, y);
-            f2_split(e, e0, e1);
-            f2_split(f2_mul(rm, d), s0, s1);
-            f2_split(f2_fma(d, minus, e), x0, x1);
-            f2_split(t, t0, t1);
-            again |= (s0 < x0) | (s1 < x1);
-            const uint32_t n0 = static_cast<uint32_t>(__float_as_int(m0) >> 31);
-            const uint32_t n1 = static_cast<uint32_t>(__float_as_int(m1) >> 31);
-            const uint32_t c0 = __float_as_uint(t0) + (s0 < e0 ? 1u : 0u);
-            const uint32_t c1 = __float_as_uint(t1) + (s1 < e1 ? 1u : 0u);
-            om[p] = __byte_perm((c0 ^ n0) - n0, (c1 ^ n1) - n1, 0x0040u);
+            om[p] = stepped(t, f2_mul(rm, d), d, e, again);
         }
         {
             const uint64_t y = f2_mul(v2[p], f2_same(iv));
@@ -493,49 +525,56 @@ __device__ __forceinline__ void unit_8_bits(const StepTensor &T, int64_t at, int
             const uint64_t q = f2_mul(c, c), lo = f2_mul(q, q), q1 = f2_mul(up, up);
             const uint64_t d = f2_fma(lo, minus, f2_mul(q1, q1));
             const uint64_t e = f2_fma(lo, minus, y);
-            f2_split(e, e0, e1);
-            f2_split(f2_mul(rv, d), s0, s1);
-            f2_split(f2_fma(d, minus, e), x0, x1);
-            f2_split(t, t0, t1);
-            again |= (s0 < x0) | (s1 < x1);
-            // a v above 0 keeps a code above 0
-            const uint32_t c0 = max(__float_as_uint(t0) + (s0 < e0 ? 1u : 0u),
-                                    0x4B000000u + min(__float_as_uint(v0), 1u));
-            const uint32_t c1 = max(__float_as_uint(t1) + (s1 < e1 ? 1u : 0u),
-                                    0x4B000000u + min(__float_as_uint(v1), 1u));
-            ov[p] = __byte_perm(c0, c1, 0x0040u);
+            ov[p] = stepped(t, f2_mul(rv, d), d, e, again);
         }
     }
-    if (again) {
+    uint32_t wm[2], wv[2];
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-            uint32_t cm2[2], cv2[2];
-            float m[2], v[2];
-            f2_split(m2[p], m[0], m[1]);
-            f2_split(v2[p], v[0], v[1]);
+    for (int h = 0; h < 2; ++h) {
+        // the signs of four elements, one byte each, and |c| negated where they are set
+        float a0, a1, a2, a3;
+        f2_split(m2[2 * h], a0, a1);
+        f2_split(m2[2 * h + 1], a2, a3);
+        const uint32_t neg = __byte_perm(sign_bytes(a0, a1), sign_bytes(a2, a3), 0x5410u);
+        const uint32_t x = __byte_perm(om[2 * h], om[2 * h + 1], 0x5410u) ^ neg;
+        wm[h] = ((x & 0x7F7F7F7Fu) + (neg & 0x01010101u)) ^ (x & 0x80808080u);
+        wv[h] = __byte_perm(ov[2 * h], ov[2 * h + 1], 0x5410u);
+    }
+    // (x - 1) & ~x has a byte's last bit set where the first zero byte is
+    const uint32_t zero = (((wv[0] - 0x01010101u) & ~wv[0]) | ((wv[1] - 0x01010101u) & ~wv[1])) & 0x80808080u;
+    if (zero != 0u && iv > 0.0f) {  // the code 0 is for v = 0 alone
 #pragma unroll
-            for (int j = 0; j < 2; ++j) quantize_both(m[j], v[j], im, iv, base + 2 * p + j, cm2[j], cv2[j]);
-            om[p] = __byte_perm(cm2[0], cm2[1], 0x0040u);
-            ov[p] = __byte_perm(cv2[0], cv2[1], 0x0040u);
+        for (int j = 0; j < 8; ++j) {
+            float v[2];
+            f2_split(v2[j >> 1], v[0], v[1]);
+            if (v[j & 1] > 0.0f && ((wv[j >> 2] >> (8 * (j & 3))) & 0xFFu) == 0u) wv[j >> 2] |= 1u << (8 * (j & 3));
         }
     }
-    const bool none = vmax == 0.0f;
-    store_bytes(static_cast<uint8_t *>(T.m) + at, 8,
-                make_uint2(__byte_perm(om[0], om[1], 0x5410u), __byte_perm(om[2], om[3], 0x5410u)));
-    store_bytes(static_cast<uint8_t *>(T.v) + at, 8,
-                make_uint2(none ? 0u : __byte_perm(ov[0], ov[1], 0x5410u),
-                           none ? 0u : __byte_perm(ov[2], ov[3], 0x5410u)));
-    if (lane == 0) {
-        T.sm[unit] = __fdiv_rn(mmax, kLevelsM);
-        T.sv[unit] = __fdiv_rn(vmax, kLevelsV);
+    if (again >> 31) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            wm[h] = wv[h] = 0u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float m[2], v[2];
+                f2_split(m2[2 * h + (j >> 1)], m[0], m[1]);
+                f2_split(v2[2 * h + (j >> 1)], v[0], v[1]);
+                uint32_t qm, qv;
+                quantize_both(m[j & 1], v[j & 1], im, iv, base + 4 * h + j, qm, qv);
+                wm[h] |= qm << (8 * j);
+                wv[h] |= qv << (8 * j);
+            }
+        }
     }
+    store_bytes(static_cast<uint8_t *>(T.m) + at, 8, make_uint2(wm[0], wm[1]));
+    store_bytes(static_cast<uint8_t *>(T.v) + at, 8, make_uint2(wv[0], wv[1]));
 }
 
 // Both kinds of moments share the walk; BITS is the moments' width.
 // The warp's 256 elements of a unit are one block of the 8-bit moments, so a
 // block's largest moment is a warp reduction and nothing leaves the warp.
 template <int BITS, int CAP>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
 adamw_kernel(const __grid_constant__ StepBatch<CAP> batch, const StepArgs a) {
     pdl_wait();
     pdl_launch_dependents();
