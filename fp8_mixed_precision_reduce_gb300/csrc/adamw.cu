@@ -351,26 +351,12 @@ __device__ __forceinline__ void load_grad(const StepTensor &T, int64_t at, int c
         for (int j = 0; j < 8; ++j) g[j] = j < cnt ? bf16_bits_to_f32(p[j]) : 0.0f;
     }
 }
-// cvt_quad, with NaN looked for in the packed codes: a byte's low 7 bits plus 1
-// reach 0x80 for the NaN code alone, which is then rewritten to 0x7F.
-__device__ __forceinline__ uint32_t cvt_quad_e4m3(float a, float b, float c, float d) {
-    uint16_t lo, hi;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
-    uint32_t q = lo | (static_cast<uint32_t>(hi) << 16);
-    const uint32_t nan = ((q & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-    if (nan != 0u) {
-        const uint32_t bytes = (nan >> 7) * 0xFFu;
-        q = (q & ~bytes) | (0x7F7F7F7Fu & bytes);
-    }
-    return q;
-}
 __device__ __forceinline__ void store_copy(const StepTensor &T, int64_t at, int cnt, const float (&w)[8]) {
     if (T.copy_kind == 2) {
         const float sw = __ldg(T.copy_scale);
-        const uint2 q = make_uint2(cvt_quad_e4m3(__fmul_rn(w[0], sw), __fmul_rn(w[1], sw), __fmul_rn(w[2], sw),
+        const uint2 q = make_uint2(cvt_quad_probed<FP8MP_E4M3>(__fmul_rn(w[0], sw), __fmul_rn(w[1], sw), __fmul_rn(w[2], sw),
                                                  __fmul_rn(w[3], sw)),
-                                   cvt_quad_e4m3(__fmul_rn(w[4], sw), __fmul_rn(w[5], sw), __fmul_rn(w[6], sw),
+                                   cvt_quad_probed<FP8MP_E4M3>(__fmul_rn(w[4], sw), __fmul_rn(w[5], sw), __fmul_rn(w[6], sw),
                                                  __fmul_rn(w[7], sw)));
         store_bytes(static_cast<uint8_t *>(T.copy) + at, cnt, q);
     } else if (T.copy_kind == 1) {
@@ -418,7 +404,6 @@ __device__ __forceinline__ float rcp_ftz(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-__device__ __forceinline__ uint64_t f2_same(float x) { return f2_pack(x, x); }
 // Largest of the warp's values >= 0 (whose bits order as they do).
 __device__ __forceinline__ float warp_max_bits(float x) {
     return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));

@@ -29,6 +29,7 @@ namespace {
 
 constexpr int NUM_THREADS = 192;  // producer warp, MMA warp, four epilogue warps
 constexpr int W_ROWS = 128;       // weight rows of a tile
+constexpr uint32_t kMaxSplits = 8;  // CTAs that may share a tile's contraction (a portable cluster)
 
 template <int NT>
 struct Cfg {
@@ -74,13 +75,27 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         : "memory");
 }
 
-// Adds the cluster's partial sums of weight row `row` and token `m`, in rank order.
+// Adds the cluster's partial sums of weight row `row` and tokens m .. m + 3, in
+// rank order; every rank's are asked for before the first is used.
 template <int NT>
-__device__ __forceinline__ float joined(uint32_t base, int row, int m, uint32_t splits) {
+__device__ __forceinline__ void joined(uint32_t base, int row, int m, uint32_t splits, float (&s)[4]) {
     const uint32_t at = base + static_cast<uint32_t>((row * Cfg<NT>::PITCH + m) * 4);
-    float s = ld_shared_cluster_f32(mapa_shared(at, 0));
-    for (uint32_t r = 1; r < splits; ++r) s = __fadd_rn(s, ld_shared_cluster_f32(mapa_shared(at, r)));
-    return s;
+    float part[kMaxSplits][4];
+#pragma unroll
+    for (uint32_t r = 0; r < kMaxSplits; ++r)
+        if (r < splits)
+            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(part[r][0]), "=f"(part[r][1]), "=f"(part[r][2]), "=f"(part[r][3])
+                         : "r"(mapa_shared(at, r))
+                         : "memory");
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[j] = part[0][j];
+#pragma unroll
+    for (uint32_t r = 1; r < kMaxSplits; ++r)
+        if (r < splits) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[j] = __fadd_rn(s[j], part[r][j]);
+        }
 }
 
 // GATED: ACT is the activation; otherwise unused.
@@ -211,46 +226,57 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) few_kernel(const __grid_consta
     tc_fence_after();
     if (warp == 1) tmem_dealloc<false>(tmem, C::TMEM_COLS);
 
-    // this CTA's share of the tile's outputs, all tokens; neighbouring threads take neighbouring outputs
+    // this CTA's share of the tile's outputs, four tokens at a time; neighbouring threads take neighbouring outputs
     const float scale = __fmul_rn(__ldg(P.sinv_a), __ldg(P.sinv_b));
     constexpr int TILE_OUTS = GATED ? 64 : W_ROWS;
-    const int mine = TILE_OUTS / static_cast<int>(splits);
+    const int mine = TILE_OUTS / static_cast<int>(splits);  // 8 .. 128, a power of two
+    const int shift = 31 - __clz(mine);
+    const float h_scale = GATED && P.out_scale != nullptr ? __ldg(P.out_scale) : 0.0f;
     float am = 0.0f;
-    for (int i = threadIdx.x; i < mine * P.rows; i += NUM_THREADS) {
-        const int m = i / mine, o = static_cast<int>(rank) * mine + (i - m * mine);
+    for (int i = threadIdx.x; i < mine * ((P.rows + 3) / 4); i += NUM_THREADS) {
+        const int m0 = 4 * (i >> shift), o = static_cast<int>(rank) * mine + (i & (mine - 1));
         const int64_t col = static_cast<int64_t>(tile) * TILE_OUTS + o;
         if (col >= P.outs) continue;
-        const float a = joined<NT>(base, o, m, splits);
-        if constexpr (GATED) {
-            const float g = __fmul_rn(a, scale), u = __fmul_rn(joined<NT>(base, 64 + o, m, splits), scale);
-            const float h = gate_act<ACT>(g) * u;
-            am = fmaxf(am, fabsf(h));
+        float a[4], b[4];
+        joined<NT>(base, o, m0, splits, a);
+        if constexpr (GATED) joined<NT>(base, 64 + o, m0, splits, b);
+        float bias = 0.0f;
+        if (!GATED && P.bias != nullptr)
+            bias = P.bias_bf16 ? bf16_bits_to_f32(static_cast<const uint16_t *>(P.bias)[col])
+                               : static_cast<const float *>(P.bias)[col];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int m = m0 + j;
+            if (m >= P.rows) break;
             const int64_t at = static_cast<int64_t>(m) * P.outs + col;
-            if (P.out_scale != nullptr)
-                static_cast<uint8_t *>(P.out)[at] =
-                    static_cast<uint8_t>(cvt_pair<FP8MP_E4M3>(__fmul_rn(h, __ldg(P.out_scale)), 0.0f) & 0xFFu);
-            else
-                static_cast<__nv_bfloat16 *>(P.out)[at] = __float2bfloat16_rn(h);
-            if (P.gu != nullptr) {
-                __nv_bfloat16 *row = reinterpret_cast<__nv_bfloat16 *>(P.gu) + static_cast<int64_t>(m) * 2 * P.outs;
-                row[col] = __float2bfloat16_rn(g);
-                row[P.outs + col] = __float2bfloat16_rn(u);
-            }
-        } else {
-            float y = __fmul_rn(a, scale);
-            if (P.bias != nullptr)
-                y = __fmaf_rn(a, scale,
-                              P.bias_bf16 ? bf16_bits_to_f32(static_cast<const uint16_t *>(P.bias)[col])
-                                          : static_cast<const float *>(P.bias)[col]);
-            const int64_t at = static_cast<int64_t>(m) * P.outs + col;
-            if (P.out_bf16) {
-                const __nv_bfloat16 b = __float2bfloat16_rn(y);
-                static_cast<__nv_bfloat16 *>(P.out)[at] = b;
-                y = __bfloat162float(b);
+            if constexpr (GATED) {
+                const float g = __fmul_rn(a[j], scale), u = __fmul_rn(b[j], scale);
+                float p, unused;
+                f2_split(gate_act<ACT>(f2_pack(g, 0.0f)), p, unused);
+                const float h = p * u;
+                am = fmaxf(am, fabsf(h));
+                if (P.out_scale != nullptr)
+                    static_cast<uint8_t *>(P.out)[at] =
+                        static_cast<uint8_t>(cvt_pair<FP8MP_E4M3>(__fmul_rn(h, h_scale), 0.0f) & 0xFFu);
+                else
+                    static_cast<__nv_bfloat16 *>(P.out)[at] = __float2bfloat16_rn(h);
+                if (P.gu != nullptr) {
+                    __nv_bfloat16 *row =
+                        reinterpret_cast<__nv_bfloat16 *>(P.gu) + static_cast<int64_t>(m) * 2 * P.outs;
+                    row[col] = __float2bfloat16_rn(g);
+                    row[P.outs + col] = __float2bfloat16_rn(u);
+                }
             } else {
-                static_cast<float *>(P.out)[at] = y;
+                float y = P.bias != nullptr ? __fmaf_rn(a[j], scale, bias) : __fmul_rn(a[j], scale);
+                if (P.out_bf16) {
+                    const __nv_bfloat16 v = __float2bfloat16_rn(y);
+                    static_cast<__nv_bfloat16 *>(P.out)[at] = v;
+                    y = __bfloat162float(v);
+                } else {
+                    static_cast<float *>(P.out)[at] = y;
+                }
+                am = fmaxf(am, fabsf(y));
             }
-            am = fmaxf(am, fabsf(y));
         }
     }
     if (P.out_amax != nullptr) block_amax_atomic(am, P.out_amax);
@@ -267,7 +293,7 @@ constexpr int kFixed = 8;
 int split_for(int64_t tiles, int num_kb, int num_sms) {
     int best = 1;
     double least = 0.0;
-    for (int s = 1; s <= 8 && s <= num_kb; s *= 2) {
+    for (int s = 1; s <= static_cast<int>(kMaxSplits) && s <= num_kb; s *= 2) {
         const int64_t slots = 2 * static_cast<int64_t>(num_sms);
         const int64_t waves = (tiles * s + slots - 1) / slots;
         const double cost = static_cast<double>(waves) * ((num_kb + s - 1) / s + kFixed);
@@ -317,9 +343,9 @@ int set_operands(FewParams &P, const uint8_t *x8, const uint8_t *w8, int64_t M, 
     P.idesc = make_idesc(FP8MP_E4M3, FP8MP_E4M3, W_ROWS, nt, 0, 0);
     const uint64_t m = static_cast<uint64_t>(M), n = static_cast<uint64_t>(outs), k = static_cast<uint64_t>(K);
     const uint32_t box = gated ? 64 : W_ROWS;
-    int rc = make_box_tmap(&P.tx, x8, 1, k, m, k, BK, static_cast<uint32_t>(nt), true);
-    if (!rc) rc = make_box_tmap(&P.tw0, w8, 1, k, n, k, BK, box, true);
-    if (!rc && gated) rc = make_box_tmap(&P.tw1, w8 + outs * K, 1, k, n, k, BK, box, true);
+    int rc = make_operand_tmap(&P.tx, x8, k, m, static_cast<uint32_t>(nt));
+    if (!rc) rc = make_operand_tmap(&P.tw0, w8, k, n, box);
+    if (!rc && gated) rc = make_operand_tmap(&P.tw1, w8 + outs * K, k, n, box);
     return rc;
 }
 

@@ -15,6 +15,7 @@ __device__ __forceinline__ uint64_t f2_from_bits(uint32_t lo, uint32_t hi) {
 __device__ __forceinline__ uint64_t f2_pack(float lo, float hi) {
     return f2_from_bits(__float_as_uint(lo), __float_as_uint(hi));
 }
+__device__ __forceinline__ uint64_t f2_same(float x) { return f2_pack(x, x); }
 __device__ __forceinline__ void f2_split(uint64_t v, float &lo, float &hi) {
     asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
 }

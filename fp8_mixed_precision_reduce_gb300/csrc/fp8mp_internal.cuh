@@ -288,6 +288,27 @@ __device__ __forceinline__ uint32_t cvt_quad(float a, float b, float c, float d)
     return cvt_pair<FMT>(a, b) | (cvt_pair<FMT>(c, d) << 16);
 }
 
+// cvt_quad with NaN looked for in the packed codes: a byte's low 7 bits plus 1
+// (E4M3) or 3 (E5M2) reach 0x80 for a NaN code alone, which becomes 0x7F.
+template <int FMT>
+__device__ __forceinline__ uint32_t cvt_quad_probed(float a, float b, float c, float d) {
+    uint16_t lo, hi;
+    if constexpr (FMT == FP8MP_E4M3) {
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    } else {
+        asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+        asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    }
+    uint32_t q = lo | (static_cast<uint32_t>(hi) << 16);
+    const uint32_t nan = ((q & 0x7F7F7F7Fu) + (FMT == FP8MP_E4M3 ? 0x01010101u : 0x03030303u)) & 0x80808080u;
+    if (nan != 0u) {
+        const uint32_t bytes = (nan >> 7) * 0xFFu;
+        q = (q & ~bytes) | (0x7F7F7F7Fu & bytes);
+    }
+    return q;
+}
+
 // max that never lets a NaN win (the NaN operand is ignored).
 __device__ __forceinline__ float max_ignore_nan(float acc, float v) { return v > acc ? v : acc; }
 

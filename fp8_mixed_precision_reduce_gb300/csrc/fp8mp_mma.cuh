@@ -255,24 +255,18 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
 
 // ------------------------------------------------------------- host side
 
-// A 2-D tensor map: outer rows of `inner` elements of esize bytes (1: bytes, 2:
-// bf16), `pitch` bytes apart; boxes of box_outer rows x box_inner elements,
-// written to shared memory with a swizzle as wide as the box's row (64 or 128
-// bytes). Elements outside the tensor are read as 0 and not written.
-inline int make_box_tmap(CUtensorMap *map, const void *ptr, int esize, uint64_t inner, uint64_t outer, uint64_t pitch,
-                         uint32_t box_inner, uint32_t box_outer, bool operand) {
+// An FP8 operand: outer rows of `inner` bytes, dense; boxes of box_outer rows x
+// 128 bytes under the 128-byte swizzle. Bytes outside the tensor are read as 0.
+inline int make_operand_tmap(CUtensorMap *map, const void *ptr, uint64_t inner, uint64_t outer, uint32_t box_outer) {
     auto enc = tensor_map_encoder();
     if (enc == nullptr) return fail(FP8MP_ERR_LAUNCH, "cuTensorMapEncodeTiled is not available");
     const cuuint64_t dims[2] = {inner, outer};
-    const cuuint64_t strides[1] = {pitch};
-    const cuuint32_t box[2] = {box_inner, box_outer};
+    const cuuint64_t strides[1] = {inner};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(BK), box_outer};
     const cuuint32_t estr[2] = {1, 1};
-    const CUresult r =
-        enc(map, esize == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-            const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            box_inner * esize == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-            operand ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_NONE,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(ptr), dims, strides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(FP8MP_ERR_LAUNCH, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
     return FP8MP_OK;
 }

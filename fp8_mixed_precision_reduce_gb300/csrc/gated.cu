@@ -5,7 +5,7 @@
 //
 // The GEMM side is the persistent tcgen05 pipeline of gemm.cu: one CTA per SM
 // (or a cluster of two on 256-row tiles), warp 0 the TMA producer, warp 1 the
-// MMA issuer, warps 2-5 the epilogue, two TMEM accumulators so that a tile's
+// MMA issuer, the others the epilogue, two TMEM accumulators so that a tile's
 // epilogue runs beside the next tile's MMAs. What differs is what a tile is
 // and what its epilogue does:
 //
@@ -14,10 +14,10 @@
 //     the up rows; one CTA alone both), so g and u of one element meet in one
 //     thread and h never leaves the SM in more than its 8 (or 16) bits. The
 //     pre-activations go out as bf16 only when the backward pass wants them.
-//   dgrad: 256 columns of dh; the epilogue fetches the tile's g and u (bf16) by
-//     TMA, one 64-column chunk ahead, and writes the E5M2 codes of dg and du.
-//     dh itself is never stored: against a GEMM that writes it in bf16 and a
-//     pass that reads it back that is 4 bytes per element less traffic.
+//   dgrad: 256 columns of dh; the epilogue reads the tile's g and u (bf16), 32
+//     columns ahead, and writes the E5M2 codes of dg and du. dh itself is never
+//     stored: against a GEMM that writes it in bf16 and a pass that reads it back
+//     that is 4 bytes per element less traffic.
 //
 // Both are bound by the tensor cores at training sizes (an epilogue of a few
 // dozen instructions per element hides behind a contraction of 4096), and by
@@ -36,48 +36,47 @@ __device__ unsigned int g_gated_timeout_flag = 0;
 
 namespace {
 
-constexpr int NUM_EPI_WARPS = 4;
-constexpr int NUM_THREADS = 64 + 32 * NUM_EPI_WARPS;
 constexpr uint32_t TMEM_COLS = 2 * TILE_N;
-constexpr int BOX_BYTES = 32 * 128;  // one staging box: 32 rows of 128 bytes
 
 enum Mode { FWD = 0, DGRAD = 1 };
 
-// Shared memory of a CTA: the operand ring, each epilogue warp's staging
-// boxes, the barriers. Forward: one box each for g, u and h per warp. Dgrad:
-// two sets of g and u boxes to load into, and one set (two for a pair, whose
-// stages are smaller) of half boxes for the codes of dg and du.
+// Shared memory of a CTA: the operand ring and the barriers. The epilogue goes
+// between tensor memory and global memory through registers, each lane a row,
+// with whole 32-byte sectors; shared memory is left to the ring, whose depth
+// counts for more: with staging boxes for TMA in its place (5 and 4 stages of 32
+// KB instead of 7) the forward pass of 16384 x 4096 -> 14336 took 1111-1217 us
+// and dgrad of 8192 x 4096 x 14336 371-440 us.
 template <bool PAIR, int MODE>
 struct Cfg {
     static constexpr int TILE_M = PAIR ? 256 : 128;
     static constexpr int TILE_COLS = MODE == FWD ? 128 : 256;  // columns of h (dh) per tile
     static constexpr int ROWS_B = PAIR ? 128 : 256;
-    static constexpr int STAGES = MODE == FWD ? (PAIR ? 5 : 3) : (PAIR ? 4 : 3);
-    static constexpr int OUT_SETS = MODE == FWD ? 1 : (PAIR ? 2 : 1);
+    static constexpr int STAGES = PAIR ? 7 : 4;
+    static constexpr int EPI_WARPS = 4;
+    static constexpr int THREADS = 64 + 32 * EPI_WARPS;
     static constexpr int A_BYTES = ROWS_A * BK;
     static constexpr int STAGE_BYTES = A_BYTES + ROWS_B * BK;
     static constexpr int TX_BYTES = PAIR ? 2 * STAGE_BYTES : STAGE_BYTES;
-    static constexpr int EPI_OFFSET = STAGES * STAGE_BYTES;
-    static constexpr int WARP_BYTES = MODE == FWD ? 3 * BOX_BYTES : 4 * BOX_BYTES + OUT_SETS * BOX_BYTES;
-    static constexpr int BAR_OFFSET = EPI_OFFSET + NUM_EPI_WARPS * WARP_BYTES;
-    static constexpr int NUM_BARS = 2 * STAGES + 5 + (MODE == DGRAD ? 2 * NUM_EPI_WARPS : 0);
+    static constexpr int BAR_OFFSET = STAGES * STAGE_BYTES;
+    static constexpr int NUM_BARS = 2 * STAGES + 5;
     static constexpr int SLOT_OFFSET = BAR_OFFSET + NUM_BARS * 8;
     static constexpr int FLAG_OFFSET = SLOT_OFFSET + 8;
     static constexpr int SMEM_ALLOC = FLAG_OFFSET + 8 + 1024;
-    static constexpr uint32_t TEMPTY_COUNT = PAIR ? 2 * NUM_EPI_WARPS : NUM_EPI_WARPS;
-    static_assert(STAGE_BYTES % 1024 == 0 && WARP_BYTES % 1024 == 0, "swizzle atoms need 1 KB alignment");
+    static constexpr uint32_t TEMPTY_COUNT = PAIR ? 2 * EPI_WARPS : EPI_WARPS;
+    static_assert(STAGE_BYTES % 1024 == 0, "swizzle atoms need 1 KB alignment");
     static_assert(SMEM_ALLOC <= 232448, "shared memory budget");
 };
 
 struct GatedParams {
     CUtensorMap ta;        // A: the rows (tokens), K-major
     CUtensorMap tb0, tb1;  // forward: the gate and the up rows of W8; dgrad: Wd8 (both)
-    CUtensorMap tg, tu;    // the halves of the pre-activations (forward: written, dgrad: read)
-    CUtensorMap to0, to1;  // forward: h; dgrad: the codes of dg and of du
+    CUtensorMap tg, tu;    // dgrad: the halves of the pre-activations, for prefetching
+    uint16_t *gu;          // the pre-activations (forward: written when not NULL, dgrad: read)
+    void *out;             // forward: h; dgrad: the codes of dg and du
+    int wide;              // gu (and a bf16 h) lie on 32-byte boundaries
     int rows, cols, num_kb;
     int tiles_m, tiles_n, num_tiles, group_m, group_n;
     uint32_t idesc;
-    int save_gu;
     const float *sinv_a, *sinv_b;
     const float *out_scale;
     float *out_amax;
@@ -86,106 +85,146 @@ struct GatedParams {
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
     return fp8mp::wait_bounded(bar, parity, abort_flag, &g_gated_timeout_flag);
 }
-__device__ __forceinline__ void bulk_wait_read_all() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(addr)
+
+// A tensor-map box, from global memory into L2.
+__device__ __forceinline__ void prefetch_box(const CUtensorMap *map, int32_t c0, int32_t c1) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1)
                  : "memory");
-    return v;
-}
-// Address of 16-byte chunk `j` of row `r` in a staging box of 128-byte rows
-// under the 128-byte swizzle, and of one of 64-byte rows under the 64-byte one.
-__device__ __forceinline__ uint32_t box_chunk(uint32_t box, int r, int j) {
-    return box + static_cast<uint32_t>(r * 128 + ((j ^ (r & 7)) << 4));
-}
-__device__ __forceinline__ uint32_t half_box_chunk(uint32_t box, int r, int j) {
-    return box + static_cast<uint32_t>(r * 64 + ((j ^ ((r >> 1) & 3)) << 4));
 }
 
-// A tile's epilogue in the forward pass, by one warp: 32 rows, 32 columns of
-// g and u at a time. Columns past F and rows past M hold zeros (the operands'
-// zero fill), whose h is 0: they need no mask in the amax.
-template <bool PAIR, int ACT, bool H_FP8>
-__device__ __forceinline__ float forward_tile(const GatedParams &P, uint32_t acc, uint32_t boxes, int lane, int row0,
-                                              int col0, float scale, float h_scale) {
-    const uint32_t box_g = boxes, box_u = boxes + BOX_BYTES, box_h = boxes + 2 * BOX_BYTES;
+// 16 bf16 values (32 bytes): one access where they lie on a 32-byte boundary,
+// two of 16 bytes otherwise.
+__device__ __forceinline__ void load_bf16x16(const uint16_t *p, bool wide, uint32_t (&w)[8]) {
+    if (wide) {
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                     : "l"(p));
+    } else {
+        const uint4 a = *reinterpret_cast<const uint4 *>(p), b = *(reinterpret_cast<const uint4 *>(p) + 1);
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+    }
+}
+__device__ __forceinline__ void store_bf16x16(uint16_t *p, bool wide, const uint32_t (&w)[8]) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
+                     "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        *(reinterpret_cast<uint4 *>(p) + 1) = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
+// A forward tile, by one warp: this lane's row, 32 columns of g and u at a time
+// (`acc`: the accumulator's column 0 of the warp's lanes). Columns past F and
+// rows past M hold zeros (the operands' zero fill), whose h is 0: they need no
+// mask in the amax, and are not stored.
+template <int ACT, bool H_FP8>
+__device__ __forceinline__ float forward_tile(const GatedParams &P, uint32_t acc, int row, int col0, float scale,
+                                              float h_scale) {
     float am = 0.0f;
+    const bool row_ok = row < P.rows;
+    const int64_t f = P.cols;
+    uint16_t *g_row = P.gu + static_cast<int64_t>(row) * 2 * f;
 #pragma unroll 1
     for (int c = 0; c < 128; c += 32) {
+        if (col0 + c >= P.cols) break;
         uint32_t rg[32], ru[32];
         tmem_ld32(acc + static_cast<uint32_t>(c), rg);
         tmem_ld32(acc + static_cast<uint32_t>(128 + c), ru);
-        if (row0 >= P.rows || col0 + c >= P.cols) continue;  // nothing of this warp's chunk exists
-        if ((c & 32) == 0) {  // the boxes' last stores must have been read
-            if (lane == 0) bulk_wait_read_all();
-            __syncwarp();
-        }
-        uint32_t hq[8];
 #pragma unroll
-        for (int o = 0; o < 4; ++o) {  // 8 columns each
-            float g[8], u[8], h[8];
+        for (int o = 0; o < 2; ++o) {  // 16 columns each
+            const int col = col0 + c + 16 * o;
+            const bool ok = row_ok && col < P.cols;
+            uint32_t wg[8], wu[8], wh[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                g[j] = __fmul_rn(__uint_as_float(rg[8 * o + j]), scale);
-                u[j] = __fmul_rn(__uint_as_float(ru[8 * o + j]), scale);
-                h[j] = gate_act<ACT>(g[j]) * u[j];
-                am = fmaxf(am, fabsf(h[j]));
-            }
-            const int chunk = ((c & 32) >> 3) + o;
-            if (P.save_gu) {
-                st_shared_v4(box_chunk(box_g, lane, chunk), pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3]),
-                             pack_bf16x2(g[4], g[5]), pack_bf16x2(g[6], g[7]));
-                st_shared_v4(box_chunk(box_u, lane, chunk), pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]),
-                             pack_bf16x2(u[4], u[5]), pack_bf16x2(u[6], u[7]));
-            }
-            if constexpr (H_FP8) {
+            for (int k = 0; k < 4; ++k) {  // four columns
+                float y[4];
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    hq[2 * o + j] =
-                        cvt_quad<FP8MP_E4M3>(__fmul_rn(h[4 * j], h_scale), __fmul_rn(h[4 * j + 1], h_scale),
-                                             __fmul_rn(h[4 * j + 2], h_scale), __fmul_rn(h[4 * j + 3], h_scale));
-            } else {
-                st_shared_v4(box_chunk(box_h, lane, chunk), pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]),
-                             pack_bf16x2(h[4], h[5]), pack_bf16x2(h[6], h[7]));
-            }
-        }
-        if constexpr (H_FP8) {
-            st_shared_v4(box_chunk(box_h, lane, c >> 4), hq[0], hq[1], hq[2], hq[3]);
-            st_shared_v4(box_chunk(box_h, lane, (c >> 4) + 1), hq[4], hq[5], hq[6], hq[7]);
-        }
-        // a box is full after its last 32 columns, or at the last column block
-        const bool last = c == 96 || col0 + c + 32 >= P.cols;
-        if ((c & 32) || last) {
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                const int at = col0 + (c & ~32);
-                if (P.save_gu) {
-                    tma_store_2d(&P.tg, box_g, at, row0);
-                    tma_store_2d(&P.tu, box_u, at, row0);
+                for (int j = 0; j < 2; ++j) {
+                    const int at = 16 * o + 4 * k + 2 * j;
+                    const uint64_t g = f2_mul(f2_from_bits(rg[at], rg[at + 1]), f2_same(scale));
+                    const uint64_t u = f2_mul(f2_from_bits(ru[at], ru[at + 1]), f2_same(scale));
+                    const uint64_t h = f2_mul(gate_act<ACT>(g), u);
+                    float v0, v1;
+                    f2_split(g, v0, v1);
+                    wg[2 * k + j] = pack_bf16x2(v0, v1);
+                    f2_split(u, v0, v1);
+                    wu[2 * k + j] = pack_bf16x2(v0, v1);
+                    f2_split(h, v0, v1);
+                    am = fmaxf(am, fmaxf(fabsf(v0), fabsf(v1)));
+                    if constexpr (H_FP8)
+                        f2_split(f2_mul(h, f2_same(h_scale)), y[2 * j], y[2 * j + 1]);
+                    else
+                        wh[2 * k + j] = pack_bf16x2(v0, v1);
                 }
-                if constexpr (!H_FP8)
-                    tma_store_2d(&P.to0, box_h, at, row0);
-                else if (last)
-                    tma_store_2d(&P.to0, box_h, col0, row0);
-                bulk_commit_group();
+                if constexpr (H_FP8) wh[k] = cvt_quad_probed<FP8MP_E4M3>(y[0], y[1], y[2], y[3]);
             }
+            if (!ok) continue;
+            if (P.gu != nullptr) {
+                store_bf16x16(g_row + col, P.wide, wg);
+                store_bf16x16(g_row + f + col, P.wide, wu);
+            }
+            if constexpr (H_FP8)
+                *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(P.out) + row * f + col) =
+                    make_uint4(wh[0], wh[1], wh[2], wh[3]);
+            else
+                store_bf16x16(static_cast<uint16_t *>(P.out) + row * f + col, P.wide, wh);
         }
     }
     return am;
 }
 
-// The loads of a dgrad tile's g and u boxes for its chunk c (64 columns), by lane 0.
-__device__ __forceinline__ void load_gu(const GatedParams &P, uint32_t boxes, uint32_t bar, int col, int row0) {
-    mbar_arrive_expect_tx(bar, 2 * BOX_BYTES);
-    tma_load_2d_cta(boxes, &P.tg, bar, col, row0);
-    tma_load_2d_cta(boxes + BOX_BYTES, &P.tu, bar, col, row0);
+// 32 columns of g and u of this lane's row (what does not exist: 0).
+struct GuChunk {
+    uint32_t g[2][8], u[2][8];
+};
+__device__ __forceinline__ void load_gu(const GatedParams &P, int row, int col, GuChunk &x) {
+    const uint16_t *p = P.gu + static_cast<int64_t>(row) * 2 * P.cols + col;
+#pragma unroll
+    for (int o = 0; o < 2; ++o) {
+        if (row < P.rows && col + 16 * o < P.cols) {
+            load_bf16x16(p + 16 * o, P.wide, x.g[o]);
+            load_bf16x16(p + P.cols + 16 * o, P.wide, x.u[o]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x.g[o][j] = x.u[o][j] = 0u;
+        }
+    }
+}
+
+// 32 columns of a dgrad tile: dg and du of this lane's row from the accumulator
+// (at `acc`) and x.
+template <int ACT>
+__device__ __forceinline__ float dgrad_columns(const GatedParams &P, uint32_t acc, const GuChunk &x, int row, int col,
+                                               float scale, float out_scale) {
+    float am = 0.0f;
+    uint32_t rd[32];
+    tmem_ld32(acc, rd);
+    uint8_t *out = static_cast<uint8_t *>(P.out) + static_cast<int64_t>(row) * 2 * P.cols + col;
+#pragma unroll
+    for (int o = 0; o < 2; ++o) {  // 16 columns each
+        uint32_t qg[4], qu[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int at = 16 * o + 4 * k;
+            const uint64_t dh[2] = {f2_mul(f2_from_bits(rd[at], rd[at + 1]), f2_same(scale)),
+                                    f2_mul(f2_from_bits(rd[at + 2], rd[at + 3]), f2_same(scale))};
+            const uint32_t g[2] = {x.g[o][2 * k], x.g[o][2 * k + 1]}, u[2] = {x.u[o][2 * k], x.u[o][2 * k + 1]};
+            gate_grad_codes<ACT>(dh, g, u, f2_same(out_scale), qg[k], qu[k], am);
+        }
+        if (row < P.rows && col + 16 * o < P.cols) {
+            *reinterpret_cast<uint4 *>(out + 16 * o) = make_uint4(qg[0], qg[1], qg[2], qg[3]);
+            *reinterpret_cast<uint4 *>(out + P.cols + 16 * o) = make_uint4(qu[0], qu[1], qu[2], qu[3]);
+        }
+    }
+    return am;
 }
 
 template <bool PAIR, int MODE, int ACT, bool H_FP8>
-__global__ void __launch_bounds__(NUM_THREADS, 1) gated_kernel(const __grid_constant__ GatedParams P) {
+__global__ void __launch_bounds__(Cfg<PAIR, MODE>::THREADS, 1) gated_kernel(const __grid_constant__ GatedParams P) {
     using C = Cfg<PAIR, MODE>;
     extern __shared__ uint8_t smem_raw[];
     uint32_t base = smem_u32(smem_raw);
@@ -199,7 +238,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gated_kernel(const __grid_cons
     auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * C::STAGES + a); };
     auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * C::STAGES + 2 + a); };
     const uint32_t drain_bar = bar0 + 8u * (2 * C::STAGES + 4);
-    auto gu_bar = [&](int w, int b) { return bar0 + 8u * (2 * C::STAGES + 5 + 2 * w + b); };  // dgrad
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::SLOT_OFFSET);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::FLAG_OFFSET);
 
@@ -218,15 +256,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gated_kernel(const __grid_cons
             mbar_init(tempty_bar(a), C::TEMPTY_COUNT);
         }
         mbar_init(drain_bar, 1);
-        if constexpr (MODE == DGRAD)
-            for (int w = 0; w < NUM_EPI_WARPS; ++w)
-                for (int b = 0; b < 2; ++b) mbar_init(gu_bar(w, b), 1);
         *abort_flag = 0;
         fence_mbar_init();
         prefetch_tmap(&P.ta);
         prefetch_tmap(&P.tb0);
         prefetch_tmap(&P.tb1);
-        prefetch_tmap(&P.to0);
     }
     if (warp == 1) {
         tmem_alloc<PAIR>(smem_u32(tmem_slot), TMEM_COLS);
@@ -258,6 +292,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gated_kernel(const __grid_cons
                 const int a_row = mb * C::TILE_M + static_cast<int>(rank) * ROWS_A;
                 const int col0 = nb * C::TILE_COLS;
                 const CUtensorMap *tb = PAIR && rank ? &P.tb1 : &P.tb0;
+                if constexpr (MODE == DGRAD) {  // the tile's g and u, into L2 by the time its epilogue runs
+                    if (a_row < P.rows)
+                        for (int c = col0; c < min(col0 + C::TILE_COLS, P.cols); c += 64) {
+                            prefetch_box(&P.tg, c, a_row);
+                            prefetch_box(&P.tu, c, a_row);
+                        }
+                }
                 for (int kb = 0; kb < num_kb; ++kb, ++it) {
                     const int s = static_cast<int>(it % C::STAGES);
                     if (!wait_bounded(empty_bar(s), ((it / C::STAGES) & 1u) ^ 1u, abort_flag)) {
@@ -334,124 +375,46 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gated_kernel(const __grid_cons
         }
     } else {
         // ---------------- epilogue warps (both CTAs of a pair)
-        const int q = warp & 3;  // this warp may access TMEM lanes 32q .. 32q+31
-        const uint32_t boxes = base + C::EPI_OFFSET + static_cast<uint32_t>((warp - 2) * C::WARP_BYTES);
+        constexpr int HALVES = C::EPI_WARPS / 4;  // warps that share a quarter of the rows, each its columns
+        const int q = warp & 3;                   // this warp may access TMEM lanes 32q .. 32q+31
+        const int half = (warp - 2) / 4;
         const float scale = __fmul_rn(__ldg(P.sinv_a), __ldg(P.sinv_b));
         const float out_scale = P.out_scale != nullptr ? __ldg(P.out_scale) : 1.0f;
         float am = 0.0f;
         int lt = 0;
-        uint32_t loaded = 0, stored = 0;  // dgrad: chunks fetched, sets of code boxes stored
         for (int r = 0; r < rounds; ++r) {
             const int tile = serpentine_tile(r, cluster_id, num_clusters);
             if (tile >= P.num_tiles) continue;
             int mb, nb;
             tile_coords(tile, P.tiles_m, P.tiles_n, P.group_m, P.group_n, mb, nb);
-            const int row0 = mb * C::TILE_M + static_cast<int>(rank) * ROWS_A + q * 32;
-            const int col0 = nb * C::TILE_COLS;
-            // chunks of 64 columns of this warp's rows that exist (dgrad)
-            int live = 0;
-            if constexpr (MODE == DGRAD) {
-                live = row0 < P.rows ? min(4, (P.cols - col0 + 63) / 64) : 0;
-                if (lane == 0 && live > 0)
-                    load_gu(P, boxes + (loaded & 1u) * 2 * BOX_BYTES, gu_bar(warp - 2, loaded & 1u), col0, row0);
-            }
+            const int row = mb * C::TILE_M + static_cast<int>(rank) * ROWS_A + q * 32 + lane;
+            constexpr int COLS = 256 / HALVES;  // dgrad: this warp's columns of a tile
+            const int col0 = nb * C::TILE_COLS + (MODE == DGRAD ? half * COLS : 0);
+            GuChunk x[2];  // dgrad: fetched while the MMAs run, then 32 columns ahead
+            if constexpr (MODE == DGRAD) load_gu(P, row, col0, x[0]);
             const int acc = lt & 1;
             const uint32_t aph = (static_cast<uint32_t>(lt) >> 1) & 1u;
             ++lt;
             int ok = 1;
             if (lane == 0) ok = wait_bounded(tfull_bar(acc), aph, abort_flag) ? 1 : 0;
             ok = __shfl_sync(0xffffffffu, ok, 0);
-            if (!ok) {
-                if (MODE == DGRAD && lane == 0 && live > 0) {  // the load in flight lands first
-                    volatile int never = 0;
-                    wait_bounded(gu_bar(warp - 2, loaded & 1u), (loaded >> 1) & 1u, &never);
-                }
-                break;
-            }
+            if (!ok) break;
             tc_fence_after();
             const uint32_t acc_addr =
                 tmem_base + static_cast<uint32_t>(acc * TILE_N) + (static_cast<uint32_t>(q * 32) << 16);
             if constexpr (MODE == FWD) {
-                am = fmaxf(am, forward_tile<PAIR, ACT, H_FP8>(P, acc_addr, boxes, lane, row0, col0, scale, out_scale));
+                am = fmaxf(am, forward_tile<ACT, H_FP8>(P, acc_addr, row, col0, scale, out_scale));
             } else {
-                bool landed = true;
 #pragma unroll 1
-                for (int c = 0; c < live && landed; ++c) {
-                    const uint32_t b = loaded & 1u;
-                    const uint32_t box_g = boxes + b * 2 * BOX_BYTES, box_u = box_g + BOX_BYTES;
-                    if (lane == 0 && c + 1 < live)  // the other set: every lane is done with it
-                        load_gu(P, boxes + (b ^ 1u) * 2 * BOX_BYTES, gu_bar(warp - 2, b ^ 1u), col0 + 64 * (c + 1),
-                                row0);
-                    landed = wait_bounded(gu_bar(warp - 2, b), (loaded >> 1) & 1u, abort_flag);
-                    ++loaded;
-                    landed = __all_sync(0xffffffffu, landed);
-                    if (!landed) {
-                        if (lane == 0 && c + 1 < live) {
-                            volatile int never = 0;
-                            wait_bounded(gu_bar(warp - 2, loaded & 1u), (loaded >> 1) & 1u, &never);
-                        }
-                        break;
-                    }
-                    // the code boxes this chunk writes: their last stores must have been read
-                    const uint32_t out =
-                        boxes + 4 * BOX_BYTES + (C::OUT_SETS == 2 ? (stored & 1u) * BOX_BYTES : 0u);
-                    if (lane == 0) {
-                        if (C::OUT_SETS == 2)
-                            bulk_wait_read_le1();
-                        else
-                            bulk_wait_read_all();
-                    }
-                    __syncwarp();
-#pragma unroll 1
-                    for (int p = 0; p < 2; ++p) {  // 32 columns each
-                        uint32_t rd[32];
-                        tmem_ld32(acc_addr + static_cast<uint32_t>(64 * c + 32 * p), rd);
-                        uint32_t qg[8], qu[8];
+                for (int c = 0; c < COLS && col0 + c < P.cols; c += 64) {
 #pragma unroll
-                        for (int o = 0; o < 4; ++o) {  // 8 columns each
-                            const uint4 wg = ld_shared_v4(box_chunk(box_g, lane, 4 * p + o));
-                            const uint4 wu = ld_shared_v4(box_chunk(box_u, lane, 4 * p + o));
-                            const uint32_t gw[4] = {wg.x, wg.y, wg.z, wg.w}, uw[4] = {wu.x, wu.y, wu.z, wu.w};
-                            float dg[8], du[8];
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const float g = __uint_as_float((j & 1) ? gw[j >> 1] & 0xFFFF0000u : gw[j >> 1] << 16);
-                                const float u = __uint_as_float((j & 1) ? uw[j >> 1] & 0xFFFF0000u : uw[j >> 1] << 16);
-                                const float dh = __fmul_rn(__uint_as_float(rd[8 * o + j]), scale);
-                                float a, da;
-                                gate_act_grad<ACT>(g, a, da);
-                                dg[j] = dh * u * da;
-                                du[j] = dh * a;
-                                am = fmaxf(am, fmaxf(fabsf(dg[j]), fabsf(du[j])));
-                            }
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                qg[2 * o + j] = cvt_quad<FP8MP_E5M2>(
-                                    __fmul_rn(dg[4 * j], out_scale), __fmul_rn(dg[4 * j + 1], out_scale),
-                                    __fmul_rn(dg[4 * j + 2], out_scale), __fmul_rn(dg[4 * j + 3], out_scale));
-                                qu[2 * o + j] = cvt_quad<FP8MP_E5M2>(
-                                    __fmul_rn(du[4 * j], out_scale), __fmul_rn(du[4 * j + 1], out_scale),
-                                    __fmul_rn(du[4 * j + 2], out_scale), __fmul_rn(du[4 * j + 3], out_scale));
-                            }
-                        }
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            st_shared_v4(half_box_chunk(out, lane, 2 * p + j), qg[4 * j], qg[4 * j + 1], qg[4 * j + 2],
-                                         qg[4 * j + 3]);
-                            st_shared_v4(half_box_chunk(out + BOX_BYTES / 2, lane, 2 * p + j), qu[4 * j],
-                                         qu[4 * j + 1], qu[4 * j + 2], qu[4 * j + 3]);
-                        }
+                    for (int p = 0; p < 2; ++p) {
+                        const int next = c + 32 * (p + 1);
+                        if (next < COLS) load_gu(P, row, col0 + next, x[p ^ 1]);
+                        am = fmaxf(am, dgrad_columns<ACT>(P, acc_addr + static_cast<uint32_t>(half * COLS + c + 32 * p),
+                                                          x[p], row, col0 + c + 32 * p, scale, out_scale));
                     }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        tma_store_2d(&P.to0, out, col0 + 64 * c, row0);
-                        tma_store_2d(&P.to1, out + BOX_BYTES / 2, col0 + 64 * c, row0);
-                        bulk_commit_group();
-                    }
-                    ++stored;
                 }
-                if (!landed) break;
             }
             tc_fence_before();
             __syncwarp();
@@ -462,8 +425,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gated_kernel(const __grid_cons
                     mbar_arrive(tempty_bar(acc));
             }
         }
-        if (lane == 0) bulk_wait_all();  // stores done before the CTA's shared memory goes away
-        __syncwarp();
         if (P.out_amax != nullptr) {
             am = warp_max(am);
             if (lane == 0) atomicMax(reinterpret_cast<int *>(P.out_amax), __float_as_int(am));
@@ -527,23 +488,12 @@ gate_bwd_kernel(const void *__restrict__ dh, const uint16_t *__restrict__ gu, in
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const uint32_t gw[4] = {g4[h].x, g4[h].y, g4[h].z, g4[h].w}, uw[4] = {u4[h].x, u4[h].y, u4[h].z, u4[h].w};
-            float dg[8], du[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float g = __uint_as_float((j & 1) ? gw[j >> 1] & 0xFFFF0000u : gw[j >> 1] << 16);
-                const float u = __uint_as_float((j & 1) ? uw[j >> 1] & 0xFFFF0000u : uw[j >> 1] << 16);
-                float a, da;
-                gate_act_grad<ACT>(g, a, da);
-                dg[j] = d[8 * h + j] * u * da;
-                du[j] = d[8 * h + j] * a;
-                am = fmaxf(am, fmaxf(fabsf(dg[j]), fabsf(du[j])));
-            }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                qg[2 * h + j] = cvt_quad<FP8MP_E5M2>(__fmul_rn(dg[4 * j], scale), __fmul_rn(dg[4 * j + 1], scale),
-                                                     __fmul_rn(dg[4 * j + 2], scale), __fmul_rn(dg[4 * j + 3], scale));
-                qu[2 * h + j] = cvt_quad<FP8MP_E5M2>(__fmul_rn(du[4 * j], scale), __fmul_rn(du[4 * j + 1], scale),
-                                                     __fmul_rn(du[4 * j + 2], scale), __fmul_rn(du[4 * j + 3], scale));
+                const int at = 8 * h + 4 * j;
+                const uint64_t dh2[2] = {f2_pack(d[at], d[at + 1]), f2_pack(d[at + 2], d[at + 3])};
+                const uint32_t g2[2] = {gw[2 * j], gw[2 * j + 1]}, u2[2] = {uw[2 * j], uw[2 * j + 1]};
+                gate_grad_codes<ACT>(dh2, g2, u2, f2_same(scale), qg[2 * h + j], qu[2 * h + j], am);
             }
         }
         *reinterpret_cast<uint4 *>(dgu8 + row * 2 * cols + col) = make_uint4(qg[0], qg[1], qg[2], qg[3]);
@@ -592,7 +542,7 @@ int prepare(const DeviceInfo &dev, int *max_pairs) {
             cudaLaunchConfig_t cfg = {};
             cudaLaunchAttribute attr[1];
             cfg.gridDim = dim3(static_cast<unsigned>(dev.num_sms & ~1));
-            cfg.blockDim = dim3(NUM_THREADS);
+            cfg.blockDim = dim3(C::THREADS);
             cfg.dynamicSmemBytes = C::SMEM_ALLOC;
             attr[0].id = cudaLaunchAttributeClusterDimension;
             attr[0].val.clusterDim.x = 2;
@@ -619,7 +569,7 @@ int launch(const GatedParams &P, cudaStream_t s, const DeviceInfo &dev) {
     const int clusters = P.num_tiles < most ? P.num_tiles : most;
     const cudaError_t e = launch_kernel_cluster(gated_kernel<PAIR, MODE, ACT, H_FP8>,
                                                 dim3(static_cast<unsigned>(PAIR ? 2 * clusters : clusters)),
-                                                dim3(NUM_THREADS), Cfg<PAIR, MODE>::SMEM_ALLOC, s, PAIR ? 2u : 1u, P);
+                                                dim3(Cfg<PAIR, MODE>::THREADS), Cfg<PAIR, MODE>::SMEM_ALLOC, s, PAIR ? 2u : 1u, P);
     if (e != cudaSuccess) return fail(FP8MP_ERR_LAUNCH, "gated: launch failed: %s", cudaGetErrorString(e));
     return FP8MP_OK;
 }
@@ -631,6 +581,21 @@ bool use_pairs(int64_t pair_tiles, const DeviceInfo &dev) {
     if (force != nullptr && std::strcmp(force, "pair") == 0) return true;
     if (force != nullptr && std::strcmp(force, "single") == 0) return false;
     return pair_tiles * 2 >= dev.num_sms;
+}
+
+// bf16 [outer x inner], rows `pitch` bytes apart, in boxes of 128 rows x 64.
+int make_bf16_tmap(CUtensorMap *map, const void *ptr, uint64_t inner, uint64_t outer, uint64_t pitch) {
+    auto enc = tensor_map_encoder();
+    if (enc == nullptr) return fail(FP8MP_ERR_LAUNCH, "cuTensorMapEncodeTiled is not available");
+    const cuuint64_t dims[2] = {inner, outer};
+    const cuuint64_t strides[1] = {pitch};
+    const cuuint32_t box[2] = {64, 128};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims, strides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(FP8MP_ERR_LAUNCH, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+    return FP8MP_OK;
 }
 
 int set_tiles(GatedParams &P, bool pair, int64_t rows, int64_t cols, int64_t kc, int tile_cols, int64_t rows_b) {
@@ -670,14 +635,13 @@ int launch_gated_fwd(const uint8_t *x8, const uint8_t *w8, int64_t M, int64_t F,
     P.sinv_b = sinv_w;
     P.out_scale = h_scale;
     P.out_amax = h_amax;
-    P.save_gu = gu != nullptr;
+    P.gu = gu;
+    P.out = h;
+    P.wide = ((reinterpret_cast<uintptr_t>(gu) | (h_size == 2 ? reinterpret_cast<uintptr_t>(h) : 0)) & 31u) == 0;
     const uint64_t m = static_cast<uint64_t>(M), f = static_cast<uint64_t>(F), k = static_cast<uint64_t>(K);
-    rc = make_box_tmap(&P.ta, x8, 1, k, m, k, BK, ROWS_A, true);
-    if (!rc) rc = make_box_tmap(&P.tb0, w8, 1, k, f, k, BK, 128, true);
-    if (!rc) rc = make_box_tmap(&P.tb1, w8 + F * K, 1, k, f, k, BK, 128, true);
-    if (!rc) rc = make_box_tmap(&P.to0, h, h_size, f, m, f * h_size, 128 / h_size, 32, false);
-    if (!rc && gu != nullptr) rc = make_box_tmap(&P.tg, gu, 2, f, m, 4 * f, 64, 32, false);
-    if (!rc && gu != nullptr) rc = make_box_tmap(&P.tu, gu + F, 2, f, m, 4 * f, 64, 32, false);
+    rc = make_operand_tmap(&P.ta, x8, k, m, ROWS_A);
+    if (!rc) rc = make_operand_tmap(&P.tb0, w8, k, f, 128);
+    if (!rc) rc = make_operand_tmap(&P.tb1, w8 + F * K, k, f, 128);
     if (rc) return rc;
 #define FP8MP_LAUNCH(PAIR_, ACT_) \
     (h_size == 1 ? launch<PAIR_, FWD, ACT_, true>(P, s, dev) : launch<PAIR_, FWD, ACT_, false>(P, s, dev))
@@ -701,13 +665,14 @@ int launch_gated_dgrad(const uint8_t *dy8, const uint8_t *wd8, const uint16_t *g
     P.out_scale = dgu_scale;
     P.out_amax = dgu_amax;
     const uint64_t m = static_cast<uint64_t>(M), f = static_cast<uint64_t>(F), n = static_cast<uint64_t>(N);
-    rc = make_box_tmap(&P.ta, dy8, 1, n, m, n, BK, ROWS_A, true);
-    if (!rc) rc = make_box_tmap(&P.tb0, wd8, 1, f, n, f, 128, BK, true);
+    rc = make_operand_tmap(&P.ta, dy8, n, m, ROWS_A);
+    if (!rc) rc = make_operand_tmap(&P.tb0, wd8, f, n, BK);
     P.tb1 = P.tb0;
-    if (!rc) rc = make_box_tmap(&P.tg, gu, 2, f, m, 4 * f, 64, 32, true);
-    if (!rc) rc = make_box_tmap(&P.tu, gu + F, 2, f, m, 4 * f, 64, 32, true);
-    if (!rc) rc = make_box_tmap(&P.to0, dgu8, 1, f, m, 2 * f, 64, 32, false);
-    if (!rc) rc = make_box_tmap(&P.to1, dgu8 + F, 1, f, m, 2 * f, 64, 32, false);
+    if (!rc) rc = make_bf16_tmap(&P.tg, gu, f, m, 4 * f);
+    if (!rc) rc = make_bf16_tmap(&P.tu, gu + F, f, m, 4 * f);
+    P.gu = const_cast<uint16_t *>(gu);
+    P.out = dgu8;
+    P.wide = (reinterpret_cast<uintptr_t>(gu) & 31u) == 0;
     if (rc) return rc;
     if (act == FP8MP_SILU)
         return pair ? launch<true, DGRAD, FP8MP_SILU, true>(P, s, dev)
