@@ -14,9 +14,9 @@
 //     the up rows; one CTA alone both), so g and u of one element meet in one
 //     thread and h never leaves the SM in more than its 8 (or 16) bits. The
 //     pre-activations go out as bf16 only when the backward pass wants them.
-//   dgrad: 256 columns of dh; the epilogue reads the tile's g and u (bf16), 32
-//     columns ahead, and writes the E5M2 codes of dg and du. dh itself is never
-//     stored: against a GEMM that writes it in bf16 and a pass that reads it back
+//   dgrad: 256 columns of dh; the epilogue takes the tile's g and u (bf16) from a
+//     ring that a warp of its own fills, and writes the E5M2 codes of dg and du.
+//     dh itself is never stored: against a GEMM that writes it in bf16 and a pass that reads it back
 //     that is 4 bytes per element less traffic.
 //
 // Both are bound by the tensor cores at training sizes (an epilogue of a few
@@ -40,25 +40,36 @@ constexpr uint32_t TMEM_COLS = 2 * TILE_N;
 
 enum Mode { FWD = 0, DGRAD = 1 };
 
-// Shared memory of a CTA: the operand ring and the barriers. The epilogue goes
-// between tensor memory and global memory through registers, each lane a row,
-// with whole 32-byte sectors; shared memory is left to the ring, whose depth
-// counts for more: with staging boxes for TMA in its place (5 and 4 stages of 32
-// KB instead of 7) the forward pass of 16384 x 4096 -> 14336 took 1111-1217 us
-// and dgrad of 8192 x 4096 x 14336 371-440 us.
+// A CTA's warps and shared memory.
+//
+// Forward: four epilogue warps go from tensor memory to global memory through
+// registers, each lane a row, in whole 32-byte sectors; shared memory is left to
+// the operand ring, whose depth counts for more (16384 x 4096 -> 14336: 1085 us
+// with 7 stages for a pair; 1156 with 5 and staging boxes for TMA stores, 1217
+// with 4).
+//
+// Dgrad: the epilogue does more per element and waits for g and u, which come
+// from DRAM; a warp alone on its scheduler is too slow for that (371-386 us for
+// 8192 x 4096 x 14336, 279 for the GEMM alone), and so are loads by the lanes
+// themselves, 32 rows apart (410-480 us). So eight warps work, two to a quarter
+// of the rows, and one more feeds them chunks of 64 columns of g and u by TMA
+// through a ring of two.
 template <bool PAIR, int MODE>
 struct Cfg {
     static constexpr int TILE_M = PAIR ? 256 : 128;
     static constexpr int TILE_COLS = MODE == FWD ? 128 : 256;  // columns of h (dh) per tile
     static constexpr int ROWS_B = PAIR ? 128 : 256;
-    static constexpr int STAGES = PAIR ? 7 : 4;
-    static constexpr int EPI_WARPS = 4;
-    static constexpr int THREADS = 64 + 32 * EPI_WARPS;
+    static constexpr int STAGES = MODE == FWD ? (PAIR ? 7 : 4) : (PAIR ? 5 : 3);
+    static constexpr int EPI_WARPS = MODE == FWD ? 4 : 8;
+    static constexpr int THREADS = 64 + 32 * EPI_WARPS + (MODE == FWD ? 0 : 32);
     static constexpr int A_BYTES = ROWS_A * BK;
     static constexpr int STAGE_BYTES = A_BYTES + ROWS_B * BK;
     static constexpr int TX_BYTES = PAIR ? 2 * STAGE_BYTES : STAGE_BYTES;
-    static constexpr int BAR_OFFSET = STAGES * STAGE_BYTES;
-    static constexpr int NUM_BARS = 2 * STAGES + 5;
+    static constexpr int GU_OFFSET = STAGES * STAGE_BYTES;
+    static constexpr int GU_BOX = 128 * 128;  // 128 rows of 64 bf16
+    static constexpr int GU_CHUNKS = MODE == FWD ? 0 : 2;
+    static constexpr int BAR_OFFSET = GU_OFFSET + GU_CHUNKS * 2 * GU_BOX;
+    static constexpr int NUM_BARS = 2 * STAGES + 5 + 2 * GU_CHUNKS;
     static constexpr int SLOT_OFFSET = BAR_OFFSET + NUM_BARS * 8;
     static constexpr int FLAG_OFFSET = SLOT_OFFSET + 8;
     static constexpr int SMEM_ALLOC = FLAG_OFFSET + 8 + 1024;
@@ -70,10 +81,10 @@ struct Cfg {
 struct GatedParams {
     CUtensorMap ta;        // A: the rows (tokens), K-major
     CUtensorMap tb0, tb1;  // forward: the gate and the up rows of W8; dgrad: Wd8 (both)
-    CUtensorMap tg, tu;    // dgrad: the halves of the pre-activations, for prefetching
-    uint16_t *gu;          // the pre-activations (forward: written when not NULL, dgrad: read)
+    CUtensorMap tg, tu;    // dgrad: the halves of the pre-activations
+    uint16_t *gu;          // forward: the pre-activations, when they are wanted
     void *out;             // forward: h; dgrad: the codes of dg and du
-    int wide;              // gu (and a bf16 h) lie on 32-byte boundaries
+    int wide;              // forward: gu (and a bf16 h) lie on 32-byte boundaries
     int rows, cols, num_kb;
     int tiles_m, tiles_n, num_tiles, group_m, group_n;
     uint32_t idesc;
@@ -86,26 +97,17 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, vola
     return fp8mp::wait_bounded(bar, parity, abort_flag, &g_gated_timeout_flag);
 }
 
-// A tensor-map box, from global memory into L2.
-__device__ __forceinline__ void prefetch_box(const CUtensorMap *map, int32_t c0, int32_t c1) {
-    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(c0), "r"(c1)
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
                  : "memory");
+    return v;
 }
 
 // 16 bf16 values (32 bytes): one access where they lie on a 32-byte boundary,
 // two of 16 bytes otherwise.
-__device__ __forceinline__ void load_bf16x16(const uint16_t *p, bool wide, uint32_t (&w)[8]) {
-    if (wide) {
-        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-                     : "l"(p));
-    } else {
-        const uint4 a = *reinterpret_cast<const uint4 *>(p), b = *(reinterpret_cast<const uint4 *>(p) + 1);
-        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-    }
-}
 __device__ __forceinline__ void store_bf16x16(uint16_t *p, bool wide, const uint32_t (&w)[8]) {
     if (wide) {
         asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
@@ -177,29 +179,12 @@ __device__ __forceinline__ float forward_tile(const GatedParams &P, uint32_t acc
     return am;
 }
 
-// 32 columns of g and u of this lane's row (what does not exist: 0).
-struct GuChunk {
-    uint32_t g[2][8], u[2][8];
-};
-__device__ __forceinline__ void load_gu(const GatedParams &P, int row, int col, GuChunk &x) {
-    const uint16_t *p = P.gu + static_cast<int64_t>(row) * 2 * P.cols + col;
-#pragma unroll
-    for (int o = 0; o < 2; ++o) {
-        if (row < P.rows && col + 16 * o < P.cols) {
-            load_bf16x16(p + 16 * o, P.wide, x.g[o]);
-            load_bf16x16(p + P.cols + 16 * o, P.wide, x.u[o]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x.g[o][j] = x.u[o][j] = 0u;
-        }
-    }
-}
-
 // 32 columns of a dgrad tile: dg and du of this lane's row from the accumulator
-// (at `acc`) and x.
+// (at `acc`) and its g and u, the 16-byte pieces `piece` .. `piece` + 3 of row
+// `r` in boxes of 128-byte rows under the 128-byte swizzle.
 template <int ACT>
-__device__ __forceinline__ float dgrad_columns(const GatedParams &P, uint32_t acc, const GuChunk &x, int row, int col,
-                                               float scale, float out_scale) {
+__device__ __forceinline__ float dgrad_columns(const GatedParams &P, uint32_t acc, uint32_t box_g, uint32_t box_u,
+                                               int r, int piece, int row, int col, float scale, float out_scale) {
     float am = 0.0f;
     uint32_t rd[32];
     tmem_ld32(acc, rd);
@@ -208,12 +193,17 @@ __device__ __forceinline__ float dgrad_columns(const GatedParams &P, uint32_t ac
     for (int o = 0; o < 2; ++o) {  // 16 columns each
         uint32_t qg[4], qu[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int at = 16 * o + 4 * k;
-            const uint64_t dh[2] = {f2_mul(f2_from_bits(rd[at], rd[at + 1]), f2_same(scale)),
-                                    f2_mul(f2_from_bits(rd[at + 2], rd[at + 3]), f2_same(scale))};
-            const uint32_t g[2] = {x.g[o][2 * k], x.g[o][2 * k + 1]}, u[2] = {x.u[o][2 * k], x.u[o][2 * k + 1]};
-            gate_grad_codes<ACT>(dh, g, u, f2_same(out_scale), qg[k], qu[k], am);
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t at = static_cast<uint32_t>(r * 128 + (((piece + 2 * o + h) ^ (r & 7)) << 4));
+            const uint4 gw = ld_shared_v4(box_g + at), uw = ld_shared_v4(box_u + at);
+            const uint32_t g[2][2] = {{gw.x, gw.y}, {gw.z, gw.w}}, u[2][2] = {{uw.x, uw.y}, {uw.z, uw.w}};
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int i = 16 * o + 8 * h + 4 * k;
+                const uint64_t dh[2] = {f2_mul(f2_from_bits(rd[i], rd[i + 1]), f2_same(scale)),
+                                        f2_mul(f2_from_bits(rd[i + 2], rd[i + 3]), f2_same(scale))};
+                gate_grad_codes<ACT>(dh, g[k], u[k], f2_same(out_scale), qg[2 * h + k], qu[2 * h + k], am);
+            }
         }
         if (row < P.rows && col + 16 * o < P.cols) {
             *reinterpret_cast<uint4 *>(out + 16 * o) = make_uint4(qg[0], qg[1], qg[2], qg[3]);
@@ -221,6 +211,11 @@ __device__ __forceinline__ float dgrad_columns(const GatedParams &P, uint32_t ac
         }
     }
     return am;
+}
+
+// Chunks of 64 columns of a dgrad tile that exist for a CTA.
+__device__ __forceinline__ int dgrad_chunks(const GatedParams &P, int cta_row0, int col0) {
+    return cta_row0 < P.rows ? min(4, (P.cols - col0 + 63) / 64) : 0;
 }
 
 template <bool PAIR, int MODE, int ACT, bool H_FP8>
@@ -238,6 +233,8 @@ __global__ void __launch_bounds__(Cfg<PAIR, MODE>::THREADS, 1) gated_kernel(cons
     auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * C::STAGES + a); };
     auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * C::STAGES + 2 + a); };
     const uint32_t drain_bar = bar0 + 8u * (2 * C::STAGES + 4);
+    auto gu_full = [&](int b) { return bar0 + 8u * (2 * C::STAGES + 5 + b); };  // dgrad
+    auto gu_empty = [&](int b) { return bar0 + 8u * (2 * C::STAGES + 5 + C::GU_CHUNKS + b); };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::SLOT_OFFSET);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::FLAG_OFFSET);
 
@@ -256,6 +253,10 @@ __global__ void __launch_bounds__(Cfg<PAIR, MODE>::THREADS, 1) gated_kernel(cons
             mbar_init(tempty_bar(a), C::TEMPTY_COUNT);
         }
         mbar_init(drain_bar, 1);
+        for (int b = 0; b < C::GU_CHUNKS; ++b) {
+            mbar_init(gu_full(b), 1);
+            mbar_init(gu_empty(b), C::EPI_WARPS);
+        }
         *abort_flag = 0;
         fence_mbar_init();
         prefetch_tmap(&P.ta);
@@ -292,13 +293,6 @@ __global__ void __launch_bounds__(Cfg<PAIR, MODE>::THREADS, 1) gated_kernel(cons
                 const int a_row = mb * C::TILE_M + static_cast<int>(rank) * ROWS_A;
                 const int col0 = nb * C::TILE_COLS;
                 const CUtensorMap *tb = PAIR && rank ? &P.tb1 : &P.tb0;
-                if constexpr (MODE == DGRAD) {  // the tile's g and u, into L2 by the time its epilogue runs
-                    if (a_row < P.rows)
-                        for (int c = col0; c < min(col0 + C::TILE_COLS, P.cols); c += 64) {
-                            prefetch_box(&P.tg, c, a_row);
-                            prefetch_box(&P.tu, c, a_row);
-                        }
-                }
                 for (int kb = 0; kb < num_kb; ++kb, ++it) {
                     const int s = static_cast<int>(it % C::STAGES);
                     if (!wait_bounded(empty_bar(s), ((it / C::STAGES) & 1u) ^ 1u, abort_flag)) {
@@ -373,25 +367,52 @@ __global__ void __launch_bounds__(Cfg<PAIR, MODE>::THREADS, 1) gated_kernel(cons
                 wait_bounded(drain_bar, 0u, &never);
             }
         }
+    } else if (MODE == DGRAD && warp == 2 + C::EPI_WARPS) {
+        if (lane == 0) {
+            // ---------------- dgrad: the producer of g and u for the epilogue
+            uint32_t n = 0;
+            bool ok = true;
+            for (int r = 0; ok && r < rounds; ++r) {
+                const int tile = serpentine_tile(r, cluster_id, num_clusters);
+                if (tile >= P.num_tiles) continue;
+                int mb, nb;
+                tile_coords(tile, P.tiles_m, P.tiles_n, P.group_m, P.group_n, mb, nb);
+                const int row0 = mb * C::TILE_M + static_cast<int>(rank) * ROWS_A, col0 = nb * C::TILE_COLS;
+                const int live = dgrad_chunks(P, row0, col0);
+                for (int c = 0; c < live; ++c, ++n) {
+                    const uint32_t b = n & 1u;
+                    if (!wait_bounded(gu_empty(b), ((n >> 1) & 1u) ^ 1u, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t box = base + C::GU_OFFSET + b * 2 * C::GU_BOX;
+                    mbar_arrive_expect_tx(gu_full(b), 2 * C::GU_BOX);
+                    tma_load_2d_cta(box, &P.tg, gu_full(b), col0 + 64 * c, row0);
+                    tma_load_2d_cta(box + C::GU_BOX, &P.tu, gu_full(b), col0 + 64 * c, row0);
+                }
+            }
+            if (!ok)  // let the loads already issued land before the CTA goes away
+                for (uint32_t j = 1; j <= 2 && j <= n; ++j) {
+                    volatile int never = 0;
+                    wait_bounded(gu_full((n - j) & 1u), ((n - j) >> 1) & 1u, &never);
+                }
+        }
     } else {
         // ---------------- epilogue warps (both CTAs of a pair)
-        constexpr int HALVES = C::EPI_WARPS / 4;  // warps that share a quarter of the rows, each its columns
-        const int q = warp & 3;                   // this warp may access TMEM lanes 32q .. 32q+31
-        const int half = (warp - 2) / 4;
+        const int q = warp & 3;  // this warp may access TMEM lanes 32q .. 32q+31
+        const int half = (warp - 2) >> 2;  // dgrad: which 32 columns of a chunk
         const float scale = __fmul_rn(__ldg(P.sinv_a), __ldg(P.sinv_b));
         const float out_scale = P.out_scale != nullptr ? __ldg(P.out_scale) : 1.0f;
         float am = 0.0f;
         int lt = 0;
+        uint32_t used = 0;  // dgrad: chunks of g and u used
         for (int r = 0; r < rounds; ++r) {
             const int tile = serpentine_tile(r, cluster_id, num_clusters);
             if (tile >= P.num_tiles) continue;
             int mb, nb;
             tile_coords(tile, P.tiles_m, P.tiles_n, P.group_m, P.group_n, mb, nb);
-            const int row = mb * C::TILE_M + static_cast<int>(rank) * ROWS_A + q * 32 + lane;
-            constexpr int COLS = 256 / HALVES;  // dgrad: this warp's columns of a tile
-            const int col0 = nb * C::TILE_COLS + (MODE == DGRAD ? half * COLS : 0);
-            GuChunk x[2];  // dgrad: fetched while the MMAs run, then 32 columns ahead
-            if constexpr (MODE == DGRAD) load_gu(P, row, col0, x[0]);
+            const int cta_row0 = mb * C::TILE_M + static_cast<int>(rank) * ROWS_A;
+            const int row = cta_row0 + q * 32 + lane, col0 = nb * C::TILE_COLS;
             const int acc = lt & 1;
             const uint32_t aph = (static_cast<uint32_t>(lt) >> 1) & 1u;
             ++lt;
@@ -405,16 +426,21 @@ __global__ void __launch_bounds__(Cfg<PAIR, MODE>::THREADS, 1) gated_kernel(cons
             if constexpr (MODE == FWD) {
                 am = fmaxf(am, forward_tile<ACT, H_FP8>(P, acc_addr, row, col0, scale, out_scale));
             } else {
+                const int live = dgrad_chunks(P, cta_row0, col0);
 #pragma unroll 1
-                for (int c = 0; c < COLS && col0 + c < P.cols; c += 64) {
-#pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        const int next = c + 32 * (p + 1);
-                        if (next < COLS) load_gu(P, row, col0 + next, x[p ^ 1]);
-                        am = fmaxf(am, dgrad_columns<ACT>(P, acc_addr + static_cast<uint32_t>(half * COLS + c + 32 * p),
-                                                          x[p], row, col0 + c + 32 * p, scale, out_scale));
-                    }
+                for (int c = 0; c < live; ++c, ++used) {
+                    const uint32_t b = used & 1u;
+                    const bool landed = wait_bounded(gu_full(b), (used >> 1) & 1u, abort_flag);
+                    ok = __all_sync(0xffffffffu, landed);
+                    if (!ok) break;
+                    const uint32_t box = base + C::GU_OFFSET + b * 2 * C::GU_BOX;
+                    const int at = 64 * c + 32 * half;
+                    am = fmaxf(am, dgrad_columns<ACT>(P, acc_addr + static_cast<uint32_t>(at), box, box + C::GU_BOX,
+                                                      q * 32 + lane, 4 * half, row, col0 + at, scale, out_scale));
+                    __syncwarp();  // every lane has used its g and u
+                    if (lane == 0) mbar_arrive(gu_empty(b));
                 }
+                if (!ok) break;
             }
             tc_fence_before();
             __syncwarp();
@@ -670,9 +696,7 @@ int launch_gated_dgrad(const uint8_t *dy8, const uint8_t *wd8, const uint16_t *g
     P.tb1 = P.tb0;
     if (!rc) rc = make_bf16_tmap(&P.tg, gu, f, m, 4 * f);
     if (!rc) rc = make_bf16_tmap(&P.tu, gu + F, f, m, 4 * f);
-    P.gu = const_cast<uint16_t *>(gu);
     P.out = dgu8;
-    P.wide = (reinterpret_cast<uintptr_t>(gu) & 31u) == 0;
     if (rc) return rc;
     if (act == FP8MP_SILU)
         return pair ? launch<true, DGRAD, FP8MP_SILU, true>(P, s, dev)
