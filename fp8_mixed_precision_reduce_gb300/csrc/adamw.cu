@@ -29,8 +29,8 @@ constexpr int kNormBlocksPerSm = 8;
 constexpr int kMaxNormBlocks = 4096;
 // Blocks per SM of a step's grid (4 are resident): shares small enough to even
 // out the tail, large enough to pay for their start. 243 M parameters, 32-bit
-// moments: 1079 us with 4, 1069 with 8, 1046 with 16, 999 with 32, 1079 with 64;
-// 8-bit: 834, 737, 706, 750, 784.
+// moments: 1079 us with 4, 1069 with 8, 1046 with 16, 999 with 32, 1079 with 64
+// (993 with 3 blocks resident, for their registers); 8-bit: 834, 737, 699, 750, 784.
 constexpr int kStepBlocksPerSm32 = 32, kStepBlocksPerSm8 = 16;
 
 // The workspace: the arrival counter, then the running sum over launches,
@@ -351,6 +351,48 @@ __device__ __forceinline__ void load_grad(const StepTensor &T, int64_t at, int c
         for (int j = 0; j < 8; ++j) g[j] = j < cnt ? bf16_bits_to_f32(p[j]) : 0.0f;
     }
 }
+// The gradients of a unit as they lie in memory, and as fp32: fetched apart, so
+// that the other loads are under way before the first of them is waited for.
+struct GradBits {
+    uint4 a, b;
+};
+__device__ __forceinline__ GradBits fetch_grad(const StepTensor &T, int64_t at, int cnt) {
+    GradBits x;
+    x.a = x.b = make_uint4(0u, 0u, 0u, 0u);
+    if (cnt == 8) {
+        if (T.grad_bf16) {
+            x.a = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(T.grad) + at));
+        } else {
+            const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const float *>(T.grad) + at);
+            x.a = __ldcs(p);
+            x.b = __ldcs(p + 1);
+        }
+        return x;
+    }
+    uint32_t w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = 0u;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        if (j >= cnt) continue;
+        if (T.grad_bf16)
+            w[j >> 1] |= static_cast<uint32_t>(static_cast<const uint16_t *>(T.grad)[at + j]) << (16 * (j & 1));
+        else
+            w[j] = __float_as_uint(static_cast<const float *>(T.grad)[at + j]);
+    }
+    x.a = make_uint4(w[0], w[1], w[2], w[3]);
+    x.b = make_uint4(w[4], w[5], w[6], w[7]);
+    return x;
+}
+__device__ __forceinline__ void grad_values(const StepTensor &T, const GradBits &x, float (&g)[8]) {
+    if (T.grad_bf16) {
+        unpack_bf16(x.a, g);
+    } else {
+        const uint32_t w[8] = {x.a.x, x.a.y, x.a.z, x.a.w, x.b.x, x.b.y, x.b.z, x.b.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[j] = __uint_as_float(w[j]);
+    }
+}
 __device__ __forceinline__ void store_copy(const StepTensor &T, int64_t at, int cnt, const float (&w)[8]) {
     if (T.copy_kind == 2) {
         const float sw = __ldg(T.copy_scale);
@@ -378,7 +420,12 @@ __device__ __forceinline__ void store_copy(const StepTensor &T, int64_t at, int 
 }
 
 // A whole unit with 8-bit moments. Per parameter it moves 15 bytes, which
-// leaves about 80 instructions at the memory's rate, so the arithmetic is done
+// leaves about 80 instructions at the memory's rate, and as many are needed: the
+// step is bound by their issue (78 per parameter at 2.5-2.9 per cycle: 243 M
+// parameters in 699 us, 0.77 of the copy rate; feeding the warps by asynchronous
+// copies, a unit ahead per thread or by a warp of its own with bulk copies,
+// raised the issue rate to 2.9 but cost as many instructions: 718-731 us). So the
+// arithmetic is done
 // two lanes at a time where it can be, and the codes are made without
 // conversions:
 //   - a byte joins the exponent of 2^23 (a byte permute) and loses it again (an
@@ -563,13 +610,13 @@ __device__ __forceinline__ void unit_8_bits(const StepTensor &T, int64_t at, int
 // The warp's 256 elements of a unit are one block of the 8-bit moments, so a
 // block's largest moment is a warp reduction and nothing leaves the warp.
 template <int BITS, int CAP>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, BITS == 8 ? 4 : 3)
 adamw_kernel(const __grid_constant__ StepBatch<CAP> batch, const StepArgs a) {
     pdl_wait();
     pdl_launch_dependents();
     const int found = a.found_inf != nullptr && *reinterpret_cast<const volatile int32_t *>(a.found_inf) != 0;
+    const Scalars s = make_scalars(a);  // (loaded beside the flag)
     if (!found) {
-        const Scalars s = make_scalars(a);
         const uint32_t seed = BITS == 8 ? *a.seed : 0u;
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         const int chunks = batch.first[batch.count];
@@ -601,9 +648,10 @@ adamw_kernel(const __grid_constant__ StepBatch<CAP> batch, const StepArgs a) {
             const int64_t left = T.n - at;
             const int cnt = left >= 8 ? 8 : (left > 0 ? static_cast<int>(left) : 0);
             float g[8], w[8], m[8], v[8];
-            load_grad(T, at, cnt, g);
+            const GradBits grad = fetch_grad(T, at, cnt);
             load8(T.w + at, cnt, w);
             if constexpr (BITS == 8) {
+                grad_values(T, grad, g);
                 const uint2 cm = load_bytes(static_cast<const uint8_t *>(T.m) + at, cnt);
                 const uint2 cv = load_bytes(static_cast<const uint8_t *>(T.v) + at, cnt);
                 const float sm = __ldg(T.sm + unit), sv = __ldg(T.sv + unit);
@@ -649,6 +697,7 @@ adamw_kernel(const __grid_constant__ StepBatch<CAP> batch, const StepArgs a) {
             } else {
                 load8(static_cast<const float *>(T.m) + at, cnt, m);
                 load8(static_cast<const float *>(T.v) + at, cnt, v);
+                grad_values(T, grad, g);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     moments(s, g[j], m[j], v[j]);
@@ -772,13 +821,18 @@ int launch_adamw_step(const fp8mp_adamw_tensor *t, int32_t n, const AdamwArgs &a
     // the tensors with fp32 moments first, then those with 8-bit ones, each in launches of one kind
     int32_t left = 0;
     for (int32_t i = 0; i < n; ++i) left += t[i].n > 0;
-    bool launched = false;
+    if (left == 0) {  // a step of nothing still counts
+        a.finish = 1;
+        const cudaError_t e = launch_step_batch<32, kStepCapSmall>(t, nullptr, 0, a, s, dev);
+        if (e != cudaSuccess)
+            return fail(FP8MP_ERR_LAUNCH, "mp_adamw_step: launch failed: %s", cudaGetErrorString(e));
+    }
     for (int bits = 32; bits >= 8; bits -= 24) {
         int32_t which[kStepCapLarge], cnt = 0;
         for (int32_t i = 0; i <= n; ++i) {
             if (i < n && t[i].n > 0 && t[i].state_bits == bits) which[cnt++] = i;
             if (cnt < kStepCapLarge && i < n) continue;
-            if (cnt == 0 && !(i == n && bits == 8 && !launched)) continue;
+            if (cnt == 0) continue;
             left -= cnt;
             a.finish = left == 0;
             cudaError_t e;
@@ -790,7 +844,6 @@ int launch_adamw_step(const fp8mp_adamw_tensor *t, int32_t n, const AdamwArgs &a
                                          : launch_step_batch<8, kStepCapLarge>(t, which, cnt, a, s, dev);
             if (e != cudaSuccess)
                 return fail(FP8MP_ERR_LAUNCH, "mp_adamw_step: launch failed: %s", cudaGetErrorString(e));
-            launched = true;
             cnt = 0;
         }
     }

@@ -195,7 +195,7 @@ class Step:
             assert torch.equal(x.copy.cpu(), want.view(torch.uint8)), ("E4M3 copy", t)
 
 
-SIZES = [1, 7, 8, 255, 256, 257, 2047, 2048, 2049, 5000, 70001]
+SIZES = [1, 7, 8, 255, 256, 257, 2047, 2048, 2049, 3839, 3840, 3841, 5000, 7680, 70001]
 
 
 @pytest.mark.parametrize("bits", [32, 8])
@@ -236,6 +236,30 @@ def test_no_tensors_at_all(cuda_lib):
     assert st.norm.item() == 0.0 and st.found.item() == 0
     st.run()
     assert st.growth.item() == 5
+    st.seed = None  # not needed without 8-bit moments
+    st.run()
+    assert st.growth.item() == 6
+
+
+def test_scales_at_any_offset(cuda_lib):
+    """The steps of the 8-bit moments need 4-byte alignment only."""
+    x = Tensor(40000, 8, seed=21)
+    for name in ("sm", "sv"):
+        s = getattr(x, name)
+        room = torch.zeros(s.numel() + 1, device="cuda")
+        room[1:] = s
+        setattr(x, name, room[1:])
+    st = Step(cuda_lib, [x])
+    st.check()
+    st.check()
+
+
+def test_large_tensors_of_both_kinds(cuda_lib):
+    tensors = [Tensor(1500001, bits, grad, copy, seed=i) for i, (bits, grad, copy) in enumerate(
+        [(8, torch.bfloat16, "e4m3"), (32, torch.float32, "bf16"), (8, torch.float32, "bf16"), (8, torch.bfloat16, None)])]
+    st = Step(cuda_lib, tensors, max_norm=1e-3)
+    st.measure()
+    st.check()
 
 
 @pytest.mark.parametrize("bits", [32, 8])
