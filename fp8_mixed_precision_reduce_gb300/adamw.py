@@ -1,0 +1,101 @@
+"""AdamW over a model's parameters in the library's many-tensor step.
+
+One call of mp_grad_norm and one of mp_adamw_step per step, whatever the number
+of parameters: the loss scale, the overflow skip, gradient clipping, the
+decoupled decay, moments in fp32 or in 8-bit codes, and the E4M3 copies of the
+weights that the next forward pass reads ([MP] "FP32 Master Copy of Weights" and
+the dynamic loss-scale procedure, "LLM) Mixed-Precision 개념 및 학습 방법
+알아보기"). This file keeps the state and passes pointers.
+"""
+
+from __future__ import annotations
+
+import torch
+
+from . import AdamWTensors, mp_adamw_step, mp_adamw_workspace_bytes, mp_grad_norm
+
+__all__ = ["AdamW"]
+
+
+class AdamW:
+    """AdamW on fp32 parameters whose gradients are of the loss times
+    ``loss_scale`` (a device tensor, adapted as the steps go).
+
+    Parameters of two or more dimensions decay by ``weight_decay``, the others
+    do not. ``state_bits`` 8 holds the moments of parameters of at least
+    ``min_8bit_size`` elements in 8 bits, the others' in 32. ``modules``: those
+    with ``copies_for_step()`` (FP8GatedMLP) get their weights' E4M3 copies
+    written by the step, under the scales of their metas: call update_scales()
+    before step().
+    """
+
+    def __init__(self, params, lr: float, betas=(0.9, 0.95), eps: float = 1e-8, weight_decay: float = 0.1,
+                 max_norm: float = 0.0, state_bits: int = 32, min_8bit_size: int = 4096, modules=(),
+                 loss_scale: float = 65536.0, growth_interval: int = 2000, seed: int = 0):
+        self.params = list(params)
+        if not self.params:
+            raise ValueError("AdamW needs at least one parameter")
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits must be 32 or 8")
+        self.lr, self.betas, self.eps, self.max_norm = lr, betas, eps, max_norm
+        self.growth_interval = growth_interval
+        dev = self.params[0].device
+        for p in self.params:
+            if p.dtype != torch.float32 or not p.is_contiguous() or p.device != dev:
+                raise ValueError("AdamW needs dense fp32 parameters on one device")
+        self.modules = list(modules)
+        self.state = []
+        for p in self.params:
+            n = p.numel()
+            if state_bits == 8 and n >= min_8bit_size:
+                blocks = (n + 255) // 256
+                self.state.append(dict(exp_avg=torch.zeros(n, dtype=torch.int8, device=dev),
+                                       exp_avg_sq=torch.zeros(n, dtype=torch.uint8, device=dev),
+                                       exp_avg_scale=torch.zeros(blocks, device=dev),
+                                       exp_avg_sq_scale=torch.zeros(blocks, device=dev)))
+            else:
+                self.state.append(dict(exp_avg=torch.zeros(n, device=dev), exp_avg_sq=torch.zeros(n, device=dev)))
+        self.weight_decay = [weight_decay if p.dim() >= 2 else 0.0 for p in self.params]
+        self.loss_scale = torch.full((1,), float(loss_scale), device=dev)
+        self.growth_tracker = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.found_inf = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.beta_pows = torch.ones(2, device=dev)
+        self.grad_norm = torch.zeros(1, device=dev)
+        self.seed = torch.full((1,), seed, dtype=torch.int32, device=dev)
+        self.workspace = torch.zeros(mp_adamw_workspace_bytes() // 4, dtype=torch.int32, device=dev)
+        self._plan, self._copies = None, None
+
+    def _tensors(self, grads) -> AdamWTensors:
+        """The step's tensors, rebuilt when a module has new copies."""
+        copies = {id(w): (c, m) for mod in self.modules for w, c, m in mod.copies_for_step()}
+        now = [(c.data_ptr(), m.scale.data_ptr()) for c, m in copies.values()]
+        if self._plan is not None and now == self._copies:
+            self._plan.set_grads(grads)
+            return self._plan
+        plan = AdamWTensors()
+        for p, g, s, decay in zip(self.params, grads, self.state, self.weight_decay):
+            c, m = copies.get(id(p), (None, None))
+            scaled = dict(copy=c, copy_scale=m.scale, copy_amax=m.cur_amax) if c is not None else {}
+            plan.add(g, p.detach(), weight_decay=decay, **s, **scaled)
+        self._plan, self._copies = plan, now
+        return plan
+
+    def step(self) -> None:
+        """One step from the parameters' .grad; nothing is read back to the host."""
+        grads = []
+        for i, p in enumerate(self.params):
+            if p.grad is None:
+                raise ValueError(f"parameter {i} has no gradient")
+            grads.append(p.grad if p.grad.is_contiguous() else p.grad.contiguous())
+        plan = self._tensors(grads)
+        mp_grad_norm(plan, self.grad_norm, self.found_inf, self.workspace)
+        mp_adamw_step(plan, self.loss_scale, self.growth_tracker, self.found_inf, self.beta_pows, self.workspace,
+                      lr=self.lr, beta1=self.betas[0], beta2=self.betas[1], eps=self.eps, seed=self.seed,
+                      grad_norm=self.grad_norm if self.max_norm > 0 else None, max_norm=self.max_norm,
+                      growth_interval=self.growth_interval)
+        for m in self.modules:
+            m.copies_written()
+
+    def zero_grad(self) -> None:
+        for p in self.params:
+            p.grad = None

@@ -1,0 +1,158 @@
+"""FP8GatedMLP: a gated feed-forward block on the library's FP8 path.
+
+y = (act(x Wg^T) * (x Wu^T)) Wd^T under the DelayedScaling recipe with the
+HYBRID format, as FP8Linear runs one linear: E4M3 for the input, the weights
+and the hidden state, E5M2 for the gradients. Forward: the cast of x, both
+projections with the gate in one launch (fp8_gated_fwd), the down projection.
+Backward: the cast of dy, its way through the down projection and the gate in
+one launch (fp8_gated_dgrad), dWd, then dx and dWg, dWu in one launch
+(fp8_gated_bwd). Any number of tokens; up to FEW_TOKENS of them (serving)
+stream the weights at the memory's rate. This file only allocates the outputs
+through torch and passes pointers.
+"""
+
+from __future__ import annotations
+
+import torch
+
+from . import (AMAX_MAX, E4M3, E5M2, FEW_TOKENS, GELU_TANH, SILU, Meta, delayed_scaling_update, fp8_gated_bwd,
+               fp8_gated_dgrad, fp8_gated_fwd, fp8_linear_bwd_rowmajor, fp8_linear_few, fp8_linear_fwd, fp8_quantize)
+
+__all__ = ["FP8GatedMLP"]
+
+
+def _rows16(rows: int, cols: int, dtype: torch.dtype, device) -> torch.Tensor:
+    """[rows rounded up to 16, cols], the added rows zero: fp8_linear_fwd and
+    fp8_linear_bwd_rowmajor take multiples of 16 tokens."""
+    t = torch.empty(((rows + 15) // 16 * 16, cols), dtype=dtype, device=device)
+    if t.shape[0] != rows:
+        t[rows:].zero_()
+    return t
+
+
+class _FP8GatedMLPFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, gate_up, down, mlp, keep):
+        K, F = mlp.features, mlp.hidden
+        x2 = x.reshape(-1, K)
+        if not x2.is_contiguous():
+            x2 = x2.contiguous()
+        M, dev = x2.shape[0], x.device
+        gu8, d8 = mlp.weight_copies()
+        X8 = torch.empty((M, K), dtype=torch.uint8, device=dev)
+        fp8_quantize(x2, E4M3, mlp.meta_x.scale, X8, None, mlp.meta_x.cur_amax)
+        few = M <= FEW_TOKENS
+        H8 = torch.empty((M, F), dtype=torch.uint8, device=dev) if few and not keep else _rows16(M, F, torch.uint8, dev)
+        gu = torch.empty((M, 2 * F), dtype=torch.bfloat16, device=dev) if keep else None
+        fp8_gated_fwd(X8, gu8, mlp.meta_x.scale_inv, mlp.meta_gate_up.scale_inv, H8[:M], act=mlp.act,
+                      h_scale=mlp.meta_h.scale, h_amax=mlp.meta_h.cur_amax, gu=gu)
+        y = torch.empty((M if few else H8.shape[0], K), dtype=x.dtype, device=dev)
+        (fp8_linear_few if few else fp8_linear_fwd)(H8[:M] if few else H8, d8, mlp.meta_h.scale_inv,
+                                                    mlp.meta_down.scale_inv, y)
+        if keep:
+            # the codes were made with this step's scales: keep those for backward
+            factors = torch.cat([mlp.meta_x.scale_inv, mlp.meta_gate_up.scale_inv, mlp.meta_h.scale_inv,
+                                 mlp.meta_down.scale_inv])
+            ctx.save_for_backward(X8, gu, H8, gu8, d8, factors)
+            ctx.mlp = mlp
+            ctx.like = (x.shape, x.dtype, gate_up.dtype, down.dtype)
+        return y[:M].reshape(x.shape)
+
+    @staticmethod
+    def backward(ctx, dy):
+        X8, gu, H8, gu8, d8, factors = ctx.saved_tensors
+        mlp = ctx.mlp
+        x_shape, x_dtype, gate_up_dtype, down_dtype = ctx.like
+        K, F, M, dev = mlp.features, mlp.hidden, X8.shape[0], dy.device
+        sinv_x, sinv_gu, sinv_h, sinv_d = factors[0:1], factors[1:2], factors[2:3], factors[3:4]
+        dy2 = dy.reshape(-1, K).to(x_dtype)
+        if not dy2.is_contiguous():
+            dy2 = dy2.contiguous()
+        md, mg = mlp.meta_dy, mlp.meta_dgu
+        D8 = _rows16(M, K, torch.uint8, dev)
+        fp8_quantize(dy2, E5M2, md.scale, D8[:M], None, md.cur_amax)
+        dx = dgate_up = ddown = None
+        if ctx.needs_input_grad[2]:
+            ddown = torch.empty((K, F), dtype=down_dtype, device=dev)
+            fp8_linear_bwd_rowmajor(D8, None, H8, md.scale_inv, None, sinv_h, None, ddown, dw_nonfinite=mlp.dw_nonfinite)
+        if ctx.needs_input_grad[0] or ctx.needs_input_grad[1]:
+            G8 = torch.empty((M, 2 * F), dtype=torch.uint8, device=dev)
+            fp8_gated_dgrad(D8[:M], d8, gu, md.scale_inv, sinv_d, mg.scale, G8, act=mlp.act, dgu_amax=mg.cur_amax)
+            if ctx.needs_input_grad[0]:
+                dx = torch.empty((M, K), dtype=x_dtype, device=dev)
+            if ctx.needs_input_grad[1]:
+                dgate_up = torch.empty((2 * F, K), dtype=gate_up_dtype, device=dev)
+            fp8_gated_bwd(None, None, X8, gu8, sinv_x, sinv_gu, None, mg.scale_inv, G8, dx, dgate_up, act=mlp.act,
+                          dw_nonfinite=mlp.dw_nonfinite if dgate_up is not None else None)
+        return (dx.reshape(x_shape) if dx is not None else None), dgate_up, ddown, None, None
+
+
+class FP8GatedMLP(torch.nn.Module):
+    """y = (act(x Wg^T) * (x Wu^T)) Wd^T with FP8 GEMMs under delayed scaling.
+
+    features and hidden must be multiples of 16. gate_up [2 hidden, features]
+    holds Wg above Wu, down [features, hidden] Wd, in high precision; their E4M3
+    copies are cast when they are not current. Call update_scales() once per
+    training step, after backward; an optimizer that writes the copies itself
+    (AdamW) does so after it. x is bf16 or fp32.
+    """
+
+    def __init__(self, features: int, hidden: int, act: int = SILU, history_len: int = 16,
+                 amax_compute_algo: int = AMAX_MAX, margin: int = 0, device="cuda", dtype: torch.dtype = torch.float32):
+        super().__init__()
+        if features % 16 or hidden % 16:
+            raise ValueError("FP8 linears need features and hidden divisible by 16")
+        if act not in (SILU, GELU_TANH):
+            raise ValueError(f"unknown activation {act}")
+        self.features, self.hidden, self.act = features, hidden, act
+        self.algo, self.margin = amax_compute_algo, margin
+
+        def weight(rows, cols):
+            bound = 1.0 / cols ** 0.5
+            return torch.nn.Parameter(torch.empty((rows, cols), device=device, dtype=dtype).uniform_(-bound, bound))
+
+        self.gate_up, self.down = weight(2 * hidden, features), weight(features, hidden)
+        self.meta_x, self.meta_gate_up = Meta(history_len, E4M3, device), Meta(history_len, E4M3, device)
+        self.meta_h, self.meta_down = Meta(history_len, E4M3, device), Meta(history_len, E4M3, device)
+        self.meta_dy, self.meta_dgu = Meta(history_len, E5M2, device), Meta(history_len, E5M2, device)
+        # 1 once a weight gradient held an Inf or NaN
+        self.dw_nonfinite = torch.zeros(1, dtype=torch.int32, device=device)
+        self._gate_up8 = torch.empty((2 * hidden, features), dtype=torch.uint8, device=device)
+        self._down8 = torch.empty((features, hidden), dtype=torch.uint8, device=device)
+        self._current = False
+
+    def metas(self):
+        return [self.meta_x, self.meta_gate_up, self.meta_h, self.meta_down, self.meta_dy, self.meta_dgu]
+
+    def weight_copies(self):
+        """The weights' E4M3 copies under their metas' scales, cast if they are
+        not current."""
+        if not self._current:
+            # new arrays: a backward pass may still hold the last ones
+            self._gate_up8, self._down8 = torch.empty_like(self._gate_up8), torch.empty_like(self._down8)
+            for w, w8, m in ((self.gate_up, self._gate_up8, self.meta_gate_up), (self.down, self._down8, self.meta_down)):
+                fp8_quantize(w.detach(), E4M3, m.scale, w8, None, m.cur_amax)
+            self._current = True
+        return self._gate_up8, self._down8
+
+    def copies_for_step(self):
+        """(weight, E4M3 copy, meta) for an optimizer that writes the copies; it
+        calls copies_written() when it has."""
+        return [(self.gate_up, self._gate_up8, self.meta_gate_up), (self.down, self._down8, self.meta_down)]
+
+    def copies_written(self) -> None:
+        self._current = True
+
+    def weights_changed(self) -> None:
+        """The weights were changed elsewhere: cast them again before their next use."""
+        self._current = False
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        keep = torch.is_grad_enabled() and (x.requires_grad or self.gate_up.requires_grad or self.down.requires_grad)
+        return _FP8GatedMLPFn.apply(x, self.gate_up, self.down, self, keep)
+
+    def update_scales(self) -> None:
+        """Roll the amax histories and refresh the scales for the next step; the
+        weights' copies, cast under the old ones, are not current after it."""
+        delayed_scaling_update(self.metas(), self.algo, self.margin)
+        self._current = False

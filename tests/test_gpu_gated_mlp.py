@@ -1,0 +1,190 @@
+"""FP8GatedMLP and AdamW together: the block's output and gradients against the
+same block in 64 bits, and the training example.
+
+FP8 rounds each operand of a GEMM by at most 2^-4 (E4M3) or 2^-3 (E5M2) of
+itself, independently from element to element, so a sum over many of them is
+off by about (2^-4 / sqrt(3)) sqrt(1 + 1) = 5 % of its spread per GEMM of two
+E4M3 operands in the 2-norm; the output sees two such GEMMs and h's rounding
+(at most 10 %), a gradient up to three with one E5M2 operand each (at most 25 %).
+What is checked here is the composition, so these rough bounds do: the kernels
+have their own tests."""
+
+import os
+import sys
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def reference(x, gate_up, down, act):
+    F = gate_up.shape[0] // 2
+    g, u = x @ gate_up[:F].T, x @ gate_up[F:].T
+    a = torch.nn.functional.silu(g) if act == 0 else torch.nn.functional.gelu(g, approximate="tanh")
+    return (a * u) @ down.T
+
+
+def relative(a, b):
+    return ((a.double() - b).norm() / b.norm()).item()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("act", [0, 1])
+@pytest.mark.parametrize("shape", [(1,), (5,), (3, 11), (64,), (65,), (2, 100), (1237,)])
+def test_block_against_64_bits(cuda_lib, shape, act, dtype):
+    from fp8_mixed_precision_reduce_gb300.gated_mlp import FP8GatedMLP
+
+    torch.manual_seed(1)
+    mlp = FP8GatedMLP(272, 528, act=act)
+    for step in range(2):  # the first step fills the histories, the second runs under their scales
+        x = torch.randn((*shape, 272), device="cuda").to(dtype).requires_grad_(True)
+        dy = (torch.randn((*shape, 272), device="cuda") * 1e-3).to(dtype)
+        mlp.zero_grad(set_to_none=True)
+        y = mlp(x)
+        y.backward(dy)
+        assert cuda_lib.fp8mp_check() == 0
+        if step == 0:
+            mlp.update_scales()
+    xr = x.detach().double().requires_grad_(True)
+    gur, dr = (w.detach().double().requires_grad_(True) for w in (mlp.gate_up, mlp.down))
+    yr = reference(xr, gur, dr, act)
+    yr.backward(dy.double())
+    assert y.shape == x.shape and y.dtype == dtype
+    assert relative(y, yr.detach()) < 0.10
+    for got, want in ((x.grad, xr.grad), (mlp.gate_up.grad, gur.grad), (mlp.down.grad, dr.grad)):
+        assert got.shape == want.shape and relative(got, want) < 0.25
+    assert mlp.dw_nonfinite.item() == 0
+
+
+def test_parts_without_gradients(cuda_lib):
+    from fp8_mixed_precision_reduce_gb300.gated_mlp import FP8GatedMLP
+
+    mlp = FP8GatedMLP(64, 96)
+    x = torch.randn((40, 64), device="cuda", requires_grad=True)
+    y = mlp(x)
+    y.sum().backward()
+    full = [x.grad, mlp.gate_up.grad, mlp.down.grad]
+    mlp.gate_up.requires_grad_(False)
+    mlp.down.requires_grad_(False)
+    mlp.gate_up.grad = mlp.down.grad = None
+    x.grad = None
+    mlp(x).sum().backward()
+    assert torch.equal(x.grad, full[0]) and mlp.gate_up.grad is None and mlp.down.grad is None
+    with torch.no_grad():
+        assert torch.equal(mlp(x), y)
+
+
+def test_gradients_after_a_recast_use_their_own_copies(cuda_lib):
+    """The scales and copies change between forward and backward: the backward
+    pass still uses those of its forward."""
+    from fp8_mixed_precision_reduce_gb300.gated_mlp import FP8GatedMLP
+
+    torch.manual_seed(2)
+    mlp = FP8GatedMLP(64, 96)
+    x = torch.randn((32, 64), device="cuda", requires_grad=True)
+    y = mlp(x)
+    y.sum().backward()
+    want = x.grad.clone()
+    x.grad = None
+    y = mlp(x)
+    # the weights' meta alone moves on: dy's and dgu's scales stay
+    cuda_lib.delayed_scaling_update([mlp.meta_gate_up, mlp.meta_down], 0)
+    mlp.weights_changed()
+    mlp.weight_copies()
+    y.sum().backward()
+    assert torch.equal(x.grad, want)
+
+
+def test_the_step_writes_what_a_cast_would(cuda_lib):
+    from fp8_mixed_precision_reduce_gb300.adamw import AdamW
+    from fp8_mixed_precision_reduce_gb300.gated_mlp import FP8GatedMLP
+
+    torch.manual_seed(3)
+    mlp = FP8GatedMLP(128, 256)
+    opt = AdamW(mlp.parameters(), lr=1e-2, state_bits=8, modules=[mlp], loss_scale=1024.0)
+    for _ in range(3):
+        x = torch.randn((48, 128), device="cuda")
+        opt.zero_grad()
+        (mlp(x).pow(2).mean() * opt.loss_scale).sum().backward()
+        mlp.update_scales()
+        opt.step()
+        assert opt.found_inf.item() == 0
+        written = [c.clone() for c in mlp.weight_copies()]
+        mlp.weights_changed()
+        assert all(torch.equal(a, b) for a, b in zip(written, mlp.weight_copies()))
+    assert opt.growth_tracker.item() == 3
+
+
+def test_an_overflowing_step_is_skipped(cuda_lib):
+    from fp8_mixed_precision_reduce_gb300.adamw import AdamW
+    from fp8_mixed_precision_reduce_gb300.gated_mlp import FP8GatedMLP
+
+    mlp = FP8GatedMLP(64, 96)
+    opt = AdamW(mlp.parameters(), lr=1e-2, modules=[mlp], loss_scale=64.0)
+    x = torch.randn((32, 64), device="cuda")
+    x[3, 5] = float("nan")
+    before = [p.detach().clone() for p in mlp.parameters()]
+    (mlp(x).sum() * opt.loss_scale).sum().backward()
+    opt.step()
+    assert opt.found_inf.item() == 1 and opt.loss_scale.item() == 32.0
+    assert all(torch.equal(a, b) for a, b in zip(before, mlp.parameters()))
+
+
+def test_refusals(cuda_lib):
+    from fp8_mixed_precision_reduce_gb300.adamw import AdamW
+    from fp8_mixed_precision_reduce_gb300.gated_mlp import FP8GatedMLP
+
+    for bad in (dict(features=60, hidden=96), dict(features=64, hidden=90), dict(features=64, hidden=96, act=7)):
+        with pytest.raises(ValueError):
+            FP8GatedMLP(**bad)
+    p = torch.nn.Parameter(torch.zeros(8, device="cuda"))
+    for params, kw in (([], {}), ([p], dict(state_bits=16)),
+                       ([torch.nn.Parameter(torch.zeros(8, device="cuda", dtype=torch.bfloat16))], {})):
+        with pytest.raises(ValueError):
+            AdamW(params, lr=1e-3, **kw)
+    with pytest.raises(ValueError):
+        AdamW([p], lr=1e-3).step()
+
+
+def plain_training(example, features, hidden, tokens, steps, lr):
+    """The example's training in fp32 torch operations with torch.optim.AdamW,
+    from the same weights and inputs."""
+    torch.manual_seed(0)
+    teacher = [torch.randn(s, device="cuda") / s[1] ** 0.5 * 1.5
+               for s in ((hidden, features), (hidden, features), (features, hidden))]
+    block = example.Block(features, hidden)
+    norm, gate_up, down = (torch.nn.Parameter(p.detach().clone()) for p in (block.norm, block.mlp.gate_up, block.mlp.down))
+    opt = torch.optim.AdamW([dict(params=[norm], weight_decay=0.0), dict(params=[gate_up, down], weight_decay=0.01)],
+                            lr=lr, betas=(0.9, 0.95), eps=1e-8)
+    losses = []
+    for _ in range(steps):
+        x = torch.randn((tokens, features), device="cuda")
+        n = x * torch.rsqrt(x.pow(2).mean(-1, keepdim=True) + 1e-6)
+        target = x + (torch.nn.functional.silu(n @ teacher[0].T) * (n @ teacher[1].T)) @ teacher[2].T
+        loss = (x + reference(n * norm, gate_up, down, 0) - target).pow(2).mean()
+        opt.zero_grad()
+        loss.backward()
+        torch.nn.utils.clip_grad_norm_([norm, gate_up, down], 1.0)
+        opt.step()
+        losses.append(loss.item())
+    return losses
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_training_example(cuda_lib, bits):
+    """The example's loss falls as it does in fp32 from the same start: the drop
+    over 150 steps within a tenth of fp32's."""
+    sys.path.insert(0, os.path.join(ROOT, "examples"))
+    try:
+        import train_gated_mlp
+    finally:
+        sys.path.pop(0)
+    sizes = dict(features=128, hidden=256, tokens=500, steps=150, lr=2e-3)
+    losses, off = train_gated_mlp.run(**sizes, bits=bits, log=lambda s: None)
+    plain = plain_training(train_gated_mlp, **sizes)
+    mean = lambda v: sum(v[-10:]) / 10  # noqa: E731
+    drop, want = losses[0] - mean(losses), plain[0] - mean(plain)
+    assert want > 0 and abs(drop - want) <= 0.1 * want, (losses[0], mean(losses), plain[0], mean(plain))
+    assert off < 0.05
