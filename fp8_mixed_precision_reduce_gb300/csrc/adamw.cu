@@ -502,8 +502,8 @@ __device__ __forceinline__ void unit_8_bits(const StepTensor &T, int64_t at, int
         uint64_t m = f2_mul(f2_pack(__fmul_rn(f0, fabsf(f0)), __fmul_rn(f1, fabsf(f1))), sm);
         uint64_t v = f2_mul(f2_mul(sq, sq), sv);
         const uint64_t u = f2_mul(f2_pack(g[2 * p], g[2 * p + 1]), f2_same(s.coef));
-        m = f2_add(f2_mul(m, f2_same(s.b1)), f2_mul(u, f2_same(s.c1)));
-        v = f2_add(f2_mul(v, f2_same(s.b2)), f2_mul(f2_mul(u, u), f2_same(s.c2)));
+        m = f2_add(f2_mul_apart(m, f2_same(s.b1)), f2_mul_apart(u, f2_same(s.c1)));
+        v = f2_add(f2_mul_apart(v, f2_same(s.b2)), f2_mul_apart(f2_mul(u, u), f2_same(s.c2)));
         m2[p] = m;
         v2[p] = v;
         float m0, m1, v0, v1, d0, d1;
@@ -550,18 +550,18 @@ __device__ __forceinline__ void unit_8_bits(const StepTensor &T, int64_t at, int
             f2_split(y, y0, y1);
             const uint64_t t = f2_fma_rz(f2_pack(sqrt_ftz(y0), sqrt_ftz(y1)), below, on);
             const uint64_t c = f2_add(t, off), d = f2_fma(c, f2_same(2.0f), one);
-            const uint64_t e = f2_fma(f2_mul(c, c), minus, y);
-            om[p] = stepped(t, f2_mul(rm, d), d, e, again);
+            const uint64_t e = f2_fma(f2_mul_apart(c, c), minus, y);
+            om[p] = stepped(t, f2_mul_apart(rm, d), d, e, again);
         }
         {
             const uint64_t y = f2_mul(v2[p], f2_same(iv));
             f2_split(y, y0, y1);
             const uint64_t t = f2_fma_rz(f2_pack(sqrt_ftz(sqrt_ftz(y0)), sqrt_ftz(sqrt_ftz(y1))), below, on);
             const uint64_t c = f2_add(t, off), up = f2_add(c, one);
-            const uint64_t q = f2_mul(c, c), lo = f2_mul(q, q), q1 = f2_mul(up, up);
-            const uint64_t d = f2_fma(lo, minus, f2_mul(q1, q1));
+            const uint64_t q = f2_mul(c, c), lo = f2_mul_apart(q, q), q1 = f2_mul(up, up);
+            const uint64_t d = f2_fma(lo, minus, f2_mul_apart(q1, q1));
             const uint64_t e = f2_fma(lo, minus, y);
-            ov[p] = stepped(t, f2_mul(rv, d), d, e, again);
+            ov[p] = stepped(t, f2_mul_apart(rv, d), d, e, again);
         }
     }
     uint32_t wm[2], wv[2];

@@ -34,7 +34,11 @@ __device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
     return d;
 }
-// The same, rounded towards zero.
+// A product that is rounded before it joins a sum: mul.f32x2 and a following
+// add.f32x2 are contracted into one fma, whatever their .rn says, where the
+// scalar instructions are not. (The sign of a zero product is lost.)
+__device__ __forceinline__ uint64_t f2_mul_apart(uint64_t a, uint64_t b) { return f2_fma(a, b, 0ull); }
+// f2_fma, rounded towards zero.
 __device__ __forceinline__ uint64_t f2_fma_rz(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t d;
     asm("fma.rz.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));

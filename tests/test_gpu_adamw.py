@@ -229,6 +229,54 @@ def test_counts_that_need_several_launches(cuda_lib, count):
     assert st.growth.item() == 1
 
 
+def codes_in_fp32(x, y, power, top, r):
+    """The header's rounding in fp32 operations, each rounded once."""
+    c = np.minimum(np.floor(y ** (1.0 / (2 if top == 127 else 4))), top).astype(np.float32)
+    one = np.float32(1)
+    c = np.where(power(c + one) <= y, c + one, c)
+    c = np.minimum(np.where(power(c) > y, c - one, c), np.float32(top))
+    lo = power(c)
+    up = r.astype(np.float32) * (power(c + one) - lo) < y - lo
+    return np.minimum(np.where(up, c + one, c), np.float32(top))
+
+
+@pytest.mark.parametrize("clip", [0.0, 1e-3, 1e-5])
+@pytest.mark.parametrize("grad", [torch.bfloat16, torch.float32])
+def test_8_bit_moments_bit_for_bit(cuda_lib, grad, clip):
+    """Moments, steps and codes equal those of the documented operations in
+    fp32, every one rounded once (no product joins a sum unrounded). A small
+    clip leaves gradients far below the moments: then all of a block decay
+    alike, and nearly every code lies at the edge of its cell."""
+    f = np.float32
+    n = 256 * 1200
+    x = Tensor(n, 8, grad, seed=31, copy=None)
+    st = Step(cuda_lib, [x], max_norm=clip)
+    st.measure()
+    for _ in range(3):
+        g, cm, cv = x.grad.float().cpu().numpy(), x.m.cpu().numpy().astype(f), x.v.cpu().numpy().astype(f)
+        sm, sv = (np.repeat(s.cpu().numpy(), 256) for s in (x.sm, x.sv))
+        pows, seed = st.pows.cpu().numpy(), st.seed.item() & 0xFFFFFFFF
+        k = f(1) / f(st.S.item())
+        if clip:
+            c = f(clip) / (f(st.norm.item()) * k + f(1e-6))
+            k = k * c if c < 1 else k
+        b1, b2 = f(0.9), f(0.95)
+        u = g * k
+        m = (cm * np.abs(cm)) * sm * b1 + u * (f(1) - b1)
+        v = ((cv * cv) * (cv * cv)) * sv * b2 + (u * u) * (f(1) - b2)
+        st.run()
+        M, V = np.abs(m).reshape(-1, 256).max(1), v.reshape(-1, 256).max(1)
+        assert_same_bits(x.sm.cpu().numpy(), M / f(16129), "steps of m")
+        assert_same_bits(x.sv.cpu().numpy(), V / f(4228250624.0), "steps of v")
+        rm, rv = uniforms(seed, 0, n)
+        im, iv = np.repeat(f(16129) / M, 256), np.repeat(f(4228250624.0) / V, 256)
+        want = codes_in_fp32(x, np.abs(m) * im, lambda c: c * c, 127, rm)
+        assert_same_bits(x.m.cpu().numpy(), np.where(m < 0, -want, want).astype(np.int8), "codes of m")
+        want = codes_in_fp32(x, v * iv, lambda c: (c * c) * (c * c), 255, rv)
+        assert_same_bits(x.v.cpu().numpy(), np.where(v > 0, np.maximum(want, 1), want).astype(np.uint8), "codes of v")
+        assert np.array_equal(pows, np.float32(pows))
+
+
 def test_no_tensors_at_all(cuda_lib):
     st = Step(cuda_lib, [], growth=4)
     st.norm.fill_(7.0)
