@@ -148,9 +148,7 @@ def _check(rc: int) -> None:
 
 
 def _ptr(t) -> int | None:
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or isinstance(t, int):
         return t
     return t.data_ptr()
 
@@ -456,8 +454,8 @@ def mp_master_step_adam(grad_bf16: torch.Tensor, master: torch.Tensor, exp_avg: 
                                       _stream(stream)))
 
 
-def _shape(t: torch.Tensor, name: str, shape, *dtypes: torch.dtype) -> None:
-    if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes or not t.is_contiguous():
+def _shape(t: torch.Tensor, name: str, shape: tuple, *dtypes: torch.dtype) -> None:
+    if t.shape != shape or t.dtype not in dtypes or not t.is_contiguous():
         raise Fp8mpError(ERR_INVALID, f"{name} must be a dense {tuple(shape)} of {' or '.join(map(str, dtypes))}, got "
                          f"{t.dtype} {tuple(t.shape)}")
 

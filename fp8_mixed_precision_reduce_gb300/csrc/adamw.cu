@@ -186,8 +186,9 @@ struct StepTensor {
     int64_t n;
     float decay;
     uint32_t ordinal;
-    int32_t grad_bf16;
-    int32_t copy_kind;  // 0 none, 1 bf16, 2 E4M3
+    int8_t grad_bf16;
+    int8_t copy_kind;  // 0 none, 1 bf16, 2 E4M3
+    int8_t codes;      // 8-bit moments
 };
 template <int CAP>
 struct StepBatch {
@@ -395,7 +396,7 @@ __device__ __forceinline__ void grad_values(const StepTensor &T, const GradBits 
 }
 __device__ __forceinline__ void store_copy(const StepTensor &T, int64_t at, int cnt, const float (&w)[8]) {
     if (T.copy_kind == 2) {
-        const float sw = __ldg(T.copy_scale);
+        const float sw = *T.copy_scale;
         const uint2 q = make_uint2(cvt_quad_probed<FP8MP_E4M3>(__fmul_rn(w[0], sw), __fmul_rn(w[1], sw), __fmul_rn(w[2], sw),
                                                  __fmul_rn(w[3], sw)),
                                    cvt_quad_probed<FP8MP_E4M3>(__fmul_rn(w[4], sw), __fmul_rn(w[5], sw), __fmul_rn(w[6], sw),
@@ -486,7 +487,7 @@ __device__ __forceinline__ void unit_8_bits(const StepTensor &T, int64_t at, int
     load8(T.w + at, 8, w);
     const uint2 cm = load_bytes(static_cast<const uint8_t *>(T.m) + at, 8);
     const uint2 cv = load_bytes(static_cast<const uint8_t *>(T.v) + at, 8);
-    const uint64_t sm = f2_same(__ldg(T.sm + unit)), sv = f2_same(__ldg(T.sv + unit));
+    const uint64_t sm = f2_same(T.sm[unit]), sv = f2_same(T.sv[unit]);
     uint64_t m2[4], v2[4];
     float mmax = 0.0f, vmax = 0.0f;
 #pragma unroll
@@ -606,18 +607,22 @@ __device__ __forceinline__ void unit_8_bits(const StepTensor &T, int64_t at, int
     store_bytes(static_cast<uint8_t *>(T.v) + at, 8, make_uint2(wv[0], wv[1]));
 }
 
-// Both kinds of moments share the walk; BITS is the moments' width.
-// The warp's 256 elements of a unit are one block of the 8-bit moments, so a
-// block's largest moment is a warp reduction and nothing leaves the warp.
-template <int BITS, int CAP>
-__global__ void __launch_bounds__(kThreads, BITS == 8 ? 4 : 3)
+// The kinds of a call's moments: all in fp32, all in 8 bits, or both. A call with
+// both runs in one launch too, each warp by its tensor's kind (61 small tensors
+// of both kinds: 9.4 us, 11.8 in a launch for each kind), a little slower for the
+// 8-bit ones (243 M parameters: 718 us, 707 in their own kernel). The warp's 256 elements of a unit are one block of the 8-bit
+// moments, so a block's largest moment is a warp reduction and nothing leaves
+// the warp.
+enum Kind { kMoments32, kMoments8, kMomentsBoth };
+template <int KIND, int CAP>
+__global__ void __launch_bounds__(kThreads, KIND == kMoments32 ? 3 : 4)
 adamw_kernel(const __grid_constant__ StepBatch<CAP> batch, const StepArgs a) {
     pdl_wait();
     pdl_launch_dependents();
-    const int found = a.found_inf != nullptr && *reinterpret_cast<const volatile int32_t *>(a.found_inf) != 0;
+    const int found = *reinterpret_cast<const volatile int32_t *>(a.found_inf) != 0;
     const Scalars s = make_scalars(a);  // (loaded beside the flag)
     if (!found) {
-        const uint32_t seed = BITS == 8 ? *a.seed : 0u;
+        const uint32_t seed = KIND == kMoments32 ? 0u : *a.seed;
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         const int chunks = batch.first[batch.count];
         int t = -1;
@@ -639,22 +644,21 @@ adamw_kernel(const __grid_constant__ StepBatch<CAP> batch, const StepArgs a) {
             const int64_t unit = static_cast<int64_t>(c - batch.first[t]) * (kThreads / 32) + warp;
             const int64_t at = unit * kUnit + 8 * lane;
             if (unit * kUnit >= T.n) continue;  // the whole warp: past the tensor's end
-            if constexpr (BITS == 8) {
-                if (unit * kUnit + kUnit <= T.n) {
-                    unit_8_bits(T, at, unit, s, shrink, key, am);
-                    continue;
-                }
+            const bool codes = KIND == kMoments8 || (KIND == kMomentsBoth && T.codes);
+            if (codes && unit * kUnit + kUnit <= T.n) {
+                unit_8_bits(T, at, unit, s, shrink, key, am);
+                continue;
             }
             const int64_t left = T.n - at;
             const int cnt = left >= 8 ? 8 : (left > 0 ? static_cast<int>(left) : 0);
             float g[8], w[8], m[8], v[8];
             const GradBits grad = fetch_grad(T, at, cnt);
             load8(T.w + at, cnt, w);
-            if constexpr (BITS == 8) {
+            if (codes) {
                 grad_values(T, grad, g);
                 const uint2 cm = load_bytes(static_cast<const uint8_t *>(T.m) + at, cnt);
                 const uint2 cv = load_bytes(static_cast<const uint8_t *>(T.v) + at, cnt);
-                const float sm = __ldg(T.sm + unit), sv = __ldg(T.sv + unit);
+                const float sm = T.sm[unit], sv = T.sv[unit];
                 const uint32_t bm[2] = {cm.x, cm.y}, bv[2] = {cv.x, cv.y};
                 float mmax = 0.0f, vmax = 0.0f;
 #pragma unroll
@@ -769,7 +773,7 @@ cudaError_t launch_norm_batch(const fp8mp_adamw_tensor *t, int32_t n, Workspace 
                          found, finish);
 }
 
-template <int BITS, int CAP>
+template <int KIND, int CAP>
 cudaError_t launch_step_batch(const fp8mp_adamw_tensor *t, const int32_t *which, int32_t n, const StepArgs &a,
                               cudaStream_t s, const DeviceInfo &dev) {
     StepBatch<CAP> b;
@@ -780,13 +784,22 @@ cudaError_t launch_step_batch(const fp8mp_adamw_tensor *t, const int32_t *which,
         const fp8mp_adamw_tensor &T = t[which[i]];
         b.t[i] = StepTensor{T.grad, T.master, T.exp_avg, T.exp_avg_sq, T.exp_avg_scale, T.exp_avg_sq_scale, T.copy,
                             T.copy_scale, T.copy_amax, T.n, T.weight_decay, static_cast<uint32_t>(which[i]),
-                            T.grad_dtype == FP8MP_BF16, T.copy == nullptr ? 0 : (T.copy_scale == nullptr ? 1 : 2)};
+                            static_cast<int8_t>(T.grad_dtype == FP8MP_BF16),
+                            static_cast<int8_t>(T.copy == nullptr ? 0 : (T.copy_scale == nullptr ? 1 : 2)),
+                            static_cast<int8_t>(T.state_bits == 8)};
         chunks += (T.n + kChunk - 1) / kChunk;
         b.first[i + 1] = static_cast<int32_t>(chunks);
     }
-    int64_t blocks = static_cast<int64_t>(dev.num_sms) * (BITS == 8 ? kStepBlocksPerSm8 : kStepBlocksPerSm32);
+    int64_t blocks = static_cast<int64_t>(dev.num_sms) * (KIND == kMoments32 ? kStepBlocksPerSm32 : kStepBlocksPerSm8);
     if (blocks > chunks) blocks = chunks < 1 ? 1 : chunks;
-    return launch_kernel(adamw_kernel<BITS, CAP>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, s, b, a);
+    return launch_kernel(adamw_kernel<KIND, CAP>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, s, b, a);
+}
+
+template <int KIND>
+cudaError_t launch_step(const fp8mp_adamw_tensor *t, const int32_t *which, int32_t n, const StepArgs &a,
+                        cudaStream_t s, const DeviceInfo &dev) {
+    return n <= kStepCapSmall ? launch_step_batch<KIND, kStepCapSmall>(t, which, n, a, s, dev)
+                              : launch_step_batch<KIND, kStepCapLarge>(t, which, n, a, s, dev);
 }
 
 }  // namespace
@@ -818,35 +831,21 @@ int launch_adamw_step(const fp8mp_adamw_tensor *t, int32_t n, const AdamwArgs &a
     StepArgs a = {args.loss_scale, args.growth, args.found_inf, args.beta_pows, args.seed, args.grad_norm,
                   args.max_norm, args.lr, args.b1, args.b2, args.eps, args.backoff, args.growth_factor, args.interval,
                   0, static_cast<Workspace *>(args.workspace)};
-    // the tensors with fp32 moments first, then those with 8-bit ones, each in launches of one kind
-    int32_t left = 0;
-    for (int32_t i = 0; i < n; ++i) left += t[i].n > 0;
-    if (left == 0) {  // a step of nothing still counts
-        a.finish = 1;
-        const cudaError_t e = launch_step_batch<32, kStepCapSmall>(t, nullptr, 0, a, s, dev);
+    bool codes = false, wide = false;
+    for (int32_t i = 0; i < n; ++i)
+        if (t[i].n > 0) (t[i].state_bits == 8 ? codes : wide) = true;
+    const auto launch = !codes ? launch_step<kMoments32> : (wide ? launch_step<kMomentsBoth> : launch_step<kMoments8>);
+    int32_t at = 0;
+    do {  // (a step of nothing still counts: one launch at least)
+        int32_t which[kStepCapLarge], cnt = 0;
+        for (; at < n && cnt < kStepCapLarge; ++at)
+            if (t[at].n > 0) which[cnt++] = at;
+        while (at < n && t[at].n == 0) ++at;
+        a.finish = at == n;
+        const cudaError_t e = launch(t, which, cnt, a, s, dev);
         if (e != cudaSuccess)
             return fail(FP8MP_ERR_LAUNCH, "mp_adamw_step: launch failed: %s", cudaGetErrorString(e));
-    }
-    for (int bits = 32; bits >= 8; bits -= 24) {
-        int32_t which[kStepCapLarge], cnt = 0;
-        for (int32_t i = 0; i <= n; ++i) {
-            if (i < n && t[i].n > 0 && t[i].state_bits == bits) which[cnt++] = i;
-            if (cnt < kStepCapLarge && i < n) continue;
-            if (cnt == 0) continue;
-            left -= cnt;
-            a.finish = left == 0;
-            cudaError_t e;
-            if (bits == 32)
-                e = cnt <= kStepCapSmall ? launch_step_batch<32, kStepCapSmall>(t, which, cnt, a, s, dev)
-                                         : launch_step_batch<32, kStepCapLarge>(t, which, cnt, a, s, dev);
-            else
-                e = cnt <= kStepCapSmall ? launch_step_batch<8, kStepCapSmall>(t, which, cnt, a, s, dev)
-                                         : launch_step_batch<8, kStepCapLarge>(t, which, cnt, a, s, dev);
-            if (e != cudaSuccess)
-                return fail(FP8MP_ERR_LAUNCH, "mp_adamw_step: launch failed: %s", cudaGetErrorString(e));
-            cnt = 0;
-        }
-    }
+    } while (at < n);
     return FP8MP_OK;
 }
 

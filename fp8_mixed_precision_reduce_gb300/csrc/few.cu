@@ -227,11 +227,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) few_kernel(const __grid_consta
     if (warp == 1) tmem_dealloc<false>(tmem, C::TMEM_COLS);
 
     // this CTA's share of the tile's outputs, four tokens at a time; neighbouring threads take neighbouring outputs
-    const float scale = __fmul_rn(__ldg(P.sinv_a), __ldg(P.sinv_b));
+    const float scale = __fmul_rn(*P.sinv_a, *P.sinv_b);
     constexpr int TILE_OUTS = GATED ? 64 : W_ROWS;
     const int mine = TILE_OUTS / static_cast<int>(splits);  // 8 .. 128, a power of two
     const int shift = 31 - __clz(mine);
-    const float h_scale = GATED && P.out_scale != nullptr ? __ldg(P.out_scale) : 0.0f;
+    const float h_scale = GATED && P.out_scale != nullptr ? *P.out_scale : 0.0f;
     float am = 0.0f;
     for (int i = threadIdx.x; i < mine * ((P.rows + 3) / 4); i += NUM_THREADS) {
         const int m0 = 4 * (i >> shift), o = static_cast<int>(rank) * mine + (i & (mine - 1));

@@ -422,8 +422,8 @@ __global__ void __launch_bounds__(Cfg<PAIR, MODE>::THREADS, 1) gated_kernel(cons
         // ---------------- epilogue warps (both CTAs of a pair)
         const int q = warp & 3;  // this warp may access TMEM lanes 32q .. 32q+31
         const int half = (warp - 2) >> 2;  // dgrad: which 32 columns of a chunk
-        const float scale = __fmul_rn(__ldg(P.sinv_a), __ldg(P.sinv_b));
-        const float out_scale = P.out_scale != nullptr ? __ldg(P.out_scale) : 1.0f;
+        const float scale = __fmul_rn(*P.sinv_a, *P.sinv_b);
+        const float out_scale = P.out_scale != nullptr ? *P.out_scale : 1.0f;
         float am = 0.0f;
         int lt = 0;
         uint32_t used = 0;  // dgrad: chunks of g and u used
@@ -528,11 +528,11 @@ struct GatePiece {
 
 template <int ACT, bool BF16>
 __global__ void __launch_bounds__(kGateThreads)
-gate_bwd_kernel(const void *__restrict__ dh, const uint16_t *__restrict__ gu, int64_t rows, int64_t cols,
-                const float *__restrict__ scale_p, uint8_t *__restrict__ dgu8, float *__restrict__ amax) {
+gate_bwd_kernel(const void *dh, const uint16_t *gu, int64_t rows, int64_t cols, const float *scale_p, uint8_t *dgu8,
+                float *amax) {
     pdl_wait();
     pdl_launch_dependents();
-    const uint64_t scale = f2_same(__ldg(scale_p));
+    const uint64_t scale = f2_same(*scale_p);
     float am = 0.0f;
     // this thread's pieces are `stride` apart; its place advances without a division
     const int64_t per_row = cols >> 3;
