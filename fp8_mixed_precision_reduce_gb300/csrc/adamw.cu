@@ -463,14 +463,15 @@ __device__ __forceinline__ uint32_t sign_bytes(float a, float b) {
     return r;
 }
 // The last bytes of t's lanes, one more where s < e, in the last two bytes of the
-// result; `again` collects in its first bit whether s < e - d anywhere. Signs of
-// differences stand for the comparisons.
+// result; `again` collects in its first bit whether s < e - d anywhere (or nearly:
+// s - e < -d (1 - 2^-20) is what it tests). Signs of differences stand for the
+// comparisons.
 __device__ __forceinline__ uint32_t stepped(uint64_t t, uint64_t s, uint64_t d, uint64_t e, uint32_t &again) {
-    const uint64_t minus = f2_pack(-1.0f, -1.0f);
     float t0, t1, z0, z1, x0, x1;
     f2_split(t, t0, t1);
-    f2_split(f2_fma(e, minus, s), z0, z1);
-    f2_split(f2_fma(f2_fma(d, minus, e), minus, s), x0, x1);
+    const uint64_t z = f2_fma(e, f2_same(-1.0f), s);
+    f2_split(z, z0, z1);
+    f2_split(f2_fma(d, f2_same(1.0f - 0x1p-20f), z), x0, x1);
     again |= __float_as_uint(x0) | __float_as_uint(x1);
     return __byte_perm(__float_as_uint(t0) + (__float_as_uint(z0) >> 31),
                        __float_as_uint(t1) + (__float_as_uint(z1) >> 31), 0x0040u);
