@@ -8,12 +8,18 @@
 //   - the weights are the MMA's M operand (128 rows per tile; gated: 64 gate
 //     rows and the 64 up rows of the same outputs), the tokens its N operand
 //     (16, 32 or 64 columns, rows past the last token zero-filled), so a stage
-//     is 16 KB of weights and 2-8 KB of tokens, in a ring of about 108 KB: two
+//     is 16 KB of weights and 2-8 KB of tokens, in a ring of about 100 KB: two
 //     CTAs share an SM and one streams while the other starts or ends;
 //   - a tile's contraction is split over the S CTAs of a cluster (split_for
-//     below); each leaves its fp32 partial sums in its shared memory, and each
-//     adds S-th of the outputs over all of them, in rank order, through
-//     distributed shared memory: no workspace, no atomics on the sums.
+//     below). Each owns an S-th of the tile's outputs; all send it their fp32
+//     partial sums of those through distributed shared memory, and after one
+//     cluster barrier it adds them from its own, in rank order: no workspace, no
+//     atomics on the sums, and no CTA has to outlive its peers. (Reading the
+//     peers' sums instead takes a second barrier, about 1 us, and 16-byte reads
+//     from 32 rows at once, 2-3 us for 33 tokens.)
+// One token through 4096 -> 2 x 14336: 20.6 us (17.3 at the copy rate), through
+// 14336 -> 4096: 12.1 (8.7); 65536 x 14336: 137 us, the copy rate. What is left is
+// the start, about 2 us to the first bytes, and the end.
 #include <atomic>
 #include <cstring>
 #include <mutex>
@@ -34,14 +40,14 @@ constexpr uint32_t kMaxSplits = 8;  // CTAs that may share a tile's contraction 
 template <int NT>
 struct Cfg {
     static constexpr int STAGE_BYTES = W_ROWS * BK + NT * BK;
-    static constexpr int STAGES = (108 * 1024) / STAGE_BYTES;
-    static constexpr int PITCH = NT + 4;  // floats per row of the partial sums: conflict-free 16-byte stores
-    static constexpr int BAR_OFFSET = STAGES * STAGE_BYTES;
+    static constexpr int RECV_BYTES = W_ROWS * NT * 4;  // partial sums from all ranks for this CTA's outputs
+    static constexpr int STAGES = (112 * 1024 - RECV_BYTES) / STAGE_BYTES;
+    static constexpr int RECV_OFFSET = STAGES * STAGE_BYTES;
+    static constexpr int BAR_OFFSET = RECV_OFFSET + RECV_BYTES;
     static constexpr int SLOT_OFFSET = BAR_OFFSET + (2 * STAGES + 2) * 8;
     static constexpr int FLAG_OFFSET = SLOT_OFFSET + 8;
     static constexpr int SMEM_ALLOC = FLAG_OFFSET + 8 + 1024;
     static constexpr uint32_t TMEM_COLS = NT < 32 ? 32 : NT;
-    static_assert(W_ROWS * PITCH * 4 <= STAGES * STAGE_BYTES, "the partial sums reuse the ring");
     static_assert(2 * (SMEM_ALLOC + 1024) <= 233472, "two CTAs per SM");
 };
 
@@ -75,28 +81,11 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         : "memory");
 }
 
-// Adds the cluster's partial sums of weight row `row` and tokens m .. m + 3, in
-// rank order; every rank's are asked for before the first is used.
-template <int NT>
-__device__ __forceinline__ void joined(uint32_t base, int row, int m, uint32_t splits, float (&s)[4]) {
-    const uint32_t at = base + static_cast<uint32_t>((row * Cfg<NT>::PITCH + m) * 4);
-    float part[kMaxSplits][4];
-#pragma unroll
-    for (uint32_t r = 0; r < kMaxSplits; ++r)
-        if (r < splits)
-            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                         : "=f"(part[r][0]), "=f"(part[r][1]), "=f"(part[r][2]), "=f"(part[r][3])
-                         : "r"(mapa_shared(at, r))
-                         : "memory");
-#pragma unroll
-    for (int j = 0; j < 4; ++j) s[j] = part[0][j];
-#pragma unroll
-    for (uint32_t r = 1; r < kMaxSplits; ++r)
-        if (r < splits) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s[j] = __fadd_rn(s[j], part[r][j]);
-        }
+__device__ __forceinline__ void st_shared_cluster_f32(uint32_t cluster_addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // GATED: ACT is the activation; otherwise unused.
 template <bool GATED, int ACT, int NT>
@@ -138,11 +127,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) few_kernel(const __grid_consta
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    if (splits > 1) cluster_arrive();  // this CTA has started: its peers may write to it
     pdl_wait();
 
     // this CTA's share of the contraction (never empty: splits <= num_kb)
     const int kb0 = static_cast<int>(static_cast<int64_t>(P.num_kb) * rank / splits);
     const int kb1 = static_cast<int>(static_cast<int64_t>(P.num_kb) * (rank + 1) / splits);
+    bool failed = false;
     if (warp == 0) {
         if (lane == 0) {
             pdl_launch_dependents();
@@ -201,86 +192,110 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) few_kernel(const __grid_consta
         int ok = 1;
         if (lane == 0) ok = wait_bounded(done_bar, 0u, abort_flag) ? 1 : 0;
         ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (ok) {
-            // every MMA is complete, so every stage has been read: the ring
-            // holds the partial sums from here on
-            tc_fence_after();
-            const int q = warp & 3, row = 32 * q + lane;
-            float *dst = reinterpret_cast<float *>(smem) + row * C::PITCH;
+        failed = !ok;
+    }
+    __syncwarp();
+    if (splits > 1) cluster_wait();
+    // local rows (weight rows whose sums one CTA owns) of the tile: gated, the
+    // gate rows and then the up rows of its outputs
+    constexpr int TILE_OUTS = GATED ? 64 : W_ROWS;
+    const int mine = TILE_OUTS / static_cast<int>(splits);  // 8 .. 128, a power of two
+    const int local_rows = W_ROWS / static_cast<int>(splits);
+    if (warp >= 2 && !failed) {
+        tc_fence_after();
+        const int q = warp & 3, row = 32 * q + lane;
+        const int o = row & (TILE_OUTS - 1);
+        const uint32_t owner = static_cast<uint32_t>(o / mine);
+        const int lr = (row / TILE_OUTS) * mine + (o & (mine - 1));
+        // received sums: [rank][token][local row]
+        uint32_t dst = base + C::RECV_OFFSET + static_cast<uint32_t>((rank * NT * local_rows + lr) * 4);
+        if (splits > 1) dst = mapa_shared(dst, owner);
 #pragma unroll
-            for (int c = 0; c < NT; c += 16) {
-                uint32_t r[16];
-                tmem_ld16(tmem + static_cast<uint32_t>(c) + (static_cast<uint32_t>(32 * q) << 16), r);
+        for (int c = 0; c < NT; c += 16) {
+            if (c >= P.rows) break;
+            uint32_t r[16];
+            tmem_ld16(tmem + static_cast<uint32_t>(c) + (static_cast<uint32_t>(32 * q) << 16), r);
 #pragma unroll
-                for (int j = 0; j < 16; j += 4)
-                    *reinterpret_cast<uint4 *>(dst + c + j) = make_uint4(r[j], r[j + 1], r[j + 2], r[j + 3]);
-            }
+            for (int j = 0; j < 16; ++j)
+                if (c + j < P.rows)
+                    st_shared_cluster_f32(dst + static_cast<uint32_t>((c + j) * local_rows * 4), __uint_as_float(r[j]));
         }
     }
     __syncwarp();
     tc_fence_before();
-    if (splits > 1)
-        cluster_sync_all();
-    else
-        __syncthreads();
+    if (splits > 1) cluster_arrive();
+    __syncthreads();  // (tensor memory has been read by every warp)
     tc_fence_after();
     if (warp == 1) tmem_dealloc<false>(tmem, C::TMEM_COLS);
+    if (splits > 1) cluster_wait();
 
-    // this CTA's share of the tile's outputs, four tokens at a time; neighbouring threads take neighbouring outputs
+    // this CTA's outputs, four at a time, all tokens
     const float scale = __fmul_rn(*P.sinv_a, *P.sinv_b);
-    constexpr int TILE_OUTS = GATED ? 64 : W_ROWS;
-    const int mine = TILE_OUTS / static_cast<int>(splits);  // 8 .. 128, a power of two
-    const int shift = 31 - __clz(mine);
+    const int quads = mine >> 2, shift = 31 - __clz(quads);
     const float h_scale = GATED && P.out_scale != nullptr ? *P.out_scale : 0.0f;
+    const float *recv = reinterpret_cast<const float *>(smem + C::RECV_OFFSET);
+    auto joined = [&](int lr, int m, float(&s)[4]) {  // in rank order
+        const float4 first = *reinterpret_cast<const float4 *>(recv + m * local_rows + lr);
+        s[0] = first.x, s[1] = first.y, s[2] = first.z, s[3] = first.w;
+        for (uint32_t r = 1; r < splits; ++r) {
+            const float4 x = *reinterpret_cast<const float4 *>(recv + (r * NT + m) * local_rows + lr);
+            s[0] = __fadd_rn(s[0], x.x), s[1] = __fadd_rn(s[1], x.y);
+            s[2] = __fadd_rn(s[2], x.z), s[3] = __fadd_rn(s[3], x.w);
+        }
+    };
     float am = 0.0f;
-    for (int i = threadIdx.x; i < mine * ((P.rows + 3) / 4); i += NUM_THREADS) {
-        const int m0 = 4 * (i >> shift), o = static_cast<int>(rank) * mine + (i & (mine - 1));
-        const int64_t col = static_cast<int64_t>(tile) * TILE_OUTS + o;
-        if (col >= P.outs) continue;
-        float a[4], b[4];
-        joined<NT>(base, o, m0, splits, a);
-        if constexpr (GATED) joined<NT>(base, 64 + o, m0, splits, b);
-        float bias = 0.0f;
-        if (!GATED && P.bias != nullptr)
-            bias = P.bias_bf16 ? bf16_bits_to_f32(static_cast<const uint16_t *>(P.bias)[col])
-                               : static_cast<const float *>(P.bias)[col];
+    for (int i = threadIdx.x; i < quads * P.rows; i += NUM_THREADS) {
+        const int m = i >> shift, o = 4 * (i & (quads - 1));
+        const int64_t col = static_cast<int64_t>(tile) * TILE_OUTS + static_cast<int64_t>(rank) * mine + o;
+        if (col >= P.outs) continue;  // (P.outs is a multiple of 16)
+        const int64_t at = static_cast<int64_t>(m) * P.outs + col;
+        float a[4], y[4];
+        joined(o, m, a);
+        if constexpr (GATED) {
+            float u[4];
+            joined(mine + o, m, u);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int m = m0 + j;
-            if (m >= P.rows) break;
-            const int64_t at = static_cast<int64_t>(m) * P.outs + col;
-            if constexpr (GATED) {
-                const float g = __fmul_rn(a[j], scale), u = __fmul_rn(b[j], scale);
-                float p, unused;
-                f2_split(gate_act<ACT>(f2_pack(g, 0.0f)), p, unused);
-                const float h = p * u;
-                am = fmaxf(am, fabsf(h));
-                if (P.out_scale != nullptr)
-                    static_cast<uint8_t *>(P.out)[at] =
-                        static_cast<uint8_t>(cvt_pair<FP8MP_E4M3>(__fmul_rn(h, h_scale), 0.0f) & 0xFFu);
-                else
-                    static_cast<__nv_bfloat16 *>(P.out)[at] = __float2bfloat16_rn(h);
-                if (P.gu != nullptr) {
-                    __nv_bfloat16 *row =
-                        reinterpret_cast<__nv_bfloat16 *>(P.gu) + static_cast<int64_t>(m) * 2 * P.outs;
-                    row[col] = __float2bfloat16_rn(g);
-                    row[P.outs + col] = __float2bfloat16_rn(u);
-                }
-            } else {
-                float y = P.bias != nullptr ? __fmaf_rn(a[j], scale, bias) : __fmul_rn(a[j], scale);
-                if (P.out_bf16) {
-                    const __nv_bfloat16 v = __float2bfloat16_rn(y);
-                    static_cast<__nv_bfloat16 *>(P.out)[at] = v;
-                    y = __bfloat162float(v);
-                } else {
-                    static_cast<float *>(P.out)[at] = y;
-                }
-                am = fmaxf(am, fabsf(y));
+            for (int j = 0; j < 4; j += 2) {
+                const uint64_t g2 = f2_mul(f2_pack(a[j], a[j + 1]), f2_same(scale));
+                const uint64_t u2 = f2_mul(f2_pack(u[j], u[j + 1]), f2_same(scale));
+                f2_split(g2, a[j], a[j + 1]);
+                f2_split(u2, u[j], u[j + 1]);
+                f2_split(f2_mul(gate_act<ACT>(g2), u2), y[j], y[j + 1]);
+                am = fmaxf(am, fmaxf(fabsf(y[j]), fabsf(y[j + 1])));
             }
+            if (P.out_scale != nullptr)
+                *reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(P.out) + at) =
+                    cvt_quad<FP8MP_E4M3>(__fmul_rn(y[0], h_scale), __fmul_rn(y[1], h_scale), __fmul_rn(y[2], h_scale),
+                                         __fmul_rn(y[3], h_scale));
+            else
+                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(P.out) + at) =
+                    make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+            if (P.gu != nullptr) {
+                uint16_t *row = P.gu + static_cast<int64_t>(m) * 2 * P.outs + col;
+                *reinterpret_cast<uint2 *>(row) = make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
+                *reinterpret_cast<uint2 *>(row + P.outs) = make_uint2(pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]));
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                y[j] = __fmul_rn(a[j], scale);
+                if (P.bias != nullptr)
+                    y[j] = __fmaf_rn(a[j], scale,
+                                     P.bias_bf16 ? bf16_bits_to_f32(static_cast<const uint16_t *>(P.bias)[col + j])
+                                                 : static_cast<const float *>(P.bias)[col + j]);
+            }
+            if (P.out_bf16) {
+                const uint32_t lo = pack_bf16x2(y[0], y[1]), hi = pack_bf16x2(y[2], y[3]);
+                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(P.out) + at) = make_uint2(lo, hi);
+                y[0] = __uint_as_float(lo << 16), y[1] = __uint_as_float(lo & 0xFFFF0000u);
+                y[2] = __uint_as_float(hi << 16), y[3] = __uint_as_float(hi & 0xFFFF0000u);
+            } else {
+                *reinterpret_cast<float4 *>(static_cast<float *>(P.out) + at) = make_float4(y[0], y[1], y[2], y[3]);
+            }
+            am = fmaxf(fmaxf(am, fmaxf(fabsf(y[0]), fabsf(y[1]))), fmaxf(fabsf(y[2]), fabsf(y[3])));
         }
     }
     if (P.out_amax != nullptr) block_amax_atomic(am, P.out_amax);
-    if (splits > 1) cluster_sync_all();  // no CTA leaves while a peer may read its sums
 }
 
 // How many CTAs share a tile's contraction. The grid runs two CTAs to an SM;
