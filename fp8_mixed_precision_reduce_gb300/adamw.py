@@ -29,6 +29,8 @@ class AdamW:
     before step().
     """
 
+    _SCALARS = ("loss_scale", "growth_tracker", "beta_pows", "seed")
+
     def __init__(self, params, lr: float, betas=(0.9, 0.95), eps: float = 1e-8, weight_decay: float = 0.1,
                  max_norm: float = 0.0, state_bits: int = 32, min_8bit_size: int = 4096, modules=(),
                  loss_scale: float = 65536.0, growth_interval: int = 2000, seed: int = 0):
@@ -93,8 +95,26 @@ class AdamW:
                       lr=self.lr, beta1=self.betas[0], beta2=self.betas[1], eps=self.eps, seed=self.seed,
                       grad_norm=self.grad_norm if self.max_norm > 0 else None, max_norm=self.max_norm,
                       growth_interval=self.growth_interval)
+        for p in self.params:
+            torch.autograd.graph.increment_version(p)
         for m in self.modules:
             m.copies_written()
+
+    def state_dict(self) -> dict:
+        """Everything but the parameters that the next step depends on."""
+        return dict(state=[{k: v.clone() for k, v in s.items()} for s in self.state],
+                    scalars={k: getattr(self, k).clone() for k in self._SCALARS})
+
+    def load_state_dict(self, saved: dict) -> None:
+        if len(saved["state"]) != len(self.state):
+            raise ValueError(f"{len(saved['state'])} saved states for {len(self.state)} parameters")
+        for mine, s in zip(self.state, saved["state"]):
+            if {k: (v.dtype, v.shape) for k, v in mine.items()} != {k: (v.dtype, v.shape) for k, v in s.items()}:
+                raise ValueError("a saved state has other types or sizes than its parameter's")
+            for k, v in s.items():
+                mine[k].copy_(v)
+        for k in self._SCALARS:
+            getattr(self, k).copy_(saved["scalars"][k])
 
     def zero_grad(self) -> None:
         for p in self.params:

@@ -17,8 +17,8 @@
 //     atomics on the sums, and no CTA has to outlive its peers. (Reading the
 //     peers' sums instead takes a second barrier, about 1 us, and 16-byte reads
 //     from 32 rows at once, 2-3 us for 33 tokens.)
-// One token through 4096 -> 2 x 14336: 20.6 us (17.3 at the copy rate), through
-// 14336 -> 4096: 12.1 (8.7); 65536 x 14336: 137 us, the copy rate. What is left is
+// One token through 4096 -> 2 x 14336: 21.2 us (17.3 at the copy rate), through
+// 14336 -> 4096: 12.9 (8.7); 65536 x 14336: 137 us, the copy rate. What is left is
 // the start, about 2 us to the first bytes, and the end.
 #include <atomic>
 #include <cstring>

@@ -119,7 +119,7 @@ class FP8GatedMLP(torch.nn.Module):
         self.dw_nonfinite = torch.zeros(1, dtype=torch.int32, device=device)
         self._gate_up8 = torch.empty((2 * hidden, features), dtype=torch.uint8, device=device)
         self._down8 = torch.empty((features, hidden), dtype=torch.uint8, device=device)
-        self._current = False
+        self._cast_of = None  # versions of the weights that the copies are of
 
     def metas(self):
         return [self.meta_x, self.meta_gate_up, self.meta_h, self.meta_down, self.meta_dy, self.meta_dgu]
@@ -127,12 +127,12 @@ class FP8GatedMLP(torch.nn.Module):
     def weight_copies(self):
         """The weights' E4M3 copies under their metas' scales, cast if they are
         not current."""
-        if not self._current:
+        if self._cast_of != self._weight_versions():
             # new arrays: a backward pass may still hold the last ones
             self._gate_up8, self._down8 = torch.empty_like(self._gate_up8), torch.empty_like(self._down8)
             for w, w8, m in ((self.gate_up, self._gate_up8, self.meta_gate_up), (self.down, self._down8, self.meta_down)):
                 fp8_quantize(w.detach(), E4M3, m.scale, w8, None, m.cur_amax)
-            self._current = True
+            self._cast_of = self._weight_versions()
         return self._gate_up8, self._down8
 
     def copies_for_step(self):
@@ -141,11 +141,19 @@ class FP8GatedMLP(torch.nn.Module):
         return [(self.gate_up, self._gate_up8, self.meta_gate_up), (self.down, self._down8, self.meta_down)]
 
     def copies_written(self) -> None:
-        self._current = True
+        """The copies are of the weights as they are now. A backward pass that
+        still needs the ones before fails, as after any change in place."""
+        for w8 in (self._gate_up8, self._down8):
+            torch.autograd.graph.increment_version(w8)
+        self._cast_of = self._weight_versions()
+
+    def _weight_versions(self):
+        return self.gate_up._version, self.down._version
 
     def weights_changed(self) -> None:
-        """The weights were changed elsewhere: cast them again before their next use."""
-        self._current = False
+        """Cast the weights again before their next use (for changes that torch
+        does not see; its own are noticed)."""
+        self._cast_of = None
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         keep = torch.is_grad_enabled() and (x.requires_grad or self.gate_up.requires_grad or self.down.requires_grad)
@@ -155,4 +163,4 @@ class FP8GatedMLP(torch.nn.Module):
         """Roll the amax histories and refresh the scales for the next step; the
         weights' copies, cast under the old ones, are not current after it."""
         delayed_scaling_update(self.metas(), self.algo, self.margin)
-        self._current = False
+        self._cast_of = None

@@ -451,6 +451,48 @@ def test_8_bit_moments_train_as_32_bit_ones_do(cuda_lib):
     assert losses[32] < 0.01 * start and losses[8] < 0.01 * start, (losses, start)
 
 
+@pytest.mark.slow
+def test_more_than_2_32_elements(cuda_lib):
+    """One tensor of 2^32 + 10007 elements with 8-bit moments, zero but for the
+    last 3000 elements: they and the random numbers of their places are right."""
+    n, tail = 2 ** 32 + 10007, 3000
+    z = lambda dtype: torch.zeros(n, dtype=dtype, device="cuda")  # noqa: E731
+    blocks = (n + 255) // 256
+    x = Tensor(1, 8, copy=None)
+    x.n, x.grad, x.master, x.m, x.v = n, z(torch.bfloat16), z(torch.float32), z(torch.int8), z(torch.uint8)
+    x.sm, x.sv = torch.zeros(blocks, device="cuda"), torch.zeros(blocks, device="cuda")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    x.grad[-tail:] = torch.randn(tail, generator=g, device="cuda").to(torch.bfloat16)
+    st = Step(cuda_lib, [x], t=0)
+    st.measure()
+    want = float(x.grad[-tail:].double().square().sum()) ** 0.5
+    assert abs(st.norm.item() - want) <= 1e-6 * want and st.found.item() == 0
+    seed = st.seed.item() & 0xFFFFFFFF
+    st.run()
+    assert not x.m[:-tail].any() and not x.v[:-tail].any() and not x.master[:-tail].any()
+    u = x.grad[-tail:].double().cpu().numpy() / 65536.0
+    m, v = (1 - f32(0.9)) * u, (1 - f32(0.95)) * u * u
+    first = (n - tail) // 256  # its block's first elements are zero
+    of = (np.arange(n - tail, n) // 256) - first
+    M, V = (np.array([z[of == b].max() for b in range(of[-1] + 1)]) for z in (np.abs(m), v))
+    key = mix32((seed + 0x9E3779B9) & 0xFFFFFFFF)
+    i = np.arange(n - tail, n, dtype=np.uint64)
+    h = mix32((key + (i & 0xFFFFFFFF) + (i >> 32) * 0x85EBCA77) & 0xFFFFFFFF)
+    for got, y, p, top, r in ((x.m, np.abs(m) * 127.0 ** 2 / M[of], 2, 127, (h & 0xFFFF) / 65536.0),
+                              (x.v, v * 255.0 ** 4 / V[of], 4, 255, (h >> 16) / 65536.0)):
+        def code(y):
+            c = np.minimum(np.floor(y ** (1.0 / p) + 1e-12), top)
+            c = np.where(c ** p > y, c - 1, c)
+            return np.where((c < top) & (r * ((c + 1) ** p - c ** p) < y - c ** p), c + 1, c)
+
+        lo, hi = code(y * (1 - 2.0 ** -20)), code(y * (1 + 2.0 ** -20))
+        if p == 4:
+            lo, hi = np.maximum(lo, 1), np.maximum(hi, 1)
+        mag = np.abs(got[-tail:].double().cpu().numpy())
+        assert ((mag >= lo) & (mag <= hi)).all()
+
+
 def test_another_stream(cuda_lib):
     tensors = [Tensor(5000, 8, seed=1), Tensor(5000, 32, seed=2)]
     st = Step(cuda_lib, tensors, max_norm=1e-3)

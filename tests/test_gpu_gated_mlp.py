@@ -117,6 +117,64 @@ def test_the_step_writes_what_a_cast_would(cuda_lib):
     assert opt.growth_tracker.item() == 3
 
 
+def test_changed_weights_are_cast_again(cuda_lib):
+    from fp8_mixed_precision_reduce_gb300.gated_mlp import FP8GatedMLP
+
+    mlp = FP8GatedMLP(64, 96)
+    x = torch.randn((32, 64), device="cuda")
+    with torch.no_grad():
+        y = mlp(x)
+        first = mlp.weight_copies()
+        assert mlp.weight_copies()[0] is first[0]  # cast once
+        mlp.down.mul_(-1)
+        assert torch.equal(mlp(x), -y)
+
+
+def test_a_stale_backward_pass_fails(cuda_lib):
+    from fp8_mixed_precision_reduce_gb300.adamw import AdamW
+    from fp8_mixed_precision_reduce_gb300.gated_mlp import FP8GatedMLP
+
+    mlp = FP8GatedMLP(64, 96)
+    opt = AdamW(mlp.parameters(), lr=1e-2, modules=[mlp])
+    y = mlp(torch.randn((32, 64), device="cuda"))
+    y.sum().backward(retain_graph=True)
+    opt.step()
+    with pytest.raises(RuntimeError):
+        y.sum().backward()
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_saved_state_continues_the_run(cuda_lib, bits):
+    from fp8_mixed_precision_reduce_gb300.adamw import AdamW
+
+    torch.manual_seed(4)
+    start = torch.randn((96, 64), device="cuda")
+    grads = [torch.randn((96, 64), device="cuda") for _ in range(4)]
+
+    def make():
+        p = torch.nn.Parameter(start.clone())
+        return p, AdamW([p], lr=1e-2, state_bits=bits, loss_scale=1.0)
+
+    def steps(p, opt, gs):
+        for g in gs:
+            p.grad = g.clone()
+            opt.step()
+
+    p, opt = make()
+    steps(p, opt, grads)
+    q, other = make()
+    steps(q, other, grads[:2])
+    saved, weights = other.state_dict(), q.detach().clone()
+    r, third = make()
+    with torch.no_grad():
+        r.copy_(weights)
+    third.load_state_dict(saved)
+    steps(r, third, grads[2:])
+    assert torch.equal(p, r)
+    with pytest.raises(ValueError):
+        AdamW([p, r], lr=1.0).load_state_dict(saved)
+
+
 def test_an_overflowing_step_is_skipped(cuda_lib):
     from fp8_mixed_precision_reduce_gb300.adamw import AdamW
     from fp8_mixed_precision_reduce_gb300.gated_mlp import FP8GatedMLP
