@@ -30,7 +30,8 @@ constexpr int kMaxNormBlocks = 4096;
 // Blocks per SM of a step's grid (4 are resident): shares small enough to even
 // out the tail, large enough to pay for their start. 243 M parameters, 32-bit
 // moments: 1079 us with 4, 1069 with 8, 1046 with 16, 999 with 32, 1079 with 64
-// (993 with 3 blocks resident, for their registers); 8-bit: 834, 737, 699, 750, 784.
+// (993 with 3 blocks resident, for their registers); 8-bit: 700 us with 4, 679
+// with 8, 669 with 16, 686 with 32.
 constexpr int kStepBlocksPerSm32 = 32, kStepBlocksPerSm8 = 16;
 
 // The workspace: the arrival counter, then the running sum over launches,
@@ -41,6 +42,19 @@ struct Workspace {
     double sum;
     float partial[kMaxNormBlocks];
 };
+
+// The tensor that chunk c belongs to: the last one with first[t] <= c (one without
+// chunks shares its `first` with the next). A walk over them instead loads a
+// constant for each: the norm and the step of 61 small tensors 9.4 us, 8.2 so.
+__device__ __forceinline__ int tensor_of(const int32_t *first, int count, int c) {
+    int t = 0, end = count;
+    while (end - t > 1) {
+        const int mid = (t + end) >> 1;
+        if (first[mid] <= c) t = mid;
+        else end = mid;
+    }
+    return t;
+}
 
 // ------------------------------------------------------------------- norm
 
@@ -87,7 +101,8 @@ __device__ __forceinline__ float block_sum(float v, float *red) {
 // block to arrive the blocks' sums in double and in block order, so the result
 // does not depend on which block that is. Inf and NaN need no test of their
 // own: either makes the sum Inf or NaN. So do squares that overflow fp32
-// (|g| > 1.8e19), which count as an overflow of the step too.
+// (|g| > 1.8e19), which count as an overflow of the step too. Bound by HBM: 243 M
+// bf16 gradients in 72.6 us, 0.99 of the copy rate.
 template <int CAP>
 __global__ void __launch_bounds__(kThreads)
 grad_norm_kernel(const __grid_constant__ NormBatch<CAP> batch, Workspace *ws, float *norm, int32_t *found_inf,
@@ -97,50 +112,55 @@ grad_norm_kernel(const __grid_constant__ NormBatch<CAP> batch, Workspace *ws, fl
     __shared__ float red[kThreads / 32];
     __shared__ int last;
     float acc = 0.0f;
-    int t = 0;
+    int t = -1;
     const int chunks = batch.first[batch.count];
     for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
-        while (c >= batch.first[t + 1]) ++t;
+        if (t < 0 || c >= batch.first[t + 1]) t = tensor_of(batch.first, batch.count, c);
         const NormTensor &T = batch.t[t];
         const int64_t base = static_cast<int64_t>(c - batch.first[t]) * kNormChunk;
         const int64_t left = T.n - base;
+        const int n = left < kNormChunk ? static_cast<int>(left) : kNormChunk;
+        // whole vectors of 16 bytes, all loaded before the first is used, then the
+        // few elements after a tensor's last
         if (T.bf16) {
             const uint16_t *g = static_cast<const uint16_t *>(T.grad) + base;
-            if (left >= kNormChunk) {
-                uint4 d[4];
+            uint4 d[4];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) d[u] = __ldcs(reinterpret_cast<const uint4 *>(g) + u * kThreads + threadIdx.x);
+            for (int u = 0; u < 4; ++u) {
+                const int i = u * kThreads + threadIdx.x;
+                d[u] = 8 * i + 8 <= n ? __ldcs(reinterpret_cast<const uint4 *>(g) + i) : make_uint4(0u, 0u, 0u, 0u);
+            }
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    float f[8];
-                    unpack_bf16(d[u], f);
-                    acc = __fadd_rn(acc, sum_squares(f));
-                }
-            } else {
-                for (int64_t i = threadIdx.x; i < left; i += kThreads) {
-                    const float f = bf16_bits_to_f32(g[i]);
-                    acc = __fmaf_rn(f, f, acc);
-                }
+            for (int u = 0; u < 4; ++u) {
+                float f[8];
+                unpack_bf16(d[u], f);
+                acc = __fadd_rn(acc, sum_squares(f));
+            }
+            const int rest = (n & ~7) + threadIdx.x;
+            if (rest < n) {
+                const float f = bf16_bits_to_f32(g[rest]);
+                acc = __fmaf_rn(f, f, acc);
             }
         } else {
             const float *g = static_cast<const float *>(T.grad) + base;
-            if (left >= kNormChunk) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float4 d[4];
+            for (int h = 0; h < 2; ++h) {
+                float4 d[4];
 #pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        d[u] = __ldcs(reinterpret_cast<const float4 *>(g) + (4 * h + u) * kThreads + threadIdx.x);
-#pragma unroll
-                    for (int u = 0; u < 4; u += 2) {
-                        const float f[8] = {d[u].x,     d[u].y,     d[u].z,     d[u].w,
-                                            d[u + 1].x, d[u + 1].y, d[u + 1].z, d[u + 1].w};
-                        acc = __fadd_rn(acc, sum_squares(f));
-                    }
+                for (int u = 0; u < 4; ++u) {
+                    const int i = (4 * h + u) * kThreads + threadIdx.x;
+                    d[u] = 4 * i + 4 <= n ? __ldcs(reinterpret_cast<const float4 *>(g) + i)
+                                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 }
-            } else {
-                for (int64_t i = threadIdx.x; i < left; i += kThreads) acc = __fmaf_rn(g[i], g[i], acc);
+#pragma unroll
+                for (int u = 0; u < 4; u += 2) {
+                    const float f[8] = {d[u].x,     d[u].y,     d[u].z,     d[u].w,
+                                        d[u + 1].x, d[u + 1].y, d[u + 1].z, d[u + 1].w};
+                    acc = __fadd_rn(acc, sum_squares(f));
+                }
             }
+            const int rest = (n & ~3) + threadIdx.x;
+            if (rest < n) acc = __fmaf_rn(g[rest], g[rest], acc);
         }
     }
     const float s = block_sum(acc, red);
@@ -422,10 +442,11 @@ __device__ __forceinline__ void store_copy(const StepTensor &T, int64_t at, int 
 
 // A whole unit with 8-bit moments. Per parameter it moves 15 bytes, which
 // leaves about 80 instructions at the memory's rate, and as many are needed: the
-// step is bound by their issue (78 per parameter at 2.5-2.9 per cycle: 243 M
-// parameters in 699 us, 0.77 of the copy rate; feeding the warps by asynchronous
-// copies, a unit ahead per thread or by a warp of its own with bulk copies,
-// raised the issue rate to 2.9 but cost as many instructions: 718-731 us). So the
+// step is bound by their issue (about 78 per parameter at 2.85 per cycle and SM:
+// 243 M parameters in 669 us, 0.81 of the copy rate). The loads are plain ones,
+// from L2 where the Ahead below has brought their lines (700 us without it).
+// Asynchronous copies into shared memory, a unit ahead per thread or by a warp
+// of its own, cost as many instructions as they gained: 718-731 us. So the
 // arithmetic is done
 // two lanes at a time where it can be, and the codes are made without
 // conversions:
@@ -608,12 +629,47 @@ __device__ __forceinline__ void unit_8_bits(const StepTensor &T, int64_t at, int
     store_bytes(static_cast<uint8_t *>(T.v) + at, 8, make_uint2(wv[0], wv[1]));
 }
 
+// Brings a warp's next unit of a tensor from DRAM to L2 while it computes this
+// one: 22 lanes ask for one 128-byte line each of gradients (lanes 0-3, or 0-7 in
+// fp32), weights (8-15), codes of m (16, 17), of v (18, 19) and the two scales.
+// Each lane keeps its array and the step per element from tensor to tensor;
+// worked out again for each unit that cost what it gained (701 us). The last
+// chunk of a tensor, which may end inside a unit, is not asked for.
+struct Ahead {
+    const char *base;
+    int shift;  // log2 of the bytes per element; 6: one in 64, a scale; -1: none
+    __device__ __forceinline__ void start(const StepTensor &T, bool any) {
+        const int lane = threadIdx.x & 31;
+        shift = -1;
+        base = nullptr;
+        if (!any || !T.codes) return;  // (many small tensors: no unit to look ahead to)
+        if (lane < 8) {
+            shift = T.grad_bf16 ? (lane < 4 ? 1 : -1) : 2;
+            base = static_cast<const char *>(T.grad) + 128 * lane;
+        } else if (lane < 16) {
+            shift = 2;
+            base = reinterpret_cast<const char *>(T.w) + 128 * (lane - 8);
+        } else if (lane >= 20 && lane < 22) {
+            shift = 6;
+            base = reinterpret_cast<const char *>(lane == 20 ? T.sm : T.sv);
+        } else if (lane < 20) {
+            shift = 0;
+            base = static_cast<const char *>(lane < 18 ? T.m : T.v) + 128 * (lane & 1);
+        }
+    }
+    __device__ __forceinline__ void fetch(int64_t first) const {
+        if (shift >= 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(base + (shift == 6 ? first >> 6 : first << shift)));
+    }
+};
+
 // The kinds of a call's moments: all in fp32, all in 8 bits, or both. A call with
 // both runs in one launch too, each warp by its tensor's kind (61 small tensors
-// of both kinds: 9.4 us, 11.8 in a launch for each kind), a little slower for the
-// 8-bit ones (243 M parameters: 718 us, 707 in their own kernel). The warp's 256 elements of a unit are one block of the 8-bit
-// moments, so a block's largest moment is a warp reduction and nothing leaves
-// the warp.
+// of both kinds, walking to a chunk's tensor: 9.4 us, 11.8 in a launch for each
+// kind), a little slower for large ones (243 M parameters: 677 us with 8-bit moments, 669 in their own
+// kernel; 1069 with fp32 ones, 993). With fp32 moments alone the step is bound by
+// HBM: 993 us, 0.97 of the copy rate. The warp's 256 elements of a unit are one
+// block of the 8-bit moments, so a block's largest moment is a warp reduction and
+// nothing leaves the warp.
 enum Kind { kMoments32, kMoments8, kMomentsBoth };
 template <int KIND, int CAP>
 __global__ void __launch_bounds__(kThreads, KIND == kMoments32 ? 3 : 4)
@@ -629,6 +685,7 @@ adamw_kernel(const __grid_constant__ StepBatch<CAP> batch, const StepArgs a) {
         int t = -1;
         float am = 0.0f, shrink = 0.0f;
         uint32_t key = 0;
+        Ahead ahead;
         for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
             if (t < 0 || c >= batch.first[t + 1]) {
                 if (t >= 0 && batch.t[t].copy_amax != nullptr) {
@@ -636,10 +693,11 @@ adamw_kernel(const __grid_constant__ StepBatch<CAP> batch, const StepArgs a) {
                     if (lane == 0) atomicMax(reinterpret_cast<int *>(batch.t[t].copy_amax), __float_as_int(am));
                 }
                 am = 0.0f;
-                t = t < 0 ? 0 : t;
-                while (c >= batch.first[t + 1]) ++t;
+                t = tensor_of(batch.first, batch.count, c);
                 shrink = __fsub_rn(1.0f, __fmul_rn(s.lr, batch.t[t].decay));
                 key = mix32(seed + (batch.t[t].ordinal + 1u) * 0x9E3779B9u);
+                if constexpr (KIND != kMoments32)
+                    ahead.start(batch.t[t], c + static_cast<int>(gridDim.x) < batch.first[t + 1] - 1);
             }
             const StepTensor &T = batch.t[t];
             const int64_t unit = static_cast<int64_t>(c - batch.first[t]) * (kThreads / 32) + warp;
@@ -647,6 +705,8 @@ adamw_kernel(const __grid_constant__ StepBatch<CAP> batch, const StepArgs a) {
             if (unit * kUnit >= T.n) continue;  // the whole warp: past the tensor's end
             const bool codes = KIND == kMoments8 || (KIND == kMomentsBoth && T.codes);
             if (codes && unit * kUnit + kUnit <= T.n) {
+                if (c + static_cast<int>(gridDim.x) < batch.first[t + 1] - 1)
+                    ahead.fetch(unit * kUnit + static_cast<int64_t>(gridDim.x) * kChunk);
                 unit_8_bits(T, at, unit, s, shrink, key, am);
                 continue;
             }
@@ -750,7 +810,7 @@ adamw_kernel(const __grid_constant__ StepBatch<CAP> batch, const StepArgs a) {
 // Tensors of one launch: as many as its parameters (at most 32,764 bytes)
 // hold, or few where few are left, for a launch with more parameters costs more.
 constexpr int kNormCapLarge = 1000, kNormCapSmall = 64;
-constexpr int kStepCapLarge = 280, kStepCapSmall = 32;
+constexpr int kStepCapLarge = 280, kStepCapSmall = 64;
 static_assert(sizeof(NormBatch<kNormCapLarge>) + 64 <= 32764, "kernel parameters");
 static_assert(sizeof(StepBatch<kStepCapLarge>) + sizeof(StepArgs) <= 32764, "kernel parameters");
 

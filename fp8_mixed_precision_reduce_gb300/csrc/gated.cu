@@ -16,8 +16,8 @@
 //     pre-activations go out as bf16 only when the backward pass wants them.
 //   dgrad: 256 columns of dh; the epilogue takes the tile's g and u (bf16) from a
 //     ring that a warp of its own fills, and writes the E5M2 codes of dg and du.
-//     dh itself is never stored: against a GEMM that writes it in bf16 and a pass that reads it back
-//     that is 4 bytes per element less traffic.
+//     dh itself is never stored: against a GEMM that writes it in bf16 and a pass
+//     that reads it back that is 4 bytes per element less traffic.
 //
 // Both are bound by the tensor cores at training sizes (an epilogue of a few
 // dozen instructions per element hides behind a contraction of 4096), and by
@@ -46,14 +46,17 @@ enum Mode { FWD = 0, DGRAD = 1 };
 // registers, each lane a row, in whole 32-byte sectors; shared memory is left to
 // the operand ring, whose depth counts for more (16384 x 4096 -> 14336: 1085 us
 // with 7 stages for a pair; 1156 with 5 and staging boxes for TMA stores, 1217
-// with 4).
+// with 4). With a relaxed arrival on the accumulators' barrier it is 1055-1069 us,
+// 3.6 PFLOP/s; the plain GEMM of that size takes 1030-1056.
 //
 // Dgrad: the epilogue does more per element and waits for g and u, which come
 // from DRAM; a warp alone on its scheduler is too slow for that (371-386 us for
 // 8192 x 4096 x 14336, 279 for the GEMM alone), and so are loads by the lanes
 // themselves, 32 rows apart (410-480 us). So eight warps work, two to a quarter
 // of the rows, and one more feeds them chunks of 64 columns of g and u by TMA
-// through a ring of two.
+// through a ring of two: 306-355 us, by the power the board allows. The MMA warp
+// then waits for its operands 35 % of the time, as g, u and the codes (0.7 GB)
+// share their way; without that traffic the launch takes 268 us.
 template <bool PAIR, int MODE>
 struct Cfg {
     static constexpr int TILE_M = PAIR ? 256 : 128;

@@ -35,8 +35,8 @@
  *   FP8MP_ERR_DEVICE (-2): the current device is not an sm_103 GPU.
  *   FP8MP_ERR_LAUNCH (-3): a CUDA call or kernel launch failed.
  *   FP8MP_ERR_TIMEOUT (-4): returned by fp8mp_check(): a bounded wait inside
- *     a kernel ran out (a GEMM's wedged pipeline, the master step's grid
- *     barrier); that kernel's output is undefined, the CUDA context stays
+ *     a kernel ran out (a wedged pipeline of a GEMM, of the gated block or of
+ *     fp8_linear_few, the master step's grid barrier); that kernel's output is undefined, the CUDA context stays
  *     usable.
  *   fp8mp_last_error() then describes the failure (thread-local).
  * Launch. Kernels are launched with programmatic stream serialization: one
@@ -44,8 +44,9 @@
  *   waits for that kernel to complete before it touches global memory, so
  *   stream order holds as usual. Environment switches, read by the library:
  *   FP8MP_PDL=0 (once per process) launches plainly; FP8MP_GEMM_ENGINE=pair
- *   or single (per call) forces a GEMM tile engine; FP8MP_FUSED_MASTER=0
- *   (per call) runs the self-scanning master steps as three launches.
+ *   or single (per call) forces a tile engine of the GEMMs and of the gated
+ *   block's; FP8MP_FUSED_MASTER=0 (per call) runs the self-scanning master
+ *   steps as three launches.
  */
 #ifndef FP8MP_H
 #define FP8MP_H
@@ -772,7 +773,7 @@ int mp_grad_norm(const fp8mp_adamw_tensor *tensors, int32_t n_tensors, float *no
  * over 2^16, for element i of tensor t of the call, with
  *   mix(x): x ^= x >> 16; x *= 0x7FEB352D; x ^= x >> 15; x *= 0x846CA68B; x ^= x >> 16
  * in 32-bit arithmetic. A block whose M is below 2^-100 (V below 2^-90) is
- * stored as 0.
+ * stored as 0, and with 8-bit moments sqrt(v) is 0 for v below 2^-126.
  * tensors     HOST array, read during the call only; tensors with n == 0 count
  *             in t but are skipped.
  * found_inf   device int32 (mp_grad_norm's, or a backward launch's
@@ -790,9 +791,9 @@ int mp_adamw_step(const fp8mp_adamw_tensor *tensors, int32_t n_tensors, float *l
 
 /*
  * fp8mp_check -- synchronises `stream`, then reports and clears the device
- * flags a kernel sets when one of its bounded waits runs out (a GEMM's
- * mbarrier wait, the master step's grid barrier): FP8MP_ERR_TIMEOUT if one
- * was set, FP8MP_ERR_LAUNCH on a CUDA error, else 0.
+ * flags a kernel sets when one of its bounded waits runs out (an mbarrier
+ * wait of a GEMM, of the gated block or of fp8_linear_few, the master step's
+ * grid barrier): FP8MP_ERR_TIMEOUT if one was set, FP8MP_ERR_LAUNCH on a CUDA error, else 0.
  */
 int fp8mp_check(void *stream);
 
