@@ -665,11 +665,11 @@ struct Ahead {
 // The kinds of a call's moments: all in fp32, all in 8 bits, or both. A call with
 // both runs in one launch too, each warp by its tensor's kind (61 small tensors
 // of both kinds, walking to a chunk's tensor: 9.4 us, 11.8 in a launch for each
-// kind), a little slower for large ones (243 M parameters: 677 us with 8-bit moments, 669 in their own
-// kernel; 1069 with fp32 ones, 993). With fp32 moments alone the step is bound by
-// HBM: 993 us, 0.97 of the copy rate. The warp's 256 elements of a unit are one
-// block of the 8-bit moments, so a block's largest moment is a warp reduction and
-// nothing leaves the warp.
+// kind), a little slower for large ones (243 M parameters: 677 us with 8-bit
+// moments, 669 in their own kernel; 1069 with fp32 ones, 993). With fp32 moments
+// alone the step is bound by HBM: 993 us, 0.97 of the copy rate. The warp's 256
+// elements of a unit are one block of the 8-bit moments, so a block's largest
+// moment is a warp reduction and nothing leaves the warp.
 enum Kind { kMoments32, kMoments8, kMomentsBoth };
 template <int KIND, int CAP>
 __global__ void __launch_bounds__(kThreads, KIND == kMoments32 ? 3 : 4)

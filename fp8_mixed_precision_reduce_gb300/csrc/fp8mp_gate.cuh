@@ -51,10 +51,15 @@ __device__ __forceinline__ void gate_act_grad(uint64_t g, uint64_t &a, uint64_t 
     const uint64_t p = gate_logistic<ACT>(g);
     a = f2_mul(g, p);
     const uint64_t slope = f2_mul(a, f2_fma(p, f2_same(-1.0f), f2_same(1.0f)));
-    if constexpr (ACT == FP8MP_SILU)
+    if constexpr (ACT == FP8MP_SILU) {
         da = f2_add(slope, p);
-    else
-        da = f2_fma(slope, f2_fma(f2_mul(g, g), f2_same(3.0f * kGelu3), f2_same(kGelu1)), p);
+    } else {
+        // g^2 stays finite: where it would not, p is 0 or 1 and the slope 0
+        float s0, s1;
+        f2_split(f2_mul(g, g), s0, s1);
+        da = f2_fma(slope, f2_fma(f2_pack(fminf(s0, 0x1p60f), fminf(s1, 0x1p60f)), f2_same(3.0f * kGelu3),
+                                  f2_same(kGelu1)), p);
+    }
 }
 
 // dg = dh u act'(g) and du = dh act(g) of four elements, as E5M2 codes under

@@ -342,6 +342,24 @@ def test_backward_flags_a_nonfinite_weight_gradient(cuda_lib):
 
 
 @pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_backward_of_saturated_gates(cuda_lib, act, dtype):
+    """|g| up to bf16's largest: act' is 1 or 0 there, and g^2 has no place in
+    fp32. Everything is a power of two or saturates: no tolerance."""
+    g = torch.tensor([2.0 ** e for e in (14, 30, 60, 63, 64, 70, 100, 127)], device="cuda")
+    gu = torch.cat([g, -g, torch.full((16,), 0.5, device="cuda")]).to(torch.bfloat16).expand(5, 32).contiguous()
+    dh = torch.full((5, 16), 2.0 ** -6, dtype=dtype, device="cuda")
+    one = torch.ones(1, device="cuda")
+    dgu8, amax = torch.empty((5, 32), dtype=torch.uint8, device="cuda"), torch.zeros(1, device="cuda")
+    x8, w8 = (torch.zeros((n, 16), dtype=torch.uint8, device="cuda") for n in (5, 32))
+    cuda_lib.fp8_gated_bwd(dh, gu, x8, w8, one, one, one, one, dgu8, None, None, act=ACTS[act], dgu_amax=amax)
+    want = torch.zeros((5, 32), dtype=torch.float64, device="cuda")
+    want[:, :8] = 2.0 ** -7
+    want[:, 16:24] = (g.double() * 2.0 ** -6).clamp(max=57344.0)
+    assert torch.equal(wide(dgu8, E5M2), want) and amax.item() == 2.0 ** 121
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
 def test_gradient_against_differences(cuda_lib, act):
     """dg, du are the derivatives of the h that the forward pass returns, by
     central differences in 64 bits of the forward formula, at the gradient
