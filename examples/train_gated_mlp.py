@@ -1,7 +1,7 @@
 """Trains a residual FP8 gated feed-forward block with the many-tensor AdamW
 step and then serves it token by token.
 
-    python examples/train_gated_mlp.py [--features 512] [--hidden 1536] [--bits 8]
+    python examples/train_gated_mlp.py [--features 512] [--hidden 1408] [--bits 8]
 
 The block learns a fixed random block of the same form, x + MLP(norm(x)), from
 synthetic inputs. Per training step: forward and backward of the block under a
@@ -34,7 +34,7 @@ class Block(torch.nn.Module):
         return x + self.mlp((x * rms * self.norm).to(torch.bfloat16)).to(x.dtype)
 
 
-def run(features=512, hidden=1536, tokens=1000, steps=300, bits=8, lr=4e-3, log=print):
+def run(features=512, hidden=1408, tokens=1000, steps=300, bits=8, lr=4e-3, log=print):
     """Returns the losses, and the largest difference between a token served
     alone and the same token in a batch, relative to the batch's output."""
     torch.manual_seed(0)
@@ -69,7 +69,7 @@ def run(features=512, hidden=1536, tokens=1000, steps=300, bits=8, lr=4e-3, log=
 if __name__ == "__main__":
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--features", type=int, default=512)
-    ap.add_argument("--hidden", type=int, default=1536)
+    ap.add_argument("--hidden", type=int, default=1408)
     ap.add_argument("--tokens", type=int, default=1000)
     ap.add_argument("--steps", type=int, default=300)
     ap.add_argument("--bits", type=int, default=8, choices=(8, 32))
