@@ -310,6 +310,13 @@ def test_backward(cuda_lib, engine, M, F, K, act, dtype):
         assert dw2 is None or torch.equal(dw2, dw)
 
 
+@pytest.mark.parametrize("M,F,K", [(1237, 2736, 1040), (300, 8192, 528), (16, 4096, 16), (2000, 5504, 256)])
+def test_backward_of_few_long_tiles(cuda_lib, engine, M, F, K):
+    """dX has few tiles with contractions of 2F, dW many of M: each tile of dX has
+    SMs of its own, and each output equals its own launch's (in test_backward)."""
+    test_backward(cuda_lib, engine, M, F, K, "silu", torch.bfloat16)
+
+
 def test_backward_of_nothing(cuda_lib):
     u8, bf, one = torch.uint8, torch.bfloat16, torch.ones(1, device="cuda")
     e = lambda *s, dtype=u8: torch.ones(s, dtype=dtype, device="cuda")  # noqa: E731
