@@ -65,13 +65,14 @@ class AdamW:
         self.grad_norm = torch.zeros(1, device=dev)
         self.seed = torch.full((1,), seed, dtype=torch.int32, device=dev)
         self.workspace = torch.zeros(mp_adamw_workspace_bytes() // 4, dtype=torch.int32, device=dev)
-        self._plan, self._copies = None, None
+        self._plan, self._arrays = None, None
 
     def _tensors(self, grads) -> AdamWTensors:
-        """The step's tensors, rebuilt when a module has new copies."""
+        """The step's tensors, rebuilt when a weight or a module's copy is another array."""
         copies = {id(w): (c, m) for mod in self.modules for w, c, m in mod.copies_for_step()}
-        now = [(c.data_ptr(), m.scale.data_ptr()) for c, m in copies.values()]
-        if self._plan is not None and now == self._copies:
+        now = [p.data_ptr() for p in self.params]
+        now += [(c.data_ptr(), m.scale.data_ptr()) for c, m in copies.values()]
+        if self._plan is not None and now == self._arrays:
             self._plan.set_grads(grads)
             return self._plan
         plan = AdamWTensors()
@@ -79,7 +80,7 @@ class AdamW:
             c, m = copies.get(id(p), (None, None))
             scaled = dict(copy=c, copy_scale=m.scale, copy_amax=m.cur_amax) if c is not None else {}
             plan.add(g, p.detach(), weight_decay=decay, **s, **scaled)
-        self._plan, self._copies = plan, now
+        self._plan, self._arrays = plan, now
         return plan
 
     def step(self) -> None:

@@ -662,6 +662,30 @@ struct Ahead {
     }
 };
 
+// A skipped step: the copies of the weights as they are, since their scales may
+// have changed since the last ones.
+template <int CAP>
+__device__ __noinline__ void copies_alone(const StepBatch<CAP> &batch) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int chunks = batch.first[batch.count];
+    for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
+        const int t = tensor_of(batch.first, batch.count, c);
+        const StepTensor &T = batch.t[t];
+        const int64_t at = static_cast<int64_t>(c - batch.first[t]) * kChunk + warp * kUnit + 8 * lane;
+        const int64_t left = T.n - at;
+        const int cnt = left >= 8 ? 8 : (left > 0 ? static_cast<int>(left) : 0);
+        if (T.copy_kind == 0) continue;
+        float w[8], am = 0.0f;
+        load8(T.w + at, cnt, w);
+        store_copy(T, at, cnt, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) am = fmaxf(am, j < cnt ? fabsf(w[j]) : 0.0f);
+        am = warp_max(am);
+        if (lane == 0 && T.copy_amax != nullptr)
+            atomicMax(reinterpret_cast<int *>(T.copy_amax), __float_as_int(am));
+    }
+}
+
 // The kinds of a call's moments: all in fp32, all in 8 bits, or both. A call with
 // both runs in one launch too, each warp by its tensor's kind (61 small tensors
 // of both kinds, walking to a chunk's tensor: 9.4 us, 11.8 in a launch for each
@@ -779,6 +803,8 @@ adamw_kernel(const __grid_constant__ StepBatch<CAP> batch, const StepArgs a) {
             am = warp_max(am);
             if (lane == 0) atomicMax(reinterpret_cast<int *>(batch.t[t].copy_amax), __float_as_int(am));
         }
+    } else {
+        copies_alone(batch);
     }
     if (!a.finish) return;
     // the last block of the call's last launch: every element has read the

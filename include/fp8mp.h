@@ -750,8 +750,10 @@ int mp_grad_norm(const fp8mp_adamw_tensor *tensors, int32_t n_tensors, float *no
  * mp_adamw_step -- one AdamW step (Adam with decoupled weight decay) over many
  * tensors at once, under dynamic loss scaling ([MP], [PT-FP8] as
  * mp_master_step_adam), with the gradients' norm clipped and the weights'
- * next copy written. When *found_inf != 0: S = S * backoff, growth = 0 and
- * nothing else changes. Else, each operation rounded once to fp32:
+ * next copy written. When *found_inf != 0: S = S * backoff, growth = 0, the
+ * copies are written of the weights as they are (*copy_scale may have changed
+ * since the last ones), and nothing else changes. Else, each operation rounded
+ * once to fp32:
  *   k  = fl32(1 / S);  with grad_norm: c = max_norm / (*grad_norm * k + 1e-6),
  *        k = k * c if c < 1
  *   u  = fl32(grad) * k

@@ -354,18 +354,49 @@ def test_overflow_skips_the_step(cuda_lib, bits):
     st = Step(cuda_lib, tensors, S=1024.0, growth=9)
     st.measure()
     assert st.found.item() == 1
-    keep = [[z.clone() for z in (x.master, x.m, x.v, x.copy, x.amax)] for x in tensors]
+    keep = [[z.clone() for z in (x.master, x.m, x.v)] for x in tensors]
     pows, seed = st.pows.clone(), st.seed.clone()
     st.run()
     for x, old in zip(tensors, keep):
-        for a, b in zip((x.master, x.m, x.v, x.copy, x.amax), old):
+        for a, b in zip((x.master, x.m, x.v), old):
             assert torch.equal(a, b)
+        # the copy is of the weights as they are, under a scale that may be new
+        want = (x.master * x.scale).clamp(-448.0, 448.0).to(torch.float8_e4m3fn).view(torch.uint8)
+        assert torch.equal(x.copy, want) and x.amax.item() == x.master.abs().max().item()
     assert st.S.item() == 512.0 and st.growth.item() == 0
     assert torch.equal(st.pows, pows) and torch.equal(st.seed, seed)
     tensors[1].grad[1234] = 0.25
     st.measure()
     assert st.found.item() == 0
     st.check()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("copy", ["e4m3", "bf16", None])
+def test_copies_of_a_skipped_step(cuda_lib, bits, copy):
+    """More tensors than one launch takes, of odd sizes, some empty or without
+    a copy; nothing past a copy's end is written."""
+    sizes = [1, 7, 8, 2047, 2048, 2049, 0, 5000] * 40
+    tensors = [Tensor(n, bits, copy=copy if i % 3 else None, seed=i) for i, n in enumerate(sizes)]
+    spare = [x.copy for x in tensors]
+    for x in tensors:
+        if x.copy is not None:
+            x.room = torch.cat([x.copy, x.copy.new_full((16,), 5)])
+            x.copy = x.room[:x.n]
+    del spare
+    st = Step(cuda_lib, tensors, found=1)
+    masters = [x.master.clone() for x in tensors]
+    st.run()
+    for x, w in zip(tensors, masters):
+        assert torch.equal(x.master, w)
+        if x.copy is None:
+            continue
+        if x.copy_kind == "bf16":
+            want = w.to(torch.bfloat16)
+        else:
+            want = (w * x.scale).clamp(-448.0, 448.0).to(torch.float8_e4m3fn).view(torch.uint8)
+            assert x.n == 0 or x.amax.item() == w.abs().max().item()
+        assert torch.equal(x.copy, want) and (x.room[x.n:] == 5).all()
 
 
 def test_loss_scale_grows(cuda_lib):

@@ -190,6 +190,39 @@ def test_an_overflowing_step_is_skipped(cuda_lib):
     assert all(torch.equal(a, b) for a, b in zip(before, mlp.parameters()))
 
 
+def test_the_copies_after_a_skipped_step(cuda_lib):
+    """update_scales changes the scales and the step that follows is skipped: the
+    next forward pass is still the weights' own."""
+    from fp8_mixed_precision_reduce_gb300.adamw import AdamW
+    from fp8_mixed_precision_reduce_gb300.gated_mlp import FP8GatedMLP
+
+    mlp = FP8GatedMLP(64, 96)
+    opt = AdamW(mlp.parameters(), lr=1e-2, modules=[mlp])
+    x = torch.randn((32, 64), device="cuda")
+    (mlp(x).sum() * float("nan")).backward()  # (an infinite gradient saturates in its cast)
+    mlp.update_scales()
+    opt.step()
+    assert opt.found_inf.item() == 1
+    y = mlp(x)
+    mlp.weights_changed()
+    assert torch.equal(y, mlp(x)) and torch.isfinite(y).all()
+
+
+def test_a_replaced_weight_is_the_one_that_is_stepped(cuda_lib):
+    from fp8_mixed_precision_reduce_gb300.adamw import AdamW
+
+    p = torch.nn.Parameter(torch.ones(300, device="cuda"))
+    opt = AdamW([p], lr=0.5)
+    p.grad = torch.ones_like(p)
+    opt.step()
+    old = p.data
+    kept = old.clone()
+    p.data = torch.full((300,), 7.0, device="cuda")
+    p.grad = torch.ones_like(p)
+    opt.step()
+    assert torch.equal(old, kept) and (p < 7.0).all()
+
+
 def test_refusals(cuda_lib):
     from fp8_mixed_precision_reduce_gb300.adamw import AdamW
     from fp8_mixed_precision_reduce_gb300.gated_mlp import FP8GatedMLP
