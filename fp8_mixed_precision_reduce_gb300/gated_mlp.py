@@ -148,7 +148,8 @@ class FP8GatedMLP(torch.nn.Module):
         self._cast_of = self._weight_versions()
 
     def _weight_versions(self):
-        return self.gate_up._version, self.down._version
+        # (another array under the same parameter, .data = ..., keeps the version)
+        return self.gate_up._version, self.gate_up.data_ptr(), self.down._version, self.down.data_ptr()
 
     def weights_changed(self) -> None:
         """Cast the weights again before their next use (for changes that torch

@@ -208,6 +208,35 @@ def test_the_copies_after_a_skipped_step(cuda_lib):
     assert torch.equal(y, mlp(x)) and torch.isfinite(y).all()
 
 
+def test_replaced_weights_are_cast_again(cuda_lib):
+    from fp8_mixed_precision_reduce_gb300.gated_mlp import FP8GatedMLP
+
+    mlp = FP8GatedMLP(64, 96)
+    x = torch.randn((5, 64), device="cuda")
+    with torch.no_grad():
+        y = mlp(x)
+        for w in (mlp.gate_up, mlp.down):
+            old = w.data
+            w.data = -old
+            z = mlp(x)
+            w.data = old
+            assert not torch.equal(z, y) and torch.equal(mlp(x), y)
+
+
+@pytest.mark.parametrize("shape", [(0, 64), (2, 0, 64), (1, 64), (2, 3, 64), (70, 64)])
+def test_any_number_of_tokens(cuda_lib, shape):
+    from fp8_mixed_precision_reduce_gb300.gated_mlp import FP8GatedMLP
+
+    mlp = FP8GatedMLP(64, 96)
+    x = torch.randn(shape, device="cuda", requires_grad=True)
+    y = mlp(x)
+    y.sum().backward()
+    assert y.shape == x.shape == x.grad.shape
+    assert torch.isfinite(mlp.gate_up.grad).all() and torch.isfinite(mlp.down.grad).all()
+    if x.numel() == 0:
+        assert (mlp.gate_up.grad == 0).all() and (mlp.down.grad == 0).all()
+
+
 def test_a_replaced_weight_is_the_one_that_is_stepped(cuda_lib):
     from fp8_mixed_precision_reduce_gb300.adamw import AdamW
 
