@@ -22,6 +22,7 @@
 // Both are bound by the tensor cores at training sizes (an epilogue of a few
 // dozen instructions per element hides behind a contraction of 4096), and by
 // their output traffic at short contractions.
+#include <algorithm>
 #include <atomic>
 #include <cstdlib>
 #include <cstring>
@@ -655,13 +656,25 @@ int launch(const GatedParams &P, cudaStream_t s, const DeviceInfo &dev) {
     return FP8MP_OK;
 }
 
-// Pairs of SMs on 256-row tiles when there are enough of them to occupy most
-// SMs, as for the plain GEMM; FP8MP_GEMM_ENGINE=pair|single overrides it.
-bool use_pairs(int64_t pair_tiles, const DeviceInfo &dev) {
+// Pairs of SMs on 256-row tiles, or single SMs on 128-row tiles? By the rounds
+// of tiles that either takes and what a round costs, fitted to six layers from
+// 512 -> 16384 to 8192 -> 4096 with 65 to 4096 tokens, in us. Forward: 0.285 per
+// k-block (at least 3.2, the epilogue) and 0.6 once for a pair, 0.36 (2.8) for a
+// single, whose operands are half as much again per product. (4096 -> 14336, 128
+// tokens: 27.9 with pairs, 25.0 with singles; 256: 28.4, 33.7; 2048 -> 5632, 384
+// tokens: 15.0, 10.6.) Dgrad, where a single has three stages only: two thirds.
+// (4096 x 14336, 128 tokens: 20.2, 24.3; 384: 31.7, 41.9.) The choice is within 5 %
+// of the better one nearly everywhere. FP8MP_GEMM_ENGINE=pair|single overrides it.
+bool use_pairs(Mode mode, int64_t rows, int64_t col_tiles, int64_t kc, const DeviceInfo &dev) {
     const char *force = std::getenv("FP8MP_GEMM_ENGINE");
     if (force != nullptr && std::strcmp(force, "pair") == 0) return true;
     if (force != nullptr && std::strcmp(force, "single") == 0) return false;
-    return pair_tiles * 2 >= dev.num_sms;
+    const int64_t pairs = dev.num_sms / 2, singles = dev.num_sms;
+    const double pair_rounds = static_cast<double>(((rows + 255) / 256 * col_tiles + pairs - 1) / pairs);
+    const double single_rounds = static_cast<double>(((rows + 127) / 128 * col_tiles + singles - 1) / singles);
+    if (mode == DGRAD) return pair_rounds <= 1.5 * single_rounds;
+    const double kb = static_cast<double>((kc + BK - 1) / BK);
+    return pair_rounds * std::max(0.285 * kb, 3.2) + 0.6 < single_rounds * std::max(0.36 * kb, 2.8);
 }
 
 // bf16 [outer x inner], rows `pitch` bytes apart, in boxes of 128 rows x 64.
@@ -706,7 +719,7 @@ int launch_gated_fwd(const uint8_t *x8, const uint8_t *w8, int64_t M, int64_t F,
     }
     if (M <= kFewTokens)
         return launch_few_gated(x8, w8, M, F, K, act, sinv_x, sinv_w, h_scale, h, h_amax, gu, s, dev);
-    const bool pair = use_pairs(((M + 255) / 256) * ((F + 127) / 128), dev);
+    const bool pair = use_pairs(FWD, M, (F + 127) / 128, K, dev);
     GatedParams P;
     std::memset(&P, 0, sizeof P);
     int rc = set_tiles(P, pair, M, F, K, 128, 2 * F);
@@ -735,7 +748,7 @@ int launch_gated_dgrad(const uint8_t *dy8, const uint8_t *wd8, const uint16_t *g
                        int act, int dy_fmt, const float *sinv_dy, const float *sinv_wd, const float *dgu_scale,
                        uint8_t *dgu8, float *dgu_amax, cudaStream_t s, const DeviceInfo &dev) {
     if (N == 0) return zero_bytes(dgu8, M * F * 2, s, dev);
-    const bool pair = use_pairs(((M + 255) / 256) * ((F + 255) / 256), dev);
+    const bool pair = use_pairs(DGRAD, M, (F + 255) / 256, N, dev);
     GatedParams P;
     std::memset(&P, 0, sizeof P);
     int rc = set_tiles(P, pair, M, F, N, 256, F);
