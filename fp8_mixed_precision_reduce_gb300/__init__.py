@@ -478,7 +478,7 @@ def fp8_gated_fwd(x8: torch.Tensor, w8: torch.Tensor, sinv_x: torch.Tensor, sinv
                                 _ptr(h_amax), _ptr(gu), _stream(stream)))
 
 
-FEW_TOKENS = 64  # FP8MP_FEW_TOKENS: most tokens of fp8_linear_few
+FEW_TOKENS = 128  # FP8MP_FEW_TOKENS: most tokens of fp8_linear_few
 
 
 def fp8_linear_few(x8: torch.Tensor, w8: torch.Tensor, sinv_x: torch.Tensor, sinv_w: torch.Tensor, y: torch.Tensor,

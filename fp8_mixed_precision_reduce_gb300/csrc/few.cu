@@ -1,15 +1,16 @@
-// few.cu -- products of FP8 weights with a few tokens (1 to 64): the gated
-// feed-forward block's first half, h = act(x Wg^T) (x Wu^T), and a plain linear,
-// y = x W^T (+ b), as a model that serves runs them token by token.
+// few.cu -- products of FP8 weights with a few tokens: the gated feed-forward
+// block's first half, h = act(x Wg^T) (x Wu^T), for 1 to 64, and a plain linear,
+// y = x W^T (+ b), for 1 to 128, as a model that serves runs them token by token.
 //
-// Every weight byte is read once and used for at most 64 products, so the
+// Every weight byte is read once and used for at most 128 products, so the
 // kernel is bound by HBM. It is shaped to keep many weight loads in flight on
 // all SMs rather than to keep the tensor cores busy:
 //   - the weights are the MMA's M operand (128 rows per tile; gated: 64 gate
 //     rows and the 64 up rows of the same outputs), the tokens its N operand
-//     (16, 32 or 64 columns, rows past the last token zero-filled), so a stage
-//     is 16 KB of weights and 2-8 KB of tokens, in a ring of about 100 KB: two
-//     CTAs share an SM and one streams while the other starts or ends;
+//     (16 to 128 columns, rows past the last token zero-filled), so a stage
+//     is 16 KB of weights and 2-16 KB of tokens, in a ring of about 100 KB: two
+//     CTAs share an SM and one streams while the other starts or ends (128
+//     columns, whose sums alone take 64 KB, have an SM for each CTA);
 //   - a tile's contraction is split over the S CTAs of a cluster (split_for
 //     below). Each owns an S-th of the tile's outputs; all send it their fp32
 //     partial sums of those through distributed shared memory, and after one
@@ -18,8 +19,8 @@
 //     peers' sums instead takes a second barrier, about 1 us, and 16-byte reads
 //     from 32 rows at once, 2-3 us for 33 tokens.)
 // One token through 4096 -> 2 x 14336: 21.2 us (17.3 at the copy rate), through
-// 14336 -> 4096: 12.9 (8.7); 65536 x 14336: 137 us, the copy rate. What is left is
-// the start, about 2 us to the first bytes, and the end.
+// 14336 -> 4096: 12.9 (8.7), 128 tokens 15.6; 65536 x 14336: 137 us, the copy rate.
+// What is left is the start, about 2 us to the first bytes, and the end.
 #include <atomic>
 #include <cstring>
 #include <mutex>
@@ -41,14 +42,15 @@ template <int NT>
 struct Cfg {
     static constexpr int STAGE_BYTES = W_ROWS * BK + NT * BK;
     static constexpr int RECV_BYTES = W_ROWS * NT * 4;  // partial sums from all ranks for this CTA's outputs
-    static constexpr int STAGES = (112 * 1024 - RECV_BYTES) / STAGE_BYTES;
+    static constexpr int CTAS = NT <= 64 ? 2 : 1;  // per SM
+    static constexpr int STAGES = ((CTAS == 2 ? 112 : 224) * 1024 - RECV_BYTES) / STAGE_BYTES;
     static constexpr int RECV_OFFSET = STAGES * STAGE_BYTES;
     static constexpr int BAR_OFFSET = RECV_OFFSET + RECV_BYTES;
     static constexpr int SLOT_OFFSET = BAR_OFFSET + (2 * STAGES + 2) * 8;
     static constexpr int FLAG_OFFSET = SLOT_OFFSET + 8;
     static constexpr int SMEM_ALLOC = FLAG_OFFSET + 8 + 1024;
     static constexpr uint32_t TMEM_COLS = NT < 32 ? 32 : NT;
-    static_assert(2 * (SMEM_ALLOC + 1024) <= 233472, "two CTAs per SM");
+    static_assert(CTAS * (SMEM_ALLOC + 1024) <= 233472, "an SM's shared memory");
 };
 
 struct FewParams {
@@ -89,7 +91,7 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 
 // GATED: ACT is the activation; otherwise unused.
 template <bool GATED, int ACT, int NT>
-__global__ void __launch_bounds__(NUM_THREADS, 2) few_kernel(const __grid_constant__ FewParams P, uint32_t splits) {
+__global__ void __launch_bounds__(NUM_THREADS, Cfg<NT>::CTAS) few_kernel(const __grid_constant__ FewParams P, uint32_t splits) {
     using C = Cfg<NT>;
     extern __shared__ uint8_t smem_raw[];
     uint32_t base = smem_u32(smem_raw);
@@ -298,19 +300,22 @@ __global__ void __launch_bounds__(NUM_THREADS, 2) few_kernel(const __grid_consta
     if (P.out_amax != nullptr) block_amax_atomic(am, P.out_amax);
 }
 
-// How many CTAs share a tile's contraction. The grid runs two CTAs to an SM;
-// each costs its share of k-blocks and, for starting, filling its ring and
-// joining, about as long as `kFixed` k-blocks of streaming take it. The split
-// with the least (waves of CTAs) x (cost of one) is taken: more CTAs even out
-// the last wave of a few tiles, fewer save fixed costs when there are many.
+// How many CTAs share a tile's contraction. Each costs its share of k-blocks and,
+// for starting, filling its ring and joining, about as long as `kFixed` k-blocks of
+// streaming take it. The split with the least (waves of clusters) x (cost of one
+// CTA) is taken: more CTAs even out the last wave of a few tiles, fewer save fixed
+// costs when there are many. `fit`: the clusters of 1, 2, 4 and 8 CTAs that the
+// device holds at once: at one CTA per SM fewer of 8 than SMs / 8, as not every
+// group of SMs is a multiple of 8 (16 tiles of 44 k-blocks, 65 tokens: 6.9 us in
+// 16 clusters of 4, 11.0 in 16 of 8, of which 15 fit).
 constexpr int kFixed = 8;
 
-int split_for(int64_t tiles, int num_kb, int num_sms) {
+int split_for(int64_t tiles, int num_kb, const std::atomic<int> (&fit)[4]) {
     int best = 1;
     double least = 0.0;
-    for (int s = 1; s <= static_cast<int>(kMaxSplits) && s <= num_kb; s *= 2) {
-        const int64_t slots = 2 * static_cast<int64_t>(num_sms);
-        const int64_t waves = (tiles * s + slots - 1) / slots;
+    for (int i = 0, s = 1; s <= static_cast<int>(kMaxSplits) && s <= num_kb; ++i, s *= 2) {
+        const int64_t at_once = fit[i].load(std::memory_order_relaxed);
+        const int64_t waves = (tiles + at_once - 1) / at_once;
         const double cost = static_cast<double>(waves) * ((num_kb + s - 1) / s + kFixed);
         if (s == 1 || cost < least) {
             least = cost;
@@ -322,32 +327,61 @@ int split_for(int64_t tiles, int num_kb, int num_sms) {
 
 std::mutex g_prepare_mutex;
 
+// Per device: the kernel's shared memory is set, and how many clusters fit.
+struct Prepared {
+    std::atomic<bool> ready;
+    std::atomic<int> fit[4];
+};
+
 template <bool GATED, int ACT, int NT>
-int launch(const FewParams &P, int64_t tiles, int splits, cudaStream_t s, const DeviceInfo &dev) {
-    static std::atomic<bool> ready[64];
-    std::atomic<bool> &mine = ready[dev.device & 63];
-    if (!mine.load(std::memory_order_acquire)) {
+int launch(const FewParams &P, int64_t tiles, cudaStream_t s, const DeviceInfo &dev) {
+    using C = Cfg<NT>;
+    static Prepared prepared[64];
+    Prepared &mine = prepared[dev.device & 63];
+    const auto kernel = few_kernel<GATED, ACT, NT>;
+    if (!mine.ready.load(std::memory_order_acquire)) {
         std::lock_guard<std::mutex> lock(g_prepare_mutex);
-        const cudaError_t e = cudaFuncSetAttribute(few_kernel<GATED, ACT, NT>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<NT>::SMEM_ALLOC);
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_ALLOC);
         if (e != cudaSuccess) return fail(FP8MP_ERR_LAUNCH, "few: smem attribute failed: %s", cudaGetErrorString(e));
-        mine.store(true, std::memory_order_release);
+        for (int i = 0; i < 4; ++i) {
+            int fit = C::CTAS * dev.num_sms >> i;
+            if (C::CTAS == 1 && i > 0) {
+                cudaLaunchConfig_t cfg = {};
+                cudaLaunchAttribute attr[1];
+                cfg.gridDim = dim3(static_cast<unsigned>(C::CTAS * dev.num_sms >> i << i));
+                cfg.blockDim = dim3(NUM_THREADS);
+                cfg.dynamicSmemBytes = C::SMEM_ALLOC;
+                attr[0].id = cudaLaunchAttributeClusterDimension;
+                attr[0].val.clusterDim.x = 1u << i;
+                attr[0].val.clusterDim.y = 1;
+                attr[0].val.clusterDim.z = 1;
+                cfg.attrs = attr;
+                cfg.numAttrs = 1;
+                int got = 0;
+                if (cudaOccupancyMaxActiveClusters(&got, kernel, &cfg) == cudaSuccess && got >= 1) fit = got;
+            }
+            mine.fit[i].store(fit, std::memory_order_relaxed);
+        }
+        mine.ready.store(true, std::memory_order_release);
     }
-    const cudaError_t e = launch_kernel_cluster(few_kernel<GATED, ACT, NT>, dim3(static_cast<unsigned>(tiles * splits)),
-                                                dim3(NUM_THREADS), Cfg<NT>::SMEM_ALLOC, s,
-                                                static_cast<unsigned>(splits), P, static_cast<uint32_t>(splits));
+    const int splits = split_for(tiles, P.num_kb, mine.fit);
+    const cudaError_t e = launch_kernel_cluster(kernel, dim3(static_cast<unsigned>(tiles * splits)), dim3(NUM_THREADS),
+                                                C::SMEM_ALLOC, s, static_cast<unsigned>(splits), P,
+                                                static_cast<uint32_t>(splits));
     if (e != cudaSuccess) return fail(FP8MP_ERR_LAUNCH, "few: launch failed: %s", cudaGetErrorString(e));
     return FP8MP_OK;
 }
 
 template <bool GATED, int ACT>
-int launch_tokens(const FewParams &P, int nt, int64_t tiles, int splits, cudaStream_t s, const DeviceInfo &dev) {
-    if (nt == 16) return launch<GATED, ACT, 16>(P, tiles, splits, s, dev);
-    if (nt == 32) return launch<GATED, ACT, 32>(P, tiles, splits, s, dev);
-    return launch<GATED, ACT, 64>(P, tiles, splits, s, dev);
+int launch_tokens(const FewParams &P, int nt, int64_t tiles, cudaStream_t s, const DeviceInfo &dev) {
+    if (nt == 16) return launch<GATED, ACT, 16>(P, tiles, s, dev);
+    if (nt == 32) return launch<GATED, ACT, 32>(P, tiles, s, dev);
+    if constexpr (!GATED)
+        if (nt == 128) return launch<GATED, ACT, 128>(P, tiles, s, dev);
+    return launch<GATED, ACT, 64>(P, tiles, s, dev);
 }
 
-// The operands of rows <= kFewTokens tokens against `outs` outputs (gated: of
+// The operands of a few tokens against `outs` outputs (gated: of
 // w8's 2 * outs rows) over K.
 int set_operands(FewParams &P, const uint8_t *x8, const uint8_t *w8, int64_t M, int64_t outs, int64_t K, bool gated,
                  int nt) {
@@ -364,7 +398,7 @@ int set_operands(FewParams &P, const uint8_t *x8, const uint8_t *w8, int64_t M, 
     return rc;
 }
 
-int token_columns(int64_t M) { return M <= 16 ? 16 : (M <= 32 ? 32 : 64); }
+int token_columns(int64_t M) { return M <= 16 ? 16 : (M <= 32 ? 32 : (M <= 64 ? 64 : 128)); }
 
 }  // namespace
 
@@ -382,9 +416,8 @@ int launch_few_gated(const uint8_t *x8, const uint8_t *w8, int64_t M, int64_t F,
     P.gu = gu;
     P.out_amax = h_amax;
     const int64_t tiles = (F + 63) / 64;
-    const int splits = split_for(tiles, P.num_kb, dev.num_sms);
-    return act == FP8MP_SILU ? launch_tokens<true, FP8MP_SILU>(P, nt, tiles, splits, s, dev)
-                             : launch_tokens<true, FP8MP_GELU_TANH>(P, nt, tiles, splits, s, dev);
+    return act == FP8MP_SILU ? launch_tokens<true, FP8MP_SILU>(P, nt, tiles, s, dev)
+                             : launch_tokens<true, FP8MP_GELU_TANH>(P, nt, tiles, s, dev);
 }
 
 int launch_few_linear(const uint8_t *x8, const uint8_t *w8, int64_t M, int64_t N, int64_t K, const float *sinv_x,
@@ -402,7 +435,7 @@ int launch_few_linear(const uint8_t *x8, const uint8_t *w8, int64_t M, int64_t N
     P.bias_bf16 = bias_dtype == FP8MP_BF16;
     P.out_amax = y_amax;
     const int64_t tiles = (N + W_ROWS - 1) / W_ROWS;
-    return launch_tokens<false, FP8MP_SILU>(P, nt, tiles, split_for(tiles, P.num_kb, dev.num_sms), s, dev);
+    return launch_tokens<false, FP8MP_SILU>(P, nt, tiles, s, dev);
 }
 
 int read_and_clear_few_timeout_flag(unsigned int *value) {

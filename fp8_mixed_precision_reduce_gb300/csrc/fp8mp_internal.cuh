@@ -193,8 +193,11 @@ int launch_gated_dgrad(const uint8_t *dy8, const uint8_t *wd8, const uint16_t *g
 int launch_gate_bwd(const void *dh, int dh_dtype, const uint16_t *gu, int64_t M, int64_t F, int act,
                     const float *dgu_scale, uint8_t *dgu8, float *dgu_amax, cudaStream_t s, const DeviceInfo &dev);
 int read_and_clear_gated_timeout_flag(unsigned int *value);
-// Products with at most kFewTokens tokens (few.cu; sizes > 0, arguments validated).
-constexpr int64_t kFewTokens = 64;
+// Products with at most kFewTokens tokens (the gated block: kFewGatedTokens; few.cu;
+// sizes > 0, arguments validated). The gated block's own tiles are faster from 65
+// tokens on (4096 -> 14336, 128 tokens: 25 us, 38 here; 2048 -> 5632: 9.6, 10.1);
+// the GEMM's 256-column tiles are not (14336 -> 4096: 49 us, 15.6 here).
+constexpr int64_t kFewTokens = 128, kFewGatedTokens = 64;
 int launch_few_gated(const uint8_t *x8, const uint8_t *w8, int64_t M, int64_t F, int64_t K, int act,
                      const float *sinv_x, const float *sinv_w, const float *h_scale, void *h, float *h_amax,
                      uint16_t *gu, cudaStream_t s, const DeviceInfo &dev);

@@ -717,7 +717,7 @@ int launch_gated_fwd(const uint8_t *x8, const uint8_t *w8, int64_t M, int64_t F,
         const int rc = zero_bytes(h, M * F * h_size, s, dev);
         return rc || gu == nullptr ? rc : zero_bytes(gu, M * F * 4, s, dev);
     }
-    if (M <= kFewTokens)
+    if (M <= kFewGatedTokens)
         return launch_few_gated(x8, w8, M, F, K, act, sinv_x, sinv_w, h_scale, h, h_amax, gu, s, dev);
     const bool pair = use_pairs(FWD, M, (F + 127) / 128, K, dev);
     GatedParams P;

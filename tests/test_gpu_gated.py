@@ -210,6 +210,12 @@ def test_linear_few(cuda_lib, M, N, K, bias, y_dtype):
         assert torch.equal(y, again)
 
 
+@pytest.mark.parametrize("M", [65, 66, 80, 96, 127, 128])
+@pytest.mark.parametrize("N,K", [(16, 16), (4096, 5632), (2048, 5632), (272, 14336), (20016, 144), (6000, 1552)])
+def test_linear_few_of_more_tokens(cuda_lib, M, N, K):
+    test_linear_few(cuda_lib, M, N, K, torch.bfloat16, torch.bfloat16)
+
+
 def test_linear_few_equals_the_linear_where_both_run(cuda_lib):
     """Whole numbers whose sums are exact in fp32: the split changes nothing."""
     g = gen(8)

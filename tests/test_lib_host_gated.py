@@ -61,7 +61,7 @@ def test_backward(lib, kw, word):
 
 
 @pytest.mark.parametrize("kw,word", [
-    (dict(M=65), "outside 0..64"), (dict(M=-1), "outside"), (dict(N=24), "multiples of 16"), (dict(K=8), "multiples of 16"),
+    (dict(M=129), "outside 0..128"), (dict(M=-1), "outside"), (dict(N=24), "multiples of 16"), (dict(K=8), "multiples of 16"),
     (dict(N=1 << 31), "2^30"), (dict(y=None), "y is NULL"), (dict(y_dtype=4), "y_dtype"), (dict(bias=P, bias_dtype=4), "bias_dtype"),
     (dict(x8=P + 1), "aligned"), (dict(w8=None), "w8"), (dict(sx=None), "sinv_x"), (dict(amax=P + 1), "misaligned")])
 def test_linear_few(lib, kw, word):
