@@ -399,6 +399,44 @@ def test_copies_of_a_skipped_step(cuda_lib, bits, copy):
         assert torch.equal(x.copy, want) and (x.room[x.n:] == 5).all()
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("grad", [torch.bfloat16, torch.float32])
+def test_nothing_past_the_ends(cuda_lib, bits, grad):
+    """Every array between bytes that the step may not write, 16 bytes past a
+    32-byte boundary: the results are those of arrays of their own."""
+    sizes = [1, 7, 8, 9, 255, 256, 257, 2047, 2049, 5000, 40001]
+    rooms = []
+
+    def place(x):
+        n = x.numel() * x.element_size()
+        room = torch.full((n + 1024,), 0x5A, dtype=torch.uint8, device="cuda")
+        at = 256 + (16 - (room.data_ptr() + 256)) % 32
+        rooms.append((room, at, n))
+        y = room[at:at + n].view(x.dtype)
+        y.copy_(x)
+        return y
+
+    both = []
+    for guarded in (False, True):
+        tensors = [Tensor(n, bits, grad=grad, copy=("e4m3", "bf16")[i % 2], seed=i) for i, n in enumerate(sizes)]
+        for x in tensors if guarded else []:
+            for k in ("master", "grad", "m", "v", "sm", "sv", "copy"):
+                if getattr(x, k) is not None:
+                    setattr(x, k, place(getattr(x, k)))
+        st = Step(cuda_lib, tensors, max_norm=1.0)
+        st.measure()
+        st.run()
+        both.append((st, tensors))
+    (st, plain), (guarded_st, guarded) = both
+    assert torch.equal(st.norm, guarded_st.norm)
+    for x, y in zip(plain, guarded):
+        for k in ("master", "m", "v", "sm", "sv", "copy"):
+            if getattr(x, k) is not None:
+                assert torch.equal(getattr(x, k).view(torch.uint8), getattr(y, k).view(torch.uint8)), (x.n, k)
+    for room, at, n in rooms:
+        assert (room[:at] == 0x5A).all() and (room[at + n:] == 0x5A).all()
+
+
 def test_loss_scale_grows(cuda_lib):
     st = Step(cuda_lib, [Tensor(100)], S=8.0, growth=1, interval=3)
     st.check()

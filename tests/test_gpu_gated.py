@@ -433,6 +433,66 @@ def test_another_stream_and_a_graph(cuda_lib):
     assert torch.equal(out[0], out[1]) and torch.equal(out[0], out[2])
 
 
+class Odd:
+    """Arrays that start 16 bytes past a 32-byte boundary, with bytes around them
+    that no call may write."""
+
+    def __init__(self):
+        self.rooms = []
+
+    def empty(self, shape, dtype):
+        n = int(np.prod(shape)) * dtype.itemsize
+        room = torch.full((n + 1024,), 0x5A, dtype=torch.uint8, device="cuda")
+        at = 256 + (16 - (room.data_ptr() + 256)) % 32
+        self.rooms.append((room, at, n))
+        return room[at:at + n].view(dtype).view(shape)
+
+    def of(self, x):
+        y = self.empty(x.shape, x.dtype)
+        y.copy_(x)
+        return y
+
+    def check(self):
+        for room, at, n in self.rooms:
+            assert room[at:at + n].data_ptr() % 32 == 16
+            assert (room[:at] == 0x5A).all() and (room[at + n:] == 0x5A).all()
+
+
+@pytest.mark.parametrize("M,F,K", [(1, 32, 16), (33, 272, 144), (64, 1024, 256), (127, 528, 80), (300, 2064, 272)])
+def test_16_byte_alignment_and_nothing_past_the_ends(cuda_lib, engine, M, F, K):
+    """Bit for bit what the same calls give on aligned arrays."""
+    g = gen(M + F)
+    u8, bf = torch.uint8, torch.bfloat16
+    x8, sx = codes((M, K), 1.0, 64.0, E4M3, g)
+    w8, sw = codes((2 * F, K), 0.2, 400.0, E4M3, g)
+    dy8, sy = codes((M, K), 1e-3, 2.0 ** 20, E5M2, g)
+    wd8, sd = codes((K, F), 0.05, 1000.0, E4M3, g)
+    dh = torch.randn((M, F), generator=g, device="cuda").to(bf)
+    bias = torch.randn((F,), generator=g, device="cuda")
+    k = torch.tensor([30.0], device="cuda")
+    odd = Odd()
+    results = []
+    for place, empty in ((lambda x: x, lambda s, d: torch.empty(s, dtype=d, device="cuda")), (odd.of, odd.empty)):
+        x, w, dy, wd, d, b = (place(z) for z in (x8, w8, dy8, wd8, dh, bias))
+        h, hb, gu = empty((M, F), u8), empty((M, F), bf), empty((M, 2 * F), bf)
+        cuda_lib.fp8_gated_fwd(x, w, sx, sw, h, h_scale=k, gu=gu)
+        cuda_lib.fp8_gated_fwd(x, w, sx, sw, hb, act=1)
+        g1, g2 = empty((M, 2 * F), u8), empty((M, 2 * F), u8)
+        cuda_lib.fp8_gated_dgrad(dy, wd, gu, sy, sd, k, g1)
+        dx, dw = empty((M, K), bf), empty((2 * F, K), torch.float32)
+        cuda_lib.fp8_gated_bwd(d, gu, x, w, sx, sw, k, sx, g2, dx, dw)
+        got = [h, hb, gu, g1, g2, dx, dw]
+        if M <= 128:
+            for dtype in (bf, torch.float32):
+                got.append(empty((M, F), dtype))
+                cuda_lib.fp8_linear_few(x, w[:F], sx, sw, got[-1], bias=b)
+        results.append(got)
+    for a, b in zip(*results):
+        assert torch.equal(a.view(u8), b.view(u8))
+    odd.check()
+    assert cuda_lib.fp8mp_check() == 0
+
+
 @pytest.mark.slow
 def test_offsets_past_32_bits(cuda_lib):
     """gu of 4.4e9 elements (8.8 GB), h of 2.2e9: the last rows are right."""
