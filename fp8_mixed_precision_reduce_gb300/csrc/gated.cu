@@ -19,6 +19,12 @@
 //     dh itself is never stored: against a GEMM that writes it in bf16 and a pass
 //     that reads it back that is 4 bytes per element less traffic.
 //
+// Roundings: the sums are the MMA's fp32 accumulators (good to 1e-5 sum |a b|),
+// everything up to the output is fp32. h and the gradients' codes are FP8 because
+// the next GEMM reads FP8, g and u bf16 because they are the largest tensors that
+// training keeps. A few codes in a million are the neighbour of what exact sums
+// would give.
+//
 // Both are bound by the tensor cores at training sizes (an epilogue of a few
 // dozen instructions per element hides behind a contraction of 4096), and by
 // their output traffic at short contractions.
