@@ -503,9 +503,10 @@ __global__ void __launch_bounds__(Cfg<PAIR, MODE>::THREADS, 1) gated_kernel(cons
 // dg = dh u act'(g), du = dh act(g) from a stored dh, as E5M2 codes. Bound by
 // HBM: dh, g and u read (2 or 4 bytes and 4), the codes written (2). Pieces of 8
 // columns, so that every access of a warp is one contiguous run, and two pieces
-// per thread and step, both loaded before either is used: 8192 x 14336 in 145 us
-// from bf16, 0.95 of the copy rate (pieces of 16 columns, whose loads leave
-// gaps: 210 us; 8 or 16 blocks per SM: 150, 64: 147).
+// per thread and step, both loaded before either is used: 8192 x 14336 in 141 us
+// from bf16, 0.98 of the copy rate (pieces of 16 columns, whose loads leave
+// gaps: 210 us; 8 or 16 blocks per SM: 150, 64: 147; 64-bit divisions for a
+// thread's first place: 146).
 constexpr int kGateThreads = 256;
 constexpr int64_t kGateBlocksPerSm = 32;
 
@@ -547,9 +548,10 @@ gate_bwd_kernel(const void *dh, const uint16_t *gu, int64_t rows, int64_t cols, 
     // this thread's pieces are `stride` apart; its place advances without a division
     const int64_t per_row = cols >> 3;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * kGateThreads;
-    const int64_t step_rows = stride / per_row, step = stride - step_rows * per_row;
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * kGateThreads + threadIdx.x;
-    int64_t row = first / per_row, piece = first - row * per_row;
+    // (the grid's threads and a row's pieces both fit 32 bits)
+    const uint32_t first = blockIdx.x * kGateThreads + threadIdx.x, width = static_cast<uint32_t>(per_row);
+    const int64_t step_rows = static_cast<uint32_t>(stride) / width, step = stride - step_rows * per_row;
+    int64_t row = first / width, piece = first - static_cast<uint32_t>(row) * width;
     auto advance = [&] {
         row += step_rows;
         piece += step;
@@ -783,6 +785,9 @@ int launch_gated_dgrad(const uint8_t *dy8, const uint8_t *wd8, const uint16_t *g
 int launch_gate_bwd(const void *dh, int dh_dtype, const uint16_t *gu, int64_t M, int64_t F, int act,
                     const float *dgu_scale, uint8_t *dgu8, float *dgu_amax, cudaStream_t s, const DeviceInfo &dev) {
     int64_t blocks = (M * (F >> 3) + kGateThreads - 1) / kGateThreads;
+    // a thread starts slowly: two pieces each, once the SMs have their share (1237 x
+    // 2736 from bf16: 5.5 us, 6.0 with one; 100 x 2064: 2.1, 1.8)
+    if (blocks > 4 * dev.num_sms) blocks = (blocks + 1) / 2;
     if (blocks > dev.num_sms * kGateBlocksPerSm) blocks = dev.num_sms * kGateBlocksPerSm;
     const dim3 grid(static_cast<unsigned>(blocks)), block(kGateThreads);
     cudaError_t e;
