@@ -19,7 +19,7 @@
 //     peers' sums instead takes a second barrier, about 1 us, and 16-byte reads
 //     from 32 rows at once, 2-3 us for 33 tokens.)
 // One token through 4096 -> 2 x 14336: 21.2 us (17.3 at the copy rate), through
-// 14336 -> 4096: 12.9 (8.7), 128 tokens 15.6; 65536 x 14336: 137 us, the copy rate.
+// 14336 -> 4096: 12.6 (8.7), 128 tokens 15.6; 65536 x 14336: 137 us, the copy rate.
 // What is left is the start, about 2 us to the first bytes, and the end.
 #include <atomic>
 #include <cstring>
@@ -132,6 +132,24 @@ __global__ void __launch_bounds__(NUM_THREADS, Cfg<NT>::CTAS) few_kernel(const _
     if (splits > 1) cluster_arrive();  // this CTA has started: its peers may write to it
     pdl_wait();
 
+    // local rows (weight rows whose sums one CTA owns) of the tile: gated, the
+    // gate rows and then the up rows of its outputs
+    constexpr int TILE_OUTS = GATED ? 64 : W_ROWS;
+    const int mine = TILE_OUTS / static_cast<int>(splits);  // 8 .. 128, a power of two
+    const int local_rows = W_ROWS / static_cast<int>(splits);
+    const int64_t col0 = static_cast<int64_t>(tile) * TILE_OUTS + static_cast<int64_t>(rank) * mine;
+    // what the last step needs besides the sums is fetched now (33 tokens, 1552 ->
+    // 6000 with a bias: 6.5 us, 7.0 if at the end)
+    const float sinv_a = *P.sinv_a, sinv_b = *P.sinv_b;
+    const float h_scale = GATED && P.out_scale != nullptr ? *P.out_scale : 0.0f;
+    __shared__ float bias[GATED ? 1 : W_ROWS];
+    if constexpr (!GATED) {
+        const int o = static_cast<int>(threadIdx.x) - 64;
+        if (P.bias != nullptr && o >= 0 && o < mine && col0 + o < P.outs)
+            bias[o] = P.bias_bf16 ? bf16_bits_to_f32(static_cast<const uint16_t *>(P.bias)[col0 + o])
+                                  : static_cast<const float *>(P.bias)[col0 + o];
+    }
+
     // this CTA's share of the contraction (never empty: splits <= num_kb)
     const int kb0 = static_cast<int>(static_cast<int64_t>(P.num_kb) * rank / splits);
     const int kb1 = static_cast<int>(static_cast<int64_t>(P.num_kb) * (rank + 1) / splits);
@@ -198,11 +216,6 @@ __global__ void __launch_bounds__(NUM_THREADS, Cfg<NT>::CTAS) few_kernel(const _
     }
     __syncwarp();
     if (splits > 1) cluster_wait();
-    // local rows (weight rows whose sums one CTA owns) of the tile: gated, the
-    // gate rows and then the up rows of its outputs
-    constexpr int TILE_OUTS = GATED ? 64 : W_ROWS;
-    const int mine = TILE_OUTS / static_cast<int>(splits);  // 8 .. 128, a power of two
-    const int local_rows = W_ROWS / static_cast<int>(splits);
     if (warp >= 2 && !failed) {
         tc_fence_after();
         const int q = warp & 3, row = 32 * q + lane;
@@ -232,9 +245,8 @@ __global__ void __launch_bounds__(NUM_THREADS, Cfg<NT>::CTAS) few_kernel(const _
     if (splits > 1) cluster_wait();
 
     // this CTA's outputs, four at a time, all tokens
-    const float scale = __fmul_rn(*P.sinv_a, *P.sinv_b);
+    const float scale = __fmul_rn(sinv_a, sinv_b);
     const int quads = mine >> 2, shift = 31 - __clz(quads);
-    const float h_scale = GATED && P.out_scale != nullptr ? *P.out_scale : 0.0f;
     const float *recv = reinterpret_cast<const float *>(smem + C::RECV_OFFSET);
     auto joined = [&](int lr, int m, float(&s)[4]) {  // in rank order
         const float4 first = *reinterpret_cast<const float4 *>(recv + m * local_rows + lr);
@@ -248,7 +260,7 @@ __global__ void __launch_bounds__(NUM_THREADS, Cfg<NT>::CTAS) few_kernel(const _
     float am = 0.0f;
     for (int i = threadIdx.x; i < quads * P.rows; i += NUM_THREADS) {
         const int m = i >> shift, o = 4 * (i & (quads - 1));
-        const int64_t col = static_cast<int64_t>(tile) * TILE_OUTS + static_cast<int64_t>(rank) * mine + o;
+        const int64_t col = col0 + o;
         if (col >= P.outs) continue;  // (P.outs is a multiple of 16)
         const int64_t at = static_cast<int64_t>(m) * P.outs + col;
         float a[4], y[4];
@@ -281,10 +293,7 @@ __global__ void __launch_bounds__(NUM_THREADS, Cfg<NT>::CTAS) few_kernel(const _
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 y[j] = __fmul_rn(a[j], scale);
-                if (P.bias != nullptr)
-                    y[j] = __fmaf_rn(a[j], scale,
-                                     P.bias_bf16 ? bf16_bits_to_f32(static_cast<const uint16_t *>(P.bias)[col + j])
-                                                 : static_cast<const float *>(P.bias)[col + j]);
+                if (P.bias != nullptr) y[j] = __fmaf_rn(a[j], scale, bias[o + j]);
             }
             if (P.out_bf16) {
                 const uint32_t lo = pack_bf16x2(y[0], y[1]), hi = pack_bf16x2(y[2], y[3]);
