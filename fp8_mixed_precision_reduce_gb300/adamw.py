@@ -24,9 +24,10 @@ class AdamW:
     Parameters of two or more dimensions decay by ``weight_decay``, the others
     do not. ``state_bits`` 8 holds the moments of parameters of at least
     ``min_8bit_size`` elements in 8 bits, the others' in 32. ``modules``: those
-    with ``copies_for_step()`` (FP8GatedMLP) get their weights' E4M3 copies
-    written by the step, under the scales of their metas: call update_scales()
-    before step().
+    with ``copies_for_step()`` (FP8GatedMLP) get the E4M3 copies of those of
+    their weights that are among ``params`` written by the step, under the
+    scales of their metas: call update_scales() before step(). (Of a weight that
+    several modules hold, the first one's copy; the others cast theirs.)
     """
 
     _SCALARS = ("loss_scale", "growth_tracker", "beta_pows", "seed")
@@ -67,9 +68,18 @@ class AdamW:
         self.workspace = torch.zeros(mp_adamw_workspace_bytes() // 4, dtype=torch.int32, device=dev)
         self._plan, self._arrays = None, None
 
-    def _tensors(self, grads) -> AdamWTensors:
+    def _copies(self):
+        """What the step writes of the modules' copies: {id(weight): (copy, meta)},
+        and each module's weights among them."""
+        mine, copies, written = {id(p) for p in self.params}, {}, []
+        for mod in self.modules:
+            of = [x for x in mod.copies_for_step() if id(x[0]) in mine and id(x[0]) not in copies]
+            copies.update((id(w), (c, m)) for w, c, m in of)
+            written.append((mod, [w for w, _, _ in of]))
+        return copies, written
+
+    def _tensors(self, grads, copies) -> AdamWTensors:
         """The step's tensors, rebuilt when a weight or a module's copy is another array."""
-        copies = {id(w): (c, m) for mod in self.modules for w, c, m in mod.copies_for_step()}
         now = [p.data_ptr() for p in self.params]
         now += [(c.data_ptr(), m.scale.data_ptr()) for c, m in copies.values()]
         if self._plan is not None and now == self._arrays:
@@ -90,7 +100,8 @@ class AdamW:
             if p.grad is None:
                 raise ValueError(f"parameter {i} has no gradient")
             grads.append(p.grad if p.grad.is_contiguous() else p.grad.contiguous())
-        plan = self._tensors(grads)
+        copies, written = self._copies()
+        plan = self._tensors(grads, copies)
         mp_grad_norm(plan, self.grad_norm, self.found_inf, self.workspace)
         mp_adamw_step(plan, self.loss_scale, self.growth_tracker, self.found_inf, self.beta_pows, self.workspace,
                       lr=self.lr, beta1=self.betas[0], beta2=self.betas[1], eps=self.eps, seed=self.seed,
@@ -98,8 +109,8 @@ class AdamW:
                       growth_interval=self.growth_interval)
         for p in self.params:
             torch.autograd.graph.increment_version(p)
-        for m in self.modules:
-            m.copies_written()
+        for mod, weights in written:
+            mod.copies_written(weights)
 
     def state_dict(self) -> dict:
         """Everything but the parameters that the next step depends on."""

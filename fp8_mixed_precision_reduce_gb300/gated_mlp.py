@@ -30,6 +30,11 @@ def _rows16(rows: int, cols: int, dtype: torch.dtype, device) -> torch.Tensor:
     return t
 
 
+def _version(w: torch.Tensor):
+    # (another array under the same parameter, .data = ..., keeps the version)
+    return w._version, w.data_ptr()
+
+
 class _FP8GatedMLPFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, gate_up, down, mlp, keep):
@@ -117,44 +122,45 @@ class FP8GatedMLP(torch.nn.Module):
         self.meta_dy, self.meta_dgu = Meta(history_len, E5M2, device), Meta(history_len, E5M2, device)
         # 1 once a weight gradient held an Inf or NaN
         self.dw_nonfinite = torch.zeros(1, dtype=torch.int32, device=device)
-        self._gate_up8 = torch.empty((2 * hidden, features), dtype=torch.uint8, device=device)
-        self._down8 = torch.empty((features, hidden), dtype=torch.uint8, device=device)
-        self._cast_of = None  # versions of the weights that the copies are of
+        # of gate_up and of down: the E4M3 copy, and the version of the weight that it is of
+        self._copies = [torch.empty(w.shape, dtype=torch.uint8, device=device) for w in (self.gate_up, self.down)]
+        self._cast_of = [None, None]
 
     def metas(self):
         return [self.meta_x, self.meta_gate_up, self.meta_h, self.meta_down, self.meta_dy, self.meta_dgu]
 
+    def _weights(self):
+        return (self.gate_up, self.meta_gate_up), (self.down, self.meta_down)
+
     def weight_copies(self):
         """The weights' E4M3 copies under their metas' scales, cast if they are
         not current."""
-        if self._cast_of != self._weight_versions():
-            # new arrays: a backward pass may still hold the last ones
-            self._gate_up8, self._down8 = torch.empty_like(self._gate_up8), torch.empty_like(self._down8)
-            for w, w8, m in ((self.gate_up, self._gate_up8, self.meta_gate_up), (self.down, self._down8, self.meta_down)):
-                fp8_quantize(w.detach(), E4M3, m.scale, w8, None, m.cur_amax)
-            self._cast_of = self._weight_versions()
-        return self._gate_up8, self._down8
+        for i, (w, m) in enumerate(self._weights()):
+            if self._cast_of[i] != _version(w):
+                # a new array: a backward pass may still hold the last one
+                self._copies[i] = torch.empty_like(self._copies[i])
+                fp8_quantize(w.detach(), E4M3, m.scale, self._copies[i], None, m.cur_amax)
+                self._cast_of[i] = _version(w)
+        return tuple(self._copies)
 
     def copies_for_step(self):
         """(weight, E4M3 copy, meta) for an optimizer that writes the copies; it
         calls copies_written() when it has."""
-        return [(self.gate_up, self._gate_up8, self.meta_gate_up), (self.down, self._down8, self.meta_down)]
+        return [(w, w8, m) for (w, m), w8 in zip(self._weights(), self._copies)]
 
-    def copies_written(self) -> None:
-        """The copies are of the weights as they are now. A backward pass that
-        still needs the ones before fails, as after any change in place."""
-        for w8 in (self._gate_up8, self._down8):
-            torch.autograd.graph.increment_version(w8)
-        self._cast_of = self._weight_versions()
-
-    def _weight_versions(self):
-        # (another array under the same parameter, .data = ..., keeps the version)
-        return self.gate_up._version, self.gate_up.data_ptr(), self.down._version, self.down.data_ptr()
+    def copies_written(self, weights=None) -> None:
+        """The copies of `weights` (all, if None) are of the weights as they are
+        now; the others are as current as they were. A backward pass that still
+        needs the ones before fails, as after any change in place."""
+        for i, (w, _) in enumerate(self._weights()):
+            if weights is None or any(w is x for x in weights):
+                torch.autograd.graph.increment_version(self._copies[i])
+                self._cast_of[i] = _version(w)
 
     def weights_changed(self) -> None:
         """Cast the weights again before their next use (for changes that torch
         does not see; its own are noticed)."""
-        self._cast_of = None
+        self._cast_of = [None, None]
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         keep = torch.is_grad_enabled() and (x.requires_grad or self.gate_up.requires_grad or self.down.requires_grad)
@@ -164,4 +170,4 @@ class FP8GatedMLP(torch.nn.Module):
         """Roll the amax histories and refresh the scales for the next step; the
         weights' copies, cast under the old ones, are not current after it."""
         delayed_scaling_update(self.metas(), self.algo, self.margin)
-        self._cast_of = None
+        self.weights_changed()

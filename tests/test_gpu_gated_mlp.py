@@ -208,6 +208,28 @@ def test_the_copies_after_a_skipped_step(cuda_lib):
     assert torch.equal(y, mlp(x)) and torch.isfinite(y).all()
 
 
+@pytest.mark.parametrize("frozen", ["gate_up", "down"])
+def test_a_frozen_weight_keeps_its_own_copy(cuda_lib, frozen):
+    """update_scales changes a weight's scale and the step does not hold that
+    weight: the next forward pass is that of a fresh cast."""
+    from fp8_mixed_precision_reduce_gb300.adamw import AdamW
+    from fp8_mixed_precision_reduce_gb300.gated_mlp import FP8GatedMLP
+
+    torch.manual_seed(5)
+    mlp = FP8GatedMLP(64, 96)
+    getattr(mlp, frozen).requires_grad_(False)
+    opt = AdamW([p for p in mlp.parameters() if p.requires_grad], lr=1e-2, modules=[mlp], loss_scale=64.0)
+    x = torch.randn((32, 64), device="cuda")
+    for _ in range(2):
+        opt.zero_grad()
+        (mlp(x).sum() * opt.loss_scale).sum().backward()
+        mlp.update_scales()
+        opt.step()
+        y = mlp(x)
+        mlp.weights_changed()
+        assert torch.equal(y, mlp(x))
+
+
 def test_replaced_weights_are_cast_again(cuda_lib):
     from fp8_mixed_precision_reduce_gb300.gated_mlp import FP8GatedMLP
 

@@ -1,0 +1,121 @@
+"""FP8GatedMLP, FP8Linear and AdamW around the library's calls, without a GPU:
+on CPU tensors, with the calls they make replaced by plain torch operations."""
+
+import pytest
+import torch
+
+import fp8_mixed_precision_reduce_gb300 as fp8mp
+from fp8_mixed_precision_reduce_gb300 import adamw, gated_mlp
+
+
+def cast(w, scale):
+    return (w.detach().float() * scale).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+
+
+def plain_quantize(x, fmt, scale, out, out_t=None, amax=None, stream=None):
+    out.copy_(cast(x, scale))
+    amax.copy_(torch.maximum(amax, x.abs().max()))
+
+
+def plain_update(metas, algo, margin=0, stream=None):
+    for m in metas:
+        if m.cur_amax.item() > 0:
+            m.scale.copy_(fp8mp.FMT_MAX[m.fmt] / m.cur_amax)
+            m.scale_inv.copy_(1 / m.scale)
+
+
+def plain_step(plan, *scalars, lr, **kw):
+    """w -= lr (grad + decay w), and the copies of a plan's rows."""
+    rows = plan.c_array()
+    for i, (grad, w, *_, copy, scale, amax) in enumerate(plan._keep):
+        w.sub_(lr * (grad + rows[i].weight_decay * w))
+        if copy is not None:
+            copy.copy_(cast(w, scale))
+            amax.copy_(torch.maximum(amax, w.abs().max()))
+
+
+@pytest.fixture
+def plain(monkeypatch):
+    fp8mp.build()
+    monkeypatch.setattr(gated_mlp, "fp8_quantize", plain_quantize)
+    monkeypatch.setattr(gated_mlp, "delayed_scaling_update", plain_update)
+    monkeypatch.setattr(adamw, "mp_grad_norm", lambda *a: None)
+    monkeypatch.setattr(adamw, "mp_adamw_step", plain_step)
+
+
+def block(seed=0):
+    torch.manual_seed(seed)
+    return gated_mlp.FP8GatedMLP(32, 48, device="cpu")
+
+
+def step(opt, *modules):
+    for p in opt.params:
+        p.grad = torch.randn_like(p)
+    for m in modules:
+        m.update_scales()
+    opt.step()
+
+
+def copies_are_current(mlp):
+    return all(torch.equal(c, cast(w, m.scale)) for c, w, m in zip(
+        mlp.weight_copies(), (mlp.gate_up, mlp.down), (mlp.meta_gate_up, mlp.meta_down)))
+
+
+# ------------------------------------- copies that a step writes, and others
+
+
+@pytest.mark.parametrize("trained", ["gate_up", "down"])
+@pytest.mark.parametrize("cast_before", [True, False])
+def test_a_weight_the_step_does_not_hold(plain, trained, cast_before):
+    mlp = block()
+    opt = adamw.AdamW([getattr(mlp, trained)], lr=1e-2, modules=[mlp])
+    for _ in range(3):
+        if cast_before:
+            mlp.weight_copies()
+        step(opt, mlp)
+        assert copies_are_current(mlp)
+
+
+def test_what_the_step_wrote_is_not_cast_again(plain, monkeypatch):
+    mlp = block()
+    opt = adamw.AdamW([mlp.gate_up], lr=1e-2, modules=[mlp])
+    mlp.weight_copies()
+    step(opt, mlp)
+    cast_weights = []
+    monkeypatch.setattr(gated_mlp, "fp8_quantize", lambda x, *a: (cast_weights.append(x.shape), plain_quantize(x, *a)))
+    mlp.weight_copies()
+    assert cast_weights == [mlp.down.shape]
+
+
+def test_two_optimizers_of_one_module(plain):
+    mlp = block()
+    first, second = (adamw.AdamW([w], lr=1e-2, modules=[mlp]) for w in (mlp.gate_up, mlp.down))
+    mlp.weight_copies()
+    for p in (mlp.gate_up, mlp.down):
+        p.grad = torch.randn_like(p)
+    mlp.update_scales()
+    first.step()
+    assert copies_are_current(mlp)
+    second.step()
+    assert copies_are_current(mlp)
+
+
+def test_a_weight_of_two_modules(plain):
+    a, b = block(1), block(2)
+    b.down = a.down
+    opt = adamw.AdamW([a.gate_up, a.down, b.gate_up], lr=1e-2, modules=[a, b])
+    for _ in range(2):
+        step(opt, a, b)
+        a.meta_down.scale.mul_(2)  # (the modules' scales of the shared weight need not agree)
+        a.weights_changed()
+        step(opt)
+        assert copies_are_current(a) and copies_are_current(b)
+
+
+def test_a_parameter_that_was_replaced(plain):
+    mlp = block()
+    opt = adamw.AdamW(mlp.parameters(), lr=1e-2, modules=[mlp])
+    step(opt, mlp)
+    mlp.down = torch.nn.Parameter(torch.randn_like(mlp.down))
+    step(opt, mlp)
+    assert copies_are_current(mlp)
