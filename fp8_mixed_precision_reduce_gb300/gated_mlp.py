@@ -163,6 +163,9 @@ class FP8GatedMLP(torch.nn.Module):
         self._cast_of = [None, None]
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
+        if x.dim() == 0 or x.shape[-1] != self.features or x.device != self._copies[0].device:
+            raise ValueError(f"x must be [..., {self.features}] on {self._copies[0].device}, got {tuple(x.shape)} on "
+                             f"{x.device}")
         keep = torch.is_grad_enabled() and (x.requires_grad or self.gate_up.requires_grad or self.down.requires_grad)
         return _FP8GatedMLPFn.apply(x, self.gate_up, self.down, self, keep)
 

@@ -119,3 +119,18 @@ def test_a_parameter_that_was_replaced(plain):
     mlp.down = torch.nn.Parameter(torch.randn_like(mlp.down))
     step(opt, mlp)
     assert copies_are_current(mlp)
+
+
+# ------------------------------------------------------------------- inputs
+
+
+@pytest.mark.parametrize("shape", [(4, 16), (2, 64), (1, 31), (0, 16), (32, 4), ()])
+def test_an_input_of_another_width_is_refused(shape):
+    """Also one whose elements would fill rows of the block's width."""
+    with pytest.raises(ValueError, match="32"):
+        block()(torch.zeros(shape))
+
+
+def test_an_input_on_another_device_is_refused():
+    with pytest.raises(ValueError, match="meta"):
+        block()(torch.zeros((4, 32), device="meta"))
