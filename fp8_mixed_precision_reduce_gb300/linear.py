@@ -126,6 +126,9 @@ class FP8Linear(torch.nn.Module):
         return self._dbias_ws
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
+        if x.dim() == 0 or x.shape[-1] != self.in_features or x.device != self.meta_x.scale.device:
+            raise ValueError(f"x must be [..., {self.in_features}] on {self.meta_x.scale.device}, got {tuple(x.shape)} on "
+                             f"{x.device}")
         return _FP8LinearFn.apply(x, self.weight, self.bias, self)
 
     def update_scales(self) -> None:

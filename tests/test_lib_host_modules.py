@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import fp8_mixed_precision_reduce_gb300 as fp8mp
-from fp8_mixed_precision_reduce_gb300 import adamw, gated_mlp
+from fp8_mixed_precision_reduce_gb300 import adamw, gated_mlp, linear
 
 
 def cast(w, scale):
@@ -134,3 +134,11 @@ def test_an_input_of_another_width_is_refused(shape):
 def test_an_input_on_another_device_is_refused():
     with pytest.raises(ValueError, match="meta"):
         block()(torch.zeros((4, 32), device="meta"))
+
+
+@pytest.mark.parametrize("x", [torch.zeros((16, 16)), torch.zeros((16, 64)), torch.zeros(()),
+                               torch.zeros((16, 32), device="meta")])
+def test_a_linear_refuses_an_input_of_another_width_or_device(x):
+    """(A weight's copy was laid out for the input's width.)"""
+    with pytest.raises(ValueError, match="32"):
+        linear.FP8Linear(32, 48, device="cpu")(x)
