@@ -79,9 +79,9 @@ class AdamW:
         return copies, written
 
     def _tensors(self, grads, copies) -> AdamWTensors:
-        """The step's tensors, rebuilt when a weight or a module's copy is another array."""
-        now = [p.data_ptr() for p in self.params]
-        now += [(c.data_ptr(), m.scale.data_ptr()) for c, m in copies.values()]
+        """The step's tensors, rebuilt when an array or a decay that they hold is another."""
+        now = [p.data_ptr() for p in self.params] + list(self.weight_decay)
+        now += [(c.data_ptr(), m.scale.data_ptr(), m.cur_amax.data_ptr()) for c, m in copies.values()]
         if self._plan is not None and now == self._arrays:
             self._plan.set_grads(grads)
             return self._plan

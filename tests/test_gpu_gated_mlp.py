@@ -274,6 +274,18 @@ def test_a_replaced_weight_is_the_one_that_is_stepped(cuda_lib):
     assert torch.equal(old, kept) and (p < 7.0).all()
 
 
+def test_a_changed_decay_applies_at_the_next_step(cuda_lib):
+    from fp8_mixed_precision_reduce_gb300.adamw import AdamW
+
+    p = torch.nn.Parameter(torch.ones((4, 64), device="cuda"))
+    opt = AdamW([p], lr=0.5, weight_decay=0.0, loss_scale=1.0)
+    for decay, want in ((0.0, 1.0), (0.5, 0.75), (0.0, 0.75)):
+        opt.weight_decay[0] = decay
+        p.grad = torch.zeros_like(p)
+        opt.step()
+        assert (p == want).all()
+
+
 def test_refusals(cuda_lib):
     from fp8_mixed_precision_reduce_gb300.adamw import AdamW
     from fp8_mixed_precision_reduce_gb300.gated_mlp import FP8GatedMLP

@@ -142,3 +142,26 @@ def test_a_linear_refuses_an_input_of_another_width_or_device(x):
     """(A weight's copy was laid out for the input's width.)"""
     with pytest.raises(ValueError, match="32"):
         linear.FP8Linear(32, 48, device="cpu")(x)
+
+
+# ------------------------------------------------ what a kept plan was made of
+
+
+def test_a_changed_decay_is_the_next_steps(plain):
+    p = torch.nn.Parameter(torch.ones(4, 16))
+    opt = adamw.AdamW([p], lr=0.5, weight_decay=0.0)
+    for decay, want in ((0.0, 1.0), (0.5, 0.75), (0.0, 0.75)):
+        opt.weight_decay[0] = decay
+        p.grad = torch.zeros_like(p)
+        opt.step()
+        assert (p == want).all()
+
+
+def test_a_replaced_amax_is_the_one_that_is_raised(plain):
+    mlp = block()
+    opt = adamw.AdamW(mlp.parameters(), lr=1e-2, modules=[mlp])
+    step(opt)
+    old = mlp.meta_down.cur_amax
+    mlp.meta_down.cur_amax, kept = torch.zeros(1), old.clone()
+    step(opt)
+    assert torch.equal(old, kept) and mlp.meta_down.cur_amax.item() == mlp.down.abs().max().item()
