@@ -626,7 +626,7 @@ def _workspace(workspace: torch.Tensor):
 def mp_grad_norm(tensors: AdamWTensors, norm: torch.Tensor, found_inf: torch.Tensor, workspace: torch.Tensor,
                  stream=None) -> None:
     """norm = the 2-norm of all the tensors' gradients (under the loss scale),
-    found_inf = 1 if their sum of squares is not finite, else 0. workspace: at
+    found_inf = 1 if their sum of squares is not finite in fp32, else 0. workspace: at
     least mp_adamw_workspace_bytes() bytes, zero-filled before its first use."""
     _check(load().mp_grad_norm(tensors.c_array(), len(tensors), _ptr(norm), _ptr(found_inf), *_workspace(workspace),
                                _stream(stream)))

@@ -736,12 +736,13 @@ int64_t mp_adamw_workspace_bytes(void);
  * overflow flag, in one pass over them:
  *   *norm      = sqrt(sum over tensors and elements of fl32(grad)^2)
  *   *found_inf = 1 if that sum is not finite, else 0
- * The sum is not finite when a gradient is Inf or NaN, or when squares leave
- * fp32 (|grad| above 1.8e19): the dynamic loss scaler then skips the step and
- * lowers S ([MP], the dynamic loss-scale procedure). The norm is that of the
- * gradients as they are, under the loss scale. Sums in fp32 within a block of
- * threads, in double across blocks, in an order fixed by the sizes and the
- * device (deterministic).
+ * A sum of 2^128 or more counts as Inf: squares are added in fp32 within a
+ * block of threads. So the sum is not finite when a gradient is Inf or NaN or
+ * when the norm reaches 2^64 (1.8e19): the dynamic loss scaler then skips the
+ * step and lowers S ([MP], the dynamic loss-scale procedure). The norm is that
+ * of the gradients as they are, under the loss scale. The blocks' sums are
+ * added in double, all in an order fixed by the sizes and the device
+ * (deterministic).
  * tensors  HOST array of n_tensors >= 0 structs, read during the call only.
  */
 int mp_grad_norm(const fp8mp_adamw_tensor *tensors, int32_t n_tensors, float *norm, int32_t *found_inf,

@@ -472,6 +472,22 @@ def test_norm_finds_overflow(cuda_lib, bad):
     assert st.found.item() == 0 and np.isfinite(st.norm.item())
 
 
+def test_norm_past_2_64(cuda_lib):
+    """64 gradients in one block of threads or in 64 blocks: a norm of 2^63, and one
+    of 2^64, which counts as infinite either way."""
+    n = 8192 * 64
+    for scattered in (False, True):
+        x = Tensor(n, grad=torch.float32, copy=None, grad_std=0.0)
+        st = Step(cuda_lib, [x])
+        places = torch.arange(64, device="cuda") * (8192 if scattered else 1)
+        x.grad[places] = 2.0 ** 60  # the norm is 2^63
+        st.measure()
+        assert st.norm.item() == 2.0 ** 63 and st.found.item() == 0
+        x.grad[places] = 2.0 ** 61  # 2^64
+        st.measure()
+        assert st.norm.item() == float("inf") and st.found.item() == 1, scattered
+
+
 def test_rounding_is_unbiased(cuda_lib):
     """Over 400 seeds the stored moments' mean is the moment: the deviation of a
     mean of 400 two-valued codes is at most half a step / 20; 5 of those."""
