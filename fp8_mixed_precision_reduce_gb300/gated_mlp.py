@@ -139,7 +139,7 @@ class FP8GatedMLP(torch.nn.Module):
             if self._cast_of[i] != _version(w):
                 # a new array: a backward pass may still hold the last one
                 self._copies[i] = torch.empty_like(self._copies[i])
-                fp8_quantize(w.detach(), E4M3, m.scale, self._copies[i], None, m.cur_amax)
+                fp8_quantize(w.detach().contiguous(), E4M3, m.scale, self._copies[i], None, m.cur_amax)
                 self._cast_of[i] = _version(w)
         return tuple(self._copies)
 

@@ -40,10 +40,10 @@ class _FP8LinearFn(torch.autograd.Function):
         W8 = torch.empty((N, K), dtype=u8, device=dev)
         # row-major copies only: the backward GEMMs read them along their rows
         fp8_quantize(x2, E4M3, layer.meta_x.scale, X8, None, layer.meta_x.cur_amax)
-        fp8_quantize(weight.detach(), E4M3, layer.meta_w.scale, W8, None, layer.meta_w.cur_amax)
+        fp8_quantize(weight.detach().contiguous(), E4M3, layer.meta_w.scale, W8, None, layer.meta_w.cur_amax)
         y = torch.empty((M, N), dtype=x.dtype, device=dev)
         fp8_linear_fwd(X8, W8, layer.meta_x.scale_inv, layer.meta_w.scale_inv, y,
-                       bias=bias.detach() if bias is not None else None, y_amax=layer.meta_y.cur_amax)
+                       bias=bias.detach().contiguous() if bias is not None else None, y_amax=layer.meta_y.cur_amax)
         # the codes were made with this step's scales: keep those for backward
         ctx.save_for_backward(X8, W8, layer.meta_x.scale_inv.clone(), layer.meta_w.scale_inv.clone())
         ctx.layer = layer

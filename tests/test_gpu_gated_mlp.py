@@ -245,6 +245,18 @@ def test_replaced_weights_are_cast_again(cuda_lib):
             assert not torch.equal(z, y) and torch.equal(mlp(x), y)
 
 
+def test_weights_of_any_strides(cuda_lib):
+    from fp8_mixed_precision_reduce_gb300.gated_mlp import FP8GatedMLP
+
+    mlp = FP8GatedMLP(64, 96)
+    x = torch.randn((5, 64), device="cuda")
+    with torch.no_grad():
+        y = mlp(x)
+        for w in (mlp.gate_up, mlp.down):
+            w.data = w.data.t().contiguous().t()
+            assert not w.is_contiguous() and torch.equal(mlp(x), y)
+
+
 @pytest.mark.parametrize("shape", [(0, 64), (2, 0, 64), (1, 64), (2, 3, 64), (70, 64)])
 def test_any_number_of_tokens(cuda_lib, shape):
     from fp8_mixed_precision_reduce_gb300.gated_mlp import FP8GatedMLP

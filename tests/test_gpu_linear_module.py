@@ -100,3 +100,16 @@ def test_fp8linear_rejects_unaligned_features(cuda_lib):
 
     with pytest.raises(ValueError):
         FP8Linear(100, 64)
+
+
+def test_weight_and_bias_of_any_strides(cuda_lib):
+    from fp8_mixed_precision_reduce_gb300.linear import FP8Linear
+
+    layer = FP8Linear(64, 96)
+    x = torch.randn((16, 64), device="cuda")
+    with torch.no_grad():
+        y = layer(x)
+        layer.weight.data = layer.weight.data.t().contiguous().t()
+        layer.bias.data = layer.bias.data[:, None].expand(96, 2).contiguous()[:, 0]
+        assert not layer.weight.is_contiguous() and not layer.bias.is_contiguous()
+        assert torch.equal(layer(x), y)

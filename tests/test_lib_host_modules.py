@@ -165,3 +165,16 @@ def test_a_replaced_amax_is_the_one_that_is_raised(plain):
     mlp.meta_down.cur_amax, kept = torch.zeros(1), old.clone()
     step(opt)
     assert torch.equal(old, kept) and mlp.meta_down.cur_amax.item() == mlp.down.abs().max().item()
+
+
+# ------------------------------------------ weights that are not as they were
+
+
+def test_a_transposed_weight_is_cast_as_it_reads(plain, monkeypatch):
+    mlp = block()
+    laid_out = []
+    monkeypatch.setattr(gated_mlp, "fp8_quantize",
+                        lambda x, *a: (laid_out.append(x.is_contiguous()), plain_quantize(x, *a)))
+    for w in (mlp.gate_up, mlp.down):
+        w.data = w.data.t().contiguous().t()
+    assert copies_are_current(mlp) and all(laid_out)
