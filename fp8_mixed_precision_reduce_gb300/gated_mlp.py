@@ -136,6 +136,9 @@ class FP8GatedMLP(torch.nn.Module):
         """The weights' E4M3 copies under their metas' scales, cast if they are
         not current."""
         for i, (w, m) in enumerate(self._weights()):
+            if w.shape != self._copies[i].shape or w.device != self._copies[i].device:
+                raise ValueError(f"a weight must stay {tuple(self._copies[i].shape)} on {self._copies[i].device}, got "
+                                 f"{tuple(w.shape)} on {w.device}")
             if self._cast_of[i] != _version(w):
                 # a new array: a backward pass may still hold the last one
                 self._copies[i] = torch.empty_like(self._copies[i])

@@ -178,3 +178,18 @@ def test_a_transposed_weight_is_cast_as_it_reads(plain, monkeypatch):
     for w in (mlp.gate_up, mlp.down):
         w.data = w.data.t().contiguous().t()
     assert copies_are_current(mlp) and all(laid_out)
+
+
+def test_a_weight_of_another_shape_is_refused(plain):
+    mlp = block()
+    for w in (mlp.gate_up, mlp.down):
+        kept = w.data
+        for other in (torch.zeros((200, 32)), kept[:16], kept.reshape(-1)):
+            w.data = other
+            with pytest.raises(ValueError, match="weight"):
+                mlp.weight_copies()
+        w.data = kept
+        mlp.weight_copies()
+    mlp.down = torch.nn.Parameter(mlp.down.to("meta"))
+    with pytest.raises(ValueError, match="weight"):
+        mlp.weight_copies()
