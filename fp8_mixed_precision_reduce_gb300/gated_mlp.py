@@ -30,9 +30,16 @@ def _rows16(rows: int, cols: int, dtype: torch.dtype, device) -> torch.Tensor:
     return t
 
 
-def _version(w: torch.Tensor):
-    # (another array under the same parameter, .data = ..., keeps the version)
-    return w._version, w.data_ptr()
+class _CastOf:
+    """Which state of a weight a copy is of. The weight's array is kept alive, so
+    that another one under the same parameter (.data = ..., which leaves the
+    version as it is) cannot have its address."""
+
+    def __init__(self, w: torch.Tensor):
+        self.version, self.array = w._version, w.detach()
+
+    def is_current(self, w: torch.Tensor) -> bool:
+        return self.version == w._version and self.array.dtype == w.dtype and self.array.is_set_to(w)
 
 
 class _FP8GatedMLPFn(torch.autograd.Function):
@@ -122,7 +129,7 @@ class FP8GatedMLP(torch.nn.Module):
         self.meta_dy, self.meta_dgu = Meta(history_len, E5M2, device), Meta(history_len, E5M2, device)
         # 1 once a weight gradient held an Inf or NaN
         self.dw_nonfinite = torch.zeros(1, dtype=torch.int32, device=device)
-        # of gate_up and of down: the E4M3 copy, and the version of the weight that it is of
+        # of gate_up and of down: the E4M3 copy, and what it is of
         self._copies = [torch.empty(w.shape, dtype=torch.uint8, device=device) for w in (self.gate_up, self.down)]
         self._cast_of = [None, None]
 
@@ -139,11 +146,11 @@ class FP8GatedMLP(torch.nn.Module):
             if w.shape != self._copies[i].shape or w.device != self._copies[i].device:
                 raise ValueError(f"a weight must stay {tuple(self._copies[i].shape)} on {self._copies[i].device}, got "
                                  f"{tuple(w.shape)} on {w.device}")
-            if self._cast_of[i] != _version(w):
+            if self._cast_of[i] is None or not self._cast_of[i].is_current(w):
                 # a new array: a backward pass may still hold the last one
                 self._copies[i] = torch.empty_like(self._copies[i])
                 fp8_quantize(w.detach().contiguous(), E4M3, m.scale, self._copies[i], None, m.cur_amax)
-                self._cast_of[i] = _version(w)
+                self._cast_of[i] = _CastOf(w)
         return tuple(self._copies)
 
     def copies_for_step(self):
@@ -158,12 +165,16 @@ class FP8GatedMLP(torch.nn.Module):
         for i, (w, _) in enumerate(self._weights()):
             if weights is None or any(w is x for x in weights):
                 torch.autograd.graph.increment_version(self._copies[i])
-                self._cast_of[i] = _version(w)
+                self._cast_of[i] = _CastOf(w)
 
     def weights_changed(self) -> None:
         """Cast the weights again before their next use (for changes that torch
         does not see; its own are noticed)."""
         self._cast_of = [None, None]
+
+    def _apply(self, fn, *args, **kw):  # .to() and the like: the arrays before are let go
+        self.weights_changed()
+        return super()._apply(fn, *args, **kw)
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         if x.dim() == 0 or x.shape[-1] != self.features or x.device != self._copies[0].device:

@@ -257,6 +257,21 @@ def test_weights_of_any_strides(cuda_lib):
             assert not w.is_contiguous() and torch.equal(mlp(x), y)
 
 
+def test_weights_replaced_more_than_once(cuda_lib):
+    from fp8_mixed_precision_reduce_gb300.gated_mlp import FP8GatedMLP
+
+    mlp = FP8GatedMLP(64, 96)
+    x = torch.randn((5, 64), device="cuda")
+    with torch.no_grad():
+        mlp(x)
+        for w in (mlp.gate_up, mlp.down):
+            for _ in range(2):  # the second may take the first's place in memory
+                w.data = w.data * 0.5
+            y = mlp(x)
+            mlp.weights_changed()
+            assert torch.equal(y, mlp(x))
+
+
 @pytest.mark.parametrize("shape", [(0, 64), (2, 0, 64), (1, 64), (2, 3, 64), (70, 64)])
 def test_any_number_of_tokens(cuda_lib, shape):
     from fp8_mixed_precision_reduce_gb300.gated_mlp import FP8GatedMLP

@@ -193,3 +193,10 @@ def test_a_weight_of_another_shape_is_refused(plain):
     mlp.down = torch.nn.Parameter(mlp.down.to("meta"))
     with pytest.raises(ValueError, match="weight"):
         mlp.weight_copies()
+
+
+def test_a_weight_transposed_in_place_is_cast_again(plain):
+    mlp = gated_mlp.FP8GatedMLP(32, 32, device="cpu")
+    mlp.weight_copies()
+    mlp.down.data = mlp.down.data.t()  # the same address and version
+    assert copies_are_current(mlp)
