@@ -99,6 +99,8 @@ class AdamW:
         for i, p in enumerate(self.params):
             if p.grad is None:
                 raise ValueError(f"parameter {i} has no gradient")
+            if not p.is_contiguous():
+                raise ValueError(f"parameter {i} is no longer dense")
             grads.append(p.grad if p.grad.is_contiguous() else p.grad.contiguous())
         copies, written = self._copies()
         plan = self._tensors(grads, copies)

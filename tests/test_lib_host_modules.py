@@ -200,3 +200,12 @@ def test_a_weight_transposed_in_place_is_cast_again(plain):
     mlp.weight_copies()
     mlp.down.data = mlp.down.data.t()  # the same address and version
     assert copies_are_current(mlp)
+
+
+def test_a_parameter_that_is_no_longer_dense_is_refused(plain):
+    p = torch.nn.Parameter(torch.ones(16, 16))
+    opt = adamw.AdamW([p], lr=1e-2)
+    step(opt)
+    p.data = p.data.t()
+    with pytest.raises(ValueError, match="dense"):
+        step(opt)
