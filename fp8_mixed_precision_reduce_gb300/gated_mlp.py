@@ -15,8 +15,9 @@ from __future__ import annotations
 
 import torch
 
-from . import (AMAX_MAX, E4M3, E5M2, FEW_TOKENS, GELU_TANH, SILU, Meta, delayed_scaling_update, fp8_gated_bwd,
-               fp8_gated_dgrad, fp8_gated_fwd, fp8_linear_bwd_rowmajor, fp8_linear_few, fp8_linear_fwd, fp8_quantize)
+from . import (AMAX_MAX, E4M3, E5M2, FEW_TOKENS, GELU_TANH, SILU, Meta, _stream, delayed_scaling_update,
+               fp8_gated_bwd, fp8_gated_dgrad, fp8_gated_fwd, fp8_linear_bwd_rowmajor, fp8_linear_few, fp8_linear_fwd,
+               fp8_quantize)
 
 __all__ = ["FP8GatedMLP"]
 
@@ -31,15 +32,34 @@ def _rows16(rows: int, cols: int, dtype: torch.dtype, device) -> torch.Tensor:
 
 
 class _CastOf:
-    """Which state of a weight a copy is of. The weight's array is kept alive, so
-    that another one under the same parameter (.data = ..., which leaves the
-    version as it is) cannot have its address."""
+    """Which state of a weight a copy is of, and when it is there. The weight's
+    array is kept alive, so that another one under the same parameter (.data =
+    ..., which leaves the version as it is) cannot have its address."""
 
     def __init__(self, w: torch.Tensor):
         self.version, self.array = w._version, w.detach()
+        self.streams, self.written = set(), None
+        if w.is_cuda and not torch.cuda.is_current_stream_capturing():
+            self.streams.add(_stream(None))
+            self.written = torch.cuda.Event()
+            self.written.record()
+
+    def __reduce__(self):  # a copy of the module casts its own
+        return type(None), ()
 
     def is_current(self, w: torch.Tensor) -> bool:
         return self.version == w._version and self.array.dtype == w.dtype and self.array.is_set_to(w)
+
+    def use(self, copy: torch.Tensor) -> None:
+        """The copy is about to be read on the current stream: one that did not
+        write it waits for it, once, and keeps the array from being reused. (A
+        stream that is being captured cannot wait for work from outside.)"""
+        if self.written is None or _stream(None) in self.streams or torch.cuda.is_current_stream_capturing():
+            return
+        stream = torch.cuda.current_stream()
+        stream.wait_event(self.written)
+        copy.record_stream(stream)
+        self.streams.add(stream.cuda_stream)
 
 
 class _FP8GatedMLPFn(torch.autograd.Function):
@@ -151,6 +171,8 @@ class FP8GatedMLP(torch.nn.Module):
                 self._copies[i] = torch.empty_like(self._copies[i])
                 fp8_quantize(w.detach().contiguous(), E4M3, m.scale, self._copies[i], None, m.cur_amax)
                 self._cast_of[i] = _CastOf(w)
+            else:
+                self._cast_of[i].use(self._copies[i])
         return tuple(self._copies)
 
     def copies_for_step(self):

@@ -272,6 +272,44 @@ def test_weights_replaced_more_than_once(cuda_lib):
             assert torch.equal(y, mlp(x))
 
 
+def test_copies_cast_on_another_stream(cuda_lib):
+    from fp8_mixed_precision_reduce_gb300.gated_mlp import FP8GatedMLP
+
+    mlp = FP8GatedMLP(64, 96)
+    x = torch.randn((5, 64), device="cuda")
+    side = torch.cuda.Stream()
+    with torch.no_grad():
+        mlp(x)
+        mlp.gate_up.mul_(-1)
+        mlp.down.mul_(-1)
+        side.wait_stream(torch.cuda.current_stream())
+        torch.cuda._sleep(400_000_000)
+        here = mlp(x)  # casts the weights, after a fifth of a second
+        with torch.cuda.stream(side):
+            there = mlp(x)
+        torch.cuda.synchronize()
+    assert torch.equal(here, there)
+
+
+def test_copies_of_a_module(cuda_lib):
+    import copy
+    import io
+
+    from fp8_mixed_precision_reduce_gb300.gated_mlp import FP8GatedMLP
+
+    mlp = FP8GatedMLP(64, 96)
+    x = torch.randn((5, 64), device="cuda")
+    with torch.no_grad():
+        y = mlp(x)
+        other = copy.deepcopy(mlp)
+        file = io.BytesIO()
+        torch.save(mlp, file)
+        file.seek(0)
+        mlp.down.mul_(-1)
+        assert torch.equal(mlp(x), -y) and torch.equal(other(x), y)
+        assert torch.equal(torch.load(file, weights_only=False)(x), y)
+
+
 @pytest.mark.parametrize("shape", [(0, 64), (2, 0, 64), (1, 64), (2, 3, 64), (70, 64)])
 def test_any_number_of_tokens(cuda_lib, shape):
     from fp8_mixed_precision_reduce_gb300.gated_mlp import FP8GatedMLP
