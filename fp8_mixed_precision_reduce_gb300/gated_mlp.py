@@ -39,7 +39,7 @@ class _CastOf:
     def __init__(self, w: torch.Tensor):
         self.version, self.array = w._version, w.detach()
         self.streams, self.written = set(), None
-        if w.is_cuda and not torch.cuda.is_current_stream_capturing():
+        if w.is_cuda:
             self.streams.add(_stream(None))
             self.written = torch.cuda.Event()
             self.written.record()
@@ -52,14 +52,17 @@ class _CastOf:
 
     def use(self, copy: torch.Tensor) -> None:
         """The copy is about to be read on the current stream: one that did not
-        write it waits for it, once, and keeps the array from being reused. (A
-        stream that is being captured cannot wait for work from outside.)"""
-        if self.written is None or _stream(None) in self.streams or torch.cuda.is_current_stream_capturing():
+        write it waits for it, once, and keeps the array from being reused."""
+        if self.written is None or _stream(None) in self.streams:
             return
         stream = torch.cuda.current_stream()
         stream.wait_event(self.written)
         copy.record_stream(stream)
         self.streams.add(stream.cuda_stream)
+
+
+def _capturing(w: torch.Tensor) -> bool:
+    return w.is_cuda and torch.cuda.is_current_stream_capturing()
 
 
 class _FP8GatedMLPFn(torch.autograd.Function):
@@ -70,7 +73,7 @@ class _FP8GatedMLPFn(torch.autograd.Function):
         if not x2.is_contiguous():
             x2 = x2.contiguous()
         M, dev = x2.shape[0], x.device
-        gu8, d8 = mlp.weight_copies()
+        gu8, d8 = mlp.weight_copies(keep)
         X8 = torch.empty((M, K), dtype=torch.uint8, device=dev)
         fp8_quantize(x2, E4M3, mlp.meta_x.scale, X8, None, mlp.meta_x.cur_amax)
         few = M <= FEW_TOKENS
@@ -126,7 +129,10 @@ class FP8GatedMLP(torch.nn.Module):
     holds Wg above Wu, down [features, hidden] Wd, in high precision; their E4M3
     copies are cast when they are not current. Call update_scales() once per
     training step, after backward; an optimizer that writes the copies itself
-    (AdamW) does so after it. x is bf16 or fp32.
+    (AdamW) does so after it. x is bf16 or fp32. In a CUDA graph the casts are
+    part of the graph, unless it is captured in eval mode without gradients
+    (serving): then it reads the copies that are current, and after a change of
+    the weights weight_copies() casts them for its next replay.
     """
 
     def __init__(self, features: int, hidden: int, act: int = SILU, history_len: int = 16,
@@ -152,6 +158,8 @@ class FP8GatedMLP(torch.nn.Module):
         # of gate_up and of down: the E4M3 copy, and what it is of
         self._copies = [torch.empty(w.shape, dtype=torch.uint8, device=device) for w in (self.gate_up, self.down)]
         self._cast_of = [None, None]
+        self._in_a_graph = [False, False]  # a captured graph reads the copy's array
+        self._trains_in_a_graph = False  # replays change the weights and their scales unseen
 
     def metas(self):
         return [self.meta_x, self.meta_gate_up, self.meta_h, self.meta_down, self.meta_dy, self.meta_dgu]
@@ -159,20 +167,31 @@ class FP8GatedMLP(torch.nn.Module):
     def _weights(self):
         return (self.gate_up, self.meta_gate_up), (self.down, self.meta_down)
 
-    def weight_copies(self):
+    def weight_copies(self, for_training: bool = False):
         """The weights' E4M3 copies under their metas' scales, cast if they are
-        not current."""
+        not current. A capture casts them in the graph, but for a pass without
+        gradients in eval mode: that graph reads the current ones, which every
+        later cast then writes in place."""
         for i, (w, m) in enumerate(self._weights()):
             if w.shape != self._copies[i].shape or w.device != self._copies[i].device:
                 raise ValueError(f"a weight must stay {tuple(self._copies[i].shape)} on {self._copies[i].device}, got "
                                  f"{tuple(w.shape)} on {w.device}")
-            if self._cast_of[i] is None or not self._cast_of[i].is_current(w):
-                # a new array: a backward pass may still hold the last one
-                self._copies[i] = torch.empty_like(self._copies[i])
-                fp8_quantize(w.detach().contiguous(), E4M3, m.scale, self._copies[i], None, m.cur_amax)
-                self._cast_of[i] = _CastOf(w)
-            else:
+            current = self._cast_of[i] is not None and self._cast_of[i].is_current(w)
+            if _capturing(w):
+                current = current and not for_training and not self.training
+                self._trains_in_a_graph |= for_training
+                self._in_a_graph[i] |= current
+            elif current:
                 self._cast_of[i].use(self._copies[i])
+            if not current:
+                # a new array, as a backward pass may still hold the last one; but a
+                # graph's stays (and a backward pass that holds it fails)
+                if self._in_a_graph[i]:
+                    torch.autograd.graph.increment_version(self._copies[i])
+                else:
+                    self._copies[i] = torch.empty_like(self._copies[i])
+                fp8_quantize(w.detach().contiguous(), E4M3, m.scale, self._copies[i], None, m.cur_amax)
+                self._note(i, w)
         return tuple(self._copies)
 
     def copies_for_step(self):
@@ -187,7 +206,12 @@ class FP8GatedMLP(torch.nn.Module):
         for i, (w, _) in enumerate(self._weights()):
             if weights is None or any(w is x for x in weights):
                 torch.autograd.graph.increment_version(self._copies[i])
-                self._cast_of[i] = _CastOf(w)
+                self._trains_in_a_graph |= _capturing(w)
+                self._note(i, w)
+
+    def _note(self, i: int, w: torch.Tensor) -> None:
+        # (what a capture records has not run, and what its replays do is not seen)
+        self._cast_of[i] = None if self._trains_in_a_graph or _capturing(w) else _CastOf(w)
 
     def weights_changed(self) -> None:
         """Cast the weights again before their next use (for changes that torch
@@ -209,4 +233,5 @@ class FP8GatedMLP(torch.nn.Module):
         """Roll the amax histories and refresh the scales for the next step; the
         weights' copies, cast under the old ones, are not current after it."""
         delayed_scaling_update(self.metas(), self.algo, self.margin)
+        self._trains_in_a_graph |= _capturing(self.gate_up)
         self.weights_changed()

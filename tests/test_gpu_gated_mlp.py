@@ -291,6 +291,99 @@ def test_copies_cast_on_another_stream(cuda_lib):
     assert torch.equal(here, there)
 
 
+def test_a_captured_cast_has_not_run(cuda_lib):
+    from fp8_mixed_precision_reduce_gb300.gated_mlp import FP8GatedMLP
+
+    mlp = FP8GatedMLP(64, 96)
+    x = torch.randn((5, 64), device="cuda")
+    with torch.no_grad():
+        mlp(x)
+        mlp.update_scales()
+        want = mlp(x)
+        mlp.weights_changed()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            y = mlp(x)
+        assert torch.equal(mlp(x), want)
+        graph.replay()
+        assert torch.equal(y, want)
+        mlp.down.mul_(-1)
+        graph.replay()
+        assert torch.equal(y, -want) and torch.equal(mlp(x), -want)
+
+
+def test_a_graph_reads_the_copies_that_are_current(cuda_lib):
+    """In eval mode it was captured without a cast: the next cast writes where it reads."""
+    from fp8_mixed_precision_reduce_gb300.gated_mlp import FP8GatedMLP
+
+    mlp = FP8GatedMLP(64, 96).eval()
+    x = torch.randn((5, 64), device="cuda")
+    with torch.no_grad():
+        want = mlp(x)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            y = mlp(x)
+        mlp.down.mul_(-1)
+        assert torch.equal(mlp(x), -want)
+        fill = [torch.full_like(c, 0x7F) for c in mlp.weight_copies() for _ in range(8)]  # freed arrays' places, if any
+        graph.replay()
+        assert torch.equal(y, -want) and len(fill) == 16
+
+
+@pytest.mark.parametrize("optimizer", ["many-tensor", "torch"])
+@pytest.mark.parametrize("warm_up", [0, 3])
+def test_a_captured_training_step(cuda_lib, warm_up, optimizer):
+    """Replays, with evaluations before and between them, are the steps."""
+    from fp8_mixed_precision_reduce_gb300.adamw import AdamW
+    from fp8_mixed_precision_reduce_gb300.gated_mlp import FP8GatedMLP
+
+    torch.manual_seed(6)
+    x = torch.randn((48, 64), device="cuda")
+    start = FP8GatedMLP(64, 96).state_dict()
+
+    def make():
+        mlp = FP8GatedMLP(64, 96)
+        mlp.load_state_dict(start)
+        if optimizer == "torch":
+            opt, loss_scale = torch.optim.SGD(mlp.parameters(), lr=1e-2), 1.0
+        else:
+            opt = AdamW(mlp.parameters(), lr=1e-2, modules=[mlp], loss_scale=64.0)
+            loss_scale = opt.loss_scale
+
+        def step():
+            opt.zero_grad()
+            (mlp(x).pow(2).mean() * loss_scale).sum().backward()
+            mlp.update_scales()
+            opt.step()
+
+        def evaluate():
+            with torch.no_grad():
+                return mlp(x)
+
+        return mlp, step, evaluate
+
+    eager, eager_step, eager_evaluate = make()
+    mlp, step, evaluate = make()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(warm_up):
+            step()
+        evaluate()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(warm_up):
+        eager_step()
+    assert torch.equal(evaluate(), eager_evaluate())
+    for _ in range(3):
+        graph.replay()
+        eager_step()
+        assert torch.equal(mlp.gate_up, eager.gate_up) and torch.equal(mlp.down, eager.down)
+        assert torch.equal(evaluate(), eager_evaluate())
+
+
 def test_copies_of_a_module(cuda_lib):
     import copy
     import io
