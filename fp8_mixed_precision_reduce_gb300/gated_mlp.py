@@ -18,6 +18,7 @@ import torch
 from . import (AMAX_MAX, E4M3, E5M2, FEW_TOKENS, GELU_TANH, SILU, Meta, _stream, delayed_scaling_update,
                fp8_gated_bwd, fp8_gated_dgrad, fp8_gated_fwd, fp8_linear_bwd_rowmajor, fp8_linear_few, fp8_linear_fwd,
                fp8_quantize)
+from .linear import first_order
 
 __all__ = ["FP8GatedMLP"]
 
@@ -119,7 +120,7 @@ class _FP8GatedMLPFn(torch.autograd.Function):
                 dgate_up = torch.empty((2 * F, K), dtype=gate_up_dtype, device=dev)
             fp8_gated_bwd(None, None, X8, gu8, sinv_x, sinv_gu, None, mg.scale_inv, G8, dx, dgate_up, act=mlp.act,
                           dw_nonfinite=mlp.dw_nonfinite if dgate_up is not None else None)
-        return (dx.reshape(x_shape) if dx is not None else None), dgate_up, ddown, None, None
+        return *first_order(dx.reshape(x_shape) if dx is not None else None, dgate_up, ddown), None, None
 
 
 class FP8GatedMLP(torch.nn.Module):

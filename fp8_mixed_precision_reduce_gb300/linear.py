@@ -25,6 +25,26 @@ from . import (AMAX_MAX, E4M3, E5M2, Meta, delayed_scaling_update, fp8_linear_bw
 __all__ = ["FP8Linear"]
 
 
+class _FirstOrder(torch.autograd.Function):
+    """A gradient that the kernels computed: it cannot be differentiated again."""
+
+    @staticmethod
+    def forward(ctx, g):
+        return g.view_as(g)
+
+    @staticmethod
+    def backward(ctx, gg):
+        raise RuntimeError("the FP8 layers have no second derivatives")
+
+
+def first_order(*grads):
+    """The gradients that a backward pass returns. Under create_graph, where they
+    would count as constants, their own derivative raises."""
+    if not torch.is_grad_enabled():
+        return grads
+    return tuple(None if g is None else _FirstOrder.apply(g.requires_grad_()) for g in grads)
+
+
 class _FP8LinearFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, layer):
@@ -77,7 +97,7 @@ class _FP8LinearFn(torch.autograd.Function):
         # dgrad and wgrad in one launch, from the row-major copies
         fp8_linear_bwd_rowmajor(D8, W8, X8, sinv_dy, sinv_w, sinv_x, dx, dw, dy_fmt=E5M2,
                                 dw_nonfinite=layer.dw_nonfinite if dw is not None else None)
-        return (dx.reshape(x_shape) if dx is not None else None), dw, db, None
+        return *first_order(dx.reshape(x_shape) if dx is not None else None, dw, db), None
 
 
 class FP8Linear(torch.nn.Module):

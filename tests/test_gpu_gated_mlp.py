@@ -384,6 +384,20 @@ def test_a_captured_training_step(cuda_lib, warm_up, optimizer):
         assert torch.equal(evaluate(), eager_evaluate())
 
 
+@pytest.mark.parametrize("kind", ["gated", "linear"])
+def test_second_derivatives_are_refused(cuda_lib, kind):
+    from fp8_mixed_precision_reduce_gb300.gated_mlp import FP8GatedMLP
+    from fp8_mixed_precision_reduce_gb300.linear import FP8Linear
+
+    layer = FP8GatedMLP(64, 96) if kind == "gated" else FP8Linear(64, 64)
+    x = torch.randn((16, 64), device="cuda", requires_grad=True)
+    g, = torch.autograd.grad(layer(x).sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        (g.pow(2).sum() + x.sum()).backward()
+    again, = torch.autograd.grad(layer(x).sum(), x)
+    assert torch.equal(again, g) and not again.requires_grad
+
+
 def test_copies_of_a_module(cuda_lib):
     import copy
     import io
