@@ -580,19 +580,20 @@ class AdamWTensors:
                 _expect(exp_avg_sq_scale, "exp_avg_sq_scale", torch.float32, blocks)
             if copy is not None:
                 _expect(copy, "copy", torch.bfloat16 if copy_scale is None else torch.uint8, n)
+        dtype = self._checked(len(self._rows), n, grad)
         self._rows.append(fp8mp_adamw_tensor(
-            None, _ptr(master), _ptr(exp_avg), _ptr(exp_avg_sq), _ptr(exp_avg_scale), _ptr(exp_avg_sq_scale),
-            _ptr(copy), _ptr(copy_scale), _ptr(copy_amax), n, float(weight_decay), F32, bits, 0))
-        self._keep.append([None, master, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, copy, copy_scale,
+            grad.data_ptr(), _ptr(master), _ptr(exp_avg), _ptr(exp_avg_sq), _ptr(exp_avg_scale), _ptr(exp_avg_sq_scale),
+            _ptr(copy), _ptr(copy_scale), _ptr(copy_amax), n, float(weight_decay), dtype, bits, 0))
+        self._keep.append([grad, master, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, copy, copy_scale,
                            copy_amax])
         self._array = None
-        self._set_grad(len(self._rows) - 1, self._rows[-1], grad)
 
-    def _set_grad(self, i: int, row, grad: torch.Tensor) -> None:
-        if grad.numel() != row.n or not grad.is_contiguous():
-            raise Fp8mpError(ERR_INVALID, f"gradient {i} must be dense with {row.n} elements")
-        row.grad, row.grad_dtype = grad.data_ptr(), _dtype_code(grad)
-        self._keep[i][0] = grad
+    @staticmethod
+    def _checked(i: int, n: int, grad: torch.Tensor) -> int:
+        """The type of a gradient that fits row i."""
+        if grad.numel() != n or not grad.is_contiguous():
+            raise Fp8mpError(ERR_INVALID, f"gradient {i} must be dense with {n} elements")
+        return _dtype_code(grad)
 
     def set_grads(self, grads) -> None:
         """This step's gradients, one for each tensor, in the order of add."""
@@ -600,8 +601,10 @@ class AdamWTensors:
         if len(grads) != len(self._rows):
             raise Fp8mpError(ERR_INVALID, f"{len(grads)} gradients for {len(self._rows)} tensors")
         rows = self.c_array()
+        dtypes = [self._checked(i, rows[i].n, g) for i, g in enumerate(grads)]
         for i, g in enumerate(grads):
-            self._set_grad(i, rows[i], g)
+            rows[i].grad, rows[i].grad_dtype = g.data_ptr(), dtypes[i]
+            self._keep[i][0] = g
 
     def c_array(self):
         if self._array is None:

@@ -97,3 +97,21 @@ def test_binding_checks_shapes_and_types():
         plan.set_grads([z(300)])
     with pytest.raises(fp8mp.Fp8mpError):
         plan.set_grads([z(300), z(301)])
+
+
+def test_a_refused_call_leaves_the_plan_as_it_was():
+    z = torch.zeros
+    plan = fp8mp.AdamWTensors()
+    first, second = z(300), z(200)
+    plan.add(first)
+    for bad in (z(300, dtype=torch.float16), z(600)[::2]):
+        with pytest.raises((TypeError, fp8mp.Fp8mpError)):
+            plan.add(bad)
+        assert len(plan) == 1
+    plan.add(second)
+    before = [(r.grad, r.grad_dtype, r.n) for r in plan.c_array()]
+    assert before == [(first.data_ptr(), fp8mp.F32, 300), (second.data_ptr(), fp8mp.F32, 200)]
+    for bad in (z(201), z(200, dtype=torch.float16), z(400)[::2]):
+        with pytest.raises((TypeError, fp8mp.Fp8mpError)):
+            plan.set_grads([z(300, dtype=torch.bfloat16), bad])
+        assert [(r.grad, r.grad_dtype, r.n) for r in plan.c_array()] == before
