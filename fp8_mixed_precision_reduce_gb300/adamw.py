@@ -46,6 +46,9 @@ class AdamW:
         for p in self.params:
             if p.dtype != torch.float32 or not p.is_contiguous() or p.device != dev:
                 raise ValueError("AdamW needs dense fp32 parameters on one device")
+        spans = sorted((p.data_ptr(), p.data_ptr() + 4 * p.numel()) for p in self.params if p.numel() > 0)
+        if any(end > start for (_, end), (start, _) in zip(spans, spans[1:])):
+            raise ValueError("AdamW was given a parameter, or a part of its memory, twice")
         self.modules = list(modules)
         self.state = []
         for p in self.params:

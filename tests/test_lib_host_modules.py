@@ -209,3 +209,22 @@ def test_a_parameter_that_is_no_longer_dense_is_refused(plain):
     p.data = p.data.t()
     with pytest.raises(ValueError, match="dense"):
         step(opt)
+
+
+# ------------------------------------------------------------------- AdamW
+
+
+def test_a_parameter_given_twice_is_refused():
+    """(Two rows of one launch would update the same memory.)"""
+    p = torch.nn.Parameter(torch.zeros(8, 8))
+    q = torch.nn.Parameter(torch.zeros(8))
+    with pytest.raises(ValueError, match="twice"):
+        adamw.AdamW([p, q, p], lr=1e-3)
+    tied = torch.nn.Parameter(p.data)
+    with pytest.raises(ValueError, match="twice"):
+        adamw.AdamW([p, q, tied], lr=1e-3)
+    with pytest.raises(ValueError, match="twice"):
+        adamw.AdamW([torch.nn.Parameter(p.data.view(-1)[16:48]), p], lr=1e-3)
+    empty = [torch.nn.Parameter(torch.zeros(0)) for _ in range(2)]
+    flat = torch.zeros(64)
+    adamw.AdamW([*empty, *(torch.nn.Parameter(flat[i:i + 16]) for i in range(0, 64, 16))], lr=1e-3)
