@@ -125,13 +125,14 @@ class AdamW:
     def load_state_dict(self, saved: dict) -> None:
         if len(saved["state"]) != len(self.state):
             raise ValueError(f"{len(saved['state'])} saved states for {len(self.state)} parameters")
-        for mine, s in zip(self.state, saved["state"]):
+        scalars = {k: getattr(self, k) for k in self._SCALARS}
+        pairs = [*zip(self.state, saved["state"]), (scalars, {k: saved["scalars"][k] for k in self._SCALARS})]
+        for mine, s in pairs:
             if {k: (v.dtype, v.shape) for k, v in mine.items()} != {k: (v.dtype, v.shape) for k, v in s.items()}:
                 raise ValueError("a saved state has other types or sizes than its parameter's")
+        for mine, s in pairs:
             for k, v in s.items():
                 mine[k].copy_(v)
-        for k in self._SCALARS:
-            getattr(self, k).copy_(saved["scalars"][k])
 
     def zero_grad(self) -> None:
         for p in self.params:

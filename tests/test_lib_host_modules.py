@@ -228,3 +228,19 @@ def test_a_parameter_given_twice_is_refused():
     empty = [torch.nn.Parameter(torch.zeros(0)) for _ in range(2)]
     flat = torch.zeros(64)
     adamw.AdamW([*empty, *(torch.nn.Parameter(flat[i:i + 16]) for i in range(0, 64, 16))], lr=1e-3)
+
+
+def test_a_state_that_does_not_fit_is_not_loaded_in_part():
+    make = lambda *shapes: adamw.AdamW([torch.nn.Parameter(torch.ones(s)) for s in shapes], lr=1e-3)  # noqa: E731
+    saved = make((8, 8), (4, 4)).state_dict()
+    for s in saved["state"]:
+        s["exp_avg"].fill_(3.0)
+    for bad in (make((8, 8), (4, 5)), make((8, 8), (4, 4))):
+        if bad.params[1].numel() == 16:
+            saved["scalars"]["loss_scale"] = torch.ones(2)
+        before = bad.state_dict()
+        with pytest.raises(ValueError):
+            bad.load_state_dict(saved)
+        after = bad.state_dict()
+        assert all(torch.equal(a[k], b[k]) for a, b in zip(before["state"], after["state"]) for k in a)
+        assert all(torch.equal(v, after["scalars"][k]) for k, v in before["scalars"].items())
