@@ -2,6 +2,7 @@
 // include/fp8mp.h: argument validation, device check, error reporting, and
 // dispatch to the kernels' launchers. No computation happens here.
 #include <atomic>
+#include <cfloat>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -969,7 +970,7 @@ int mp_adamw_step(const fp8mp_adamw_tensor *tensors, int32_t n_tensors, float *l
     CHECK_SCALAR(grad_norm, false);
     REQUIRE(grad_norm == nullptr || max_norm > 0.0f, "%s: clipping needs max_norm > 0", fn);
     REQUIRE(beta1 >= 0.0f && beta1 < 1.0f && beta2 >= 0.0f && beta2 < 1.0f, "%s: betas must lie in [0, 1)", fn);
-    REQUIRE(eps > 0.0f, "%s: eps must be > 0", fn);
+    REQUIRE(eps >= FLT_MIN, "%s: eps must be a normal number > 0", fn);
     REQUIRE(growth_interval >= 1, "%s: growth_interval must be >= 1", fn);
     DeviceInfo dev;
     rc = current_device(&dev);

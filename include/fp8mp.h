@@ -786,7 +786,7 @@ int mp_grad_norm(const fp8mp_adamw_tensor *tensors, int32_t n_tensors, float *no
  * seed        device uint32, required when a tensor has 8-bit moments.
  * grad_norm   device float (mp_grad_norm's) or NULL for no clipping;
  *             max_norm > 0 with it.
- * beta1, beta2 in [0, 1), eps > 0, growth_interval >= 1.
+ * beta1, beta2 in [0, 1), eps >= 2^-126, growth_interval >= 1.
  */
 int mp_adamw_step(const fp8mp_adamw_tensor *tensors, int32_t n_tensors, float *loss_scale, int32_t *growth_tracker,
                   const int32_t *found_inf, float *beta_pows, uint32_t *seed, const float *grad_norm, float max_norm,

@@ -115,3 +115,11 @@ def test_a_refused_call_leaves_the_plan_as_it_was():
         with pytest.raises((TypeError, fp8mp.Fp8mpError)):
             plan.set_grads([z(300, dtype=torch.bfloat16), bad])
         assert [(r.grad, r.grad_dtype, r.n) for r in plan.c_array()] == before
+
+
+@pytest.mark.parametrize("eps", [1e-45, 1e-40, 2.0 ** -126 * (1 - 2.0 ** -23), -1e-8])
+def test_an_eps_without_a_reciprocal_is_refused(lib, eps):
+    """The steps with 8-bit moments divide by flushing reciprocals: 0 / eps has to
+    be 0 where a moment is."""
+    assert step(lib, [row()], eps=eps) == fp8mp.ERR_INVALID
+    assert "eps" in fp8mp.last_error(), fp8mp.last_error()
