@@ -48,6 +48,7 @@
 // device flag that fp8mp_check() reports, tells the other roles of its CTA
 // to stop, waits (bounded) for its own copies / MMAs in flight, and the CTA
 // frees its TMEM and returns.
+#include <algorithm>
 #include <atomic>
 #include <cstdlib>
 #include <cstring>
@@ -682,17 +683,26 @@ int prepare_engine(const DeviceInfo &dev) {
 }
 
 // How the tiles are dealt. Where problem 0's long tiles are fewer than the
-// clusters, the serpentine gives some of their clusters a short tile as well;
-// if the others can take all the short ones in the time of one long tile, they
-// do. (The backward of 2 x 2736 outputs from 1040 inputs, 1237 tokens: 25 tiles
-// of 43 k-blocks and 110 of 10 on 76 pairs, gate pass included 32.6 us, 36.0
-// by the serpentine. Larger launches have more long tiles than clusters.)
+// clusters, the serpentine gives some of their clusters short tiles as well; where
+// the others can take all the short ones in about the time of one long tile, they
+// may. By the cost of each in k-blocks, a tile costing kTileFloor of them at least
+// (its epilogue, 4.1 us against 0.28 us per k-block): the larger of a long tile and
+// a cluster's short ones against a long tile and a short one in every other round.
+// Backward, tokens x outputs x inputs, us so and by the serpentine: 1232 x 5472 x
+// 1040 20.5, 24.5; 128 x 11264 x 2048 30.7, 47.5; 2048 x 65536 x 1024 152, 217. The
+// other way: 128 x 2048 x 12800 72.5, 33.5; 512 x 28672 x 4096 177, 172. (8 instead
+// of 16: 5-9 % slower than the serpentine for 512 tokens and 4096 inputs; 24: 20-30 %
+// lost for 5632 or 14336 outputs. fp32 and bf16 outputs alike.)
+constexpr int kTileFloor = 16;
 void deal_tiles(GemmBatch &b, int clusters) {
     b.own = 0;
     if (b.nprob < 2 || b.tiles0 >= clusters || b.num_tiles <= clusters) return;
-    const int n0 = b.tiles0, n1 = b.num_tiles - n0;
-    const int others = clusters - n0, each = (n1 + others - 1) / others;
-    if (static_cast<int64_t>(each) * b.prob[1].p.num_kb <= b.prob[0].p.num_kb) b.own = n0;
+    const int64_t n0 = b.tiles0, n1 = b.num_tiles - n0, others = clusters - n0, each = (n1 + others - 1) / others;
+    const int64_t rounds = (b.num_tiles + static_cast<int64_t>(clusters) - 1) / clusters;
+    const int64_t kb0 = b.prob[0].p.num_kb, kb1 = b.prob[1].p.num_kb;
+    const int64_t cost0 = std::max<int64_t>(kb0, kTileFloor), cost1 = std::max<int64_t>(kb1, kTileFloor);
+    if (each * kb1 <= kb0 && std::max(cost0, each * cost1) < cost0 + (rounds - 1) * cost1)
+        b.own = static_cast<int>(n0);
 }
 
 }  // namespace

@@ -370,3 +370,37 @@ def test_metric_shape_full_size_sampled(cuda_lib, orc):
     assert cuda_lib.fp8mp_check() == 0
     assert torch.equal(dx1.view(torch.int16), dx.view(torch.int16))
     assert torch.equal(dw1.view(torch.int16), dw.view(torch.int16))
+
+
+@pytest.mark.parametrize("M,N,K", [(128, 2048, 12800), (16, 4096, 12800), (256, 8192, 8192), (128, 11264, 2048)])
+def test_both_gradients_take_no_longer_than_one_after_the_other(cuda_lib, M, N, K):
+    """One launch of dX and dW against a launch for each, by device time: the same
+    tiles and one start instead of two, so a quarter more is what unlucky dealing
+    of the tiles may cost."""
+    codes = lambda r, c: torch.randint(0, 100, (r, c), device="cuda", dtype=torch.uint8)  # noqa: E731
+    dy, w, x, one = codes(M, N), codes(N, K), codes(M, K), sc(1.0)
+    dx, dw = (torch.empty(s, dtype=torch.bfloat16, device="cuda") for s in ((M, K), (N, K)))
+
+    def microseconds(*calls):
+        def run():
+            for gx, gw in calls:
+                cuda_lib.fp8_linear_bwd_rowmajor(dy, w, x, one, one, one, gx, gw)
+
+        for _ in range(3):
+            run()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(10):
+                run()
+        times = []
+        for _ in range(9):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            graph.replay()
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b) * 100)
+        return sorted(times)[4]
+
+    together, apart = microseconds((dx, dw)), microseconds((dx, None), (None, dw))
+    assert together <= 1.25 * apart, (together, apart)
