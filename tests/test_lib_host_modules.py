@@ -244,3 +244,18 @@ def test_a_state_that_does_not_fit_is_not_loaded_in_part():
         after = bad.state_dict()
         assert all(torch.equal(a[k], b[k]) for a, b in zip(before["state"], after["state"]) for k in a)
         assert all(torch.equal(v, after["scalars"][k]) for k, v in before["scalars"].items())
+
+
+# ----------------------------------------------------------------- binding
+
+
+def test_the_current_stream_without_torchs_raw_call(monkeypatch):
+    class Stream:
+        cuda_stream = 77
+
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: Stream())
+    for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"):
+        with monkeypatch.context() as m:
+            m.delattr(torch._C, name, raising=False)
+            assert fp8mp._stream(None) == 77
+    assert fp8mp._stream(5) == 5 and fp8mp._stream(Stream()) == 77
