@@ -53,8 +53,9 @@ enum Mode { FWD = 0, DGRAD = 1 };
 // registers, each lane a row, in whole 32-byte sectors; shared memory is left to
 // the operand ring, whose depth counts for more (16384 x 4096 -> 14336: 1085 us
 // with 7 stages for a pair; 1156 with 5 and staging boxes for TMA stores, 1217
-// with 4). With a relaxed arrival on the accumulators' barrier it is 1055-1069 us,
-// 3.6 PFLOP/s; the plain GEMM of that size takes 1030-1056.
+// with 4). Now 1045-1064 us where the board's power allows it, 3.6 PFLOP/s; the plain
+// GEMM of that size takes 1030-1056. (A relaxed arrival on the accumulators' barrier
+// is level with the release there: 1045-1064 us both, three runs each in turn.)
 //
 // Dgrad: the epilogue does more per element and waits for g and u, which come
 // from DRAM; a warp alone on its scheduler is too slow for that (371-386 us for
@@ -114,14 +115,6 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
                  : "r"(addr)
                  : "memory");
     return v;
-}
-
-// Arrive on a barrier of the cluster without ordering this thread's earlier
-// writes: what it signals is that tensor memory has been read, which
-// tcgen05.wait::ld has already waited for. A release here would hold the epilogue
-// until its global stores have been performed.
-__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // 32 bytes to a 32-byte boundary in one store.
@@ -477,7 +470,7 @@ __global__ void __launch_bounds__(Cfg<PAIR, MODE>::THREADS, 1) gated_kernel(cons
             __syncwarp();
             if (lane == 0) {
                 if constexpr (PAIR)
-                    mbar_arrive_cluster_relaxed(mapa_shared(tempty_bar(acc), 0));  // the MMA issuer's barrier
+                    mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0));  // the MMA issuer's barrier
                 else
                     mbar_arrive(tempty_bar(acc));
             }
