@@ -70,6 +70,7 @@ LR, MU, S0 = 1e-4, 0.9, 2.0 ** 16
 METRIC = "FP8 linear fwd+bwd TFLOP/s at M=8192,K=N=4096; % of GB300 dense FP8 peak"
 WORKLOAD = "transformer proj linear 4096->4096, M=8192 tokens (seq 2048 x batch 4), bf16 in, FP8 HYBRID delayed scaling"
 GEMM_SRC = os.path.join(ROOT, "fp8_mixed_precision_reduce_gb300", "csrc", "gemm.cu")
+GEMM_HEADERS = ("fp8mp_mma.cuh", "fp8mp_async.cuh")  # beside it: the kernel's TMA, MMA and raster code
 TRAFFIC = os.path.join(ROOT, "profiles", "gemm_fp8_kernel_dram_bytes.json")
 FALLBACK_BF16_TFLOPS = 1900.0
 FP8_OVER_BF16 = 4.5 / 2.25  # nominal dense ratio
@@ -93,15 +94,21 @@ def load_peaks():
 
 
 def gemm_source_sha256() -> str:
-    with open(GEMM_SRC, "rb") as f:
-        return hashlib.sha256(f.read()).hexdigest()
+    """Of gemm.cu and the headers that hold the rest of its kernel."""
+    h = hashlib.sha256()
+    for path in (GEMM_SRC, *(os.path.join(os.path.dirname(GEMM_SRC), name) for name in GEMM_HEADERS)):
+        if os.path.exists(path):
+            with open(path, "rb") as f:
+                h.update(f.read())
+    return h.hexdigest()
 
 
 def gemm_traffic(label=None):
     """DRAM bytes (read + write) per GEMM launch from the ncu capture that
     `--ingest-ncu` recorded: the launch labelled `label` ("fwd", "bwd"), or
     the mean over both when None. None when there is no record or it was
-    taken on another gemm.cu (its sha256 is stored with the numbers)."""
+    taken on other sources of the kernel (their sha256 is stored with the
+    numbers)."""
     try:
         with open(TRAFFIC) as f:
             rec = json.load(f)
@@ -173,7 +180,7 @@ def parse_ncu_dram_csv(path, kernel="gemm_fp8_kernel", labels=("fwd", "bwd")):
 
 def ingest_ncu(csv_path, command, out_path=None):
     """Writes the GEMM launches' DRAM bytes from an ncu CSV export, keyed by
-    the sha256 of the gemm.cu they were captured on, for the bench line's
+    the sha256 of the sources (gemm_source_sha256) they were captured on, for the bench line's
     roofline.traffic."""
     by, per_launch = parse_ncu_dram_csv(csv_path)
     if not by:

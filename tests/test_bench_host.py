@@ -88,6 +88,22 @@ def test_traffic_lookup_is_keyed_to_the_gemm_source(tmp_path, monkeypatch):
     assert bench.gemm_traffic() is None
 
 
+@pytest.mark.parametrize("header", ["fp8mp_mma.cuh", "fp8mp_async.cuh"])
+def test_traffic_lookup_is_keyed_to_the_gemm_headers(tmp_path, monkeypatch, header):
+    csrc = os.path.dirname(bench.GEMM_SRC)
+    for name in ("gemm.cu", "fp8mp_mma.cuh", "fp8mp_async.cuh"):
+        with open(os.path.join(csrc, name), "rb") as f:
+            (tmp_path / name).write_bytes(f.read())
+    monkeypatch.setattr(bench, "GEMM_SRC", str(tmp_path / "gemm.cu"))
+    monkeypatch.setattr(bench, "TRAFFIC", str(tmp_path / "traffic.json"))
+    rec = {"gemm_cu_sha256": bench.gemm_source_sha256(), "dram_bytes_per_launch": {"fwd": 100.0}}
+    (tmp_path / "traffic.json").write_text(json.dumps(rec))
+    assert bench.gemm_traffic("fwd") == 100.0
+    with open(tmp_path / header, "a") as f:
+        f.write("// changed")
+    assert bench.gemm_traffic("fwd") is None
+
+
 RAW_CSV = """"ID","Process ID","Kernel Name","dram__bytes_read.sum","dram__bytes_write.sum","gpu__time_duration.sum"
 "","","","Mbyte","Kbyte","us"
 "0","7","void fp8mp::gemm_fp8_kernel<1>(fp8mp::Params)","59.25","31,600.5","78.0"
