@@ -155,10 +155,10 @@ def _ptr(t) -> int | None:
 
 def _stream(stream) -> int | None:
     if stream is None:  # the current device's current stream
-        raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
-        if raw is None or device is None:  # (not torch's public calls, but 3 us faster)
+        try:  # (not torch's public calls, but 3 us faster)
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        except AttributeError:
             return torch.cuda.current_stream().cuda_stream
-        return raw(device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -551,7 +551,7 @@ class AdamWTensors:
     given; set_grads replaces the gradients when a step has new ones."""
 
     def __init__(self):
-        self._rows, self._keep, self._array = [], [], None
+        self._rows, self._keep, self._sizes, self._array = [], [], [], None
 
     def __len__(self) -> int:
         return len(self._rows)
@@ -589,6 +589,7 @@ class AdamWTensors:
             _ptr(copy), _ptr(copy_scale), _ptr(copy_amax), n, float(weight_decay), dtype, bits, 0))
         self._keep.append([grad, master, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, copy, copy_scale,
                            copy_amax])
+        self._sizes.append(n)
         self._array = None
 
     @staticmethod
@@ -603,11 +604,11 @@ class AdamWTensors:
         grads = list(grads)
         if len(grads) != len(self._rows):
             raise Fp8mpError(ERR_INVALID, f"{len(grads)} gradients for {len(self._rows)} tensors")
-        rows = self.c_array()
-        dtypes = [self._checked(i, rows[i].n, g) for i, g in enumerate(grads)]
-        for i, g in enumerate(grads):
-            rows[i].grad, rows[i].grad_dtype = g.data_ptr(), dtypes[i]
-            self._keep[i][0] = g
+        self.c_array()
+        dtypes = [self._checked(i, n, g) for i, (n, g) in enumerate(zip(self._sizes, grads))]
+        for row, keep, g, dtype in zip(self._rows, self._keep, grads, dtypes):
+            row.grad, row.grad_dtype = g.data_ptr(), dtype
+            keep[0] = g
 
     def c_array(self):
         if self._array is None:

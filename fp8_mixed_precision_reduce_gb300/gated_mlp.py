@@ -32,32 +32,44 @@ def _rows16(rows: int, cols: int, dtype: torch.dtype, device) -> torch.Tensor:
     return t
 
 
-class _CastOf:
-    """Which state of a weight a copy is of, and when it is there. The weight's
+class _CopyState:
+    """Which state of a weight its copy is of, and when it is there. The weight's
     array is kept alive, so that another one under the same parameter (.data =
     ..., which leaves the version as it is) cannot have its address."""
 
-    def __init__(self, w: torch.Tensor):
-        self.version, self.array = w._version, w.detach()
-        self.streams, self.written = set(), None
-        if w.is_cuda:
-            self.streams.add(_stream(None))
-            self.written = torch.cuda.Event()
-            self.written.record()
+    def __init__(self):
+        self.version = self.array = self.event = None
+        self.streams, self.wait = (), False  # those that the copy is there for; whether others wait for the event
 
     def __reduce__(self):  # a copy of the module casts its own
-        return type(None), ()
+        return _CopyState, ()
+
+    def note(self, w: torch.Tensor, cast: bool) -> None:
+        """What has been enqueued on the current stream makes the copy w's: a cast,
+        which only this module knows of, or a step, which its caller orders before
+        the weight's uses."""
+        self.version, self.array, self.wait = w._version, w.detach(), cast
+        if w.is_cuda:
+            self.streams = {_stream(None)}
+            if cast:
+                self.event = self.event or torch.cuda.Event()
+                self.event.record()
+
+    def forget(self) -> None:
+        self.array = None
 
     def is_current(self, w: torch.Tensor) -> bool:
-        return self.version == w._version and self.array.dtype == w.dtype and self.array.is_set_to(w)
+        a = self.array
+        return a is not None and self.version == w._version and a.dtype == w.dtype and a.is_set_to(w)
 
     def use(self, copy: torch.Tensor) -> None:
-        """The copy is about to be read on the current stream: one that did not
-        write it waits for it, once, and keeps the array from being reused."""
-        if self.written is None or _stream(None) in self.streams:
+        """The copy is about to be read on the current stream, which is not among
+        `streams`: that one waits for its cast and keeps the array from being reused."""
+        if not copy.is_cuda:
             return
         stream = torch.cuda.current_stream()
-        stream.wait_event(self.written)
+        if self.wait:
+            stream.wait_event(self.event)
         copy.record_stream(stream)
         self.streams.add(stream.cuda_stream)
 
@@ -158,7 +170,7 @@ class FP8GatedMLP(torch.nn.Module):
         self.dw_nonfinite = torch.zeros(1, dtype=torch.int32, device=device)
         # of gate_up and of down: the E4M3 copy, and what it is of
         self._copies = [torch.empty(w.shape, dtype=torch.uint8, device=device) for w in (self.gate_up, self.down)]
-        self._cast_of = [None, None]
+        self._cast_of = [_CopyState(), _CopyState()]
         self._in_a_graph = [False, False]  # a captured graph reads the copy's array
         self._trains_in_a_graph = False  # replays change the weights and their scales unseen
 
@@ -173,26 +185,29 @@ class FP8GatedMLP(torch.nn.Module):
         not current. A capture casts them in the graph, but for a pass without
         gradients in eval mode: that graph reads the current ones, which every
         later cast then writes in place."""
+        capturing = _capturing(self.gate_up)
+        here = _stream(None) if self.gate_up.is_cuda else None
         for i, (w, m) in enumerate(self._weights()):
-            if w.shape != self._copies[i].shape or w.device != self._copies[i].device:
-                raise ValueError(f"a weight must stay {tuple(self._copies[i].shape)} on {self._copies[i].device}, got "
-                                 f"{tuple(w.shape)} on {w.device}")
-            current = self._cast_of[i] is not None and self._cast_of[i].is_current(w)
-            if _capturing(w):
+            w8, state = self._copies[i], self._cast_of[i]
+            current = state.is_current(w)
+            if capturing:
                 current = current and not for_training and not self.training
-                self._trains_in_a_graph |= for_training
-                self._in_a_graph[i] |= current
-            elif current:
-                self._cast_of[i].use(self._copies[i])
+                self._trains_in_a_graph = self._trains_in_a_graph or for_training
+                self._in_a_graph[i] = self._in_a_graph[i] or current
+            elif current and here not in state.streams:
+                state.use(w8)
             if not current:
+                if w.shape != w8.shape or w.device != w8.device:
+                    raise ValueError(f"a weight must stay {tuple(w8.shape)} on {w8.device}, got {tuple(w.shape)} on "
+                                     f"{w.device}")
                 # a new array, as a backward pass may still hold the last one; but a
                 # graph's stays (and a backward pass that holds it fails)
                 if self._in_a_graph[i]:
-                    torch.autograd.graph.increment_version(self._copies[i])
+                    torch.autograd.graph.increment_version(w8)
                 else:
-                    self._copies[i] = torch.empty_like(self._copies[i])
-                fp8_quantize(w.detach().contiguous(), E4M3, m.scale, self._copies[i], None, m.cur_amax)
-                self._note(i, w)
+                    w8 = self._copies[i] = torch.empty_like(w8)
+                fp8_quantize(w.detach().contiguous(), E4M3, m.scale, w8, None, m.cur_amax)
+                self._note(i, w, capturing, cast=True)
         return tuple(self._copies)
 
     def copies_for_step(self):
@@ -204,20 +219,26 @@ class FP8GatedMLP(torch.nn.Module):
         """The copies of `weights` (all, if None) are of the weights as they are
         now; the others are as current as they were. A backward pass that still
         needs the ones before fails, as after any change in place."""
+        capturing = _capturing(self.gate_up)
+        if capturing:
+            self._trains_in_a_graph = True
         for i, (w, _) in enumerate(self._weights()):
             if weights is None or any(w is x for x in weights):
                 torch.autograd.graph.increment_version(self._copies[i])
-                self._trains_in_a_graph |= _capturing(w)
-                self._note(i, w)
+                self._note(i, w, capturing, cast=False)
 
-    def _note(self, i: int, w: torch.Tensor) -> None:
+    def _note(self, i: int, w: torch.Tensor, capturing: bool, cast: bool) -> None:
         # (what a capture records has not run, and what its replays do is not seen)
-        self._cast_of[i] = None if self._trains_in_a_graph or _capturing(w) else _CastOf(w)
+        if capturing or self._trains_in_a_graph:
+            self._cast_of[i].forget()
+        else:
+            self._cast_of[i].note(w, cast)
 
     def weights_changed(self) -> None:
         """Cast the weights again before their next use (for changes that torch
         does not see; its own are noticed)."""
-        self._cast_of = [None, None]
+        for state in self._cast_of:
+            state.forget()
 
     def _apply(self, fn, *args, **kw):  # .to() and the like: the arrays before are let go
         self.weights_changed()
@@ -234,5 +255,6 @@ class FP8GatedMLP(torch.nn.Module):
         """Roll the amax histories and refresh the scales for the next step; the
         weights' copies, cast under the old ones, are not current after it."""
         delayed_scaling_update(self.metas(), self.algo, self.margin)
-        self._trains_in_a_graph |= _capturing(self.gate_up)
+        if _capturing(self.gate_up):
+            self._trains_in_a_graph = True
         self.weights_changed()
