@@ -450,7 +450,7 @@ int launch_few_linear(const uint8_t *x8, const uint8_t *w8, int64_t M, int64_t N
 int read_and_clear_few_timeout_flag(unsigned int *value) {
     unsigned int v = 0, zero = 0;
     cudaError_t e = cudaMemcpyFromSymbol(&v, g_few_timeout_flag, sizeof v);
-    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_few_timeout_flag, &zero, sizeof zero);
+    if (e == cudaSuccess && v != 0) e = cudaMemcpyToSymbol(g_few_timeout_flag, &zero, sizeof zero);
     if (e != cudaSuccess) return fail(FP8MP_ERR_LAUNCH, "reading the timeout flag failed: %s", cudaGetErrorString(e));
     *value = v;
     return FP8MP_OK;

@@ -803,7 +803,7 @@ int launch_gate_bwd(const void *dh, int dh_dtype, const uint16_t *gu, int64_t M,
 int read_and_clear_gated_timeout_flag(unsigned int *value) {
     unsigned int v = 0, zero = 0;
     cudaError_t e = cudaMemcpyFromSymbol(&v, g_gated_timeout_flag, sizeof v);
-    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_gated_timeout_flag, &zero, sizeof zero);
+    if (e == cudaSuccess && v != 0) e = cudaMemcpyToSymbol(g_gated_timeout_flag, &zero, sizeof zero);
     if (e != cudaSuccess) return fail(FP8MP_ERR_LAUNCH, "reading the timeout flag failed: %s", cudaGetErrorString(e));
     *value = v;
     return FP8MP_OK;

@@ -736,7 +736,7 @@ int launch_barrier_selftest(cudaStream_t s) {
 int read_and_clear_master_timeout_flag(unsigned int *value) {
     unsigned int v = 0, zero = 0;
     cudaError_t e = cudaMemcpyFromSymbol(&v, g_master_timeout_flag, sizeof v);
-    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_master_timeout_flag, &zero, sizeof zero);
+    if (e == cudaSuccess && v != 0) e = cudaMemcpyToSymbol(g_master_timeout_flag, &zero, sizeof zero);
     if (e != cudaSuccess) return fail(FP8MP_ERR_LAUNCH, "reading the timeout flag failed: %s", cudaGetErrorString(e));
     *value = v;
     return FP8MP_OK;

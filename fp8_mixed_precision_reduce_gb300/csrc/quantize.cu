@@ -1100,7 +1100,7 @@ int launch_quantize(const void *x, int x_dtype, int64_t rows, int64_t cols, int 
 int read_and_clear_cast_timeout_flag(unsigned int *value) {
     unsigned int v = 0, zero = 0;
     cudaError_t e = cudaMemcpyFromSymbol(&v, g_cast_timeout_flag, sizeof v);
-    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_cast_timeout_flag, &zero, sizeof zero);
+    if (e == cudaSuccess && v != 0) e = cudaMemcpyToSymbol(g_cast_timeout_flag, &zero, sizeof zero);
     if (e != cudaSuccess) return fail(FP8MP_ERR_LAUNCH, "reading the timeout flag failed: %s", cudaGetErrorString(e));
     *value = v;
     return FP8MP_OK;
