@@ -104,7 +104,10 @@ class AdamW:
                 raise ValueError(f"parameter {i} has no gradient")
             if not p.is_contiguous():
                 raise ValueError(f"parameter {i} is no longer dense")
-            grads.append(p.grad if p.grad.is_contiguous() else p.grad.contiguous())
+            g = p.grad
+            if not g.is_contiguous() or g.data_ptr() % 16:  # (the library reads dense rows of 16 bytes)
+                g = g.clone(memory_format=torch.contiguous_format)
+            grads.append(g)
         copies, written = self._copies()
         plan = self._tensors(grads, copies)
         mp_grad_norm(plan, self.grad_norm, self.found_inf, self.workspace)

@@ -259,3 +259,16 @@ def test_the_current_stream_without_torchs_raw_call(monkeypatch):
             m.delattr(torch._C, name, raising=False)
             assert fp8mp._stream(None) == 77
     assert fp8mp._stream(5) == 5 and fp8mp._stream(Stream()) == 77
+
+
+def test_gradients_at_any_address(plain, monkeypatch):
+    """Views into a flat buffer, after a tensor of odd size."""
+    params = [torch.nn.Parameter(torch.zeros(n)) for n in (5, 7, 16)]
+    flat = torch.arange(28.0)
+    for p, g in zip(params, flat.split([5, 7, 16])):
+        p.grad = g
+    seen = []
+    monkeypatch.setattr(adamw, "mp_grad_norm", lambda plan, *a: seen.extend(r.grad for r in plan.c_array()))
+    adamw.AdamW(params, lr=1.0, weight_decay=0.0).step()
+    assert all(address % 16 == 0 for address in seen) and len(seen) == 3
+    assert torch.equal(torch.cat([p.detach() for p in params]), -flat)
