@@ -277,6 +277,22 @@ def test_8_bit_moments_bit_for_bit(cuda_lib, grad, clip):
         assert np.array_equal(pows, np.float32(pows))
 
 
+@pytest.mark.parametrize("seed", [31, 2 ** 31 - 1, -1])
+def test_powers_and_seed_advance_with_every_step(cuda_lib, seed):
+    """Bit for bit; a skipped step leaves them."""
+    st = Step(cuda_lib, [Tensor(5000, 8, seed=1), Tensor(300, 32, seed=2)], max_norm=1e-3, seed=seed)
+    st.measure()
+    pows, want_seed = st.pows.cpu().numpy(), seed
+    for found in (0, 0, 1, 0):
+        st.found.fill_(found)
+        st.run()
+        if not found:
+            pows = pows * np.float32([st.b1, st.b2])
+            want_seed = (want_seed + 1 + 2 ** 31) % 2 ** 32 - 2 ** 31
+        assert_same_bits(st.pows.cpu().numpy(), pows, "powers")
+        assert st.seed.item() == want_seed
+
+
 def test_no_tensors_at_all(cuda_lib):
     st = Step(cuda_lib, [], growth=4)
     st.norm.fill_(7.0)
