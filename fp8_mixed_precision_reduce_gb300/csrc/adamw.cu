@@ -45,7 +45,7 @@ struct Workspace {
 
 // The tensor that chunk c belongs to: the last one with first[t] <= c (one without
 // chunks shares its `first` with the next). A walk over them instead loads a
-// constant for each: the norm and the step of 61 small tensors 9.4 us, 8.2 so.
+// constant for each: the step of 61 small tensors 9.4 us, 8.3 so.
 __device__ __forceinline__ int tensor_of(const int32_t *first, int count, int c) {
     int t = 0, end = count;
     while (end - t > 1) {

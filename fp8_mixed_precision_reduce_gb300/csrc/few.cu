@@ -8,9 +8,9 @@
 //   - the weights are the MMA's M operand (128 rows per tile; gated: 64 gate
 //     rows and the 64 up rows of the same outputs), the tokens its N operand
 //     (16 to 128 columns, rows past the last token zero-filled), so a stage
-//     is 16 KB of weights and 2-16 KB of tokens, in a ring of about 100 KB: two
+//     is 16 KB of weights and 2-16 KB of tokens, in a ring of 72 to 90 KB: two
 //     CTAs share an SM and one streams while the other starts or ends (128
-//     columns, whose sums alone take 64 KB, have an SM for each CTA);
+//     columns, whose sums alone take 64 KB, have an SM for each CTA, 160 KB);
 //   - a tile's contraction is split over the S CTAs of a cluster (split_for
 //     below). Each owns an S-th of the tile's outputs; all send it their fp32
 //     partial sums of those through distributed shared memory, and after one

@@ -7,9 +7,10 @@
 //                       = g / (1 + exp(-z)),   z = 2 s (g + c g^3),
 //                  s = sqrt(2 / pi), c = 0.044715
 // so with p = 1 / (1 + exp(-z)): act = g p, act' = p + g p (1 - p) z'(g).
-// exp2 and the reciprocal are the hardware's approximations (2 ulp each): the
-// results are rounded to bf16 or FP8 next, and the amax is good to 2^-20. The
-// rest is done on pairs.
+// exp2 and the reciprocal are the hardware's approximations (2 ulp each), the
+// exponent is rounded once: p is good to (4 + 1.2 |z|) 2^-23 of itself, which a
+// contraction's accumulation (1e-5 sum |a b|) hides. The results are rounded to bf16
+// or FP8 next; the amax has that error and no other. The rest is done on pairs.
 #pragma once
 
 #include "fp8mp_f32x2.cuh"

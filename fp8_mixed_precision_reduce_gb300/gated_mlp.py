@@ -166,7 +166,8 @@ class FP8GatedMLP(torch.nn.Module):
         self.meta_x, self.meta_gate_up = Meta(history_len, E4M3, device), Meta(history_len, E4M3, device)
         self.meta_h, self.meta_down = Meta(history_len, E4M3, device), Meta(history_len, E4M3, device)
         self.meta_dy, self.meta_dgu = Meta(history_len, E5M2, device), Meta(history_len, E5M2, device)
-        # 1 once a weight gradient held an Inf or NaN
+        # 1 once a weight gradient held an Inf or NaN, until its reader clears it
+        # (AdamW finds the step's by its own pass over the gradients)
         self.dw_nonfinite = torch.zeros(1, dtype=torch.int32, device=device)
         # of gate_up and of down: the E4M3 copy, and what it is of
         self._copies = [torch.empty(w.shape, dtype=torch.uint8, device=device) for w in (self.gate_up, self.down)]
@@ -235,8 +236,8 @@ class FP8GatedMLP(torch.nn.Module):
             self._cast_of[i].note(w, cast)
 
     def weights_changed(self) -> None:
-        """Cast the weights again before their next use (for changes that torch
-        does not see; its own are noticed)."""
+        """Cast the weights again before their next use: for changes that torch does
+        not see, as through .data or a pointer; its own are noticed."""
         for state in self._cast_of:
             state.forget()
 

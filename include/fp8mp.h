@@ -781,7 +781,7 @@ int mp_grad_norm(const fp8mp_adamw_tensor *tensors, int32_t n_tensors, float *no
  * tensors     HOST array, read during the call only; tensors with n == 0 count
  *             in t but are skipped.
  * found_inf   device int32 (mp_grad_norm's, or a backward launch's
- *             dw_nonfinite), read only.
+ *             dw_nonfinite, which the caller then clears), read only.
  * beta_pows   device float[2], (beta1^(t-1), beta2^(t-1)); 1 at first.
  * seed        device uint32, required when a tensor has 8-bit moments.
  * grad_norm   device float (mp_grad_norm's) or NULL for no clipping;
