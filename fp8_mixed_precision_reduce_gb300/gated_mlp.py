@@ -206,7 +206,8 @@ class FP8GatedMLP(torch.nn.Module):
                 if self._in_a_graph[i]:
                     torch.autograd.graph.increment_version(w8)
                 else:
-                    w8 = self._copies[i] = torch.empty_like(w8)
+                    with torch.inference_mode(False):  # (an evaluation's copy serves training too)
+                        w8 = self._copies[i] = torch.empty_like(w8)
                 fp8_quantize(w.detach().contiguous(), E4M3, m.scale, w8, None, m.cur_amax)
                 self._note(i, w, capturing, cast=True)
         return tuple(self._copies)

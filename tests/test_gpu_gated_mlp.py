@@ -398,6 +398,18 @@ def test_second_derivatives_are_refused(cuda_lib, kind):
     assert torch.equal(again, g) and not again.requires_grad
 
 
+def test_training_after_an_evaluation_in_inference_mode(cuda_lib):
+    from fp8_mixed_precision_reduce_gb300.gated_mlp import FP8GatedMLP
+
+    mlp = FP8GatedMLP(64, 96)
+    x = torch.randn((32, 64), device="cuda")
+    with torch.inference_mode():
+        y = mlp(x)
+    z = mlp(x)
+    z.sum().backward()
+    assert torch.equal(y, z) and torch.isfinite(mlp.down.grad).all()
+
+
 def test_copies_of_a_module(cuda_lib):
     import copy
     import io

@@ -272,3 +272,13 @@ def test_gradients_at_any_address(plain, monkeypatch):
     adamw.AdamW(params, lr=1.0, weight_decay=0.0).step()
     assert all(address % 16 == 0 for address in seen) and len(seen) == 3
     assert torch.equal(torch.cat([p.detach() for p in params]), -flat)
+
+
+def test_copies_cast_in_inference_mode_serve_training_too(plain):
+    mlp = block()
+    with torch.inference_mode():
+        mlp.weight_copies()
+    opt = adamw.AdamW(mlp.parameters(), lr=1e-2, modules=[mlp])
+    assert not any(c.is_inference() for c in mlp.weight_copies())
+    step(opt, mlp)
+    assert copies_are_current(mlp)
