@@ -548,10 +548,11 @@ def fp8_gated_bwd(dh: torch.Tensor | None, gu: torch.Tensor | None, x8: torch.Te
 class AdamWTensors:
     """The tensors of mp_grad_norm and mp_adamw_step: add each one once, keep
     the object over the steps. It holds references to every tensor it was
-    given; set_grads replaces the gradients when a step has new ones."""
+    given; set_grads replaces the gradients when a step has new ones, and
+    release_grads lets go of them in between."""
 
     def __init__(self):
-        self._rows, self._keep, self._sizes, self._array = [], [], [], None
+        self._rows, self._keep, self._sizes, self._array, self._released = [], [], [], None, False
 
     def __len__(self) -> int:
         return len(self._rows)
@@ -604,13 +605,25 @@ class AdamWTensors:
         grads = list(grads)
         if len(grads) != len(self._rows):
             raise Fp8mpError(ERR_INVALID, f"{len(grads)} gradients for {len(self._rows)} tensors")
-        self.c_array()
+        self._rows_array()
         dtypes = [self._checked(i, n, g) for i, (n, g) in enumerate(zip(self._sizes, grads))]
         for row, keep, g, dtype in zip(self._rows, self._keep, grads, dtypes):
             row.grad, row.grad_dtype = g.data_ptr(), dtype
             keep[0] = g
+        self._released = False
+
+    def release_grads(self) -> None:
+        """Lets go of the gradients: set_grads has to give new ones before the next call."""
+        for keep in self._keep:
+            keep[0] = None
+        self._released = bool(self._keep)
 
     def c_array(self):
+        if self._released:
+            raise Fp8mpError(ERR_INVALID, "the gradients were released: set_grads first")
+        return self._rows_array()
+
+    def _rows_array(self):
         if self._array is None:
             self._array = (fp8mp_adamw_tensor * max(1, len(self._rows)))(*self._rows)
             self._rows = [self._array[i] for i in range(len(self._rows))]

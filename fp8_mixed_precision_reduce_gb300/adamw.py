@@ -115,6 +115,7 @@ class AdamW:
                       lr=self.lr, beta1=self.betas[0], beta2=self.betas[1], eps=self.eps, seed=self.seed,
                       grad_norm=self.grad_norm if self.max_norm > 0 else None, max_norm=self.max_norm,
                       growth_interval=self.growth_interval)
+        plan.release_grads()
         torch.autograd.graph.increment_version(self.params)
         for mod, weights in written:
             mod.copies_written(weights)

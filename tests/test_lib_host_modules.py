@@ -1,6 +1,9 @@
 """FP8GatedMLP, FP8Linear and AdamW around the library's calls, without a GPU:
 on CPU tensors, with the calls they make replaced by plain torch operations."""
 
+import gc
+import weakref
+
 import pytest
 import torch
 
@@ -282,3 +285,26 @@ def test_copies_cast_in_inference_mode_serve_training_too(plain):
     assert not any(c.is_inference() for c in mlp.weight_copies())
     step(opt, mlp)
     assert copies_are_current(mlp)
+
+
+def test_a_step_lets_its_gradients_go(plain):
+    p = torch.nn.Parameter(torch.zeros(8, 8))
+    opt = adamw.AdamW([p], lr=1e-2)
+    for _ in range(2):
+        p.grad = torch.ones(8, 8)
+        grad = weakref.ref(p.grad)
+        opt.step()
+        opt.zero_grad()
+        gc.collect()
+        assert grad() is None
+
+
+def test_a_plan_without_its_gradients_is_refused():
+    plan = fp8mp.AdamWTensors()
+    plan.add(torch.zeros(300))
+    plan.release_grads()
+    with pytest.raises(fp8mp.Fp8mpError, match="set_grads"):
+        plan.c_array()
+    g = torch.zeros(300)
+    plan.set_grads([g])
+    assert plan.c_array()[0].grad == g.data_ptr()
