@@ -149,6 +149,10 @@ class FP8Linear(torch.nn.Module):
         if x.dim() == 0 or x.shape[-1] != self.in_features or x.device != self.meta_x.scale.device:
             raise ValueError(f"x must be [..., {self.in_features}] on {self.meta_x.scale.device}, got {tuple(x.shape)} on "
                              f"{x.device}")
+        for name, t, shape in (("weight", self.weight, (self.out_features, self.in_features)),
+                               ("bias", self.bias, (self.out_features,))):
+            if t is not None and (t.shape != shape or t.device != x.device):
+                raise ValueError(f"{name} must be {shape} on {x.device}, got {tuple(t.shape)} on {t.device}")
         return _FP8LinearFn.apply(x, self.weight, self.bias, self)
 
     def update_scales(self) -> None:

@@ -308,3 +308,16 @@ def test_a_plan_without_its_gradients_is_refused():
     g = torch.zeros(300)
     plan.set_grads([g])
     assert plan.c_array()[0].grad == g.data_ptr()
+
+
+def test_a_linear_refuses_a_weight_or_bias_of_another_shape():
+    x = torch.zeros((16, 32))
+    for name, other in (("weight", torch.zeros((48, 64))), ("weight", torch.zeros((32, 32))), ("bias", torch.zeros(16))):
+        layer = linear.FP8Linear(32, 48, device="cpu")
+        getattr(layer, name).data = other
+        with pytest.raises(ValueError, match=name):
+            layer(x)
+    layer = linear.FP8Linear(32, 48, device="cpu")
+    layer.weight = torch.nn.Parameter(layer.weight.to("meta"))
+    with pytest.raises(ValueError, match="weight"):
+        layer(x)
