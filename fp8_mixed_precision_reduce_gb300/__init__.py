@@ -32,6 +32,8 @@ EXPORTS = ("fp8_quantize", "fp8_quantize_ex", "fp8_quantize_current", "fp8_quant
            "mp_master_step_prescanned_ex", "mp_master_step_adam_prescanned_ex",
            "mp_master_step_prescanned_scaling_ex", "mp_master_step_adam_prescanned_scaling_ex", "fp8_gated_fwd", "fp8_linear_few", "fp8_gated_dgrad", "fp8_gated_bwd",
            "mp_adamw_workspace_bytes", "mp_grad_norm", "mp_adamw_step",
+           "fp8_rmsnorm_fwd", "fp8_rmsnorm_bwd", "fp8_rmsnorm_bwd_workspace_bytes", "mp_logprobs_fwd", "mp_logprobs_bwd",
+           "mp_embedding_fwd", "mp_embedding_bwd", "mp_embedding_bwd_workspace_bytes",
            "fp8mp_check", "fp8mp_last_error",
            "fp8mp_version", "fp8mp_selftest_timeout", "fp8mp_selftest_barrier_timeout")
 
@@ -122,6 +124,19 @@ def load(path: str | None = None):
     L.mp_grad_norm.restype = ctypes.c_int
     L.mp_adamw_step.argtypes = [A, I32, P, P, P, P, P, P, F, F, F, F, F, F, F, I32, P, I64, P]
     L.mp_adamw_step.restype = ctypes.c_int
+    L.fp8_rmsnorm_fwd.argtypes = [P, I32, P, P, I32, I64, I64, P, I32, F, P, P, I32, P, P, P]
+    L.fp8_rmsnorm_bwd.argtypes = [P, I32, P, P, I32, P, I64, I64, P, I32, P, P, P, I32, P, I64, P]
+    L.fp8_rmsnorm_bwd_workspace_bytes.argtypes = [I64, I64]
+    L.mp_logprobs_fwd.argtypes = [P, I32, I64, I64, I64, P, P, P, P, P, P, I32, P]
+    L.mp_logprobs_bwd.argtypes = [P, I32, I64, I64, I64, P, P, P, P, P, P, P, P, P]
+    L.mp_embedding_fwd.argtypes = [P, I64, P, I32, I64, I64, P, F, P, I32, P]
+    L.mp_embedding_bwd.argtypes = [P, I64, P, I32, I64, I64, F, P, I32, P, I64, P]
+    L.mp_embedding_bwd_workspace_bytes.argtypes = [I64, I64, I64]
+    for name in ("fp8_rmsnorm_fwd", "fp8_rmsnorm_bwd", "mp_logprobs_fwd", "mp_logprobs_bwd", "mp_embedding_fwd",
+                 "mp_embedding_bwd"):
+        getattr(L, name).restype = ctypes.c_int
+    for name in ("fp8_rmsnorm_bwd_workspace_bytes", "mp_embedding_bwd_workspace_bytes"):
+        getattr(L, name).restype = I64
     L.fp8mp_check.argtypes = [P]
     L.fp8mp_selftest_timeout.argtypes = [P]
     L.fp8mp_selftest_barrier_timeout.argtypes = [P]
@@ -665,6 +680,190 @@ def mp_adamw_step(tensors: AdamWTensors, loss_scale: torch.Tensor, growth_tracke
                                 _ptr(found_inf), _ptr(beta_pows), _ptr(seed), _ptr(grad_norm), float(max_norm),
                                 float(lr), float(beta1), float(beta2), float(eps), float(backoff),
                                 float(growth_factor), int(growth_interval), *_workspace(workspace), _stream(stream)))
+
+
+def _like(what: str, device, **tensors) -> None:
+    """Every tensor lies on `device`."""
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise Fp8mpError(ERR_INVALID, f"{name} must be on {device} as {what}, got {t.device}")
+
+
+_HIGH = (torch.bfloat16, torch.float32)
+_F32 = (torch.float32,)
+MAX_NORM_COLS = 16384  # FP8MP_MAX_NORM_COLS
+MAX_TOP = 32  # FP8MP_MAX_TOP
+
+
+def fp8_rmsnorm_fwd(x: torch.Tensor, w: torch.Tensor, y: torch.Tensor, rstd: torch.Tensor, eps: float = 1e-6,
+                    residual: torch.Tensor | None = None, total: torch.Tensor | None = None,
+                    y_scale: torch.Tensor | None = None, y_amax: torch.Tensor | None = None, stream=None) -> None:
+    """total = x + residual (x alone without one), rstd[m] = 1 / sqrt(mean(total^2) + eps),
+    y[M, K] = total * rstd * w: E4M3 codes (uint8) under y_scale, or bf16 / fp32
+    without it. y_amax = max(y_amax, max|y|). total may be residual itself."""
+    if x.dim() != 2:
+        raise Fp8mpError(ERR_INVALID, f"x must be [M, K], got {tuple(x.shape)}")
+    M, K = x.shape
+    _shape(x, "x", (M, K), *_HIGH)
+    _shape(w, "w", (K,), *_HIGH)
+    _shape(y, "y", (M, K), *((torch.uint8,) if y_scale is not None else _HIGH))
+    _shape(rstd, "rstd", (M,), *_F32)
+    if (residual is None) != (total is None):
+        raise Fp8mpError(ERR_INVALID, "residual and total come together")
+    if residual is not None:
+        _shape(residual, "residual", (M, K), *_HIGH)
+        _shape(total, "total", (M, K), residual.dtype)
+    for name, t in (("y_scale", y_scale), ("y_amax", y_amax)):
+        if t is not None:
+            _expect(t, name, torch.float32, 1)
+    _like("x", x.device, w=w, y=y, rstd=rstd, residual=residual, total=total, y_scale=y_scale, y_amax=y_amax)
+    _check(load().fp8_rmsnorm_fwd(_ptr(x), _dtype_code(x), _ptr(residual), _ptr(total),
+                                  _dtype_code(residual) if residual is not None else F32, M, K, _ptr(w), _dtype_code(w),
+                                  float(eps), _ptr(y_scale), _ptr(y), F32 if y_scale is not None else _dtype_code(y),
+                                  _ptr(y_amax), _ptr(rstd), _stream(stream)))
+
+
+def fp8_rmsnorm_bwd_workspace_bytes(M: int, K: int) -> int:
+    return int(load().fp8_rmsnorm_bwd_workspace_bytes(M, K))
+
+
+def fp8_rmsnorm_bwd(dy: torch.Tensor, total: torch.Tensor, w: torch.Tensor, rstd: torch.Tensor,
+                    dresidual: torch.Tensor, dw: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                    dtotal: torch.Tensor | None = None, dx: torch.Tensor | None = None, stream=None) -> None:
+    """Backward pass of fp8_rmsnorm_fwd: dresidual = the gradient of x and of the
+    residual, from dy and the stream's own gradient dtotal (which dresidual may be
+    itself); dx the same in dy's type; dw the weight's, which needs a workspace of
+    fp8_rmsnorm_bwd_workspace_bytes(M, K) bytes. total: x itself without a residual."""
+    if dy.dim() != 2:
+        raise Fp8mpError(ERR_INVALID, f"dy must be [M, K], got {tuple(dy.shape)}")
+    M, K = dy.shape
+    _shape(dy, "dy", (M, K), *_HIGH)
+    _shape(total, "total", (M, K), *_HIGH)
+    _shape(w, "w", (K,), *_HIGH)
+    _shape(rstd, "rstd", (M,), *_F32)
+    _shape(dresidual, "dresidual", (M, K), total.dtype)
+    if dtotal is not None:
+        _shape(dtotal, "dtotal", (M, K), total.dtype)
+    if dx is not None:
+        _shape(dx, "dx", (M, K), dy.dtype)
+    if dw is not None:
+        _shape(dw, "dw", (K,), *_HIGH)
+        if workspace is None:
+            raise Fp8mpError(ERR_INVALID, "dw needs a workspace")
+    _like("dy", dy.device, total=total, w=w, rstd=rstd, dresidual=dresidual, dw=dw, workspace=workspace, dtotal=dtotal,
+          dx=dx)
+    _check(load().fp8_rmsnorm_bwd(_ptr(dy), _dtype_code(dy), _ptr(dtotal), _ptr(total), _dtype_code(total), _ptr(rstd),
+                                  M, K, _ptr(w), _dtype_code(w), _ptr(dresidual), _ptr(dx), _ptr(dw),
+                                  _dtype_code(dw) if dw is not None else F32,
+                                  *(_workspace(workspace) if workspace is not None else (None, 0)), _stream(stream)))
+
+
+def _logits(logits: torch.Tensor, vocab: int | None):
+    if logits.dim() != 2:
+        raise Fp8mpError(ERR_INVALID, f"logits must be [M, columns], got {tuple(logits.shape)}")
+    _shape(logits, "logits", tuple(logits.shape), *_HIGH)
+    M, ld = logits.shape
+    V = ld if vocab is None else int(vocab)
+    if not 1 <= V <= ld:
+        raise Fp8mpError(ERR_INVALID, f"vocab must lie in 1..{ld}, got {V}")
+    return M, V, ld
+
+
+def mp_logprobs_fwd(logits: torch.Tensor, targets: torch.Tensor | None, logprob: torch.Tensor | None,
+                    stats: torch.Tensor, entropy: torch.Tensor | None = None, top_logprob: torch.Tensor | None = None,
+                    top_id: torch.Tensor | None = None, vocab: int | None = None, stream=None) -> None:
+    """logprob[m] = log p of targets[m] (int64; 0 where it is not in 0..V-1) under
+    logits [M, columns], of which the first `vocab` (all, if None) count; stats [M, 2]
+    = (largest logit, log of the sum of exp(logit - largest)); entropy [M]; the
+    top_id.shape[1] (at most MAX_TOP) most probable tokens and their log p, of equal
+    logits the lower index first."""
+    M, V, ld = _logits(logits, vocab)
+    _shape(stats, "stats", (M, 2), *_F32)
+    if (targets is None) != (logprob is None):
+        raise Fp8mpError(ERR_INVALID, "targets and logprob come together")
+    if targets is not None:
+        _shape(targets, "targets", (M,), torch.int64)
+        _shape(logprob, "logprob", (M,), *_F32)
+    if entropy is not None:
+        _shape(entropy, "entropy", (M,), *_F32)
+    if (top_logprob is None) != (top_id is None):
+        raise Fp8mpError(ERR_INVALID, "top_logprob and top_id come together")
+    top = 0
+    if top_id is not None:
+        if top_id.dim() != 2:
+            raise Fp8mpError(ERR_INVALID, f"top_id must be [M, top], got {tuple(top_id.shape)}")
+        top = top_id.shape[1]
+        _shape(top_id, "top_id", (M, top), torch.int64)
+        _shape(top_logprob, "top_logprob", (M, top), *_F32)
+    _like("logits", logits.device, targets=targets, logprob=logprob, stats=stats, entropy=entropy,
+          top_logprob=top_logprob, top_id=top_id)
+    _check(load().mp_logprobs_fwd(_ptr(logits), _dtype_code(logits), M, V, ld, _ptr(targets), _ptr(logprob), _ptr(stats),
+                                  _ptr(entropy), _ptr(top_logprob), _ptr(top_id), top, _stream(stream)))
+
+
+def mp_logprobs_bwd(logits: torch.Tensor, targets: torch.Tensor, stats: torch.Tensor, dlogprob: torch.Tensor,
+                    dlogits: torch.Tensor, entropy: torch.Tensor | None = None, dentropy: torch.Tensor | None = None,
+                    scale: torch.Tensor | None = None, amax: torch.Tensor | None = None, vocab: int | None = None,
+                    stream=None) -> None:
+    """The logits' gradient from those of logprob and entropy (with mp_logprobs_fwd's
+    stats and entropy): dlogits [M, columns] in the logits' type, which may be logits
+    itself, or E5M2 codes (uint8) under scale, with amax = max(amax, max|gradient|).
+    Columns from `vocab` on get 0."""
+    M, V, ld = _logits(logits, vocab)
+    _shape(targets, "targets", (M,), torch.int64)
+    _shape(stats, "stats", (M, 2), *_F32)
+    _shape(dlogprob, "dlogprob", (M,), *_F32)
+    _shape(dlogits, "dlogits", (M, ld), torch.uint8 if scale is not None else logits.dtype)
+    if (entropy is None) != (dentropy is None):
+        raise Fp8mpError(ERR_INVALID, "entropy and dentropy come together")
+    if entropy is not None:
+        _shape(entropy, "entropy", (M,), *_F32)
+        _shape(dentropy, "dentropy", (M,), *_F32)
+    for name, t in (("scale", scale), ("amax", amax)):
+        if t is not None:
+            _expect(t, name, torch.float32, 1)
+    _like("logits", logits.device, targets=targets, stats=stats, dlogprob=dlogprob, dlogits=dlogits, entropy=entropy,
+          dentropy=dentropy, scale=scale, amax=amax)
+    _check(load().mp_logprobs_bwd(_ptr(logits), _dtype_code(logits), M, V, ld, _ptr(targets), _ptr(stats),
+                                  _ptr(dlogprob), _ptr(entropy), _ptr(dentropy), _ptr(scale), _ptr(dlogits), _ptr(amax),
+                                  _stream(stream)))
+
+
+def mp_embedding_fwd(ids: torch.Tensor, table: torch.Tensor, out: torch.Tensor, scale: float = 1.0,
+                     sinv: torch.Tensor | None = None, stream=None) -> None:
+    """out[m] = table[ids[m]] * scale (ids int64 [M]; zeros where an id is not in
+    0..V-1). table [V, K]: bf16, fp32, or E4M3 codes (uint8) whose values sinv scales."""
+    if table.dim() != 2 or ids.dim() != 1:
+        raise Fp8mpError(ERR_INVALID, f"table must be [V, K] and ids [M], got {tuple(table.shape)}, {tuple(ids.shape)}")
+    (V, K), M = table.shape, ids.shape[0]
+    _shape(ids, "ids", (M,), torch.int64)
+    _shape(table, "table", (V, K), *((torch.uint8,) if sinv is not None else _HIGH))
+    _shape(out, "out", (M, K), *_HIGH)
+    if sinv is not None:
+        _expect(sinv, "sinv", torch.float32, 1)
+    _like("ids", ids.device, table=table, out=out, sinv=sinv)
+    _check(load().mp_embedding_fwd(_ptr(ids), M, _ptr(table), F32 if sinv is not None else _dtype_code(table), V, K,
+                                   _ptr(sinv), float(scale), _ptr(out), _dtype_code(out), _stream(stream)))
+
+
+def mp_embedding_bwd_workspace_bytes(M: int, V: int, K: int) -> int:
+    return int(load().mp_embedding_bwd_workspace_bytes(M, V, K))
+
+
+def mp_embedding_bwd(ids: torch.Tensor, dy: torch.Tensor, dtable: torch.Tensor, workspace: torch.Tensor,
+                     scale: float = 1.0, stream=None) -> None:
+    """dtable[v] = scale * (sum of the dy[m] with ids[m] == v), for every row v of
+    dtable [V, K]; the same bits at every call. workspace: at least
+    mp_embedding_bwd_workspace_bytes(M, V, K) bytes."""
+    if dtable.dim() != 2 or ids.dim() != 1:
+        raise Fp8mpError(ERR_INVALID, f"dtable must be [V, K] and ids [M], got {tuple(dtable.shape)}, {tuple(ids.shape)}")
+    (V, K), M = dtable.shape, ids.shape[0]
+    _shape(ids, "ids", (M,), torch.int64)
+    _shape(dy, "dy", (M, K), *_HIGH)
+    _shape(dtable, "dtable", (V, K), *_HIGH)
+    _like("ids", ids.device, dy=dy, dtable=dtable, workspace=workspace)
+    _check(load().mp_embedding_bwd(_ptr(ids), M, _ptr(dy), _dtype_code(dy), V, K, float(scale), _ptr(dtable),
+                                   _dtype_code(dtable), *_workspace(workspace), _stream(stream)))
 
 
 def fp8mp_check(stream=None) -> int:

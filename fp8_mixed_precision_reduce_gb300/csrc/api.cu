@@ -981,6 +981,253 @@ int mp_adamw_step(const fp8mp_adamw_tensor *tensors, int32_t n_tensors, float *l
     return launch_adamw_step(tensors, n_tensors, a, static_cast<cudaStream_t>(stream), dev);
 }
 
+// Whether two arrays share memory.
+static bool overlap(const void *p, int64_t np, const void *q, int64_t nq) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return a < b + static_cast<uintptr_t>(nq) && b < a + static_cast<uintptr_t>(np);
+}
+static int64_t width(int32_t dtype) { return dtype == FP8MP_BF16 ? 2 : 4; }
+
+// A pointer to elements of `n` bytes each, aligned to them.
+static int check_elements(const void *p, uintptr_t n, const char *fn, const char *name, bool required) {
+    if (p == nullptr) {
+        if (required) return fail(FP8MP_ERR_INVALID, "%s: %s is NULL", fn, name);
+        return FP8MP_OK;
+    }
+    if (reinterpret_cast<uintptr_t>(p) % n != 0) return fail(FP8MP_ERR_INVALID, "%s: %s is misaligned", fn, name);
+    return FP8MP_OK;
+}
+
+#define CHECK_ELEMENTS(p, n, required)                              \
+    do {                                                            \
+        const int rc_ = check_elements((p), (n), fn, #p, (required)); \
+        if (rc_) return rc_;                                        \
+    } while (0)
+
+static bool valid_norm_dims(int64_t M, int64_t K) {
+    return M >= 0 && M <= (1ll << 30) && K >= 0 && K <= FP8MP_MAX_NORM_COLS && K % 16 == 0;
+}
+
+int64_t fp8_rmsnorm_bwd_workspace_bytes(int64_t M, int64_t K) {
+    return valid_norm_dims(M, K) ? rmsnorm_workspace_bytes(M, K) : -1;
+}
+
+static int check_norm_dims(const char *fn, int64_t M, int64_t K) {
+    REQUIRE(valid_norm_dims(M, K), "%s: M = %lld outside 0..2^30, or K = %lld no multiple of 16 in 0..%d", fn,
+            (long long)M, (long long)K, FP8MP_MAX_NORM_COLS);
+    return FP8MP_OK;
+}
+
+int fp8_rmsnorm_fwd(const void *x, int32_t x_dtype, const void *residual, void *total, int32_t t_dtype, int64_t M,
+                    int64_t K, const void *w, int32_t w_dtype, float eps, const float *y_scale, void *y,
+                    int32_t y_dtype, float *y_amax, float *rstd, void *stream) {
+    const char *fn = "fp8_rmsnorm_fwd";
+    clear_error();
+    int rc = check_norm_dims(fn, M, K);
+    if (rc) return rc;
+    REQUIRE(valid_dtype(x_dtype), "%s: x_dtype %d invalid", fn, x_dtype);
+    REQUIRE(valid_dtype(w_dtype), "%s: w_dtype %d invalid", fn, w_dtype);
+    REQUIRE(residual == nullptr || valid_dtype(t_dtype), "%s: t_dtype %d invalid", fn, t_dtype);
+    REQUIRE(y_scale != nullptr || valid_dtype(y_dtype), "%s: y_dtype %d invalid", fn, y_dtype);
+    REQUIRE((residual == nullptr) == (total == nullptr), "%s: residual and total come together", fn);
+    REQUIRE(eps >= 0.0f && eps <= FLT_MAX, "%s: eps must be finite and >= 0", fn);
+    if (M == 0 || K == 0) return FP8MP_OK;
+    CHECK_PTR(x, true);
+    CHECK_PTR(residual, false);
+    CHECK_PTR(total, false);
+    CHECK_PTR(w, true);
+    CHECK_PTR(y, true);
+    CHECK_SCALAR(y_scale, false);
+    CHECK_SCALAR(y_amax, false);
+    CHECK_SCALAR(rstd, true);
+    const int64_t n = M * K;
+    const int64_t ny = n * (y_scale != nullptr ? 1 : width(y_dtype));
+    REQUIRE(!overlap(y, ny, x, n * width(x_dtype)), "%s: x and y overlap", fn);
+    if (residual != nullptr) {
+        const int64_t nt = n * width(t_dtype);
+        REQUIRE(total == residual || !overlap(total, nt, residual, nt), "%s: residual and total overlap in part", fn);
+        REQUIRE(!overlap(total, nt, x, n * width(x_dtype)), "%s: x and total overlap", fn);
+        REQUIRE(!overlap(y, ny, total, nt) && !overlap(y, ny, residual, nt), "%s: y overlaps residual or total", fn);
+    }
+    DeviceInfo dev;
+    rc = current_device(&dev);
+    if (rc) return rc;
+    return launch_rmsnorm_fwd(x, x_dtype, residual, total, t_dtype, M, K, w, w_dtype, eps, y_scale, y, y_dtype, y_amax,
+                              rstd, static_cast<cudaStream_t>(stream), dev);
+}
+
+int fp8_rmsnorm_bwd(const void *dy, int32_t dy_dtype, const void *dtotal, const void *total, int32_t t_dtype,
+                    const float *rstd, int64_t M, int64_t K, const void *w, int32_t w_dtype, void *dresidual,
+                    void *dx, void *dw, int32_t dw_dtype, void *workspace, int64_t workspace_bytes, void *stream) {
+    const char *fn = "fp8_rmsnorm_bwd";
+    clear_error();
+    int rc = check_norm_dims(fn, M, K);
+    if (rc) return rc;
+    REQUIRE(valid_dtype(dy_dtype), "%s: dy_dtype %d invalid", fn, dy_dtype);
+    REQUIRE(valid_dtype(t_dtype), "%s: t_dtype %d invalid", fn, t_dtype);
+    REQUIRE(valid_dtype(w_dtype), "%s: w_dtype %d invalid", fn, w_dtype);
+    REQUIRE(dw == nullptr || valid_dtype(dw_dtype), "%s: dw_dtype %d invalid", fn, dw_dtype);
+    if (K == 0 || (M == 0 && dw == nullptr)) return FP8MP_OK;
+    CHECK_PTR(dw, false);
+    if (M > 0) {
+        CHECK_PTR(dy, true);
+        CHECK_PTR(dtotal, false);
+        CHECK_PTR(total, true);
+        CHECK_PTR(w, true);
+        CHECK_PTR(dresidual, true);
+        CHECK_PTR(dx, false);
+        CHECK_SCALAR(rstd, true);
+        const int64_t nt = M * K * width(t_dtype), nd = M * K * width(dy_dtype);
+        REQUIRE(dtotal == nullptr || dresidual == dtotal || !overlap(dresidual, nt, dtotal, nt),
+                "%s: dtotal and dresidual overlap in part", fn);
+        REQUIRE(!overlap(dresidual, nt, total, nt) && !overlap(dresidual, nt, dy, nd),
+                "%s: dresidual overlaps total or dy", fn);
+        if (dx != nullptr)
+            REQUIRE(!overlap(dx, nd, dresidual, nt) && !overlap(dx, nd, total, nt) && !overlap(dx, nd, dy, nd) &&
+                        (dtotal == nullptr || !overlap(dx, nd, dtotal, nt)),
+                    "%s: dx overlaps another array", fn);
+        if (dw != nullptr) {
+            CHECK_PTR(workspace, true);
+            REQUIRE(workspace_bytes >= rmsnorm_workspace_bytes(M, K), "%s: workspace of %lld bytes, %lld needed", fn,
+                    (long long)workspace_bytes, (long long)rmsnorm_workspace_bytes(M, K));
+        }
+    }
+    DeviceInfo dev;
+    rc = current_device(&dev);
+    if (rc) return rc;
+    return launch_rmsnorm_bwd(dy, dy_dtype, dtotal, total, t_dtype, rstd, M, K, w, w_dtype, dresidual, dx, dw, dw_dtype,
+                              workspace, static_cast<cudaStream_t>(stream));
+}
+
+static int check_logits(const char *fn, const void *logits, int32_t x_dtype, int64_t M, int64_t V, int64_t ld) {
+    REQUIRE(valid_dtype(x_dtype), "%s: x_dtype %d invalid", fn, x_dtype);
+    REQUIRE(M >= 0 && M <= (1ll << 30), "%s: M = %lld outside 0..2^30", fn, (long long)M);
+    REQUIRE(V >= 1 && V <= ld && ld <= 0x7FFFFFFFll, "%s: V = %lld, ld = %lld: 1 <= V <= ld < 2^31", fn, (long long)V,
+            (long long)ld);
+    if (M > 0) CHECK_ELEMENTS(logits, static_cast<uintptr_t>(width(x_dtype)), true);
+    return FP8MP_OK;
+}
+
+int mp_logprobs_fwd(const void *logits, int32_t x_dtype, int64_t M, int64_t V, int64_t ld, const int64_t *targets,
+                    float *logprob, float *stats, float *entropy, float *top_logprob, int64_t *top_id, int32_t top,
+                    void *stream) {
+    const char *fn = "mp_logprobs_fwd";
+    clear_error();
+    int rc = check_logits(fn, logits, x_dtype, M, V, ld);
+    if (rc) return rc;
+    REQUIRE(top >= 0 && top <= FP8MP_MAX_TOP && top <= V, "%s: top = %d outside 0..min(%d, V)", fn, top, FP8MP_MAX_TOP);
+    REQUIRE((targets == nullptr) == (logprob == nullptr), "%s: targets and logprob come together", fn);
+    if (M == 0) return FP8MP_OK;
+    CHECK_ELEMENTS(targets, 8, false);
+    CHECK_ELEMENTS(logprob, 4, false);
+    CHECK_ELEMENTS(stats, 8, true);
+    CHECK_ELEMENTS(entropy, 4, false);
+    if (top > 0) {
+        CHECK_ELEMENTS(top_logprob, 4, true);
+        CHECK_ELEMENTS(top_id, 8, true);
+    }
+    DeviceInfo dev;
+    rc = current_device(&dev);
+    if (rc) return rc;
+    return launch_logprobs_fwd(logits, x_dtype, M, V, ld, targets, logprob, stats, entropy, top_logprob, top_id, top,
+                               static_cast<cudaStream_t>(stream), dev);
+}
+
+int mp_logprobs_bwd(const void *logits, int32_t x_dtype, int64_t M, int64_t V, int64_t ld, const int64_t *targets,
+                    const float *stats, const float *dlogprob, const float *entropy, const float *dentropy,
+                    const float *scale, void *dlogits, float *amax, void *stream) {
+    const char *fn = "mp_logprobs_bwd";
+    clear_error();
+    int rc = check_logits(fn, logits, x_dtype, M, V, ld);
+    if (rc) return rc;
+    REQUIRE((entropy == nullptr) == (dentropy == nullptr), "%s: entropy and dentropy come together", fn);
+    REQUIRE(scale == nullptr || ld % 16 == 0, "%s: codes need ld to be a multiple of 16 (got %lld)", fn, (long long)ld);
+    if (M == 0) return FP8MP_OK;
+    CHECK_ELEMENTS(targets, 8, true);
+    CHECK_ELEMENTS(stats, 8, true);
+    CHECK_ELEMENTS(dlogprob, 4, true);
+    CHECK_ELEMENTS(entropy, 4, false);
+    CHECK_ELEMENTS(dentropy, 4, false);
+    CHECK_SCALAR(scale, false);
+    CHECK_SCALAR(amax, false);
+    const int64_t nx = M * ld * width(x_dtype);
+    if (scale != nullptr) {
+        CHECK_PTR(logits, true);
+        CHECK_PTR(dlogits, true);
+        REQUIRE(!overlap(logits, nx, dlogits, M * ld), "%s: logits and their gradient's codes overlap", fn);
+    } else {
+        CHECK_ELEMENTS(dlogits, static_cast<uintptr_t>(width(x_dtype)), true);
+        REQUIRE((reinterpret_cast<uintptr_t>(logits) - reinterpret_cast<uintptr_t>(dlogits)) % 16 == 0,
+                "%s: logits and dlogits must have the same address modulo 16", fn);
+        REQUIRE(logits == dlogits || !overlap(logits, nx, dlogits, nx), "%s: logits and dlogits overlap in part", fn);
+    }
+    DeviceInfo dev;
+    rc = current_device(&dev);
+    if (rc) return rc;
+    return launch_logprobs_bwd(logits, x_dtype, M, V, ld, targets, stats, dlogprob, entropy, dentropy, scale, dlogits,
+                               amax, static_cast<cudaStream_t>(stream), dev);
+}
+
+static bool valid_table_dims(int64_t M, int64_t V, int64_t K) {
+    return M >= 0 && M < (1ll << 30) && V >= 0 && V <= 0x7FFFFFFFll && K >= 0 && K <= (1ll << 20) && K % 16 == 0;
+}
+
+int64_t mp_embedding_bwd_workspace_bytes(int64_t M, int64_t V, int64_t K) {
+    return valid_table_dims(M, V, K) ? embedding_workspace_bytes(M, V, K) : -1;
+}
+
+static int check_table(const char *fn, const int64_t *ids, int64_t M, int64_t V, int64_t K) {
+    REQUIRE(valid_table_dims(M, V, K),
+            "%s: M = %lld outside 0..2^30 - 1, V = %lld outside 0..2^31 - 1, or K = %lld no multiple of 16 in 0..2^20", fn,
+            (long long)M, (long long)V, (long long)K);
+    if (M > 0 && K > 0) CHECK_ELEMENTS(ids, 8, true);
+    return FP8MP_OK;
+}
+
+int mp_embedding_fwd(const int64_t *ids, int64_t M, const void *table, int32_t table_dtype, int64_t V, int64_t K,
+                     const float *sinv, float scale, void *out, int32_t out_dtype, void *stream) {
+    const char *fn = "mp_embedding_fwd";
+    clear_error();
+    int rc = check_table(fn, ids, M, V, K);
+    if (rc) return rc;
+    REQUIRE(sinv != nullptr || valid_dtype(table_dtype), "%s: table_dtype %d invalid", fn, table_dtype);
+    REQUIRE(valid_dtype(out_dtype), "%s: out_dtype %d invalid", fn, out_dtype);
+    if (M == 0 || K == 0) return FP8MP_OK;
+    CHECK_PTR(table, V > 0);
+    CHECK_PTR(out, true);
+    CHECK_SCALAR(sinv, false);
+    REQUIRE(V == 0 || !overlap(table, V * K * (sinv != nullptr ? 1 : width(table_dtype)), out, M * K * width(out_dtype)),
+            "%s: table and out overlap", fn);
+    DeviceInfo dev;
+    rc = current_device(&dev);
+    if (rc) return rc;
+    return launch_embedding_fwd(ids, M, table, sinv != nullptr ? 0 : table_dtype == FP8MP_BF16 ? 1 : 2, V, K, sinv, scale,
+                                out, out_dtype, static_cast<cudaStream_t>(stream), dev);
+}
+
+int mp_embedding_bwd(const int64_t *ids, int64_t M, const void *dy, int32_t dy_dtype, int64_t V, int64_t K, float scale,
+                     void *dtable, int32_t dtable_dtype, void *workspace, int64_t workspace_bytes, void *stream) {
+    const char *fn = "mp_embedding_bwd";
+    clear_error();
+    int rc = check_table(fn, ids, M, V, K);
+    if (rc) return rc;
+    REQUIRE(valid_dtype(dy_dtype), "%s: dy_dtype %d invalid", fn, dy_dtype);
+    REQUIRE(valid_dtype(dtable_dtype), "%s: dtable_dtype %d invalid", fn, dtable_dtype);
+    if (V == 0 || K == 0) return FP8MP_OK;
+    CHECK_PTR(dy, M > 0);
+    CHECK_PTR(dtable, true);
+    CHECK_PTR(workspace, true);
+    REQUIRE(workspace_bytes >= embedding_workspace_bytes(M, V, K), "%s: workspace of %lld bytes, %lld needed", fn,
+            (long long)workspace_bytes, (long long)embedding_workspace_bytes(M, V, K));
+    REQUIRE(M == 0 || !overlap(dy, M * K * width(dy_dtype), dtable, V * K * width(dtable_dtype)),
+            "%s: dy and dtable overlap", fn);
+    DeviceInfo dev;
+    rc = current_device(&dev);
+    if (rc) return rc;
+    return launch_embedding_bwd(ids, M, dy, dy_dtype, V, K, scale, dtable, dtable_dtype, workspace,
+                                static_cast<cudaStream_t>(stream), dev);
+}
+
 int fp8mp_selftest_timeout(void *stream) {
     clear_error();
     DeviceInfo dev;

@@ -1,0 +1,83 @@
+// fp8mp_pieces.cuh -- eight consecutive elements ("a piece") of a bf16 or fp32
+// row in registers, as the row-wise kernels move them: 16- or 32-byte loads and
+// stores, values in pairs of fp32. Not part of the ABI.
+#pragma once
+
+#include "fp8mp_f32x2.cuh"
+#include "fp8mp_internal.cuh"
+
+namespace fp8mp {
+
+constexpr int kPiece = 8;
+
+template <bool BF16>
+struct Piece {
+    uint32_t w[BF16 ? 4 : 8];
+    // Elements 2 i and 2 i + 1.
+    __device__ __forceinline__ uint64_t pair(int i) const {
+        if constexpr (BF16) return f2_from_bits(w[i] << 16, w[i] & 0xFFFF0000u);
+        else return f2_from_bits(w[2 * i], w[2 * i + 1]);
+    }
+};
+
+// Piece `i` of an array; read once.
+template <bool BF16>
+__device__ __forceinline__ Piece<BF16> load_piece(const void *x, int64_t i) {
+    Piece<BF16> r;
+    const uint4 *p = reinterpret_cast<const uint4 *>(x) + (BF16 ? i : 2 * i);
+#pragma unroll
+    for (int j = 0; j < (BF16 ? 1 : 2); ++j) {
+        const uint4 v = __ldcs(p + j);
+        r.w[4 * j] = v.x;
+        r.w[4 * j + 1] = v.y;
+        r.w[4 * j + 2] = v.z;
+        r.w[4 * j + 3] = v.w;
+    }
+    return r;
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Four pairs rounded to the array's type.
+template <bool BF16>
+__device__ __forceinline__ Piece<BF16> round_piece(const uint64_t (&v)[4]) {
+    Piece<BF16> r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        f2_split(v[i], lo, hi);
+        if constexpr (BF16) {
+            r.w[i] = bf16_pair(lo, hi);
+        } else {
+            r.w[2 * i] = __float_as_uint(lo);
+            r.w[2 * i + 1] = __float_as_uint(hi);
+        }
+    }
+    return r;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store_piece(void *x, int64_t i, const Piece<BF16> &r) {
+    uint4 *p = reinterpret_cast<uint4 *>(x) + (BF16 ? i : 2 * i);
+#pragma unroll
+    for (int j = 0; j < (BF16 ? 1 : 2); ++j)
+        p[j] = make_uint4(r.w[4 * j], r.w[4 * j + 1], r.w[4 * j + 2], r.w[4 * j + 3]);
+}
+
+// The same with the type known at run time (uniform over the launch).
+__device__ __forceinline__ void store_rounded(void *x, int64_t i, const uint64_t (&v)[4], bool bf16) {
+    if (bf16) store_piece<true>(x, i, round_piece<true>(v));
+    else store_piece<false>(x, i, round_piece<false>(v));
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+}  // namespace fp8mp

@@ -793,6 +793,131 @@ int mp_adamw_step(const fp8mp_adamw_tensor *tensors, int32_t n_tensors, float *l
                   float lr, float beta1, float beta2, float eps, float backoff, float growth_factor,
                   int32_t growth_interval, void *workspace, int64_t workspace_bytes, void *stream);
 
+/* Most columns of a row of fp8_rmsnorm_fwd. */
+#define FP8MP_MAX_NORM_COLS 16384
+
+/*
+ * fp8_rmsnorm_fwd -- the residual's addition, the root-mean-square norm and
+ * the cast that a block's first linear reads, in one pass:
+ *   t[m, k]  = round_{t_dtype}(x[m, k] + residual[m, k])      (t = x without residual)
+ *   rstd[m]  = 1 / sqrt(sum_k t[m, k]^2 / K + eps)
+ *   y        = (t * rstd) * w[k]                              (fp32)
+ *   out      = sat_rne_E4M3(fl32(y * y_scale[0]))  when y_scale != NULL, the
+ *              next linear's input under its delayed scale; else y in y_dtype
+ *   *y_amax  = max(*y_amax, max |y|)     (fp32 y, NaN left out; when != NULL)
+ * The norm is of t as it is stored, so the backward pass finds the same. The
+ * sum is fp32: a row of a norm of 2^64 or more has rstd = 0.
+ *
+ * x [M x K] of x_dtype; residual and total [M x K] of t_dtype, both or neither
+ * (total receives t and may be the residual itself, but not overlap it
+ * otherwise); w [K] of w_dtype; y [M x K] bytes or y_dtype; rstd [M] fp32.
+ * K a multiple of 16, at most FP8MP_MAX_NORM_COLS; any M >= 0. M == 0 or
+ * K == 0: no-op.
+ */
+int fp8_rmsnorm_fwd(const void *x, int32_t x_dtype, const void *residual, void *total, int32_t t_dtype, int64_t M,
+                    int64_t K, const void *w, int32_t w_dtype, float eps, const float *y_scale, void *y,
+                    int32_t y_dtype, float *y_amax, float *rstd, void *stream);
+
+/*
+ * fp8_rmsnorm_bwd -- backward pass of fp8_rmsnorm_fwd, from the gradient dy of
+ * y (the cast counts as the identity) and dtotal of t (the residual stream's):
+ *   n = t * rstd,  g = dy * w
+ *   dresidual[m, k] = rstd (g - n mean_k(g n)) + dtotal       the gradient of
+ *                     x and of the residual alike
+ *   dx = the same, in dy_dtype                                (when != NULL)
+ *   dw[k] = sum_m dy n                                        (when != NULL)
+ * dy [M x K] of dy_dtype; dtotal (or NULL), total (t; x itself without a
+ * residual) and dresidual [M x K] of t_dtype, where dresidual may be dtotal
+ * itself; dw [K] of dw_dtype. dw needs a workspace of
+ * fp8_rmsnorm_bwd_workspace_bytes(M, K) bytes, 16-byte aligned, whatever it
+ * holds; calls that share one must not overlap on the GPU. dw is summed in
+ * fp32 in an order that M and K fix. Sizes as fp8_rmsnorm_fwd; M == 0 gives
+ * dw = 0.
+ */
+int fp8_rmsnorm_bwd(const void *dy, int32_t dy_dtype, const void *dtotal, const void *total, int32_t t_dtype,
+                    const float *rstd, int64_t M, int64_t K, const void *w, int32_t w_dtype, void *dresidual,
+                    void *dx, void *dw, int32_t dw_dtype, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* -1 for a shape that fp8_rmsnorm_bwd refuses. */
+int64_t fp8_rmsnorm_bwd_workspace_bytes(int64_t M, int64_t K);
+
+/* Most alternatives of mp_logprobs_fwd. */
+#define FP8MP_MAX_TOP 32
+
+/*
+ * mp_logprobs_fwd -- log probabilities of given tokens under logits over a
+ * vocabulary of V, with the entropy and the most probable tokens:
+ *   stats[m]   = (max_v x[m, v], log sum_v exp(x[m, v] - max))     (fp32)
+ *   log p(v)   = (x[m, v] - stats[m][0]) - stats[m][1]
+ *   logprob[m] = log p(targets[m]); 0 where targets[m] is not in 0 .. V - 1
+ *                (a prompt's or padding's token)
+ *   entropy[m] = -sum_v p(v) log p(v)                              (when != NULL)
+ *   top_id[m, i], top_logprob[m, i], i < top: the tokens of the largest
+ *                logits, largest first, of equal ones the lower index first,
+ *                and their log p                                   (top > 0)
+ * Masked tokens are logits of -Inf (p = 0) or of the type's lowest value. A
+ * row without any logit above -Inf has stats (-Inf, -Inf), log p = -Inf
+ * throughout and entropy 0. A row with a NaN or +Inf has NaN results; in the
+ * order of top_id a NaN is the smallest.
+ *
+ * logits [M x ld] of x_dtype, dense; columns V .. ld - 1 (a vocabulary padded
+ * for the GEMM) are left out. The array is aligned to its elements, rows need
+ * no alignment. targets [M] int64 (8-byte aligned; with logprob, both or
+ * neither); logprob, entropy [M] fp32; stats [M x 2] fp32, 8-byte aligned;
+ * top_logprob [M x top] fp32 and top_id [M x top] int64, top in
+ * 0 .. min(FP8MP_MAX_TOP, V). 1 <= V <= ld < 2^31; M == 0: no-op.
+ */
+int mp_logprobs_fwd(const void *logits, int32_t x_dtype, int64_t M, int64_t V, int64_t ld, const int64_t *targets,
+                    float *logprob, float *stats, float *entropy, float *top_logprob, int64_t *top_id, int32_t top,
+                    void *stream);
+
+/*
+ * mp_logprobs_bwd -- gradient of the logits from those of logprob and entropy:
+ *   dx[m, v] = a (1[v = targets[m]] - p(v)) - b p(v) (log p(v) + entropy[m])
+ * with a = dlogprob[m] (0 where targets[m] is not in 0 .. V - 1), b =
+ * dentropy[m], p from stats. Rows with a = b = 0, and rows without any
+ * probability, get 0, whatever their logits hold.
+ *   scale == NULL: dlogits [M x ld] of x_dtype; it may be logits itself.
+ *   else:          dlogits [M x ld] = sat_rne_E5M2(fl32(dx * scale[0])), what
+ *                  the head's backward GEMMs read; ld a multiple of 16 and
+ *                  logits 16-byte aligned.
+ *   *amax = max(*amax, max |dx|)         (fp32 dx, NaN left out; when != NULL)
+ * Columns V .. ld - 1 of dlogits get 0. entropy and dentropy: both or neither.
+ * Without scale, logits and dlogits have the same address modulo 16.
+ */
+int mp_logprobs_bwd(const void *logits, int32_t x_dtype, int64_t M, int64_t V, int64_t ld, const int64_t *targets,
+                    const float *stats, const float *dlogprob, const float *entropy, const float *dentropy,
+                    const float *scale, void *dlogits, float *amax, void *stream);
+
+/*
+ * mp_embedding_fwd -- rows of an embedding table, scaled:
+ *   out[m, k] = table[ids[m], k] * factor       factor = scale, or
+ *               fl32(sinv[0] * scale) when sinv != NULL, rounded to out_dtype;
+ *   a row of zeros where ids[m] is not in 0 .. V - 1 (padding).
+ * table [V x K] of table_dtype, or E4M3 codes when sinv != NULL (the copy that
+ * mp_adamw_step writes; table_dtype is then not used); ids [M] int64, 8-byte
+ * aligned. K a multiple of 16, V < 2^31. M == 0 or K == 0: no-op.
+ */
+int mp_embedding_fwd(const int64_t *ids, int64_t M, const void *table, int32_t table_dtype, int64_t V, int64_t K,
+                     const float *sinv, float scale, void *out, int32_t out_dtype, void *stream);
+
+/*
+ * mp_embedding_bwd -- the table's gradient:
+ *   dtable[v, k] = (sum over the m with ids[m] = v of dy[m, k]) * scale
+ * for every v (0 where no token names it), summed in fp32 in the order of m
+ * within runs whose lengths M fixes, so results repeat bit for bit. dy [M x K]
+ * of dy_dtype, dtable [V x K] of dtable_dtype. workspace: at least
+ * mp_embedding_bwd_workspace_bytes(M, V, K) bytes, 16-byte aligned, whatever it
+ * holds; calls that share one must not overlap on the GPU. Sizes as
+ * mp_embedding_fwd, M < 2^30; M == 0 gives dtable = 0.
+ */
+int mp_embedding_bwd(const int64_t *ids, int64_t M, const void *dy, int32_t dy_dtype, int64_t V, int64_t K,
+                     float scale, void *dtable, int32_t dtable_dtype, void *workspace, int64_t workspace_bytes,
+                     void *stream);
+
+/* -1 for a shape that mp_embedding_bwd refuses. */
+int64_t mp_embedding_bwd_workspace_bytes(int64_t M, int64_t V, int64_t K);
+
 /*
  * fp8mp_check -- synchronises `stream`, then reports and clears the device
  * flags a kernel sets when one of its bounded waits runs out (an mbarrier
