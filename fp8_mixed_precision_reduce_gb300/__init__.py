@@ -682,17 +682,33 @@ def mp_adamw_step(tensors: AdamWTensors, loss_scale: torch.Tensor, growth_tracke
                                 float(growth_factor), int(growth_interval), *_workspace(workspace), _stream(stream)))
 
 
-def _like(what: str, device, **tensors) -> None:
-    """Every tensor lies on `device`."""
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise Fp8mpError(ERR_INVALID, f"{name} must be on {device} as {what}, got {t.device}")
-
-
 _HIGH = (torch.bfloat16, torch.float32)
-_F32 = (torch.float32,)
+_F32, _I64, _U8 = (torch.float32,), (torch.int64,), (torch.uint8,)
+_CODE = {torch.float32: F32, torch.bfloat16: BF16}
 MAX_NORM_COLS = 16384  # FP8MP_MAX_NORM_COLS
 MAX_TOP = 32  # FP8MP_MAX_TOP
+
+
+def _addresses(rows, stream):
+    """The tensors' addresses (None for None) and the stream. rows: (tensor, name,
+    shape or None, types); all must be dense and on the current CUDA device."""
+    device, out = None, []
+    for t, name, shape, dtypes in rows:
+        if t is None:
+            out.append(None)
+            continue
+        if t.dtype not in dtypes or not t.is_contiguous() or (shape is not None and t.shape != shape):
+            raise Fp8mpError(ERR_INVALID, f"{name} must be a dense {shape if shape is not None else 'tensor'} of "
+                             f"{' or '.join(map(str, dtypes))}, got {t.dtype} {tuple(t.shape)}")
+        if device is None:
+            device = t.get_device()
+        elif t.get_device() != device:
+            raise Fp8mpError(ERR_INVALID, f"{name} is on {t.device}, the others are not")
+        out.append(t.data_ptr())
+    if device is None or device < 0 or device != torch.cuda.current_device():
+        raise Fp8mpError(ERR_INVALID, "the tensors must be on the current CUDA device")
+    out.append(_stream(stream))
+    return out
 
 
 def fp8_rmsnorm_fwd(x: torch.Tensor, w: torch.Tensor, y: torch.Tensor, rstd: torch.Tensor, eps: float = 1e-6,
@@ -701,26 +717,20 @@ def fp8_rmsnorm_fwd(x: torch.Tensor, w: torch.Tensor, y: torch.Tensor, rstd: tor
     """total = x + residual (x alone without one), rstd[m] = 1 / sqrt(mean(total^2) + eps),
     y[M, K] = total * rstd * w: E4M3 codes (uint8) under y_scale, or bf16 / fp32
     without it. y_amax = max(y_amax, max|y|). total may be residual itself."""
-    if x.dim() != 2:
-        raise Fp8mpError(ERR_INVALID, f"x must be [M, K], got {tuple(x.shape)}")
-    M, K = x.shape
-    _shape(x, "x", (M, K), *_HIGH)
-    _shape(w, "w", (K,), *_HIGH)
-    _shape(y, "y", (M, K), *((torch.uint8,) if y_scale is not None else _HIGH))
-    _shape(rstd, "rstd", (M,), *_F32)
+    shape = x.shape
+    if len(shape) != 2:
+        raise Fp8mpError(ERR_INVALID, f"x must be [M, K], got {tuple(shape)}")
+    M, K = shape
     if (residual is None) != (total is None):
         raise Fp8mpError(ERR_INVALID, "residual and total come together")
-    if residual is not None:
-        _shape(residual, "residual", (M, K), *_HIGH)
-        _shape(total, "total", (M, K), residual.dtype)
-    for name, t in (("y_scale", y_scale), ("y_amax", y_amax)):
-        if t is not None:
-            _expect(t, name, torch.float32, 1)
-    _like("x", x.device, w=w, y=y, rstd=rstd, residual=residual, total=total, y_scale=y_scale, y_amax=y_amax)
-    _check(load().fp8_rmsnorm_fwd(_ptr(x), _dtype_code(x), _ptr(residual), _ptr(total),
-                                  _dtype_code(residual) if residual is not None else F32, M, K, _ptr(w), _dtype_code(w),
-                                  float(eps), _ptr(y_scale), _ptr(y), F32 if y_scale is not None else _dtype_code(y),
-                                  _ptr(y_amax), _ptr(rstd), _stream(stream)))
+    px, pw, py, pr, pres, ptot, ps, pa, st = _addresses((
+        (x, "x", None, _HIGH), (w, "w", (K,), _HIGH), (y, "y", shape, _HIGH if y_scale is None else _U8),
+        (rstd, "rstd", (M,), _F32), (residual, "residual", shape, _HIGH),
+        (total, "total", shape, _HIGH if residual is None else (residual.dtype,)), (y_scale, "y_scale", (1,), _F32),
+        (y_amax, "y_amax", (1,), _F32)), stream)
+    _check(load().fp8_rmsnorm_fwd(px, _CODE[x.dtype], pres, ptot, F32 if residual is None else _CODE[residual.dtype], M, K,
+                                  pw, _CODE[w.dtype], eps, ps, py, F32 if y_scale is not None else _CODE[y.dtype], pa, pr,
+                                  st))
 
 
 def fp8_rmsnorm_bwd_workspace_bytes(M: int, K: int) -> int:
@@ -732,36 +742,27 @@ def fp8_rmsnorm_bwd(dy: torch.Tensor, total: torch.Tensor, w: torch.Tensor, rstd
                     dtotal: torch.Tensor | None = None, dx: torch.Tensor | None = None, stream=None) -> None:
     """Backward pass of fp8_rmsnorm_fwd: dresidual = the gradient of x and of the
     residual, from dy and the stream's own gradient dtotal (which dresidual may be
-    itself); dx the same in dy's type; dw the weight's, which needs a workspace of
-    fp8_rmsnorm_bwd_workspace_bytes(M, K) bytes. total: x itself without a residual."""
-    if dy.dim() != 2:
-        raise Fp8mpError(ERR_INVALID, f"dy must be [M, K], got {tuple(dy.shape)}")
-    M, K = dy.shape
-    _shape(dy, "dy", (M, K), *_HIGH)
-    _shape(total, "total", (M, K), *_HIGH)
-    _shape(w, "w", (K,), *_HIGH)
-    _shape(rstd, "rstd", (M,), *_F32)
-    _shape(dresidual, "dresidual", (M, K), total.dtype)
-    if dtotal is not None:
-        _shape(dtotal, "dtotal", (M, K), total.dtype)
-    if dx is not None:
-        _shape(dx, "dx", (M, K), dy.dtype)
-    if dw is not None:
-        _shape(dw, "dw", (K,), *_HIGH)
-        if workspace is None:
-            raise Fp8mpError(ERR_INVALID, "dw needs a workspace")
-    _like("dy", dy.device, total=total, w=w, rstd=rstd, dresidual=dresidual, dw=dw, workspace=workspace, dtotal=dtotal,
-          dx=dx)
-    _check(load().fp8_rmsnorm_bwd(_ptr(dy), _dtype_code(dy), _ptr(dtotal), _ptr(total), _dtype_code(total), _ptr(rstd),
-                                  M, K, _ptr(w), _dtype_code(w), _ptr(dresidual), _ptr(dx), _ptr(dw),
-                                  _dtype_code(dw) if dw is not None else F32,
-                                  *(_workspace(workspace) if workspace is not None else (None, 0)), _stream(stream)))
+    itself); dx the same in dy's type; dw the weight's, which needs a workspace (uint8)
+    of fp8_rmsnorm_bwd_workspace_bytes(M, K). total: x itself without a residual."""
+    shape = dy.shape
+    if len(shape) != 2:
+        raise Fp8mpError(ERR_INVALID, f"dy must be [M, K], got {tuple(shape)}")
+    M, K = shape
+    if dw is not None and workspace is None:
+        raise Fp8mpError(ERR_INVALID, "dw needs a workspace")
+    like = (total.dtype,)
+    pdy, pt, pw, pr, pdr, pdw, pws, pdt, pdx, st = _addresses((
+        (dy, "dy", None, _HIGH), (total, "total", shape, _HIGH), (w, "w", (K,), _HIGH), (rstd, "rstd", (M,), _F32),
+        (dresidual, "dresidual", shape, like), (dw, "dw", (K,), _HIGH), (workspace, "workspace", None, _U8),
+        (dtotal, "dtotal", shape, like), (dx, "dx", shape, (dy.dtype,))), stream)
+    _check(load().fp8_rmsnorm_bwd(pdy, _CODE[dy.dtype], pdt, pt, _CODE[total.dtype], pr, M, K, pw, _CODE[w.dtype], pdr, pdx,
+                                  pdw, F32 if dw is None else _CODE[dw.dtype], pws,
+                                  0 if workspace is None else workspace.numel(), st))
 
 
 def _logits(logits: torch.Tensor, vocab: int | None):
     if logits.dim() != 2:
         raise Fp8mpError(ERR_INVALID, f"logits must be [M, columns], got {tuple(logits.shape)}")
-    _shape(logits, "logits", tuple(logits.shape), *_HIGH)
     M, ld = logits.shape
     V = ld if vocab is None else int(vocab)
     if not 1 <= V <= ld:
@@ -778,27 +779,19 @@ def mp_logprobs_fwd(logits: torch.Tensor, targets: torch.Tensor | None, logprob:
     top_id.shape[1] (at most MAX_TOP) most probable tokens and their log p, of equal
     logits the lower index first."""
     M, V, ld = _logits(logits, vocab)
-    _shape(stats, "stats", (M, 2), *_F32)
-    if (targets is None) != (logprob is None):
-        raise Fp8mpError(ERR_INVALID, "targets and logprob come together")
-    if targets is not None:
-        _shape(targets, "targets", (M,), torch.int64)
-        _shape(logprob, "logprob", (M,), *_F32)
-    if entropy is not None:
-        _shape(entropy, "entropy", (M,), *_F32)
-    if (top_logprob is None) != (top_id is None):
-        raise Fp8mpError(ERR_INVALID, "top_logprob and top_id come together")
+    if (targets is None) != (logprob is None) or (top_logprob is None) != (top_id is None):
+        raise Fp8mpError(ERR_INVALID, "targets and logprob, top_logprob and top_id come together")
     top = 0
     if top_id is not None:
-        if top_id.dim() != 2:
-            raise Fp8mpError(ERR_INVALID, f"top_id must be [M, top], got {tuple(top_id.shape)}")
-        top = top_id.shape[1]
-        _shape(top_id, "top_id", (M, top), torch.int64)
-        _shape(top_logprob, "top_logprob", (M, top), *_F32)
-    _like("logits", logits.device, targets=targets, logprob=logprob, stats=stats, entropy=entropy,
-          top_logprob=top_logprob, top_id=top_id)
-    _check(load().mp_logprobs_fwd(_ptr(logits), _dtype_code(logits), M, V, ld, _ptr(targets), _ptr(logprob), _ptr(stats),
-                                  _ptr(entropy), _ptr(top_logprob), _ptr(top_id), top, _stream(stream)))
+        top = top_id.shape[-1] if top_id.dim() == 2 else -1
+        if not 0 <= top <= min(MAX_TOP, V):
+            raise Fp8mpError(ERR_INVALID, f"top_id must be [M, 0..{min(MAX_TOP, V)}], got {tuple(top_id.shape)}")
+    row = (M,)
+    px, pt, pl, ps, pe, pv, pi, st = _addresses((
+        (logits, "logits", None, _HIGH), (targets, "targets", row, _I64), (logprob, "logprob", row, _F32),
+        (stats, "stats", (M, 2), _F32), (entropy, "entropy", row, _F32), (top_logprob, "top_logprob", (M, top), _F32),
+        (top_id, "top_id", (M, top), _I64)), stream)
+    _check(load().mp_logprobs_fwd(px, _CODE[logits.dtype], M, V, ld, pt, pl, ps, pe, pv, pi, top, st))
 
 
 def mp_logprobs_bwd(logits: torch.Tensor, targets: torch.Tensor, stats: torch.Tensor, dlogprob: torch.Tensor,
@@ -810,40 +803,33 @@ def mp_logprobs_bwd(logits: torch.Tensor, targets: torch.Tensor, stats: torch.Te
     itself, or E5M2 codes (uint8) under scale, with amax = max(amax, max|gradient|).
     Columns from `vocab` on get 0."""
     M, V, ld = _logits(logits, vocab)
-    _shape(targets, "targets", (M,), torch.int64)
-    _shape(stats, "stats", (M, 2), *_F32)
-    _shape(dlogprob, "dlogprob", (M,), *_F32)
-    _shape(dlogits, "dlogits", (M, ld), torch.uint8 if scale is not None else logits.dtype)
     if (entropy is None) != (dentropy is None):
         raise Fp8mpError(ERR_INVALID, "entropy and dentropy come together")
-    if entropy is not None:
-        _shape(entropy, "entropy", (M,), *_F32)
-        _shape(dentropy, "dentropy", (M,), *_F32)
-    for name, t in (("scale", scale), ("amax", amax)):
-        if t is not None:
-            _expect(t, name, torch.float32, 1)
-    _like("logits", logits.device, targets=targets, stats=stats, dlogprob=dlogprob, dlogits=dlogits, entropy=entropy,
-          dentropy=dentropy, scale=scale, amax=amax)
-    _check(load().mp_logprobs_bwd(_ptr(logits), _dtype_code(logits), M, V, ld, _ptr(targets), _ptr(stats),
-                                  _ptr(dlogprob), _ptr(entropy), _ptr(dentropy), _ptr(scale), _ptr(dlogits), _ptr(amax),
-                                  _stream(stream)))
+    row = (M,)
+    px, pt, ps, pa, pd, pe, pb, pc, pm, st = _addresses((
+        (logits, "logits", None, _HIGH), (targets, "targets", row, _I64), (stats, "stats", (M, 2), _F32),
+        (dlogprob, "dlogprob", row, _F32), (dlogits, "dlogits", (M, ld), (logits.dtype,) if scale is None else _U8),
+        (entropy, "entropy", row, _F32), (dentropy, "dentropy", row, _F32), (scale, "scale", (1,), _F32),
+        (amax, "amax", (1,), _F32)), stream)
+    _check(load().mp_logprobs_bwd(px, _CODE[logits.dtype], M, V, ld, pt, ps, pa, pe, pb, pc, pd, pm, st))
+
+
+def _table(ids: torch.Tensor, table: torch.Tensor, name: str):
+    if table.dim() != 2 or ids.dim() != 1:
+        raise Fp8mpError(ERR_INVALID, f"{name} must be [V, K] and ids [M], got {tuple(table.shape)}, {tuple(ids.shape)}")
+    return ids.shape[0], *table.shape
 
 
 def mp_embedding_fwd(ids: torch.Tensor, table: torch.Tensor, out: torch.Tensor, scale: float = 1.0,
                      sinv: torch.Tensor | None = None, stream=None) -> None:
     """out[m] = table[ids[m]] * scale (ids int64 [M]; zeros where an id is not in
     0..V-1). table [V, K]: bf16, fp32, or E4M3 codes (uint8) whose values sinv scales."""
-    if table.dim() != 2 or ids.dim() != 1:
-        raise Fp8mpError(ERR_INVALID, f"table must be [V, K] and ids [M], got {tuple(table.shape)}, {tuple(ids.shape)}")
-    (V, K), M = table.shape, ids.shape[0]
-    _shape(ids, "ids", (M,), torch.int64)
-    _shape(table, "table", (V, K), *((torch.uint8,) if sinv is not None else _HIGH))
-    _shape(out, "out", (M, K), *_HIGH)
-    if sinv is not None:
-        _expect(sinv, "sinv", torch.float32, 1)
-    _like("ids", ids.device, table=table, out=out, sinv=sinv)
-    _check(load().mp_embedding_fwd(_ptr(ids), M, _ptr(table), F32 if sinv is not None else _dtype_code(table), V, K,
-                                   _ptr(sinv), float(scale), _ptr(out), _dtype_code(out), _stream(stream)))
+    M, V, K = _table(ids, table, "table")
+    pi, pt, po, ps, st = _addresses((
+        (ids, "ids", None, _I64), (table, "table", None, _HIGH if sinv is None else _U8), (out, "out", (M, K), _HIGH),
+        (sinv, "sinv", (1,), _F32)), stream)
+    _check(load().mp_embedding_fwd(pi, M, pt, F32 if sinv is not None else _CODE[table.dtype], V, K, ps, scale, po,
+                                   _CODE[out.dtype], st))
 
 
 def mp_embedding_bwd_workspace_bytes(M: int, V: int, K: int) -> int:
@@ -853,17 +839,14 @@ def mp_embedding_bwd_workspace_bytes(M: int, V: int, K: int) -> int:
 def mp_embedding_bwd(ids: torch.Tensor, dy: torch.Tensor, dtable: torch.Tensor, workspace: torch.Tensor,
                      scale: float = 1.0, stream=None) -> None:
     """dtable[v] = scale * (sum of the dy[m] with ids[m] == v), for every row v of
-    dtable [V, K]; the same bits at every call. workspace: at least
-    mp_embedding_bwd_workspace_bytes(M, V, K) bytes."""
-    if dtable.dim() != 2 or ids.dim() != 1:
-        raise Fp8mpError(ERR_INVALID, f"dtable must be [V, K] and ids [M], got {tuple(dtable.shape)}, {tuple(ids.shape)}")
-    (V, K), M = dtable.shape, ids.shape[0]
-    _shape(ids, "ids", (M,), torch.int64)
-    _shape(dy, "dy", (M, K), *_HIGH)
-    _shape(dtable, "dtable", (V, K), *_HIGH)
-    _like("ids", ids.device, dy=dy, dtable=dtable, workspace=workspace)
-    _check(load().mp_embedding_bwd(_ptr(ids), M, _ptr(dy), _dtype_code(dy), V, K, float(scale), _ptr(dtable),
-                                   _dtype_code(dtable), *_workspace(workspace), _stream(stream)))
+    dtable [V, K]; the same bits at every call. workspace (uint8): at least
+    mp_embedding_bwd_workspace_bytes(M, V, K)."""
+    M, V, K = _table(ids, dtable, "dtable")
+    pi, pd, pt, pw, st = _addresses((
+        (ids, "ids", None, _I64), (dy, "dy", (M, K), _HIGH), (dtable, "dtable", None, _HIGH),
+        (workspace, "workspace", None, _U8)), stream)
+    _check(load().mp_embedding_bwd(pi, M, pd, _CODE[dy.dtype], V, K, scale, pt, _CODE[dtable.dtype], pw, workspace.numel(),
+                                   st))
 
 
 def fp8mp_check(stream=None) -> int:

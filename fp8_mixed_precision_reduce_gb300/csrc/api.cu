@@ -1096,7 +1096,7 @@ int fp8_rmsnorm_bwd(const void *dy, int32_t dy_dtype, const void *dtotal, const 
     rc = current_device(&dev);
     if (rc) return rc;
     return launch_rmsnorm_bwd(dy, dy_dtype, dtotal, total, t_dtype, rstd, M, K, w, w_dtype, dresidual, dx, dw, dw_dtype,
-                              workspace, static_cast<cudaStream_t>(stream));
+                              workspace, static_cast<cudaStream_t>(stream), dev);
 }
 
 static int check_logits(const char *fn, const void *logits, int32_t x_dtype, int64_t M, int64_t V, int64_t ld) {
@@ -1173,7 +1173,7 @@ static bool valid_table_dims(int64_t M, int64_t V, int64_t K) {
 }
 
 int64_t mp_embedding_bwd_workspace_bytes(int64_t M, int64_t V, int64_t K) {
-    return valid_table_dims(M, V, K) ? embedding_workspace_bytes(M, V, K) : -1;
+    return valid_table_dims(M, V, K) ? embedding_workspace_bytes(M, K) : -1;
 }
 
 static int check_table(const char *fn, const int64_t *ids, int64_t M, int64_t V, int64_t K) {
@@ -1216,9 +1216,9 @@ int mp_embedding_bwd(const int64_t *ids, int64_t M, const void *dy, int32_t dy_d
     if (V == 0 || K == 0) return FP8MP_OK;
     CHECK_PTR(dy, M > 0);
     CHECK_PTR(dtable, true);
-    CHECK_PTR(workspace, true);
-    REQUIRE(workspace_bytes >= embedding_workspace_bytes(M, V, K), "%s: workspace of %lld bytes, %lld needed", fn,
-            (long long)workspace_bytes, (long long)embedding_workspace_bytes(M, V, K));
+    CHECK_PTR(workspace, M > 0);
+    REQUIRE(workspace_bytes >= embedding_workspace_bytes(M, K), "%s: workspace of %lld bytes, %lld needed", fn,
+            (long long)workspace_bytes, (long long)embedding_workspace_bytes(M, K));
     REQUIRE(M == 0 || !overlap(dy, M * K * width(dy_dtype), dtable, V * K * width(dtable_dtype)),
             "%s: dy and dtable overlap", fn);
     DeviceInfo dev;

@@ -6,16 +6,21 @@
 // Backward: dtable[v] = scale (sum over the m with id_m = v of dy[m]), for every v: the
 // whole table is written, zeros mostly, which is what bounds it. The tokens are sorted
 // first, by (id, position), so that each row's sum has one order and no atomics:
-//   1. sort: a stable radix sort of 9 bits a pass by one cluster of 8 CTAs. A warp
-//      owns a run of consecutive positions and a histogram of its own; counts are
-//      joined over the warps in shared memory and over the CTAs through distributed
-//      shared memory. It also marks the ids that occur in a bitmap.
-//   2. sum: the sorted tokens in chunks of equal length, whatever their ids, so that
+//   1. sort: a stable radix sort of at most 9 bits a pass. A warp owns a run of
+//      consecutive positions and a histogram of its own. Up to 16384 tokens are sorted
+//      by one block in its shared memory, id and position in one word; more by a
+//      cluster of 8 CTAs, whose counts are joined through distributed shared memory.
+//   2. zero: every block looks through the ids for those among its rows and zeroes the
+//      others. It runs beside the one block's sort, which hardly touches global memory
+//      (the cluster's, whose every pass does, took 4 times as long beside it).
+//   3. sum: the sorted tokens in chunks of equal length, whatever their ids, so that
 //      an id that half of the batch holds is no one's long tail: a thread adds eight
 //      columns over a chunk in fp32 and writes a row where its id's run lies within the
-//      chunk, else a partial sum. The rows of ids that do not occur are zeroed.
-//   3. join: the partial sums of each run over several chunks, in their order.
+//      chunk, else a partial sum.
+//   4. join: the partial sums of each run over several chunks, in their order.
 // Ids outside 0 .. V - 1 sort last and have no row.
+#include <atomic>
+
 #include "fp8mp_async.cuh"
 #include "fp8mp_pieces.cuh"
 
@@ -25,11 +30,13 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kSortCtas = 8, kSortThreads = 512, kSortWarps = kSortThreads / 32;
+constexpr int kZeroThreads = 512, kZeroBatch = 8;
 constexpr int kDigitBits = 9, kBins = 1 << kDigitBits;
 constexpr int kBatch = 8;           // keys that a lane has in flight
-constexpr int kMinChunk = 16;       // tokens of a chunk, at least
-constexpr int kMaxChunks = 1024;
-constexpr int kZeroRows = 8;        // rows that a block zeroes at a time
+constexpr int kMinChunk = 4;        // tokens of a chunk, at least
+constexpr int64_t kSumItems = 1024 * 152;  // chunks times pieces of a row, about, where the chunks are longer
+constexpr uint32_t kZeroRows = 8;     // rows that a block zeroes in a row
+constexpr uint32_t kWindow = 32 * 4096;  // rows whose marks it holds at a time
 static_assert(kBins == kSortThreads, "a thread for each bin");
 
 // ----------------------------------------------------------------- forward
@@ -40,9 +47,8 @@ struct EmbedArgs {
     const float *sinv;
     void *out;
     int64_t M, V;
-    int units;  // of 16 columns
+    int units;  // 16-byte units of an output row
     float scale;
-    bool out_bf16;
 };
 
 __device__ __forceinline__ void e4m3_pairs(uint32_t codes, uint64_t &lo, uint64_t &hi) {
@@ -61,42 +67,83 @@ __device__ __forceinline__ void e4m3_pairs(uint32_t codes, uint64_t &lo, uint64_
     hi = wide(h1);
 }
 
-// TABLE: 0 E4M3, 1 bf16, 2 fp32. A thread moves 16 columns of a row.
-template <int TABLE>
+// TABLE: 0 E4M3, 1 bf16, 2 fp32. A thread writes 16 bytes of each of kRows rows (8 bf16
+// or 4 fp32 columns, so that a warp's store covers whole lines), whose ids and then
+// whose columns are in flight together.
+constexpr int kRows = 4;
+
+template <int BYTES>
+__device__ __forceinline__ void load_words(uint32_t (&w)[BYTES / 4], const uint8_t *p) {
+    if constexpr (BYTES == 4) {
+        w[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+    } else if constexpr (BYTES == 8) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
+        w[0] = v.x;
+        w[1] = v.y;
+    } else {
+#pragma unroll
+        for (int j = 0; j < BYTES / 16; ++j) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + j);
+            w[4 * j] = v.x;
+            w[4 * j + 1] = v.y;
+            w[4 * j + 2] = v.z;
+            w[4 * j + 3] = v.w;
+        }
+    }
+}
+
+template <int TABLE, bool OBF>
 __global__ void __launch_bounds__(kThreads) embed_fwd_kernel(const EmbedArgs a) {
+    constexpr int COLS = OBF ? 8 : 4, BYTES = COLS * (TABLE == 0 ? 1 : TABLE == 1 ? 2 : 4);
     pdl_wait();
     pdl_launch_dependents();
     const float factor = TABLE == 0 ? __ldg(a.sinv) * a.scale : a.scale;
-    const uint64_t f2 = f2_same(factor);
-    const int64_t items = a.M * a.units, step = static_cast<int64_t>(gridDim.x) * kThreads;
-    for (int64_t it = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; it < items; it += step) {
-        const int64_t m = it / a.units;
-        const int64_t unit = it - m * a.units;
-        const int64_t id = __ldg(a.ids + m);
-        uint64_t v[2][4] = {};
-        if (id >= 0 && id < a.V) {
-            const int64_t at = id * a.units + unit;
-            if constexpr (TABLE == 0) {
-                const uint4 q = __ldg(reinterpret_cast<const uint4 *>(a.table) + at);
-                e4m3_pairs(q.x, v[0][0], v[0][1]);
-                e4m3_pairs(q.y, v[0][2], v[0][3]);
-                e4m3_pairs(q.z, v[1][0], v[1][1]);
-                e4m3_pairs(q.w, v[1][2], v[1][3]);
-            } else {
-                const Piece<TABLE == 1> p = load_piece<TABLE == 1>(a.table, 2 * at), r = load_piece<TABLE == 1>(a.table, 2 * at + 1);
+    const int64_t items = a.M * a.units, first = static_cast<int64_t>(blockIdx.x) * (kThreads * kRows) + threadIdx.x;
+    int64_t at[kRows];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    v[0][j] = p.pair(j);
-                    v[1][j] = r.pair(j);
+    for (int r = 0; r < kRows; ++r) {
+        const int64_t it = first + r * kThreads;
+        at[r] = -1;
+        if (it < items) {
+            const int64_t m = items <= 0xFFFFFFFFll ? static_cast<uint32_t>(it) / static_cast<uint32_t>(a.units) : it / a.units;
+            const int64_t id = __ldg(a.ids + m);
+            if (id >= 0 && id < a.V) at[r] = id * a.units + (it - m * a.units);
+        }
+    }
+    uint32_t q[kRows][BYTES / 4];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+        if (at[r] >= 0) load_words<BYTES>(q[r], a.table + at[r] * BYTES);
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+        const int64_t it = first + r * kThreads;
+        if (it >= items) break;
+        uint32_t o[4] = {0u, 0u, 0u, 0u};
+        if (at[r] >= 0) {
+            uint64_t v[COLS / 2];
+#pragma unroll
+            for (int j = 0; j < COLS / 2; ++j) {
+                if constexpr (TABLE == 0) {
+                    if ((j & 1) == 0) e4m3_pairs(q[r][j / 2], v[j], v[j + 1]);
+                } else if constexpr (TABLE == 1) {
+                    v[j] = f2_from_bits(q[r][j] << 16, q[r][j] & 0xFFFF0000u);
+                } else {
+                    v[j] = f2_from_bits(q[r][2 * j], q[r][2 * j + 1]);
                 }
             }
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[h][j] = f2_mul(v[h][j], f2);
+            for (int j = 0; j < COLS / 2; ++j) {
+                float lo, hi;
+                f2_split(f2_mul(v[j], f2_same(factor)), lo, hi);
+                if constexpr (OBF) {
+                    o[j] = bf16_pair(lo, hi);
+                } else {
+                    o[2 * j] = __float_as_uint(lo);
+                    o[2 * j + 1] = __float_as_uint(hi);
+                }
+            }
         }
-        store_rounded(a.out, 2 * it, v[0], a.out_bf16);
-        store_rounded(a.out, 2 * it + 1, v[1], a.out_bf16);
+        reinterpret_cast<uint4 *>(a.out)[it] = make_uint4(o[0], o[1], o[2], o[3]);
     }
 }
 
@@ -105,15 +152,81 @@ __global__ void __launch_bounds__(kThreads) embed_fwd_kernel(const EmbedArgs a) 
 struct SortArgs {
     const int64_t *ids;
     uint32_t *key[2], *pos[2];
-    uint32_t *bitmap;
     int64_t M, V;
     int passes;
 };
+
+struct ZeroArgs {
+    const int64_t *ids;
+    uint4 *table;  // the gradient
+    int64_t M, V;
+    int row;       // 16-byte units of a row of it
+};
+
+// Block b of B zeroes its rows, kZeroRows of every B * kZeroRows, but for those whose
+// ids occur: it marks them in shared memory, kWindow of its rows at a time. EARLY: it
+// runs beside the kernel before it, whose arrays it does not touch and which lets it
+// start when whatever came before is complete; it waits for it at its end.
+template <bool EARLY>
+__global__ void __launch_bounds__(kZeroThreads, 2) embed_zero_kernel(const ZeroArgs a) {
+    __shared__ uint32_t marks[kWindow / 32 + 1];
+    if constexpr (!EARLY) {
+        pdl_wait();
+        pdl_launch_dependents();
+    }
+    const int across = a.row < kZeroThreads ? a.row : kZeroThreads, down = kZeroThreads / across;
+    const int r0 = threadIdx.x / across, p0 = threadIdx.x - r0 * across;
+    // its groups of rows: part, part + parts, ..
+    const uint32_t part = blockIdx.x, parts = gridDim.x;
+    const uint32_t groups = static_cast<uint32_t>((a.V + kZeroRows - 1) / kZeroRows);
+    const uint32_t mine = groups > part ? (groups - part + parts - 1) / parts * kZeroRows : 0u;
+    for (uint32_t first = 0; first < mine; first += kWindow) {
+        const uint32_t rows = mine - first < kWindow ? mine - first : kWindow;
+        __syncthreads();
+        for (uint32_t i = threadIdx.x; i < rows / 32 + 1; i += kZeroThreads) marks[i] = 0u;
+        __syncthreads();
+        for (int64_t i = threadIdx.x; i < a.M; i += kZeroThreads * kZeroBatch) {
+            int64_t id[kZeroBatch];
+#pragma unroll
+            for (int j = 0; j < kZeroBatch; ++j) id[j] = i + j * kZeroThreads < a.M ? __ldg(a.ids + i + j * kZeroThreads) : -1;
+#pragma unroll
+            for (int j = 0; j < kZeroBatch; ++j) {
+                if (id[j] < 0 || id[j] >= a.V) continue;
+                const uint32_t group = static_cast<uint32_t>(id[j]) / kZeroRows, turn = group / parts;
+                const uint32_t at = turn * kZeroRows + static_cast<uint32_t>(id[j]) % kZeroRows - first;
+                if (group - turn * parts == part && at < rows) atomicOr(&marks[at >> 5], 1u << (at & 31));
+            }
+        }
+        __syncthreads();
+        for (uint32_t r = r0; r < rows && r0 < down; r += down) {
+            const uint32_t n = first + r;
+            const int64_t v = static_cast<int64_t>(n / kZeroRows * parts + part) * kZeroRows + n % kZeroRows;
+            if (v >= a.V || marks[r >> 5] >> (r & 31) & 1u) continue;
+            for (int p = p0; p < a.row; p += across) a.table[v * a.row + p] = make_uint4(0, 0, 0, 0);
+        }
+    }
+    if constexpr (EARLY) {
+        pdl_wait();
+        pdl_launch_dependents();
+    }
+}
 
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
     uint32_t v;
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
     return v;
+}
+
+// The lanes whose digit is this one's. (A vote for each bit: __match_any_sync, slow where
+// many lanes differ, made the sort of 32768 tokens 60 us.)
+__device__ __forceinline__ uint32_t lanes_with(uint32_t digit, int bits, bool in) {
+    uint32_t peers = __ballot_sync(0xffffffffu, in);
+    for (int b = 0; b < bits; ++b) {
+        const bool one = digit >> b & 1u;
+        const uint32_t ones = __ballot_sync(0xffffffffu, one);
+        peers &= one ? ones : ~ones;
+    }
+    return peers;
 }
 
 // Sorted keys and positions end up in key[passes & 1], pos[passes & 1].
@@ -130,12 +243,11 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const SortA
     const int64_t run = ((a.M + kSortCtas * kSortWarps - 1) / (kSortCtas * kSortWarps) + 31) / 32 * 32;
     const int64_t first = (rank * kSortWarps + warp) * run;
     const int64_t last = first + run < a.M ? first + run : a.M;
-    const int64_t words = (a.V + 31) / 32;
-    for (int64_t i = rank * kSortThreads + tid; i < words; i += kSortCtas * kSortThreads) a.bitmap[i] = 0u;
     for (int pass = 0; pass < a.passes; ++pass) {
         const int shift = pass * kDigitBits;
-        const uint32_t *key_in = a.key[pass & 1], *pos_in = a.pos[pass & 1];
-        uint32_t *key_out = a.key[~pass & 1], *pos_out = a.pos[~pass & 1];
+        const bool odd = pass & 1;  // (no index into the parameters: they would be copied to the stack)
+        const uint32_t *key_in = odd ? a.key[1] : a.key[0], *pos_in = odd ? a.pos[1] : a.pos[0];
+        uint32_t *key_out = odd ? a.key[0] : a.key[1], *pos_out = odd ? a.pos[0] : a.pos[1];
         const auto key_at = [&](int64_t i) {
             if (pass > 0) return __ldcg(key_in + i);
             const int64_t id = __ldg(a.ids + i);
@@ -143,22 +255,28 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const SortA
         };
         for (int w = 0; w < kSortWarps; ++w) hist[w][tid] = 0u;
         __syncthreads();
-        for (int64_t i = first; i < last; i += 32 * kBatch) {
-            uint32_t k[kBatch];
+        uint32_t k[kBatch], p[kBatch];
+        const auto load = [&](int64_t i) {
 #pragma unroll
-            for (int j = 0; j < kBatch; ++j)
-                if (i + j * 32 + lane < last) k[j] = key_at(i + j * 32 + lane);
+            for (int j = 0; j < kBatch; ++j) {
+                const int64_t at = i + j * 32 + lane;
+                if (at >= last) continue;
+                k[j] = key_at(at);
+                p[j] = pass > 0 ? __ldcg(pos_in + at) : static_cast<uint32_t>(at);
+            }
+        };
+        for (int64_t i = first; i < last; i += 32 * kBatch) {
+            load(i);
 #pragma unroll
             for (int j = 0; j < kBatch; ++j)
                 if (i + j * 32 + lane < last) atomicAdd(&hist[warp][k[j] >> shift & (kBins - 1)], 1u);
         }
         __syncthreads();
-        uint32_t sum = 0;
-        for (int w = 0; w < kSortWarps; ++w) {
-            const uint32_t c = hist[w][tid];
-            hist[w][tid] = sum;
-            sum += c;
-        }
+        uint32_t count[kSortWarps], sum = 0;
+#pragma unroll
+        for (int w = 0; w < kSortWarps; ++w) count[w] = hist[w][tid];
+#pragma unroll
+        for (int w = 0; w < kSortWarps; ++w) sum += count[w];
         total[tid] = sum;
         cluster_sync_all();
         uint32_t before = 0, all = 0;
@@ -178,23 +296,18 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const SortA
         __syncthreads();
         uint32_t base = before + upto - all;
         for (int w = 0; w < warp; ++w) base += scan[w];
-        for (int w = 0; w < kSortWarps; ++w) hist[w][tid] += base;
+#pragma unroll
+        for (int w = 0; w < kSortWarps; ++w) {
+            hist[w][tid] = base;
+            base += count[w];
+        }
         __syncthreads();
         for (int64_t i = first; i < last; i += 32 * kBatch) {
-            uint32_t k[kBatch], p[kBatch];
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-                const int64_t at = i + j * 32 + lane;
-                if (at < last) {
-                    k[j] = key_at(at);
-                    p[j] = pass > 0 ? __ldcg(pos_in + at) : static_cast<uint32_t>(at);
-                }
-            }
+            if (run > 32 * kBatch) load(i);  // (else they are still there)
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
                 const bool in = i + j * 32 + lane < last;
-                const uint32_t digit = in ? k[j] >> shift & (kBins - 1) : kBins;
-                const uint32_t peers = __match_any_sync(0xffffffffu, digit);
+                const uint32_t digit = in ? k[j] >> shift & (kBins - 1) : 0u, peers = lanes_with(digit, kDigitBits, in);
                 uint32_t to = 0;
                 if (in) to = hist[warp][digit] + __popc(peers & ((1u << lane) - 1u));
                 __syncwarp();
@@ -203,7 +316,6 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const SortA
                 if (in) {
                     key_out[to] = k[j];
                     pos_out[to] = p[j];
-                    if (pass == 0 && k[j] < none) atomicOr(a.bitmap + (k[j] >> 5), 1u << (k[j] & 31));
                 }
             }
         }
@@ -211,11 +323,99 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const SortA
     }
 }
 
+// The sort of up to kOneMost tokens by one block: words of (key, position), the key
+// above `low` bits of position, in registers while they change places in shared memory.
+constexpr int kOneThreads = 1024, kOneWarps = kOneThreads / 32, kOneEach = 16;
+constexpr int kOneMost = kOneThreads * kOneEach;
+constexpr int kOneSmem = (kOneMost + kOneWarps * kBins) * 4;
+
+__global__ void __launch_bounds__(kOneThreads, 1) embed_sort_one_kernel(const SortArgs a, int low, int digit_bits) {
+    extern __shared__ uint32_t sorted[];  // a word for each token, then a histogram for each warp
+    __shared__ uint32_t scan[kOneWarps];
+    pdl_wait();
+    pdl_launch_dependents();
+    uint32_t *hist = sorted + kOneMost;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int M = static_cast<int>(a.M), rounds = (M + kOneThreads - 1) / kOneThreads;
+    const int first = warp * rounds * 32 + lane;  // a warp's words: consecutive
+    const uint32_t bins = 1u << digit_bits, mask = bins - 1u;
+    uint32_t w[kOneEach];
+#pragma unroll
+    for (int j = 0; j < kOneEach; ++j) {
+        const int i = first + j * 32;
+        if (j >= rounds || i >= M) continue;
+        const int64_t id = __ldg(a.ids + i);
+        w[j] = static_cast<uint32_t>(id >= 0 && id < a.V ? id : a.V) << low | static_cast<uint32_t>(i);
+    }
+    uint32_t *mine = hist + warp * kBins;
+    for (int pass = 0; pass < a.passes; ++pass) {
+        const int shift = low + pass * digit_bits;
+        for (uint32_t i = lane; i < bins; i += 32) mine[i] = 0u;
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < kOneEach; ++j)
+            if (j < rounds && first + j * 32 < M) atomicAdd(&mine[w[j] >> shift & mask], 1u);
+        __syncthreads();
+        // a pair of threads for each bin: where each warp's words of it go
+        const uint32_t bin = tid >> 1, half = tid & 1;
+        uint32_t *column = hist + half * (kOneWarps / 2) * kBins + bin;
+        uint32_t count[kOneWarps / 2], sum = 0;
+#pragma unroll
+        for (int k = 0; k < kOneWarps / 2; ++k) count[k] = bin < bins ? column[k * kBins] : 0u;
+#pragma unroll
+        for (int k = 0; k < kOneWarps / 2; ++k) sum += count[k];
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, sum, 1), all = sum + other;
+        uint32_t upto = half == 0 ? all : 0u;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        if (lane == 31) scan[warp] = upto;
+        __syncthreads();
+        uint32_t before = lane < warp ? scan[lane] : 0u;
+        before = __reduce_add_sync(0xffffffffu, before);
+        uint32_t base = before + upto - all + (half == 1 ? other : 0u);
+        if (bin < bins) {
+#pragma unroll
+            for (int k = 0; k < kOneWarps / 2; ++k) {
+                column[k * kBins] = base;
+                base += count[k];
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kOneEach; ++j) {
+            if (j >= rounds) break;
+            const bool in = first + j * 32 < M;
+            const uint32_t digit = in ? w[j] >> shift & mask : 0u, peers = lanes_with(digit, digit_bits, in);
+            uint32_t to = 0;
+            if (in) to = mine[digit] + __popc(peers & ((1u << lane) - 1u));
+            __syncwarp();
+            if (in && lane == __ffs(peers) - 1) mine[digit] += __popc(peers);
+            __syncwarp();
+            if (in) sorted[to] = w[j];
+        }
+        __syncthreads();
+        if (pass + 1 < a.passes) {
+#pragma unroll
+            for (int j = 0; j < kOneEach; ++j)
+                if (j < rounds && first + j * 32 < M) w[j] = sorted[first + j * 32];
+        }
+        // (the next pass's first barrier parts these reads from its writes)
+    }
+    for (int i = tid; i < M; i += kOneThreads) {
+        const uint32_t v = sorted[i];
+        a.key[0][i] = v >> low;
+        a.pos[0][i] = v & ((1u << low) - 1u);
+    }
+}
+
 // --------------------------------------------------------------------- sum
 
 struct SumArgs {
     const void *dy;
-    const uint32_t *key, *pos, *bitmap;
+    const uint32_t *key, *pos;
     void *out;
     float *partial;  // [chunks][2][K]: of a run from before the chunk, of a run past its end
     int64_t M, V;
@@ -233,26 +433,36 @@ __device__ __forceinline__ void write_row(const SumArgs &a, uint32_t v, int piec
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) embed_sum_kernel(const SumArgs a) {
+__global__ void __launch_bounds__(kThreads, BF16 ? 4 : 3) embed_sum_kernel(const SumArgs a) {
     pdl_wait();
     pdl_launch_dependents();
     const uint32_t none = static_cast<uint32_t>(a.V);
-    const int64_t items = static_cast<int64_t>(a.chunks) * a.pieces, step = static_cast<int64_t>(gridDim.x) * kThreads;
-    for (int64_t it = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; it < items; it += step) {
+    const int64_t it = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    if (it < static_cast<int64_t>(a.chunks) * a.pieces) {
         const int c = static_cast<int>(it / a.pieces), piece = static_cast<int>(it - static_cast<int64_t>(c) * a.pieces);
         const int64_t i0 = c * a.chunk, i1 = i0 + a.chunk < a.M ? i0 + a.chunk : a.M;
         uint32_t now = __ldg(a.key + i0);
         bool whole = i0 == 0 || __ldg(a.key + i0 - 1) != now;  // the run starts in this chunk
         uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
         constexpr int kAhead = 4;
+        uint32_t next_key[kAhead], next_pos[kAhead];  // a batch ahead of the rows that they name
+        const auto look = [&](int64_t i) {
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                next_key[j] = i + j < i1 ? __ldg(a.key + i + j) : none;
+                next_pos[j] = i + j < i1 ? __ldg(a.pos + i + j) : 0u;
+            }
+        };
+        look(i0);
         for (int64_t i = i0; i < i1 && now != none; i += kAhead) {
             uint32_t key[kAhead];
             Piece<BF16> d[kAhead];
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
-                key[j] = i + j < i1 ? __ldg(a.key + i + j) : none;
-                if (key[j] != none) d[j] = load_piece<BF16>(a.dy, static_cast<int64_t>(__ldg(a.pos + i + j)) * a.pieces + piece);
+                key[j] = next_key[j];
+                if (key[j] != none) d[j] = load_piece<BF16>(a.dy, static_cast<int64_t>(next_pos[j]) * a.pieces + piece);
             }
+            look(i + kAhead);
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
                 if (i + j >= i1) break;
@@ -275,20 +485,6 @@ __global__ void __launch_bounds__(kThreads) embed_sum_kernel(const SumArgs a) {
             else store_piece<false>(a.partial, (2ll * c + (whole ? 1 : 0)) * a.pieces + piece, round_piece<false>(sum));
         }
     }
-    // the rows of ids that do not occur
-    const int across = a.pieces < kThreads ? a.pieces : kThreads, down = kThreads / across;
-    const int r0 = threadIdx.x / across, p0 = threadIdx.x - r0 * across;
-    if (r0 >= down) return;
-    const uint64_t zero[4] = {0ull, 0ull, 0ull, 0ull};
-    const int64_t groups = (a.V + kZeroRows - 1) / kZeroRows;
-    for (int64_t g = blockIdx.x; g < groups; g += gridDim.x) {
-        const uint32_t bits = __ldg(a.bitmap + g * kZeroRows / 32) >> (g * kZeroRows & 31);
-        for (int r = r0; r < kZeroRows; r += down) {
-            const int64_t v = g * kZeroRows + r;
-            if (v >= a.V || bits >> r & 1u) continue;
-            for (int p = p0; p < a.pieces; p += across) store_rounded(a.out, v * a.pieces + p, zero, a.out_bf16);
-        }
-    }
 }
 
 // -------------------------------------------------------------------- join
@@ -301,64 +497,91 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(const SumArgs a) {
     if (it >= static_cast<int64_t>(a.chunks) * a.pieces) return;
     const int c = static_cast<int>(it / a.pieces), piece = static_cast<int>(it - static_cast<int64_t>(c) * a.pieces);
     // the run that the chunk ends in, if it starts in it and goes on
-    const int64_t end = (c + 1) * a.chunk;
+    const int64_t begin = c * a.chunk, end = begin + a.chunk;
     if (end >= a.M) return;
-    const uint32_t v = __ldg(a.key + end - 1);
-    if (v == none || __ldg(a.key + end) != v) return;
-    const int64_t begin = c * a.chunk;
-    if (__ldg(a.key + begin) == v && begin > 0 && __ldg(a.key + begin - 1) == v) return;
-    uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
-    int64_t row = 2ll * c + 1;
-    for (int next = c + 1;; ++next) {
-        const float4 *p = reinterpret_cast<const float4 *>(a.partial) + 2 * (row * a.pieces + piece);
-        const float4 x = __ldcg(p), y = __ldcg(p + 1);
-        sum[0] = f2_add(sum[0], f2_pack(x.x, x.y));
-        sum[1] = f2_add(sum[1], f2_pack(x.z, x.w));
-        sum[2] = f2_add(sum[2], f2_pack(y.x, y.y));
-        sum[3] = f2_add(sum[3], f2_pack(y.z, y.w));
-        if (next >= a.chunks || __ldg(a.key + next * a.chunk) != v) break;
-        row = 2ll * next;
+    const uint32_t v = __ldg(a.key + end - 1), after = __ldg(a.key + end), start = __ldg(a.key + begin),
+                   before = begin > 0 ? __ldg(a.key + begin - 1) : none;
+    if (v == none || after != v || (start == v && before == v)) return;
+    const float4 *partial = reinterpret_cast<const float4 *>(a.partial) + 2 * piece;
+    const auto part = [&](int64_t row, int h) { return __ldcg(partial + row * a.pieces * 2 + h); };
+    float4 x = part(2ll * c + 1, 0), y = part(2ll * c + 1, 1);
+    uint64_t sum[4] = {f2_pack(x.x, x.y), f2_pack(x.z, x.w), f2_pack(y.x, y.y), f2_pack(y.z, y.w)};
+    // the chunks that begin with it, some at a time so that their loads overlap
+    constexpr int kAhead = 8;
+    for (int next = c + 1; next < a.chunks; next += kAhead) {
+        bool more[kAhead];
+        float4 p[kAhead][2];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            more[j] = next + j < a.chunks && __ldg(a.key + (next + j) * a.chunk) == v;
+            if (next + j < a.chunks) {
+                p[j][0] = part(2ll * (next + j), 0);
+                p[j][1] = part(2ll * (next + j), 1);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            if (!more[j]) break;
+            sum[0] = f2_add(sum[0], f2_pack(p[j][0].x, p[j][0].y));
+            sum[1] = f2_add(sum[1], f2_pack(p[j][0].z, p[j][0].w));
+            sum[2] = f2_add(sum[2], f2_pack(p[j][1].x, p[j][1].y));
+            sum[3] = f2_add(sum[3], f2_pack(p[j][1].z, p[j][1].w));
+        }
+        if (!more[kAhead - 1]) break;
     }
     write_row(a, v, piece, sum);
 }
 
-// The workspace: keys and positions, each twice; the bitmap; the partial sums.
+cudaError_t sort_one(const SortArgs &so, int low, int digit_bits, cudaStream_t s, int device) {
+    static std::atomic<bool> ready[64];  // per device: the kernel may have its shared memory
+    std::atomic<bool> &mine = ready[device & 63];
+    if (!mine.load(std::memory_order_acquire)) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(embed_sort_one_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kOneSmem);
+        if (e != cudaSuccess) return e;
+        mine.store(true, std::memory_order_release);
+    }
+    return launch_kernel(embed_sort_one_kernel, dim3(1), dim3(kOneThreads), kOneSmem, s, so, low, digit_bits);
+}
+
+// The workspace: keys and positions, each twice; the partial sums.
 struct Layout {
-    int64_t chunk, chunks, bitmap, partial, bytes;
+    int64_t chunk, chunks, partial, bytes;
 };
 int64_t round16(int64_t n) { return (n + 15) / 16 * 16; }
-Layout layout_of(int64_t M, int64_t V, int64_t K) {
+Layout layout_of(int64_t M, int64_t K) {
     Layout l;
-    l.chunk = (M + kMaxChunks - 1) / kMaxChunks;
+    l.chunk = (M * (K / kPiece) + kSumItems - 1) / kSumItems;
     if (l.chunk < kMinChunk) l.chunk = kMinChunk;
     l.chunks = (M + l.chunk - 1) / l.chunk;
-    l.bitmap = 4 * round16(4 * M);
-    l.partial = l.bitmap + round16((V + 31) / 32 * 4);
+    l.partial = 4 * round16(4 * M);
     l.bytes = l.partial + 2 * l.chunks * K * 4;
     return l;
 }
 
 }  // namespace
 
-int64_t embedding_workspace_bytes(int64_t M, int64_t V, int64_t K) { return layout_of(M, V, K).bytes; }
+int64_t embedding_workspace_bytes(int64_t M, int64_t K) { return layout_of(M, K).bytes; }
 
 int launch_embedding_fwd(const int64_t *ids, int64_t M, const void *table, int table_kind, int64_t V, int64_t K,
                          const float *sinv, float scale, void *out, int out_dtype, cudaStream_t s, const DeviceInfo &dev) {
-    const EmbedArgs a = {ids, static_cast<const uint8_t *>(table), sinv, out, M, V, static_cast<int>(K / 16), scale,
-                         out_dtype == FP8MP_BF16};
-    const int64_t need = (M * a.units + kThreads - 1) / kThreads, most = 32ll * dev.num_sms;
-    const dim3 grid(static_cast<unsigned>(need < most ? need : most)), block(kThreads);
+    const bool bf16 = out_dtype == FP8MP_BF16;
+    const EmbedArgs a = {ids, static_cast<const uint8_t *>(table), sinv, out, M, V, static_cast<int>(K / (bf16 ? 8 : 4)), scale};
+    const dim3 grid(static_cast<unsigned>((M * a.units + kThreads * kRows - 1) / (kThreads * kRows))), block(kThreads);
     cudaError_t e;
-    if (table_kind == 0) e = launch_kernel(embed_fwd_kernel<0>, grid, block, 0, s, a);
-    else if (table_kind == 1) e = launch_kernel(embed_fwd_kernel<1>, grid, block, 0, s, a);
-    else e = launch_kernel(embed_fwd_kernel<2>, grid, block, 0, s, a);
+    if (table_kind == 0)
+        e = launch_kernel(bf16 ? embed_fwd_kernel<0, true> : embed_fwd_kernel<0, false>, grid, block, 0, s, a);
+    else if (table_kind == 1)
+        e = launch_kernel(bf16 ? embed_fwd_kernel<1, true> : embed_fwd_kernel<1, false>, grid, block, 0, s, a);
+    else
+        e = launch_kernel(bf16 ? embed_fwd_kernel<2, true> : embed_fwd_kernel<2, false>, grid, block, 0, s, a);
     if (e != cudaSuccess) return fail(FP8MP_ERR_LAUNCH, "embedding: launch failed: %s", cudaGetErrorString(e));
     return FP8MP_OK;
 }
 
 int launch_embedding_bwd(const int64_t *ids, int64_t M, const void *dy, int dy_dtype, int64_t V, int64_t K, float scale,
                          void *dtable, int out_dtype, void *workspace, cudaStream_t s, const DeviceInfo &dev) {
-    const Layout l = layout_of(M, V, K);
+    const Layout l = layout_of(M, K);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     SortArgs so = {};
     so.ids = ids;
@@ -367,17 +590,30 @@ int launch_embedding_bwd(const int64_t *ids, int64_t M, const void *dy, int dy_d
         so.key[i] = reinterpret_cast<uint32_t *>(ws + i * each);
         so.pos[i] = reinterpret_cast<uint32_t *>(ws + (2 + i) * each);
     }
-    so.bitmap = reinterpret_cast<uint32_t *>(ws + l.bitmap);
     so.M = M;
     so.V = V;
-    so.passes = 1;  // keys are 0 .. V
-    while (V >> (so.passes * kDigitBits) != 0) ++so.passes;
-    cudaError_t e = launch_kernel_cluster(embed_sort_kernel, dim3(kSortCtas), dim3(kSortThreads), 0, s, kSortCtas, so);
+    int key_bits = 1, low = 1;  // keys are 0 .. V, positions 0 .. M - 1
+    while (V >> key_bits != 0) ++key_bits;
+    while ((M - 1) >> low > 0) ++low;
+    so.passes = (key_bits + kDigitBits - 1) / kDigitBits;
+    const bool one = M <= kOneMost && key_bits + low <= 32;
+    ZeroArgs z = {ids, static_cast<uint4 *>(dtable), M, V, static_cast<int>(K * (out_dtype == FP8MP_BF16 ? 2 : 4) / 16)};
+    // two blocks an SM, but for the one that sorts; of at least 32 KB
+    const int64_t want = V * z.row / 2048 + 1, most = 2ll * (dev.num_sms - (one ? 1 : 0));
+    const dim3 zero_grid(static_cast<unsigned>(want < most ? want : most));
+    cudaError_t e = cudaSuccess;
+    if (one) {
+        const int digit_bits = (key_bits + so.passes - 1) / so.passes;
+        e = sort_one(so, low, digit_bits, s, dev.device);
+        if (e == cudaSuccess) e = launch_kernel(embed_zero_kernel<true>, zero_grid, dim3(kZeroThreads), 0, s, z);
+    } else {
+        e = launch_kernel_cluster(embed_sort_kernel, dim3(kSortCtas), dim3(kSortThreads), 0, s, kSortCtas, so);
+        if (e == cudaSuccess) e = launch_kernel(embed_zero_kernel<false>, zero_grid, dim3(kZeroThreads), 0, s, z);
+    }
     SumArgs a = {};
     a.dy = dy;
-    a.key = so.key[so.passes & 1];
-    a.pos = so.pos[so.passes & 1];
-    a.bitmap = so.bitmap;
+    a.key = so.key[one ? 0 : so.passes & 1];
+    a.pos = so.pos[one ? 0 : so.passes & 1];
     a.out = dtable;
     a.partial = reinterpret_cast<float *>(ws + l.partial);
     a.M = M;
@@ -387,10 +623,9 @@ int launch_embedding_bwd(const int64_t *ids, int64_t M, const void *dy, int dy_d
     a.pieces = static_cast<int>(K / kPiece);
     a.scale = scale;
     a.out_bf16 = out_dtype == FP8MP_BF16;
-    const int64_t items = l.chunks * a.pieces, groups = (V + kZeroRows - 1) / kZeroRows;
-    const int64_t blocks = (items + kThreads - 1) / kThreads, need = blocks > groups ? blocks : groups, most = 4ll * dev.num_sms;
-    const dim3 grid(static_cast<unsigned>(need < most ? need : most)), block(kThreads);
-    if (e == cudaSuccess)
+    const int64_t items = l.chunks * a.pieces, blocks = (items + kThreads - 1) / kThreads;
+    const dim3 grid(static_cast<unsigned>(blocks)), block(kThreads);
+    if (e == cudaSuccess && items > 0)
         e = dy_dtype == FP8MP_BF16 ? launch_kernel(embed_sum_kernel<true>, grid, block, 0, s, a)
                                    : launch_kernel(embed_sum_kernel<false>, grid, block, 0, s, a);
     if (e == cudaSuccess && l.chunks > 1)

@@ -233,14 +233,14 @@ int launch_rmsnorm_fwd(const void *x, int x_dtype, const void *r, void *t, int r
                        float *y_amax, float *rstd, cudaStream_t s, const DeviceInfo &dev);
 int launch_rmsnorm_bwd(const void *dy, int dy_dtype, const void *dtotal, const void *t, int t_dtype, const float *rstd,
                        int64_t M, int64_t K, const void *w, int w_dtype, void *dr, void *dx, void *dw, int dw_dtype,
-                       void *workspace, cudaStream_t s);
+                       void *workspace, cudaStream_t s, const DeviceInfo &dev);
 int launch_logprobs_fwd(const void *x, int x_dtype, int64_t M, int64_t V, int64_t ld, const int64_t *target,
                         float *logprob, float *stats, float *entropy, float *top, int64_t *ids, int k, cudaStream_t s,
                         const DeviceInfo &dev);
 int launch_logprobs_bwd(const void *x, int x_dtype, int64_t M, int64_t V, int64_t ld, const int64_t *target,
                         const float *stats, const float *dlogprob, const float *entropy, const float *dentropy,
                         const float *scale, void *dlogits, float *amax, cudaStream_t s, const DeviceInfo &dev);
-int64_t embedding_workspace_bytes(int64_t M, int64_t V, int64_t K);
+int64_t embedding_workspace_bytes(int64_t M, int64_t K);
 int launch_embedding_fwd(const int64_t *ids, int64_t M, const void *table, int table_kind, int64_t V, int64_t K,
                          const float *sinv, float scale, void *out, int out_dtype, cudaStream_t s, const DeviceInfo &dev);
 int launch_embedding_bwd(const int64_t *ids, int64_t M, const void *dy, int dy_dtype, int64_t V, int64_t K, float scale,

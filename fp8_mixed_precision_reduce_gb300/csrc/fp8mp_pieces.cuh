@@ -20,11 +20,22 @@ struct Piece {
     }
 };
 
-// Piece `i` of an array; read once.
+// Piece `i` of an array; read once. 32 bytes move as one access where they may, so
+// that a warp's covers whole lines.
 template <bool BF16>
 __device__ __forceinline__ Piece<BF16> load_piece(const void *x, int64_t i) {
     Piece<BF16> r;
     const uint4 *p = reinterpret_cast<const uint4 *>(x) + (BF16 ? i : 2 * i);
+    if constexpr (!BF16) {
+        if ((reinterpret_cast<uintptr_t>(p) & 31u) == 0) {
+            asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                         : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]), "=r"(r.w[5]),
+                           "=r"(r.w[6]), "=r"(r.w[7])
+                         : "l"(p)
+                         : "memory");
+            return r;
+        }
+    }
 #pragma unroll
     for (int j = 0; j < (BF16 ? 1 : 2); ++j) {
         const uint4 v = __ldcs(p + j);
@@ -63,6 +74,14 @@ __device__ __forceinline__ Piece<BF16> round_piece(const uint64_t (&v)[4]) {
 template <bool BF16>
 __device__ __forceinline__ void store_piece(void *x, int64_t i, const Piece<BF16> &r) {
     uint4 *p = reinterpret_cast<uint4 *>(x) + (BF16 ? i : 2 * i);
+    if constexpr (!BF16) {
+        if ((reinterpret_cast<uintptr_t>(p) & 31u) == 0) {
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r.w[0]), "r"(r.w[1]),
+                         "r"(r.w[2]), "r"(r.w[3]), "r"(r.w[4]), "r"(r.w[5]), "r"(r.w[6]), "r"(r.w[7])
+                         : "memory");
+            return;
+        }
+    }
 #pragma unroll
     for (int j = 0; j < (BF16 ? 1 : 2); ++j)
         p[j] = make_uint4(r.w[4 * j], r.w[4 * j + 1], r.w[4 * j + 2], r.w[4 * j + 3]);

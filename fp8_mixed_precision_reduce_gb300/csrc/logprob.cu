@@ -16,7 +16,7 @@
 // The k most probable tokens come out of the same pass. Each thread keeps the
 // largest logit of its share of the row; with tau the k-th largest of those, every
 // one of the k largest logits is at least tau, and only the shares whose largest is
-// can hold one: about k of 512, which are read again (from L2) by a warp each. What
+// can hold one: about k of 256, which are read again (from L2) by all threads. What
 // they hold from tau on is ranked by counting. Where more than fits is at tau or
 // above (equal logits, nearly all masked), a bisection on the value finds the k-th
 // largest, and its equals are taken from the lowest index on.
@@ -33,8 +33,9 @@ namespace fp8mp {
 
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kUnroll = 4;      // 16-byte loads that a thread has in flight
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kPerSm = 4;       // CTAs of the forward pass
+constexpr int kUnroll = 8;      // 16-byte loads that a thread of it has in flight
 constexpr int kMaxSplits = 8;   // CTAs that may share a row (a portable cluster)
 constexpr int kMaxTop = FP8MP_MAX_TOP;
 constexpr int kCandidates = 1024;
@@ -186,17 +187,17 @@ struct Slice {
     int head, tail;   // elements of the row's head and tail that are its own
 
     __device__ __forceinline__ int64_t elements() const { return head + tail + (p1 - p0) * Row<BF16>::EP; }
-    // The elements of thread t's share: f(index, logit).
+    // The elements of a thread's share: f(index, logit).
     template <typename F>
-    __device__ __forceinline__ void share(int t, int first, int step, F f) const {
-        const int64_t body = row.head;
-        for (int64_t p = p0 + t + static_cast<int64_t>(first) * kThreads; p < p1; p += static_cast<int64_t>(step) * kThreads) {
+    __device__ __forceinline__ void share(F f) const {
+        const int t = threadIdx.x;
+        for (int64_t p = p0 + t; p < p1; p += kThreads) {
             const uint4 q = __ldg(row.body() + p);
 #pragma unroll
-            for (int j = 0; j < Row<BF16>::EP; ++j) f(body + p * Row<BF16>::EP + j, element<BF16>(q, j));
+            for (int j = 0; j < Row<BF16>::EP; ++j) f(row.head + p * Row<BF16>::EP + j, element<BF16>(q, j));
         }
-        if (first == 0 && t < head) f(t, row.at(t));
-        if (first == 0 && t >= 32 && t - 32 < tail) f(row.tail_at() + t - 32, row.at(row.tail_at() + t - 32));
+        if (t < head) f(t, row.at(t));
+        if (t >= 32 && t - 32 < tail) f(row.tail_at() + t - 32, row.at(row.tail_at() + t - 32));
     }
 };
 
@@ -221,41 +222,56 @@ __device__ __forceinline__ void best_of_slice(const Slice<BF16> &sl, float large
     const bool empty = sl.p0 + tid >= sl.p1 && tid >= sl.head && !(tid >= 32 && tid - 32 < sl.tail);
     const uint32_t mine = empty ? 0u : order_of(largest);
     if (tid == 0) sh.n_found = sh.n_shares = 0u;
-    // tau: the want-th largest of the shares' largest, bit by bit (of bf16, whose
-    // low 16 bits are all ones below zero and all zeros above, they go together)
+    // tau: the want-th largest of the shares' largest, in its upper 16 bits, bit by
+    // bit (of bf16 that is all of it: the lower ones are all set below zero)
     uint32_t tau = 0u;
-    for (int bit = 31; bit >= (BF16 ? 16 : 0); --bit) {
+    for (int bit = 31; bit >= 16; --bit) {
         const uint32_t trial = tau | 1u << bit;
         if (static_cast<uint32_t>(__syncthreads_count(mine >= trial)) >= want) tau = trial;
     }
     if (BF16 && static_cast<uint32_t>(__syncthreads_count(mine >= (tau | 0xFFFFu))) >= want) tau |= 0xFFFFu;
     if (mine >= tau) sh.shares[atomicAdd(&sh.n_shares, 1u)] = static_cast<uint16_t>(tid);
     __syncthreads();
-    for (uint32_t i = tid >> 5; i < sh.n_shares; i += kWarps)
-        sl.share(sh.shares[i], lane, 32, [&](int64_t index, float x) {
-            const uint32_t key = order_of(x);
-            if (key < tau) return;
-            const uint32_t at = atomicAdd(&sh.n_found, 1u);
-            if (at < kCandidates) sh.found[at] = candidate(key, index);
-        });
+    const auto keep = [&](int64_t index, float x) {
+        const uint32_t key = order_of(x);
+        if (key < tau) return;
+        const uint32_t at = atomicAdd(&sh.n_found, 1u);
+        if (at < kCandidates) sh.found[at] = candidate(key, index);
+    };
+    // their pieces, dealt to all threads, and the elements off the 16-byte boundaries
+    const uint32_t each = static_cast<uint32_t>((sl.p1 - sl.p0 + kThreads - 1) / kThreads), all_pieces = each * sh.n_shares;
+    for (uint32_t i = tid; i < all_pieces; i += kThreads) {
+        const uint32_t share = i / each;
+        const int64_t p = sl.p0 + sh.shares[share] + static_cast<int64_t>(i - share * each) * kThreads;
+        if (p >= sl.p1) continue;
+        const uint4 q = __ldg(sl.row.body() + p);
+#pragma unroll
+        for (int j = 0; j < Row<BF16>::EP; ++j) keep(sl.row.head + p * Row<BF16>::EP + j, element<BF16>(q, j));
+    }
+    if (tid < sl.head) keep(tid, sl.row.at(tid));
+    if (tid >= 32 && tid - 32 < sl.tail) keep(sl.row.tail_at() + tid - 32, sl.row.at(sl.row.tail_at() + tid - 32));
     __syncthreads();
     uint32_t n = sh.n_found;
     if (n > kCandidates || n < want) {
         // the want-th largest logit itself, by bisection, starting from what is
-        // most likely: that tau is it, over and over
-        const uint32_t total = n;
-        uint32_t lo = tau, hi = 0xFFFFFFFFu;
-        if (total < want) lo = 0u;  // (shares of NaN alone: their largest is not there)
+        // most likely: that tau, to its last bit, is it, over and over
+        for (int bit = 15; !BF16 && bit >= 0; --bit) {
+            const uint32_t trial = tau | 1u << bit;
+            if (static_cast<uint32_t>(__syncthreads_count(mine >= trial)) >= want) tau = trial;
+        }
+        uint32_t lo = tau, hi = 0xFFFFFFFFu, c = 0;
+        sl.share([&](int64_t, float x) { c += order_of(x) >= lo; });
+        if (block_count(c, sh) < want) lo = 0u;  // (shares of NaN alone: their largest is not there)
         for (uint32_t mid = lo + 1u; hi - lo > 1u; mid = lo + (hi - lo) / 2u) {
-            uint32_t c = 0;
-            sl.share(tid, 0, 1, [&](int64_t, float x) { c += order_of(x) >= mid; });
+            c = 0;
+            sl.share([&](int64_t, float x) { c += order_of(x) >= mid; });
             if (block_count(c, sh) >= want) lo = mid;
             else hi = mid;
         }
         // those above it, fewer than `want`, then its equals from the lowest index on
         if (tid == 0) sh.n_found = 0u;
         __syncthreads();
-        sl.share(tid, 0, 1, [&](int64_t index, float x) {
+        sl.share([&](int64_t index, float x) {
             const uint32_t key = order_of(x);
             if (key > lo) sh.found[atomicAdd(&sh.n_found, 1u)] = candidate(key, index);
         });
@@ -284,8 +300,8 @@ __device__ __forceinline__ void best_of_slice(const Slice<BF16> &sl, float large
                 }
             }
             // exclusive prefix of the counts
-            const uint32_t c = __popc(equal);
-            uint32_t upto = c;
+            const uint32_t own = __popc(equal);
+            uint32_t upto = own;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
@@ -294,7 +310,7 @@ __device__ __forceinline__ void best_of_slice(const Slice<BF16> &sl, float large
             __syncthreads();
             if (lane == 31) sh.warp_count[tid >> 5] = upto;
             __syncthreads();
-            uint32_t at = have + upto - c, all = 0;
+            uint32_t at = have + upto - own, all = 0;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 const uint32_t v = sh.warp_count[w];
@@ -329,7 +345,7 @@ __device__ __forceinline__ void st_cluster_u64(uint32_t addr, uint64_t v) {
 }
 
 template <bool BF16, bool ENT, bool TOP>
-__global__ void __launch_bounds__(kThreads, 2) logp_fwd_kernel(const LogpArgs a) {
+__global__ void __launch_bounds__(kThreads, kPerSm) logp_fwd_kernel(const LogpArgs a) {
     __shared__ float warp_part[kWarps][3];
     __shared__ float cta_part[kMaxSplits][3];  // the first CTA's: all the CTAs' (m, S, T)
     __shared__ std::conditional_t<TOP, TopShared, Nothing> sh;
@@ -465,7 +481,9 @@ __global__ void __launch_bounds__(kThreads, 2) logp_fwd_kernel(const LogpArgs a)
 
 // ---------------------------------------------------------------- gradient
 
-constexpr int kGradThreads = 256;
+constexpr int kGradThreads = 256, kGradUnroll = 4;
+constexpr int64_t kGradBytes = 131072, kMinGradBytes = 8192;  // of logits for each CTA, about, and at least
+constexpr int kGradPerSm = 6;  // CTAs
 
 struct LogpGradArgs {
     const uint8_t *x;
@@ -506,13 +524,25 @@ __global__ void __launch_bounds__(kGradThreads) logp_bwd_kernel(const LogpGradAr
     const int part = static_cast<int>(blockIdx.x % a.splits);
     const R row(a.x + m_row * a.ld * ES, a.ld);  // the columns from V on included: theirs is 0
     uint8_t *out = a.out + m_row * a.ld * (CODES ? 1 : ES);
+    const int64_t p0 = row.pieces * part / a.splits, p1 = row.pieces * (part + 1) / a.splits;
+    const uint4 *body = row.body();
+    // the first logits are on their way before what the row's elements share
+    uint4 q[kGradUnroll];
+    const auto fetch = [&](int64_t p) {
+#pragma unroll
+        for (int u = 0; u < kGradUnroll; ++u)
+            if (p + u * kGradThreads < p1) q[u] = __ldcs(body + p + u * kGradThreads);
+    };
+    fetch(p0 + tid);
     RowGrad g;
     const float2 st = a.stats[m_row];
     g.target = a.target[m_row];
-    const bool given = g.target >= 0 && g.target < a.V;
-    if (!given) g.target = -1;
-    g.a = given ? a.da[m_row] : 0.0f;
+    g.a = a.da[m_row];
     const float b = ENT ? a.db[m_row] : 0.0f;
+    if (!(g.target >= 0 && g.target < a.V)) {
+        g.target = -1;
+        g.a = 0.0f;
+    }
     // log2 S in two parts; the second, below an ulp of the first, goes into c
     g.m = st.x;
     g.l2 = st.y * kLog2e;
@@ -523,15 +553,10 @@ __global__ void __launch_bounds__(kGradThreads) logp_bwd_kernel(const LogpGradAr
     const bool zero = st.y == -__uint_as_float(0x7F800000u) || (g.a == 0.0f && b == 0.0f);
     const float scale = CODES ? __ldg(a.scale) : 1.0f;
     float am = 0.0f;
-    const int64_t p0 = row.pieces * part / a.splits, p1 = row.pieces * (part + 1) / a.splits;
-    const uint4 *body = row.body();
-    for (int64_t p = p0 + tid; p < p1; p += kGradThreads * kUnroll) {
-        uint4 q[kUnroll];
+    for (int64_t p = p0 + tid; p < p1; p += kGradThreads * kGradUnroll) {
+        if (p != p0 + tid && !zero) fetch(p);
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-            if (!zero && p + u * kGradThreads < p1) q[u] = __ldcs(body + p + u * kGradThreads);
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
+        for (int u = 0; u < kGradUnroll; ++u) {
             const int64_t i = p + u * kGradThreads;
             if (i >= p1) break;
             const int64_t first = row.head + i * EP;
@@ -580,6 +605,24 @@ __global__ void __launch_bounds__(kGradThreads) logp_bwd_kernel(const LogpGradAr
     if (a.amax != nullptr) block_amax_atomic(am, a.amax);
 }
 
+// CTAs that share a row of `bytes`: those with which the last is done first, when an
+// SM takes in 45 B/ns, a CTA alone 16, and a CTA costs 3 us of its own, 4 with peers.
+int splits_for(int64_t M, int64_t bytes, int num_sms) {
+    int best = 1;
+    double least = 0.0;
+    for (int s = 1; s <= kMaxSplits; s *= 2) {
+        const int64_t ctas = M * s, slots = static_cast<int64_t>(num_sms) * kPerSm;
+        const double waves = static_cast<double>((ctas + slots - 1) / slots), part = static_cast<double>(bytes) / s;
+        const double by_sm = static_cast<double>((ctas + num_sms - 1) / num_sms) * part / 45.0, by_cta = waves * part / 16.0;
+        const double ns = (by_sm > by_cta ? by_sm : by_cta) + waves * (s == 1 ? 3000.0 : 4000.0);
+        if (s == 1 || ns < least) {
+            least = ns;
+            best = s;
+        }
+    }
+    return best;
+}
+
 template <bool BF16, bool ENT>
 cudaError_t fwd(const LogpArgs &a, int64_t M, cudaStream_t s) {
     const dim3 grid(static_cast<unsigned>(M * a.splits)), block(kThreads);
@@ -602,10 +645,7 @@ int launch_logprobs_fwd(const void *x, int x_dtype, int64_t M, int64_t V, int64_
                         const DeviceInfo &dev) {
     LogpArgs a = {static_cast<const uint8_t *>(x), target, logprob, entropy, top, reinterpret_cast<float2 *>(stats), ids,
                   V, ld, 1, k};
-    // CTAs for a row: as long as all rows' fit two to an SM and each has a full
-    // round of loads
-    const int64_t round = static_cast<int64_t>(kThreads) * kUnroll * 16 / (x_dtype == FP8MP_BF16 ? 2 : 4);
-    while (a.splits < kMaxSplits && M * a.splits * 2 <= 2 * dev.num_sms && V >= a.splits * 2 * round / 2) a.splits *= 2;
+    a.splits = splits_for(M, V * (x_dtype == FP8MP_BF16 ? 2 : 4), dev.num_sms);
     const bool b = x_dtype == FP8MP_BF16;
     cudaError_t e;
     if (entropy != nullptr) e = b ? fwd<true, true>(a, M, s) : fwd<false, true>(a, M, s);
@@ -619,8 +659,12 @@ int launch_logprobs_bwd(const void *x, int x_dtype, int64_t M, int64_t V, int64_
                         const float *scale, void *dlogits, float *amax, cudaStream_t s, const DeviceInfo &dev) {
     LogpGradArgs a = {static_cast<const uint8_t *>(x), target, reinterpret_cast<const float2 *>(stats), dlogprob, dentropy,
                       entropy, scale, amax, static_cast<uint8_t *>(dlogits), V, ld, 1};
-    const int64_t round = static_cast<int64_t>(kGradThreads) * kUnroll * 16 / (x_dtype == FP8MP_BF16 ? 2 : 4);
-    while (M * a.splits < 32ll * dev.num_sms && ld >= a.splits * 2 * round) a.splits *= 2;
+    const int64_t bytes = ld * (x_dtype == FP8MP_BF16 ? 2 : 4), few = (static_cast<int64_t>(kGradPerSm) * dev.num_sms + M - 1) / M;
+    int64_t parts = bytes / kGradBytes;
+    if (parts < few) parts = few;
+    if (parts > bytes / kMinGradBytes) parts = bytes / kMinGradBytes;
+    if (parts > 0x7FFFFFFFll / M) parts = 0x7FFFFFFFll / M;
+    a.splits = static_cast<int>(parts < 1 ? 1 : parts);
     const bool b = x_dtype == FP8MP_BF16;
     cudaError_t e;
     if (scale != nullptr) e = b ? bwd<true, true>(a, M, s) : bwd<false, true>(a, M, s);

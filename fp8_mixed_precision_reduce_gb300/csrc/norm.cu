@@ -10,19 +10,32 @@
 // code), 8 backward (dy, t, dT, dt). The weight and its gradient's running sums
 // stay in registers over all rows that a thread's columns see.
 //
-// Rows of up to kWarpRow columns belong to one warp each, which needs no barrier;
-// longer ones to a block whose threads hold 16 columns each (32 from 8192 on, so
-// that a block has at most 512 threads).
+// A thread takes 16 columns of a row (32 of rows past 4096), a warp or several up to
+// 512 threads share it, and rows of up to 2048 columns are taken two to eight at a
+// time by a block of 256 threads. Each warp copies its own pieces of the rows to come
+// into shared memory (cp.async) and reads nothing else there, so no barrier is
+// needed but the one inside a row's sum, and loads are in flight while a row is
+// reduced and written.
+#include <algorithm>
+#include <atomic>
+#include <mutex>
+
 #include "fp8mp_pieces.cuh"
 
 namespace fp8mp {
 
 namespace {
 
-constexpr int kWarpRow = 1024;      // columns up to which a warp takes a row
-constexpr int kWarpRowsPerBlock = 8;
-constexpr int kMaxThreads = 512;    // of a block that takes a row
-constexpr int kGradBlocks = 456;    // most blocks of the backward pass, each of which leaves a row of sums
+constexpr int kBlock = 256;         // threads of a block whose threads take 16 columns, at most
+constexpr int kWideBlock = 512;     // 32 columns
+constexpr int kMaxGroups = kBlock / 32;  // rows that a block takes at a time, at most
+// Blocks of kBlock threads for each SM in the forward pass, where two or three are
+// resident: shares small enough to even out the tail. 16384 x 4096, bf16 with
+// residual: 82.5 us with 3, 73.9 with 4, 72.7 with 8, 76.9 with 36; without
+// residual 43.4, 49.2, 45.2, 56.6; 8192 x 4096 with an fp32 residual 62.8, 62.8, 58.3, 68.3.
+constexpr int kBlocksPerSm = 8;
+constexpr int kGradSms = 152;       // the backward pass's blocks are for so many SMs; each leaves a row of sums
+constexpr int kSmem = 216 * 1024;   // what the blocks on an SM may use together
 
 struct NormArgs {
     const void *x, *r, *w;
@@ -30,7 +43,7 @@ struct NormArgs {
     float *rstd, *amax;
     const float *scale;
     int64_t M;
-    int K;
+    int K, tpr;  // threads that share a row
     float eps;
     bool w_bf16, y_bf16;
 };
@@ -41,21 +54,106 @@ struct NormGradArgs {
     void *dr, *dx;
     float *partial;  // [gridDim.x][K] sums of dy n, or NULL
     int64_t M;
-    int K;
+    int K, tpr;
     bool w_bf16;
 };
 
-// The sum over the threads that share a row. `red` alternates between two halves
-// from row to row: a thread writes one again only when all have left the barrier
-// of the row between, and with it their reads.
-template <bool WARP>
-__device__ __forceinline__ float row_sum(float v, float *red) {
+constexpr int threads_of(int n) { return n == 2 ? kBlock : kWideBlock; }
+// Blocks that an SM holds, of threads with N pieces each and `bytes` of a row.
+constexpr int per_sm(int threads, int n, int bytes, int stages) {
+    const int by_threads = n == 2 ? 3 * kBlock / threads : kWideBlock / threads;
+    const int by_smem = kSmem / (threads * bytes * stages);
+    return by_threads < 1 || by_smem < 1 ? 1 : by_threads < by_smem ? by_threads : by_smem;
+}
+// Rows in flight for each group of threads: three where that costs no blocks, two
+// where they fit; else one, refilled piece by piece as it is used for the last time.
+constexpr int stages(int bytes, int n) {
+    const int threads = threads_of(n), blocks = n == 2 ? 3 : 1;
+    return threads * bytes * 3 * blocks <= kSmem ? 3 : threads * bytes * 2 <= kSmem ? 2 : 1;
+}
+
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// A warp's copies of one array's pieces: N of a row for each lane, 32 pieces one
+// after another. A lane copies 16-byte units 32 lanes apart, so it reads what other
+// lanes copied: the warp meets between the copies' arrival and their use, and
+// between their use and the next copies.
+template <bool BF16, int N>
+struct Slot {
+    static constexpr int UNITS = BF16 ? 1 : 2, BYTES = N * UNITS * 16;
+    const uint8_t *next;  // the lane's first unit of the next row to fetch
+    int64_t step;         // to the one after it
+    int units, gap;       // of the row from there on; from piece v to piece v + 1
+    uint32_t to, from;    // where the lane's first unit goes, and where its first piece lies, in the first stage
+
+    // `ring`: of this array, in the first stage; row: the first one, rows: between a block's rows
+    __device__ __forceinline__ Slot(uint32_t ring, const void *x, int64_t row, int64_t rows, int pieces, int tid, int tpr) {
+        const int lane = threadIdx.x & 31, first = (tid - lane) * UNITS + lane;
+        next = static_cast<const uint8_t *>(x) + (row * pieces * UNITS + first) * 16;
+        step = rows * pieces * (UNITS * 16);
+        units = pieces * UNITS - first;
+        gap = tpr * UNITS;
+        to = ring + (threadIdx.x - lane) * (UNITS * 16) + lane * 16;
+        from = ring + threadIdx.x * (UNITS * 16);
+    }
+    __device__ __forceinline__ void fetch(uint32_t stage, int v) const {
+#pragma unroll
+        for (int j = 0; j < UNITS; ++j)
+            if (v * gap + j * 32 < units)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + stage + v * blockDim.x * (UNITS * 16) + j * 512),
+                             "l"(next + (v * gap + j * 32) * 16)
+                             : "memory");
+    }
+    __device__ __forceinline__ Piece<BF16> read(uint32_t stage, int v) const {
+        Piece<BF16> r;
+#pragma unroll
+        for (int j = 0; j < UNITS; ++j)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(r.w[4 * j]), "=r"(r.w[4 * j + 1]), "=r"(r.w[4 * j + 2]), "=r"(r.w[4 * j + 3])
+                         : "r"(from + stage + v * blockDim.x * (UNITS * 16) + j * 16)
+                         : "memory");
+        return r;
+    }
+};
+
+// 1 / sqrt(v) to an ulp: the hardware's approximation and a step of Newton's, where
+// nothing in it leaves the normal numbers.
+__device__ __forceinline__ float inverse_root(float v) {
+    if (v > 0x1p-100f && v < 0x1p100f) {
+        float r;
+        asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+        return fmaf(r * 0.5f, fmaf(-v * r, r, 1.0f), r);
+    }
+    return __frcp_rn(__fsqrt_rn(v));
+}
+
+constexpr int kMaxWarps = kWideBlock / 32;
+
+// The sum over the tpr threads of group g. `red` (zeros behind the group's warps)
+// alternates between two halves from row to row: a thread writes one again only when
+// all have left the barrier of the row between, and with it their reads.
+__device__ __forceinline__ float row_sum(float v, float (&red)[kMaxWarps], int g, int tpr, int tid) {
     v = warp_sum(v);
-    if constexpr (WARP) return v;
-    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    if (lane == 0) red[threadIdx.x >> 5] = v;
+    if (tpr == 32) return v;
+    if ((tid & 31) == 0) red[tid >> 5] = v;
+    asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "r"(tpr) : "memory");
+    float4 s = *reinterpret_cast<const float4 *>(red);
+    for (int w = 4; w < tpr >> 5; w += 4) {
+        const float4 more = *reinterpret_cast<const float4 *>(red + w);
+        s.x += more.x;
+        s.y += more.y;
+        s.z += more.z;
+        s.w += more.w;
+    }
+    return (s.x + s.y) + (s.z + s.w);
+}
+__device__ __forceinline__ void clear(float (&red)[2][kMaxGroups][kMaxWarps]) {
+    for (int i = threadIdx.x; i < 2 * kMaxGroups * kMaxWarps; i += blockDim.x) (&red[0][0][0])[i] = 0.0f;
     __syncthreads();
-    return warp_sum(lane < warps ? red[lane] : 0.0f);
 }
 
 template <int N>
@@ -79,42 +177,74 @@ __device__ __forceinline__ void load_weight(uint64_t (&w)[N][4], const void *p, 
 }
 
 // RES: 0 no residual, 1 bf16, 2 fp32. N pieces of a row for each thread.
-template <bool XBF, int RES, int N, bool WARP>
-__global__ void __launch_bounds__(WARP ? 32 * kWarpRowsPerBlock : kMaxThreads) norm_fwd_kernel(const NormArgs a) {
-    __shared__ float red[2][32];
+template <bool XBF, int RES, int N>
+struct Fwd {
+    using SX = Slot<XBF, N>;
+    using SR = Slot<RES == 1, N>;
+    static constexpr int BYTES = SX::BYTES + (RES ? SR::BYTES : 0), S = stages(BYTES, N);
+};
+
+template <bool XBF, int RES, int N>
+__global__ void __launch_bounds__(threads_of(N), (per_sm(threads_of(N), N, Fwd<XBF, RES, N>::BYTES, Fwd<XBF, RES, N>::S)))
+    norm_fwd_kernel(const NormArgs a) {
+    using F = Fwd<XBF, RES, N>;
+    using SX = typename F::SX;
+    using SR = typename F::SR;
+    constexpr bool RBF = RES == 1;
+    constexpr int BYTES = F::BYTES, S = F::S;
+    extern __shared__ uint4 ring[];
+    __shared__ __align__(16) float red[2][kMaxGroups][kMaxWarps];
+    clear(red);
     pdl_wait();
     pdl_launch_dependents();
-    constexpr bool RBF = RES == 1;
-    const int tpr = WARP ? 32 : static_cast<int>(blockDim.x), tid = WARP ? threadIdx.x & 31 : threadIdx.x;
-    const int64_t rows = WARP ? kWarpRowsPerBlock : 1;
+    const int tpr = a.tpr, g = threadIdx.x / tpr, tid = threadIdx.x - g * tpr, groups = blockDim.x / tpr;
     const int pieces = a.K / kPiece;
-    uint64_t w[N][4];
-    load_weight<N>(w, a.w, a.w_bf16, tid, tpr, pieces);
-    const uint64_t scale = f2_same(a.scale != nullptr ? __ldg(a.scale) : 1.0f);
-    float am = 0.0f;
-    int turn = 0;
-    for (int64_t m = blockIdx.x * rows + (WARP ? threadIdx.x >> 5 : 0); m < a.M; m += gridDim.x * rows, turn ^= 1) {
-        const int64_t row = m * pieces;
-        Piece<XBF> xs[N];
-        Piece<RBF> rs[RES ? N : 1];
+    const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+    const uint32_t stage_bytes = blockDim.x * BYTES;
+    int64_t m = static_cast<int64_t>(blockIdx.x) * groups + g, to_fetch = m;
+    SX sx(smem_u32(ring), a.x, m, step, pieces, tid, tpr);
+    SR sr(smem_u32(ring) + blockDim.x * SX::BYTES, a.r, m, step, pieces, tid, tpr);
+    const auto fetch_row = [&](uint32_t stage) {
+        if (to_fetch < a.M) {
 #pragma unroll
-        for (int v = 0; v < N; ++v) {
-            const int i = tid + v * tpr;
-            if (i < pieces) {
-                xs[v] = load_piece<XBF>(a.x, row + i);
-                if constexpr (RES != 0) rs[v] = load_piece<RBF>(a.r, row + i);
+            for (int v = 0; v < N; ++v) {
+                sx.fetch(stage, v);
+                if constexpr (RES != 0) sr.fetch(stage, v);
             }
         }
+        to_fetch += step;
+        sx.next += sx.step;
+        if constexpr (RES != 0) sr.next += sr.step;
+        cp_async_commit();
+    };
+    for (int s = 0; s < (S > 1 ? S - 1 : 1); ++s) fetch_row(s * stage_bytes);
+    uint64_t w[N][4];
+    load_weight<N>(w, a.w, a.w_bf16, tid, tpr, pieces);
+    const float inv_k = __frcp_rn(static_cast<float>(a.K));
+    const uint64_t scale = f2_same(a.scale != nullptr ? __ldg(a.scale) : 1.0f);
+    float am = 0.0f;
+    for (int s = 0, turn = 0; m < a.M; m += step, turn ^= 1) {
+        if constexpr (S > 1) {
+            __syncwarp();
+            fetch_row((s == 0 ? S - 1 : s - 1) * stage_bytes);
+        }
+        cp_async_wait<S - 1>();
+        __syncwarp();
+        const uint32_t now = s * stage_bytes;
+        s = s == S - 1 ? 0 : s + 1;
+        const int64_t row = m * pieces;
         uint64_t t[N][4], sum = 0ull;
 #pragma unroll
         for (int v = 0; v < N; ++v) {
             const int i = tid + v * tpr;
             if (i < pieces) {
+                const Piece<XBF> x = sx.read(now, v);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) t[v][j] = xs[v].pair(j);
+                for (int j = 0; j < 4; ++j) t[v][j] = x.pair(j);
                 if constexpr (RES != 0) {
+                    const Piece<RBF> r = sr.read(now, v);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) t[v][j] = f2_add(t[v][j], rs[v].pair(j));
+                    for (int j = 0; j < 4; ++j) t[v][j] = f2_add(t[v][j], r.pair(j));
                     const Piece<RBF> q = round_piece<RBF>(t[v]);
                     store_piece<RBF>(a.t, row + i, q);
 #pragma unroll
@@ -124,10 +254,14 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRowsPerBlock : kMaxThreads) n
                 for (int j = 0; j < 4; ++j) sum = f2_fma(t[v][j], t[v][j], sum);
             }
         }
+        if constexpr (S == 1) {
+            __syncwarp();
+            fetch_row(0);
+        }
         float s0, s1;
         f2_split(sum, s0, s1);
-        const float total = row_sum<WARP>(s0 + s1, red[turn]);
-        const float rstd = __frcp_rn(__fsqrt_rn(__fdiv_rn(total, static_cast<float>(a.K)) + a.eps));
+        const float total = row_sum(s0 + s1, red[turn][g], g, tpr, tid);
+        const float rstd = inverse_root(fmaf(total, inv_k, a.eps));
         if (tid == 0) a.rstd[m] = rstd;
         const uint64_t r2 = f2_same(rstd);
 #pragma unroll
@@ -161,15 +295,57 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRowsPerBlock : kMaxThreads) n
     if (a.amax != nullptr) block_amax_atomic(am, a.amax);
 }
 
-template <bool XBF, bool RBF, int N, bool WARP>
-__global__ void __launch_bounds__(WARP ? 32 * kWarpRowsPerBlock : kMaxThreads) norm_bwd_kernel(const NormGradArgs a) {
-    __shared__ float red[2][32];
-    __shared__ float join[WARP ? kWarpRow : 1];
+template <bool XBF, bool RBF, int N>
+struct Bwd {
+    using SX = Slot<XBF, N>;
+    using SR = Slot<RBF, N>;
+    static constexpr int BYTES = SX::BYTES + 2 * SR::BYTES, S = stages(BYTES, N);
+};
+
+template <bool XBF, bool RBF, int N>
+__global__ void __launch_bounds__(threads_of(N), (per_sm(threads_of(N), N, Bwd<XBF, RBF, N>::BYTES, Bwd<XBF, RBF, N>::S)))
+    norm_bwd_kernel(const NormGradArgs a) {
+    using B = Bwd<XBF, RBF, N>;
+    using SX = typename B::SX;
+    using SR = typename B::SR;
+    constexpr int BYTES = B::BYTES, S = B::S;
+    extern __shared__ uint4 ring[];
+    __shared__ __align__(16) float red[2][kMaxGroups][kMaxWarps];
+    clear(red);
     pdl_wait();
     pdl_launch_dependents();
-    const int tpr = WARP ? 32 : static_cast<int>(blockDim.x), tid = WARP ? threadIdx.x & 31 : threadIdx.x;
-    const int64_t rows = WARP ? kWarpRowsPerBlock : 1;
+    const int tpr = a.tpr, g = threadIdx.x / tpr, tid = threadIdx.x - g * tpr, groups = blockDim.x / tpr;
     const int pieces = a.K / kPiece;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+    const uint32_t stage_bytes = blockDim.x * BYTES, t_ring = smem_u32(ring) + blockDim.x * SX::BYTES;
+    int64_t m = static_cast<int64_t>(blockIdx.x) * groups + g, to_fetch = m;
+    SX sdy(smem_u32(ring), a.dy, m, step, pieces, tid, tpr);
+    SR st(t_ring, a.t, m, step, pieces, tid, tpr);
+    // (dT lies behind t, and is as far from it in memory for every row)
+    const uint32_t dt_ring = blockDim.x * SR::BYTES;
+    const int64_t dt_away = static_cast<const uint8_t *>(a.dtotal) - static_cast<const uint8_t *>(a.t);
+    const auto fetch = [&](uint32_t stage, int v) {
+        if (to_fetch >= a.M) return;
+        sdy.fetch(stage, v);
+        st.fetch(stage, v);
+        if (a.dtotal != nullptr) {
+            SR sdt = st;
+            sdt.next += dt_away;
+            sdt.fetch(stage + dt_ring, v);
+        }
+    };
+    const auto fetched = [&] {
+        to_fetch += step;
+        sdy.next += sdy.step;
+        st.next += st.step;
+        cp_async_commit();
+    };
+    const auto fetch_row = [&](uint32_t stage) {
+#pragma unroll
+        for (int v = 0; v < N; ++v) fetch(stage, v);
+        fetched();
+    };
+    for (int s = 0; s < (S > 1 ? S - 1 : 1); ++s) fetch_row(s * stage_bytes);
     const float inv_k = __frcp_rn(static_cast<float>(a.K));
     uint64_t w[N][4], dw[N][4];
     load_weight<N>(w, a.w, a.w_bf16, tid, tpr, pieces);
@@ -177,30 +353,28 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRowsPerBlock : kMaxThreads) n
     for (int v = 0; v < N; ++v)
 #pragma unroll
         for (int j = 0; j < 4; ++j) dw[v][j] = 0ull;
-    int turn = 0;
-    for (int64_t m = blockIdx.x * rows + (WARP ? threadIdx.x >> 5 : 0); m < a.M; m += gridDim.x * rows, turn ^= 1) {
-        const int64_t row = m * pieces;
-        const float rstd = __ldg(a.rstd + m);
-        Piece<XBF> dy[N];
-        Piece<RBF> t[N], dt[N];
-#pragma unroll
-        for (int v = 0; v < N; ++v) {
-            const int i = tid + v * tpr;
-            if (i < pieces) {
-                dy[v] = load_piece<XBF>(a.dy, row + i);
-                t[v] = load_piece<RBF>(a.t, row + i);
-                if (a.dtotal != nullptr) dt[v] = load_piece<RBF>(a.dtotal, row + i);
-            }
+    float next_rstd = m < a.M ? __ldg(a.rstd + m) : 0.0f;
+    for (int s = 0, turn = 0; m < a.M; m += step, turn ^= 1) {
+        if constexpr (S > 1) {
+            __syncwarp();
+            fetch_row((s == 0 ? S - 1 : s - 1) * stage_bytes);
         }
-        const uint64_t r2 = f2_same(rstd);
+        const uint64_t r2 = f2_same(next_rstd);
+        if (m + step < a.M) next_rstd = __ldg(a.rstd + m + step);
+        cp_async_wait<S - 1>();
+        __syncwarp();
+        const uint32_t now = s * stage_bytes;
+        s = s == S - 1 ? 0 : s + 1;
+        const int64_t row = m * pieces;
         uint64_t sum = 0ull;
 #pragma unroll
         for (int v = 0; v < N; ++v) {
-            const int i = tid + v * tpr;
-            if (i < pieces) {
+            if (tid + v * tpr < pieces) {
+                const Piece<XBF> dy = sdy.read(now, v);
+                const Piece<RBF> t = st.read(now, v);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const uint64_t n = f2_mul(t[v].pair(j), r2), d = dy[v].pair(j);
+                    const uint64_t n = f2_mul(t.pair(j), r2), d = dy.pair(j);
                     dw[v][j] = f2_fma(d, n, dw[v][j]);
                     sum = f2_fma(f2_mul(d, w[v][j]), n, sum);
                 }
@@ -208,31 +382,45 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRowsPerBlock : kMaxThreads) n
         }
         float s0, s1;
         f2_split(sum, s0, s1);
-        const float c = row_sum<WARP>(s0 + s1, red[turn]) * inv_k;
+        const float c = row_sum(s0 + s1, red[turn][g], g, tpr, tid) * inv_k;
         const uint64_t neg_c = f2_same(-c);
 #pragma unroll
         for (int v = 0; v < N; ++v) {
             const int i = tid + v * tpr;
             if (i < pieces) {
+                const Piece<XBF> dy = sdy.read(now, v);
+                const Piece<RBF> t = st.read(now, v);
                 uint64_t d[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint64_t n = f2_mul(t[v].pair(j), r2);
-                    const uint64_t g = f2_fma(n, neg_c, f2_mul(dy[v].pair(j), w[v][j]));
-                    d[j] = a.dtotal != nullptr ? f2_fma(g, r2, dt[v].pair(j)) : f2_mul(g, r2);
+                for (int j = 0; j < 4; ++j) d[j] = f2_fma(f2_mul(t.pair(j), r2), neg_c, f2_mul(dy.pair(j), w[v][j]));
+                if (a.dtotal != nullptr) {
+                    const Piece<RBF> dt = st.read(now + dt_ring, v);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) d[j] = f2_fma(d[j], r2, dt.pair(j));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) d[j] = f2_mul(d[j], r2);
                 }
                 store_piece<RBF>(a.dr, row + i, round_piece<RBF>(d));
                 if (a.dx != nullptr) store_piece<XBF>(a.dx, row + i, round_piece<XBF>(d));
             }
+            if constexpr (S == 1) {
+                __syncwarp();
+                fetch(0, v);
+            }
         }
+        if constexpr (S == 1) fetched();
     }
     if (a.partial == nullptr) return;
     float *out = a.partial + static_cast<int64_t>(blockIdx.x) * a.K;
-    if constexpr (WARP) {  // the warps' sums one after another
+    if (groups > 1) {  // the groups' sums one after another, in the ring's memory
+        float *join = reinterpret_cast<float *>(ring);
+        cp_async_wait<0>();
+        __syncthreads();
         for (int i = threadIdx.x; i < a.K; i += blockDim.x) join[i] = 0.0f;
-        for (int k = 0; k < kWarpRowsPerBlock; ++k) {
+        for (int k = 0; k < groups; ++k) {
             __syncthreads();
-            if (static_cast<int>(threadIdx.x >> 5) != k) continue;
+            if (g != k) continue;
 #pragma unroll
             for (int v = 0; v < N; ++v) {
                 const int i = tid + v * tpr;
@@ -296,52 +484,96 @@ __global__ void __launch_bounds__(kSumThreads) norm_dw_kernel(const float *parti
     }
 }
 
-// Threads of a block, and pieces of a row for each (4 for a warp).
+// Pieces of a row for each thread, threads that share it, rows that a block takes
+// at a time.
 struct Shape {
-    int threads, pieces;
-    bool warp;
+    int pieces, tpr, groups;
+    int threads() const { return tpr * groups; }
 };
 Shape shape_of(int64_t K) {
-    if (K <= kWarpRow) return {32 * kWarpRowsPerBlock, 4, true};
-    const int n = K <= 2 * kPiece * kMaxThreads ? 2 : 4;
+    const int n = K <= 2 * kPiece * kBlock ? 2 : 4;
     const int64_t threads = (K / kPiece + n - 1) / n;
-    return {static_cast<int>((threads + 31) / 32 * 32), n, false};
+    const int tpr = static_cast<int>((threads + 31) / 32 * 32);
+    return {n, tpr, tpr < kBlock ? kBlock / tpr : 1};
 }
-int64_t rows_of(const Shape &s) { return s.warp ? kWarpRowsPerBlock : 1; }
 
+std::mutex g_prepare_mutex;
+
+// Launches a kernel of `blocks` blocks, allowed once their shared memory.
+template <typename A>
+cudaError_t launch_rows(void (*kernel)(A), std::atomic<bool> (&ready)[64], int64_t blocks, const Shape &shape, int smem,
+                        cudaStream_t s, int device, const A &a) {
+    std::atomic<bool> &mine = ready[device & 63];
+    if (!mine.load(std::memory_order_acquire)) {
+        std::lock_guard<std::mutex> lock(g_prepare_mutex);
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess) return e;
+        mine.store(true, std::memory_order_release);
+    }
+    return launch_kernel(kernel, dim3(static_cast<unsigned>(blocks)), dim3(shape.threads()), smem, s, a);
+}
+
+int64_t least(int64_t a, int64_t b) { return a < b ? a : b; }
+
+template <bool XBF, int RES, int N>
+cudaError_t fwd(NormArgs a, const Shape &shape, cudaStream_t s, const DeviceInfo &dev) {
+    using F = Fwd<XBF, RES, N>;
+    static std::atomic<bool> ready[64];
+    a.tpr = shape.tpr;
+    const int64_t most = static_cast<int64_t>(dev.num_sms) * kBlocksPerSm * kBlock / shape.threads();
+    return launch_rows(norm_fwd_kernel<XBF, RES, N>, ready, least((a.M + shape.groups - 1) / shape.groups, most), shape,
+                       F::BYTES * F::S * shape.threads(), s, dev.device, a);
+}
 template <bool XBF, int RES>
 cudaError_t fwd(const NormArgs &a, cudaStream_t s, const DeviceInfo &dev) {
     const Shape shape = shape_of(a.K);
-    const int64_t need = (a.M + rows_of(shape) - 1) / rows_of(shape);
-    const int64_t most = static_cast<int64_t>(dev.num_sms) * (1536 / shape.threads);
-    const dim3 grid(static_cast<unsigned>(need < most ? need : most)), block(shape.threads);
-    if (shape.warp) return launch_kernel(norm_fwd_kernel<XBF, RES, 4, true>, grid, block, 0, s, a);
-    if (shape.pieces == 2) return launch_kernel(norm_fwd_kernel<XBF, RES, 2, false>, grid, block, 0, s, a);
-    return launch_kernel(norm_fwd_kernel<XBF, RES, 4, false>, grid, block, 0, s, a);
+    return shape.pieces == 2 ? fwd<XBF, RES, 2>(a, shape, s, dev) : fwd<XBF, RES, 4>(a, shape, s, dev);
 }
 
-int64_t grad_blocks(int64_t M, int64_t K) {
-    const int64_t rows = rows_of(shape_of(K)), need = (M + rows - 1) / rows;
-    return need < kGradBlocks ? need : kGradBlocks;
+// Blocks of the backward pass, which fix the order of dw's sum.
+template <bool XBF, bool RBF, int N>
+int64_t grad_blocks(int64_t M, const Shape &shape) {
+    using B = Bwd<XBF, RBF, N>;
+    return least((M + shape.groups - 1) / shape.groups, kGradSms * per_sm(shape.threads(), N, B::BYTES, B::S));
 }
-
 template <bool XBF, bool RBF>
-cudaError_t bwd(const NormGradArgs &a, cudaStream_t s) {
+int64_t grad_blocks(int64_t M, int64_t K) {
+    const Shape shape = shape_of(K);
+    return shape.pieces == 2 ? grad_blocks<XBF, RBF, 2>(M, shape) : grad_blocks<XBF, RBF, 4>(M, shape);
+}
+
+template <bool XBF, bool RBF, int N>
+cudaError_t bwd(NormGradArgs a, const Shape &shape, cudaStream_t s, const DeviceInfo &dev) {
+    using B = Bwd<XBF, RBF, N>;
+    static std::atomic<bool> ready[64];
+    a.tpr = shape.tpr;
+    return launch_rows(norm_bwd_kernel<XBF, RBF, N>, ready, grad_blocks<XBF, RBF, N>(a.M, shape), shape,
+                       B::BYTES * B::S * shape.threads(), s, dev.device, a);
+}
+template <bool XBF, bool RBF>
+cudaError_t bwd(const NormGradArgs &a, void *dw, bool dw_bf16, cudaStream_t s, const DeviceInfo &dev) {
     const Shape shape = shape_of(a.K);
-    const dim3 grid(static_cast<unsigned>(grad_blocks(a.M, a.K))), block(shape.threads);
-    if (shape.warp) return launch_kernel(norm_bwd_kernel<XBF, RBF, 4, true>, grid, block, 0, s, a);
-    if (shape.pieces == 2) return launch_kernel(norm_bwd_kernel<XBF, RBF, 2, false>, grid, block, 0, s, a);
-    return launch_kernel(norm_bwd_kernel<XBF, RBF, 4, false>, grid, block, 0, s, a);
+    cudaError_t e = cudaSuccess;
+    if (a.M > 0) e = shape.pieces == 2 ? bwd<XBF, RBF, 2>(a, shape, s, dev) : bwd<XBF, RBF, 4>(a, shape, s, dev);
+    if (e == cudaSuccess && dw != nullptr)
+        e = launch_kernel(norm_dw_kernel, dim3(static_cast<unsigned>((a.K + 31) / 32)), dim3(kSumThreads), 0, s,
+                          static_cast<const float *>(a.partial), static_cast<int>(grad_blocks<XBF, RBF>(a.M, a.K)), a.K, dw,
+                          dw_bf16);
+    return e;
 }
 
 }  // namespace
 
-int64_t rmsnorm_workspace_bytes(int64_t M, int64_t K) { return grad_blocks(M, K) * K * 4; }
+int64_t rmsnorm_workspace_bytes(int64_t M, int64_t K) {
+    const int64_t blocks[] = {grad_blocks<true, true>(M, K), grad_blocks<true, false>(M, K), grad_blocks<false, true>(M, K),
+                              grad_blocks<false, false>(M, K)};
+    return *std::max_element(blocks, blocks + 4) * K * 4;
+}
 
 int launch_rmsnorm_fwd(const void *x, int x_dtype, const void *r, void *t, int r_dtype, int64_t M, int64_t K,
                        const void *w, int w_dtype, float eps, const float *y_scale, void *y, int y_dtype,
                        float *y_amax, float *rstd, cudaStream_t s, const DeviceInfo &dev) {
-    const NormArgs a = {x, r, w, t, y, rstd, y_amax, y_scale, M, static_cast<int>(K), eps,
+    const NormArgs a = {x, r, w, t, y, rstd, y_amax, y_scale, M, static_cast<int>(K), 0, eps,
                         w_dtype == FP8MP_BF16, y_dtype == FP8MP_BF16};
     const bool xb = x_dtype == FP8MP_BF16, rb = r_dtype == FP8MP_BF16;
     cudaError_t e;
@@ -354,19 +586,14 @@ int launch_rmsnorm_fwd(const void *x, int x_dtype, const void *r, void *t, int r
 
 int launch_rmsnorm_bwd(const void *dy, int dy_dtype, const void *dtotal, const void *t, int t_dtype, const float *rstd,
                        int64_t M, int64_t K, const void *w, int w_dtype, void *dr, void *dx, void *dw, int dw_dtype,
-                       void *workspace, cudaStream_t s) {
+                       void *workspace, cudaStream_t s, const DeviceInfo &dev) {
     const NormGradArgs a = {dy, dtotal, t, w, rstd, dr, dx, dw != nullptr ? static_cast<float *>(workspace) : nullptr,
-                            M, static_cast<int>(K), w_dtype == FP8MP_BF16};
+                            M, static_cast<int>(K), 0, w_dtype == FP8MP_BF16};
     const bool xb = dy_dtype == FP8MP_BF16, rb = t_dtype == FP8MP_BF16;
-    cudaError_t e = cudaSuccess;
-    if (M > 0) {
-        if (rb) e = xb ? bwd<true, true>(a, s) : bwd<false, true>(a, s);
-        else e = xb ? bwd<true, false>(a, s) : bwd<false, false>(a, s);
-    }
-    if (e == cudaSuccess && dw != nullptr)
-        e = launch_kernel(norm_dw_kernel, dim3(static_cast<unsigned>((K + 31) / 32)), dim3(kSumThreads), 0, s,
-                          static_cast<const float *>(workspace), static_cast<int>(M > 0 ? grad_blocks(M, K) : 0),
-                          static_cast<int>(K), dw, dw_dtype == FP8MP_BF16);
+    const bool wb = dw_dtype == FP8MP_BF16;
+    cudaError_t e;
+    if (rb) e = xb ? bwd<true, true>(a, dw, wb, s, dev) : bwd<false, true>(a, dw, wb, s, dev);
+    else e = xb ? bwd<true, false>(a, dw, wb, s, dev) : bwd<false, false>(a, dw, wb, s, dev);
     if (e != cudaSuccess) return fail(FP8MP_ERR_LAUNCH, "rmsnorm: launch failed: %s", cudaGetErrorString(e));
     return FP8MP_OK;
 }
