@@ -1,0 +1,366 @@
+"""FP8GatedMLP with its norm, FP8LMHead and TokenEmbedding together: values and
+gradients against the same layers in 64 bits, streams, graphs, and the example.
+
+The kernels have their own tests; what is checked here is the composition. Where a
+GEMM's operands are rounded to FP8 the bounds are those of test_gpu_gated_mlp.py
+(relative 2-norm: 5 % for each GEMM of two E4M3 operands, 10 % where an E5M2 operand
+takes part); what does not pass through a GEMM is held to its own rounding."""
+
+import os
+import sys
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def norm64(t, w, eps):
+    return t / torch.sqrt(t.square().mean(-1, keepdim=True) + eps) * w
+
+
+def mlp64(x, gate_up, down):
+    F = gate_up.shape[0] // 2
+    return (torch.nn.functional.silu(x @ gate_up[:F].T) * (x @ gate_up[F:].T)) @ down.T
+
+
+def relative(a, b):
+    return ((a.double() - b).norm() / b.norm()).item()
+
+
+@pytest.mark.parametrize("x_dtype,r_dtype", [(BF, BF), (BF, F32), (F32, F32), (F32, BF), (BF, None), (F32, None)])
+@pytest.mark.parametrize("shape", [(1,), (3, 11), (300,)])
+def test_block_with_norm_against_64_bits(cuda_lib, shape, x_dtype, r_dtype):
+    from fp8_mixed_precision_reduce_gb300.gated_mlp import FP8GatedMLP
+
+    torch.manual_seed(1)
+    mlp = FP8GatedMLP(272, 528, norm_eps=1e-6)
+    with torch.no_grad():
+        mlp.norm.add_(torch.randn(272, device="cuda") * 0.1)
+    for turn in range(2):  # the first pass fills the histories, the second runs under their scales
+        x = torch.randn((*shape, 272), device="cuda").to(x_dtype).requires_grad_(True)
+        r = (torch.randn((*shape, 272), device="cuda") * 3).to(r_dtype).requires_grad_(True) if r_dtype else None
+        dy = (torch.randn((*shape, 272), device="cuda") * 1e-3).to(x_dtype)
+        dt = (torch.randn((*shape, 272), device="cuda") * 1e-3).to(r_dtype or x_dtype)
+        mlp.zero_grad(set_to_none=True)
+        y, total = mlp(x, r)
+        torch.autograd.backward([y, total], [dy, dt])
+        assert cuda_lib.fp8mp_check() == 0
+        if turn == 0:
+            mlp.update_scales()
+    leaves = [t.detach().double().requires_grad_(True) for t in (x, mlp.norm, mlp.gate_up, mlp.down)]
+    rd = r.detach().double().requires_grad_(True) if r_dtype else None
+    xd, nd, gd, dd = leaves
+    td = xd + rd if r_dtype else xd
+    yd = mlp64(norm64(td, nd, 1e-6), gd, dd)
+    torch.autograd.backward([yd, td], [dy.double(), dt.double()])
+    assert y.shape == total.shape == x.shape and y.dtype == x_dtype and total.dtype == (r_dtype or x_dtype)
+    if r_dtype:
+        assert torch.equal(total, (x.float() + r.float()).to(r_dtype))
+    else:
+        assert total is x
+    assert relative(y, yd.detach()) < 0.10
+    grads = [(x.grad, xd.grad), (mlp.norm.grad, nd.grad), (mlp.gate_up.grad, gd.grad), (mlp.down.grad, dd.grad)]
+    if r_dtype:
+        grads.append((r.grad, rd.grad))
+        assert r.grad.dtype == r_dtype
+    for got, want in grads:
+        assert got.shape == want.shape and relative(got, want) < 0.25
+
+
+def test_the_stream_alone(cuda_lib):
+    """Gradients of the sum, or of y, alone."""
+    from fp8_mixed_precision_reduce_gb300.gated_mlp import FP8GatedMLP
+
+    torch.manual_seed(2)
+    mlp = FP8GatedMLP(64, 96, norm_eps=1e-6)
+    x, r = (torch.randn((24, 64), device="cuda", requires_grad=True) for _ in range(2))
+    g = torch.randn((24, 64), device="cuda")
+    mlp(x, r)[1].backward(g)
+    assert torch.equal(x.grad, g) and torch.equal(r.grad, g) and mlp.norm.grad is None
+    x.grad = r.grad = None
+    mlp(x, r)[0].backward(g)
+    only = x.grad.clone()
+    assert torch.equal(x.grad, r.grad) and mlp.norm.grad is not None
+    x.grad = r.grad = None
+    y, total = mlp(x, r)
+    torch.autograd.backward([y, total], [g, g])
+    assert torch.allclose(x.grad, only + g, rtol=1e-6, atol=1e-6)
+    # parts without gradients
+    for frozen in ([mlp.gate_up, mlp.down], [mlp.norm], [mlp.norm, mlp.gate_up, mlp.down]):
+        for p in mlp.parameters():
+            p.requires_grad_(not any(p is q for q in frozen))
+            p.grad = None
+        x.grad = None
+        mlp(x, r.detach())[0].backward(g)
+        assert torch.equal(x.grad, only) and all(p.grad is None for p in frozen)
+    with torch.no_grad():
+        y2, total2 = mlp(x, r)
+        assert torch.equal(y2, y) and torch.equal(total2, total)
+
+
+def test_no_second_derivative(cuda_lib):
+    from fp8_mixed_precision_reduce_gb300.embedding import TokenEmbedding
+    from fp8_mixed_precision_reduce_gb300.gated_mlp import FP8GatedMLP
+    from fp8_mixed_precision_reduce_gb300.lm_head import FP8LMHead
+
+    x = torch.randn((16, 64), device="cuda", requires_grad=True)
+    r = torch.randn((16, 64), device="cuda", requires_grad=True)
+    t = torch.zeros(16, dtype=torch.int64, device="cuda")
+    e = TokenEmbedding(30, 64)
+    for out, of in ((FP8GatedMLP(64, 96, norm_eps=1e-6)(x, r)[0], (x, r)), (FP8LMHead(64, 30)(x, t)[0], (x,)),
+                    (e(t).float(), (e.weight,))):
+        grads = torch.autograd.grad(out.square().sum(), of, create_graph=True)
+        with pytest.raises(RuntimeError, match="second"):
+            sum(g.square().sum() for g in grads).backward()
+
+
+@pytest.mark.parametrize("x_dtype,r_dtype", [(BF, None), (F32, None), (BF, F32)])
+@pytest.mark.parametrize("tokens,vocab", [((1,), 17), ((2, 9), 1000), ((129,), 4096), ((333,), 5003)])
+def test_head_against_64_bits(cuda_lib, tokens, vocab, x_dtype, r_dtype):
+    from fp8_mixed_precision_reduce_gb300.lm_head import FP8LMHead
+
+    torch.manual_seed(3)
+    head = FP8LMHead(272, vocab, norm_eps=1e-6 if r_dtype else None)
+    with torch.no_grad():
+        head.weight.mul_(4)
+    t = torch.randint(0, vocab, tokens, device="cuda")
+    if t.numel() > 2:
+        t.view(-1)[1] = -100
+    for turn in range(2):
+        x = torch.randn((*tokens, 272), device="cuda").to(x_dtype).requires_grad_(True)
+        r = torch.randn((*tokens, 272), device="cuda").to(r_dtype).requires_grad_(True) if r_dtype else None
+        da, db = torch.randn(tokens, device="cuda"), torch.randn(tokens, device="cuda") * 0.1
+        head.zero_grad(set_to_none=True)
+        logprob, entropy = head(x, t, r)
+        torch.autograd.backward([logprob, entropy], [da, db])
+        assert cuda_lib.fp8mp_check() == 0
+        if turn == 0:
+            head.update_scales()
+    xd, wd = x.detach().double().requires_grad_(True), head.weight.detach()[:vocab].double().requires_grad_(True)
+    n = xd
+    if r_dtype:
+        rd, nd = r.detach().double().requires_grad_(True), head.norm.detach().double().requires_grad_(True)
+        n = norm64(xd + rd, nd, 1e-6)
+    logits = n @ wd.T
+    logp = torch.log_softmax(logits, -1)
+    given = t >= 0
+    at = torch.where(given, logp.gather(-1, t.clamp_min(0)[..., None])[..., 0], 0.0)
+    H = -(logp.exp() * logp).sum(-1)
+    # the logits' gradient saturates at the largest of the pass before (of one token whose
+    # weight was a tenth of this pass's, a tenth is left): 57344 / scale
+    (dlogits,) = torch.autograd.grad([at, H], logits, [da.double(), db.double()], retain_graph=True)
+    most = 57344.0 / head.meta_dlogits.scale.item()
+    logits.backward(dlogits.clamp(-most, most))
+    assert logprob.shape == entropy.shape == t.shape and logprob.dtype == F32
+    assert (logprob[~given] == 0).all()
+    # the logits have a spread of 4 and 5 % of it as error, and log p one logit's and the sum's
+    assert (logprob.double() - at.detach()).square().mean().sqrt().item() < 0.5
+    assert (entropy.double() - H.detach()).square().mean().sqrt().item() < 0.5
+    assert head.weight.grad.shape == head.weight.shape and not head.weight.grad[vocab:].any()
+    grads = [(x.grad, xd.grad), (head.weight.grad[:vocab], wd.grad)]
+    if r_dtype:
+        grads += [(r.grad, rd.grad), (head.norm.grad, nd.grad)]
+    for got, want in grads:
+        assert relative(got, want) < 0.25
+    assert head.dw_nonfinite.item() == 0
+
+
+def test_head_is_its_kernels(cuda_lib):
+    """The same calls by hand give the same bits."""
+    from fp8_mixed_precision_reduce_gb300.lm_head import FP8LMHead
+
+    torch.manual_seed(4)
+    M, K, V = 48, 64, 500
+    head = FP8LMHead(K, V)
+    x = torch.randn((M, K), device="cuda", requires_grad=True)
+    t = torch.randint(0, V, (M,), device="cuda")
+    logprob, entropy = head(x, t)
+    da = torch.randn(M, device="cuda")
+    logprob.backward(da)
+    X8 = torch.empty((M, K), dtype=torch.uint8, device="cuda")
+    (W8,) = head.weight_copies()
+    one = torch.ones(1, device="cuda")
+    cuda_lib.fp8_quantize(x.detach(), cuda_lib.E4M3, one, X8)
+    logits = torch.empty((M, 512), dtype=BF, device="cuda")
+    cuda_lib.fp8_linear_few(X8, W8, one, one, logits)
+    stats, lp, H = torch.empty((M, 2), device="cuda"), torch.empty(M, device="cuda"), torch.empty(M, device="cuda")
+    cuda_lib.mp_logprobs_fwd(logits, t, lp, stats, entropy=H, vocab=V)
+    assert torch.equal(lp, logprob) and torch.equal(H, entropy)
+    D8 = torch.empty((M, 512), dtype=torch.uint8, device="cuda")
+    cuda_lib.mp_logprobs_bwd(logits, t, stats, da, D8, scale=one, vocab=V)
+    dx, dw = torch.empty_like(x), torch.empty_like(head.weight)
+    cuda_lib.fp8_linear_bwd_rowmajor(D8, W8, X8, one, one, one, dx, dw)
+    assert torch.equal(dx, x.grad) and torch.equal(dw, head.weight.grad)
+    top, ids = head.top(x, 5)
+    want = torch.sort(logits[:, :V].float(), dim=1, descending=True, stable=True).indices[:, :5]
+    assert torch.equal(ids, want)
+    assert torch.allclose(top, torch.log_softmax(logits[:, :V].float(), 1).gather(1, want), atol=1e-5)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("dtype,out", [(F32, BF), (BF, BF), (F32, F32)])
+@pytest.mark.parametrize("shape", [(), (1,), (4, 33), (0,), (2, 0)])
+def test_embedding(cuda_lib, shape, dtype, out, fp8):
+    from fp8_mixed_precision_reduce_gb300.embedding import TokenEmbedding
+
+    torch.manual_seed(5)
+    e = TokenEmbedding(300, 48, scale=3.0, fp8=fp8, dtype=dtype, out_dtype=out)
+    ids = torch.randint(-20, 320, shape, device="cuda")
+    y = e(ids)
+    inside = (ids >= 0) & (ids < 300)
+    table = e.weight.detach().float()
+    if fp8:
+        table = (table * 1.0).clamp(-448, 448).to(torch.float8_e4m3fn).float()  # (the first scale is 1)
+    want = torch.where(inside[..., None], table[ids.clamp(0, 299)] * 3.0, 0.0).to(out)
+    assert torch.equal(y, want) and y.dtype == out and y.shape == (*shape, 48)
+    dy = torch.randn_like(y)
+    y.backward(dy)
+    g = torch.zeros((300, 48), dtype=torch.float64, device="cuda")
+    g.index_put_((ids[inside],), dy[inside].double() * 3.0, accumulate=True)
+    assert e.weight.grad.dtype == dtype
+    assert torch.allclose(e.weight.grad.double(), g, rtol=1e-2 if dtype == BF else 1e-5, atol=1e-5)
+    assert cuda_lib.fp8mp_check() == 0
+
+
+def test_embedding_and_head_of_one_weight(cuda_lib):
+    from fp8_mixed_precision_reduce_gb300.adamw import AdamW
+    from fp8_mixed_precision_reduce_gb300.embedding import TokenEmbedding
+    from fp8_mixed_precision_reduce_gb300.lm_head import FP8LMHead
+
+    torch.manual_seed(6)
+    head = FP8LMHead(64, 256)
+    e = TokenEmbedding(256, 64, fp8=True)
+    e.weight = head.weight
+    opt = AdamW([head.weight], lr=1e-3, modules=[head, e], loss_scale=1024.0)
+    ids = torch.randint(0, 256, (100,), device="cuda")
+    for _ in range(3):
+        opt.zero_grad()
+        (-head(e(ids), ids)[0].mean() * opt.loss_scale).sum().backward()
+        both = head.weight.grad.clone()
+        head.weight.grad = None
+        x = e(ids).detach()
+        (-head(x, ids)[0].mean() * opt.loss_scale).sum().backward()
+        assert not torch.equal(both, head.weight.grad)  # (the lookup's part)
+        head.weight.grad = both
+        head.update_scales()
+        e.update_scales()
+        opt.step()
+        for m in (head, e):
+            ((w, meta),) = m._weights()
+            want = (w.detach() * meta.scale).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+            assert torch.equal(m.weight_copies()[0], want)
+    assert opt.found_inf.item() == 0 and cuda_lib.fp8mp_check() == 0
+
+
+def model(cuda_lib, seed=7):
+    sys.path.insert(0, os.path.join(ROOT, "examples"))
+    import train_language_model as ex
+
+    torch.manual_seed(seed)
+    return ex.Model(500, 64, 96, 2)
+
+
+def passes(m, ids):
+    logprob, entropy = m(ids[:, :-1], ids[:, 1:])
+    (-logprob.mean() - 0.01 * entropy.mean()).backward()
+    return logprob, entropy
+
+
+def test_a_model_on_another_stream(cuda_lib):
+    m = model(cuda_lib)
+    ids = torch.randint(0, 500, (8, 20), device="cuda")
+    want = passes(m, ids)
+    grads = [p.grad.clone() for p in m.parameters()]
+    m.zero_grad(set_to_none=True)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = passes(m, ids)
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert all(torch.equal(p.grad, g) for p, g in zip(m.parameters(), grads))
+
+
+def test_serving_from_a_graph(cuda_lib):
+    m = model(cuda_lib).eval()
+    ids = torch.randint(0, 500, (5,), device="cuda")
+    with torch.no_grad():
+        m.top(ids, 3)  # (the weights are cast)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            logprob, tokens = m.top(ids, 3)
+        for seed in range(3):
+            ids.copy_(torch.randint(-1, 500, (5,), device="cuda"))
+            graph.replay()
+            want = m.top(ids, 3)
+            assert torch.equal(logprob, want[0]) and torch.equal(tokens, want[1])
+        m.head.weight.mul_(-1)
+        m.head.weight_copies()
+        graph.replay()
+        assert torch.equal(tokens, m.top(ids, 3)[1])
+
+
+def test_a_training_pass_from_a_graph(cuda_lib):
+    m = model(cuda_lib)
+    ids = torch.randint(0, 500, (8, 20), device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):  # (as captures of a backward pass ask for)
+        passes(m, ids)
+    torch.cuda.current_stream().wait_stream(side)
+    m.zero_grad(set_to_none=True)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        logprob, _ = passes(m, ids)
+    for seed in range(2):
+        ids.copy_(torch.randint(0, 500, (8, 20), device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [logprob.clone()] + [p.grad.clone() for p in m.parameters()]
+        twin = model(cuda_lib)
+        want = [passes(twin, ids)[0]] + [p.grad for p in twin.parameters()]
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_the_example_runs(cuda_lib, bits):
+    sys.path.insert(0, os.path.join(ROOT, "examples"))
+    import train_language_model as ex
+
+    losses, good = ex.run(vocab=203, features=64, hidden=96, blocks=2, batch=8, length=15, steps=6, bits=bits, log=lambda s: None)
+    assert len(losses) == 6 and all(0 < x < 50 for x in losses) and 0 <= good <= 1
+    assert cuda_lib.fp8mp_check() == 0
+
+
+def test_a_models_gradients_against_differences_of_scales(cuda_lib):
+    """The gradient of the whole model's loss with respect to each norm's weight, scaled
+    by (1 + h) and (1 - h): differences of the FP8 model are no use (its codes jump), so
+    of the same model in 64 bits."""
+    m = model(cuda_lib)
+    ids = torch.randint(0, 500, (16, 33), device="cuda")
+    for _ in range(2):
+        m.zero_grad(set_to_none=True)
+        logprob, _ = m(ids[:, :-1], ids[:, 1:])
+        (-logprob.mean() * 1024).backward()
+        for f in m.fp8_modules():
+            f.update_scales()
+
+    def loss(factor):
+        e = m.embedding
+        x, r = e.weight.double()[ids[:, :-1]] * e.scale, None
+        for b in m.blocks:
+            t = x if r is None else x + r
+            x, r = mlp64(norm64(t, b.norm.double() * factor, 1e-6), b.gate_up.double(), b.down.double()), t
+        n = norm64(x + r, m.head.norm.double(), 1e-6)
+        logp = torch.log_softmax(n @ m.head.weight.double()[:500].T, -1)
+        return -logp.gather(-1, ids[:, 1:, None]).mean().item()
+
+    with torch.no_grad():
+        h = 1e-4
+        want = (loss(1 + h) - loss(1 - h)) / (2 * h) * 1024
+        got = sum((b.norm.grad.double() * b.norm.double()).sum().item() for b in m.blocks)
+        size = sum((b.norm.grad.double() * b.norm.double()).norm().item() for b in m.blocks)
+    assert abs(got - want) <= 0.25 * max(abs(want), size), (got, want)

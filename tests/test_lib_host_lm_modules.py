@@ -1,0 +1,142 @@
+"""FP8GatedMLP with its norm, FP8LMHead and TokenEmbedding without a GPU: what they
+refuse, and their weights' copies, on CPU tensors with the casts in plain torch."""
+
+import copy
+
+import pytest
+import torch
+
+import fp8_mixed_precision_reduce_gb300 as fp8mp
+from fp8_mixed_precision_reduce_gb300 import adamw, embedding, gated_mlp, lm_head
+from test_lib_host_modules import cast, plain, step  # noqa: F401
+
+I64 = torch.int64
+
+
+def mlp(**kw):
+    return gated_mlp.FP8GatedMLP(32, 48, device="cpu", norm_eps=1e-6, **kw)
+
+
+def head(**kw):
+    return lm_head.FP8LMHead(32, 50, device="cpu", **kw)
+
+
+def table(**kw):
+    return embedding.TokenEmbedding(50, 32, device="cpu", **kw)
+
+
+@pytest.mark.parametrize("make", [
+    lambda: gated_mlp.FP8GatedMLP(16400, 32, device="cpu", norm_eps=1e-6), lambda: gated_mlp.FP8GatedMLP(32, 32, device="cpu", norm_eps=-1.0),
+    lambda: gated_mlp.FP8GatedMLP(32, 32, device="cpu", norm_eps=float("nan")), lambda: lm_head.FP8LMHead(24, 50, device="cpu"),
+    lambda: lm_head.FP8LMHead(32, 0, device="cpu"), lambda: lm_head.FP8LMHead(32, 50, device="cpu", norm_eps=float("inf")),
+    lambda: embedding.TokenEmbedding(50, 40, device="cpu"), lambda: embedding.TokenEmbedding(0, 32, device="cpu"),
+    lambda: embedding.TokenEmbedding(50, 32, device="cpu", out_dtype=torch.float16)])
+def test_sizes_that_no_kernel_takes(make):
+    with pytest.raises(ValueError):
+        make()
+
+
+@pytest.mark.parametrize("make", [mlp, lambda: head(norm_eps=1e-6)])
+def test_residuals_that_do_not_fit(make):
+    m = make()
+    call = (lambda x, r: m(x, r)) if isinstance(m, gated_mlp.FP8GatedMLP) else (lambda x, r: m(x, torch.zeros(4, dtype=I64), r))
+    x = torch.zeros((4, 32))
+    for r in (torch.zeros((3, 32)), torch.zeros((4, 32, 1)), torch.zeros((4, 32), dtype=torch.float16), torch.zeros((4, 32), device="meta")):
+        with pytest.raises(ValueError, match="residual"):
+            call(x, r)
+    m.norm.data = torch.ones(16)
+    with pytest.raises(ValueError, match="norm"):
+        call(x, x)
+
+
+def test_a_residual_needs_the_norm():
+    x = torch.zeros((4, 32))
+    with pytest.raises(ValueError, match="norm"):
+        gated_mlp.FP8GatedMLP(32, 48, device="cpu")(x, x)
+    with pytest.raises(ValueError, match="norm"):
+        head()(x, torch.zeros(4, dtype=I64), x)
+
+
+@pytest.mark.parametrize("x,t", [(torch.zeros(4, 16), torch.zeros(4, dtype=I64)), (torch.zeros(4, 32), torch.zeros(4)),
+                                 (torch.zeros(4, 32), torch.zeros(5, dtype=I64)), (torch.zeros(4, 32), torch.zeros((4, 1), dtype=I64)),
+                                 (torch.zeros(4, 32), torch.zeros(4, dtype=I64, device="meta"))])
+def test_targets_that_do_not_fit(x, t):
+    with pytest.raises(ValueError):
+        head()(x, t)
+
+
+@pytest.mark.parametrize("k", [0, -1, 33, 51])
+def test_top_of_too_many(k):
+    with pytest.raises(ValueError, match="k must"):
+        head().top(torch.zeros(4, 32), k)
+    with pytest.raises(ValueError, match="1..7"):
+        lm_head.FP8LMHead(32, 7, device="cpu").top(torch.zeros(4, 32), 8)
+
+
+@pytest.mark.parametrize("ids", [torch.zeros(3), torch.zeros(3, dtype=torch.int32), torch.zeros(3, dtype=I64, device="meta")])
+def test_ids_that_do_not_fit(ids):
+    with pytest.raises(ValueError, match="ids"):
+        table()(ids)
+
+
+def test_an_embedding_of_another_shape_is_refused():
+    m = table()
+    m.weight.data = torch.zeros((49, 32))
+    with pytest.raises(ValueError, match="weight"):
+        m(torch.zeros(3, dtype=I64))
+
+
+def test_rows_are_dense_and_aligned():
+    flat = torch.arange(200.0)
+    for x in (flat[:64].view(2, 32), flat[1:65].view(2, 32), flat[:128].view(2, 64)[:, :32], flat[:64].view(32, 2).t(),
+              flat[:32].expand(3, 32)):
+        rows = gated_mlp._rows(x, 32)
+        assert rows.is_contiguous() and rows.data_ptr() % 16 == 0 and torch.equal(rows, x.reshape(-1, 32))
+
+
+def test_the_heads_added_rows_have_no_token():
+    m = head()
+    assert m.weight.shape == (64, 32) and (m.weight[50:] == 0).all() and (m.weight[:50] != 0).any(1).all()
+
+
+def test_steps_write_the_copies(plain):  # noqa: F811
+    torch.manual_seed(0)
+    modules = [mlp(), head(norm_eps=1e-6), table(fp8=True), table()]
+    params = [p for m in modules for p in m.parameters()]
+    opt = adamw.AdamW(params, lr=1e-2, modules=modules)
+    for _ in range(3):
+        step(opt, *modules)
+        for m in modules:
+            for c, (w, meta) in zip(m.weight_copies(), m._weights()):
+                assert torch.equal(c, cast(w, meta.scale))
+    assert modules[3].weight_copies() == () and modules[3].metas() == []
+
+
+def test_only_the_weights_have_copies(plain):  # noqa: F811
+    """The norm's weight is read as it is."""
+    assert len(mlp()._copies) == 2 and len(head(norm_eps=1e-6)._copies) == 1
+    assert [n for n, _ in gated_mlp.FP8GatedMLP(32, 48, device="cpu").named_parameters()] == ["gate_up", "down"]
+
+
+def test_a_copy_of_a_module_casts_its_own(plain):  # noqa: F811
+    m = table(fp8=True)
+    m.weight_copies()
+    twin = copy.deepcopy(m)
+    with torch.no_grad():
+        twin.weight.mul_(-1)
+    (mine,), (its,) = m.weight_copies(), twin.weight_copies()
+    assert torch.equal(mine, cast(m.weight, m.meta_weight.scale)) and torch.equal(its, cast(twin.weight, twin.meta_weight.scale))
+
+
+def test_a_weight_held_twice(plain):  # noqa: F811
+    """An embedding and a head that share one weight."""
+    h = lm_head.FP8LMHead(32, 64, device="cpu")
+    e = embedding.TokenEmbedding(64, 32, device="cpu", fp8=True)
+    e.weight = h.weight
+    opt = adamw.AdamW([h.weight], lr=1e-2, modules=[h, e])
+    for _ in range(2):
+        step(opt, h, e)
+        for m in (h, e):
+            (c,), ((w, meta),) = m.weight_copies(), m._weights()
+            assert torch.equal(c, cast(w, meta.scale))
+    assert fp8mp.E4M3 == h.meta_weight.fmt
