@@ -41,9 +41,9 @@ class Model(torch.nn.Module):
             x, residual = block(x, residual)
         return x, residual
 
-    def forward(self, ids, targets):
+    def forward(self, ids, targets, entropy: bool = False):
         x, residual = self.stream(ids)
-        return self.head(x, targets, residual)
+        return self.head(x, targets, residual, entropy)
 
     def top(self, ids, k: int = 1):
         x, residual = self.stream(ids)
@@ -68,7 +68,7 @@ def run(vocab=1000, features=256, hidden=704, blocks=2, batch=32, length=63, ste
     losses = []
     for step in range(steps):
         ids = texts(follow, batch, length)
-        logprob, _ = model(ids[:, :-1], ids[:, 1:])
+        logprob = model(ids[:, :-1], ids[:, 1:])
         loss = -logprob.mean()
         opt.zero_grad()
         (loss * opt.loss_scale).sum().backward()

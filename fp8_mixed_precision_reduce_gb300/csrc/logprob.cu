@@ -482,8 +482,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) logp_fwd_kernel(const LogpAr
 // ---------------------------------------------------------------- gradient
 
 constexpr int kGradThreads = 256, kGradUnroll = 4;
-constexpr int64_t kGradBytes = 131072, kMinGradBytes = 8192;  // of logits for each CTA, about, and at least
-constexpr int kGradPerSm = 6;  // CTAs
+constexpr int kGradPerSm = 5;  // CTAs
+constexpr int kGradRound = kGradThreads * kGradUnroll;  // pieces of a row that a CTA has in flight
 
 struct LogpGradArgs {
     const uint8_t *x;
@@ -495,6 +495,8 @@ struct LogpGradArgs {
     int64_t V, ld;
     int splits;  // CTAs that share a row
 };
+
+__host__ __device__ inline int64_t least(int64_t a, int64_t b) { return a < b ? a : b; }
 
 // What a row's elements share: dx = p (c0 + c1 z), with z = log2 p.
 struct RowGrad {
@@ -514,7 +516,7 @@ __device__ __forceinline__ float grad_of(float x, const RowGrad &g) {
 }
 
 template <bool BF16, bool CODES, bool ENT>
-__global__ void __launch_bounds__(kGradThreads) logp_bwd_kernel(const LogpGradArgs a) {
+__global__ void __launch_bounds__(kGradThreads, kGradPerSm) logp_bwd_kernel(const LogpGradArgs a) {
     using R = Row<BF16>;
     constexpr int ES = R::ES, EP = R::EP;
     pdl_wait();
@@ -524,7 +526,9 @@ __global__ void __launch_bounds__(kGradThreads) logp_bwd_kernel(const LogpGradAr
     const int part = static_cast<int>(blockIdx.x % a.splits);
     const R row(a.x + m_row * a.ld * ES, a.ld);  // the columns from V on included: theirs is 0
     uint8_t *out = a.out + m_row * a.ld * (CODES ? 1 : ES);
-    const int64_t p0 = row.pieces * part / a.splits, p1 = row.pieces * (part + 1) / a.splits;
+    // whole rounds for each CTA, the row's last one but for the rest
+    const int64_t rounds = (row.pieces + kGradRound - 1) / kGradRound;
+    const int64_t p0 = rounds * part / a.splits * kGradRound, p1 = least(rounds * (part + 1) / a.splits * kGradRound, row.pieces);
     const uint4 *body = row.body();
     // the first logits are on their way before what the row's elements share
     uint4 q[kGradUnroll];
@@ -623,6 +627,22 @@ int splits_for(int64_t M, int64_t bytes, int num_sms) {
     return best;
 }
 
+// CTAs that share a row of `pieces` in the backward pass: those with which the last
+// is done first, when a CTA costs a round and a half of its own.
+int grad_splits_for(int64_t M, int64_t pieces, int num_sms) {
+    const int64_t rounds = (pieces + kGradRound - 1) / kGradRound, slots = static_cast<int64_t>(num_sms) * kGradPerSm;
+    int best = 1;
+    int64_t fewest = 0;
+    for (int s = 1; s <= 64 && s <= rounds; ++s) {
+        const int64_t cost = (M * s + slots - 1) / slots * (2 * ((rounds + s - 1) / s) + 3);
+        if (s == 1 || cost < fewest) {
+            fewest = cost;
+            best = s;
+        }
+    }
+    return best;
+}
+
 template <bool BF16, bool ENT>
 cudaError_t fwd(const LogpArgs &a, int64_t M, cudaStream_t s) {
     const dim3 grid(static_cast<unsigned>(M * a.splits)), block(kThreads);
@@ -659,12 +679,7 @@ int launch_logprobs_bwd(const void *x, int x_dtype, int64_t M, int64_t V, int64_
                         const float *scale, void *dlogits, float *amax, cudaStream_t s, const DeviceInfo &dev) {
     LogpGradArgs a = {static_cast<const uint8_t *>(x), target, reinterpret_cast<const float2 *>(stats), dlogprob, dentropy,
                       entropy, scale, amax, static_cast<uint8_t *>(dlogits), V, ld, 1};
-    const int64_t bytes = ld * (x_dtype == FP8MP_BF16 ? 2 : 4), few = (static_cast<int64_t>(kGradPerSm) * dev.num_sms + M - 1) / M;
-    int64_t parts = bytes / kGradBytes;
-    if (parts < few) parts = few;
-    if (parts > bytes / kMinGradBytes) parts = bytes / kMinGradBytes;
-    if (parts > 0x7FFFFFFFll / M) parts = 0x7FFFFFFFll / M;
-    a.splits = static_cast<int>(parts < 1 ? 1 : parts);
+    a.splits = grad_splits_for(M, ld / (x_dtype == FP8MP_BF16 ? 8 : 4), dev.num_sms);
     const bool b = x_dtype == FP8MP_BF16;
     cudaError_t e;
     if (scale != nullptr) e = b ? bwd<true, true>(a, M, s) : bwd<false, true>(a, M, s);

@@ -42,31 +42,33 @@ def _logits_of(x, residual, norm, head, for_training: bool):
 
 class _FP8LMHeadFn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, residual, norm, weight, targets, head, keep):
+    def forward(ctx, x, residual, norm, weight, targets, head, with_entropy, keep):
         logits, X8, w8, normed, rstd, norm = _logits_of(x, residual, norm, head, keep)
         M, dev = logits.shape[0], x.device
         t = targets.reshape(-1)
         t = t if t.is_contiguous() else t.contiguous()
-        logprob, entropy = (torch.empty(M, dtype=torch.float32, device=dev) for _ in range(2))
+        logprob = torch.empty(M, dtype=torch.float32, device=dev)
+        entropy = torch.empty_like(logprob) if with_entropy else None
         stats = torch.empty((M, 2), dtype=torch.float32, device=dev)
         mp_logprobs_fwd(logits, t, logprob, stats, entropy=entropy, vocab=head.vocab)
-        logprob, entropy = logprob.reshape(targets.shape), entropy.reshape(targets.shape)
+        logprob = logprob.reshape(targets.shape)
+        entropy = entropy.reshape(targets.shape) if with_entropy else None
         if keep:
             factors = torch.cat([head.meta_x.scale_inv, head.meta_weight.scale_inv])
             ctx.save_for_backward(logits, X8, w8, t, stats, entropy, factors, normed if norm is not None else None, rstd, norm)
             ctx.head = head
             ctx.like = (x.shape, x.dtype, weight.dtype)
             ctx.set_materialize_grads(False)
-        return logprob, entropy
+        return (logprob, entropy) if with_entropy else logprob
 
     @staticmethod
-    def backward(ctx, dlogprob, dentropy):
+    def backward(ctx, dlogprob, dentropy=None):
         logits, X8, w8, t, stats, entropy, factors, normed, rstd, norm = ctx.saved_tensors
         head = ctx.head
         x_shape, x_dtype, w_dtype = ctx.like
         need_x, need_residual, need_norm, need_weight = ctx.needs_input_grad[:4]
         if dlogprob is None and dentropy is None:
-            return (None,) * 7
+            return (None,) * 8
         M, K, dev = logits.shape[0], head.features, logits.device
         flat = lambda g: g.to(torch.float32).reshape(-1).contiguous()  # noqa: E731
         da = flat(dlogprob) if dlogprob is not None else torch.zeros(M, dtype=torch.float32, device=dev)
@@ -88,7 +90,7 @@ class _FP8LMHeadFn(torch.autograd.Function):
                 dx, dresidual, dnorm = _norm_grads(dx, normed, None, norm, rstd, x_dtype, need_norm)
         dx = dx.reshape(x_shape) if need_x else None
         dresidual = dresidual.reshape(x_shape) if need_residual else None
-        return *first_order(dx, dresidual, dnorm, dw), None, None, None
+        return *first_order(dx, dresidual, dnorm, dw), None, None, None, None
 
 
 class FP8LMHead(_WeightCopies, torch.nn.Module):
@@ -99,9 +101,9 @@ class FP8LMHead(_WeightCopies, torch.nn.Module):
     weight is kept in high precision with an E4M3 copy as FP8GatedMLP keeps its own;
     call update_scales() once per training step, after backward.
 
-    head(x, targets) gives (log p of each target, entropy), fp32 in the targets' shape,
-    differentiable; a target outside 0 .. vocab - 1 (a prompt's or padding's) has log p 0
-    and no gradient. head.top(x, k) gives the k most probable tokens and their log p.
+    head(x, targets) gives the log p of each target, with entropy=True (log p, entropy),
+    fp32 in the targets' shape, differentiable; a target outside 0 .. vocab - 1 (a prompt's
+    or padding's) has log p 0 and no gradient. head.top(x, k) gives the k most probable tokens and their log p.
     With norm_eps both take the residual stream: n = norm(x + residual).
     """
 
@@ -135,14 +137,14 @@ class FP8LMHead(_WeightCopies, torch.nn.Module):
         _check_input(x, residual, self.features, self._copies[0].device, self.norm)
         _check_norm_weight(self.norm, x, self.features)
 
-    def forward(self, x: torch.Tensor, targets: torch.Tensor, residual: torch.Tensor | None = None):
+    def forward(self, x: torch.Tensor, targets: torch.Tensor, residual: torch.Tensor | None = None, entropy: bool = False):
         self._check(x, residual)
         if targets.shape != x.shape[:-1] or targets.dtype != torch.int64 or targets.device != x.device:
             raise ValueError(f"targets must be int64 {tuple(x.shape[:-1])} on {x.device}, got {targets.dtype} "
                              f"{tuple(targets.shape)} on {targets.device}")
         inputs = (x, residual, self.norm, self.weight)
         keep = torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs)
-        return _FP8LMHeadFn.apply(*inputs, targets, self, keep)
+        return _FP8LMHeadFn.apply(*inputs, targets, self, entropy, keep)
 
     @torch.no_grad()
     def top(self, x: torch.Tensor, k: int = 1, residual: torch.Tensor | None = None):

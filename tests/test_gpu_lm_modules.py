@@ -110,7 +110,7 @@ def test_no_second_derivative(cuda_lib):
     r = torch.randn((16, 64), device="cuda", requires_grad=True)
     t = torch.zeros(16, dtype=torch.int64, device="cuda")
     e = TokenEmbedding(30, 64)
-    for out, of in ((FP8GatedMLP(64, 96, norm_eps=1e-6)(x, r)[0], (x, r)), (FP8LMHead(64, 30)(x, t)[0], (x,)),
+    for out, of in ((FP8GatedMLP(64, 96, norm_eps=1e-6)(x, r)[0], (x, r)), (FP8LMHead(64, 30)(x, t), (x,)),
                     (e(t).float(), (e.weight,))):
         grads = torch.autograd.grad(out.square().sum(), of, create_graph=True)
         with pytest.raises(RuntimeError, match="second"):
@@ -134,7 +134,7 @@ def test_head_against_64_bits(cuda_lib, tokens, vocab, x_dtype, r_dtype):
         r = torch.randn((*tokens, 272), device="cuda").to(r_dtype).requires_grad_(True) if r_dtype else None
         da, db = torch.randn(tokens, device="cuda"), torch.randn(tokens, device="cuda") * 0.1
         head.zero_grad(set_to_none=True)
-        logprob, entropy = head(x, t, r)
+        logprob, entropy = head(x, t, r, entropy=True)
         torch.autograd.backward([logprob, entropy], [da, db])
         assert cuda_lib.fp8mp_check() == 0
         if turn == 0:
@@ -177,7 +177,7 @@ def test_head_is_its_kernels(cuda_lib):
     head = FP8LMHead(K, V)
     x = torch.randn((M, K), device="cuda", requires_grad=True)
     t = torch.randint(0, V, (M,), device="cuda")
-    logprob, entropy = head(x, t)
+    logprob, entropy = head(x, t, entropy=True)
     da = torch.randn(M, device="cuda")
     logprob.backward(da)
     X8 = torch.empty((M, K), dtype=torch.uint8, device="cuda")
@@ -188,7 +188,7 @@ def test_head_is_its_kernels(cuda_lib):
     cuda_lib.fp8_linear_few(X8, W8, one, one, logits)
     stats, lp, H = torch.empty((M, 2), device="cuda"), torch.empty(M, device="cuda"), torch.empty(M, device="cuda")
     cuda_lib.mp_logprobs_fwd(logits, t, lp, stats, entropy=H, vocab=V)
-    assert torch.equal(lp, logprob) and torch.equal(H, entropy)
+    assert torch.equal(lp, logprob) and torch.equal(H, entropy) and torch.equal(head(x, t), logprob)
     D8 = torch.empty((M, 512), dtype=torch.uint8, device="cuda")
     cuda_lib.mp_logprobs_bwd(logits, t, stats, da, D8, scale=one, vocab=V)
     dx, dw = torch.empty_like(x), torch.empty_like(head.weight)
@@ -238,11 +238,11 @@ def test_embedding_and_head_of_one_weight(cuda_lib):
     ids = torch.randint(0, 256, (100,), device="cuda")
     for _ in range(3):
         opt.zero_grad()
-        (-head(e(ids), ids)[0].mean() * opt.loss_scale).sum().backward()
+        (-head(e(ids), ids).mean() * opt.loss_scale).sum().backward()
         both = head.weight.grad.clone()
         head.weight.grad = None
         x = e(ids).detach()
-        (-head(x, ids)[0].mean() * opt.loss_scale).sum().backward()
+        (-head(x, ids).mean() * opt.loss_scale).sum().backward()
         assert not torch.equal(both, head.weight.grad)  # (the lookup's part)
         head.weight.grad = both
         head.update_scales()
@@ -264,7 +264,7 @@ def model(cuda_lib, seed=7):
 
 
 def passes(m, ids):
-    logprob, entropy = m(ids[:, :-1], ids[:, 1:])
+    logprob, entropy = m(ids[:, :-1], ids[:, 1:], entropy=True)
     (-logprob.mean() - 0.01 * entropy.mean()).backward()
     return logprob, entropy
 
@@ -343,7 +343,7 @@ def test_a_models_gradients_against_differences_of_scales(cuda_lib):
     ids = torch.randint(0, 500, (16, 33), device="cuda")
     for _ in range(2):
         m.zero_grad(set_to_none=True)
-        logprob, _ = m(ids[:, :-1], ids[:, 1:])
+        logprob = m(ids[:, :-1], ids[:, 1:])
         (-logprob.mean() * 1024).backward()
         for f in m.fp8_modules():
             f.update_scales()
