@@ -15,7 +15,8 @@
 // time by a block of 256 threads. Each warp copies its own pieces of the rows to come
 // into shared memory (cp.async) and reads nothing else there, so no barrier is
 // needed but the one inside a row's sum, and loads are in flight while a row is
-// reduced and written.
+// reduced and written. 16384 x 4096, bf16: forward with residual and E4M3 out 71 us
+// (6.6 TB/s), backward 86 (6.3), 86 and 126 with loads into registers instead.
 #include <atomic>
 #include <mutex>
 

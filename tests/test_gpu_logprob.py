@@ -2,9 +2,10 @@
 
 Tolerances. u = 2^-24, z = (x - m) log2(e). exp2's hardware approximation is good
 to 4 u of the result, its argument to 2 u |z|, so a term of S is off by
-(2 |z| ln 2 + 4) u of itself. A thread adds V / 1024 terms to each of four running
-sums, whose rescaling (one product, as an exponential, at every larger maximum, at most
-every V / 512 / 32 terms) and 9 joins add (V / 1024 + 60) u at most. log S adds two
+(2 |z| ln 2 + 4) u of itself. Of a long row a thread
+adds V / 1024 terms to each of four running sums (of a short one, of at most 16384
+elements, V / 128: 128), whose rescaling (one product, as an exponential, at every larger
+maximum) and 9 joins add (V / 1024 + 60) u at most (of a short one V / 128 + 60). log S adds two
 roundings of |log S|, the subtractions those of their results. What is sum_v p_v |z_v| or
 p_v z_v^2 there is taken from the 64-bit p."""
 
@@ -53,8 +54,9 @@ def reference(x):
     p = torch.exp(logp)
     z = torch.where(p > 0, d, 0.0).abs() / LN2
     V = x.shape[1]
-    of_s = (p * (2 * LN2 * z + 4)).sum(1) + V / 1024 + 60 + 4 * log_s[:, 0]
-    of_h = of_s + LN2 * (p * z * (2 * LN2 * z + 8)).sum(1) + LN2 * (V / 1024 + 64) * (p * z).sum(1)
+    adds = V / (128 if V <= 16384 else 1024) + 60
+    of_s = (p * (2 * LN2 * z + 4)).sum(1) + adds + 4 * log_s[:, 0]
+    of_h = of_s + LN2 * (p * z * (2 * LN2 * z + 8)).sum(1) + LN2 * (adds + 4) * (p * z).sum(1)
     return logp, d, log_s[:, 0], of_s, of_h
 
 
@@ -63,7 +65,8 @@ def ranked(x, k):
     return torch.sort(x.float() + 0.0, dim=1, descending=True, stable=True).indices[:, :k]
 
 
-SIZES = [(1, 1), (3, 2), (2, 7), (5, 50), (9, 1000), (4, 4097), (1, 50001), (333, 5003), (7, 128000), (40, 128000), (150, 33333)]
+SIZES = [(1, 1), (3, 2), (2, 7), (5, 50), (9, 1000), (4, 4097), (1, 50001), (333, 5003), (7, 128000), (40, 128000), (150, 33333),
+         (5000, 515), (6000, 8001), (5001, 16385)]
 
 
 @pytest.mark.parametrize("M,V", SIZES)
@@ -72,26 +75,27 @@ SIZES = [(1, 1), (3, 2), (2, 7), (5, 50), (9, 1000), (4, 4097), (1, 50001), (333
 def test_forward(cuda_lib, M, V, dtype, masked):
     x, t = logits(M, V, dtype, masked=masked)
     k = min(V, 20)
-    logprob, stats, H, top, ids = forward(cuda_lib, x, t, k)
     logp, d, log_s, of_s, of_h = reference(x)
     given = t >= 0
     at = logp.gather(1, t.clamp_min(0)[:, None])[:, 0]
     room = (of_s + 2 * d.gather(1, t.clamp_min(0)[:, None])[:, 0].abs() + 2) * U
-    assert (logprob[~given] == 0).all()
-    assert ((logprob.double() - at).abs() <= room)[given].all()
-    assert torch.equal(stats[:, 0], x.float().amax(1))
-    assert ((stats[:, 1].double() - log_s).abs() <= of_s * U).all()
     want = -(torch.exp(logp) * torch.where(logp > -INF, logp, 0.0)).sum(1)
-    assert ((H.double() - want).abs() <= of_h * U).all()
-    best = ranked(x, k)
-    assert torch.equal(ids, best)
-    want, far = logp.gather(1, best), d.gather(1, best)
-    assert torch.equal(torch.isinf(top), torch.isinf(want))
-    fine = torch.isfinite(want)
-    assert ((top.double() - want).abs() <= (of_s[:, None] + 2 * far.abs() + 2) * U)[fine].all()
-    # without the extras, the same bits
-    plain = forward(cuda_lib, x, t, entropy=False)
-    assert torch.equal(plain[0], logprob) and torch.equal(plain[1], stats)
+    # with everything, with the entropy, with neither: short rows go another way without the top
+    for kk, entropy in ((k, True), (0, True), (0, False)):
+        logprob, stats, H, top, ids = forward(cuda_lib, x, t, kk, entropy)
+        assert (logprob[~given] == 0).all()
+        assert ((logprob.double() - at).abs() <= room)[given].all()
+        assert torch.equal(stats[:, 0], x.float().amax(1))
+        assert ((stats[:, 1].double() - log_s).abs() <= of_s * U).all()
+        if entropy:
+            assert ((H.double() - want).abs() <= of_h * U).all()
+        if kk:
+            best = ranked(x, k)
+            assert torch.equal(ids, best)
+            wanted, far = logp.gather(1, best), d.gather(1, best)
+            assert torch.equal(torch.isinf(top), torch.isinf(wanted))
+            fine = torch.isfinite(wanted)
+            assert ((top.double() - wanted).abs() <= (of_s[:, None] + 2 * far.abs() + 2) * U)[fine].all()
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -161,7 +165,7 @@ def test_rows_of_infinities_nan_and_lowest_values(cuda_lib, dtype, M):
     assert torch.isfinite(dx[others]).all()
 
 
-BACK = [(1, 1), (3, 7), (5, 50), (9, 1008), (4, 4097), (2, 50001), (333, 5008), (7, 128000), (1300, 2064)]
+BACK = [(1, 1), (3, 7), (5, 50), (9, 1008), (4, 4097), (2, 50001), (333, 5008), (7, 128000), (1300, 2064), (2001, 2047)]
 
 
 @pytest.mark.parametrize("M,V", BACK)
