@@ -1104,6 +1104,7 @@ static int check_logits(const char *fn, const void *logits, int32_t x_dtype, int
     REQUIRE(M >= 0 && M <= (1ll << 30), "%s: M = %lld outside 0..2^30", fn, (long long)M);
     REQUIRE(V >= 1 && V <= ld && ld <= 0x7FFFFFFFll, "%s: V = %lld, ld = %lld: 1 <= V <= ld < 2^31", fn, (long long)V,
             (long long)ld);
+    REQUIRE(M == 0 || ld <= (1ll << 44) / M, "%s: M * ld too large", fn);
     if (M > 0) CHECK_ELEMENTS(logits, static_cast<uintptr_t>(width(x_dtype)), true);
     return FP8MP_OK;
 }
@@ -1180,6 +1181,7 @@ static int check_table(const char *fn, const int64_t *ids, int64_t M, int64_t V,
     REQUIRE(valid_table_dims(M, V, K),
             "%s: M = %lld outside 0..2^30 - 1, V = %lld outside 0..2^31 - 1, or K = %lld no multiple of 16 in 0..2^20", fn,
             (long long)M, (long long)V, (long long)K);
+    REQUIRE(K == 0 || M <= (1ll << 40) / K, "%s: M * K too large", fn);
     if (M > 0 && K > 0) CHECK_ELEMENTS(ids, 8, true);
     return FP8MP_OK;
 }

@@ -101,9 +101,10 @@ def _codes_of(x2, residual, norm, eps, meta, X8):
     return total, rstd
 
 
-def _norm_grads(dxn, total, dtotal, norm, rstd, x_dtype, need_norm):
+def _norm_grads(dxn, total, dtotal, norm, rstd, x_dtype, need_norm, shape):
     """(dx, dresidual, dnorm) of _codes_of's norm from the gradient of its output and of
-    the sum."""
+    the sum. Of one type, dx and dresidual are one tensor, as an addition's gradients
+    are: two views of its memory would each be taken for a gradient of its own."""
     M, K = dxn.shape
     dresidual = torch.empty_like(total)
     dx = torch.empty((M, K), dtype=x_dtype, device=dxn.device) if x_dtype != total.dtype else None
@@ -114,7 +115,8 @@ def _norm_grads(dxn, total, dtotal, norm, rstd, x_dtype, need_norm):
     if dtotal is not None:
         dtotal = _rows(dtotal.to(total.dtype), K)
     fp8_rmsnorm_bwd(dxn, total, norm, rstd, dresidual, dnorm, workspace, dtotal=dtotal, dx=dx)
-    return dresidual if dx is None else dx, dresidual, dnorm
+    dresidual = dresidual.reshape(shape)
+    return dresidual if dx is None else dx.reshape(shape), dresidual, dnorm
 
 
 def _check_norm_weight(norm, x, features: int) -> None:
@@ -202,10 +204,10 @@ class _FP8GatedMLPFn(torch.autograd.Function):
             fp8_gated_bwd(None, None, X8, gu8, sinv_x, sinv_gu, None, mg.scale_inv, G8, dx, dgate_up, act=mlp.act,
                           dw_nonfinite=mlp.dw_nonfinite if dgate_up is not None else None)
         if need_in and norm is not None:
-            dx, dresidual, dnorm = _norm_grads(dx, _rows(normed, K), dtotal, norm, rstd, x_dtype, need_norm)
-        dx = dx.reshape(x_shape) if need_x else None
-        dresidual = dresidual.reshape(x_shape) if need_residual else None
-        return *first_order(dx, dresidual, dnorm, dgate_up, ddown), None, None
+            dx, dresidual, dnorm = _norm_grads(dx, _rows(normed, K), dtotal, norm, rstd, x_dtype, need_norm, x_shape)
+        elif dx is not None:
+            dx = dx.reshape(x_shape)
+        return *first_order(dx if need_x else None, dresidual if need_residual else None, dnorm, dgate_up, ddown), None, None
 
 
 class _WeightCopies:

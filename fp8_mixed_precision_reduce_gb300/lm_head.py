@@ -87,10 +87,10 @@ class _FP8LMHeadFn(torch.autograd.Function):
         if dx is not None:
             dx = dx[:M]
             if norm is not None:
-                dx, dresidual, dnorm = _norm_grads(dx, normed, None, norm, rstd, x_dtype, need_norm)
-        dx = dx.reshape(x_shape) if need_x else None
-        dresidual = dresidual.reshape(x_shape) if need_residual else None
-        return *first_order(dx, dresidual, dnorm, dw), None, None, None, None
+                dx, dresidual, dnorm = _norm_grads(dx, normed, None, norm, rstd, x_dtype, need_norm, x_shape)
+            else:
+                dx = dx.reshape(x_shape)
+        return *first_order(dx if need_x else None, dresidual if need_residual else None, dnorm, dw), None, None, None, None
 
 
 class FP8LMHead(_WeightCopies, torch.nn.Module):

@@ -101,6 +101,28 @@ def test_the_stream_alone(cuda_lib):
         assert torch.equal(y2, y) and torch.equal(total2, total)
 
 
+@pytest.mark.parametrize("shape", [(24, 64), (4, 6, 64)])
+def test_gradients_of_x_and_the_residual_are_apart(cuda_lib, shape):
+    """They are equal, but what accumulates into one is not the other's."""
+    from fp8_mixed_precision_reduce_gb300.gated_mlp import FP8GatedMLP
+    from fp8_mixed_precision_reduce_gb300.lm_head import FP8LMHead
+
+    torch.manual_seed(9)
+    g = torch.randn(shape, device="cuda")
+    t = torch.randint(0, 30, shape[:-1], device="cuda")
+    mlp, head = FP8GatedMLP(64, 96, norm_eps=1e-6), FP8LMHead(64, 30, norm_eps=1e-6)
+    for out in (lambda x, r: (mlp(x, r)[0] * g).sum(), lambda x, r: (mlp(x, r)[1] * g).sum(), lambda x, r: head(x, t, r).sum()):
+        x, r = (torch.randn(shape, device="cuda", requires_grad=True) for _ in range(2))
+        out(x, r).backward()
+        once = x.grad.clone()
+        assert torch.equal(r.grad, once) and x.grad.data_ptr() != r.grad.data_ptr()
+        out(x, r).backward()
+        assert torch.equal(x.grad, 2 * once) and torch.equal(r.grad, 2 * once)
+        x.grad = None
+        out(x, x).backward()  # (x + x is another norm's input: the gradients add up)
+        assert x.grad.shape == x.shape and torch.isfinite(x.grad).all()
+
+
 def test_no_second_derivative(cuda_lib):
     from fp8_mixed_precision_reduce_gb300.embedding import TokenEmbedding
     from fp8_mixed_precision_reduce_gb300.gated_mlp import FP8GatedMLP

@@ -1,9 +1,9 @@
 """fp8_rmsnorm_fwd and fp8_rmsnorm_bwd against the formulas in 64 bits.
 
-Tolerances. u = 2^-24. The sum of squares: a thread adds at most 16 (a block's
-row) or 16 (a warp's) pairs' squares one after another, then 5 + 5 shuffles and one
-join of the pair's halves, all of one sign, so it is good to 27 u; rstd takes half
-of that and four operations of its own: 18 u, 20 allowed. y has two products more.
+Tolerances. u = 2^-24. The sum of squares: a thread adds at most 16 pairs' squares one
+after another, then 5 + 5 shuffles and one join of the pair's halves, all of one sign,
+so it is good to 27 u; rstd takes half of that and four operations of its own: 18 u,
+20 allowed. y has two products more.
 Backward: each of n, g, g n is rounded once or twice; the mean has 27 u of the sum
 of |g n|; the bounds below count them. Outputs add half a step of their type."""
 
@@ -15,7 +15,7 @@ U = 2.0 ** -24
 HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: U}
 BF, F32 = torch.bfloat16, torch.float32
 SIZES = [(1, 16), (9, 16), (5, 272), (300, 1024), (3, 1040), (77, 2736), (2, 4096), (1237, 4096), (4, 8192), (3, 8208),
-         (2, 16384), (0, 64)]
+         (2, 16384), (0, 64), (700, 16384), (500, 6160), (6000, 1024), (11000, 272)]
 
 
 def guarded(shape, dtype):

@@ -59,7 +59,7 @@ LOGP = dict(x=P, dtype=1, M=3, V=100, ld=112, targets=P, logprob=P, stats=P, ent
 
 @pytest.mark.parametrize("kw,word", [
     (dict(dtype=2), "x_dtype"), (dict(M=-1), "M = -1"), (dict(V=0), "V = 0"), (dict(V=113), "V = 113"),
-    (dict(ld=1 << 31), "2^31"), (dict(x=None), "logits is NULL"), (dict(x=P + 1), "misaligned"),
+    (dict(ld=1 << 31), "2^31"), (dict(M=1 << 30, ld=1 << 20), "too large"), (dict(x=None), "logits is NULL"), (dict(x=P + 1), "misaligned"),
     (dict(x=P + 2, dtype=0), "misaligned"), (dict(targets=None), "together"), (dict(logprob=None), "together"),
     (dict(targets=P + 4), "targets"), (dict(stats=None), "stats"), (dict(stats=P + 4), "stats"), (dict(entropy=P + 2), "entropy"),
     (dict(k=33), "top = 33"), (dict(k=-1), "top = -1"), (dict(k=8, V=7), "top = 8"), (dict(k=3, ids=P), "top_logprob"),
@@ -85,7 +85,7 @@ EMBED = dict(ids=P, M=3, table=P, dtype=1, V=10, K=32, sinv=None, scale=1.0, out
 
 
 @pytest.mark.parametrize("kw,word", [
-    (dict(M=-1), "M = -1"), (dict(V=-1), "V = -1"), (dict(V=1 << 31), "2^31"), (dict(K=24), "multiple of 16"),
+    (dict(M=-1), "M = -1"), (dict(V=-1), "V = -1"), (dict(V=1 << 31), "2^31"), (dict(M=1 << 29, K=1 << 16), "too large"), (dict(K=24), "multiple of 16"),
     (dict(ids=None), "ids"), (dict(ids=P + 4), "misaligned"), (dict(dtype=2), "table_dtype"), (dict(out_dtype=2), "out_dtype"),
     (dict(table=None), "table"), (dict(table=P + 8), "aligned"), (dict(out=None), "out is NULL"), (dict(sinv=P + 2), "sinv"),
     (dict(out=P + 16), "overlap")])
