@@ -7,21 +7,24 @@
 // Backward: dtable[v] = scale (sum over the m with id_m = v of dy[m]), for every v: the
 // whole table is written, zeros mostly, which is what bounds it. The tokens are sorted
 // first, by (id, position), so that each row's sum has one order and no atomics:
-//   1. sort: a stable radix sort of at most 9 bits a pass. A warp owns a run of
-//      consecutive positions and a histogram of its own. Up to 16384 tokens are sorted
-//      by one block in its shared memory, id and position in one word; more by a
-//      cluster of 8 CTAs, whose counts are joined through distributed shared memory.
+//   1. sort: a stable radix sort. A warp owns a run of consecutive positions and a
+//      histogram of its own. Up to 4096 tokens are sorted by one block in its shared
+//      memory, id and position in one word; up to 32768 by a cluster of 8 CTAs, whose
+//      counts and words go through distributed shared memory (16384 tokens and 50000 x
+//      768: 42.6 us in all, 47.7 with one block; 1000 and 32000 x 768: 16.7 with one
+//      block, 20.6 with a cluster, which starts later); more, or with ids too large for
+//      that, by a cluster through global memory.
 //   2. zero: every block looks through the ids for those among its rows and zeroes the
-//      others. It runs beside the one block's sort, which hardly touches global memory
-//      (the cluster's, whose every pass does, took 4 times as long beside it).
+//      others. It runs beside a sort in shared memory (one through global memory takes 4
+//      times as long beside it, and does not).
 //   3. sum: the sorted tokens in chunks of equal length, whatever their ids, so that
 //      an id that half of the batch holds is no one's long tail: a thread adds eight
 //      columns over a chunk in fp32 and writes a row where its id's run lies within the
 //      chunk, else a partial sum.
 //   4. join: the partial sums of each run over several chunks, in their order.
 // Ids outside 0 .. V - 1 sort last and have no row.
-// 16384 tokens, 128000 x 4096 in bf16: 198 us, of which the zeros 152 (6.5 TB/s) and the
-// sum 29. 77 tokens, 1000 x 272: 11.5 us, the latency of four launches.
+// 16384 tokens, 128000 x 4096 in bf16: 197 us, of which the zeros 152 (6.5 TB/s) and the
+// sum 29. 77 tokens, 1000 x 272: 8.0 us, the latency of three launches.
 #include <atomic>
 
 #include "fp8mp_async.cuh"
@@ -38,8 +41,7 @@ constexpr int kDigitBits = 9, kBins = 1 << kDigitBits;
 constexpr int kBatch = 8;           // keys that a lane has in flight
 constexpr int kMinChunk = 4;        // tokens of a chunk, at least
 constexpr int64_t kSumItems = 1024 * 152;  // chunks times pieces of a row, about, where the chunks are longer
-constexpr uint32_t kZeroRows = 8;     // rows that a block zeroes in a row
-constexpr uint32_t kWindow = 32 * 4096;  // rows whose marks it holds at a time
+constexpr int64_t kWindow = 32 * 4096;  // rows whose marks a block of the zeroing holds at a time
 static_assert(kBins == kSortThreads, "a thread for each bin");
 
 // ----------------------------------------------------------------- forward
@@ -166,48 +168,46 @@ struct ZeroArgs {
     int row;       // 16-byte units of a row of it
 };
 
-// Block b of B zeroes its rows, kZeroRows of every B * kZeroRows, but for those whose
-// ids occur: it marks them in shared memory, kWindow of its rows at a time. EARLY: it
-// runs beside the kernel before it, whose arrays it does not touch and which lets it
-// start when whatever came before is complete; it waits for it at its end.
+// Block `part` of `parts`, of THREADS threads, zeroes the rows of its share of the table
+// but for those whose ids occur: it marks them in shared memory, kWindow rows at a time.
+template <int THREADS>
+__device__ __forceinline__ void zero_rows(const ZeroArgs &a, uint32_t *marks, int64_t part, int64_t parts) {
+    const int across = a.row < THREADS ? a.row : THREADS, down = THREADS / across;
+    const int r0 = threadIdx.x / across, p0 = threadIdx.x - r0 * across;
+    const int64_t end = a.V * (part + 1) / parts;
+    for (int64_t v0 = a.V * part / parts; v0 < end; v0 += kWindow) {
+        const uint32_t rows = static_cast<uint32_t>(end - v0 < kWindow ? end - v0 : kWindow);
+        __syncthreads();
+        for (uint32_t i = threadIdx.x; i < (rows + 31) / 32; i += THREADS) marks[i] = 0u;
+        __syncthreads();
+        for (int64_t i = threadIdx.x; i < a.M; i += THREADS * kZeroBatch) {
+            uint64_t at[kZeroBatch];
+#pragma unroll
+            for (int j = 0; j < kZeroBatch; ++j)
+                at[j] = i + j * THREADS < a.M ? static_cast<uint64_t>(__ldg(a.ids + i + j * THREADS) - v0) : ~0ull;
+#pragma unroll
+            for (int j = 0; j < kZeroBatch; ++j)
+                if (at[j] < rows) atomicOr(&marks[at[j] >> 5], 1u << (at[j] & 31));
+        }
+        __syncthreads();
+        for (uint32_t r = r0; r < rows && r0 < down; r += down) {
+            if (marks[r >> 5] >> (r & 31) & 1u) continue;
+            uint4 *row = a.table + (v0 + r) * a.row;
+            for (int p = p0; p < a.row; p += across) row[p] = make_uint4(0, 0, 0, 0);
+        }
+    }
+}
+
+// EARLY: it runs beside the kernel before it, whose arrays it does not touch and which
+// lets it start when whatever came before is complete; it waits for it at its end.
 template <bool EARLY>
 __global__ void __launch_bounds__(kZeroThreads, 2) embed_zero_kernel(const ZeroArgs a) {
-    __shared__ uint32_t marks[kWindow / 32 + 1];
+    __shared__ uint32_t marks[kWindow / 32];
     if constexpr (!EARLY) {
         pdl_wait();
         pdl_launch_dependents();
     }
-    const int across = a.row < kZeroThreads ? a.row : kZeroThreads, down = kZeroThreads / across;
-    const int r0 = threadIdx.x / across, p0 = threadIdx.x - r0 * across;
-    // its groups of rows: part, part + parts, ..
-    const uint32_t part = blockIdx.x, parts = gridDim.x;
-    const uint32_t groups = static_cast<uint32_t>((a.V + kZeroRows - 1) / kZeroRows);
-    const uint32_t mine = groups > part ? (groups - part + parts - 1) / parts * kZeroRows : 0u;
-    for (uint32_t first = 0; first < mine; first += kWindow) {
-        const uint32_t rows = mine - first < kWindow ? mine - first : kWindow;
-        __syncthreads();
-        for (uint32_t i = threadIdx.x; i < rows / 32 + 1; i += kZeroThreads) marks[i] = 0u;
-        __syncthreads();
-        for (int64_t i = threadIdx.x; i < a.M; i += kZeroThreads * kZeroBatch) {
-            int64_t id[kZeroBatch];
-#pragma unroll
-            for (int j = 0; j < kZeroBatch; ++j) id[j] = i + j * kZeroThreads < a.M ? __ldg(a.ids + i + j * kZeroThreads) : -1;
-#pragma unroll
-            for (int j = 0; j < kZeroBatch; ++j) {
-                if (id[j] < 0 || id[j] >= a.V) continue;
-                const uint32_t group = static_cast<uint32_t>(id[j]) / kZeroRows, turn = group / parts;
-                const uint32_t at = turn * kZeroRows + static_cast<uint32_t>(id[j]) % kZeroRows - first;
-                if (group - turn * parts == part && at < rows) atomicOr(&marks[at >> 5], 1u << (at & 31));
-            }
-        }
-        __syncthreads();
-        for (uint32_t r = r0; r < rows && r0 < down; r += down) {
-            const uint32_t n = first + r;
-            const int64_t v = static_cast<int64_t>(n / kZeroRows * parts + part) * kZeroRows + n % kZeroRows;
-            if (v >= a.V || marks[r >> 5] >> (r & 31) & 1u) continue;
-            for (int p = p0; p < a.row; p += across) a.table[v * a.row + p] = make_uint4(0, 0, 0, 0);
-        }
-    }
+    zero_rows<kZeroThreads>(a, marks, blockIdx.x, gridDim.x);
     if constexpr (EARLY) {
         pdl_wait();
         pdl_launch_dependents();
@@ -220,14 +220,15 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
     return v;
 }
 
-// The lanes whose digit is this one's. (A vote for each bit: __match_any_sync, slow where
-// many lanes differ, made the sort of 32768 tokens 60 us.)
-__device__ __forceinline__ uint32_t lanes_with(uint32_t digit, int bits, bool in) {
+// The lanes whose digit is this one's: a vote for each bit. (__match_any_sync is slow where
+// many lanes differ.)
+template <int BITS>
+__device__ __forceinline__ uint32_t lanes_with(uint32_t digit, bool in) {
     uint32_t peers = __ballot_sync(0xffffffffu, in);
-    for (int b = 0; b < bits; ++b) {
-        const bool one = digit >> b & 1u;
-        const uint32_t ones = __ballot_sync(0xffffffffu, one);
-        peers &= one ? ones : ~ones;
+#pragma unroll
+    for (int b = 0; b < BITS; ++b) {
+        const uint32_t ones = __ballot_sync(0xffffffffu, (digit & (1u << b)) != 0u);
+        peers &= ones ^ ((digit >> b & 1u) - 1u);
     }
     return peers;
 }
@@ -310,7 +311,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const SortA
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
                 const bool in = i + j * 32 + lane < last;
-                const uint32_t digit = in ? k[j] >> shift & (kBins - 1) : 0u, peers = lanes_with(digit, kDigitBits, in);
+                const uint32_t digit = in ? k[j] >> shift & (kBins - 1) : 0u, peers = lanes_with<kDigitBits>(digit, in);
                 uint32_t to = 0;
                 if (in) to = hist[warp][digit] + __popc(peers & ((1u << lane) - 1u));
                 __syncwarp();
@@ -326,17 +327,25 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const SortA
     }
 }
 
-// The sort of up to kOneMost tokens by one block: words of (key, position), the key
-// above `low` bits of position, in registers while they change places in shared memory.
-constexpr int kOneThreads = 1024, kOneWarps = kOneThreads / 32, kOneEach = 16;
+// The sort of up to kOneMost tokens by one block, while the other blocks zero the rows
+// without a token: words of (key, position), the key above `low` bits of position, in registers while they change places in shared memory.
+// Digits of up to 10 bits: one pass for up to 1023 ids, two for up to 2^20.
+constexpr int kOneThreads = 1024, kOneWarps = kOneThreads / 32, kOneEach = 4;
+constexpr int kOneBits = 10, kOneBins = 1 << kOneBits;
 constexpr int kOneMost = kOneThreads * kOneEach;
-constexpr int kOneSmem = (kOneMost + kOneWarps * kBins) * 4;
+constexpr int kOneSmem = (kOneMost + kOneWarps * kOneBins) * 4;
+static_assert(kOneBins == kOneThreads, "a thread for each bin");
+static_assert(kWindow / 8 <= kOneSmem, "the zeroing's marks");
 
-__global__ void __launch_bounds__(kOneThreads, 1) embed_sort_one_kernel(const SortArgs a, int low, int digit_bits) {
+__global__ void __launch_bounds__(kOneThreads, 1) embed_sort_one_kernel(const SortArgs a, const ZeroArgs z, int low, int digit_bits) {
     extern __shared__ uint32_t sorted[];  // a word for each token, then a histogram for each warp
     __shared__ uint32_t scan[kOneWarps];
     pdl_wait();
     pdl_launch_dependents();
+    if (blockIdx.x > 0) {
+        zero_rows<kOneThreads>(z, sorted, blockIdx.x - 1, gridDim.x - 1);
+        return;
+    }
     uint32_t *hist = sorted + kOneMost;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int M = static_cast<int>(a.M), rounds = (M + kOneThreads - 1) / kOneThreads;
@@ -350,7 +359,7 @@ __global__ void __launch_bounds__(kOneThreads, 1) embed_sort_one_kernel(const So
         const int64_t id = __ldg(a.ids + i);
         w[j] = static_cast<uint32_t>(id >= 0 && id < a.V ? id : a.V) << low | static_cast<uint32_t>(i);
     }
-    uint32_t *mine = hist + warp * kBins;
+    uint32_t *mine = hist + warp * kOneBins;
     for (int pass = 0; pass < a.passes; ++pass) {
         const int shift = low + pass * digit_bits;
         for (uint32_t i = lane; i < bins; i += 32) mine[i] = 0u;
@@ -359,16 +368,13 @@ __global__ void __launch_bounds__(kOneThreads, 1) embed_sort_one_kernel(const So
         for (int j = 0; j < kOneEach; ++j)
             if (j < rounds && first + j * 32 < M) atomicAdd(&mine[w[j] >> shift & mask], 1u);
         __syncthreads();
-        // a pair of threads for each bin: where each warp's words of it go
-        const uint32_t bin = tid >> 1, half = tid & 1;
-        uint32_t *column = hist + half * (kOneWarps / 2) * kBins + bin;
-        uint32_t count[kOneWarps / 2], sum = 0;
+        // a thread for each bin: where each warp's words of it go
+        uint32_t count[kOneWarps], all = 0;
 #pragma unroll
-        for (int k = 0; k < kOneWarps / 2; ++k) count[k] = bin < bins ? column[k * kBins] : 0u;
+        for (int k = 0; k < kOneWarps; ++k) count[k] = static_cast<uint32_t>(tid) < bins ? hist[k * kOneBins + tid] : 0u;
 #pragma unroll
-        for (int k = 0; k < kOneWarps / 2; ++k) sum += count[k];
-        const uint32_t other = __shfl_xor_sync(0xffffffffu, sum, 1), all = sum + other;
-        uint32_t upto = half == 0 ? all : 0u;
+        for (int k = 0; k < kOneWarps; ++k) all += count[k];
+        uint32_t upto = all;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
@@ -376,13 +382,11 @@ __global__ void __launch_bounds__(kOneThreads, 1) embed_sort_one_kernel(const So
         }
         if (lane == 31) scan[warp] = upto;
         __syncthreads();
-        uint32_t before = lane < warp ? scan[lane] : 0u;
-        before = __reduce_add_sync(0xffffffffu, before);
-        uint32_t base = before + upto - all + (half == 1 ? other : 0u);
-        if (bin < bins) {
+        uint32_t base = upto - all + __reduce_add_sync(0xffffffffu, lane < warp ? scan[lane] : 0u);
+        if (static_cast<uint32_t>(tid) < bins) {
 #pragma unroll
-            for (int k = 0; k < kOneWarps / 2; ++k) {
-                column[k * kBins] = base;
+            for (int k = 0; k < kOneWarps; ++k) {
+                hist[k * kOneBins + tid] = base;
                 base += count[k];
             }
         }
@@ -391,7 +395,7 @@ __global__ void __launch_bounds__(kOneThreads, 1) embed_sort_one_kernel(const So
         for (int j = 0; j < kOneEach; ++j) {
             if (j >= rounds) break;
             const bool in = first + j * 32 < M;
-            const uint32_t digit = in ? w[j] >> shift & mask : 0u, peers = lanes_with(digit, digit_bits, in);
+            const uint32_t digit = in ? w[j] >> shift & mask : 0u, peers = lanes_with<kOneBits>(digit, in);
             uint32_t to = 0;
             if (in) to = mine[digit] + __popc(peers & ((1u << lane) - 1u));
             __syncwarp();
@@ -411,6 +415,104 @@ __global__ void __launch_bounds__(kOneThreads, 1) embed_sort_one_kernel(const So
         const uint32_t v = sorted[i];
         a.key[0][i] = v >> low;
         a.pos[0][i] = v & ((1u << low) - 1u);
+    }
+}
+
+// The same by the cluster, for more tokens: a CTA holds consecutive words, and they
+// change places through distributed shared memory.
+constexpr int kWideEach = 8;
+constexpr int kWideMost = kSortCtas * kSortThreads * kWideEach;
+constexpr int kWideSmem = (kSortThreads * kWideEach + (kSortWarps + 1) * kBins) * 4;
+
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+__global__ void __launch_bounds__(kSortThreads, 1) embed_sort_wide_kernel(const SortArgs a, int low, int digit_bits) {
+    extern __shared__ uint32_t sorted[];  // the CTA's words, a histogram for each warp, the CTA's counts
+    __shared__ uint32_t scan[kSortWarps];
+    pdl_wait();
+    pdl_launch_dependents();
+    uint32_t *hist = sorted + kSortThreads * kWideEach, *total = hist + kSortWarps * kBins;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t rank = cluster_ctarank();
+    const int M = static_cast<int>(a.M), rounds = (M + kSortCtas * kSortThreads - 1) / (kSortCtas * kSortThreads);
+    const int each = kSortThreads * rounds;                                 // words of a CTA
+    const int mine0 = warp * rounds * 32 + lane, first = static_cast<int>(rank) * each + mine0;  // a warp's: consecutive
+    const uint32_t bins = 1u << digit_bits, mask = bins - 1u;
+    uint32_t w[kWideEach];
+#pragma unroll
+    for (int j = 0; j < kWideEach; ++j) {
+        const int i = first + j * 32;
+        if (j >= rounds || i >= M) continue;
+        const int64_t id = __ldg(a.ids + i);
+        w[j] = static_cast<uint32_t>(id >= 0 && id < a.V ? id : a.V) << low | static_cast<uint32_t>(i);
+    }
+    uint32_t *mine = hist + warp * kBins;
+    for (int pass = 0; pass < a.passes; ++pass) {
+        const int shift = low + pass * digit_bits;
+        for (uint32_t i = lane; i < kBins; i += 32) mine[i] = 0u;
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < kWideEach; ++j)
+            if (j < rounds && first + j * 32 < M) atomicAdd(&mine[w[j] >> shift & mask], 1u);
+        __syncthreads();
+        // a thread for each bin
+        uint32_t count[kSortWarps], sum = 0;
+#pragma unroll
+        for (int k = 0; k < kSortWarps; ++k) count[k] = hist[k * kBins + tid];
+#pragma unroll
+        for (int k = 0; k < kSortWarps; ++k) sum += count[k];
+        total[tid] = sum;
+        cluster_sync_all();  // (every CTA has its words in registers, too)
+        uint32_t before = 0, all = 0;
+#pragma unroll
+        for (uint32_t r = 0; r < kSortCtas; ++r) {
+            const uint32_t c = ld_cluster_u32(mapa_shared(smem_u32(&total[tid]), r));
+            if (r < rank) before += c;
+            all += c;
+        }
+        uint32_t upto = all;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        if (lane == 31) scan[warp] = upto;
+        __syncthreads();
+        uint32_t base = before + upto - all + __reduce_add_sync(0xffffffffu, lane < warp ? scan[lane] : 0u);
+#pragma unroll
+        for (int k = 0; k < kSortWarps; ++k) {
+            hist[k * kBins + tid] = base;
+            base += count[k];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kWideEach; ++j) {
+            if (j >= rounds) break;
+            const bool in = first + j * 32 < M;
+            const uint32_t digit = in ? w[j] >> shift & mask : 0u, peers = lanes_with<kDigitBits>(digit, in);
+            uint32_t to = 0;
+            if (in) to = mine[digit] + __popc(peers & ((1u << lane) - 1u));
+            __syncwarp();
+            if (in && lane == __ffs(peers) - 1) mine[digit] += __popc(peers);
+            __syncwarp();
+            if (in) {
+                const uint32_t cta = to / static_cast<uint32_t>(each);
+                st_cluster_u32(mapa_shared(smem_u32(&sorted[to - cta * each]), cta), w[j]);
+            }
+        }
+        cluster_sync_all();
+        if (pass + 1 < a.passes) {
+#pragma unroll
+            for (int j = 0; j < kWideEach; ++j)
+                if (j < rounds && first + j * 32 < M) w[j] = sorted[mine0 + j * 32];
+        }
+    }
+    for (int i = tid; i < each && static_cast<int>(rank) * each + i < M; i += kSortThreads) {
+        const uint32_t v = sorted[i];
+        a.key[0][rank * each + i] = v >> low;
+        a.pos[0][rank * each + i] = v & ((1u << low) - 1u);
     }
 }
 
@@ -535,16 +637,43 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(const SumArgs a) {
     write_row(a, v, piece, sum);
 }
 
-cudaError_t sort_one(const SortArgs &so, int low, int digit_bits, cudaStream_t s, int device) {
-    static std::atomic<bool> ready[64];  // per device: the kernel may have its shared memory
+// A kernel may have its shared memory, from the first call on a device on.
+template <typename K>
+cudaError_t allow_smem(K *kernel, int bytes, std::atomic<bool> (&ready)[64], int device) {
     std::atomic<bool> &mine = ready[device & 63];
-    if (!mine.load(std::memory_order_acquire)) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(embed_sort_one_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kOneSmem);
-        if (e != cudaSuccess) return e;
-        mine.store(true, std::memory_order_release);
+    if (mine.load(std::memory_order_acquire)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) mine.store(true, std::memory_order_release);
+    return e;
+}
+
+// The tokens sorted and the rows without one zeroed.
+cudaError_t sort_and_zero(SortArgs so, const ZeroArgs &z, int key_bits, int low, cudaStream_t s, const DeviceInfo &dev) {
+    const bool one = so.M <= kOneMost && key_bits + low <= 32, wide = !one && so.M <= kWideMost && key_bits + low <= 32;
+    const int most_bits = one ? kOneBits : kDigitBits;
+    so.passes = (key_bits + most_bits - 1) / most_bits;
+    const int digit_bits = (key_bits + so.passes - 1) / so.passes;
+    // blocks of at least 32 KB, one or two to an SM, but where the sort runs
+    const int64_t want = z.V * z.row / 2048 + 1, sms = dev.num_sms;
+    const int64_t most = one ? sms - 1 : wide ? 2 * sms - kSortCtas : 2 * sms;
+    const unsigned blocks = static_cast<unsigned>(want < most ? want : most);
+    if (one) {
+        static std::atomic<bool> ready[64];
+        const cudaError_t e = allow_smem(embed_sort_one_kernel, kOneSmem, ready, dev.device);
+        return e != cudaSuccess ? e : launch_kernel(embed_sort_one_kernel, dim3(1 + blocks), dim3(kOneThreads), kOneSmem, s, so, z, low, digit_bits);
     }
-    return launch_kernel(embed_sort_one_kernel, dim3(1), dim3(kOneThreads), kOneSmem, s, so, low, digit_bits);
+    cudaError_t e;
+    if (wide) {
+        static std::atomic<bool> ready[64];
+        e = allow_smem(embed_sort_wide_kernel, kWideSmem, ready, dev.device);
+        if (e == cudaSuccess)
+            e = launch_kernel_cluster(embed_sort_wide_kernel, dim3(kSortCtas), dim3(kSortThreads), kWideSmem, s, kSortCtas, so,
+                                      low, digit_bits);
+    } else {
+        e = launch_kernel_cluster(embed_sort_kernel, dim3(kSortCtas), dim3(kSortThreads), 0, s, kSortCtas, so);
+    }
+    if (e != cudaSuccess) return e;
+    return launch_kernel(wide ? embed_zero_kernel<true> : embed_zero_kernel<false>, dim3(blocks), dim3(kZeroThreads), 0, s, z);
 }
 
 // The workspace: keys and positions, each twice; the partial sums.
@@ -555,8 +684,8 @@ int64_t round16(int64_t n) { return (n + 15) / 16 * 16; }
 Layout layout_of(int64_t M, int64_t K) {
     Layout l;
     l.chunk = (M * (K / kPiece) + kSumItems - 1) / kSumItems;
-    int64_t shortest = kMinChunk;  // about sqrt(M / 32): the sum walks a chunk, the join the chunks of a run
-    while (shortest * shortest * 32 < M) shortest *= 2;
+    int64_t shortest = kMinChunk;  // about sqrt(M / 64): the sum walks a chunk, the join the chunks of a run
+    while (shortest * shortest * 64 < M) shortest *= 2;
     if (l.chunk < shortest) l.chunk = shortest;
     l.chunks = (M + l.chunk - 1) / l.chunk;
     l.partial = 4 * round16(4 * M);
@@ -600,25 +729,15 @@ int launch_embedding_bwd(const int64_t *ids, int64_t M, const void *dy, int dy_d
     int key_bits = 1, low = 1;  // keys are 0 .. V, positions 0 .. M - 1
     while (V >> key_bits != 0) ++key_bits;
     while ((M - 1) >> low > 0) ++low;
-    so.passes = (key_bits + kDigitBits - 1) / kDigitBits;
-    const bool one = M <= kOneMost && key_bits + low <= 32;
-    ZeroArgs z = {ids, static_cast<uint4 *>(dtable), M, V, static_cast<int>(K * (out_dtype == FP8MP_BF16 ? 2 : 4) / 16)};
-    // two blocks an SM, but for the one that sorts; of at least 32 KB
-    const int64_t want = V * z.row / 2048 + 1, most = 2ll * (dev.num_sms - (one ? 1 : 0));
-    const dim3 zero_grid(static_cast<unsigned>(want < most ? want : most));
-    cudaError_t e = cudaSuccess;
-    if (one) {
-        const int digit_bits = (key_bits + so.passes - 1) / so.passes;
-        e = sort_one(so, low, digit_bits, s, dev.device);
-        if (e == cudaSuccess) e = launch_kernel(embed_zero_kernel<true>, zero_grid, dim3(kZeroThreads), 0, s, z);
-    } else {
-        e = launch_kernel_cluster(embed_sort_kernel, dim3(kSortCtas), dim3(kSortThreads), 0, s, kSortCtas, so);
-        if (e == cudaSuccess) e = launch_kernel(embed_zero_kernel<false>, zero_grid, dim3(kZeroThreads), 0, s, z);
-    }
+    const ZeroArgs z = {ids, static_cast<uint4 *>(dtable), M, V, static_cast<int>(K * (out_dtype == FP8MP_BF16 ? 2 : 4) / 16)};
+    cudaError_t e = sort_and_zero(so, z, key_bits, low, s, dev);
     SumArgs a = {};
     a.dy = dy;
-    a.key = so.key[one ? 0 : so.passes & 1];
-    a.pos = so.pos[one ? 0 : so.passes & 1];
+    // (a sort through global memory leaves them in the arrays of the other turn after an odd number of passes)
+    const bool words = M <= kWideMost && key_bits + low <= 32;
+    const int turn = words ? 0 : (key_bits + kDigitBits - 1) / kDigitBits & 1;
+    a.key = so.key[turn];
+    a.pos = so.pos[turn];
     a.out = dtable;
     a.partial = reinterpret_cast<float *>(ws + l.partial);
     a.M = M;

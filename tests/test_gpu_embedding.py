@@ -82,7 +82,8 @@ def hold(got, ids, dy, scale):
 
 @pytest.mark.parametrize("M,V,K", [(1, 1, 16), (17, 3, 16), (77, 1000, 272), (1000, 77, 1040), (3000, 511, 48), (3000, 512, 64),
                                    (2500, 513, 64), (5000, 30000, 4096), (40000, 262144, 16), (70000, 300, 32), (0, 40, 16), (5000, 2 ** 21 + 5, 16),
-                                   (16384, 262143, 16), (16385, 511, 16)])
+                                   (16384, 262143, 16), (16385, 511, 16), (4096, 1023, 16), (4097, 1024, 16),
+                                   (32768, 131071, 16), (32768, 131072, 16), (32769, 100, 16)])
 @pytest.mark.parametrize("dy,out", [(BF, BF), (BF, F32), (F32, BF), (F32, F32)])
 def test_backward(cuda_lib, M, V, K, dy, out):
     ids = some_ids(M, V, 2, spread=6.0)
