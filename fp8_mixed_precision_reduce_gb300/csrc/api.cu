@@ -9,7 +9,7 @@
 #include <cstring>
 #include <mutex>
 
-#include "fp8mp_internal.cuh"
+#include "fp8mp_lm.cuh"
 
 namespace fp8mp {
 

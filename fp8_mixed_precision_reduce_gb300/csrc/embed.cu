@@ -28,6 +28,7 @@
 #include <atomic>
 
 #include "fp8mp_async.cuh"
+#include "fp8mp_lm.cuh"
 #include "fp8mp_pieces.cuh"
 
 namespace fp8mp {

@@ -31,6 +31,7 @@
 #include <type_traits>
 
 #include "fp8mp_async.cuh"
+#include "fp8mp_lm.cuh"
 #include "fp8mp_pieces.cuh"
 
 namespace fp8mp {

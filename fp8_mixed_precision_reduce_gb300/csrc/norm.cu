@@ -20,6 +20,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "fp8mp_lm.cuh"
 #include "fp8mp_pieces.cuh"
 
 namespace fp8mp {
