@@ -73,9 +73,9 @@ __device__ __forceinline__ void e4m3_pairs(uint32_t codes, uint64_t &lo, uint64_
     hi = wide(h1);
 }
 
-// TABLE: 0 E4M3, 1 bf16, 2 fp32. A thread writes 16 bytes of each of kRows rows (8 bf16
-// or 4 fp32 columns, so that a warp's store covers whole lines), whose ids and then
-// whose columns are in flight together.
+// TABLE: 0 E4M3, 1 bf16, 2 fp32. A thread writes 16 bytes (8 bf16 or 4 fp32 columns, so that
+// a warp's store covers whole lines) of each of kRows rows at a time, whose ids and then
+// whose columns are in flight together; blockDim.x threads or fewer take a row.
 constexpr int kRows = 4;
 
 template <int BYTES>
@@ -104,52 +104,51 @@ __global__ void __launch_bounds__(kThreads) embed_fwd_kernel(const EmbedArgs a) 
     pdl_wait();
     pdl_launch_dependents();
     const float factor = TABLE == 0 ? __ldg(a.sinv) * a.scale : a.scale;
-    const int64_t items = a.M * a.units, first = static_cast<int64_t>(blockIdx.x) * (kThreads * kRows) + threadIdx.x;
-    int64_t at[kRows];
+    const int across = a.units < kThreads ? a.units : kThreads, down = kThreads / across;
+    const int r0 = threadIdx.x / across, p0 = threadIdx.x - r0 * across;
+    if (r0 >= down) return;
+    const int64_t m0 = static_cast<int64_t>(blockIdx.x) * (down * kRows) + r0;
+    int64_t id[kRows];  // -1: no row
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-        const int64_t it = first + r * kThreads;
-        at[r] = -1;
-        if (it < items) {
-            const int64_t m = items <= 0xFFFFFFFFll ? static_cast<uint32_t>(it) / static_cast<uint32_t>(a.units) : it / a.units;
-            const int64_t id = __ldg(a.ids + m);
-            if (id >= 0 && id < a.V) at[r] = id * a.units + (it - m * a.units);
-        }
+        id[r] = m0 + r * down < a.M ? __ldg(a.ids + m0 + r * down) : -1;
+        if (id[r] >= a.V) id[r] = -1;
     }
-    uint32_t q[kRows][BYTES / 4];
+    for (int p = p0; p < a.units; p += across) {
+        uint32_t q[kRows][BYTES / 4];
 #pragma unroll
-    for (int r = 0; r < kRows; ++r)
-        if (at[r] >= 0) load_words<BYTES>(q[r], a.table + at[r] * BYTES);
+        for (int r = 0; r < kRows; ++r)
+            if (id[r] >= 0) load_words<BYTES>(q[r], a.table + (id[r] * a.units + p) * BYTES);
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-        const int64_t it = first + r * kThreads;
-        if (it >= items) break;
-        uint32_t o[4] = {0u, 0u, 0u, 0u};
-        if (at[r] >= 0) {
-            uint64_t v[COLS / 2];
+        for (int r = 0; r < kRows; ++r) {
+            if (m0 + r * down >= a.M) break;
+            uint32_t o[4] = {0u, 0u, 0u, 0u};
+            if (id[r] >= 0) {
+                uint64_t v[COLS / 2];
 #pragma unroll
-            for (int j = 0; j < COLS / 2; ++j) {
-                if constexpr (TABLE == 0) {
-                    if ((j & 1) == 0) e4m3_pairs(q[r][j / 2], v[j], v[j + 1]);
-                } else if constexpr (TABLE == 1) {
-                    v[j] = f2_from_bits(q[r][j] << 16, q[r][j] & 0xFFFF0000u);
-                } else {
-                    v[j] = f2_from_bits(q[r][2 * j], q[r][2 * j + 1]);
+                for (int j = 0; j < COLS / 2; ++j) {
+                    if constexpr (TABLE == 0) {
+                        if ((j & 1) == 0) e4m3_pairs(q[r][j / 2], v[j], v[j + 1]);
+                    } else if constexpr (TABLE == 1) {
+                        v[j] = f2_from_bits(q[r][j] << 16, q[r][j] & 0xFFFF0000u);
+                    } else {
+                        v[j] = f2_from_bits(q[r][2 * j], q[r][2 * j + 1]);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < COLS / 2; ++j) {
+                    float lo, hi;
+                    f2_split(f2_mul(v[j], f2_same(factor)), lo, hi);
+                    if constexpr (OBF) {
+                        o[j] = bf16_pair(lo, hi);
+                    } else {
+                        o[2 * j] = __float_as_uint(lo);
+                        o[2 * j + 1] = __float_as_uint(hi);
+                    }
                 }
             }
-#pragma unroll
-            for (int j = 0; j < COLS / 2; ++j) {
-                float lo, hi;
-                f2_split(f2_mul(v[j], f2_same(factor)), lo, hi);
-                if constexpr (OBF) {
-                    o[j] = bf16_pair(lo, hi);
-                } else {
-                    o[2 * j] = __float_as_uint(lo);
-                    o[2 * j + 1] = __float_as_uint(hi);
-                }
-            }
+            reinterpret_cast<uint4 *>(a.out)[(m0 + r * down) * a.units + p] = make_uint4(o[0], o[1], o[2], o[3]);
         }
-        reinterpret_cast<uint4 *>(a.out)[it] = make_uint4(o[0], o[1], o[2], o[3]);
     }
 }
 
@@ -702,7 +701,8 @@ int launch_embedding_fwd(const int64_t *ids, int64_t M, const void *table, int t
                          const float *sinv, float scale, void *out, int out_dtype, cudaStream_t s, const DeviceInfo &dev) {
     const bool bf16 = out_dtype == FP8MP_BF16;
     const EmbedArgs a = {ids, static_cast<const uint8_t *>(table), sinv, out, M, V, static_cast<int>(K / (bf16 ? 8 : 4)), scale};
-    const dim3 grid(static_cast<unsigned>((M * a.units + kThreads * kRows - 1) / (kThreads * kRows))), block(kThreads);
+    const int64_t rows = (a.units < kThreads ? kThreads / a.units : 1) * kRows;  // of a block
+    const dim3 grid(static_cast<unsigned>((M + rows - 1) / rows)), block(kThreads);
     cudaError_t e;
     if (table_kind == 0)
         e = launch_kernel(bf16 ? embed_fwd_kernel<0, true> : embed_fwd_kernel<0, false>, grid, block, 0, s, a);

@@ -293,7 +293,7 @@ __device__ __forceinline__ void best_of_slice(const Slice<BF16> &sl, float large
         __syncthreads();
         uint32_t have = sh.n_found;
         const int64_t body = sl.row.head;
-        // step -1: the head; the pieces 512 at a time; then the tail
+        // step -1: the head; a piece for each thread at a time; then the tail
         const int64_t steps = (sl.p1 - sl.p0 + kThreads - 1) / kThreads;
         for (int64_t step = -1; step <= steps && have < want; ++step) {
             int64_t first = 0;
