@@ -16,7 +16,7 @@
 // into shared memory (cp.async) and reads nothing else there, so no barrier is
 // needed but the one inside a row's sum, and loads are in flight while a row is
 // reduced and written. 16384 x 4096, bf16: forward with residual and E4M3 out 71 us
-// (6.6 TB/s), backward 86 (6.3), 86 and 126 with loads into registers instead.
+// (6.6 TB/s), backward 82.6 (6.5), 86 and 126 with loads into registers instead.
 #include <atomic>
 #include <mutex>
 
@@ -86,27 +86,28 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <bool BF16, int N>
 struct Slot {
     static constexpr int UNITS = BF16 ? 1 : 2, BYTES = N * UNITS * 16;
-    const uint8_t *next;  // the lane's first unit of the next row to fetch
+    int64_t next;         // address of the lane's first unit of the next row to fetch
     int64_t step;         // to the one after it
     int units, gap;       // of the row from there on; from piece v to piece v + 1
     uint32_t to, from;    // where the lane's first unit goes, and where its first piece lies, in the first stage
 
-    // `ring`: of this array, in the first stage; row: the first one, rows: between a block's rows
+    // `ring`: of this array, in the first stage; row: the first one, rows: between a block's rows.
+    // x: the array, or NULL where each fetch names its own.
     __device__ __forceinline__ Slot(uint32_t ring, const void *x, int64_t row, int64_t rows, int pieces, int tid, int tpr) {
         const int lane = threadIdx.x & 31, first = (tid - lane) * UNITS + lane;
-        next = static_cast<const uint8_t *>(x) + (row * pieces * UNITS + first) * 16;
+        next = reinterpret_cast<int64_t>(x) + (row * pieces * UNITS + first) * 16;
         step = rows * pieces * (UNITS * 16);
         units = pieces * UNITS - first;
         gap = tpr * UNITS;
         to = ring + (threadIdx.x - lane) * (UNITS * 16) + lane * 16;
         from = ring + threadIdx.x * (UNITS * 16);
     }
-    __device__ __forceinline__ void fetch(uint32_t stage, int v) const {
+    __device__ __forceinline__ void fetch(uint32_t stage, int v, const void *x = nullptr) const {
 #pragma unroll
         for (int j = 0; j < UNITS; ++j)
             if (v * gap + j * 32 < units)
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + stage + v * blockDim.x * (UNITS * 16) + j * 512),
-                             "l"(next + (v * gap + j * 32) * 16)
+                             "l"(static_cast<const uint8_t *>(x) + next + (v * gap + j * 32) * 16)
                              : "memory");
     }
     __device__ __forceinline__ Piece<BF16> read(uint32_t stage, int v) const {
@@ -138,8 +139,8 @@ constexpr int kMaxWarps = kWideBlock / 32;
 // alternates between two halves from row to row: a thread writes one again only when
 // all have left the barrier of the row between, and with it their reads. The warps'
 // sums are joined by shuffles, or added up by every thread, which costs latency or
-// instructions: forward without residual, 16384 x 4096, 40.4 us and 44.3; backward 89.5
-// and 85.7.
+// instructions: forward without residual, 16384 x 4096, 40.4 us and 44.3; backward 89.2
+// and 82.6.
 template <bool SHUFFLE>
 __device__ __forceinline__ float row_sum(float v, float (&red)[kMaxWarps], int g, int tpr, int tid) {
     v = warp_sum(v);
@@ -325,27 +326,28 @@ __global__ void __launch_bounds__(threads_of(N), (per_sm(threads_of(N), N, Bwd<X
     const int tpr = a.tpr, g = threadIdx.x / tpr, tid = threadIdx.x - g * tpr, groups = blockDim.x / tpr;
     const int pieces = a.K / kPiece;
     const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
-    const uint32_t stage_bytes = blockDim.x * BYTES, t_ring = smem_u32(ring) + blockDim.x * SX::BYTES;
+    const uint32_t stage_bytes = blockDim.x * BYTES;
     int64_t m = static_cast<int64_t>(blockIdx.x) * groups + g, to_fetch = m;
-    SX sdy(smem_u32(ring), a.dy, m, step, pieces, tid, tpr);
-    SR st(t_ring, a.t, m, step, pieces, tid, tpr);
-    // (dT lies behind t, and is as far from it in memory for every row)
-    const uint32_t dt_ring = blockDim.x * SR::BYTES;
-    const int64_t dt_away = static_cast<const uint8_t *>(a.dtotal) - static_cast<const uint8_t *>(a.t);
+    // Arrays of one type share a Slot, their pieces lying one behind another: it is its
+    // registers that are short (16384 x 4096 bf16 82.6 us, 85.8 with a Slot each).
+    constexpr bool SAME = XBF == RBF;
+    const uint32_t t_ring = SAME ? blockDim.x * SX::BYTES : 0u, dt_ring = t_ring + blockDim.x * SR::BYTES;
+    SX sdy(smem_u32(ring), nullptr, m, step, pieces, tid, tpr);
+    SR other(smem_u32(ring) + blockDim.x * SX::BYTES, nullptr, m, step, pieces, tid, tpr);
+    const auto st = [&]() -> const SR & {
+        if constexpr (SAME) return sdy;
+        else return other;
+    };
     const auto fetch = [&](uint32_t stage, int v) {
         if (to_fetch >= a.M) return;
-        sdy.fetch(stage, v);
-        st.fetch(stage, v);
-        if (a.dtotal != nullptr) {
-            SR sdt = st;
-            sdt.next += dt_away;
-            sdt.fetch(stage + dt_ring, v);
-        }
+        sdy.fetch(stage, v, a.dy);
+        st().fetch(stage + t_ring, v, a.t);
+        if (a.dtotal != nullptr) st().fetch(stage + dt_ring, v, a.dtotal);
     };
     const auto fetched = [&] {
         to_fetch += step;
         sdy.next += sdy.step;
-        st.next += st.step;
+        if constexpr (!SAME) other.next += other.step;
         cp_async_commit();
     };
     const auto fetch_row = [&](uint32_t stage) {
@@ -379,7 +381,7 @@ __global__ void __launch_bounds__(threads_of(N), (per_sm(threads_of(N), N, Bwd<X
         for (int v = 0; v < N; ++v) {
             if (tid + v * tpr < pieces) {
                 const Piece<XBF> dy = sdy.read(now, v);
-                const Piece<RBF> t = st.read(now, v);
+                const Piece<RBF> t = st().read(now + t_ring, v);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const uint64_t n = f2_mul(t.pair(j), r2), d = dy.pair(j);
@@ -397,12 +399,12 @@ __global__ void __launch_bounds__(threads_of(N), (per_sm(threads_of(N), N, Bwd<X
             const int i = tid + v * tpr;
             if (i < pieces) {
                 const Piece<XBF> dy = sdy.read(now, v);
-                const Piece<RBF> t = st.read(now, v);
+                const Piece<RBF> t = st().read(now + t_ring, v);
                 uint64_t d[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) d[j] = f2_fma(f2_mul(t.pair(j), r2), neg_c, f2_mul(dy.pair(j), w[v][j]));
                 if (a.dtotal != nullptr) {
-                    const Piece<RBF> dt = st.read(now + dt_ring, v);
+                    const Piece<RBF> dt = st().read(now + dt_ring, v);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) d[j] = f2_fma(d[j], r2, dt.pair(j));
                 } else {

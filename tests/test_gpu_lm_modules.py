@@ -222,6 +222,74 @@ def test_head_is_its_kernels(cuda_lib):
     assert torch.allclose(top, torch.log_softmax(logits[:, :V].float(), 1).gather(1, want), atol=1e-5)
 
 
+@pytest.mark.parametrize("tokens", [(), (1,), (128,), (3, 67), (300,)])
+def test_top_of_any_number_of_tokens(cuda_lib, tokens):
+    """As log p of the tokens that it gives, and as each token alone."""
+    from fp8_mixed_precision_reduce_gb300.lm_head import FP8LMHead
+
+    torch.manual_seed(10)
+    head = FP8LMHead(64, 1003, norm_eps=1e-6)
+    x, r = (torch.randn((*tokens, 64), device="cuda").to(BF) for _ in range(2))
+    logprob, ids = head.top(x, 4, r)
+    assert logprob.shape == ids.shape == (*tokens, 4) and ids.dtype == torch.int64
+    for i in range(4):
+        assert torch.allclose(head(x, ids[..., i].contiguous(), r).detach(), logprob[..., i], rtol=1e-5, atol=1e-5)
+    if tokens:
+        flat = lambda t: t.reshape(-1, 64)  # noqa: E731
+        for m in (0, x.numel() // 64 - 1):
+            _, alone = head.top(flat(x)[m], 1, flat(r)[m])
+            assert alone[0] == ids.reshape(-1, 4)[m, 0]
+
+
+def test_inputs_of_other_strides_and_broadcast_ones(cuda_lib):
+    """The same values as dense tensors give the same bits; gradients gather where the
+    strides say."""
+    from fp8_mixed_precision_reduce_gb300.embedding import TokenEmbedding
+    from fp8_mixed_precision_reduce_gb300.gated_mlp import FP8GatedMLP
+    from fp8_mixed_precision_reduce_gb300.lm_head import FP8LMHead
+
+    torch.manual_seed(11)
+    mlp, head, e = FP8GatedMLP(64, 96, norm_eps=1e-6), FP8LMHead(64, 30, norm_eps=1e-6), TokenEmbedding(30, 64, out_dtype=F32)
+    base = torch.randn(4 * 9 * 64 + 3, device="cuda", requires_grad=True)
+    ids = torch.randint(0, 30, (9, 8), device="cuda").t()[::2]
+    assert ids.shape == (4, 9) and not ids.is_contiguous()
+    for shape, stride, offset in (((4, 9, 64), (576, 64, 1), 1), ((4, 9, 64), (64, 256, 1), 0), ((4, 9, 64), (0, 64, 1), 0),
+                                  ((4, 9, 64), (9, 1, 36), 3)):
+        x = base.as_strided(shape, stride, offset)
+        dense = x.detach().contiguous().clone().requires_grad_(True)
+        r = torch.randn(shape, device="cuda")
+        y, total = mlp(x, r)
+        y2, total2 = mlp(dense, r)
+        assert torch.equal(y, y2) and torch.equal(total, total2)
+        assert torch.equal(head(r, ids, x), head(r, ids.contiguous(), dense))
+        base.grad = None
+        y.sum().backward()
+        y2.sum().backward()
+        places = torch.arange(base.numel(), device="cuda").as_strided(shape, stride, offset).reshape(-1)
+        want = torch.zeros_like(base).index_put_((places,), dense.grad.reshape(-1), accumulate=True)
+        assert torch.allclose(base.grad, want, rtol=1e-5, atol=1e-6)
+    out = e(ids)
+    assert torch.equal(out, e(ids.contiguous()))
+    out.backward(torch.ones(1, device="cuda").expand(4, 9, 64))
+    count = torch.bincount(ids.reshape(-1), minlength=30).float()
+    assert torch.equal(e.weight.grad, count[:, None].expand(30, 64))
+
+
+@pytest.mark.parametrize("shape", [(0, 64), (2, 0, 64)])
+def test_no_tokens(cuda_lib, shape):
+    from fp8_mixed_precision_reduce_gb300.gated_mlp import FP8GatedMLP
+    from fp8_mixed_precision_reduce_gb300.lm_head import FP8LMHead
+
+    mlp, head = FP8GatedMLP(64, 96, norm_eps=1e-6), FP8LMHead(64, 30, norm_eps=1e-6)
+    x, r = (torch.zeros(shape, device="cuda", requires_grad=True) for _ in range(2))
+    y, total = mlp(x, r)
+    logprob, entropy = head(y, torch.zeros(shape[:-1], dtype=torch.int64, device="cuda"), total, entropy=True)
+    (logprob.sum() + entropy.sum()).backward()
+    assert y.shape == total.shape == shape and logprob.shape == shape[:-1] and x.grad.shape == shape
+    assert all((p.grad == 0).all() for m in (mlp, head) for p in m.parameters())
+    assert head.top(x, 3, r)[1].shape == (*shape[:-1], 3) and cuda_lib.fp8mp_check() == 0
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("dtype,out", [(F32, BF), (BF, BF), (F32, F32)])
 @pytest.mark.parametrize("shape", [(), (1,), (4, 33), (0,), (2, 0)])
