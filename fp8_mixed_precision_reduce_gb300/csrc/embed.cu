@@ -637,16 +637,6 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(const SumArgs a) {
     write_row(a, v, piece, sum);
 }
 
-// A kernel may have its shared memory, from the first call on a device on.
-template <typename K>
-cudaError_t allow_smem(K *kernel, int bytes, std::atomic<bool> (&ready)[64], int device) {
-    std::atomic<bool> &mine = ready[device & 63];
-    if (mine.load(std::memory_order_acquire)) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess) mine.store(true, std::memory_order_release);
-    return e;
-}
-
 // The tokens sorted and the rows without one zeroed.
 cudaError_t sort_and_zero(SortArgs so, const ZeroArgs &z, int key_bits, int low, cudaStream_t s, const DeviceInfo &dev) {
     const bool one = so.M <= kOneMost && key_bits + low <= 32, wide = !one && so.M <= kWideMost && key_bits + low <= 32;

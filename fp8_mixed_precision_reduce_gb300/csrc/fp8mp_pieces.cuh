@@ -3,12 +3,34 @@
 // stores, values in pairs of fp32. Not part of the ABI.
 #pragma once
 
+#include <atomic>
+
 #include "fp8mp_f32x2.cuh"
 #include "fp8mp_internal.cuh"
 
 namespace fp8mp {
 
 constexpr int kPiece = 8;
+
+// 16 bytes from global to shared memory, past L1 and the registers.
+__device__ __forceinline__ void cp_async_16(uint32_t to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A kernel may have its shared memory, from the first call on a device on.
+template <typename K>
+cudaError_t allow_smem(K *kernel, int bytes, std::atomic<bool> (&ready)[64], int device) {
+    std::atomic<bool> &mine = ready[device & 63];
+    if (mine.load(std::memory_order_acquire)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) mine.store(true, std::memory_order_release);
+    return e;
+}
 
 template <bool BF16>
 struct Piece {

@@ -11,16 +11,16 @@
 // Forward: one pass with the running maximum and sums of a softmax, in registers,
 // joined over the threads and, when there are few rows, over the up to 8 CTAs of a
 // cluster that share a row, through the first one's shared memory; many short rows are
-// taken by a warp each. Bound by HBM (the logits, once): 8192 x 128000 in bf16 288 us,
-// 7.3 TB/s; with the entropy 310 us, where instruction issue begins to. Seven rows of
-// that length, with their 20 best tokens, 6.9 us: latency of the loads, of the
+// taken by a warp each. Bound by HBM (the logits, once): 8192 x 128000 in bf16 286 us,
+// 7.3 TB/s; with the entropy 295 us, where instruction issue begins to. Seven rows of
+// that length, with their 20 best tokens, 6.4 us: latency of the loads, of the
 // selection's barriers and of the cluster's.
 //
 // The k most probable tokens come out of the same pass. Each thread keeps the
-// largest logit of its share of the row; with tau the k-th largest of those, every
-// one of the k largest logits is at least tau, and only the shares whose largest is
-// can hold one: about k of 256, which are read again (from L2) by all threads. What
-// they hold from tau on is ranked by counting. Where more than fits is at tau or
+// largest logit of its share of the row; with tau the k-th largest of those or a bit
+// less, every one of the k largest logits is at least tau, and only the shares whose
+// largest is can hold one: k to 1.5 k of 256, which are read again (from L2) by all
+// threads. What they hold from tau on is ranked by counting. Where more than fits is at tau or
 // above (equal logits, nearly all masked), a bisection on the value finds the k-th
 // largest, and its equals are taken from the lowest index on.
 //
@@ -180,7 +180,7 @@ struct TopShared {
     uint64_t best[kMaxTop];
     uint64_t merged[kMaxSplits * kMaxTop];  // the first CTA's: all the CTAs' best
     uint16_t shares[kThreads];
-    uint32_t warp_count[kWarps];
+    uint32_t warp_count[kWarps], warp_min[kWarps];
     uint32_t n_found, n_shares;
 };
 
@@ -193,6 +193,10 @@ struct Slice {
     int64_t p0, p1;   // its pieces
     int head, tail;   // elements of the row's head and tail that are its own
 
+    // Element `i` of the head (0 to 7) and of the tail (8 to 15), or -1: none.
+    __device__ __forceinline__ int64_t edge(int i) const {
+        return i < 8 ? (i < head ? i : -1) : i - 8 < tail ? row.tail_at() + i - 8 : -1;
+    }
     __device__ __forceinline__ int64_t elements() const { return head + tail + (p1 - p0) * Row<BF16>::EP; }
     // The elements of a thread's share: f(index, logit).
     template <typename F>
@@ -221,30 +225,41 @@ __device__ __forceinline__ uint32_t block_count(uint32_t c, TopShared &sh) {
 }
 
 // sh.best = the `want` (at most the slice's elements) best candidates of the slice,
-// best first. `largest`: the largest logit of this thread's share (NaN left out),
-// -Inf for an empty one.
-template <bool BF16>
-__device__ __forceinline__ void best_of_slice(const Slice<BF16> &sl, float largest, uint32_t want, TopShared &sh) {
+// best first. `largest`: the largest logit of this thread's pieces (NaN left out).
+// `meanwhile` runs before the shares are read again.
+template <bool BF16, typename F>
+__device__ __forceinline__ void best_of_slice(const Slice<BF16> &sl, float largest, uint32_t want, TopShared &sh, F meanwhile) {
     const int tid = threadIdx.x, lane = tid & 31;
-    const bool empty = sl.p0 + tid >= sl.p1 && tid >= sl.head && !(tid >= 32 && tid - 32 < sl.tail);
-    const uint32_t mine = empty ? 0u : order_of(largest);
+    const uint32_t mine = sl.p0 + tid < sl.p1 ? order_of(largest) : 0u;
     if (tid == 0) sh.n_found = sh.n_shares = 0u;
-    uint32_t tau = 0u;
-    if (want == 1u) {
-        const uint32_t most = __reduce_max_sync(0xffffffffu, mine);
-        if (lane == 0) sh.warp_count[tid >> 5] = most;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) tau = max(tau, sh.warp_count[w]);
-    } else {
-        // the want-th largest of the shares' largest, in its upper 16 bits, bit by bit
-        // (of bf16 that is all of it: the lower ones are all set below zero)
-        for (int bit = 31; bit >= 16; --bit) {
-            const uint32_t trial = tau | 1u << bit;
-            if (static_cast<uint32_t>(__syncthreads_count(mine >= trial)) >= want) tau = trial;
-        }
-        if (BF16 && static_cast<uint32_t>(__syncthreads_count(mine >= (tau | 0xFFFFu))) >= want) tau |= 0xFFFFu;
+    // tau: the want-th largest of the shares' largest or one of the next few, by bisection
+    // between their extremes, five or six barriers mostly
+    const uint32_t most = __reduce_max_sync(0xffffffffu, mine), fewest = __reduce_min_sync(0xffffffffu, mine);
+    if (lane == 0) {
+        sh.warp_count[tid >> 5] = most;
+        sh.warp_min[tid >> 5] = fewest;
     }
+    __syncthreads();
+    uint32_t tau = 0xFFFFFFFFu, above = 0u;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        above = max(above, sh.warp_count[w]);
+        tau = min(tau, sh.warp_min[w]);
+    }
+    if (want == 1u) tau = above;
+    else ++above;
+    const auto bisect = [&](uint32_t enough, int steps) {
+        for (uint32_t have = kThreads; steps > 0 && above - tau > 1u && have > enough; --steps) {
+            const uint32_t mid = tau + (above - tau) / 2u, c = static_cast<uint32_t>(__syncthreads_count(mine >= mid));
+            if (c >= want) {
+                tau = mid;
+                have = c;
+            } else {
+                above = mid;
+            }
+        }
+    };
+    bisect(want + want / 2u, 16);
     if (mine >= tau) sh.shares[atomicAdd(&sh.n_shares, 1u)] = static_cast<uint16_t>(tid);
     __syncthreads();
     const auto keep = [&](int64_t index, float x) {
@@ -253,27 +268,36 @@ __device__ __forceinline__ void best_of_slice(const Slice<BF16> &sl, float large
         const uint32_t at = atomicAdd(&sh.n_found, 1u);
         if (at < kCandidates) sh.found[at] = candidate(key, index);
     };
-    // their pieces, dealt to all threads, and the elements off the 16-byte boundaries
+    // their pieces, dealt to all threads, and the elements off the 16-byte boundaries. One
+    // piece in flight is enough: what a share's strided pieces cost is their sectors' traffic
+    // beside the other CTAs' rows (two or four in flight: as fast or slower).
     const uint32_t each = static_cast<uint32_t>((sl.p1 - sl.p0 + kThreads - 1) / kThreads), all_pieces = each * sh.n_shares;
+    meanwhile();
+    const int64_t off_at = tid < 16 ? sl.edge(tid) : -1;
+    const float off = off_at >= 0 ? sl.row.at(off_at) : 0.0f;
+    const float least = value_of(tau);
     for (uint32_t i = tid; i < all_pieces; i += kThreads) {
         const uint32_t share = i / each;
         const int64_t p = sl.p0 + sh.shares[share] + static_cast<int64_t>(i - share * each) * kThreads;
         if (p >= sl.p1) continue;
         const uint4 q = __ldg(sl.row.body() + p);
+        if (piece_max<BF16>(q) < least) continue;
+        uint32_t may = 0;
 #pragma unroll
-        for (int j = 0; j < Row<BF16>::EP; ++j) keep(sl.row.head + p * Row<BF16>::EP + j, element<BF16>(q, j));
+        for (int j = 0; j < Row<BF16>::EP; ++j) may |= static_cast<uint32_t>(!(element<BF16>(q, j) < least)) << j;
+        for (; may != 0u; may &= may - 1u) {
+            const int j = __ffs(may) - 1, w = BF16 ? j >> 1 : j;
+            const uint32_t v = w < 2 ? (w == 0 ? q.x : q.y) : w == 2 ? q.z : q.w;
+            keep(sl.row.head + p * Row<BF16>::EP + j, __uint_as_float(!BF16 ? v : j & 1 ? v & 0xFFFF0000u : v << 16));
+        }
     }
-    if (tid < sl.head) keep(tid, sl.row.at(tid));
-    if (tid >= 32 && tid - 32 < sl.tail) keep(sl.row.tail_at() + tid - 32, sl.row.at(sl.row.tail_at() + tid - 32));
+    if (off_at >= 0) keep(off_at, off);
     __syncthreads();
     uint32_t n = sh.n_found;
     if (n > kCandidates || n < want) {
         // the want-th largest logit itself, by bisection, starting from what is
         // most likely: that tau, to its last bit, is it, over and over
-        for (int bit = 15; !BF16 && bit >= 0; --bit) {
-            const uint32_t trial = tau | 1u << bit;
-            if (static_cast<uint32_t>(__syncthreads_count(mine >= trial)) >= want) tau = trial;
-        }
+        bisect(0u, 32);
         uint32_t lo = tau, hi = 0xFFFFFFFFu, c = 0;
         sl.share([&](int64_t, float x) { c += order_of(x) >= lo; });
         if (block_count(c, sh) < want) lo = 0u;  // (shares of NaN alone: their largest is not there)
@@ -381,11 +405,17 @@ __device__ __forceinline__ void add_one(Running<ENT> &run, float x) {
     run.raise(x);
     run.add(f2_from_bits(__float_as_uint(x), 0xFF800000u), f2_same(-run.m), 0);
 }
+// (m, S, T) of the warp's parts.
 __device__ __forceinline__ void join_warp(float &m, float &S, float &T) {
+    const float to = value_of(__reduce_max_sync(0xffffffffu, order_of(m))), d = (m - to) * kLog2e, f = exp2_approx(d);
+    T = f > 0.0f ? f * (T + d * S) : 0.0f;
+    S *= f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        join_parts(m, S, T, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, S, o),
-                   __shfl_xor_sync(0xffffffffu, T, o));
+    for (int o = 16; o > 0; o >>= 1) {
+        S += __shfl_xor_sync(0xffffffffu, S, o);
+        T += __shfl_xor_sync(0xffffffffu, T, o);
+    }
+    m = to;
 }
 
 // log p of a logit, from the row's (m, log S). S is 0 where every logit is -Inf.
@@ -393,14 +423,11 @@ __device__ __forceinline__ float log_p(float x, float m, float log_s) {
     const float d = x - m, inf = __uint_as_float(0x7F800000u);
     return d == -inf && log_s == log_s ? -inf : d - log_s;
 }
-template <bool BF16, bool ENT>
-__device__ __forceinline__ void write_row(const LogpArgs &a, int64_t m_row, const Row<BF16> &row, float m, float S, float T,
-                                          float log_s) {
+template <bool ENT>
+__device__ __forceinline__ void write_row(const LogpArgs &a, int64_t m_row, int64_t target, float x_target, float m, float S,
+                                          float T, float log_s) {
     a.stats[m_row] = make_float2(S == 0.0f ? -__uint_as_float(0x7F800000u) : m, log_s);
-    if (a.logprob != nullptr) {
-        const int64_t t = a.target[m_row];
-        a.logprob[m_row] = t >= 0 && t < a.V ? log_p(row.at(t), m, log_s) : 0.0f;
-    }
+    if (a.logprob != nullptr) a.logprob[m_row] = target >= 0 && target < a.V ? log_p(x_target, m, log_s) : 0.0f;
     if (ENT) a.entropy[m_row] = S == 0.0f ? 0.0f : log_s - kLn2 * T / S;
 }
 
@@ -415,12 +442,14 @@ __global__ void __launch_bounds__(kThreads, kPerSm) logp_rows_kernel(const LogpA
     const Row<BF16> row(a.x + m_row * a.ld * Row<BF16>::ES, a.V);
     Running<ENT> run;
     for (int64_t p = lane; p < row.pieces; p += 32 * kUnroll) add_pieces<BF16>(run, row.body(), p, row.pieces, 32);
+    const int64_t target = lane == 0 && a.logprob != nullptr ? a.target[m_row] : -1;
     if (lane < row.head) add_one(run, row.at(lane));
     if (lane < row.tail) add_one(run, row.at(row.tail_at() + lane));
+    const float x_target = target >= 0 && target < a.V ? row.at(target) : 0.0f;
     float m = run.m, S, T;
     run.total(S, T);
     join_warp(m, S, T);
-    if (lane == 0) write_row<BF16, ENT>(a, m_row, row, m, S, T, logf(S));
+    if (lane == 0) write_row<ENT>(a, m_row, target, x_target, m, S, T, logf(S));
 }
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
@@ -455,16 +484,17 @@ __global__ void __launch_bounds__(kThreads, kPerSm) logp_fwd_kernel(const LogpAr
         const float top = add_pieces<BF16>(run, row.body(), p, sl.p1, kThreads);
         if (TOP) largest = fmaxf(largest, top);
     }
-    {  // the elements off the 16-byte boundaries
-        const bool h = tid < sl.head, t = tid >= 32 && tid - 32 < sl.tail;
-        if (h || t) {
-            const float x = row.at(h ? tid : row.tail_at() + tid - 32);
-            if (TOP) largest = fmaxf(largest, x);
-            add_one(run, x);
-        }
-    }
     float m = run.m, S, T;
     run.total(S, T);
+    // Warp 0 joins the warps' parts (lanes 0 to 7) and the elements off the 16-byte
+    // boundaries (8 to 23); these and the target's logit are on their way meanwhile.
+    int64_t target = -1;
+    float off = __uint_as_float(0xFF800000u), x_target = 0.0f;
+    if (tid < 32) {
+        const int64_t at = lane >= kWarps && lane < kWarps + 16 ? sl.edge(lane - kWarps) : -1;
+        if (at >= 0) off = row.at(at);
+        if (lane == 0 && rank == 0 && a.logprob != nullptr) target = a.target[m_row];
+    }
     join_warp(m, S, T);
     if (lane == 0) {
         warp_part[tid >> 5][0] = m;
@@ -473,16 +503,27 @@ __global__ void __launch_bounds__(kThreads, kPerSm) logp_fwd_kernel(const LogpAr
     }
     __syncthreads();
     if (tid < 32) {
-        m = lane < kWarps ? warp_part[lane][0] : -FLT_MAX;
-        S = lane < kWarps ? warp_part[lane][1] : 0.0f;
-        T = lane < kWarps ? warp_part[lane][2] : 0.0f;
+        if (!TOP && target >= 0 && target < a.V) x_target = row.at(target);
+        Running<ENT> one;
+        add_one(one, off);
+        m = one.m;
+        one.total(S, T);
+        if (lane < kWarps) {
+            m = warp_part[lane][0];
+            S = warp_part[lane][1];
+            T = warp_part[lane][2];
+        }
         join_warp(m, S, T);
     }
     const uint32_t k = TOP ? static_cast<uint32_t>(a.k) : 0u;
     if constexpr (TOP) {
         const int64_t n = sl.elements();
         const uint32_t want = n < static_cast<int64_t>(k) ? static_cast<uint32_t>(n) : k;
-        if (want > 0) best_of_slice<BF16>(sl, largest, want, sh);
+        const auto aim = [&] {
+            if (target >= 0 && target < a.V) x_target = row.at(target);
+        };
+        if (want > 0) best_of_slice<BF16>(sl, largest, want, sh, aim);
+        else aim();
         if (tid >= static_cast<int>(want) && tid < static_cast<int>(k)) sh.best[tid] = 0ull;
         __syncthreads();
     }
@@ -518,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) logp_fwd_kernel(const LogpAr
     }
     if (tid >= 32) return;
     const float log_s = logf(S);
-    if (lane == 0) write_row<BF16, ENT>(a, m_row, row, m, S, T, log_s);
+    if (lane == 0) write_row<ENT>(a, m_row, target, x_target, m, S, T, log_s);
     if constexpr (TOP) {
         for (uint32_t i = lane; i < k; i += 32) {
             const uint64_t c = sh.best[i];
@@ -662,22 +703,18 @@ __global__ void __launch_bounds__(kGradThreads, WARP ? 4 : kGradPerSm) logp_bwd_
     if (a.amax != nullptr) block_amax_atomic(am, a.amax);
 }
 
-// CTAs that share a row of `bytes`: those with which the last is done first, when an
-// SM takes in 45 B/ns, a CTA alone 16, and a CTA costs 3 us of its own, 4 with peers.
+// CTAs that share a row of `bytes`. Clusters start later the more of them an SM gets, so
+// M s^2 is bounded, and each CTA has three quarters of a round of loads at least, twice
+// that where an SM has several. bf16, V 128000, by 1, 2, 4 and 8 CTAs a row: 8 rows 6.7, 4.4,
+// 3.1, 2.5 us; 64 rows with their 20 best 16.3, 11.5, 9.5, 11.0; 256 with 5 18.4, 17.7, 21.8, 30;
+// V 32000, 128 rows 3.8, 3.7, 4.7, 8.2; 333 rows of 50001 in fp32 14.4, 17.2, 17.8, 20.6.
 int splits_for(int64_t M, int64_t bytes, int num_sms) {
-    int best = 1;
-    double least = 0.0;
-    for (int s = 1; s <= kMaxSplits; s *= 2) {
-        const int64_t ctas = M * s, slots = static_cast<int64_t>(num_sms) * kPerSm;
-        const double waves = static_cast<double>((ctas + slots - 1) / slots), part = static_cast<double>(bytes) / s;
-        const double by_sm = static_cast<double>((ctas + num_sms - 1) / num_sms) * part / 45.0, by_cta = waves * part / 16.0;
-        const double ns = (by_sm > by_cta ? by_sm : by_cta) + waves * (s == 1 ? 3000.0 : 4000.0);
-        if (s == 1 || ns < least) {
-            least = ns;
-            best = s;
-        }
-    }
-    return best;
+    const int64_t part = kThreads * kUnroll * 16 / 4 * 3;
+    int s = 1;
+    while (s < kMaxSplits && M * (2 * s) * (2 * s) <= 8ll * num_sms &&
+           bytes >= 2 * s * (M * 2 * s > num_sms ? 2 * part : part))
+        s *= 2;
+    return s;
 }
 
 // CTAs that share a row of `pieces` in the backward pass: those with which the last

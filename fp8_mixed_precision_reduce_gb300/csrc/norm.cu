@@ -18,7 +18,6 @@
 // reduced and written. 16384 x 4096, bf16: forward with residual and E4M3 out 71 us
 // (6.6 TB/s), backward 82.6 (6.5), 86 and 126 with loads into registers instead.
 #include <atomic>
-#include <mutex>
 
 #include "fp8mp_lm.cuh"
 #include "fp8mp_pieces.cuh"
@@ -73,12 +72,6 @@ constexpr int stages(int bytes, int n) {
     return threads * bytes * 3 * blocks <= kSmem ? 3 : threads * bytes * 2 <= kSmem ? 2 : 1;
 }
 
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-
 // A warp's copies of one array's pieces: N of a row for each lane, 32 pieces one
 // after another. A lane copies 16-byte units 32 lanes apart, so it reads what other
 // lanes copied: the warp meets between the copies' arrival and their use, and
@@ -106,9 +99,8 @@ struct Slot {
 #pragma unroll
         for (int j = 0; j < UNITS; ++j)
             if (v * gap + j * 32 < units)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + stage + v * blockDim.x * (UNITS * 16) + j * 512),
-                             "l"(static_cast<const uint8_t *>(x) + next + (v * gap + j * 32) * 16)
-                             : "memory");
+                cp_async_16(to + stage + v * blockDim.x * (UNITS * 16) + j * 512,
+                            static_cast<const uint8_t *>(x) + next + (v * gap + j * 32) * 16);
     }
     __device__ __forceinline__ Piece<BF16> read(uint32_t stage, int v) const {
         Piece<BF16> r;
@@ -507,19 +499,12 @@ Shape shape_of(int64_t K) {
     return {n, tpr, tpr < kBlock ? kBlock / tpr : 1};
 }
 
-std::mutex g_prepare_mutex;
-
 // Launches a kernel of `blocks` blocks, allowed once their shared memory.
 template <typename A>
 cudaError_t launch_rows(void (*kernel)(A), std::atomic<bool> (&ready)[64], int64_t blocks, const Shape &shape, int smem,
                         cudaStream_t s, int device, const A &a) {
-    std::atomic<bool> &mine = ready[device & 63];
-    if (!mine.load(std::memory_order_acquire)) {
-        std::lock_guard<std::mutex> lock(g_prepare_mutex);
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-        if (e != cudaSuccess) return e;
-        mine.store(true, std::memory_order_release);
-    }
+    const cudaError_t e = allow_smem(kernel, kSmem, ready, device);
+    if (e != cudaSuccess) return e;
     return launch_kernel(kernel, dim3(static_cast<unsigned>(blocks)), dim3(shape.threads()), smem, s, a);
 }
 
