@@ -119,6 +119,42 @@ def test_ties_go_to_the_lowest_index(cuda_lib, dtype, k):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("M", [12, 48, 200, 400])
+@pytest.mark.parametrize("offset", [0, 1])
+def test_long_rows_over_any_number_of_ctas(cuda_lib, dtype, M, offset):
+    """The selection of rows that 8, 4, 2 and 1 CTAs share: ties across them, all that is
+    allowed in one's part, infinities and NaN there; off the 16-byte boundaries too."""
+    V, k = 100003, 32
+    i = torch.arange(V, device="cuda", dtype=F32)
+    g = torch.Generator(device="cuda").manual_seed(21)
+    rows = torch.stack([torch.zeros(V, device="cuda"), i % 7, torch.where(i == V - 1, 1.0, -INF), torch.where(i == 0, 1.0, -INF),
+                        torch.where((i > 60000) & (i < 60040), i, -INF), torch.where(i % 12501 == 0, 3.0, -3e38),
+                        -(i - 50000).abs() / 4096, torch.randn(V, generator=g, device="cuda"),
+                        torch.where(i > V - 20, 2.0, 1.0), torch.where(i < 20, 2.0, 1.0),
+                        torch.where(i % 2 == 0, -INF, -3e38), torch.randn(V, generator=g, device="cuda")])
+    x = rows.repeat((M + 11) // 12, 1)[:M].to(dtype)
+    room = torch.empty(M * V + offset, dtype=dtype, device="cuda")
+    y = room[offset:].view(M, V).copy_(x)
+    t = torch.randint(0, V, (M,), generator=g, device="cuda")
+    logprob, stats, H, top, ids = forward(cuda_lib, y, t, k)
+    assert torch.equal(ids, ranked(x, k))
+    logp, d, log_s, of_s, of_h = reference(x[:12])
+    assert torch.equal(stats[:, 0], x.float().amax(1))
+    want = -(torch.exp(logp) * torch.where(logp > -INF, logp, 0.0)).sum(1)
+    assert ((stats[:12, 1].double() - log_s).abs() <= of_s * U).all() and ((H[:12].double() - want).abs() <= of_h * U).all()
+    at, far = logp.gather(1, t[:12, None])[:, 0], d.gather(1, t[:12, None])[:, 0]
+    fine = torch.isfinite(at)
+    assert torch.equal(torch.isinf(logprob[:12]), ~fine)
+    assert ((logprob[:12].double() - at).abs() <= (of_s + 2 * far.abs() + 2) * U)[fine].all()
+    y[:, 99999] = float("nan")
+    *_, top, ids = forward(cuda_lib, y, t, 2)
+    x[:, 99999] = -INF
+    best = ranked(x, 2)
+    several = torch.isfinite(x.float()).sum(1) >= 2
+    assert torch.isnan(top).all() and torch.equal(ids[several], best[several])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("M", [11, 500])
 def test_rows_of_infinities_nan_and_lowest_values(cuda_lib, dtype, M):
     V = 9001
