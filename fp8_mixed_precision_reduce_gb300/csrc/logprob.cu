@@ -717,16 +717,17 @@ int splits_for(int64_t M, int64_t bytes, int num_sms) {
     return s;
 }
 
-// CTAs that share a row of `pieces` in the backward pass: those with which the last
-// is done first, when a CTA costs a round and a half of its own.
+// CTAs that share a row of `pieces` in the backward pass. A CTA costs an SM 0.2 us, and
+// the last one's rounds, 1.3 us each, are not hidden. To codes, by 1, 2, 4 CTAs a row: 512 x
+// 32000 13.9, 11.7, 12.1 us; 2048 x 32000 35.5, 35.7, 39.9; 256 x 128000 28.3, 25.3, 20.9.
 int grad_splits_for(int64_t M, int64_t pieces, int num_sms) {
-    const int64_t rounds = (pieces + kGradRound - 1) / kGradRound, slots = static_cast<int64_t>(num_sms) * kGradPerSm;
+    const int64_t rounds = (pieces + kGradRound - 1) / kGradRound;
     int best = 1;
-    int64_t fewest = 0;
+    int64_t least = 0;
     for (int s = 1; s <= 64 && s <= rounds; ++s) {
-        const int64_t cost = (M * s + slots - 1) / slots * (2 * ((rounds + s - 1) / s) + 3);
-        if (s == 1 || cost < fewest) {
-            fewest = cost;
+        const int64_t cost = M * s + 6ll * num_sms * ((rounds + s - 1) / s);
+        if (s == 1 || cost < least) {
+            least = cost;
             best = s;
         }
     }
@@ -753,18 +754,20 @@ cudaError_t fwd(const LogpArgs &a, int64_t M, cudaStream_t s, int num_sms) {
 }
 
 template <bool BF16, bool CODES, bool ENT>
-cudaError_t bwd(const LogpGradArgs &a, cudaStream_t s) {
+cudaError_t bwd(const LogpGradArgs &a, cudaStream_t s, int num_sms) {
     const dim3 block(kGradThreads);
-    // up to two rounds of a warp (16384 rows of 512, codes: 9.8 us, 39.1 by blocks)
-    if (a.ld <= 2 * 32 * kGradUnroll * Row<BF16>::EP) {
+    // A warp takes up to two rounds (16384 rows of 512, codes: 9.8 us, 39.1 by blocks), up to
+    // four when there is a row for every warp (8192 rows of 4000: 21.9, 29.1; 1024: 7.0, 5.3).
+    const int64_t round = 32 * kGradUnroll * Row<BF16>::EP;
+    if (a.ld <= 2 * round || (a.ld <= 4 * round && a.M >= 4ll * num_sms * (kGradThreads / 32))) {
         const dim3 grid(static_cast<unsigned>((a.M + kGradThreads / 32 - 1) / (kGradThreads / 32)));
         return launch_kernel(logp_bwd_kernel<BF16, CODES, ENT, true>, grid, block, 0, s, a);
     }
     return launch_kernel(logp_bwd_kernel<BF16, CODES, ENT, false>, dim3(static_cast<unsigned>(a.M * a.splits)), block, 0, s, a);
 }
 template <bool BF16, bool CODES>
-cudaError_t bwd(const LogpGradArgs &a, cudaStream_t s) {
-    return a.db != nullptr ? bwd<BF16, CODES, true>(a, s) : bwd<BF16, CODES, false>(a, s);
+cudaError_t bwd(const LogpGradArgs &a, cudaStream_t s, int num_sms) {
+    return a.db != nullptr ? bwd<BF16, CODES, true>(a, s, num_sms) : bwd<BF16, CODES, false>(a, s, num_sms);
 }
 
 }  // namespace
@@ -791,8 +794,8 @@ int launch_logprobs_bwd(const void *x, int x_dtype, int64_t M, int64_t V, int64_
     a.splits = grad_splits_for(M, ld / (x_dtype == FP8MP_BF16 ? 8 : 4), dev.num_sms);
     const bool b = x_dtype == FP8MP_BF16;
     cudaError_t e;
-    if (scale != nullptr) e = b ? bwd<true, true>(a, s) : bwd<false, true>(a, s);
-    else e = b ? bwd<true, false>(a, s) : bwd<false, false>(a, s);
+    if (scale != nullptr) e = b ? bwd<true, true>(a, s, dev.num_sms) : bwd<false, true>(a, s, dev.num_sms);
+    else e = b ? bwd<true, false>(a, s, dev.num_sms) : bwd<false, false>(a, s, dev.num_sms);
     if (e != cudaSuccess) return fail(FP8MP_ERR_LAUNCH, "logprobs: launch failed: %s", cudaGetErrorString(e));
     return FP8MP_OK;
 }

@@ -202,9 +202,10 @@ def test_rows_of_infinities_nan_and_lowest_values(cuda_lib, dtype, M):
 
 
 BACK = [(1, 1), (3, 7), (5, 50), (9, 1008), (4, 4097), (2, 50001), (333, 5008), (7, 128000), (1300, 2064), (2001, 2047)]
+MANY = [(4900, 2064), (4900, 4096), (4863, 4096), (4900, 1031)]  # a warp for each row, or a block
 
 
-@pytest.mark.parametrize("M,V", BACK)
+@pytest.mark.parametrize("M,V", BACK + MANY)
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("entropy", [False, True])
 @pytest.mark.parametrize("codes", [False, True])
