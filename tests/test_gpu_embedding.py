@@ -83,7 +83,8 @@ def hold(got, ids, dy, scale):
 @pytest.mark.parametrize("M,V,K", [(1, 1, 16), (17, 3, 16), (77, 1000, 272), (1000, 77, 1040), (3000, 511, 48), (3000, 512, 64),
                                    (2500, 513, 64), (5000, 30000, 4096), (40000, 262144, 16), (70000, 300, 32), (0, 40, 16), (5000, 2 ** 21 + 5, 16),
                                    (16384, 262143, 16), (16385, 511, 16), (4096, 1023, 16), (4097, 1024, 16),
-                                   (32768, 131071, 16), (32768, 131072, 16), (32769, 100, 16)])
+                                   (32768, 131071, 16), (32768, 131072, 16), (32769, 100, 16),
+                                   (32, 9, 4112), (127, 40, 48), (128, 30000, 1040), (129, 40, 48), (128, 3, 16384)])
 @pytest.mark.parametrize("dy,out", [(BF, BF), (BF, F32), (F32, BF), (F32, F32)])
 def test_backward(cuda_lib, M, V, K, dy, out):
     ids = some_ids(M, V, 2, spread=6.0)
@@ -94,7 +95,7 @@ def test_backward(cuda_lib, M, V, K, dy, out):
 
 
 @pytest.mark.parametrize("ids", ["one", "none", "rising", "falling", "two", "edges"])
-@pytest.mark.parametrize("M", [15, 16, 17, 2049, 40000])
+@pytest.mark.parametrize("M", [15, 16, 17, 127, 128, 129, 130, 131, 132, 133, 2049, 40000])
 def test_runs(cuda_lib, ids, M):
     """One id throughout, none inside the table, all different, two that alternate,
     runs that end with the chunks."""
@@ -115,6 +116,32 @@ def test_the_order_of_equal_ids_is_theirs(cuda_lib):
     d[1], d[5] = 2.0, 3.0
     got = backward(cuda_lib, ids, d, 5, F32)
     assert (got[3] == (torch.tensor(1e8) + 1 - 1e8).item()).all() and (got[1] == 5).all()
+
+
+@pytest.mark.parametrize("M", [128, 129, 5000])
+def test_the_order_of_equal_ids_among_others(cuda_lib, M):
+    ids = torch.arange(M, device="cuda") + 10
+    ids[[5, 60, M - 1]] = 3
+    d = torch.zeros((M, 16), device="cuda")
+    d[5], d[60], d[M - 1] = 1e8, 1.0, -1e8
+    got = backward(cuda_lib, ids, d, 6000, F32)
+    assert (got[3] == (torch.tensor(1e8) + 1 - 1e8).item()).all()
+
+
+@pytest.mark.parametrize("M", [100, 200])
+def test_gradient_of_a_table_of_many_rows(cuda_lib, M):
+    """More rows than a block marks at a time, and more bytes than 2^32."""
+    V, K = 40000003, 64
+    ids = torch.randint(0, V, (M,), generator=rng(11), device="cuda")
+    ids[0], ids[1], ids[2], ids[3] = V - 1, V - 1, 0, 131072
+    d = torch.randint(1, 9, (M, K), generator=rng(12), device="cuda").to(BF)
+    dt = torch.full((V, K), 9, dtype=BF, device="cuda")
+    ws = torch.empty(cuda_lib.mp_embedding_bwd_workspace_bytes(M, V, K), dtype=torch.uint8, device="cuda")
+    cuda_lib.mp_embedding_bwd(ids, d, dt, ws)
+    rows, back = torch.unique(ids, return_inverse=True)
+    want = torch.zeros((len(rows), K), device="cuda").index_put_((back,), d.float(), accumulate=True)
+    assert torch.equal(dt[rows].float(), want) and cuda_lib.fp8mp_check() == 0
+    assert int(dt.view(torch.int32).ne(0).any(1).sum()) == len(rows)
 
 
 def test_nan_stays_in_its_row(cuda_lib):
