@@ -34,6 +34,10 @@ constexpr int kMaxGroups = kBlock / 32;  // rows that a block takes at a time, a
 // residual: 82.5 us with 3, 73.9 with 4, 72.7 with 8, 76.9 with 36; without
 // residual 43.4, 49.2, 45.2, 56.6; 8192 x 4096 with an fp32 residual 62.8, 62.8, 58.3, 68.3.
 constexpr int kBlocksPerSm = 8;
+// Up to so many rows (or rows at a time) an SM, as many blocks as are resident: a second
+// wave of blocks would begin with a row's whole latency. 2000 x 4096 11.3 us, 14.8 by more
+// blocks; 1000 x 8192 12.8, 19.0; 8741 x 912 11.1, 14.4; 4000 x 4096 20.2, 22.0; 6000 29.2, 28.4.
+constexpr int64_t kFewUnits = 28;
 constexpr int kGradSms = 152;       // the backward pass's blocks are for so many SMs; each leaves a row of sums
 constexpr int kSmem = 216 * 1024;   // what the blocks on an SM may use together
 
@@ -515,8 +519,11 @@ cudaError_t fwd(NormArgs a, const Shape &shape, cudaStream_t s, const DeviceInfo
     using F = Fwd<XBF, RES, N>;
     static std::atomic<bool> ready[64];
     a.tpr = shape.tpr;
-    const int64_t most = static_cast<int64_t>(dev.num_sms) * kBlocksPerSm * kBlock / shape.threads();
-    return launch_rows(norm_fwd_kernel<XBF, RES, N>, ready, least((a.M + shape.groups - 1) / shape.groups, most), shape,
+    // (per_sm is for the largest block: of smaller ones as many more, nearly)
+    constexpr int kResident = per_sm(threads_of(N), N, F::BYTES, F::S) * threads_of(N);
+    const int64_t units = (a.M + shape.groups - 1) / shape.groups;
+    const int64_t threads = units <= kFewUnits * dev.num_sms ? kResident : kBlocksPerSm * kBlock;
+    return launch_rows(norm_fwd_kernel<XBF, RES, N>, ready, least(units, dev.num_sms * threads / shape.threads()), shape,
                        F::BYTES * F::S * shape.threads(), s, dev.device, a);
 }
 template <bool XBF, int RES>
