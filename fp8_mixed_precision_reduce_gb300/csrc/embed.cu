@@ -189,7 +189,7 @@ __device__ __forceinline__ void zero_rows(const ZeroArgs &a, uint32_t *marks, in
             uint64_t at[kZeroBatch];
 #pragma unroll
             for (int j = 0; j < kZeroBatch; ++j)
-                at[j] = i + j * THREADS < a.M ? static_cast<uint64_t>(__ldg(a.ids + i + j * THREADS) - v0) : ~0ull;
+                at[j] = i + j * THREADS < a.M ? static_cast<uint64_t>(__ldg(a.ids + i + j * THREADS)) - static_cast<uint64_t>(v0) : ~0ull;
 #pragma unroll
             for (int j = 0; j < kZeroBatch; ++j)
                 if (at[j] < rows) atomicOr(&marks[at[j] >> 5], 1u << (at[j] & 31));

@@ -519,11 +519,10 @@ cudaError_t fwd(NormArgs a, const Shape &shape, cudaStream_t s, const DeviceInfo
     using F = Fwd<XBF, RES, N>;
     static std::atomic<bool> ready[64];
     a.tpr = shape.tpr;
-    // (per_sm is for the largest block: of smaller ones as many more, nearly)
-    constexpr int kResident = per_sm(threads_of(N), N, F::BYTES, F::S) * threads_of(N);
-    const int64_t units = (a.M + shape.groups - 1) / shape.groups;
-    const int64_t threads = units <= kFewUnits * dev.num_sms ? kResident : kBlocksPerSm * kBlock;
-    return launch_rows(norm_fwd_kernel<XBF, RES, N>, ready, least(units, dev.num_sms * threads / shape.threads()), shape,
+    constexpr int kResident = per_sm(threads_of(N), N, F::BYTES, F::S) * threads_of(N);  // threads
+    const int64_t units = (a.M + shape.groups - 1) / shape.groups, sms = dev.num_sms;
+    const int64_t most = units <= kFewUnits * sms ? sms * (kResident / shape.threads()) : sms * kBlocksPerSm * kBlock / shape.threads();
+    return launch_rows(norm_fwd_kernel<XBF, RES, N>, ready, least(units, most), shape,
                        F::BYTES * F::S * shape.threads(), s, dev.device, a);
 }
 template <bool XBF, int RES>
@@ -539,7 +538,7 @@ cudaError_t fwd(const NormArgs &a, cudaStream_t s, const DeviceInfo &dev) {
 int64_t grad_blocks(int64_t M, int64_t K) {
     const Shape shape = shape_of(K);
     const int64_t units = (M + shape.groups - 1) / shape.groups;
-    const int64_t most = kGradSms * (shape.pieces == 2 ? 3 * kBlock : kWideBlock) / shape.threads();
+    const int64_t most = kGradSms * ((shape.pieces == 2 ? 3 * kBlock : kWideBlock) / shape.threads());
     return least(units, units < 4 * most && shape.pieces == 2 ? 2 * kGradSms : most);
 }
 
