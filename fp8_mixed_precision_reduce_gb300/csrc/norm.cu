@@ -33,7 +33,9 @@ constexpr int kMaxGroups = kBlock / 32;  // rows that a block takes at a time, a
 // resident: shares small enough to even out the tail. 16384 x 4096, bf16 with
 // residual: 82.5 us with 3, 73.9 with 4, 72.7 with 8, 76.9 with 36; without
 // residual 43.4, 49.2, 45.2, 56.6; 8192 x 4096 with an fp32 residual 62.8, 62.8, 58.3, 68.3.
-constexpr int kBlocksPerSm = 8;
+// Wide ones, one or two of which are resident, in whole waves: 6000 x 11472 84.9 us with
+// one, 78.4 with 4, 90.4 with 5.3; 12000 x 5600 84.6, 76.3, 78.2; 8000 x 16384 151.5, 142.9.
+constexpr int kBlocksPerSm = 8, kWaves = 4;
 // Up to so many rows (or rows at a time) an SM, as many blocks as are resident: a second
 // wave of blocks would begin with a row's whole latency. 2000 x 4096 11.3 us, 14.8 by more
 // blocks; 1000 x 8192 12.8, 19.0; 8741 x 912 11.1, 14.4; 4000 x 4096 20.2, 22.0; 6000 29.2, 28.4.
@@ -521,7 +523,8 @@ cudaError_t fwd(NormArgs a, const Shape &shape, cudaStream_t s, const DeviceInfo
     a.tpr = shape.tpr;
     constexpr int kResident = per_sm(threads_of(N), N, F::BYTES, F::S) * threads_of(N);  // threads
     const int64_t units = (a.M + shape.groups - 1) / shape.groups, sms = dev.num_sms;
-    const int64_t most = units <= kFewUnits * sms ? sms * (kResident / shape.threads()) : sms * kBlocksPerSm * kBlock / shape.threads();
+    const int64_t resident = sms * (kResident / shape.threads());
+    const int64_t most = units <= kFewUnits * sms ? resident : N == 2 ? sms * kBlocksPerSm * kBlock / shape.threads() : kWaves * resident;
     return launch_rows(norm_fwd_kernel<XBF, RES, N>, ready, least(units, most), shape,
                        F::BYTES * F::S * shape.threads(), s, dev.device, a);
 }
@@ -531,15 +534,17 @@ cudaError_t fwd(const NormArgs &a, cudaStream_t s, const DeviceInfo &dev) {
     return shape.pieces == 2 ? fwd<XBF, RES, 2>(a, shape, s, dev) : fwd<XBF, RES, 4>(a, shape, s, dev);
 }
 
-// Blocks of the backward pass, which fix the order of dw's sum: three of kBlock threads
-// an SM (bf16: as many as are resident; fp32 rows, of which two are: 8192 x 4096 91 us
-// with two, 85.5 with three), but two where that leaves each fewer than four rows, since
-// each leaves a row of sums too (1237 x 2736 with an fp32 residual: 16.2 and 13.7 us).
-int64_t grad_blocks(int64_t M, int64_t K) {
+// Blocks of the backward pass, which fix the order of dw's sum: what an SM holds of them,
+// three of kBlock threads, two with dy and stream in fp32 (8192 x 4096 84.2 us, 91.3 with
+// three; with bf16 dy 85 to 92 with either, by the arrays' addresses), and two where three
+// would leave each fewer than four rows, since each leaves a row of sums too (1237 x 2736
+// with an fp32 residual: 16.2 and 13.7 us). 3.4 of 224 threads, of which three are
+// resident, in place of three: 16000 x 3584 98.7 us, not 71.5.
+int64_t grad_blocks(int64_t M, int64_t K, bool fp32) {
     const Shape shape = shape_of(K);
     const int64_t units = (M + shape.groups - 1) / shape.groups;
-    const int64_t most = kGradSms * ((shape.pieces == 2 ? 3 * kBlock : kWideBlock) / shape.threads());
-    return least(units, units < 4 * most && shape.pieces == 2 ? 2 * kGradSms : most);
+    const int64_t most = kGradSms * ((shape.pieces == 2 ? (fp32 ? 2 : 3) * kBlock : kWideBlock) / shape.threads());
+    return least(units, units < 4 * most && shape.pieces == 2 ? least(most, 2 * kGradSms) : most);
 }
 
 template <bool XBF, bool RBF, int N>
@@ -547,7 +552,7 @@ cudaError_t bwd(NormGradArgs a, const Shape &shape, cudaStream_t s, const Device
     using B = Bwd<XBF, RBF, N>;
     static std::atomic<bool> ready[64];
     a.tpr = shape.tpr;
-    return launch_rows(norm_bwd_kernel<XBF, RBF, N>, ready, grad_blocks(a.M, a.K), shape,
+    return launch_rows(norm_bwd_kernel<XBF, RBF, N>, ready, grad_blocks(a.M, a.K, !XBF && !RBF), shape,
                        B::BYTES * B::S * shape.threads(), s, dev.device, a);
 }
 template <bool XBF, bool RBF>
@@ -557,14 +562,17 @@ cudaError_t bwd(const NormGradArgs &a, void *dw, bool dw_bf16, cudaStream_t s, c
     if (a.M > 0) e = shape.pieces == 2 ? bwd<XBF, RBF, 2>(a, shape, s, dev) : bwd<XBF, RBF, 4>(a, shape, s, dev);
     if (e == cudaSuccess && dw != nullptr)
         e = launch_kernel(norm_dw_kernel, dim3(static_cast<unsigned>((a.K + 31) / 32)), dim3(kSumThreads), 0, s,
-                          static_cast<const float *>(a.partial), static_cast<int>(grad_blocks(a.M, a.K)), a.K, dw,
+                          static_cast<const float *>(a.partial), static_cast<int>(grad_blocks(a.M, a.K, !XBF && !RBF)), a.K, dw,
                           dw_bf16);
     return e;
 }
 
 }  // namespace
 
-int64_t rmsnorm_workspace_bytes(int64_t M, int64_t K) { return grad_blocks(M, K) * K * 4; }
+int64_t rmsnorm_workspace_bytes(int64_t M, int64_t K) {
+    const int64_t a = grad_blocks(M, K, false), b = grad_blocks(M, K, true);
+    return (a > b ? a : b) * K * 4;
+}
 
 int launch_rmsnorm_fwd(const void *x, int x_dtype, const void *r, void *t, int r_dtype, int64_t M, int64_t K,
                        const void *w, int w_dtype, float eps, const float *y_scale, void *y, int y_dtype,

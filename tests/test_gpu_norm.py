@@ -15,7 +15,8 @@ U = 2.0 ** -24
 HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: U}
 BF, F32 = torch.bfloat16, torch.float32
 SIZES = [(1, 16), (9, 16), (5, 272), (300, 1024), (3, 1040), (77, 2736), (2, 4096), (1237, 4096), (4, 8192), (3, 8208),
-         (2, 16384), (0, 64), (700, 16384), (500, 6160), (6000, 1024), (11000, 272)]
+         (2, 16384), (0, 64), (700, 16384), (500, 6160), (6000, 1024), (11000, 272),
+         (200, 11472), (4250, 3584), (4300, 3584), (4300, 5616), (700, 3600)]
 
 
 def guarded(shape, dtype):
