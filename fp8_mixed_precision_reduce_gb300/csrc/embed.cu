@@ -7,16 +7,16 @@
 // Backward: dtable[v] = scale (sum over the m with id_m = v of dy[m]), for every v: the
 // whole table is written, zeros mostly, which is what bounds it. The tokens are sorted
 // first, by (id, position), so that each row's sum has one order and no atomics:
-//   1. sort: a stable radix sort. A warp owns a run of consecutive positions and a
-//      histogram of its own. Up to 4096 tokens are sorted by one block in its shared
-//      memory, id and position in one word; up to 32768 by a cluster of 8 CTAs, whose
-//      counts and words go through distributed shared memory (16384 tokens and 50000 x
-//      768: 42.6 us in all, 47.7 with one block; 1000 and 32000 x 768: 16.7 with one
-//      block, 20.6 with a cluster, which starts later); more, or with ids too large for
-//      that, by a cluster through global memory.
+//   1. sort. Up to 4096 tokens: every block counts, for its share of the tokens, the
+//      smaller keys and the equal ones before it (4096^2 comparisons are 1.5 us of the
+//      device). More: a stable radix sort, in which a warp owns a run of consecutive
+//      positions and a histogram of its own; up to 32768 by a cluster of 8 CTAs, whose
+//      counts and words of id and position go through distributed shared memory (16384
+//      tokens and 50000 x 768: 42.5 us in all); more, or with ids too large for that, by
+//      a cluster through global memory.
 //   2. zero: every block looks through the ids for those among its rows and zeroes the
-//      others. It runs beside a sort in shared memory (one through global memory takes 4
-//      times as long beside it, and does not).
+//      others. It runs beside the counting, or a sort in shared memory (one through global
+//      memory takes 4 times as long beside it, and does not).
 //   3. sum: the sorted tokens in chunks of equal length, whatever their ids, so that
 //      an id that half of the batch holds is no one's long tail: a thread adds eight
 //      columns over a chunk in fp32 and writes a row where its id's run lies within the
@@ -175,32 +175,46 @@ struct ZeroArgs {
 
 // Block `part` of `parts`, of THREADS threads, zeroes the rows of its share of the table
 // but for those whose ids occur: it marks them in shared memory, kWindow rows at a time.
-template <int THREADS>
-__device__ __forceinline__ void zero_rows(const ZeroArgs &a, uint32_t *marks, int64_t part, int64_t parts) {
-    const int across = a.row < THREADS ? a.row : THREADS, down = THREADS / across;
+// `tokens(f)`: f of each id, from one thread. The first ZEROS threads zero, while the
+// others run `beside`, once.
+template <int THREADS, int ZEROS, typename F, typename G>
+__device__ __forceinline__ void zero_rows(const ZeroArgs &a, uint32_t *marks, int64_t part, int64_t parts, F tokens, G beside) {
+    const int across = a.row < ZEROS ? a.row : ZEROS, down = ZEROS / across;
     const int r0 = threadIdx.x / across, p0 = threadIdx.x - r0 * across;
-    const int64_t end = a.V * (part + 1) / parts;
-    for (int64_t v0 = a.V * part / parts; v0 < end; v0 += kWindow) {
+    const int64_t begin = a.V * part / parts, end = a.V * (part + 1) / parts;
+    for (int64_t v0 = begin; v0 < end || v0 == begin; v0 += kWindow) {
         const uint32_t rows = static_cast<uint32_t>(end - v0 < kWindow ? end - v0 : kWindow);
         __syncthreads();
         for (uint32_t i = threadIdx.x; i < (rows + 31) / 32; i += THREADS) marks[i] = 0u;
         __syncthreads();
-        for (int64_t i = threadIdx.x; i < a.M; i += THREADS * kZeroBatch) {
-            uint64_t at[kZeroBatch];
-#pragma unroll
-            for (int j = 0; j < kZeroBatch; ++j)
-                at[j] = i + j * THREADS < a.M ? static_cast<uint64_t>(__ldg(a.ids + i + j * THREADS)) - static_cast<uint64_t>(v0) : ~0ull;
-#pragma unroll
-            for (int j = 0; j < kZeroBatch; ++j)
-                if (at[j] < rows) atomicOr(&marks[at[j] >> 5], 1u << (at[j] & 31));
-        }
+        tokens([&](int64_t id) {
+            const uint64_t at = static_cast<uint64_t>(id) - static_cast<uint64_t>(v0);
+            if (at < rows) atomicOr(&marks[at >> 5], 1u << (at & 31));
+        });
         __syncthreads();
+        if (ZEROS < THREADS && threadIdx.x >= ZEROS) {
+            if (v0 == begin) beside();
+            continue;
+        }
         for (uint32_t r = r0; r < rows && r0 < down; r += down) {
             if (marks[r >> 5] >> (r & 31) & 1u) continue;
             uint4 *row = a.table + (v0 + r) * a.row;
             for (int p = p0; p < a.row; p += across) row[p] = make_uint4(0, 0, 0, 0);
         }
     }
+}
+template <int THREADS>
+__device__ __forceinline__ void zero_rows(const ZeroArgs &a, uint32_t *marks, int64_t part, int64_t parts) {
+    const auto tokens = [&](auto f) {
+        for (int64_t i = threadIdx.x; i < a.M; i += THREADS * kZeroBatch) {
+            int64_t id[kZeroBatch];
+#pragma unroll
+            for (int j = 0; j < kZeroBatch; ++j) id[j] = i + j * THREADS < a.M ? __ldg(a.ids + i + j * THREADS) : -1;
+#pragma unroll
+            for (int j = 0; j < kZeroBatch; ++j) f(id[j]);
+        }
+    };
+    zero_rows<THREADS, THREADS>(a, marks, part, parts, tokens, [] {});
 }
 
 // EARLY: it runs beside the kernel before it, whose arrays it does not touch and which
@@ -332,99 +346,70 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const SortA
     }
 }
 
-// The sort of up to kOneMost tokens by one block, while the other blocks zero the rows
-// without a token: words of (key, position), the key above `low` bits of position, in registers while they change places in shared memory.
-// Digits of up to 10 bits: one pass for up to 1023 ids, two for up to 2^20.
-constexpr int kOneThreads = 1024, kOneWarps = kOneThreads / 32, kOneEach = 4;
-constexpr int kOneBits = 10, kOneBins = 1 << kOneBits;
-constexpr int kOneMost = kOneThreads * kOneEach;
-constexpr int kOneSmem = (kOneMost + kOneWarps * kOneBins) * 4;
-static_assert(kOneBins == kOneThreads, "a thread for each bin");
-static_assert(kWindow / 8 <= kOneSmem, "the zeroing's marks");
+// Up to kRankMost tokens: half of every block zeroes its rows, and the other half finds
+// where its share of the tokens goes, two for a warp at a time, by counting the keys before
+// them. bf16, 4096 tokens: 5000 x 64 13.8 us (16.5 and 15.2 with 8 and 24 warps of 32 that
+// count), 32000 x 2048 35.5 (34.8, 39.5); 3361 in fp32, 2952 x 1120 19.3, by a radix sort in
+// one block 22.9.
+constexpr int kRankThreads = 1024, kRankZeros = 512, kRankWarps = (kRankThreads - kRankZeros) / 32;
+constexpr int kRankMost = 4096;
 
-__global__ void __launch_bounds__(kOneThreads, 1) embed_sort_one_kernel(const SortArgs a, const ZeroArgs z, int low, int digit_bits) {
-    extern __shared__ uint32_t sorted[];  // a word for each token, then a histogram for each warp
-    __shared__ uint32_t scan[kOneWarps];
+__global__ void __launch_bounds__(kRankThreads, 1) embed_rank_kernel(const SortArgs a, const ZeroArgs z) {
+    constexpr int kEach = kRankMost / kRankThreads;
+    __shared__ uint32_t marks[kWindow / 32];
+    __shared__ __align__(16) uint32_t key[kRankMost];
     pdl_wait();
     pdl_launch_dependents();
-    if (blockIdx.x > 0) {
-        zero_rows<kOneThreads>(z, sorted, blockIdx.x - 1, gridDim.x - 1);
-        return;
+    const int M = static_cast<int>(a.M), lane = threadIdx.x & 31, fours = (M + 3) / 4;
+    int64_t id[kEach];
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+        const int i = threadIdx.x + j * kRankThreads;
+        id[j] = i < M ? __ldg(a.ids + i) : -1;
     }
-    uint32_t *hist = sorted + kOneMost;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int M = static_cast<int>(a.M), rounds = (M + kOneThreads - 1) / kOneThreads;
-    const int first = warp * rounds * 32 + lane;  // a warp's words: consecutive
-    const uint32_t bins = 1u << digit_bits, mask = bins - 1u;
-    uint32_t w[kOneEach];
 #pragma unroll
-    for (int j = 0; j < kOneEach; ++j) {
-        const int i = first + j * 32;
-        if (j >= rounds || i >= M) continue;
-        const int64_t id = __ldg(a.ids + i);
-        w[j] = static_cast<uint32_t>(id >= 0 && id < a.V ? id : a.V) << low | static_cast<uint32_t>(i);
+    for (int j = 0; j < kEach; ++j) {
+        const int i = threadIdx.x + j * kRankThreads;
+        if (i < 4 * fours) key[i] = i >= M ? 0xFFFFFFFFu : static_cast<uint32_t>(id[j] >= 0 && id[j] < a.V ? id[j] : a.V);
     }
-    uint32_t *mine = hist + warp * kOneBins;
-    for (int pass = 0; pass < a.passes; ++pass) {
-        const int shift = low + pass * digit_bits;
-        for (uint32_t i = lane; i < bins; i += 32) mine[i] = 0u;
-        __syncwarp();
+    const auto tokens = [&](auto f) {
 #pragma unroll
-        for (int j = 0; j < kOneEach; ++j)
-            if (j < rounds && first + j * 32 < M) atomicAdd(&mine[w[j] >> shift & mask], 1u);
-        __syncthreads();
-        // a thread for each bin: where each warp's words of it go
-        uint32_t count[kOneWarps], all = 0;
+        for (int j = 0; j < kEach; ++j) f(id[j]);
+    };
+    const auto rank = [&] {
+        const int last = static_cast<int>(a.M * (blockIdx.x + 1) / gridDim.x);
+        const int warp = (threadIdx.x - kRankZeros) >> 5;
+        for (int i = static_cast<int>(a.M * blockIdx.x / gridDim.x) + 2 * warp; i < last; i += 2 * kRankWarps) {
+            // smaller keys, and of its own those of earlier positions: all but its own four's
+            const int at[2] = {i, i + 1 < last ? i + 1 : i};
+            const uint32_t mine[2] = {key[at[0]], key[at[1]]};
+            uint32_t n[2] = {0u, 0u};
+#pragma unroll 4
+            for (int c = lane; c < fours; c += 32) {
+                const uint4 q = reinterpret_cast<const uint4 *>(key)[c];
 #pragma unroll
-        for (int k = 0; k < kOneWarps; ++k) count[k] = static_cast<uint32_t>(tid) < bins ? hist[k * kOneBins + tid] : 0u;
+                for (int u = 0; u < 2; ++u) {
+                    const uint32_t below = mine[u] + (4 * c + 3 < at[u] ? 1u : 0u);
+                    n[u] += (q.x < below) + (q.y < below) + (q.z < below) + (q.w < below);
+                }
+            }
 #pragma unroll
-        for (int k = 0; k < kOneWarps; ++k) all += count[k];
-        uint32_t upto = all;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += v;
-        }
-        if (lane == 31) scan[warp] = upto;
-        __syncthreads();
-        uint32_t base = upto - all + __reduce_add_sync(0xffffffffu, lane < warp ? scan[lane] : 0u);
-        if (static_cast<uint32_t>(tid) < bins) {
-#pragma unroll
-            for (int k = 0; k < kOneWarps; ++k) {
-                hist[k * kOneBins + tid] = base;
-                base += count[k];
+            for (int u = 0; u < 2; ++u) {
+                if (lane < (at[u] & 3)) n[u] += key[(at[u] & ~3) + lane] == mine[u];
+                n[u] = __reduce_add_sync(0xffffffffu, n[u]);
+                if (lane == 0) {
+                    a.key[0][n[u]] = mine[u];
+                    a.pos[0][n[u]] = static_cast<uint32_t>(at[u]);
+                }
             }
         }
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < kOneEach; ++j) {
-            if (j >= rounds) break;
-            const bool in = first + j * 32 < M;
-            const uint32_t digit = in ? w[j] >> shift & mask : 0u, peers = lanes_with<kOneBits>(digit, in);
-            uint32_t to = 0;
-            if (in) to = mine[digit] + __popc(peers & ((1u << lane) - 1u));
-            __syncwarp();
-            if (in && lane == __ffs(peers) - 1) mine[digit] += __popc(peers);
-            __syncwarp();
-            if (in) sorted[to] = w[j];
-        }
-        __syncthreads();
-        if (pass + 1 < a.passes) {
-#pragma unroll
-            for (int j = 0; j < kOneEach; ++j)
-                if (j < rounds && first + j * 32 < M) w[j] = sorted[first + j * 32];
-        }
-        // (the next pass's first barrier parts these reads from its writes)
-    }
-    for (int i = tid; i < M; i += kOneThreads) {
-        const uint32_t v = sorted[i];
-        a.key[0][i] = v >> low;
-        a.pos[0][i] = v & ((1u << low) - 1u);
-    }
+    };
+    zero_rows<kRankThreads, kRankZeros>(z, marks, blockIdx.x, gridDim.x, tokens, rank);
 }
 
-// The same by the cluster, for more tokens: a CTA holds consecutive words, and they
-// change places through distributed shared memory.
+// More tokens: a radix sort by a cluster of words of (key, position), the key above `low`
+// bits of position. A CTA holds consecutive words in registers, and they change places
+// through distributed shared memory.
 constexpr int kWideEach = 8;
 constexpr int kWideMost = kSortCtas * kSortThreads * kWideEach;
 constexpr int kWideSmem = (kSortThreads * kWideEach + (kSortWarps + 1) * kBins) * 4;
@@ -731,19 +716,17 @@ cudaError_t few(const ZeroArgs &z, const SumArgs &a, cudaStream_t s, const Devic
 
 // The tokens sorted and the rows without one zeroed.
 cudaError_t sort_and_zero(SortArgs so, const ZeroArgs &z, int key_bits, int low, cudaStream_t s, const DeviceInfo &dev) {
-    const bool one = so.M <= kOneMost && key_bits + low <= 32, wide = !one && so.M <= kWideMost && key_bits + low <= 32;
-    const int most_bits = one ? kOneBits : kDigitBits;
-    so.passes = (key_bits + most_bits - 1) / most_bits;
+    const bool rank = so.M <= kRankMost, wide = !rank && so.M <= kWideMost && key_bits + low <= 32;
+    so.passes = (key_bits + kDigitBits - 1) / kDigitBits;
     const int digit_bits = (key_bits + so.passes - 1) / so.passes;
     // blocks of at least 32 KB, one or two to an SM, but where the sort runs
     const int64_t want = z.V * z.row / 2048 + 1, sms = dev.num_sms;
-    const int64_t most = one ? sms - 1 : wide ? 2 * sms - kSortCtas : 2 * sms;
-    const unsigned blocks = static_cast<unsigned>(want < most ? want : most);
-    if (one) {
-        static std::atomic<bool> ready[64];
-        const cudaError_t e = allow_smem(embed_sort_one_kernel, kOneSmem, ready, dev.device);
-        return e != cudaSuccess ? e : launch_kernel(embed_sort_one_kernel, dim3(1 + blocks), dim3(kOneThreads), kOneSmem, s, so, z, low, digit_bits);
+    if (rank) {  // (and of at most two tokens for each warp that ranks)
+        const int64_t for_tokens = so.M / (2 * kRankWarps) + 1, blocks = want > for_tokens ? want : for_tokens;
+        return launch_kernel(embed_rank_kernel, dim3(static_cast<unsigned>(blocks < sms ? blocks : sms)), dim3(kRankThreads), 0, s, so, z);
     }
+    const int64_t most = wide ? 2 * sms - kSortCtas : 2 * sms;
+    const unsigned blocks = static_cast<unsigned>(want < most ? want : most);
     cudaError_t e;
     if (wide) {
         static std::atomic<bool> ready[64];
@@ -816,7 +799,7 @@ int launch_embedding_bwd(const int64_t *ids, int64_t M, const void *dy, int dy_d
     SumArgs a = {};
     a.dy = dy;
     // (a sort through global memory leaves them in the arrays of the other turn after an odd number of passes)
-    const bool words = M <= kWideMost && key_bits + low <= 32;
+    const bool words = M <= kRankMost || (M <= kWideMost && key_bits + low <= 32);
     const int turn = words ? 0 : (key_bits + kDigitBits - 1) / kDigitBits & 1;
     a.key = so.key[turn];
     a.pos = so.pos[turn];
