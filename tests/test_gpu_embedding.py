@@ -84,7 +84,8 @@ def hold(got, ids, dy, scale):
                                    (2500, 513, 64), (5000, 30000, 4096), (40000, 262144, 16), (70000, 300, 32), (0, 40, 16), (5000, 2 ** 21 + 5, 16),
                                    (16384, 262143, 16), (16385, 511, 16), (4096, 1023, 16), (4097, 1024, 16),
                                    (32768, 131071, 16), (32768, 131072, 16), (32769, 100, 16),
-                                   (32, 9, 4112), (127, 40, 48), (128, 30000, 1040), (129, 40, 48), (128, 3, 16384)])
+                                   (32, 9, 4112), (127, 40, 48), (128, 30000, 1040), (129, 40, 48), (128, 3, 16384),
+                                   (0, 40, 2064), (300, 70, 4112), (4095, 600, 1040)])
 @pytest.mark.parametrize("dy,out", [(BF, BF), (BF, F32), (F32, BF), (F32, F32)])
 def test_backward(cuda_lib, M, V, K, dy, out):
     ids = some_ids(M, V, 2, spread=6.0)
