@@ -15,6 +15,9 @@ only allocates the outputs through torch and passes pointers.
 
 from __future__ import annotations
 
+import threading
+import weakref
+
 import torch
 
 from . import (AMAX_MAX, E4M3, E5M2, FEW_TOKENS, GELU_TANH, MAX_NORM_COLS, SILU, Meta, _stream,
@@ -81,6 +84,43 @@ def _capturing(w: torch.Tensor) -> bool:
     return w.is_cuda and torch.cuda.is_current_stream_capturing()
 
 
+class _Pass:
+    """Lives as long as the graph of an eager pass on the default stream."""
+
+    def __init__(self, leaves):
+        self.leaves = leaves
+
+
+_passes, _passes_lock = weakref.WeakSet(), threading.Lock()
+
+
+def _watch(ctx, *inputs) -> None:
+    """In the forward of a pass that keeps its graph: notes what _refuse_capture asks for."""
+    ctx.captured = None
+    leaves = [weakref.ref(t) for t in inputs if t is not None and t.is_cuda and t.requires_grad and t.is_leaf]
+    if not leaves:
+        return
+    if torch.cuda.is_current_stream_capturing():
+        ctx.captured = leaves
+    elif _stream(None) == 0:
+        ctx.alive = _Pass(leaves)
+        with _passes_lock:
+            _passes.add(ctx.alive)
+
+
+def _refuse_capture(ctx) -> None:
+    """A leaf's gradient is added up on the stream of the pass whose graph has held it
+    longest. Is that the default stream, which a capture cannot take in, a captured
+    backward pass would end the process; an exception takes its place."""
+    if ctx.captured is None:
+        return
+    with _passes_lock:
+        alive = {id(t) for p in list(_passes) for t in (r() for r in p.leaves) if t is not None}
+    if any(r() is not None and id(r()) in alive for r in ctx.captured):
+        raise RuntimeError("a backward pass cannot be captured while an eager pass with the same weights or inputs, "
+                           "made on the default stream, still has its graph: drop its outputs first")
+
+
 def _rows(x: torch.Tensor, cols: int) -> torch.Tensor:
     """x as dense rows on a 16-byte boundary."""
     x2 = x.reshape(-1, cols)
@@ -145,6 +185,7 @@ class _FP8GatedMLPFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, residual, norm, gate_up, down, mlp, keep):
         K, F = mlp.features, mlp.hidden
+        leaves = (x, residual, norm, gate_up, down)
         x2 = _rows(x, K)
         M, dev = x2.shape[0], x.device
         gu8, d8 = mlp.weight_copies(keep)
@@ -169,12 +210,14 @@ class _FP8GatedMLPFn(torch.autograd.Function):
             ctx.save_for_backward(X8, gu, H8, gu8, d8, factors, normed, rstd, norm)
             ctx.mlp = mlp
             ctx.like = (x.shape, x.dtype, gate_up.dtype, down.dtype)
+            _watch(ctx, *leaves)
             ctx.set_materialize_grads(False)
         y = y[:M].reshape(x.shape)
         return y if total is None else (y, total)
 
     @staticmethod
     def backward(ctx, dy, dtotal=None):
+        _refuse_capture(ctx)
         X8, gu, H8, gu8, d8, factors, normed, rstd, norm = ctx.saved_tensors
         mlp = ctx.mlp
         x_shape, x_dtype, gate_up_dtype, down_dtype = ctx.like
@@ -307,7 +350,9 @@ class FP8GatedMLP(_WeightCopies, torch.nn.Module):
     (AdamW) does so after it. x is bf16 or fp32. In a CUDA graph the casts are
     part of the graph, unless it is captured in eval mode without gradients
     (serving): then it reads the copies that are current, and after a change of
-    the weights weight_copies() casts them for its next replay.
+    the weights weight_copies() casts them for its next replay. A captured backward
+    pass is refused while an eager pass with the same weights, made on the default
+    stream, still has its graph.
 
     With norm_eps the block begins with a root-mean-square norm (weight: norm
     [features]) and takes part in a residual stream: block(x, residual) gives

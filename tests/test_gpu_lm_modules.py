@@ -7,6 +7,7 @@ GEMM's operands are rounded to FP8 the bounds are those of test_gpu_gated_mlp.py
 takes part); what does not pass through a GEMM is held to its own rounding."""
 
 import os
+import subprocess
 import sys
 
 import pytest
@@ -413,6 +414,52 @@ def test_a_training_pass_from_a_graph(cuda_lib):
         twin = model(cuda_lib)
         want = [passes(twin, ids)[0]] + [p.grad for p in twin.parameters()]
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+CAPTURED_BESIDE_AN_EAGER_PASS = """
+import torch
+from fp8_mixed_precision_reduce_gb300.embedding import TokenEmbedding
+from fp8_mixed_precision_reduce_gb300.gated_mlp import FP8GatedMLP
+from fp8_mixed_precision_reduce_gb300.lm_head import FP8LMHead
+
+e, head, mlp = TokenEmbedding(30, 64), FP8LMHead(64, 30, norm_eps=1e-6), FP8GatedMLP(64, 96, norm_eps=1e-6)
+ids = torch.randint(0, 30, (8,), device="cuda")
+r = torch.randn(8, 64, device="cuda")
+for run, module in ((lambda: e(ids), e), (lambda: head(r, ids), head), (lambda: mlp(r)[0], mlp)):
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run().float().sum().backward()
+    torch.cuda.current_stream().wait_stream(side)
+    module.zero_grad(set_to_none=True)
+    eager = run()
+    try:
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            run().float().sum().backward()
+        print("captured")
+    except RuntimeError as err:
+        print("refused" if "eager pass" in str(err) else err)
+    with torch.no_grad():
+        y = run()
+    del eager
+    module.zero_grad(set_to_none=True)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run().float().sum().backward()
+    graph.replay()
+    got = [p.grad.clone() for p in module.parameters()]
+    module.zero_grad(set_to_none=True)
+    run().float().sum().backward()
+    print("same" if all(torch.equal(a, p.grad) for a, p in zip(got, module.parameters())) else "other")
+"""
+
+
+def test_a_captured_backward_pass_beside_an_eager_graph_is_refused(cuda_lib):
+    """In a process of its own: without the refusal it would end."""
+    r = subprocess.run([sys.executable, "-c", CAPTURED_BESIDE_AN_EAGER_PASS], cwd=ROOT, capture_output=True, text=True,
+                       timeout=600)
+    assert r.returncode == 0, r.stderr[-2000:]
+    assert r.stdout.split() == ["refused", "same"] * 3, r.stdout
 
 
 @pytest.mark.parametrize("bits", [8, 32])
