@@ -223,10 +223,10 @@ class _FP8GatedMLPFn(torch.autograd.Function):
         x_shape, x_dtype, gate_up_dtype, down_dtype = ctx.like
         need_x, need_residual, need_norm, need_gate_up, need_down = ctx.needs_input_grad[:5]
         K, F, M, dev = mlp.features, mlp.hidden, X8.shape[0], X8.device
-        if dy is None:  # only the sum was used: its gradient is the residual's and x's
+        if dy is None:  # only the sum was used: its gradient is the residual's and x's, and may be differentiated again
             dx, dresidual = (dtotal.to(t) if n and dtotal is not None else None
                              for n, t in ((need_x, x_dtype), (need_residual, normed.dtype if normed is not None else x_dtype)))
-            return *first_order(dx, dresidual), None, None, None, None, None
+            return dx, dresidual, None, None, None, None, None
         sinv_x, sinv_gu, sinv_h, sinv_d = factors[0:1], factors[1:2], factors[2:3], factors[3:4]
         dy2 = _rows(dy.to(x_dtype), K)
         md, mg = mlp.meta_dy, mlp.meta_dgu

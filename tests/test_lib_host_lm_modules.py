@@ -140,3 +140,34 @@ def test_a_weight_held_twice(plain):  # noqa: F811
             (c,), ((w, meta),) = m.weight_copies(), m._weights()
             assert torch.equal(c, cast(w, meta.scale))
     assert fp8mp.E4M3 == h.meta_weight.fmt
+
+
+# ------------------------------- passes on the CPU, the kernels' outputs left as they are
+
+
+@pytest.fixture
+def no_kernels(plain, monkeypatch):  # noqa: F811
+    nothing = lambda *a, **kw: None  # noqa: E731
+    for mod in (gated_mlp, lm_head, embedding):
+        for name in dir(mod):
+            if name.startswith(("fp8_", "mp_")) and callable(getattr(mod, name)) and not name.endswith("_bytes"):
+                monkeypatch.setattr(mod, name, nothing)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+
+
+@pytest.mark.parametrize("x_dtype,r_dtype", [(torch.float32, torch.float32), (torch.bfloat16, torch.float32), (torch.float32, torch.bfloat16)])
+def test_the_streams_gradient_is_its_callers(no_kernels, x_dtype, r_dtype):
+    """Where only the sum is used the block is an addition: the caller's gradient stays
+    as it is, and has a derivative of its own."""
+    m = mlp()
+    x = torch.randn((4, 32)).to(x_dtype).requires_grad_(True)
+    r = torch.randn((4, 32)).to(r_dtype).requires_grad_(True)
+    g = torch.randn((4, 32)).to(r_dtype)
+    dx, dr = torch.autograd.grad([m(x, r)[1]], [x, r], grad_outputs=[g], create_graph=True)
+    assert not g.requires_grad and g.grad_fn is None
+    assert torch.equal(dr, g) and torch.equal(dx, g.to(x_dtype)) and dx.dtype == x_dtype
+    g.requires_grad_(True)
+    dx, dr = torch.autograd.grad([m(x, r)[1]], [x, r], grad_outputs=[g], create_graph=True)
+    v = torch.randn((4, 32)).bfloat16()
+    (again,) = torch.autograd.grad([dx, dr], [g], grad_outputs=[v.to(x_dtype), v.to(r_dtype)])
+    assert torch.equal(again, v.to(r_dtype) + v.to(r_dtype))
