@@ -23,8 +23,8 @@ __all__ = ["FP8LMHead"]
 
 
 def _logits_of(x, residual, norm, head, for_training: bool):
-    """The logits' rows (bf16, [tokens or more, vocabulary rounded up]), and what they
-    were made of."""
+    """The logits' rows (head.logits_dtype, [tokens, vocabulary rounded up]), and what
+    they were made of."""
     K = head.features
     x2 = _rows(x, K)
     M, dev = x2.shape[0], x.device
@@ -34,7 +34,7 @@ def _logits_of(x, residual, norm, head, for_training: bool):
     norm = norm.detach().contiguous() if norm is not None else None
     total, rstd = _codes_of(x2, _rows(residual, K) if residual is not None else None, norm, head.norm_eps, head.meta_x,
                             X8[:M])
-    logits = torch.empty((M if few else X8.shape[0], w8.shape[0]), dtype=torch.bfloat16, device=dev)
+    logits = torch.empty((M if few else X8.shape[0], w8.shape[0]), dtype=head.logits_dtype, device=dev)
     (fp8_linear_few if few else fp8_linear_fwd)(X8[:M] if few else X8, w8, head.meta_x.scale_inv, head.meta_weight.scale_inv,
                                                 logits)
     return logits[:M], X8, w8, x2 if total is None else total, rstd, norm
@@ -108,15 +108,23 @@ class FP8LMHead(_WeightCopies, torch.nn.Module):
     fp32 in the targets' shape, differentiable; a target outside 0 .. vocab - 1 (a prompt's
     or padding's) has log p 0 and no gradient. head.top(x, k) gives the k most probable tokens and their log p.
     With norm_eps both take the residual stream: n = norm(x + residual).
+
+    The logits are held in bf16, whatever x's type, until log p is taken from them in
+    fp32: a logit of 16 to 32 is off by up to 2^-4, and top takes the lower token of two that
+    bf16 makes equal. With logits_dtype=torch.float32 they are the product's own fp32, and
+    take twice the memory.
     """
 
     def __init__(self, features: int, vocab: int, history_len: int = 16, amax_compute_algo: int = AMAX_MAX,
-                 margin: int = 0, device="cuda", dtype: torch.dtype = torch.float32, norm_eps: float | None = None):
+                 margin: int = 0, device="cuda", dtype: torch.dtype = torch.float32, norm_eps: float | None = None,
+                 logits_dtype: torch.dtype = torch.bfloat16):
         super().__init__()
+        if logits_dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError("logits_dtype must be bf16 or fp32")
         if features % 16 or features < 16 or vocab < 1:
             raise ValueError("FP8 linears need features divisible by 16, and a vocabulary")
         _check_norm(features, norm_eps)
-        self.features, self.vocab = features, vocab
+        self.features, self.vocab, self.logits_dtype = features, vocab, logits_dtype
         self.algo, self.margin = amax_compute_algo, margin
         bound = 1.0 / features ** 0.5
         weight = torch.empty(((vocab + 15) // 16 * 16, features), device=device, dtype=dtype).uniform_(-bound, bound)

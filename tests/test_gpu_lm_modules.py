@@ -501,3 +501,72 @@ def test_a_models_gradients_against_differences_of_scales(cuda_lib):
         got = sum((b.norm.grad.double() * b.norm.double()).sum().item() for b in m.blocks)
         size = sum((b.norm.grad.double() * b.norm.double()).norm().item() for b in m.blocks)
     assert abs(got - want) <= 0.25 * max(abs(want), size), (got, want)
+
+
+@pytest.mark.parametrize("tokens", [(1,), (2, 9), (333,)])
+@pytest.mark.parametrize("x_dtype", [BF, F32])
+def test_head_with_logits_in_fp32(cuda_lib, tokens, x_dtype):
+    """The same calls by hand with fp32 logits give the same bits; and of the product of
+    the codes in 64 bits the logits are off by no more than fp32 sums are: 64 products of
+    two 4-bit significands, exact, added with fewer than 64 roundings (of up to 2^-22 of the
+    terms' sum, where the tensor core cuts), and two scales. log p moves by at most twice
+    the largest error of a logit; x - m and its product with log2(e) round by 2^-24 of
+    at most twice the largest logit each, the difference by 2^-24 of itself, and the 500 terms
+    of S and their sum by less than 2^-22 a term."""
+    from fp8_mixed_precision_reduce_gb300.lm_head import FP8LMHead
+
+    torch.manual_seed(12)
+    K, V = 64, 500
+    head = FP8LMHead(K, V, logits_dtype=F32)
+    with torch.no_grad():
+        head.weight.mul_(8)
+    x = (torch.randn((*tokens, K), device="cuda") * 4).to(x_dtype).requires_grad_(True)
+    t = torch.randint(0, V, tokens, device="cuda")
+    logprob, entropy = head(x, t, entropy=True)
+    da = torch.randn(tokens, device="cuda")
+    logprob.backward(da)
+    M, rows = x.numel() // K, (x.numel() // K + 15) // 16 * 16
+    X8 = torch.zeros((rows, K), dtype=torch.uint8, device="cuda")
+    (W8,) = head.weight_copies()
+    one = torch.ones(1, device="cuda")
+    cuda_lib.fp8_quantize(x.detach().reshape(M, K), cuda_lib.E4M3, one, X8[:M])
+    logits = torch.empty((rows, 512), device="cuda")
+    if M <= cuda_lib.FEW_TOKENS:
+        cuda_lib.fp8_linear_few(X8[:M], W8, one, one, logits[:M])
+    else:
+        cuda_lib.fp8_linear_fwd(X8, W8, one, one, logits)
+    logits = logits[:M]
+    stats, lp, H = torch.empty((M, 2), device="cuda"), torch.empty(M, device="cuda"), torch.empty(M, device="cuda")
+    cuda_lib.mp_logprobs_fwd(logits, t.reshape(-1), lp, stats, entropy=H, vocab=V)
+    assert torch.equal(lp, logprob.reshape(-1)) and torch.equal(H, entropy.reshape(-1))
+    D8 = torch.zeros((rows, 512), dtype=torch.uint8, device="cuda")
+    cuda_lib.mp_logprobs_bwd(logits, t.reshape(-1), stats, da.reshape(-1), D8[:M], scale=one, vocab=V)
+    dx, dw = torch.empty((rows, K), dtype=x_dtype, device="cuda"), torch.empty_like(head.weight)
+    cuda_lib.fp8_linear_bwd_rowmajor(D8, W8, X8, one, one, one, dx, dw)
+    assert torch.equal(dx[:M].reshape(x.shape), x.grad) and torch.equal(dw, head.weight.grad)
+    xd, wd = (c.view(torch.float8_e4m3fn).double() for c in (X8[:M], W8[:V]))
+    exact, room = xd @ wd.T, 66 * 2.0 ** -22 * (xd.abs() @ wd.abs().T)
+    logp = torch.log_softmax(exact, -1)
+    want = logp.gather(1, t.reshape(-1, 1))[:, 0]
+    worst = room.max(1).values  # log p is off by the target's logit and by a mean of all of them
+    bound = 2 * worst + 2.0 ** -23 * (2 * exact.abs().max(1).values + want.abs() + 8) + 500 * 2.0 ** -22
+    assert ((logprob.detach().reshape(-1).double() - want).abs() <= bound).all()
+    assert cuda_lib.fp8mp_check() == 0
+
+
+def test_top_of_logits_that_bf16_makes_equal(cuda_lib):
+    """Logits of 17 and 17 + 2^-6: equal in bf16, where the lower token comes first."""
+    from fp8_mixed_precision_reduce_gb300.lm_head import FP8LMHead
+
+    for dtype, want in ((None, [3, 7]), (BF, [3, 7]), (F32, [7, 3])):
+        head = FP8LMHead(32, 40, **({} if dtype is None else dict(logits_dtype=dtype)))
+        with torch.no_grad():
+            head.weight.zero_()
+            head.weight[3, 0] = head.weight[7, 0] = 16.0
+            head.weight[3, 1] = head.weight[7, 1] = 1.0
+            head.weight[7, 2] = 2.0 ** -6
+        x = torch.ones((3, 32), device="cuda")
+        logprob, ids = head.top(x, 2)
+        assert ids.tolist() == [want] * 3
+        gap = logprob[:, 0] - logprob[:, 1]  # (of two values in (-1, -0.5), rounded by 2^-25 each)
+        assert ((gap - (2.0 ** -6 if dtype is F32 else 0.0)).abs() <= 2.0 ** -24).all()

@@ -142,6 +142,13 @@ def test_a_weight_held_twice(plain):  # noqa: F811
     assert fp8mp.E4M3 == h.meta_weight.fmt
 
 
+def test_logits_of_another_type_are_refused():
+    for dtype in (torch.float16, torch.float64, None):
+        with pytest.raises(ValueError, match="logits"):
+            head(logits_dtype=dtype)
+    assert head().logits_dtype is torch.bfloat16 and head(logits_dtype=torch.float32).logits_dtype is torch.float32
+
+
 # ------------------------------- passes on the CPU, the kernels' outputs left as they are
 
 
