@@ -166,7 +166,7 @@ class FP8LMHead(_WeightCopies, torch.nn.Module):
             raise ValueError(f"k must lie in 1..{min(MAX_TOP, self.vocab)}, got {k}")
         logits, *_ = _logits_of(x, residual, self.norm, self, False)
         M, dev = logits.shape[0], x.device
-        stats, logprob = torch.empty((M, 2), device=dev), torch.empty((M, k), device=dev)
+        stats, logprob = (torch.empty((M, n), dtype=torch.float32, device=dev) for n in (2, k))
         tokens = torch.empty((M, k), dtype=torch.int64, device=dev)
         mp_logprobs_fwd(logits, None, None, stats, top_logprob=logprob, top_id=tokens, vocab=self.vocab)
         return logprob.reshape(*x.shape[:-1], k), tokens.reshape(*x.shape[:-1], k)

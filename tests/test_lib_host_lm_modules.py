@@ -178,3 +178,23 @@ def test_the_streams_gradient_is_its_callers(no_kernels, x_dtype, r_dtype):
     v = torch.randn((4, 32)).bfloat16()
     (again,) = torch.autograd.grad([dx, dr], [g], grad_outputs=[v.to(x_dtype), v.to(r_dtype)])
     assert torch.equal(again, v.to(r_dtype) + v.to(r_dtype))
+
+
+@pytest.fixture
+def bf16_by_default():
+    torch.set_default_dtype(torch.bfloat16)
+    yield
+    torch.set_default_dtype(torch.float32)
+
+
+def test_top_under_another_default_type(no_kernels, bf16_by_default, monkeypatch):
+    """What the kernels write in fp32 is fp32 whatever torch's default is."""
+    seen = []
+    monkeypatch.setattr(lm_head, "mp_logprobs_fwd", lambda logits, t, lp, stats, entropy=None, top_logprob=None, top_id=None, vocab=None:
+                        seen.extend(x.dtype for x in (stats, lp, entropy, top_logprob) if x is not None))
+    m = head(norm_eps=1e-6)
+    logprob, ids = m.top(torch.zeros((4, 32)), 3, torch.zeros((4, 32)))
+    with torch.no_grad():
+        m(torch.zeros((4, 32)), torch.zeros(4, dtype=I64), torch.zeros((4, 32)), entropy=True)
+    assert logprob.dtype is torch.float32 and ids.dtype is I64
+    assert len(seen) == 5 and set(seen) == {torch.float32}
