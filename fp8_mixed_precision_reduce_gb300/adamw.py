@@ -42,7 +42,7 @@ class AdamW:
             raise ValueError("state_bits must be 32 or 8")
         self.lr, self.betas, self.eps, self.max_norm = lr, betas, eps, max_norm
         self.growth_interval = growth_interval
-        dev = self.params[0].device
+        dev, f32 = self.params[0].device, torch.float32
         for p in self.params:
             if p.dtype != torch.float32 or not p.is_contiguous() or p.device != dev:
                 raise ValueError("AdamW needs dense fp32 parameters on one device")
@@ -57,16 +57,17 @@ class AdamW:
                 blocks = (n + 255) // 256
                 self.state.append(dict(exp_avg=torch.zeros(n, dtype=torch.int8, device=dev),
                                        exp_avg_sq=torch.zeros(n, dtype=torch.uint8, device=dev),
-                                       exp_avg_scale=torch.zeros(blocks, device=dev),
-                                       exp_avg_sq_scale=torch.zeros(blocks, device=dev)))
+                                       exp_avg_scale=torch.zeros(blocks, dtype=f32, device=dev),
+                                       exp_avg_sq_scale=torch.zeros(blocks, dtype=f32, device=dev)))
             else:
-                self.state.append(dict(exp_avg=torch.zeros(n, device=dev), exp_avg_sq=torch.zeros(n, device=dev)))
+                self.state.append(dict(exp_avg=torch.zeros(n, dtype=f32, device=dev),
+                                       exp_avg_sq=torch.zeros(n, dtype=f32, device=dev)))
         self.weight_decay = [weight_decay if p.dim() >= 2 else 0.0 for p in self.params]
-        self.loss_scale = torch.full((1,), float(loss_scale), device=dev)
+        self.loss_scale = torch.full((1,), float(loss_scale), dtype=f32, device=dev)
         self.growth_tracker = torch.zeros(1, dtype=torch.int32, device=dev)
         self.found_inf = torch.zeros(1, dtype=torch.int32, device=dev)
-        self.beta_pows = torch.ones(2, device=dev)
-        self.grad_norm = torch.zeros(1, device=dev)
+        self.beta_pows = torch.ones(2, dtype=f32, device=dev)
+        self.grad_norm = torch.zeros(1, dtype=f32, device=dev)
         self.seed = torch.full((1,), seed, dtype=torch.int32, device=dev)
         self.workspace = torch.zeros(mp_adamw_workspace_bytes() // 4, dtype=torch.int32, device=dev)
         self._plan, self._arrays = None, None

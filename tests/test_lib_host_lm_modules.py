@@ -198,3 +198,13 @@ def test_top_under_another_default_type(no_kernels, bf16_by_default, monkeypatch
         m(torch.zeros((4, 32)), torch.zeros(4, dtype=I64), torch.zeros((4, 32)), entropy=True)
     assert logprob.dtype is torch.float32 and ids.dtype is I64
     assert len(seen) == 5 and set(seen) == {torch.float32}
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_adamw_under_another_default_type(plain, bf16_by_default, bits):  # noqa: F811
+    m = table(fp8=True)
+    opt = adamw.AdamW(m.parameters(), lr=1e-2, state_bits=bits, min_8bit_size=1, modules=[m])
+    for t in (opt.loss_scale, opt.beta_pows, opt.grad_norm):
+        assert t.dtype is torch.float32
+    step(opt, m)
+    assert torch.equal(m.weight_copies()[0], cast(m.weight, m.meta_weight.scale))
