@@ -11,8 +11,8 @@ from __future__ import annotations
 import torch
 
 from . import (AMAX_MAX, E4M3, Meta, mp_embedding_bwd, mp_embedding_bwd_workspace_bytes, mp_embedding_fwd)
-from .gated_mlp import _refuse_capture, _rows, _watch, _WeightCopies
-from .linear import first_order
+from .gated_mlp import _rows, _WeightCopies
+from .linear import first_order, refuse_capture, watch_leaves
 
 __all__ = ["TokenEmbedding"]
 
@@ -31,12 +31,12 @@ class _TokenEmbeddingFn(torch.autograd.Function):
         if keep:
             ctx.save_for_backward(flat)
             ctx.like = (weight.shape, weight.dtype, module.scale)
-            _watch(ctx, weight)
+            watch_leaves(ctx)
         return out.reshape(*ids.shape, module.features)
 
     @staticmethod
     def backward(ctx, dy):
-        _refuse_capture(ctx)
+        refuse_capture(ctx)
         (ids,) = ctx.saved_tensors
         (V, K), dtype, scale = ctx.like
         dy2 = _rows(dy, K)

@@ -15,16 +15,13 @@ only allocates the outputs through torch and passes pointers.
 
 from __future__ import annotations
 
-import threading
-import weakref
-
 import torch
 
 from . import (AMAX_MAX, E4M3, E5M2, FEW_TOKENS, GELU_TANH, MAX_NORM_COLS, SILU, Meta, _stream,
                delayed_scaling_update, fp8_gated_bwd, fp8_gated_dgrad, fp8_gated_fwd, fp8_linear_bwd_rowmajor,
                fp8_linear_few, fp8_linear_fwd, fp8_quantize, fp8_rmsnorm_bwd, fp8_rmsnorm_bwd_workspace_bytes,
                fp8_rmsnorm_fwd)
-from .linear import first_order
+from .linear import first_order, refuse_capture, watch_leaves
 
 __all__ = ["FP8GatedMLP"]
 
@@ -82,43 +79,6 @@ class _CopyState:
 
 def _capturing(w: torch.Tensor) -> bool:
     return w.is_cuda and torch.cuda.is_current_stream_capturing()
-
-
-class _Pass:
-    """Lives as long as the graph of an eager pass on the default stream."""
-
-    def __init__(self, leaves):
-        self.leaves = leaves
-
-
-_passes, _passes_lock = weakref.WeakSet(), threading.Lock()
-
-
-def _watch(ctx, *inputs) -> None:
-    """In the forward of a pass that keeps its graph: notes what _refuse_capture asks for."""
-    ctx.captured = None
-    leaves = [weakref.ref(t) for t in inputs if t is not None and t.is_cuda and t.requires_grad and t.is_leaf]
-    if not leaves:
-        return
-    if torch.cuda.is_current_stream_capturing():
-        ctx.captured = leaves
-    elif _stream(None) == 0:
-        ctx.alive = _Pass(leaves)
-        with _passes_lock:
-            _passes.add(ctx.alive)
-
-
-def _refuse_capture(ctx) -> None:
-    """A leaf's gradient is added up on the stream of the pass whose graph has held it
-    longest. Is that the default stream, which a capture cannot take in, a captured
-    backward pass would end the process; an exception takes its place."""
-    if ctx.captured is None:
-        return
-    with _passes_lock:
-        alive = {id(t) for p in list(_passes) for t in (r() for r in p.leaves) if t is not None}
-    if any(r() is not None and id(r()) in alive for r in ctx.captured):
-        raise RuntimeError("a backward pass cannot be captured while an eager pass with the same weights or inputs, "
-                           "made on the default stream, still has its graph: drop its outputs first")
 
 
 def _rows(x: torch.Tensor, cols: int) -> torch.Tensor:
@@ -185,7 +145,6 @@ class _FP8GatedMLPFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, residual, norm, gate_up, down, mlp, keep):
         K, F = mlp.features, mlp.hidden
-        leaves = (x, residual, norm, gate_up, down)
         x2 = _rows(x, K)
         M, dev = x2.shape[0], x.device
         gu8, d8 = mlp.weight_copies(keep)
@@ -210,14 +169,14 @@ class _FP8GatedMLPFn(torch.autograd.Function):
             ctx.save_for_backward(X8, gu, H8, gu8, d8, factors, normed, rstd, norm)
             ctx.mlp = mlp
             ctx.like = (x.shape, x.dtype, gate_up.dtype, down.dtype)
-            _watch(ctx, *leaves)
+            watch_leaves(ctx)
             ctx.set_materialize_grads(False)
         y = y[:M].reshape(x.shape)
         return y if total is None else (y, total)
 
     @staticmethod
     def backward(ctx, dy, dtotal=None):
-        _refuse_capture(ctx)
+        refuse_capture(ctx)
         X8, gu, H8, gu8, d8, factors, normed, rstd, norm = ctx.saved_tensors
         mlp = ctx.mlp
         x_shape, x_dtype, gate_up_dtype, down_dtype = ctx.like
@@ -351,8 +310,10 @@ class FP8GatedMLP(_WeightCopies, torch.nn.Module):
     part of the graph, unless it is captured in eval mode without gradients
     (serving): then it reads the copies that are current, and after a change of
     the weights weight_copies() casts them for its next replay. A captured backward
-    pass is refused while an eager pass with the same weights, made on the default
-    stream, still has its graph.
+    pass is refused where torch would end the process: a pass of this library's modules
+    with the same weights or inputs that was made before on the default stream still had
+    its graph. What torch's own operations hold of a weight (a penalty on it, a view of it
+    as the input) is not seen: drop their results before a capture, too.
 
     With norm_eps the block begins with a root-mean-square norm (weight: norm
     [features]) and takes part in a residual stream: block(x, residual) gives

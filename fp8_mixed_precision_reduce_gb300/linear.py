@@ -19,10 +19,13 @@ from __future__ import annotations
 
 import torch
 
-from . import (AMAX_MAX, E4M3, E5M2, Meta, delayed_scaling_update, fp8_linear_bwd_rowmajor, fp8_linear_fwd,
+from . import (AMAX_MAX, E4M3, E5M2, Meta, _stream, delayed_scaling_update, fp8_linear_bwd_rowmajor, fp8_linear_fwd,
                fp8_quantize, fp8_quantize_dbias, fp8_quantize_dbias_workspace_bytes)
 
 __all__ = ["FP8Linear"]
+
+
+_Leaf = torch._C._functions.AccumulateGrad  # a leaf's node
 
 
 class _FirstOrder(torch.autograd.Function):
@@ -43,6 +46,30 @@ def first_order(*grads):
     if not torch.is_grad_enabled():
         return grads
     return tuple(None if g is None else _FirstOrder.apply(g.requires_grad_()) for g in grads)
+
+
+_FIRST = "fp8mp: stream of the first pass"
+
+
+def watch_leaves(ctx) -> None:
+    """In the forward of a pass that keeps its graph: notes what refuse_capture asks for.
+    A leaf's gradient is added up on the stream on which the first pass to take the leaf in
+    was made: it made the leaf's node, which lasts until no graph holds it any more
+    (whichever goes first) and here carries that stream along."""
+    here, capturing = _stream(None), torch.cuda.is_current_stream_capturing()
+    ctx.waits_outside = False
+    for node, _ in ctx.next_functions:
+        if type(node) is _Leaf and node.metadata.setdefault(_FIRST, here) == 0 and capturing:
+            ctx.waits_outside = True
+
+
+def refuse_capture(ctx) -> None:
+    """A capture cannot take in the default stream: where a leaf's gradient would be added
+    up there, torch would end the process, and an exception takes its place."""
+    if ctx.waits_outside:
+        raise RuntimeError("a backward pass cannot be captured while an eager pass with the same weights or inputs, "
+                           "made on the default stream before any other, still had its graph: drop its outputs, and "
+                           "those of later passes, before the capture")
 
 
 class _FP8LinearFn(torch.autograd.Function):
@@ -67,11 +94,13 @@ class _FP8LinearFn(torch.autograd.Function):
         # the codes were made with this step's scales: keep those for backward
         ctx.save_for_backward(X8, W8, layer.meta_x.scale_inv.clone(), layer.meta_w.scale_inv.clone())
         ctx.layer = layer
+        watch_leaves(ctx)
         ctx.shapes = (x.shape, x.dtype, weight.dtype, None if bias is None else bias.dtype)
         return y.reshape(*x.shape[:-1], N)
 
     @staticmethod
     def backward(ctx, dy):
+        refuse_capture(ctx)
         X8, W8, sinv_x, sinv_w = ctx.saved_tensors
         layer = ctx.layer
         x_shape, x_dtype, w_dtype, b_dtype = ctx.shapes

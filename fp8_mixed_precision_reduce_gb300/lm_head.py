@@ -15,9 +15,9 @@ import torch
 
 from . import (AMAX_MAX, E4M3, E5M2, FEW_TOKENS, MAX_TOP, Meta, fp8_linear_bwd_rowmajor, fp8_linear_few,
                fp8_linear_fwd, mp_logprobs_bwd, mp_logprobs_fwd)
-from .gated_mlp import (_check_input, _check_norm, _check_norm_weight, _codes_of, _norm_grads, _refuse_capture, _rows,
-                        _rows16, _watch, _WeightCopies)
-from .linear import first_order
+from .gated_mlp import (_check_input, _check_norm, _check_norm_weight, _codes_of, _norm_grads, _rows, _rows16,
+                        _WeightCopies)
+from .linear import first_order, refuse_capture, watch_leaves
 
 __all__ = ["FP8LMHead"]
 
@@ -43,7 +43,6 @@ def _logits_of(x, residual, norm, head, for_training: bool):
 class _FP8LMHeadFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, residual, norm, weight, targets, head, with_entropy, keep):
-        leaves = (x, residual, norm, weight)
         logits, X8, w8, normed, rstd, norm = _logits_of(x, residual, norm, head, keep)
         M, dev = logits.shape[0], x.device
         t = targets.reshape(-1)
@@ -60,12 +59,12 @@ class _FP8LMHeadFn(torch.autograd.Function):
             ctx.head = head
             ctx.like = (x.shape, x.dtype, weight.dtype)
             ctx.set_materialize_grads(False)
-            _watch(ctx, *leaves)
+            watch_leaves(ctx)
         return (logprob, entropy) if with_entropy else logprob
 
     @staticmethod
     def backward(ctx, dlogprob, dentropy=None):
-        _refuse_capture(ctx)
+        refuse_capture(ctx)
         logits, X8, w8, t, stats, entropy, factors, normed, rstd, norm = ctx.saved_tensors
         head = ctx.head
         x_shape, x_dtype, w_dtype = ctx.like

@@ -570,3 +570,65 @@ def test_top_of_logits_that_bf16_makes_equal(cuda_lib):
         assert ids.tolist() == [want] * 3
         gap = logprob[:, 0] - logprob[:, 1]  # (of two values in (-1, -0.5), rounded by 2^-25 each)
         assert ((gap - (2.0 ** -6 if dtype is F32 else 0.0)).abs() <= 2.0 ** -24).all()
+
+
+WHICH_CAPTURES_ARE_REFUSED = """
+import torch
+from fp8_mixed_precision_reduce_gb300.embedding import TokenEmbedding
+from fp8_mixed_precision_reduce_gb300.gated_mlp import FP8GatedMLP
+from fp8_mixed_precision_reduce_gb300.linear import FP8Linear
+from fp8_mixed_precision_reduce_gb300.lm_head import FP8LMHead
+
+linear, e, head, mlp = FP8Linear(64, 64), TokenEmbedding(30, 64), FP8LMHead(64, 30, norm_eps=1e-6), FP8GatedMLP(64, 96, norm_eps=1e-6)
+ids = torch.randint(0, 30, (16,), device="cuda")
+r = torch.randn(16, 64, device="cuda")
+
+def beside(run, stream):
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        y = run()
+    torch.cuda.current_stream().wait_stream(stream)
+    return y
+
+for run, module in ((lambda: linear(r), linear), (lambda: e(ids), e), (lambda: head(r, ids), head), (lambda: mlp(r)[0], mlp)):
+    side = torch.cuda.Stream()
+
+    def refused():
+        module.zero_grad(set_to_none=True)
+        try:
+            with torch.cuda.graph(torch.cuda.CUDAGraph()):
+                run().float().sum().backward()
+        except RuntimeError as err:
+            assert "eager pass" in str(err), err
+            return True
+        return False
+
+    beside(run, side).float().sum().backward()
+    eager = run()
+    assert refused()
+    later = beside(run, side)
+    del eager  # (the leaves' nodes are still the first pass's)
+    assert refused()
+    del later
+    older = beside(run, side)
+    eager = run()
+    module.zero_grad(set_to_none=True)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run().float().sum().backward()
+    graph.replay()
+    torch.cuda.synchronize()
+    got = [p.grad.clone() for p in module.parameters()]
+    del older, eager, graph
+    module.zero_grad(set_to_none=True)
+    run().float().sum().backward()
+    assert all(torch.equal(a, p.grad) for a, p in zip(got, module.parameters()))
+    print("ok")
+"""
+
+
+def test_which_captured_backward_passes_are_refused(cuda_lib):
+    """In a process of its own: what should be refused would end it."""
+    r = subprocess.run([sys.executable, "-c", WHICH_CAPTURES_ARE_REFUSED], cwd=ROOT, capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stderr[-2000:]
+    assert r.stdout.split() == ["ok"] * 4, r.stdout

@@ -2,12 +2,13 @@
 refuse, and their weights' copies, on CPU tensors with the casts in plain torch."""
 
 import copy
+import types
 
 import pytest
 import torch
 
 import fp8_mixed_precision_reduce_gb300 as fp8mp
-from fp8_mixed_precision_reduce_gb300 import adamw, embedding, gated_mlp, lm_head
+from fp8_mixed_precision_reduce_gb300 import adamw, embedding, gated_mlp, linear, lm_head
 from test_lib_host_modules import cast, plain, step  # noqa: F401
 
 I64 = torch.int64
@@ -155,11 +156,14 @@ def test_logits_of_another_type_are_refused():
 @pytest.fixture
 def no_kernels(plain, monkeypatch):  # noqa: F811
     nothing = lambda *a, **kw: None  # noqa: E731
-    for mod in (gated_mlp, lm_head, embedding):
+    for mod in (gated_mlp, lm_head, embedding, linear):
         for name in dir(mod):
             if name.startswith(("fp8_", "mp_")) and callable(getattr(mod, name)) and not name.endswith("_bytes"):
                 monkeypatch.setattr(mod, name, nothing)
-    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    where = types.SimpleNamespace(stream=0, capturing=False)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: where.capturing)
+    monkeypatch.setattr(linear, "_stream", lambda s: where.stream)
+    return where
 
 
 @pytest.mark.parametrize("x_dtype,r_dtype", [(torch.float32, torch.float32), (torch.bfloat16, torch.float32), (torch.float32, torch.bfloat16)])
@@ -208,3 +212,72 @@ def test_adamw_under_another_default_type(plain, bf16_by_default, bits):  # noqa
         assert t.dtype is torch.float32
     step(opt, m)
     assert torch.equal(m.weight_copies()[0], cast(m.weight, m.meta_weight.scale))
+
+
+def passes():
+    """Of each module: a pass with its leaves."""
+    lin, m, h, e = linear.FP8Linear(32, 32, device="cpu"), mlp(), head(norm_eps=1e-6), table()
+    r = torch.zeros((16, 32))
+    return [lambda x: lin(x), lambda x: m(x, r)[0], lambda x: h(x, torch.zeros(16, dtype=I64), r),
+            lambda x: e(torch.zeros(16, dtype=I64)).float()]
+
+
+@pytest.mark.parametrize("which", range(4))
+def test_which_captured_backward_passes_are_refused(no_kernels, which):
+    """A leaf's gradient is added up on the stream of the first pass that took it in, as
+    long as any pass holds it: the default stream's cannot be captured."""
+    where, run = no_kernels, passes()[which]
+    x = torch.zeros((16, 32), requires_grad=True)
+
+    def on(stream, capturing=False):
+        where.stream, where.capturing = stream, capturing
+        return run(x).sum()
+
+    def refused(y):
+        where.stream, where.capturing = 9, True
+        try:
+            y.backward()
+        except RuntimeError as err:
+            assert "eager pass" in str(err)
+            return True
+        return False
+
+    eager = on(0)
+    assert refused(on(9, True))
+    side = on(5)
+    assert refused(on(9, True))
+    del eager  # (the leaf's node is still the first pass's)
+    assert refused(on(9, True))
+    captured = on(9, True)
+    del side
+    assert refused(captured)
+    del captured
+    assert not refused(on(9, True))
+    side = on(5)
+    eager = on(0)
+    assert not refused(on(9, True))  # (an older pass than the default stream's made the node)
+    del side
+    assert not refused(on(9, True))
+    del eager
+    captured = on(9, True)
+    eager = on(0)
+    assert not refused(captured)
+    del captured, eager
+    with torch.no_grad():
+        y = on(0)
+    assert not refused(on(9, True)) and not y.requires_grad
+    on(0).backward()
+    assert not refused(on(9, True))
+
+
+@pytest.mark.parametrize("first", range(3))
+@pytest.mark.parametrize("second", range(3))
+def test_a_leaf_of_two_modules(no_kernels, first, second):
+    where, x = no_kernels, torch.zeros((16, 32), requires_grad=True)
+    eager = passes()[first](x)
+    where.stream, where.capturing = 9, True
+    captured = passes()[second](x)
+    with pytest.raises(RuntimeError, match="eager pass"):
+        captured.sum().backward()
+    del eager, captured
+    passes()[second](x).sum().backward()
