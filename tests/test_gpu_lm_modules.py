@@ -632,3 +632,32 @@ def test_which_captured_backward_passes_are_refused(cuda_lib):
     r = subprocess.run([sys.executable, "-c", WHICH_CAPTURES_ARE_REFUSED], cwd=ROOT, capture_output=True, text=True, timeout=600)
     assert r.returncode == 0, r.stderr[-2000:]
     assert r.stdout.split() == ["ok"] * 4, r.stdout
+
+
+def test_every_gradient_of_the_examples_model_against_64_bits(cuda_lib):
+    """Embedding, two blocks and head in a training pass. The bounds are the sums of the
+    parts' (5 % for each rounding to E4M3 or product of it, 10 % where an E5M2 operand takes
+    part) over the longest way to a gradient: forward through the table's copy, four GEMMs
+    and the head (30 %), backward through the head (10 %), two a block (40 %) and
+    a weight's product (10 %). Less than 1, which no gradient of a wrong sign or of
+    another input would be."""
+    m = model(cuda_lib)
+    ids = torch.randint(0, 500, (16, 33), device="cuda")
+    for turn in range(2):  # the first pass fills the histories, the second runs under their scales
+        m.zero_grad(set_to_none=True)
+        logprob = m(ids[:, :-1], ids[:, 1:])
+        (-logprob.mean() * 1024).backward()
+        if turn == 0:
+            for f in m.fp8_modules():
+                f.update_scales()
+    of = {n: p.detach().double().requires_grad_(True) for n, p in m.named_parameters()}
+    x, r = of["embedding.weight"][ids[:, :-1]] * m.embedding.scale, None
+    for i in range(len(m.blocks)):
+        t = x if r is None else x + r
+        x, r = mlp64(norm64(t, of[f"blocks.{i}.norm"], 1e-6), of[f"blocks.{i}.gate_up"], of[f"blocks.{i}.down"]), t
+    logits = norm64(x + r, of["head.norm"], 1e-6) @ of["head.weight"][:500].T
+    want = torch.log_softmax(logits, -1).gather(-1, ids[:, 1:, None])[..., 0]
+    (-want.mean() * 1024).backward()
+    assert relative(logprob.detach() - logprob.detach().mean(), (want - want.mean()).detach()) < 0.6
+    worst = {n: relative(p.grad, of[n].grad) for n, p in m.named_parameters()}
+    assert len(worst) == 9 and all(w < 0.9 for w in worst.values()), worst
