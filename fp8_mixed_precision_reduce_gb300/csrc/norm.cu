@@ -535,24 +535,27 @@ cudaError_t fwd(const NormArgs &a, cudaStream_t s, const DeviceInfo &dev) {
 }
 
 // Blocks of the backward pass, which fix the order of dw's sum: what an SM holds of them,
-// three of kBlock threads, two with dy and stream in fp32 (8192 x 4096 84.2 us, 91.3 with
-// three; with bf16 dy 85 to 92 with either, by the arrays' addresses), and two where three
-// would leave each fewer than four rows, since each leaves a row of sums too (1237 x 2736
-// with an fp32 residual: 16.2 and 13.7 us). 3.4 of 224 threads, of which three are
-// resident, in place of three: 16000 x 3584 98.7 us, not 71.5.
-int64_t grad_blocks(int64_t M, int64_t K, bool fp32) {
+// since each leaves a row of sums, and one that starts when another ends begins with a row's
+// whole latency. Of kBlock threads that is three, or two by their rows in shared memory with
+// a stream in fp32. bf16 dy, by two and by three: fp32 stream 500 x 4096 10.6 and 12.8 us, 1237 x
+// 2736 13.4, 15.6, 3000 x 2736 23.9, 25.8, 60000 x 256 40.6, 43.4, 8192 x 4096 91.1, 91.8, 12000 x
+// 1760 57.1, 55.9; bf16 stream 500 x 4096 10.3, 9.8, 2400 x 2736 17.7, 16.7, 8192 x 4096 55.3, 45.5.
+// fp32 dy, fp32 stream: 8192 x 4096 84.3, 91.2; bf16 stream 1237 x 2736 15.2, 14.4, 8192 x 4096 83.3,
+// 76.6. In whole blocks: 3.4 of 224 threads in place of three, 16000 x 3584 98.7 us, not 71.5.
+constexpr int grad_per_sm(bool fp32_stream) { return fp32_stream ? 2 : 3; }
+int64_t grad_blocks(int64_t M, int64_t K, bool fp32_stream) {
     const Shape shape = shape_of(K);
     const int64_t units = (M + shape.groups - 1) / shape.groups;
-    const int64_t most = kGradSms * ((shape.pieces == 2 ? (fp32 ? 2 : 3) * kBlock : kWideBlock) / shape.threads());
-    return least(units, units < 4 * most && shape.pieces == 2 ? least(most, 2 * kGradSms) : most);
+    return least(units, kGradSms * ((shape.pieces == 2 ? grad_per_sm(fp32_stream) * kBlock : kWideBlock) / shape.threads()));
 }
 
 template <bool XBF, bool RBF, int N>
 cudaError_t bwd(NormGradArgs a, const Shape &shape, cudaStream_t s, const DeviceInfo &dev) {
     using B = Bwd<XBF, RBF, N>;
+    static_assert(N != 2 || per_sm(kBlock, N, B::BYTES, B::S) == grad_per_sm(!RBF), "the blocks that are resident");
     static std::atomic<bool> ready[64];
     a.tpr = shape.tpr;
-    return launch_rows(norm_bwd_kernel<XBF, RBF, N>, ready, grad_blocks(a.M, a.K, !XBF && !RBF), shape,
+    return launch_rows(norm_bwd_kernel<XBF, RBF, N>, ready, grad_blocks(a.M, a.K, !RBF), shape,
                        B::BYTES * B::S * shape.threads(), s, dev.device, a);
 }
 template <bool XBF, bool RBF>
@@ -562,7 +565,7 @@ cudaError_t bwd(const NormGradArgs &a, void *dw, bool dw_bf16, cudaStream_t s, c
     if (a.M > 0) e = shape.pieces == 2 ? bwd<XBF, RBF, 2>(a, shape, s, dev) : bwd<XBF, RBF, 4>(a, shape, s, dev);
     if (e == cudaSuccess && dw != nullptr)
         e = launch_kernel(norm_dw_kernel, dim3(static_cast<unsigned>((a.K + 31) / 32)), dim3(kSumThreads), 0, s,
-                          static_cast<const float *>(a.partial), static_cast<int>(grad_blocks(a.M, a.K, !XBF && !RBF)), a.K, dw,
+                          static_cast<const float *>(a.partial), static_cast<int>(grad_blocks(a.M, a.K, !RBF)), a.K, dw,
                           dw_bf16);
     return e;
 }
@@ -570,8 +573,7 @@ cudaError_t bwd(const NormGradArgs &a, void *dw, bool dw_bf16, cudaStream_t s, c
 }  // namespace
 
 int64_t rmsnorm_workspace_bytes(int64_t M, int64_t K) {
-    const int64_t a = grad_blocks(M, K, false), b = grad_blocks(M, K, true);
-    return (a > b ? a : b) * K * 4;
+    return grad_blocks(M, K, false) * K * 4;  // (the larger)
 }
 
 int launch_rmsnorm_fwd(const void *x, int x_dtype, const void *r, void *t, int r_dtype, int64_t M, int64_t K,

@@ -831,8 +831,8 @@ int fp8_rmsnorm_fwd(const void *x, int32_t x_dtype, const void *residual, void *
  * itself; dw [K] of dw_dtype. dw needs a workspace of
  * fp8_rmsnorm_bwd_workspace_bytes(M, K) bytes, 16-byte aligned, whatever it
  * holds; calls that share one must not overlap on the GPU. dw is summed in
- * fp32 in an order that M and K fix. Sizes as fp8_rmsnorm_fwd; M == 0 gives
- * dw = 0.
+ * fp32 in an order that M, K, dy_dtype and t_dtype fix. Sizes as
+ * fp8_rmsnorm_fwd; M == 0 gives dw = 0.
  */
 int fp8_rmsnorm_bwd(const void *dy, int32_t dy_dtype, const void *dtotal, const void *total, int32_t t_dtype,
                     const float *rstd, int64_t M, int64_t K, const void *w, int32_t w_dtype, void *dresidual,
