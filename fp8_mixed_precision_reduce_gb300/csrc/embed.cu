@@ -27,8 +27,9 @@
 // finds equal ids by votes: it saves two launches and, where one id is nearly all of them,
 // loses some of it to that row's sum. fp32, 77 tokens, 1000 x 272: 3.8 us, 7.3 in steps, one
 // id throughout 8.2 and 8.9; 128 tokens, 8000 x 1024: 9.7 and 11.9, one id 18.4 and 15.2.
-// 16384 tokens, 128000 x 4096 in bf16: 197 us, of which the zeros 152 (6.5 TB/s) and the
-// sum 29.
+// 16384 tokens, 128000 x 4096 in bf16: 194 us, of which the zeros 152 (6.5 TB/s) and the
+// sum 29. Where the sort goes through global memory: 65536 tokens, 50000 x 768 95 us; 32768 tokens,
+// 151936 x 2048 152 (128000 x 2048, whose ids still fit beside the position, 129).
 #include <atomic>
 
 #include "fp8mp_async.cuh"
@@ -539,7 +540,9 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 4 : 3) embed_sum_kernel(const
         uint32_t now = __ldg(a.key + i0);
         bool whole = i0 == 0 || __ldg(a.key + i0 - 1) != now;  // the run starts in this chunk
         uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
-        // (fp32: 32768 tokens, 1000 x 2048 70.8 us, 76.6 with 4, which does not fit the registers)
+        // fp32: 32768 tokens, 1000 x 2048 70.8 us, 76.6 with 4, which do not fit the registers. bf16: four,
+        // with 68 bytes of them spilled, 193.4 us for 16384 tokens, 128000 x 4096 and 49.2 for 32768,
+        // 1000 x 2048; two, none spilled, 194.4 and 50.2; four in three blocks an SM, none spilled, 200.9 and 55.3.
         constexpr int kAhead = BF16 ? 4 : 2;
         uint32_t next_key[kAhead], next_pos[kAhead];  // a batch ahead of the rows that they name
         const auto look = [&](int64_t i) {

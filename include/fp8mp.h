@@ -831,8 +831,8 @@ int fp8_rmsnorm_fwd(const void *x, int32_t x_dtype, const void *residual, void *
  * itself; dw [K] of dw_dtype. dw needs a workspace of
  * fp8_rmsnorm_bwd_workspace_bytes(M, K) bytes, 16-byte aligned, whatever it
  * holds; calls that share one must not overlap on the GPU. dw is summed in
- * fp32 in an order that M, K, dy_dtype and t_dtype fix. Sizes as
- * fp8_rmsnorm_fwd; M == 0 gives dw = 0.
+ * fp32 in an order that M, K and t_dtype fix. Sizes as fp8_rmsnorm_fwd;
+ * M == 0 gives dw = 0.
  */
 int fp8_rmsnorm_bwd(const void *dy, int32_t dy_dtype, const void *dtotal, const void *total, int32_t t_dtype,
                     const float *rstd, int64_t M, int64_t K, const void *w, int32_t w_dtype, void *dresidual,
@@ -904,8 +904,10 @@ int mp_embedding_fwd(const int64_t *ids, int64_t M, const void *table, int32_t t
 /*
  * mp_embedding_bwd -- the table's gradient:
  *   dtable[v, k] = (sum over the m with ids[m] = v of dy[m, k]) * scale
- * for every v (0 where no token names it), summed in fp32 in the order of m
- * within runs whose lengths M fixes, so results repeat bit for bit. dy [M x K]
+ * for every v (0 where no token names it), summed in fp32 in an order that M, K
+ * and the ids fix, so results repeat bit for bit: a row's tokens in parts, in the
+ * order of m, then the parts' sums in theirs. Where a part ends depends on M and K
+ * (tables of other widths may round their sums in another order). dy [M x K]
  * of dy_dtype, dtable [V x K] of dtable_dtype. workspace: at least
  * mp_embedding_bwd_workspace_bytes(M, V, K) bytes, 16-byte aligned, whatever it
  * holds; calls that share one must not overlap on the GPU. Sizes as
