@@ -22,17 +22,18 @@ class _TokenEmbeddingFn(torch.autograd.Function):
     def forward(ctx, ids, weight, module, keep):
         flat = ids.reshape(-1)
         flat = flat if flat.is_contiguous() else flat.contiguous()
-        out = torch.empty((flat.shape[0], module.features), dtype=module.out_dtype, device=ids.device)
+        out = torch.empty((*ids.shape, module.features), dtype=module.out_dtype, device=ids.device)
+        rows = out.view(-1, module.features)
         if module.fp8:
             (table,) = module.weight_copies(keep)
-            mp_embedding_fwd(flat, table, out, scale=module.scale, sinv=module.meta_weight.scale_inv)
+            mp_embedding_fwd(flat, table, rows, scale=module.scale, sinv=module.meta_weight.scale_inv)
         else:
-            mp_embedding_fwd(flat, weight.detach().contiguous(), out, scale=module.scale)
+            mp_embedding_fwd(flat, weight.detach().contiguous(), rows, scale=module.scale)
         if keep:
             ctx.save_for_backward(flat)
             ctx.like = (weight.shape, weight.dtype, module.scale)
             watch_leaves(ctx)
-        return out.reshape(*ids.shape, module.features)
+        return out
 
     @staticmethod
     def backward(ctx, dy):

@@ -47,12 +47,11 @@ class _FP8LMHeadFn(torch.autograd.Function):
         M, dev = logits.shape[0], x.device
         t = targets.reshape(-1)
         t = t if t.is_contiguous() else t.contiguous()
-        logprob = torch.empty(M, dtype=torch.float32, device=dev)
+        logprob = torch.empty(targets.shape, dtype=torch.float32, device=dev)
         entropy = torch.empty_like(logprob) if with_entropy else None
         stats = torch.empty((M, 2), dtype=torch.float32, device=dev)
-        mp_logprobs_fwd(logits, t, logprob, stats, entropy=entropy, vocab=head.vocab)
-        logprob = logprob.reshape(targets.shape)
-        entropy = entropy.reshape(targets.shape) if with_entropy else None
+        mp_logprobs_fwd(logits, t, logprob.view(-1), stats, entropy=entropy.view(-1) if with_entropy else None,
+                        vocab=head.vocab)
         if keep:
             factors = torch.cat([head.meta_x.scale_inv, head.meta_weight.scale_inv])
             ctx.save_for_backward(logits, X8, w8, t, stats, entropy, factors, normed if norm is not None else None, rstd, norm)

@@ -281,3 +281,19 @@ def test_a_leaf_of_two_modules(no_kernels, first, second):
         captured.sum().backward()
     del eager, captured
     passes()[second](x).sum().backward()
+
+
+@pytest.mark.parametrize("shape", [(), (5,), (2, 3), (0,)])
+def test_results_may_be_changed_in_place(no_kernels, shape):
+    """As torch.nn.Embedding's and a loss's may: they are tensors of their own."""
+    ids = torch.zeros(shape, dtype=I64)
+    out = table(out_dtype=torch.float32)(ids)
+    assert out.shape == (*shape, 32)
+    out += 1
+    out.sum().backward()
+    for h, entropy in ((head(), False), (head(norm_eps=1e-6), True)):
+        got = h(torch.zeros((*shape, 32)), ids, entropy=entropy)
+        logprob = got[0] if entropy else got
+        assert logprob.shape == shape and (not entropy or got[1].shape == shape)
+        logprob *= 2
+        logprob.sum().backward()
